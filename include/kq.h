@@ -486,6 +486,175 @@ typedef enum { KQ_PQ2_0_MMA_SYNC = 0, KQ_PQ2_0_TCGEN05 = 1 } kq_pq2_0_consumer;
 int kq_set_pq2_0_consumer(int consumer);
 int kq_get_pq2_0_consumer(void);
 
+/* ---- attention between the projections --------------------------------------- */
+
+/* What a decode or prompt step runs between its quantized projections: the
+ * bookkeeping of a paged cache, the norms and position rotation of queries and
+ * keys, the write of keys and values into the cache in 4 bits, and attention
+ * over it ("Kipp Benchmarks": quantized KV rows, streaming attention over a
+ * block table; the cache here holds scale4_gs32 blocks, 4.5 bits per value).
+ *
+ * A step: kq_slot_map -> (projections) -> kq_kv_append -> kq_attn_paged ->
+ * (output projection).  Everything runs on device-side lengths, nothing is
+ * read back, so a step can be captured in a CUDA graph. */
+
+typedef enum { KQ_F32 = 0, KQ_F16 = 1, KQ_BF16 = 2 } kq_dtype;
+
+/* Rows of heads: element (t, h, i) lies at data[t * token_stride + h *
+ * head_stride + i].  data is 16-byte aligned device memory, both strides times
+ * the element size are multiples of 16 bytes (heads may lie apart, as where
+ * queries and gates alternate; tokens too, as in the rows of a fused
+ * projection).  Strides count elements. */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kq_heads;
+
+/* A paged key/value cache of one layer, in device memory owned by the caller.
+ * data: pages x kv_heads blocks of kq_kv_block_bytes each, a page's blocks in
+ * head order.  A block holds page_size tokens of one head as granules of 16
+ * tokens; a granule of head dimension D is, in this order,
+ *   key codes     32-bit [slab][token 16][c 4][group]: dimensions 32 group + 8 c + 0..7
+ *   value codes   16-bit [slab][token / 8][r 8][token % 8 / 2][group][token % 2]:
+ *                 dimensions 32 group + 4 r + 0..3
+ *   key scales    fp16 [slab][token 16][group]
+ *   value scales  fp16 [slab][token 16][group]
+ * with the dimension cut into slabs of 128 (one slab of 64 at D = 64) and a
+ * slab into groups of 32; nibble j of a word is its j-th dimension, and code q
+ * stands for scale * (q - 8), as in the SCALE4 weight format.
+ * Slot s is token s % page_size of page s / page_size.
+ *   head_dim 64, 128 or 256; page_size a positive multiple of 16; kv_heads,
+ *   pages >= 1; pages * page_size < 2^31. */
+typedef struct {
+  void* data;
+  int64_t pages;
+  int32_t page_size;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t reserved; /* 0 */
+} kq_kv_cache;
+
+/* Bytes of one page of one head: page_size * head_dim * 9 / 8; 0 for sizes the
+ * cache does not take. */
+int64_t kq_kv_block_bytes(int32_t page_size, int32_t head_dim);
+
+/* Block tables and slot maps of a step, from the requests' lengths.
+ * Request r has d_cached[r] tokens in the cache and brings d_new[r] >= 0 more.
+ * Its pages are d_block_table[r * table_stride + j]; the first
+ * ceil(cached / page_size) are given, those that the new tokens need beyond
+ * them are taken from d_free_pages, in request order, and written to the table
+ * (other entries are left alone; a call repeated on the same inputs writes the
+ * same).  Outputs:
+ *   d_q_start   [requests + 1]  first new token of each request, and the total
+ *   d_kv_len    [requests]      cached + new
+ *   d_positions [tokens]        position of each new token in its request
+ *   d_slots     [tokens]        page * page_size + position % page_size
+ *   d_pages_used [1]            pages taken from the free list
+ * tokens is the capacity of the two token arrays: entries past the step's
+ * total get position 0 and slot -1, which kq_kv_append skips.
+ *  - All arrays int32, 16-byte aligned.  requests >= 1, tokens >= 0 (a step may
+ *    have none), free_count >= 0 (d_free_pages may then be NULL).
+ *  - On the device: a negative length counts as 0; new tokens past the
+ *    capacity are dropped; a token whose page the free list or the table's row
+ *    cannot hold gets slot -1 (and -1 in the table where the row has room).
+ *    Each sets KQ_ERR_RANGE for kq_device_status.
+ *  - Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
+int kq_slot_map(const int32_t* d_cached, const int32_t* d_new, int64_t requests, int32_t page_size,
+                const int32_t* d_free_pages, int64_t free_count, int32_t* d_block_table, int64_t table_stride,
+                int32_t* d_q_start, int32_t* d_kv_len, int32_t* d_positions, int32_t* d_slots, int64_t tokens,
+                int32_t* d_pages_used, void* stream);
+
+/* Cosines and sines of the position rotation, on the host in FP64, rounded
+ * once: out[p][i] = cos(p * base^(-2 i / rope_dim)) and out[p][rope_dim / 2 +
+ * i] the sine, i < rope_dim / 2, p < positions.  rope_dim even, base > 0. */
+int kq_rope_table_host(float* out, int64_t positions, int32_t rope_dim, double base);
+
+/* Norm and rotation of query and key heads of head_dim D.
+ *  - y = x / sqrt(mean(x^2) + eps) * weight, weights fp32 [D] (NULL: ones);
+ *    norm = 0 leaves the norm out (weights then NULL).
+ *  - The first rope_dim dimensions turn by the token's position: with
+ *    interleaved = 0 dimension i pairs with i + rope_dim / 2, with 1 the pairs
+ *    are (2 i, 2 i + 1); (a, b) -> (a cos - b sin, b cos + a sin).  rope_dim: 0
+ *    (no rotation) or a multiple of 16 up to D.  d_rope: fp32
+ *    [rope_positions][rope_dim] as kq_rope_table_host writes it.
+ *  - fp32 arithmetic whatever the types, one rounding at the end. */
+typedef struct {
+  int32_t q_heads, kv_heads, head_dim;
+  int32_t rope_dim;
+  int32_t interleaved;
+  int32_t norm;
+  float eps;
+  int32_t reserved; /* 0 */
+  const float* q_weight;
+  const float* k_weight;
+  const float* d_rope;
+  int64_t rope_positions;
+} kq_qk_norm;
+
+/* q_out = rotate(norm(q)), k_out = rotate(norm(k)) for `tokens` tokens of
+ * `dtype` (kq_dtype) elements, in one pass.  d_positions int32 [tokens].
+ * In place is allowed (an output view equal to its input).  A position outside
+ * [0, rope_positions) yields zero rows and sets KQ_ERR_RANGE for
+ * kq_device_status.  tokens = 0 is a no-op.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
+int kq_qk_norm_rope(const kq_qk_norm* p, int dtype, const kq_heads* q, const kq_heads* k, const int32_t* d_positions,
+                    int64_t tokens, const kq_heads* q_out, const kq_heads* k_out, void* stream);
+
+/* The same pass with the keys, and the values as they are, quantized into the
+ * cache at d_slots (int32 [tokens]) instead of a key output: per 32 dimensions
+ * the SCALE4 rules of kq_quantize_scale4 on the fp32 values (no rounding to
+ * `dtype` before).  q and q_out may both be NULL (keys and values only).
+ *  - A negative slot writes nothing to the cache for its token.  A slot past
+ *    the cache sets KQ_ERR_RANGE and writes nothing.  Two tokens of one call
+ *    must not share a slot.
+ *  - A group holding a NaN or infinity reads back as NaN and sets
+ *    KQ_ERR_NONFINITE; one whose scale overflows fp16 reads back as NaN and
+ *    sets KQ_ERR_RANGE.
+ * Errors: as kq_qk_norm_rope. */
+int kq_kv_append(const kq_qk_norm* p, const kq_kv_cache* cache, int dtype, const kq_heads* q, const kq_heads* k,
+                 const kq_heads* v, const int32_t* d_positions, const int32_t* d_slots, int64_t tokens,
+                 const kq_heads* q_out, void* stream);
+
+/* What the cache holds at d_slots: k_out, v_out [count][kv_heads][D] of
+ * `dtype`, code * scale in fp32 rounded once.  A negative slot reads as zeros;
+ * one past the cache too, and sets KQ_ERR_RANGE. */
+int kq_kv_read(const kq_kv_cache* cache, const int32_t* d_slots, int64_t count, int dtype, const kq_heads* k_out,
+               const kq_heads* v_out, void* stream);
+
+/* Attention of the new tokens of a step over the cache (their own keys and
+ * values appended before).  Token i of the n new ones of request r stands at
+ * position p = kv_len[r] - n + i and sees the positions max(0, p - window + 1)
+ * .. p of its request (window = 0: all up to p):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * for each query head h with key head h / (q_heads / kv_heads).  A query that
+ * sees nothing (p < 0) gets zeros.
+ *  - q, out: `dtype` rows of heads, `tokens` of them, the first q_start[r] ..
+ *    q_start[r + 1] - 1 being request r's; rows past q_start[requests] are left
+ *    alone.  q_heads a multiple of kv_heads.
+ *  - d_q_start [requests + 1], d_kv_len [requests], d_block_table
+ *    [requests][table_stride]: int32, as kq_slot_map writes them.
+ *  - max_new: an upper bound of the requests' new tokens (1 for a decode step).
+ *  - Scores, softmax statistics and sums in fp32, codes exact.  fp32 queries
+ *    and the probabilities that go with them enter the tensor cores as two
+ *    fp16 parts.
+ *  - On the device: a page id outside the cache hides its keys; a length past
+ *    the table's row is cut to it; q_start past `tokens` or decreasing, or a
+ *    request with more than max_new, hides the tokens concerned (their rows are
+ *    left unwritten).  Each sets KQ_ERR_RANGE for kq_device_status.
+ *  - Workspace: kq_attn_workspace_bytes, 16-byte aligned; everything in it is
+ *    written before it is read.
+ *  - requests >= 1; tokens = 0 is a no-op.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_WORKSPACE,
+ * KQ_ERR_CUDA. */
+int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq_heads* q, const int32_t* d_q_start,
+                  const int32_t* d_kv_len, const int32_t* d_block_table, int64_t table_stride, int64_t requests,
+                  int64_t tokens, int64_t max_new, float scale, int64_t window, const kq_heads* out, void* d_ws,
+                  size_t ws_bytes, void* stream);
+/* Workspace bytes of kq_attn_paged; 0 for arguments it does not take. */
+size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_t requests, int64_t tokens,
+                               int64_t max_new);
+
 /* ---- device status --------------------------------------------------------- */
 
 /* binaryVersion (major*10 + minor) of the streaming kernel as loaded on the

@@ -66,11 +66,35 @@ class kq_link(ctypes.Structure):
                 ("alpha", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+KQ_F32 = 0
+KQ_F16 = 1
+KQ_BF16 = 2
+
+
+class kq_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class kq_kv_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class kq_qk_norm(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("d_rope", ctypes.c_void_p), ("rope_positions", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _QP = ctypes.POINTER(kq_qmat)
+_HP = ctypes.POINTER(kq_heads)
+_CP = ctypes.POINTER(kq_kv_cache)
+_NP = ctypes.POINTER(kq_qk_norm)
 
 # name -> (restype, argtypes); every symbol declared in include/kq.h
 SIGNATURES = {
@@ -118,6 +142,15 @@ SIGNATURES = {
     "kq_decode_plan_destroy": (None, [_P]),
     "kq_stream_read": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P]),
     "kq_selftest_bounded_wait": (ctypes.c_int, [_I64, _P]),
+    "kq_kv_block_bytes": (_I64, [_I32, _I32]),
+    "kq_slot_map": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _P]),
+    "kq_rope_table_host": (ctypes.c_int, [_P, _I64, _I32, ctypes.c_double]),
+    "kq_qk_norm_rope": (ctypes.c_int, [_NP, ctypes.c_int, _HP, _HP, _P, _I64, _HP, _HP, _P]),
+    "kq_kv_append": (ctypes.c_int, [_NP, _CP, ctypes.c_int, _HP, _HP, _HP, _P, _P, _I64, _HP, _P]),
+    "kq_kv_read": (ctypes.c_int, [_CP, _P, _I64, ctypes.c_int, _HP, _HP, _P]),
+    "kq_attn_paged": (ctypes.c_int, [_CP, ctypes.c_int, _I32, _HP, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_float,
+                                     _I64, _HP, _P, _SZ, _P]),
+    "kq_attn_workspace_bytes": (_SZ, [_CP, _I32, _I64, _I64, _I64]),
     "kq_device_status": (ctypes.c_int, [ctypes.c_int]),
     "kq_set_pq2_0_consumer": (ctypes.c_int, [ctypes.c_int]),
     "kq_get_pq2_0_consumer": (ctypes.c_int, []),
@@ -405,6 +438,135 @@ def kq_stream_read(d_src, nbytes, d_sink, stage_bytes=34816, stages=4, stream=No
 
 def kq_device_status(clear=True):
     return _lib.kq_device_status(1 if clear else 0)
+
+
+# ---- attention between the projections -----------------------------------------------
+
+def kq_kv_block_bytes(page_size, head_dim):
+    return _lib.kq_kv_block_bytes(page_size, head_dim)
+
+
+class KVCache:
+    """A paged 4-bit key/value cache of one layer: a torch tensor of
+    [pages, kv_heads, kq_kv_block_bytes] bytes (`data`, or a new zeroed one)
+    and the descriptor that points at it."""
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, data=None, device="cuda"):
+        import torch
+
+        nb = kq_kv_block_bytes(page_size, head_dim)
+        if nb <= 0 or pages < 1 or kv_heads < 1:
+            raise KQError(KQ_ERR_SHAPE, f"KVCache({pages}, {page_size}, {kv_heads}, {head_dim})")
+        if data is None:
+            data = torch.zeros(pages, kv_heads, nb, dtype=torch.uint8, device=device)
+        elif data.numel() * data.element_size() != pages * kv_heads * nb or not data.is_contiguous():
+            raise KQError(KQ_ERR_SHAPE, f"KVCache data: {pages} x {kv_heads} x {nb} contiguous bytes are needed")
+        self.data = data
+        self.pages, self.page_size, self.kv_heads, self.head_dim = int(pages), int(page_size), int(kv_heads), int(head_dim)
+        self.desc = kq_kv_cache(data.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim, 0)
+
+
+class QKNorm:
+    """A kq_qk_norm descriptor and the device tensors it points at: fp32
+    weights [head_dim] (None: ones), the fp32 rotation table [positions,
+    rope_dim] (kq_rope_table_host).  norm=False leaves the norm out."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, rope_dim=0, q_weight=None, k_weight=None, rope=None, eps=1e-6,
+                 interleaved=False, norm=True):
+        self.q_weight, self.k_weight, self.rope = q_weight, k_weight, rope
+        self.desc = kq_qk_norm(q_heads, kv_heads, head_dim, rope_dim, int(interleaved), int(norm), eps, 0,
+                               _ptr(q_weight), _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0])
+
+
+def _dtype(t):
+    name = str(t.dtype)
+    return {"torch.float32": KQ_F32, "torch.float16": KQ_F16, "torch.bfloat16": KQ_BF16}.get(name, -1)
+
+
+def _heads(t, heads, head_dim, name, like=None):
+    """kq_heads of a [tokens, heads, head_dim] view whose innermost dimension is contiguous (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim) or (t.stride(2) != 1 and t.numel()) or \
+            (like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype)):
+        raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(t.shape)} {t.dtype} strides {t.stride()}: [tokens, {heads}, {head_dim}] "
+                                    "of one type for all, innermost contiguous, is needed")
+    return ctypes.byref(kq_heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0))
+
+
+def _ints(t, count, name):
+    """Address of a contiguous int32 tensor of at least `count` elements."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch.int32" or not t.is_contiguous() or t.numel() < count:
+        raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous int32 tensor of {count} elements is needed, not "
+                                    f"{tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def kq_slot_map(d_cached, d_new, page_size, d_free_pages, d_block_table, d_q_start, d_kv_len, d_positions, d_slots,
+                d_pages_used, stream=None):
+    """Block tables and slot maps of a step; d_block_table [requests, table_stride], the capacity of the token arrays is
+    d_slots' length."""
+    r, t = d_cached.numel(), d_slots.numel()
+    if d_block_table.dim() != 2 or d_block_table.shape[0] < r:
+        raise KQError(KQ_ERR_SHAPE, f"block table {tuple(d_block_table.shape)} for {r} requests")
+    _check(_lib.kq_slot_map(_ints(d_cached, r, "d_cached"), _ints(d_new, r, "d_new"), r, page_size,
+                            _ints(d_free_pages, 0, "d_free_pages"), 0 if d_free_pages is None else d_free_pages.numel(),
+                            _ints(d_block_table, 0, "d_block_table"), d_block_table.shape[1],
+                            _ints(d_q_start, r + 1, "d_q_start"), _ints(d_kv_len, r, "d_kv_len"),
+                            _ints(d_positions, t, "d_positions"), _ints(d_slots, t, "d_slots"), t,
+                            _ints(d_pages_used, 1, "d_pages_used"), _stream(stream)), "kq_slot_map")
+
+
+def kq_rope_table_host(positions, rope_dim, base):
+    out = np.empty((positions, rope_dim), dtype=np.float32)
+    _check(_lib.kq_rope_table_host(out.ctypes.data, positions, rope_dim, base), "kq_rope_table_host")
+    return out
+
+
+def kq_qk_norm_rope(p, q, k, d_positions, q_out, k_out, stream=None):
+    """Norm and rotation of q [tokens, q_heads, D] and k [tokens, kv_heads, D] (strided views) into q_out, k_out."""
+    d = p.desc
+    _check(_lib.kq_qk_norm_rope(ctypes.byref(d), _dtype(q), _heads(q, d.q_heads, d.head_dim, "q"),
+                                _heads(k, d.kv_heads, d.head_dim, "k", q), _ints(d_positions, q.shape[0], "d_positions"),
+                                q.shape[0], _heads(q_out, d.q_heads, d.head_dim, "q_out", q),
+                                _heads(k_out, d.kv_heads, d.head_dim, "k_out", q), _stream(stream)), "kq_qk_norm_rope")
+
+
+def kq_kv_append(p, cache, q, k, v, d_positions, d_slots, q_out, stream=None):
+    """Norm and rotation of q into q_out; keys (normed, rotated) and values into the cache at d_slots, in 4 bits.
+    q and q_out may be None."""
+    d, t = p.desc, k.shape[0]
+    _check(_lib.kq_kv_append(ctypes.byref(d), ctypes.byref(cache.desc), _dtype(k), _heads(q, d.q_heads, d.head_dim, "q", k),
+                             _heads(k, d.kv_heads, d.head_dim, "k"), _heads(v, d.kv_heads, d.head_dim, "v", k),
+                             _ints(d_positions, t, "d_positions"), _ints(d_slots, t, "d_slots"), t,
+                             _heads(q_out, d.q_heads, d.head_dim, "q_out", k), _stream(stream)), "kq_kv_append")
+
+
+def kq_kv_read(cache, d_slots, k_out, v_out, stream=None):
+    """What the cache holds at d_slots, as values: k_out, v_out [count, kv_heads, D]."""
+    _check(_lib.kq_kv_read(ctypes.byref(cache.desc), _ints(d_slots, k_out.shape[0], "d_slots"), k_out.shape[0],
+                           _dtype(k_out), _heads(k_out, cache.kv_heads, cache.head_dim, "k_out"),
+                           _heads(v_out, cache.kv_heads, cache.head_dim, "v_out", k_out), _stream(stream)), "kq_kv_read")
+
+
+def kq_attn_workspace_bytes(cache, q_heads, requests, tokens, max_new):
+    return _lib.kq_attn_workspace_bytes(ctypes.byref(cache.desc), q_heads, requests, tokens, max_new)
+
+
+def kq_attn_paged(cache, q, d_q_start, d_kv_len, d_block_table, out, scale, max_new, window=0, ws=None, stream=None):
+    """Attention of the step's new tokens q [tokens, q_heads, D] over the cache, causal, optionally over a sliding
+    window; at most max_new new tokens a request."""
+    p, nb = _ws(ws)
+    r, hq = d_kv_len.numel(), q.shape[1] if q.dim() == 3 else 0
+    if d_block_table.dim() != 2 or d_block_table.shape[0] < r:
+        raise KQError(KQ_ERR_SHAPE, f"block table {tuple(d_block_table.shape)} for {r} requests")
+    _check(_lib.kq_attn_paged(ctypes.byref(cache.desc), _dtype(q), hq, _heads(q, hq, cache.head_dim, "q"),
+                              _ints(d_q_start, r + 1, "d_q_start"), _ints(d_kv_len, r, "d_kv_len"),
+                              _ints(d_block_table, 0, "d_block_table"), d_block_table.shape[1], r, q.shape[0], max_new,
+                              scale, window, _heads(out, hq, cache.head_dim, "out", q), p, nb, _stream(stream)),
+           "kq_attn_paged")
 
 
 KQ_PQ2_0_MMA_SYNC = 0

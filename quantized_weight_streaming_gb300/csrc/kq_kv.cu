@@ -1,0 +1,622 @@
+// What a step does around its attention: slot maps from the requests' lengths,
+// the norms and rotation of query and key heads, and the cache write in 4 bits.
+// (The cache's layout: kq_kv.cuh; "Kipp Benchmarks": quantized KV rows,
+// block-table indirection.)
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kq_device.cuh"
+#include "kq_internal.h"
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace kv {
+
+__device__ unsigned int g_kv_status = 0;
+__device__ __forceinline__ void kv_flag(int status) { atomicOr(&g_kv_status, 1u << status); }
+
+// ---------------------------------------------------------------------------
+// Slot maps
+// ---------------------------------------------------------------------------
+
+// A token's page needs the number of pages that earlier requests take from the
+// free list: an exclusive sum over the requests.  Every CTA owns a range of
+// tokens and runs the sum itself, kScan requests at a time, up to the chunk that
+// ends its range (CTA 0 runs it to the end and writes the per-request outputs),
+// so the whole map is one launch with no pass over intermediate sums.  A page
+// is entered in the table by the one token that opens it.
+constexpr int kScanThreads = 256;
+constexpr int kScan = 4 * kScanThreads;
+constexpr int kMapTokens = 2048;  // tokens of a CTA
+
+struct SlotArgs {
+  const int32_t *cached, *fresh, *free_pages;
+  int32_t *table, *q_start, *kv_len, *positions, *slots, *used;
+  int64_t requests, free_count, table_stride, tokens;
+  int32_t page_size;
+};
+
+__global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
+  __shared__ int32_t s_first[kScan + 1];  // first token of each request of the chunk
+  __shared__ int32_t s_pages[kScan];      // pages taken before it
+  __shared__ int32_t s_cached[kScan];
+  __shared__ int2 s_warp[kScanThreads / 32];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * kMapTokens, t1 = min(a.tokens, t0 + kMapTokens);
+  const bool writer = blockIdx.x == 0;
+  const int P = a.page_size;
+  int32_t run_tokens = 0, run_pages = 0;
+  bool range = false;
+  for (int64_t base = 0; base < a.requests; base += kScan) {
+    // four successive requests a thread
+    int32_t c[4], n[4], need[4];
+    int2 sum = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = base + 4 * tid + i;
+      c[i] = r < a.requests ? a.cached[r] : 0;
+      n[i] = r < a.requests ? a.fresh[r] : 0;
+      if (c[i] < 0 || n[i] < 0 || c[i] > 0x7fffffff - n[i]) range = true;
+      c[i] = max(c[i], 0);
+      n[i] = min(max(n[i], 0), 0x7fffffff - c[i]);
+      const int64_t end = (int64_t)c[i] + n[i];
+      need[i] = (int32_t)((end + P - 1) / P - ((int64_t)c[i] + P - 1) / P);
+      sum.x += n[i];
+      sum.y += need[i];
+    }
+    int2 inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(~0u, inc.x, o), y = __shfl_up_sync(~0u, inc.y, o);
+      if (lane >= o) inc.x += x, inc.y += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int2 before = make_int2(run_tokens, run_pages), total = before;
+#pragma unroll
+    for (int w = 0; w < kScanThreads / 32; ++w) {
+      if (w < warp) before.x += s_warp[w].x, before.y += s_warp[w].y;
+      total.x += s_warp[w].x, total.y += s_warp[w].y;
+    }
+    before.x += inc.x - sum.x;
+    before.y += inc.y - sum.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * tid + i;
+      s_first[j] = before.x;
+      s_pages[j] = before.y;
+      s_cached[j] = c[i];
+      if (writer && base + j < a.requests) {
+        a.q_start[base + j] = before.x;
+        a.kv_len[base + j] = c[i] + n[i];
+      }
+      before.x += n[i];
+      before.y += need[i];
+    }
+    if (tid == kScanThreads - 1) s_first[kScan] = before.x;
+    __syncthreads();
+    // the CTA's tokens that belong to this chunk's requests
+    const int64_t lo = max(t0, (int64_t)run_tokens), hi = min(t1, (int64_t)total.x);
+    for (int64_t t = lo + tid; t < hi; t += kScanThreads) {
+      int l = 0, h = kScan;  // the last request whose first token is not after t
+      while (h - l > 1) {
+        const int m = (l + h) >> 1;
+        if (s_first[m] <= t) l = m; else h = m;
+      }
+      const int32_t pos = s_cached[l] + (int32_t)(t - s_first[l]);
+      const int32_t old = (int32_t)(((int64_t)s_cached[l] + P - 1) / P), at = pos / P;
+      int32_t* row = a.table + (base + l) * a.table_stride;
+      int32_t page = -1;
+      if (pos < 0 || at >= a.table_stride) {  // pos < 0: the lengths' sum left 31 bits
+        range = true;
+      } else if (at < old) {
+        page = row[at];
+      } else {
+        const int64_t f = (int64_t)s_pages[l] + (at - old);
+        if (f >= 0 && f < a.free_count) page = a.free_pages[f]; else range = true;
+        if (pos % P == 0) row[at] = page;
+      }
+      const int64_t slot = page < 0 ? -1 : (int64_t)page * P + pos % P;
+      if (slot > 0x7fffffff) range = true;
+      a.positions[t] = pos;
+      a.slots[t] = slot > 0x7fffffff ? -1 : (int32_t)slot;
+    }
+    run_tokens = total.x;
+    run_pages = total.y;
+    if (!writer && run_tokens >= t1) break;
+    __syncthreads();
+  }
+  if (writer && tid == 0) {
+    a.q_start[a.requests] = run_tokens;
+    a.used[0] = run_pages;
+    if (run_tokens > a.tokens) range = true;
+  }
+  for (int64_t t = max(t0, (int64_t)run_tokens) + tid; t < t1; t += kScanThreads) {
+    a.positions[t] = 0;
+    a.slots[t] = -1;
+  }
+  if (range) kv_flag(KQ_ERR_RANGE);
+}
+
+// ---------------------------------------------------------------------------
+// Norm, rotation, cache write
+// ---------------------------------------------------------------------------
+
+struct View {
+  void* data;
+  int64_t token, head;  // strides in elements
+};
+
+struct QkArgs {
+  View q, k, v, q_out, k_out;
+  const float *q_weight, *k_weight, *rope;
+  const int32_t *positions, *slots;
+  int64_t rope_positions, tokens;
+  int32_t q_heads, kv_heads, rope_dim, interleaved, norm;
+  float eps;
+  Cache cache;
+};
+
+// n with |n - a/d| <= 1/2, halves up: round-half-away(a / d) for a >= 0, d > 0.
+// d is an fp16 value, so (n + 1/2) d is exact in fp32 for n < 16 and the two
+// comparisons decide what the quotient's own rounding cannot.
+__device__ __forceinline__ int round_ratio(float a, float d, float inv) {
+  float n = floorf(fminf(a * inv, 15.f) + 0.5f);
+  if (a >= (n + 0.5f) * d) n += 1.f;
+  if (a < (n - 0.5f) * d) n -= 1.f;
+  return (int)n;
+}
+
+// The four lanes of a 32-dimension group hold 8 values each: the group's scale
+// (SCALE4: the first value of largest magnitude over -8, rounded to fp16) and
+// this lane's eight codes, nibble j the j-th value.
+__device__ __forceinline__ uint32_t quantize_group(const float (&x)[8], __half& scale) {
+  float m = x[0];
+  bool bad = !(fabsf(x[0]) <= 3.402823466e38f);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+    if (fabsf(x[i]) > fabsf(m)) m = x[i];
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const float y = __shfl_xor_sync(~0u, m, o);
+    const bool mine_first = (threadIdx.x & o) == 0;
+    if (mine_first ? fabsf(y) > fabsf(m) : fabsf(y) >= fabsf(m)) m = y;
+  }
+  bad = __shfl_xor_sync(~0u, (int)bad, 1) | (int)bad;
+  bad = __shfl_xor_sync(~0u, (int)bad, 2) | (int)bad;
+  scale = __float2half_rn(m * -0.125f);
+  if (bad) scale = __ushort_as_half((unsigned short)0x7FFF);
+  const float d = __half2float(scale), mag = fabsf(d);
+  uint32_t w = 0x88888888u;
+  if (mag > 0.f && mag <= 65504.f) {
+    const float inv = 1.f / mag;
+    w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = round_ratio(fabsf(x[i]), mag, inv);
+      const int q = (x[i] < 0.f) != (d < 0.f) ? 8 - n : 8 + n;
+      w |= (uint32_t)min(max(q, 0), 15) << (4 * i);
+    }
+  } else if (mag != 0.f) {
+    kv_flag(bad ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
+  }
+  return w;
+}
+
+// Bound by the bytes of its rows.  A head row is spread over D / 8 lanes, 8
+// dimensions a lane (16 or 32 bytes), so its sum of squares is a few shuffles
+// and its other half for the rotation one shuffle a value.  A row group takes
+// kHeads heads of one token (kinds do not mix), loading all their rows before
+// the first is reduced, and keeps the token's cosines and sines in registers.
+constexpr int kQkThreads = 256;
+
+template <typename T, int D, int kHeads, bool kAppend>
+__global__ void __launch_bounds__(kQkThreads) qk_kernel(QkArgs a) {
+  using L = Layout<D>;
+  constexpr int kLanes = D / 8, kRows = kQkThreads / kLanes;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int row = threadIdx.x / kLanes, l = threadIdx.x % kLanes, e0 = 8 * l;
+  const int qc = (a.q_heads + kHeads - 1) / kHeads, kc = (a.kv_heads + kHeads - 1) / kHeads;
+  const int chunks = qc + kc + (kAppend ? kc : 0);
+  const int64_t item = (int64_t)blockIdx.x * kRows + row;
+  const bool live = item < a.tokens * chunks;  // whole warps stay for the shuffles
+  const int64_t t = live ? item / chunks : 0;
+  const int chunk = live ? (int)(item % chunks) : 0;
+  const int kind = chunk < qc ? 0 : (chunk < qc + kc ? 1 : 2);
+  const int h0 = (kind == 0 ? chunk : (kind == 1 ? chunk - qc : chunk - qc - kc)) * kHeads;
+  const int heads = live ? min(kHeads, (kind == 0 ? a.q_heads : a.kv_heads) - h0) : 0;
+  const View& in = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
+  const T* src = static_cast<const T*>(in.data) + t * in.token + h0 * in.head + e0;
+  float x[kHeads][8];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (i < heads) {
+      load8(src + i * in.head, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    }
+  }
+  float w[8], cs[8], sn[8];
+  const int half_dim = a.rope_dim / 2;
+  const bool turns = e0 < a.rope_dim && kind < 2;
+  bool zero = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = 1.f, cs[j] = 1.f, sn[j] = 0.f;
+  if (live && kind < 2) {
+    const float* wt = kind == 0 ? a.q_weight : a.k_weight;
+    if (wt) load8(wt + e0, w);
+    if (a.rope_dim) {
+      const int32_t pos = a.positions[t];
+      zero = pos < 0 || pos >= a.rope_positions;
+      if (zero) {
+        if (l == 0) kv_flag(KQ_ERR_RANGE);
+      } else if (turns) {
+        const float* tab = a.rope + (int64_t)pos * a.rope_dim;
+        if (a.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            cs[2 * j] = cs[2 * j + 1] = tab[e0 / 2 + j];
+            const float s = tab[half_dim + e0 / 2 + j];
+            sn[2 * j] = -s, sn[2 * j + 1] = s;
+          }
+        } else {
+          const int i0 = e0 < half_dim ? e0 : e0 - half_dim;
+          load8(tab + i0, cs);
+          load8(tab + half_dim + i0, sn);
+          if (e0 < half_dim) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
+          }
+        }
+      }
+    }
+  }
+  const int partner = e0 < half_dim ? l + half_dim / 8 : l - half_dim / 8;
+  const View& outv = kind == 0 ? a.q_out : a.k_out;
+  int32_t slot = -1;
+  if (kAppend && live && kind > 0) {
+    slot = a.slots[t];
+    if (slot >= a.cache.pages * a.cache.page_size) {
+      if (l == 0) kv_flag(KQ_ERR_RANGE);
+      slot = -1;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (a.norm) {  // value rows share the warp's shuffles and stay as they are
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o, kLanes);
+      if (kind < 2) {
+        const float r = __frsqrt_rn(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = x[i][j] * r * w[j];
+      }
+    }
+    if (a.rope_dim) {
+      if (a.interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float u = x[i][j], v = x[i][j + 1];
+          if (turns) {
+            x[i][j] = fmaf(u, cs[j], v * sn[j]);
+            x[i][j + 1] = fmaf(v, cs[j + 1], u * sn[j + 1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float other = __shfl_sync(~0u, x[i][j], turns ? partner : l, kLanes);
+          if (turns) x[i][j] = fmaf(x[i][j], cs[j], other * sn[j]);
+        }
+      }
+      if (zero) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+      }
+    }
+    if (kind == 0 || !kAppend) {
+      if (i < heads) store8(static_cast<T*>(outv.data) + t * outv.token + (h0 + i) * outv.head + e0, x[i]);
+    }
+    if constexpr (kAppend) {
+      __half scale;
+      const bool writes = kind > 0 && i < heads && slot >= 0;
+      if (!__any_sync(~0u, writes)) continue;
+      if (!writes) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;  // no flag from rows that are not written
+      }
+      const uint32_t codes = quantize_group(x[i], scale);
+      if (writes) {
+        const int page = slot / a.cache.page_size, in_page = slot - page * a.cache.page_size;
+        uint8_t* g = a.cache.data + ((int64_t)page * a.cache.kv_heads + h0 + i) * a.cache.block_bytes +
+                     (in_page / kGranule) * L::kBytes;
+        const int tok = in_page % kGranule;
+        if (kind == 1) {
+          *reinterpret_cast<uint32_t*>(g + L::key_word(tok, l)) = codes;
+          if (l % 4 == 0) *reinterpret_cast<__half*>(g + L::key_scale(tok, l / 4)) = scale;
+        } else {
+          *reinterpret_cast<uint16_t*>(g + L::value_unit(tok, 2 * l)) = (uint16_t)codes;
+          *reinterpret_cast<uint16_t*>(g + L::value_unit(tok, 2 * l + 1)) = (uint16_t)(codes >> 16);
+          if (l % 4 == 0) *reinterpret_cast<__half*>(g + L::key_scale(tok, l / 4) + D) = scale;
+        }
+      }
+    }
+  }
+}
+
+// One row of one slot a row group: its codes' values in `T`.
+template <typename T, int D>
+__global__ void __launch_bounds__(kQkThreads) read_kernel(Cache c, const int32_t* slots, int64_t count, View k, View v) {
+  using L = Layout<D>;
+  constexpr int kLanes = D / 8, kRows = kQkThreads / kLanes;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t item = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;
+  const int l = threadIdx.x % kLanes;
+  if (item >= count * c.kv_heads) return;
+  const int64_t t = item / c.kv_heads;
+  const int h = (int)(item % c.kv_heads);
+  int32_t slot = slots[t];
+  if (slot >= c.pages * c.page_size) {
+    if (l == 0) kv_flag(KQ_ERR_RANGE);
+    slot = -1;
+  }
+  float kx[8] = {}, vx[8] = {};
+  if (slot >= 0) {
+    const int page = slot / c.page_size, in_page = slot - page * c.page_size, tok = in_page % kGranule;
+    const uint8_t* g =
+        c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes + (in_page / kGranule) * L::kBytes;
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(g + L::key_word(tok, l));
+    const uint32_t vw = *reinterpret_cast<const uint16_t*>(g + L::value_unit(tok, 2 * l)) |
+                        (uint32_t)*reinterpret_cast<const uint16_t*>(g + L::value_unit(tok, 2 * l + 1)) << 16;
+    const float ks = __half2float(*reinterpret_cast<const __half*>(g + L::key_scale(tok, l / 4)));
+    const float vs = __half2float(*reinterpret_cast<const __half*>(g + L::key_scale(tok, l / 4) + D));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      kx[j] = (float)((int)(kw >> (4 * j) & 15u) - 8) * ks;
+      vx[j] = (float)((int)(vw >> (4 * j) & 15u) - 8) * vs;
+    }
+  }
+  store8(static_cast<T*>(k.data) + t * k.token + h * k.head + 8 * l, kx);
+  store8(static_cast<T*>(v.data) + t * v.token + h * v.head + 8 * l, vx);
+}
+
+template <typename T, int D, bool kAppend>
+static cudaError_t launch_qk(const QkArgs& a, cudaStream_t st) {
+  constexpr int kRows = kQkThreads / (D / 8);
+  // Four heads a row group once that still fills the GPU, one below: a decode step is a few hundred rows.
+  const int64_t rows = a.tokens * (a.q_heads + (kAppend ? 2 : 1) * (int64_t)a.kv_heads);
+  const int heads = rows >= 4 * 152 * 2 * kRows ? 4 : 1;
+  const int64_t chunks = (a.q_heads + heads - 1) / heads + (kAppend ? 2 : 1) * ((a.kv_heads + heads - 1) / heads);
+  const int64_t grid = (a.tokens * chunks + kRows - 1) / kRows;
+  auto k = heads == 4 ? qk_kernel<T, D, 4, kAppend> : qk_kernel<T, D, 1, kAppend>;
+  return launch_dependent(k, dim3((unsigned)grid), dim3(kQkThreads), 0, st, a);
+}
+
+template <typename T, bool kAppend>
+static cudaError_t launch_qk(int d, const QkArgs& a, cudaStream_t st) {
+  return d == 64 ? launch_qk<T, 64, kAppend>(a, st)
+                 : (d == 128 ? launch_qk<T, 128, kAppend>(a, st) : launch_qk<T, 256, kAppend>(a, st));
+}
+
+template <bool kAppend>
+static cudaError_t launch_qk(int dtype, int d, const QkArgs& a, cudaStream_t st) {
+  return dtype == KQ_F32 ? launch_qk<float, kAppend>(d, a, st)
+                         : (dtype == KQ_F16 ? launch_qk<__half, kAppend>(d, a, st)
+                                            : launch_qk<__nv_bfloat16, kAppend>(d, a, st));
+}
+
+template <typename T>
+static cudaError_t launch_read(const Cache& c, int d, const int32_t* slots, int64_t n, View k, View v, cudaStream_t st) {
+  const int64_t rows = kQkThreads / (d / 8), grid = (n * c.kv_heads + rows - 1) / rows;
+  auto f = d == 64 ? read_kernel<T, 64> : (d == 128 ? read_kernel<T, 128> : read_kernel<T, 256>);
+  return launch_dependent(f, dim3((unsigned)grid), dim3(kQkThreads), 0, st, c, slots, n, k, v);
+}
+
+static View view(const kq_heads* h) { return h ? View{h->data, h->token_stride, h->head_stride} : View{nullptr, 0, 0}; }
+
+}  // namespace kv
+
+int check_cache(const kq_kv_cache* c) {
+  if (!c) return fail(KQ_ERR_INVALID_ARG, "cache is NULL");
+  if (!c->data) return fail(KQ_ERR_INVALID_ARG, "NULL cache data");
+  if (c->reserved != 0) return fail(KQ_ERR_INVALID_ARG, "reserved field of the cache is not 0");
+  if (c->pages < 1 || c->kv_heads < 1 || kq_kv_block_bytes(c->page_size, c->head_dim) == 0)
+    return fail(KQ_ERR_SHAPE, "cache of %lld pages of %d tokens, %d heads of %d (pages, heads >= 1, page_size a multiple of 16, head_dim 64, 128 or 256)",
+                (long long)c->pages, c->page_size, c->kv_heads, c->head_dim);
+  if (c->pages > 0x7fffffffll / c->page_size)
+    return fail(KQ_ERR_SHAPE, "cache of %lld pages of %d tokens: slots pass 31 bits", (long long)c->pages, c->page_size);
+  if (!aligned16(c->data)) return fail(KQ_ERR_ALIGNMENT, "cache not 16-byte aligned");
+  return KQ_OK;
+}
+
+int check_heads(const kq_heads* h, const char* name, int dtype) {
+  if (!h || !h->data) return fail(KQ_ERR_INVALID_ARG, "%s is NULL", name);
+  const int64_t per = dtype == KQ_F32 ? 4 : 8;
+  if (!aligned16(h->data)) return fail(KQ_ERR_ALIGNMENT, "%s not 16-byte aligned", name);
+  if (h->token_stride < 0 || h->head_stride < 0) return fail(KQ_ERR_SHAPE, "negative stride of %s", name);
+  if (h->token_stride % per || h->head_stride % per)
+    return fail(KQ_ERR_ALIGNMENT, "strides of %s are not multiples of 16 bytes", name);
+  return KQ_OK;
+}
+
+kv::Cache cache_view(const kq_kv_cache* c) {
+  return kv::Cache{static_cast<uint8_t*>(c->data), kq_kv_block_bytes(c->page_size, c->head_dim), c->pages, c->page_size,
+                   c->kv_heads};
+}
+
+static int check_dtype(int dtype) {
+  if (dtype != KQ_F32 && dtype != KQ_F16 && dtype != KQ_BF16) return fail(KQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  return KQ_OK;
+}
+
+static int check_qk(const kq_qk_norm* p, const int32_t* pos, int64_t tokens) {
+  if (!p) return fail(KQ_ERR_INVALID_ARG, "p is NULL");
+  if (p->reserved != 0 || (p->norm != 0 && p->norm != 1) || (p->interleaved != 0 && p->interleaved != 1))
+    return fail(KQ_ERR_INVALID_ARG, "norm and interleaved are 0 or 1, reserved is 0");
+  if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+    return fail(KQ_ERR_SHAPE, "head_dim = %d (64, 128 or 256)", p->head_dim);
+  if (p->q_heads < 1 || p->kv_heads < 1 || p->q_heads > 4096 || p->kv_heads > 4096)
+    return fail(KQ_ERR_SHAPE, "%d query and %d key heads (1 to 4096)", p->q_heads, p->kv_heads);
+  if (p->rope_dim < 0 || p->rope_dim > p->head_dim || p->rope_dim % 16)
+    return fail(KQ_ERR_SHAPE, "rope_dim = %d (a multiple of 16 up to head_dim)", p->rope_dim);
+  if (p->norm && !(p->eps >= 0.f && std::isfinite(p->eps))) return fail(KQ_ERR_INVALID_ARG, "eps is negative or not finite");
+  if (!p->norm && (p->q_weight || p->k_weight)) return fail(KQ_ERR_INVALID_ARG, "weights given without the norm");
+  if (p->rope_dim) {
+    if (!p->d_rope || !pos) return fail(KQ_ERR_INVALID_ARG, "rotation without a table or positions");
+    if (p->rope_positions < 1) return fail(KQ_ERR_SHAPE, "rope_positions = %lld", (long long)p->rope_positions);
+  }
+  if ((p->q_weight && !aligned16(p->q_weight)) || (p->k_weight && !aligned16(p->k_weight)) ||
+      (p->d_rope && !aligned16(p->d_rope)) || (pos && !aligned16(pos)))
+    return fail(KQ_ERR_ALIGNMENT, "weights, table or positions not 16-byte aligned");
+  if (tokens < 0 || tokens > 0x7fffffffll / 8192) return fail(KQ_ERR_SHAPE, "tokens = %lld", (long long)tokens);
+  return KQ_OK;
+}
+
+static kv::QkArgs qk_args(const kq_qk_norm* p, const int32_t* pos, int64_t tokens) {
+  kv::QkArgs a{};
+  a.q_weight = p->q_weight, a.k_weight = p->k_weight, a.rope = p->d_rope;
+  a.positions = pos, a.rope_positions = p->rope_positions, a.tokens = tokens;
+  a.q_heads = p->q_heads, a.kv_heads = p->kv_heads, a.rope_dim = p->rope_dim, a.interleaved = p->interleaved;
+  a.norm = p->norm, a.eps = p->eps;
+  return a;
+}
+
+int read_kv_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, kv::g_kv_status, sizeof(v)) != cudaSuccess) return -1;
+  if (clear && v) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(kv::g_kv_status, &z, sizeof(z)) != cudaSuccess) return -1;
+  }
+  return (int)v;
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+int64_t kq_kv_block_bytes(int32_t page_size, int32_t head_dim) {
+  if (page_size < 16 || page_size % 16 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return 0;
+  return (int64_t)page_size * head_dim * 9 / 8;
+}
+
+int kq_slot_map(const int32_t* d_cached, const int32_t* d_new, int64_t requests, int32_t page_size,
+                const int32_t* d_free_pages, int64_t free_count, int32_t* d_block_table, int64_t table_stride,
+                int32_t* d_q_start, int32_t* d_kv_len, int32_t* d_positions, int32_t* d_slots, int64_t tokens,
+                int32_t* d_pages_used, void* stream) {
+  clear_error();
+  if (!d_cached || !d_new || !d_block_table || !d_q_start || !d_kv_len || !d_pages_used ||
+      (free_count != 0 && !d_free_pages) || (tokens != 0 && (!d_positions || !d_slots)))
+    return fail(KQ_ERR_INVALID_ARG, "NULL pointer");
+  if (requests < 1 || requests > 0x7fffffffll || table_stride < 1 || free_count < 0 || tokens < 0 || tokens > 0x7fffffffll)
+    return fail(KQ_ERR_SHAPE, "requests = %lld, table_stride = %lld, free_count = %lld, tokens = %lld",
+                (long long)requests, (long long)table_stride, (long long)free_count, (long long)tokens);
+  if (page_size < 16 || page_size % 16) return fail(KQ_ERR_SHAPE, "page_size = %d (a positive multiple of 16)", page_size);
+  for (const void* p : {(const void*)d_cached, (const void*)d_new, (const void*)d_free_pages, (const void*)d_block_table,
+                        (const void*)d_q_start, (const void*)d_kv_len, (const void*)d_positions, (const void*)d_slots,
+                        (const void*)d_pages_used})
+    if (!aligned16(p)) return fail(KQ_ERR_ALIGNMENT, "an array is not 16-byte aligned");
+  kv::SlotArgs a{d_cached, d_new, d_free_pages, d_block_table, d_q_start, d_kv_len, d_positions, d_slots, d_pages_used,
+                 requests, free_count, table_stride, tokens, page_size};
+  const int64_t grid = std::max<int64_t>(1, (tokens + kv::kMapTokens - 1) / kv::kMapTokens);
+  KQ_CUDA_TRY(launch_dependent(kv::slot_map_kernel, dim3((unsigned)grid), dim3(kv::kScanThreads), 0,
+                               static_cast<cudaStream_t>(stream), a));
+  return KQ_OK;
+}
+
+int kq_rope_table_host(float* out, int64_t positions, int32_t rope_dim, double base) {
+  clear_error();
+  if (!out) return fail(KQ_ERR_INVALID_ARG, "NULL pointer");
+  if (positions < 1 || rope_dim < 2 || rope_dim % 2)
+    return fail(KQ_ERR_SHAPE, "positions = %lld, rope_dim = %d", (long long)positions, rope_dim);
+  if (!(base > 0) || !std::isfinite(base)) return fail(KQ_ERR_INVALID_ARG, "base must be positive and finite");
+  for (int i = 0; i < rope_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rope_dim);
+    for (int64_t p = 0; p < positions; ++p) {
+      out[p * rope_dim + i] = (float)std::cos((double)p * f);
+      out[p * rope_dim + rope_dim / 2 + i] = (float)std::sin((double)p * f);
+    }
+  }
+  return KQ_OK;
+}
+
+int kq_qk_norm_rope(const kq_qk_norm* p, int dtype, const kq_heads* q, const kq_heads* k, const int32_t* d_positions,
+                    int64_t tokens, const kq_heads* q_out, const kq_heads* k_out, void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (int s = check_qk(p, d_positions, tokens)) return s;
+  if (tokens == 0) return KQ_OK;
+  if (int s = check_heads(q, "q", dtype)) return s;
+  if (int s = check_heads(k, "k", dtype)) return s;
+  if (int s = check_heads(q_out, "q_out", dtype)) return s;
+  if (int s = check_heads(k_out, "k_out", dtype)) return s;
+  kv::QkArgs a = qk_args(p, d_positions, tokens);
+  a.q = kv::view(q), a.k = kv::view(k), a.q_out = kv::view(q_out), a.k_out = kv::view(k_out);
+  KQ_CUDA_TRY(kv::launch_qk<false>(dtype, p->head_dim, a, static_cast<cudaStream_t>(stream)));
+  return KQ_OK;
+}
+
+int kq_kv_append(const kq_qk_norm* p, const kq_kv_cache* cache, int dtype, const kq_heads* q, const kq_heads* k,
+                 const kq_heads* v, const int32_t* d_positions, const int32_t* d_slots, int64_t tokens,
+                 const kq_heads* q_out, void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (int s = check_qk(p, d_positions, tokens)) return s;
+  if (int s = check_cache(cache)) return s;
+  if (cache->kv_heads != p->kv_heads || cache->head_dim != p->head_dim)
+    return fail(KQ_ERR_SHAPE, "cache of %d heads of %d, keys of %d heads of %d", cache->kv_heads, cache->head_dim,
+                p->kv_heads, p->head_dim);
+  if (tokens == 0) return KQ_OK;
+  if (!q != !q_out) return fail(KQ_ERR_INVALID_ARG, "q and q_out come together");
+  if (q) {
+    if (int s = check_heads(q, "q", dtype)) return s;
+    if (int s = check_heads(q_out, "q_out", dtype)) return s;
+  }
+  if (int s = check_heads(k, "k", dtype)) return s;
+  if (int s = check_heads(v, "v", dtype)) return s;
+  if (!d_slots) return fail(KQ_ERR_INVALID_ARG, "d_slots is NULL");
+  if (!aligned16(d_slots)) return fail(KQ_ERR_ALIGNMENT, "d_slots not 16-byte aligned");
+  kv::QkArgs a = qk_args(p, d_positions, tokens);
+  if (!q) a.q_heads = 0;
+  a.q = kv::view(q), a.k = kv::view(k), a.v = kv::view(v), a.q_out = kv::view(q_out);
+  a.slots = d_slots;
+  a.cache = cache_view(cache);
+  KQ_CUDA_TRY(kv::launch_qk<true>(dtype, p->head_dim, a, static_cast<cudaStream_t>(stream)));
+  return KQ_OK;
+}
+
+int kq_kv_read(const kq_kv_cache* cache, const int32_t* d_slots, int64_t count, int dtype, const kq_heads* k_out,
+               const kq_heads* v_out, void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (int s = check_cache(cache)) return s;
+  if (count == 0) return KQ_OK;
+  if (int s = check_heads(k_out, "k_out", dtype)) return s;
+  if (int s = check_heads(v_out, "v_out", dtype)) return s;
+  if (!d_slots) return fail(KQ_ERR_INVALID_ARG, "d_slots is NULL");
+  if (!aligned16(d_slots)) return fail(KQ_ERR_ALIGNMENT, "d_slots not 16-byte aligned");
+  if (count < 0 || count > 0x7fffffffll / cache->kv_heads) return fail(KQ_ERR_SHAPE, "count = %lld", (long long)count);
+  const kv::Cache c = cache_view(cache);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const kv::View k = kv::view(k_out), v = kv::view(v_out);
+  KQ_CUDA_TRY(dtype == KQ_F32 ? kv::launch_read<float>(c, cache->head_dim, d_slots, count, k, v, st)
+                              : (dtype == KQ_F16 ? kv::launch_read<__half>(c, cache->head_dim, d_slots, count, k, v, st)
+                                                 : kv::launch_read<__nv_bfloat16>(c, cache->head_dim, d_slots, count, k, v, st)));
+  return KQ_OK;
+}
+
+}  // extern "C"
