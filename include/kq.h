@@ -639,9 +639,9 @@ int kq_kv_read(const kq_kv_cache* cache, const int32_t* d_slots, int64_t count, 
  *    and the probabilities that go with them enter the tensor cores as two
  *    fp16 parts.
  *  - On the device: a page id outside the cache hides its keys; a length past
- *    the table's row is cut to it; q_start past `tokens` or decreasing, or a
- *    request with more than max_new, hides the tokens concerned (their rows are
- *    left unwritten).  Each sets KQ_ERR_RANGE for kq_device_status.
+ *    the table's row is cut to it; a request whose q_start passes `tokens` or
+ *    decreases, or that brings more than max_new tokens, is left out (its rows
+ *    stay unwritten).  Each sets KQ_ERR_RANGE for kq_device_status.
  *  - Workspace: kq_attn_workspace_bytes, 16-byte aligned; everything in it is
  *    written before it is read.
  *  - requests >= 1; tokens = 0 is a no-op.

@@ -1,8 +1,44 @@
 // Attention of a step's new tokens over the paged 4-bit cache.
 //
-// A first, plain kernel: one CTA per (token, query head), one key per thread
-// for the scores of a chunk of keys, one or two dimensions per thread for the
-// values, running maximum and sum in between (one pass over the cache).
+// For a query row (a token and one of the query heads that share a key head)
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = 2^(c q . k_j - m),  c = scale log2(e),
+// in one pass over the keys with a running reference m.  With one to a few new
+// tokens a request this is bound by the bytes of the cache: 4.5 bits a value,
+// two multiply-adds each per query row, so about 14 flops a byte at a group of
+// four heads, which CUDA cores do not keep up with at 6.8 TB/s.  The kernel
+// below feeds the warp-level tensor instruction (m16n8k16, fp16 in, fp32
+// accumulators) from the codes as they lie in the cache:
+//
+//  - A 4-bit code masked in place in an fp16 half is the subnormal q 2^-24 (or
+//    16 q 2^-24 one nibble further: the other operand, or the result, is
+//    divided by 16), so a 32-bit word of eight codes becomes four operand
+//    registers in a shift and four ANDs, with no conversion.  The tensor core
+//    aligns a subnormal's products as if it were 2^-14, so its sums lose the
+//    bits that a code leaves unused: for fp32 queries the codes are shifted to
+//    the top of the mantissa (four shifts and four ANDs; rows of fp32 outputs
+//    were up to 1.2e-5 off without).
+//  - The zero point: the score accumulators start at -8 sum(q) (a group's 32
+//    products cancel no more than their own size); value codes are centred by an
+//    fp16 subtraction, exact on subnormals, because 8 sum(p') grows with the
+//    context while the sum that is left grows with its square root (subtracting
+//    it at the end lost 1.3e-5 of fp32 rows at 500 keys).
+//  - Key scales multiply the score accumulators, one per group of 32
+//    dimensions, in fp32; value scales multiply the probabilities before these
+//    are rounded to fp16 (p' = p * scale).  Codes stay exact throughout.
+//  - Eight query rows make one tile: rows 0..7 of the first product's A
+//    operand hold the queries rounded to fp16 (scaled by a power of two per
+//    row), rows 8..15, for fp32 queries, what that rounding left out, so that
+//    the two accumulators of a score lie in one lane.  fp32 probabilities are
+//    split the same way into two products.
+//  - m moves only when a score passes it by 6 (p' then reaches 2^15 at most),
+//    so that the accumulators are rarely rescaled.
+//
+// Work is counted in tiles of keys per (request, key head, eight query rows),
+// laid end to end and cut into equal runs, one per warp, whatever the requests'
+// lengths.  A warp has its run streamed through its own ring of shared-memory
+// stages (bulk copies of whole granules, 4608 bytes a tile), so warps never
+// wait for one another.  A row cut between warps leaves partial sums in the
+// workspace; a second launch joins them in a fixed order.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -27,112 +63,733 @@ struct Args {
   void* out;
   int64_t q_token, q_head, out_token, out_head;
   const int32_t *q_start, *kv_len, *table;
-  int64_t table_stride, requests, tokens, max_new, window;
-  int32_t q_heads;
+  int64_t table_stride, requests, tokens, max_new;
+  int32_t window;  // 0: none
+  int32_t q_heads, group;
   float scale;
+  int64_t* base;    // workspace: first work unit of each request, and the total
+  float* partials;  // workspace: two slots per warp of 8 rows x D sums, 8 references, 8 weights
 };
 
-constexpr int kThreads = 128;
+constexpr int kSms = 152;
+constexpr int kRows = 8;             // query rows of a tile
+constexpr float kSlack = 6.f;        // log2 by which a score may pass the reference
+constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
+constexpr int kCombineThreads = 256;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) attn_plain_kernel(Args a) {
+struct Config {
+  static constexpr bool kSplit = sizeof(T) == 4;        // two fp16 parts
+  static constexpr int kWarps = D == 256 ? 7 : 11;         // with the copying warp, 2 or 3 a scheduler: 255 or 168 registers
+  static constexpr int kStages = D == 256 ? 6 : 4;
+  static constexpr int kTileGranules = 256 / D;
+  static constexpr int kTile = kTileGranules * kGranule;  // keys
+  static constexpr int kStageBytes = kTileGranules * Layout<D>::kBytes;
+  static constexpr int kThreads = 32 * (kWarps + 1);      // and the warp that issues the copies
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kSmem = kRing + kWarps * kStages * 20;  // two barriers and a word a stage
+};
+// D = 256: one granule of 4608 bytes; 128: two; 64: four.
+
+constexpr int warps_of(int d) { return d == 256 ? Config<float, 256>::kWarps : Config<float, 128>::kWarps; }
+// Floats of a partial result: 8 rows x D sums, 8 references, 8 weights.
+constexpr int64_t partial_floats(int d) { return kRows * (int64_t)d + 2 * kRows; }
+template <int D>
+constexpr int64_t kPartial = kRows * (int64_t)D + 2 * kRows;
+
+// What a request asks for.  Tiles of `tile` keys from tile0 on cover every key
+// that one of its tokens sees.
+struct Request {
+  int32_t first, n;      // its new tokens
+  int32_t len, pos0;     // keys held; position of its first new token (negative: that token sees nothing)
+  int32_t lo;            // first key that one of its tokens sees
+  int32_t tile0, tiles, row_tiles;  // row_tiles: tiles of eight query rows
+};
+
+__device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile, bool report) {
+  Request q;
+  q.first = a.q_start[r];
+  const int32_t end = a.q_start[r + 1];
+  int32_t len = a.kv_len[r];
+  const int64_t room = a.table_stride * a.cache.page_size;
+  bool bad = len < 0 || len > room;
+  q.n = end - q.first;
+  if (q.first < 0 || end < q.first || end > a.tokens || q.n > a.max_new) bad = true, q.n = 0;
+  len = max(len, 0);
+  q.pos0 = len - q.n;
+  q.len = (int32_t)min((int64_t)len, room);
+  q.lo = a.window ? max(0, max(q.pos0, 0) - (a.window - 1)) : 0;
+  q.tile0 = q.lo / tile;
+  q.tiles = q.n > 0 && q.len > q.lo ? (q.len - 1) / tile - q.tile0 + 1 : 0;
+  q.row_tiles = (int32_t)(((int64_t)q.n * a.group + kRows - 1) / kRows);
+  if (bad && report) attn_flag(KQ_ERR_RANGE);
+  return q;
+}
+__device__ __forceinline__ int64_t units_of(const Request& q, int kv_heads) {
+  return (int64_t)q.row_tiles * kv_heads * q.tiles;
+}
+
+// Work unit w of `total` cut into `runs`: the first one of run i.
+__device__ __forceinline__ int64_t run_start(int64_t i, int64_t total, int64_t runs) { return i * total / runs; }
+__device__ __forceinline__ int64_t run_of(int64_t unit, int64_t total, int64_t runs) {
+  return ((unit + 1) * runs - 1) / total;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_from_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    static_assert(N == 2, "two or four words");
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+// Pair j (nibbles j and j + 4 of a word, j = 0..3) of codes as two fp16
+// subnormals q * kUnit * 2^-24, odd pairs times kOdd besides.
+template <bool kSplit>
+struct Codes;
+template <>
+struct Codes<false> {
+  static constexpr int kUnitLog = 0;
+  static constexpr float kOdd = 16.f;
+  __device__ static uint32_t pair(uint32_t w, int j) { return (j < 2 ? w : w >> 8) & (j % 2 ? 0x00F000F0u : 0x000F000Fu); }
+  __device__ static uint32_t eights(int j) { return j % 2 ? 0x00800080u : 0x00080008u; }
+};
+template <>
+struct Codes<true> {
+  static constexpr int kUnitLog = 6;
+  static constexpr float kOdd = 1.f;
+  __device__ static uint32_t pair(uint32_t w, int j) {
+    return (j == 0 ? w << 6 : (j == 1 ? w << 2 : (j == 2 ? w >> 2 : w >> 6))) & 0x03C003C0u;
+  }
+  __device__ static uint32_t eights(int) { return 0x02000200u; }
+};
+// The same, minus the zero point.
+template <bool kSplit>
+__device__ __forceinline__ uint32_t centred(uint32_t w, int j) {
+  const uint32_t codes = Codes<kSplit>::pair(w, j), eights = Codes<kSplit>::eights(j);
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&codes), *reinterpret_cast<const __half2*>(&eights));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, int D>
+struct Row {
+  static constexpr int kQ = D / 32;  // groups
+  static constexpr int kLo = Config<T, D>::kSplit ? kQ : 1;
+  uint32_t hi[kQ][4];                // operand A rows 0..7: dimensions (0,4), (1,5), (2,6), (3,7) of 8 c .., odd pairs / kOdd
+  uint32_t lo[kLo][4];               // rows 8..15
+  float zero_hi[kQ], zero_lo[kLo];   // where the accumulators start
+  float factor;                      // score in log2 units = factor * accumulated
+  float m, l;                        // reference (log2), this lane's share of the weight
+  int32_t key_lo, key_hi;            // keys that the lane's row sees
+  int32_t all_lo, all_hi;            // keys that every row of the tile sees
+  float o[kQ][2][4];                 // sums: dimensions 4 r + {0, 2} (and one further, times kOdd), rows 2 c, 2 c + 1
+};
+
+// Joins m and the exponent of the largest value scale: true sum = stored * 2^reference.
+__device__ __forceinline__ float reference(float m, int exponent) { return m + (float)(exponent - kHeadroom); }
+
+template <typename T, int D, bool kMask>
+__device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const uint8_t* stage, int32_t key0, uint32_t bad) {
   using L = Layout<D>;
-  __shared__ float s_q[D], s_p[kThreads], s_red[kThreads / 32];
-  __shared__ int64_t s_base[kThreads];
+  using C = Config<T, D>;
+  using Q = Codes<C::kSplit>;
+  constexpr int G = L::kGroups, kBlocks = 2 * C::kTileGranules;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  float s[kBlocks][2];
+  uint32_t seen = 0;  // bit 2 b + j: the row sees token 2 c + j of block b
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    const uint8_t* g0 = stage + (b / 2) * L::kBytes;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl) {
+      uint32_t kw[G], ks[G];  // ks: G scales of token 2 c, then of 2 c + 1
+      load_words<G>(kw, g0 + L::kKeys + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
+      load_words<G>(ks, g0 + L::kKeyScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int q = sl * G + g;
+        float acc[4] = {w.zero_hi[q], w.zero_hi[q], 0.f, 0.f};
+        uint32_t l0 = 0, l1 = 0, l2 = 0, l3 = 0;
+        if constexpr (C::kSplit) {
+          acc[2] = acc[3] = w.zero_lo[q];
+          l0 = w.lo[q][0], l1 = w.lo[q][1], l2 = w.lo[q][2], l3 = w.lo[q][3];
+        }
+        mma(acc, w.hi[q][0], l0, w.hi[q][1], l1, Q::pair(kw[g], 0), Q::pair(kw[g], 1));
+        mma(acc, w.hi[q][2], l2, w.hi[q][3], l3, Q::pair(kw[g], 2), Q::pair(kw[g], 3));
+        const float2 d0 = unpack2(ks[g / 2]), d1 = unpack2(ks[G / 2 + g / 2]);
+        if constexpr (C::kSplit) acc[0] += acc[2], acc[1] += acc[3];
+        s0 = fmaf(g % 2 ? d0.y : d0.x, acc[0], s0);
+        s1 = fmaf(g % 2 ? d1.y : d1.x, acc[1], s1);
+      }
+    }
+    s[b][0] = s0 * w.factor;
+    s[b][1] = s1 * w.factor;
+    if constexpr (kMask) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int32_t key = key0 + 8 * b + 2 * c + j;
+        const bool see = key >= w.key_lo && key < w.key_hi && !(bad >> (b / 2) & 1u);
+        seen |= (uint32_t)see << (2 * b + j);
+        if (!see) s[b][j] = -INFINITY;
+      }
+    }
+  }
+  // the largest value scale of the lane's tokens, and whether a reference has to move
+  float top = s[0][0];
+  __half2 dm = __float2half2_rn(0.f);
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    top = fmaxf(top, fmaxf(s[b][0], s[b][1]));
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl) {
+      uint32_t vs[G];
+      load_words<G>(vs, stage + (b / 2) * L::kBytes + L::kValueScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const __half2 d = __habs2(*reinterpret_cast<__half2*>(&vs[i]));
+        if (!kMask || (seen >> (2 * b + (i >= G / 2)) & 1u)) dm = __hmax2(dm, d);
+      }
+    }
+  }
+  const float dmax = fmaxf(__low2float(dm), __high2float(dm));
+  const bool moves = top > w.m + kSlack, grows = dmax > ldexpf(1.f, exponent);
+  if (__any_sync(~0u, moves || grows)) {
+    // every lane of a row agrees on whether it moves: a row's own scores alone decide its reference
+    float row = top;
+    row = fmaxf(row, __shfl_xor_sync(~0u, row, 1));
+    row = fmaxf(row, __shfl_xor_sync(~0u, row, 2));
+    float d = dmax;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) d = fmaxf(d, __shfl_xor_sync(~0u, d, o));
+    const float before = reference(w.m, exponent);
+    const bool fresh = w.m == -INFINITY;
+    if (row > w.m + kSlack) w.m = row;
+    if (d > ldexpf(1.f, exponent)) {
+      int e;
+      frexpf(d, &e);  // d <= 2^e
+      exponent = max(exponent, min(e, 17));
+    }
+    const float keep = fresh ? 0.f : exp2_approx(before - reference(w.m, exponent));
+    w.l *= keep;
+    const float k0 = __shfl_sync(~0u, keep, 8 * c), k1 = __shfl_sync(~0u, keep, 8 * c + 4);
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) w.o[q][j][0] *= k0, w.o[q][j][1] *= k1, w.o[q][j][2] *= k0, w.o[q][j][3] *= k1;
+    }
+  }
+  const float ref = w.m == -INFINITY ? 0.f : reference(w.m, exponent);
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s[b][j] = exp2_approx(s[b][j] - ref);
+      w.l += s[b][j];
+    }
+  }
+#pragma unroll
+  for (int gr = 0; gr < C::kTileGranules; ++gr) {
+    const uint8_t* g0 = stage + gr * L::kBytes;
+#pragma unroll
+    for (int sl = 0; sl < L::kSlabs; ++sl) {
+      uint32_t v0[G], v1[G], s0[G], s1[G];
+      load_words<G>(v0, g0 + L::kValues + sl * L::kKeySlab + lane * (L::kBlock / 32));
+      load_words<G>(v1, g0 + L::kValues + sl * L::kKeySlab + L::kBlock + lane * (L::kBlock / 32));
+      load_words<G>(s0, g0 + L::kValueScales + sl * L::kScaleSlab + (2 * c) * G * 2);
+      load_words<G>(s1, g0 + L::kValueScales + sl * L::kScaleSlab + (8 + 2 * c) * G * 2);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int q = sl * G + g;
+        const float2 a0 = unpack2(s0[g / 2]), a1 = unpack2(s0[G / 2 + g / 2]);
+        const float2 b0 = unpack2(s1[g / 2]), b1 = unpack2(s1[G / 2 + g / 2]);
+        float p00 = s[2 * gr][0] * (g % 2 ? a0.y : a0.x), p01 = s[2 * gr][1] * (g % 2 ? a1.y : a1.x);
+        float p10 = s[2 * gr + 1][0] * (g % 2 ? b0.y : b0.x), p11 = s[2 * gr + 1][1] * (g % 2 ? b1.y : b1.x);
+        if constexpr (kMask) {  // a hidden key's scale may be anything
+          if (!(seen >> (4 * gr) & 1u)) p00 = 0.f;
+          if (!(seen >> (4 * gr + 1) & 1u)) p01 = 0.f;
+          if (!(seen >> (4 * gr + 2) & 1u)) p10 = 0.f;
+          if (!(seen >> (4 * gr + 3) & 1u)) p11 = 0.f;
+        }
+        const uint32_t h0 = pack2(p00, p01), h1 = pack2(p10, p11);
+        uint32_t e0 = 0, e1 = 0;
+        if constexpr (C::kSplit) {
+          const float2 r0 = unpack2(h0), r1 = unpack2(h1);
+          e0 = pack2(p00 - r0.x, p01 - r0.y), e1 = pack2(p10 - r1.x, p11 - r1.y);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t u0 = centred<C::kSplit>(v0[g], 2 * j), u1 = centred<C::kSplit>(v0[g], 2 * j + 1);
+          const uint32_t u2 = centred<C::kSplit>(v1[g], 2 * j), u3 = centred<C::kSplit>(v1[g], 2 * j + 1);
+          // the tensor core truncates as it accumulates: 16 keys at a time, joined by rounded additions
+          float t[4];
+          mma_from_zero(t, u0, u1, u2, u3, h0, h1);
+          if constexpr (C::kSplit) mma(t, u0, u1, u2, u3, e0, e1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w.o[q][j][i] += t[i];
+        }
+      }
+    }
+  }
+}
+
+// Position in the list of work units: request, row within it (key head outer,
+// query rows inner), tile.  Warp-uniform.
+struct Cursor {
+  int64_t unit, end, r;
+  Request q;
+  int32_t row, tile;           // tile: from the request's first
+  int32_t need_lo, need_hi;    // tiles that the row looks at
+};
+
+template <int kTile>
+__device__ __forceinline__ void enter_row(const Args& a, Cursor& c) {
+  const int32_t x = c.row % c.q.row_tiles * kRows;
+  const int32_t i0 = x / a.group, i1 = min(c.q.n - 1, (x + kRows - 1) / a.group);
+  const int32_t hi = min(c.q.len, c.q.pos0 + i1 + 1);
+  const int32_t lo = a.window ? max(0, c.q.pos0 + i0 - (a.window - 1)) : 0;
+  c.need_lo = lo / kTile - c.q.tile0;
+  c.need_hi = hi > lo ? (hi - 1) / kTile + 1 - c.q.tile0 : 0;
+}
+template <int kTile>
+__device__ __forceinline__ void next_row(const Args& a, Cursor& c) {
+  c.tile = 0;
+  if (++c.row == c.q.row_tiles * a.cache.kv_heads) {
+    c.row = 0;
+    do c.q = request_of(a, ++c.r, kTile, false);
+    while (units_of(c.q, a.cache.kv_heads) == 0);  // a unit remains, so some request has it
+  }
+  enter_row<kTile>(a, c);
+}
+// Moves to the next tile that its row looks at; false at the end of the run.
+template <int kTile>
+__device__ __forceinline__ bool seek(const Args& a, Cursor& c) {
+  while (c.unit < c.end) {
+    if (c.tile == c.q.tiles) next_row<kTile>(a, c);
+    if (c.tile >= c.need_lo && c.tile < c.need_hi) return true;
+    const int32_t to = c.tile < c.need_lo ? min(c.need_lo, c.q.tiles) : c.q.tiles;
+    const int32_t step = (int32_t)min((int64_t)(to - c.tile), c.end - c.unit);
+    c.tile += step;
+    c.unit += step;
+  }
+  return false;
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void begin_row(const Args& a, const Cursor& cur, Row<T, D>& w) {
+  constexpr int kQ = D / 32;
+  using C = Codes<Config<T, D>::kSplit>;
+  constexpr float kZero = -8.f * (1 << C::kUnitLog) / 16777216.f;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const int32_t x = cur.row % cur.q.row_tiles * kRows + lane / 4, h = cur.row / cur.q.row_tiles;
+  const int32_t i = x / a.group;
+  const bool live = i < cur.q.n;
+  const int32_t pos = cur.q.pos0 + i;
+  // rows past the last one hold zeros and see everything: they never ask for the masked path
+  w.key_lo = live ? (a.window ? max(0, pos - (a.window - 1)) : 0) : 0;
+  w.key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
+  w.all_lo = w.key_lo, w.all_hi = w.key_hi;
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    w.all_lo = max(w.all_lo, __shfl_xor_sync(~0u, w.all_lo, o));
+    w.all_hi = min(w.all_hi, __shfl_xor_sync(~0u, w.all_hi, o));
+  }
+  const T* src = static_cast<const T*>(a.q) + (int64_t)(cur.q.first + i) * a.q_token +
+                 (int64_t)(h * a.group + x % a.group) * a.q_head + 8 * c;
+  float x8[kQ][8], top = 0.f;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    if (live) {
+      kv::load8(src + 32 * q, x8[q]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x8[q][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x8[q][j]));
+  }
+  top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+  // the row times 2^e lies below 2^15 (2^e itself stays a normal number)
+  int e = 0;
+  if (top > 0.f && top <= 3.402823466e38f) frexpf(top, &e);
+  e = min(max(15 - e, -110), 110);
+  const float up = ldexpf(1.f, e);
+  w.factor = ldexpf(a.scale * 1.4426950408889634f, 24 - C::kUnitLog - e);
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    float zh = 0.f, zl = 0.f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float f = p % 2 ? 1.f / C::kOdd : 1.f, back = p % 2 ? C::kOdd : 1.f;
+      const float u = x8[q][p] * up * f, v = x8[q][p + 4] * up * f;
+      w.hi[q][p] = pack2(u, v);
+      const float2 r = unpack2(w.hi[q][p]);
+      zh += (r.x + r.y) * back;
+      if constexpr (Config<T, D>::kSplit) {
+        w.lo[q][p] = pack2(u - r.x, v - r.y);
+        const float2 t = unpack2(w.lo[q][p]);
+        zl += (t.x + t.y) * back;
+      }
+    }
+    zh += __shfl_xor_sync(~0u, zh, 1);
+    zh += __shfl_xor_sync(~0u, zh, 2);
+    w.zero_hi[q] = zh * kZero;
+    if constexpr (Config<T, D>::kSplit) {
+      zl += __shfl_xor_sync(~0u, zl, 1);
+      zl += __shfl_xor_sync(~0u, zl, 2);
+      w.zero_lo[q] = zl * kZero;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w.o[q][0][j] = w.o[q][1][j] = 0.f;
+  }
+  w.m = live ? -INFINITY : 0.f;
+  w.l = 0.f;
+}
+
+// What a sum over codes is multiplied by.
+template <typename T, int D>
+constexpr float kOut = 16777216.f / (1 << Codes<Config<T, D>::kSplit>::kUnitLog);
+
+// Ends a row (whole: the output itself) or this warp's part of it.
+template <typename T, int D>
+__device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T, D>& w, int exponent, float* partial) {
+  const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
+  w.l += __shfl_xor_sync(~0u, w.l, 1);
+  w.l += __shfl_xor_sync(~0u, w.l, 2);
+  const int32_t x0 = cur.row % cur.q.row_tiles * kRows, h = cur.row / cur.q.row_tiles;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float l = __shfl_sync(~0u, w.l, 8 * c + 4 * j);
+    const int32_t x = x0 + 2 * c + j, i = x / a.group;
+    if (i >= cur.q.n) continue;
+    const float f = partial ? 1.f : (l == 0.f ? 0.f : kOut<T, D> / l);
+    T* dst = static_cast<T*>(a.out) + (int64_t)(cur.q.first + i) * a.out_token +
+             (int64_t)(h * a.group + x % a.group) * a.out_head;
+#pragma unroll
+    for (int q = 0; q < D / 32; ++q) {
+      const float f16 = f / Codes<Config<T, D>::kSplit>::kOdd;
+      const float4 v = make_float4(w.o[q][0][j] * f, w.o[q][0][j + 2] * f16, w.o[q][1][j] * f, w.o[q][1][j + 2] * f16);
+      if (partial) {
+        *reinterpret_cast<float4*>(partial + (2 * c + j) * D + 32 * q + 4 * r) = v;
+      } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst + 32 * q + 4 * r) = v;
+      } else {
+        union { uint2 u; T t[4]; } y;
+        y.t[0] = kv::from_float<T>(v.x), y.t[1] = kv::from_float<T>(v.y);
+        y.t[2] = kv::from_float<T>(v.z), y.t[3] = kv::from_float<T>(v.w);
+        *reinterpret_cast<uint2*>(dst + 32 * q + 4 * r) = y.u;
+      }
+    }
+  }
+  if (partial && c == 0) {
+    partial[kRows * D + r] = w.m == -INFINITY ? -INFINITY : reference(w.m, exponent);
+    partial[kRows * D + kRows + r] = w.l;
+  }
+}
+
+// A consumer warp per run, and one more warp whose lane i issues the copies of
+// consumer i's tiles, some stages ahead of it.
+template <typename T, int D>
+__global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args a) {
+  using L = Layout<D>;
+  using C = Config<T, D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_first[C::kThreads];  // units before each request of a chunk
+  __shared__ int64_t s_warp[C::kWarps + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool producer = warp == C::kWarps;
+  const int me = producer ? min(lane, C::kWarps - 1) : warp;  // the consumer that this thread works for
+  uint8_t* ring = smem + me * C::kStages * C::kStageBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing) + me * C::kStages;
+  uint64_t* empty = full + C::kWarps * C::kStages;
+  volatile uint32_t* hidden = reinterpret_cast<uint32_t*>(smem + C::kRing + C::kWarps * C::kStages * 16) + me * C::kStages;
+  if (!producer && lane < C::kStages) {
+    mbar_init(&full[lane], 1);
+    mbar_init(&empty[lane], 1);
+    fence_barrier_init();
+  }
   grid_dependency_wait();
   allow_dependent_launch();
-  const int tid = threadIdx.x;
-  const int64_t t = blockIdx.x / a.q_heads;
-  const int h = (int)(blockIdx.x % a.q_heads), hk = h / (a.q_heads / a.cache.kv_heads);
-  int64_t l = 0, r = a.requests;  // the last request that starts at or before t
-  while (r - l > 1) {
-    const int64_t m = (l + r) / 2;
-    if (a.q_start[m] <= t) l = m; else r = m;
-  }
-  const int32_t first = a.q_start[l], end = a.q_start[l + 1];
-  if (t < first || t >= end) return;
-  if (end > a.tokens || end - first > a.max_new) {
-    if (tid == 0) attn_flag(KQ_ERR_RANGE);
-    if (t - first >= a.max_new) return;
-  }
-  int64_t len = a.kv_len[l];
-  const int64_t pos = len - (end - first) + (t - first);
-  if (len > a.table_stride * a.cache.page_size) {
-    if (tid == 0) attn_flag(KQ_ERR_RANGE);
-    len = a.table_stride * a.cache.page_size;
-  }
-  const int64_t hi = min(pos + 1, len), lo = a.window ? max((int64_t)0, pos - a.window + 1) : 0;
-  for (int i = tid; i < D; i += kThreads)
-    s_q[i] = kv::to_float(static_cast<const T*>(a.q)[t * a.q_token + h * a.q_head + i]);
-  __syncthreads();
-  float m = -INFINITY, sum = 0.f, acc[(D + kThreads - 1) / kThreads] = {};
-  for (int64_t base = lo; base < hi; base += kThreads) {
-    const int64_t j = base + tid;
-    float s = -INFINITY;
-    int64_t at = -1;
-    if (j < hi) {
-      const int32_t page = a.table[l * a.table_stride + j / a.cache.page_size];
-      if (page < 0 || page >= a.cache.pages) {
-        attn_flag(KQ_ERR_RANGE);
-      } else {
-        const int in_page = (int)(j % a.cache.page_size), tok = in_page % kGranule;
-        at = ((int64_t)page * a.cache.kv_heads + hk) * a.cache.block_bytes + (in_page / kGranule) * L::kBytes;
-        const uint8_t* g = a.cache.data + at;
-        s = 0.f;
-        for (int w = 0; w < D / 8; ++w) {
-          const uint32_t c = *reinterpret_cast<const uint32_t*>(g + L::key_word(tok, w));
-          const float d = __half2float(*reinterpret_cast<const __half*>(g + L::key_scale(tok, w / 4)));
-          float x = 0.f;
+
+  // The units before each request, kThreads requests at a time: once for the total, and (with more than one chunk)
+  // again to find where this thread's run begins.
+  const int64_t runs = (int64_t)kSms * C::kWarps, run = (int64_t)me * kSms + blockIdx.x;
+  const int chunks = (int)((a.requests + C::kThreads - 1) / C::kThreads);
+  int64_t total = 0;
+  Cursor cur;
+  cur.unit = cur.end = 0;
+  for (int pass = 0; pass < (chunks > 1 ? 2 : 1); ++pass) {
+    int64_t before = 0;
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int64_t r = (int64_t)ch * C::kThreads + tid;
+      const bool mine = r < a.requests;
+      int64_t u = 0;
+      if (mine) u = units_of(request_of(a, r, C::kTile, blockIdx.x == 0 && pass == 0), a.cache.kv_heads);
+      int64_t inc = u;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x = fmaf((float)((int)(c >> (4 * i) & 15u) - 8), s_q[8 * w + i], x);
-          s = fmaf(x, d, s);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += x;
+      }
+      __syncthreads();  // the previous chunk's sums have been read
+      if (lane == 31) s_warp[warp] = inc;
+      __syncthreads();
+      int64_t at = before + inc - u, sum = before;
+#pragma unroll
+      for (int i = 0; i <= C::kWarps; ++i) {
+        if (i < warp) at += s_warp[i];
+        sum += s_warp[i];
+      }
+      s_first[tid] = at;
+      if (blockIdx.x == 0 && pass == 0 && mine) a.base[r] = at;
+      __syncthreads();
+      if (pass == 0) total = sum;
+      if (pass == 1 || chunks == 1) {
+        const int64_t u0 = run_start(run, total, runs), u1 = run_start(run + 1, total, runs);
+        if (u0 < u1 && u0 >= before && u0 < sum) {
+          int l = 0, h = (int)min((int64_t)C::kThreads, a.requests - (int64_t)ch * C::kThreads);
+          while (h - l > 1) {  // the last request that starts at or before u0
+            const int m = (l + h) >> 1;
+            if (s_first[m] <= u0) l = m; else h = m;
+          }
+          cur.unit = u0, cur.end = u1;
+          cur.r = (int64_t)ch * C::kThreads + l;
+          cur.q = request_of(a, cur.r, C::kTile, false);
+          const int64_t in = u0 - s_first[l];
+          cur.row = (int32_t)(in / cur.q.tiles);
+          cur.tile = (int32_t)(in % cur.q.tiles);
         }
-        s *= a.scale;
       }
+      before = sum;
     }
-    s_base[tid] = at;
-    float top = s;
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (tid % 32 == 0) s_red[tid / 32] = top;
-    __syncthreads();
-    for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, s_red[i]);
-    const float now = fmaxf(m, top), keep = m == -INFINITY ? 0.f : __expf(m - now);
-    s_p[tid] = at < 0 ? 0.f : __expf(s - now);
-    m = now;
-    __syncthreads();
-    sum *= keep;
-    for (int i = 0; i < kThreads; ++i) sum += s_p[i];
-#pragma unroll
-    for (int k = 0; k < (D + kThreads - 1) / kThreads; ++k) {
-      const int e = tid + k * kThreads;
-      if (e >= D) continue;
-      float o = acc[k] * keep;
-      for (int i = 0; i < kThreads; ++i) {
-        if (s_base[i] < 0) continue;
-        const uint8_t* g = a.cache.data + s_base[i];
-        const int tok = (int)((base + i) % a.cache.page_size % kGranule);
-        const uint32_t c = *reinterpret_cast<const uint16_t*>(g + L::value_unit(tok, e / 4));
-        const float d = __half2float(*reinterpret_cast<const __half*>(g + L::key_scale(tok, e / 32) + D));
-        o = fmaf(s_p[i] * d, (float)((int)(c >> (4 * (e % 4)) & 15u) - 8), o);
+  }
+  if (blockIdx.x == 0 && tid == 0) a.base[a.requests] = total;
+  if (cur.unit == cur.end) return;
+  enter_row<C::kTile>(a, cur);
+
+  if (producer) {
+    if (lane >= C::kWarps) return;
+    const uint64_t policy = l2_policy_evict_first();
+    const int per_page = a.cache.page_size / kGranule;
+    const int32_t* row = nullptr;
+    int64_t row_of = -1;
+    int32_t at = -1, id = -1, next = -1;  // page `at` of the request, and the page after it in flight
+    uint32_t made = 0;
+    long long since = clock64();
+    while (seek<C::kTile>(a, cur)) {
+      const int st = made % C::kStages;
+      if (made >= C::kStages) {
+        bool free = true;
+        while (!mbar_test_wait(&empty[st], (made / C::kStages - 1) & 1)) {
+          if (clock64() - since > kWaitLimitCycles) {
+            free = false;
+            break;
+          }
+          __nanosleep(64);
+        }
+        if (!free) break;  // the consumer reports it
+        since = clock64();
       }
-      acc[k] = o;
+      if (cur.r != row_of) row_of = cur.r, row = a.table + cur.r * a.table_stride, at = -1;
+      const int32_t pages = (cur.q.len + a.cache.page_size - 1) / a.cache.page_size;  // the table's row holds them
+      const int32_t g0 = (cur.q.tile0 + cur.tile) * C::kTileGranules;
+      int64_t src[C::kTileGranules];
+      uint32_t have = 0;
+      int32_t page = g0 / per_page, sub = g0 - page * per_page;
+#pragma unroll
+      for (int i = 0; i < C::kTileGranules; ++i) {
+        src[i] = -1;
+        if (page < pages) {
+          if (page != at) {
+            id = at >= 0 && page == at + 1 ? next : row[page];
+            at = page;
+            next = page + 1 < pages ? row[page + 1] : -1;
+          }
+          const int32_t key = (g0 + i) * kGranule;
+          if (id >= 0 && id < a.cache.pages) {
+            src[i] = ((int64_t)id * a.cache.kv_heads + cur.row / cur.q.row_tiles) * a.cache.block_bytes + sub * L::kBytes;
+            have |= 1u << i;
+          } else if (key < cur.q.len && key + kGranule > cur.q.lo) {
+            attn_flag(KQ_ERR_RANGE);  // (a page below a sliding window may be gone)
+          }
+        }
+        if (++sub == per_page) sub = 0, ++page;
+      }
+      hidden[st] = ~have & ((1u << C::kTileGranules) - 1);
+      mbar_arrive_expect_tx(&full[st], __popc(have) * L::kBytes);
+      uint8_t* dst = ring + st * C::kStageBytes;
+      if (C::kTileGranules > 1 && have == (1u << C::kTileGranules) - 1 &&
+          src[C::kTileGranules - 1] - src[0] == (C::kTileGranules - 1) * L::kBytes) {
+        bulk_g2s(dst, a.cache.data + src[0], C::kStageBytes, &full[st], policy);  // within one page: one copy
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kTileGranules; ++i)
+          if (have >> i & 1u) bulk_g2s(dst + i * L::kBytes, a.cache.data + src[i], L::kBytes, &full[st], policy);
+      }
+      ++made;
+      ++cur.tile;
+      ++cur.unit;
+    }
+    // the ring stays until the last copies have landed (they have, unless a consumer gave up)
+    for (uint32_t i = made > C::kStages ? made - C::kStages : 0; i < made; ++i)
+      mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1);
+    return;
+  }
+
+  Row<T, D> w;
+  bool first = true;
+  uint32_t used = 0;
+  while (cur.unit < cur.end) {
+    if (cur.tile == cur.q.tiles) next_row<C::kTile>(a, cur);
+    const int32_t from = cur.tile;
+    const int32_t to = (int32_t)min((int64_t)cur.q.tiles, from + (cur.end - cur.unit));
+    begin_row<T, D>(a, cur, w);
+    int exponent = -24;  // of the value scales so far
+    for (int32_t t = max(from, cur.need_lo); t < min(to, cur.need_hi); ++t) {
+      const int st = used % C::kStages;
+      if (!mbar_wait_suspend(&full[st], (used / C::kStages) & 1)) {
+        attn_flag(KQ_ERR_TIMEOUT);
+        return;
+      }
+      const int32_t key0 = (cur.q.tile0 + t) * C::kTile;
+      const uint32_t bad = hidden[st];
+      const uint8_t* stage = ring + st * C::kStageBytes;
+      if (bad || key0 < w.all_lo || key0 + C::kTile > w.all_hi)
+        attend_tile<T, D, true>(w, exponent, stage, key0, bad);
+      else
+        attend_tile<T, D, false>(w, exponent, stage, key0, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      ++used;
+    }
+    const bool whole = from == 0 && to == cur.q.tiles;
+    float* partial = whole ? nullptr : a.partials + (2 * run + (first ? 0 : 1)) * kPartial<D>;
+    end_row<T, D>(a, cur, w, exponent, partial);
+    first = false;
+    cur.unit += to - from;
+    cur.tile = to;
+  }
+}
+
+// Rows that were cut between warps: their parts joined in run order; rows that
+// see nothing: zeros.  One CTA per token (or, where these are few, per token
+// and head); the parts of a row are shared out over the CTA's warps.
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int heads_per_cta) {
+  using C = Config<T, D>;
+  constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
+  __shared__ int64_t s_request;
+  __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int per_token = a.q_heads / heads_per_cta;
+  const int64_t t = blockIdx.x / per_token;
+  if (tid == 0) s_request = -1;
+  __syncthreads();
+  for (int64_t r = tid; r < a.requests; r += kCombineThreads)
+    if (a.q_start[r] <= t && t < a.q_start[r + 1]) s_request = r;
+  __syncthreads();
+  const int64_t r = s_request;
+  if (r < 0) return;
+  const Request q = request_of(a, r, C::kTile, false);
+  const int32_t i = (int32_t)(t - q.first);
+  if (i < 0 || i >= q.n) return;
+  const int64_t runs = (int64_t)kSms * C::kWarps, total = a.base[a.requests], base = a.base[r];
+  const int h0 = (int)(blockIdx.x % per_token) * heads_per_cta;
+  for (int h = h0; h < h0 + heads_per_cta; ++h) {
+    const int32_t x = i * a.group + h % a.group;
+    T* dst = static_cast<T*>(a.out) + t * a.out_token + (int64_t)h * a.out_head;
+    if (q.tiles == 0) {
+      for (int e = tid; e < D; e += kCombineThreads) dst[e] = kv::from_float<T>(0.f);
+      continue;
+    }
+    const int64_t row = (int64_t)(h / a.group) * q.row_tiles + x / kRows;
+    const int64_t lo = base + row * q.tiles, hi = lo + q.tiles;
+    const int64_t w0 = run_of(lo, total, runs), w1 = run_of(hi - 1, total, runs);
+    if (w0 == w1) continue;
+    float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
+    for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
+      const int64_t begin = run_start(w, total, runs);
+      if (begin == run_start(w + 1, total, runs)) continue;
+      const float* p = a.partials + (2 * w + (begin >= lo ? 0 : 1)) * kPartial<D>;
+      const float m = p[kRows * D + x % kRows], l = p[kRows * D + kRows + x % kRows];
+      const float* o = p + (x % kRows) * D + lane * kPer;
+      const float now = fmaxf(ref, m);
+      const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
+      // a row of NaN scores keeps its reference at -inf and its weight NaN: it goes through
+      weight = weight * keep + (m == -INFINITY ? l : l * f);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[e] * f;
+      ref = now;
+    }
+    if (lane == 0) s_ref[warp] = ref, s_weight[warp] = weight;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = acc[e];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w]);
+    for (int e = tid; e < D; e += kCombineThreads) {
+      float sum = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = s_ref[w] == -INFINITY ? 0.f : exp2_approx(s_ref[w] - top);
+        sum += s_sum[w][e] * f;
+        l += s_ref[w] == -INFINITY ? s_weight[w] : s_weight[w] * f;
+      }
+      dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (kOut<T, D> / l));
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int k = 0; k < (D + kThreads - 1) / kThreads; ++k) {
-    const int e = tid + k * kThreads;
-    if (e < D)
-      static_cast<T*>(a.out)[t * a.out_token + h * a.out_head + e] = kv::from_float<T>(sum == 0.f ? 0.f : acc[k] / sum);
-  }
+}
+
+template <typename T, int D>
+static cudaError_t launch(const Args& a, cudaStream_t st) {
+  using C = Config<T, D>;
+  static const cudaError_t opted =
+      cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (opted != cudaSuccess) return opted;
+  if (cudaError_t e = launch_dependent(attend_kernel<T, D>, dim3(kSms), dim3(C::kThreads), C::kSmem, st, a)) return e;
+  const int heads = a.tokens * a.q_heads <= 4096 ? 1 : a.q_heads;
+  return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(a.tokens * (a.q_heads / heads))), dim3(kCombineThreads), 0,
+                          st, a, heads);
 }
 
 template <typename T>
 static cudaError_t launch(int d, const Args& a, cudaStream_t st) {
-  const dim3 grid((unsigned)(a.tokens * a.q_heads));
-  auto k = d == 64 ? attn_plain_kernel<T, 64> : (d == 128 ? attn_plain_kernel<T, 128> : attn_plain_kernel<T, 256>);
-  return launch_dependent(k, grid, dim3(kThreads), 0, st, a);
+  return d == 64 ? launch<T, 64>(a, st) : (d == 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st));
 }
+
+static size_t base_bytes(int64_t requests) { return (size_t)((requests + 1) * 8 + 15) / 16 * 16; }
 
 }  // namespace attn
 
@@ -167,7 +824,8 @@ size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_
                                int64_t max_new) {
   clear_error();
   if (check_attn(cache, q_heads, requests, tokens, max_new)) return 0;
-  return 0;
+  const int d = cache->head_dim;
+  return attn::base_bytes(requests) + (size_t)(2 * attn::kSms * attn::warps_of(d) * attn::partial_floats(d)) * sizeof(float);
 }
 
 int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq_heads* q, const int32_t* d_q_start,
@@ -195,8 +853,11 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
   a.q = q->data, a.q_token = q->token_stride, a.q_head = q->head_stride;
   a.out = out->data, a.out_token = out->token_stride, a.out_head = out->head_stride;
   a.q_start = d_q_start, a.kv_len = d_kv_len, a.table = d_block_table;
-  a.table_stride = table_stride, a.requests = requests, a.tokens = tokens, a.max_new = max_new, a.window = window;
-  a.q_heads = q_heads, a.scale = scale;
+  a.table_stride = table_stride, a.requests = requests, a.tokens = tokens, a.max_new = max_new;
+  a.window = (int32_t)(window > 0x7fffffff ? 0x7fffffff : window);
+  a.q_heads = q_heads, a.group = q_heads / cache->kv_heads, a.scale = scale;
+  a.base = static_cast<int64_t*>(d_ws);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + attn::base_bytes(requests));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32 ? attn::launch<float>(cache->head_dim, a, st)
                               : (dtype == KQ_F16 ? attn::launch<__half>(cache->head_dim, a, st)
