@@ -17,11 +17,12 @@
 //    bits that a code leaves unused: for fp32 queries the codes are shifted to
 //    the top of the mantissa (four shifts and four ANDs; rows of fp32 outputs
 //    were up to 1.2e-5 off without).
-//  - The zero point: the score accumulators start at -8 sum(q) (a group's 32
-//    products cancel no more than their own size); value codes are centred by an
-//    fp16 subtraction, exact on subnormals, because 8 sum(p') grows with the
-//    context while the sum that is left grows with its square root (subtracting
-//    it at the end lost 1.3e-5 of fp32 rows at 500 keys).
+//  - The zero point: -8 sum(q) is added to a group's score (32 products cancel
+//    no more than their own size).  8 sum(p') grows with the context while the
+//    sum that is left grows with its square root, so it is subtracted every 16
+//    keys, by a product that both value products of a group start from (at the
+//    very end it cost fp32 rows 1.3e-5 at 500 keys), or, for fp32 queries, from
+//    the codes (an fp16 subtraction, exact on subnormals).
 //  - Key scales multiply the score accumulators, one per group of 32
 //    dimensions, in fp32; value scales multiply the probabilities before these
 //    are rounded to fp16 (p' = p * scale).  Codes stay exact throughout.
@@ -152,6 +153,37 @@ __device__ __forceinline__ void mma_from_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ void mma_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
@@ -179,7 +211,7 @@ struct Codes<false> {
   static constexpr int kUnitLog = 0;
   static constexpr float kOdd = 16.f;
   __device__ static uint32_t pair(uint32_t w, int j) { return (j < 2 ? w : w >> 8) & (j % 2 ? 0x00F000F0u : 0x000F000Fu); }
-  __device__ static uint32_t eights(int j) { return j % 2 ? 0x00800080u : 0x00080008u; }
+  static constexpr uint32_t kMinus8 = 0x80088008u, kMinus8Odd = 0x80808080u;  // the zero point of either kind of pair
 };
 template <>
 struct Codes<true> {
@@ -188,15 +220,13 @@ struct Codes<true> {
   __device__ static uint32_t pair(uint32_t w, int j) {
     return (j == 0 ? w << 6 : (j == 1 ? w << 2 : (j == 2 ? w >> 2 : w >> 6))) & 0x03C003C0u;
   }
-  __device__ static uint32_t eights(int) { return 0x02000200u; }
+  // minus the zero point, exact
+  __device__ static uint32_t centred(uint32_t w, int j) {
+    const uint32_t codes = pair(w, j), eights = 0x02000200u;
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&codes), *reinterpret_cast<const __half2*>(&eights));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
-// The same, minus the zero point.
-template <bool kSplit>
-__device__ __forceinline__ uint32_t centred(uint32_t w, int j) {
-  const uint32_t codes = Codes<kSplit>::pair(w, j), eights = Codes<kSplit>::eights(j);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&codes), *reinterpret_cast<const __half2*>(&eights));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 template <typename T, int D>
 struct Row {
@@ -204,12 +234,21 @@ struct Row {
   static constexpr int kLo = Config<T, D>::kSplit ? kQ : 1;
   uint32_t hi[kQ][4];                // operand A rows 0..7: dimensions (0,4), (1,5), (2,6), (3,7) of 8 c .., odd pairs / kOdd
   uint32_t lo[kLo][4];               // rows 8..15
-  float zero_hi[kQ], zero_lo[kLo];   // where the accumulators start
+  float zero[kQ];                    // -8 sum(q) of each group
   float factor;                      // score in log2 units = factor * accumulated
   float m, l;                        // reference (log2), this lane's share of the weight
+  float dmax;                        // power of two that no value scale so far passes
   int32_t key_lo, key_hi;            // keys that the lane's row sees
   int32_t all_lo, all_hi;            // keys that every row of the tile sees
+  int32_t any_lo, any_hi;            // keys that one of them sees
   float o[kQ][2][4];                 // sums: dimensions 4 r + {0, 2} (and one further, times kOdd), rows 2 c, 2 c + 1
+
+  __device__ __forceinline__ void add(int q, int j, const float (&t)[4]) {
+    float(&x)[4] = o[q][j];
+    const float2 u = add2(make_float2(x[0], x[1]), make_float2(t[0], t[1]));
+    const float2 v = add2(make_float2(x[2], x[3]), make_float2(t[2], t[3]));
+    x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
+  }
 };
 
 // Joins m and the exponent of the largest value scale: true sum = stored * 2^reference.
@@ -222,12 +261,30 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
   using Q = Codes<C::kSplit>;
   constexpr int G = L::kGroups, kBlocks = 2 * C::kTileGranules;
   const int lane = threadIdx.x & 31, c = lane & 3;
-  float s[kBlocks][2];
+  // The largest of the tile's value scales: 256 bytes of them whatever D, two words a lane.
+  float dmax;
+  {
+    constexpr int kLanes = 32 / C::kTileGranules;  // of a granule
+    const uint2 v = *reinterpret_cast<const uint2*>(stage + lane / kLanes * L::kBytes + L::kValueScales + lane % kLanes * 8);
+    __half2 h[2] = {__habs2(*reinterpret_cast<const __half2*>(&v.x)), __habs2(*reinterpret_cast<const __half2*>(&v.y))};
+    if constexpr (kMask) {  // hidden keys' scales may be anything
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int in = lane % kLanes * 8 + 4 * i;  // byte in the granule's scales
+        const int32_t key = key0 + lane / kLanes * kGranule + in % L::kScaleSlab / (2 * G);
+        if (key < w.any_lo || key >= w.any_hi || (bad >> (lane / kLanes) & 1u)) h[i] = __float2half2_rn(0.f);
+      }
+    }
+    const __half2 m = __hmax2(h[0], h[1]);
+    dmax = __half2float(__hmax(__low2half(m), __high2half(m)));
+  }
+  float2 s[kBlocks];
   uint32_t seen = 0;  // bit 2 b + j: the row sees token 2 c + j of block b
+  float top = -INFINITY;
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) {
     const uint8_t* g0 = stage + (b / 2) * L::kBytes;
-    float s0 = 0.f, s1 = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int sl = 0; sl < L::kSlabs; ++sl) {
       uint32_t kw[G], ks[G];  // ks: G scales of token 2 c, then of 2 c + 1
@@ -236,51 +293,30 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int q = sl * G + g;
-        float acc[4] = {w.zero_hi[q], w.zero_hi[q], 0.f, 0.f};
+        float acc[4];
         uint32_t l0 = 0, l1 = 0, l2 = 0, l3 = 0;
-        if constexpr (C::kSplit) {
-          acc[2] = acc[3] = w.zero_lo[q];
-          l0 = w.lo[q][0], l1 = w.lo[q][1], l2 = w.lo[q][2], l3 = w.lo[q][3];
-        }
-        mma(acc, w.hi[q][0], l0, w.hi[q][1], l1, Q::pair(kw[g], 0), Q::pair(kw[g], 1));
+        if constexpr (C::kSplit) l0 = w.lo[q][0], l1 = w.lo[q][1], l2 = w.lo[q][2], l3 = w.lo[q][3];
+        mma_from_zero(acc, w.hi[q][0], l0, w.hi[q][1], l1, Q::pair(kw[g], 0), Q::pair(kw[g], 1));
         mma(acc, w.hi[q][2], l2, w.hi[q][3], l3, Q::pair(kw[g], 2), Q::pair(kw[g], 3));
+        float2 dot = add2(make_float2(acc[0], acc[1]), make_float2(w.zero[q], w.zero[q]));
+        if constexpr (C::kSplit) dot = add2(dot, make_float2(acc[2], acc[3]));
         const float2 d0 = unpack2(ks[g / 2]), d1 = unpack2(ks[G / 2 + g / 2]);
-        if constexpr (C::kSplit) acc[0] += acc[2], acc[1] += acc[3];
-        s0 = fmaf(g % 2 ? d0.y : d0.x, acc[0], s0);
-        s1 = fmaf(g % 2 ? d1.y : d1.x, acc[1], s1);
+        sum = fma2(g % 2 ? make_float2(d0.y, d1.y) : make_float2(d0.x, d1.x), dot, sum);
       }
     }
-    s[b][0] = s0 * w.factor;
-    s[b][1] = s1 * w.factor;
+    s[b] = mul2(sum, make_float2(w.factor, w.factor));
     if constexpr (kMask) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int32_t key = key0 + 8 * b + 2 * c + j;
-        const bool see = key >= w.key_lo && key < w.key_hi && !(bad >> (b / 2) & 1u);
-        seen |= (uint32_t)see << (2 * b + j);
-        if (!see) s[b][j] = -INFINITY;
-      }
+      const int32_t key = key0 + 8 * b + 2 * c;
+      const bool held = !(bad >> (b / 2) & 1u);
+      const bool s0 = held && key >= w.key_lo && key < w.key_hi, s1 = held && key + 1 >= w.key_lo && key + 1 < w.key_hi;
+      seen |= (uint32_t)s0 << (2 * b) | (uint32_t)s1 << (2 * b + 1);
+      if (!s0) s[b].x = -INFINITY;
+      if (!s1) s[b].y = -INFINITY;
     }
+    top = fmaxf(top, fmaxf(s[b].x, s[b].y));
   }
-  // the largest value scale of the lane's tokens, and whether a reference has to move
-  float top = s[0][0];
-  __half2 dm = __float2half2_rn(0.f);
-#pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
-    top = fmaxf(top, fmaxf(s[b][0], s[b][1]));
-#pragma unroll
-    for (int sl = 0; sl < L::kSlabs; ++sl) {
-      uint32_t vs[G];
-      load_words<G>(vs, stage + (b / 2) * L::kBytes + L::kValueScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const __half2 d = __habs2(*reinterpret_cast<__half2*>(&vs[i]));
-        if (!kMask || (seen >> (2 * b + (i >= G / 2)) & 1u)) dm = __hmax2(dm, d);
-      }
-    }
-  }
-  const float dmax = fmaxf(__low2float(dm), __high2float(dm));
-  const bool moves = top > w.m + kSlack, grows = dmax > ldexpf(1.f, exponent);
+  // whether a reference has to move
+  const bool moves = top > w.m + kSlack, grows = dmax > w.dmax;
   if (__any_sync(~0u, moves || grows)) {
     // every lane of a row agrees on whether it moves: a row's own scores alone decide its reference
     float row = top;
@@ -292,10 +328,11 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
     const float before = reference(w.m, exponent);
     const bool fresh = w.m == -INFINITY;
     if (row > w.m + kSlack) w.m = row;
-    if (d > ldexpf(1.f, exponent)) {
+    if (d > w.dmax) {
       int e;
       frexpf(d, &e);  // d <= 2^e
       exponent = max(exponent, min(e, 17));
+      w.dmax = ldexpf(1.f, exponent);
     }
     const float keep = fresh ? 0.f : exp2_approx(before - reference(w.m, exponent));
     w.l *= keep;
@@ -306,14 +343,12 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
       for (int j = 0; j < 2; ++j) w.o[q][j][0] *= k0, w.o[q][j][1] *= k1, w.o[q][j][2] *= k0, w.o[q][j][3] *= k1;
     }
   }
-  const float ref = w.m == -INFINITY ? 0.f : reference(w.m, exponent);
+  const float ref = w.m == -INFINITY ? 0.f : -reference(w.m, exponent);
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[b][j] = exp2_approx(s[b][j] - ref);
-      w.l += s[b][j];
-    }
+    s[b] = add2(s[b], make_float2(ref, ref));
+    s[b] = make_float2(exp2_approx(s[b].x), exp2_approx(s[b].y));
+    w.l += s[b].x + s[b].y;
   }
 #pragma unroll
   for (int gr = 0; gr < C::kTileGranules; ++gr) {
@@ -330,30 +365,38 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
         const int q = sl * G + g;
         const float2 a0 = unpack2(s0[g / 2]), a1 = unpack2(s0[G / 2 + g / 2]);
         const float2 b0 = unpack2(s1[g / 2]), b1 = unpack2(s1[G / 2 + g / 2]);
-        float p00 = s[2 * gr][0] * (g % 2 ? a0.y : a0.x), p01 = s[2 * gr][1] * (g % 2 ? a1.y : a1.x);
-        float p10 = s[2 * gr + 1][0] * (g % 2 ? b0.y : b0.x), p11 = s[2 * gr + 1][1] * (g % 2 ? b1.y : b1.x);
+        float2 p0 = mul2(s[2 * gr], g % 2 ? make_float2(a0.y, a1.y) : make_float2(a0.x, a1.x));
+        float2 p1 = mul2(s[2 * gr + 1], g % 2 ? make_float2(b0.y, b1.y) : make_float2(b0.x, b1.x));
         if constexpr (kMask) {  // a hidden key's scale may be anything
-          if (!(seen >> (4 * gr) & 1u)) p00 = 0.f;
-          if (!(seen >> (4 * gr + 1) & 1u)) p01 = 0.f;
-          if (!(seen >> (4 * gr + 2) & 1u)) p10 = 0.f;
-          if (!(seen >> (4 * gr + 3) & 1u)) p11 = 0.f;
+          if (!(seen >> (4 * gr) & 1u)) p0.x = 0.f;
+          if (!(seen >> (4 * gr + 1) & 1u)) p0.y = 0.f;
+          if (!(seen >> (4 * gr + 2) & 1u)) p1.x = 0.f;
+          if (!(seen >> (4 * gr + 3) & 1u)) p1.y = 0.f;
         }
-        const uint32_t h0 = pack2(p00, p01), h1 = pack2(p10, p11);
-        uint32_t e0 = 0, e1 = 0;
+        const uint32_t h0 = pack2(p0.x, p0.y), h1 = pack2(p1.x, p1.y);
+        // The tensor core truncates as it accumulates: 16 keys at a time, joined by rounded additions.
         if constexpr (C::kSplit) {
           const float2 r0 = unpack2(h0), r1 = unpack2(h1);
-          e0 = pack2(p00 - r0.x, p01 - r0.y), e1 = pack2(p10 - r1.x, p11 - r1.y);
-        }
+          const uint32_t e0 = pack2(p0.x - r0.x, p0.y - r0.y), e1 = pack2(p1.x - r1.x, p1.y - r1.y);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t u0 = centred<C::kSplit>(v0[g], 2 * j), u1 = centred<C::kSplit>(v0[g], 2 * j + 1);
-          const uint32_t u2 = centred<C::kSplit>(v1[g], 2 * j), u3 = centred<C::kSplit>(v1[g], 2 * j + 1);
-          // the tensor core truncates as it accumulates: 16 keys at a time, joined by rounded additions
-          float t[4];
-          mma_from_zero(t, u0, u1, u2, u3, h0, h1);
-          if constexpr (C::kSplit) mma(t, u0, u1, u2, u3, e0, e1);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t u0 = Q::centred(v0[g], 2 * j), u1 = Q::centred(v0[g], 2 * j + 1);
+            const uint32_t u2 = Q::centred(v1[g], 2 * j), u3 = Q::centred(v1[g], 2 * j + 1);
+            float t[4];
+            mma_from_zero(t, u0, u1, u2, u3, h0, h1);
+            mma(t, u0, u1, u2, u3, e0, e1);
+            w.add(q, j, t);
+          }
+        } else {
+          float zero[4];  // -8 sum(p'), in the units of either row
+          mma_from_zero(zero, Q::kMinus8, Q::kMinus8Odd, Q::kMinus8, Q::kMinus8Odd, h0, h1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w.o[q][j][i] += t[i];
+          for (int j = 0; j < 2; ++j) {
+            float t[4];
+            mma_from(t, zero, Q::pair(v0[g], 2 * j), Q::pair(v0[g], 2 * j + 1), Q::pair(v1[g], 2 * j),
+                     Q::pair(v1[g], 2 * j + 1), h0, h1);
+            w.add(q, j, t);
+          }
         }
       }
     }
@@ -416,8 +459,11 @@ __device__ __forceinline__ void begin_row(const Args& a, const Cursor& cur, Row<
   w.key_lo = live ? (a.window ? max(0, pos - (a.window - 1)) : 0) : 0;
   w.key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
   w.all_lo = w.key_lo, w.all_hi = w.key_hi;
+  w.any_lo = live ? w.key_lo : 0x7fffffff, w.any_hi = live ? w.key_hi : 0;
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) {
+    w.any_lo = min(w.any_lo, __shfl_xor_sync(~0u, w.any_lo, o));
+    w.any_hi = max(w.any_hi, __shfl_xor_sync(~0u, w.any_hi, o));
     w.all_lo = max(w.all_lo, __shfl_xor_sync(~0u, w.all_lo, o));
     w.all_hi = min(w.all_hi, __shfl_xor_sync(~0u, w.all_hi, o));
   }
@@ -459,17 +505,14 @@ __device__ __forceinline__ void begin_row(const Args& a, const Cursor& cur, Row<
         zl += (t.x + t.y) * back;
       }
     }
+    zh += zl;
     zh += __shfl_xor_sync(~0u, zh, 1);
     zh += __shfl_xor_sync(~0u, zh, 2);
-    w.zero_hi[q] = zh * kZero;
-    if constexpr (Config<T, D>::kSplit) {
-      zl += __shfl_xor_sync(~0u, zl, 1);
-      zl += __shfl_xor_sync(~0u, zl, 2);
-      w.zero_lo[q] = zl * kZero;
-    }
+    w.zero[q] = zh * kZero;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.o[q][0][j] = w.o[q][1][j] = 0.f;
   }
+  w.dmax = 0.f;
   w.m = live ? -INFINITY : 0.f;
   w.l = 0.f;
 }
