@@ -77,12 +77,13 @@ constexpr int kRows = 8;             // query rows of a tile
 constexpr float kSlack = 6.f;        // log2 by which a score may pass the reference
 constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
 constexpr int kCombineThreads = 256;
+constexpr int kLeastRun = 2;         // tiles of a run, where there are fewer than two for every warp
 
 template <typename T, int D>
 struct Config {
   static constexpr bool kSplit = sizeof(T) == 4;        // two fp16 parts
-  static constexpr int kWarps = D == 256 ? 7 : 11;         // with the copying warp, 2 or 3 a scheduler: 255 or 168 registers
-  static constexpr int kStages = D == 256 ? 6 : 4;
+  static constexpr int kWarps = (D == 256 ? 8 : 12) - 1;
+  static constexpr int kStages = kWarps < 8 ? 6 : (kWarps < 12 ? 4 : 3);
   static constexpr int kTileGranules = 256 / D;
   static constexpr int kTile = kTileGranules * kGranule;  // keys
   static constexpr int kStageBytes = kTileGranules * Layout<D>::kBytes;
@@ -92,7 +93,7 @@ struct Config {
 };
 // D = 256: one granule of 4608 bytes; 128: two; 64: four.
 
-constexpr int warps_of(int d) { return d == 256 ? Config<float, 256>::kWarps : Config<float, 128>::kWarps; }
+constexpr int kMaxWarps = 15;
 // Floats of a partial result: 8 rows x D sums, 8 references, 8 weights.
 constexpr int64_t partial_floats(int d) { return kRows * (int64_t)d + 2 * kRows; }
 template <int D>
@@ -130,11 +131,20 @@ __device__ __forceinline__ int64_t units_of(const Request& q, int kv_heads) {
   return (int64_t)q.row_tiles * kv_heads * q.tiles;
 }
 
-// Work unit w of `total` cut into `runs`: the first one of run i.
-__device__ __forceinline__ int64_t run_start(int64_t i, int64_t total, int64_t runs) { return i * total / runs; }
-__device__ __forceinline__ int64_t run_of(int64_t unit, int64_t total, int64_t runs) {
-  return ((unit + 1) * runs - 1) / total;
-}
+// The work units cut into runs: the first `extra` of them per + 1 long, the others per.  No run is empty.
+struct Runs {
+  int64_t per, extra, count;
+  __device__ __forceinline__ Runs(int64_t total, int64_t most) {
+    count = min(most, (total + kLeastRun - 1) / kLeastRun);
+    per = count ? total / count : 0;
+    extra = total - per * count;
+  }
+  __device__ __forceinline__ int64_t start(int64_t i) const { return i * per + min(i, extra); }
+  __device__ __forceinline__ int64_t of(int64_t unit) const {
+    const int64_t cut = extra * (per + 1);
+    return unit < cut ? unit / (per + 1) : extra + (unit - cut) / per;
+  }
+};
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -239,8 +249,6 @@ struct Row {
   float m, l;                        // reference (log2), this lane's share of the weight
   float dmax;                        // power of two that no value scale so far passes
   int32_t key_lo, key_hi;            // keys that the lane's row sees
-  int32_t all_lo, all_hi;            // keys that every row of the tile sees
-  int32_t any_lo, any_hi;            // keys that one of them sees
   float o[kQ][2][4];                 // sums: dimensions 4 r + {0, 2} (and one further, times kOdd), rows 2 c, 2 c + 1
 
   __device__ __forceinline__ void add(int q, int j, const float (&t)[4]) {
@@ -251,11 +259,23 @@ struct Row {
   }
 };
 
+// Position in the list of work units: request, row within it (key head outer,
+// query rows inner), tile.  Warp-uniform.
+struct Cursor {
+  int64_t unit, end, r;
+  Request q;
+  int32_t row, tile;           // tile: from the request's first
+  int32_t need_lo, need_hi;    // tiles that the row looks at
+  int32_t all_lo, all_hi;      // keys that every query row of the tile sees
+  int32_t any_lo, any_hi;      // keys that one of them sees
+};
+
 // Joins m and the exponent of the largest value scale: true sum = stored * 2^reference.
 __device__ __forceinline__ float reference(float m, int exponent) { return m + (float)(exponent - kHeadroom); }
 
 template <typename T, int D, bool kMask>
-__device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const uint8_t* stage, int32_t key0, uint32_t bad) {
+__device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const uint8_t* stage, int32_t key0, uint32_t bad,
+                                            const Cursor& cur) {
   using L = Layout<D>;
   using C = Config<T, D>;
   using Q = Codes<C::kSplit>;
@@ -272,7 +292,7 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
       for (int i = 0; i < 2; ++i) {
         const int in = lane % kLanes * 8 + 4 * i;  // byte in the granule's scales
         const int32_t key = key0 + lane / kLanes * kGranule + in % L::kScaleSlab / (2 * G);
-        if (key < w.any_lo || key >= w.any_hi || (bad >> (lane / kLanes) & 1u)) h[i] = __float2half2_rn(0.f);
+        if (key < cur.any_lo || key >= cur.any_hi || (bad >> (lane / kLanes) & 1u)) h[i] = __float2half2_rn(0.f);
       }
     }
     const __half2 m = __hmax2(h[0], h[1]);
@@ -403,15 +423,6 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
   }
 }
 
-// Position in the list of work units: request, row within it (key head outer,
-// query rows inner), tile.  Warp-uniform.
-struct Cursor {
-  int64_t unit, end, r;
-  Request q;
-  int32_t row, tile;           // tile: from the request's first
-  int32_t need_lo, need_hi;    // tiles that the row looks at
-};
-
 template <int kTile>
 __device__ __forceinline__ void enter_row(const Args& a, Cursor& c) {
   const int32_t x = c.row % c.q.row_tiles * kRows;
@@ -446,7 +457,7 @@ __device__ __forceinline__ bool seek(const Args& a, Cursor& c) {
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void begin_row(const Args& a, const Cursor& cur, Row<T, D>& w) {
+__device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>& w) {
   constexpr int kQ = D / 32;
   using C = Codes<Config<T, D>::kSplit>;
   constexpr float kZero = -8.f * (1 << C::kUnitLog) / 16777216.f;
@@ -458,15 +469,9 @@ __device__ __forceinline__ void begin_row(const Args& a, const Cursor& cur, Row<
   // rows past the last one hold zeros and see everything: they never ask for the masked path
   w.key_lo = live ? (a.window ? max(0, pos - (a.window - 1)) : 0) : 0;
   w.key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
-  w.all_lo = w.key_lo, w.all_hi = w.key_hi;
-  w.any_lo = live ? w.key_lo : 0x7fffffff, w.any_hi = live ? w.key_hi : 0;
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) {
-    w.any_lo = min(w.any_lo, __shfl_xor_sync(~0u, w.any_lo, o));
-    w.any_hi = max(w.any_hi, __shfl_xor_sync(~0u, w.any_hi, o));
-    w.all_lo = max(w.all_lo, __shfl_xor_sync(~0u, w.all_lo, o));
-    w.all_hi = min(w.all_hi, __shfl_xor_sync(~0u, w.all_hi, o));
-  }
+  cur.all_lo = __reduce_max_sync(~0u, w.key_lo), cur.all_hi = __reduce_min_sync(~0u, w.key_hi);
+  cur.any_lo = __reduce_min_sync(~0u, live ? w.key_lo : 0x7fffffff);
+  cur.any_hi = __reduce_max_sync(~0u, live ? w.key_hi : 0);
   const T* src = static_cast<const T*>(a.q) + (int64_t)(cur.q.first + i) * a.q_token +
                  (int64_t)(h * a.group + x % a.group) * a.q_head + 8 * c;
   float x8[kQ][8], top = 0.f;
@@ -567,6 +572,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_first[C::kThreads];  // units before each request of a chunk
   __shared__ int64_t s_warp[C::kWarps + 1];
+  __shared__ Cursor s_cursor[C::kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool producer = warp == C::kWarps;
   const int me = producer ? min(lane, C::kWarps - 1) : warp;  // the consumer that this thread works for
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
 
   // The units before each request, kThreads requests at a time: once for the total, and (with more than one chunk)
   // again to find where this thread's run begins.
-  const int64_t runs = (int64_t)kSms * C::kWarps, run = (int64_t)me * kSms + blockIdx.x;
+  const int64_t run = (int64_t)me * kSms + blockIdx.x;
   const int chunks = (int)((a.requests + C::kThreads - 1) / C::kThreads);
   int64_t total = 0;
   Cursor cur;
@@ -616,8 +622,9 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       __syncthreads();
       if (pass == 0) total = sum;
       if (pass == 1 || chunks == 1) {
-        const int64_t u0 = run_start(run, total, runs), u1 = run_start(run + 1, total, runs);
-        if (u0 < u1 && u0 >= before && u0 < sum) {
+        const Runs runs(total, (int64_t)kSms * C::kWarps);
+        const int64_t u0 = runs.start(run), u1 = runs.start(run + 1);
+        if (run < runs.count && u0 >= before && u0 < sum) {
           int l = 0, h = (int)min((int64_t)C::kThreads, a.requests - (int64_t)ch * C::kThreads);
           while (h - l > 1) {  // the last request that starts at or before u0
             const int m = (l + h) >> 1;
@@ -707,36 +714,42 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
     return;
   }
 
+  // The cursor waits in shared memory while a row's tiles go by.
+  Cursor& c = s_cursor[warp];
   Row<T, D> w;
   bool first = true;
   uint32_t used = 0;
   while (cur.unit < cur.end) {
     if (cur.tile == cur.q.tiles) next_row<C::kTile>(a, cur);
-    const int32_t from = cur.tile;
-    const int32_t to = (int32_t)min((int64_t)cur.q.tiles, from + (cur.end - cur.unit));
     begin_row<T, D>(a, cur, w);
+    __syncwarp();
+    if (lane == 0) c = cur;
+    __syncwarp();
+    const int32_t from = c.tile;
+    const int32_t to = (int32_t)min((int64_t)c.q.tiles, from + (c.end - c.unit));
     int exponent = -24;  // of the value scales so far
-    for (int32_t t = max(from, cur.need_lo); t < min(to, cur.need_hi); ++t) {
+    for (int32_t t = max(from, c.need_lo); t < min(to, c.need_hi); ++t) {
       const int st = used % C::kStages;
       if (!mbar_wait_suspend(&full[st], (used / C::kStages) & 1)) {
         attn_flag(KQ_ERR_TIMEOUT);
         return;
       }
-      const int32_t key0 = (cur.q.tile0 + t) * C::kTile;
+      const int32_t key0 = (c.q.tile0 + t) * C::kTile;
       const uint32_t bad = hidden[st];
       const uint8_t* stage = ring + st * C::kStageBytes;
-      if (bad || key0 < w.all_lo || key0 + C::kTile > w.all_hi)
-        attend_tile<T, D, true>(w, exponent, stage, key0, bad);
+      if (bad || key0 < c.all_lo || key0 + C::kTile > c.all_hi)
+        attend_tile<T, D, true>(w, exponent, stage, key0, bad, c);
       else
-        attend_tile<T, D, false>(w, exponent, stage, key0, 0);
+        attend_tile<T, D, false>(w, exponent, stage, key0, 0, c);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       ++used;
     }
-    const bool whole = from == 0 && to == cur.q.tiles;
+    const bool whole = from == 0 && to == c.q.tiles;
     float* partial = whole ? nullptr : a.partials + (2 * run + (first ? 0 : 1)) * kPartial<D>;
-    end_row<T, D>(a, cur, w, exponent, partial);
+    end_row<T, D>(a, c, w, exponent, partial);
     first = false;
+    cur = c;
     cur.unit += to - from;
     cur.tile = to;
   }
@@ -766,7 +779,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int he
   const Request q = request_of(a, r, C::kTile, false);
   const int32_t i = (int32_t)(t - q.first);
   if (i < 0 || i >= q.n) return;
-  const int64_t runs = (int64_t)kSms * C::kWarps, total = a.base[a.requests], base = a.base[r];
+  const int64_t base = a.base[r];
+  const Runs runs(a.base[a.requests], (int64_t)kSms * C::kWarps);
   const int h0 = (int)(blockIdx.x % per_token) * heads_per_cta;
   for (int h = h0; h < h0 + heads_per_cta; ++h) {
     const int32_t x = i * a.group + h % a.group;
@@ -777,13 +791,11 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int he
     }
     const int64_t row = (int64_t)(h / a.group) * q.row_tiles + x / kRows;
     const int64_t lo = base + row * q.tiles, hi = lo + q.tiles;
-    const int64_t w0 = run_of(lo, total, runs), w1 = run_of(hi - 1, total, runs);
+    const int64_t w0 = runs.of(lo), w1 = runs.of(hi - 1);
     if (w0 == w1) continue;
     float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
     for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
-      const int64_t begin = run_start(w, total, runs);
-      if (begin == run_start(w + 1, total, runs)) continue;
-      const float* p = a.partials + (2 * w + (begin >= lo ? 0 : 1)) * kPartial<D>;
+      const float* p = a.partials + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * kPartial<D>;
       const float m = p[kRows * D + x % kRows], l = p[kRows * D + kRows + x % kRows];
       const float* o = p + (x % kRows) * D + lane * kPer;
       const float now = fmaxf(ref, m);
@@ -868,7 +880,7 @@ size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_
   clear_error();
   if (check_attn(cache, q_heads, requests, tokens, max_new)) return 0;
   const int d = cache->head_dim;
-  return attn::base_bytes(requests) + (size_t)(2 * attn::kSms * attn::warps_of(d) * attn::partial_floats(d)) * sizeof(float);
+  return attn::base_bytes(requests) + (size_t)(2 * attn::kSms * attn::kMaxWarps * attn::partial_floats(d)) * sizeof(float);
 }
 
 int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq_heads* q, const int32_t* d_q_start,
