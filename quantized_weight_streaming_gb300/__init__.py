@@ -183,11 +183,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_raw_stream = None  # torch's lookup of the current stream's handle, once torch is imported
+
+
+def _current_stream():
+    """Handle of the current stream (torch.cuda.current_stream() builds a Stream object first: 3 us a call against 0.2)."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # initialises CUDA
+        get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if get is None or device is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw_stream = lambda: get(device())  # noqa: E731
+    return _raw_stream()
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -478,30 +494,44 @@ class QKNorm:
                                _ptr(q_weight), _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0])
 
 
+_DTYPES = {}  # torch dtype -> (kq_dtype or -1, whether it is int32), filled on first use
+
+
+def _kind(dtype):
+    k = _DTYPES.get(dtype)
+    if k is None:
+        names = {"torch.float32": KQ_F32, "torch.float16": KQ_F16, "torch.bfloat16": KQ_BF16}
+        k = _DTYPES[dtype] = (names.get(str(dtype), -1), str(dtype) == "torch.int32")
+    return k
+
+
 def _dtype(t):
-    name = str(t.dtype)
-    return {"torch.float32": KQ_F32, "torch.float16": KQ_F16, "torch.bfloat16": KQ_BF16}.get(name, -1)
+    return _kind(t.dtype)[0]
 
 
 def _heads(t, heads, head_dim, name, like=None):
     """kq_heads of a [tokens, heads, head_dim] view whose innermost dimension is contiguous (None -> NULL)."""
     if t is None:
         return None
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim) or (t.stride(2) != 1 and t.numel()) or \
-            (like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype)):
-        raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(t.shape)} {t.dtype} strides {t.stride()}: [tokens, {heads}, {head_dim}] "
-                                    "of one type for all, innermost contiguous, is needed")
-    return ctypes.byref(kq_heads(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0))
+    shape = t.shape
+    if len(shape) == 3:
+        n, h, d = shape
+        st, sh, sd = t.stride()
+        if h == heads and d == head_dim and (sd == 1 or n == 0) and \
+                (like is None or (n == like.shape[0] and t.dtype is like.dtype)):
+            return kq_heads(t.data_ptr(), st if n > 1 else 0, sh if h > 1 else 0)
+    raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(shape)} {t.dtype} strides {t.stride()}: [tokens, {heads}, {head_dim}] "
+                                "of one type for all, innermost contiguous, is needed")
 
 
 def _ints(t, count, name):
     """Address of a contiguous int32 tensor of at least `count` elements."""
     if t is None:
         return None
-    if str(t.dtype) != "torch.int32" or not t.is_contiguous() or t.numel() < count:
-        raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous int32 tensor of {count} elements is needed, not "
-                                    f"{tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
+    if _kind(t.dtype)[1] and t.is_contiguous() and t.numel() >= count:
+        return t.data_ptr()
+    raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous int32 tensor of {count} elements is needed, not "
+                                f"{tuple(t.shape)} {t.dtype}")
 
 
 def kq_slot_map(d_cached, d_new, page_size, d_free_pages, d_block_table, d_q_start, d_kv_len, d_positions, d_slots,

@@ -29,7 +29,7 @@ __device__ __forceinline__ void kv_flag(int status) { atomicOr(&g_kv_status, 1u 
 // is entered in the table by the one token that opens it.
 constexpr int kScanThreads = 256;
 constexpr int kScan = 4 * kScanThreads;
-constexpr int kMapTokens = 2048;  // tokens of a CTA
+constexpr int kMapTokens = 512;  // tokens of a CTA
 
 struct SlotArgs {
   const int32_t *cached, *fresh, *free_pages;
@@ -99,10 +99,11 @@ __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
     }
     if (tid == kScanThreads - 1) s_first[kScan] = before.x;
     __syncthreads();
+    const int in_chunk = (int)min((int64_t)kScan, a.requests - base);
     // the CTA's tokens that belong to this chunk's requests
     const int64_t lo = max(t0, (int64_t)run_tokens), hi = min(t1, (int64_t)total.x);
     for (int64_t t = lo + tid; t < hi; t += kScanThreads) {
-      int l = 0, h = kScan;  // the last request whose first token is not after t
+      int l = 0, h = in_chunk;  // the last request whose first token is not after t
       while (h - l > 1) {
         const int m = (l + h) >> 1;
         if (s_first[m] <= t) l = m; else h = m;
