@@ -42,8 +42,11 @@
 // workspace; a second launch joins them in a fixed order.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
+#include "kq_attn.cuh"
 #include "kq_device.cuh"
 #include "kq_internal.h"
 #include "kq_kv.cuh"
@@ -51,28 +54,9 @@
 namespace kq {
 namespace attn {
 
-using kv::Cache;
-using kv::kGranule;
-using kv::Layout;
-
 __device__ unsigned int g_attn_status = 0;
 __device__ __forceinline__ void attn_flag(int status) { atomicOr(&g_attn_status, 1u << status); }
 
-struct Args {
-  Cache cache;
-  const void* q;
-  void* out;
-  int64_t q_token, q_head, out_token, out_head;
-  const int32_t *q_start, *kv_len, *table;
-  int64_t table_stride, requests, tokens, max_new;
-  int32_t window;  // 0: none
-  int32_t q_heads, group;
-  float scale;
-  int64_t* base;    // workspace: first work unit of each request, and the total
-  float* partials;  // workspace: two slots per warp of 8 rows x D sums, 8 references, 8 weights
-};
-
-constexpr int kSms = 152;
 constexpr int kRows = 8;             // query rows of a tile
 constexpr float kSlack = 6.f;        // log2 by which a score may pass the reference
 constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
@@ -99,58 +83,6 @@ constexpr int64_t partial_floats(int d) { return kRows * (int64_t)d + 2 * kRows;
 template <int D>
 constexpr int64_t kPartial = kRows * (int64_t)D + 2 * kRows;
 
-// What a request asks for.  Tiles of `tile` keys from tile0 on cover every key
-// that one of its tokens sees.
-struct Request {
-  int32_t first, n;      // its new tokens
-  int32_t len, pos0;     // keys held; position of its first new token (negative: that token sees nothing)
-  int32_t lo;            // first key that one of its tokens sees
-  int32_t tile0, tiles, row_tiles;  // row_tiles: tiles of eight query rows
-};
-
-__device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile, bool report) {
-  Request q;
-  q.first = a.q_start[r];
-  const int32_t end = a.q_start[r + 1];
-  int32_t len = a.kv_len[r];
-  const int64_t room = a.table_stride * a.cache.page_size;
-  bool bad = len < 0 || len > room;
-  q.n = end - q.first;
-  if (q.first < 0 || end < q.first || end > a.tokens || q.n > a.max_new) bad = true, q.n = 0;
-  len = max(len, 0);
-  q.pos0 = len - q.n;
-  q.len = (int32_t)min((int64_t)len, room);
-  q.lo = a.window ? max(0, max(q.pos0, 0) - (a.window - 1)) : 0;
-  q.tile0 = q.lo / tile;
-  q.tiles = q.n > 0 && q.len > q.lo ? (q.len - 1) / tile - q.tile0 + 1 : 0;
-  q.row_tiles = (int32_t)(((int64_t)q.n * a.group + kRows - 1) / kRows);
-  if (bad && report) attn_flag(KQ_ERR_RANGE);
-  return q;
-}
-__device__ __forceinline__ int64_t units_of(const Request& q, int kv_heads) {
-  return (int64_t)q.row_tiles * kv_heads * q.tiles;
-}
-
-// The work units cut into runs: the first `extra` of them per + 1 long, the others per.  No run is empty.
-struct Runs {
-  int64_t per, extra, count;
-  __device__ __forceinline__ Runs(int64_t total, int64_t most) {
-    count = min(most, (total + kLeastRun - 1) / kLeastRun);
-    per = count ? total / count : 0;
-    extra = total - per * count;
-  }
-  __device__ __forceinline__ int64_t start(int64_t i) const { return i * per + min(i, extra); }
-  __device__ __forceinline__ int64_t of(int64_t unit) const {
-    const int64_t cut = extra * (per + 1);
-    return unit < cut ? unit / (per + 1) : extra + (unit - cut) / per;
-  }
-};
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -169,37 +101,6 @@ __device__ __forceinline__ void mma_from(float (&d)[4], const float (&c)[4], uin
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// Two fp32 operations an instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
-
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
   if constexpr (N == 4) {
@@ -258,6 +159,11 @@ struct Row {
     x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
   }
 };
+
+__device__ __forceinline__ int32_t row_tiles(const Request& q) { return (q.rows + kRows - 1) / kRows; }
+__device__ __forceinline__ int64_t units_of(const Args& a, const Request& q) {
+  return q.rows > a.few_rows ? 0 : (int64_t)row_tiles(q) * a.cache.kv_heads * q.tiles;
+}
 
 // Position in the list of work units: request, row within it (key head outer,
 // query rows inner), tile.  Warp-uniform.
@@ -425,7 +331,7 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
 
 template <int kTile>
 __device__ __forceinline__ void enter_row(const Args& a, Cursor& c) {
-  const int32_t x = c.row % c.q.row_tiles * kRows;
+  const int32_t x = c.row % row_tiles(c.q) * kRows;
   const int32_t i0 = x / a.group, i1 = min(c.q.n - 1, (x + kRows - 1) / a.group);
   const int32_t hi = min(c.q.len, c.q.pos0 + i1 + 1);
   const int32_t lo = a.window ? max(0, c.q.pos0 + i0 - (a.window - 1)) : 0;
@@ -435,10 +341,10 @@ __device__ __forceinline__ void enter_row(const Args& a, Cursor& c) {
 template <int kTile>
 __device__ __forceinline__ void next_row(const Args& a, Cursor& c) {
   c.tile = 0;
-  if (++c.row == c.q.row_tiles * a.cache.kv_heads) {
+  if (++c.row == row_tiles(c.q) * a.cache.kv_heads) {
     c.row = 0;
-    do c.q = request_of(a, ++c.r, kTile, false);
-    while (units_of(c.q, a.cache.kv_heads) == 0);  // a unit remains, so some request has it
+    do c.q = request_of(a, ++c.r, kTile);
+    while (units_of(a, c.q) == 0);  // a unit remains, so some request has it
   }
   enter_row<kTile>(a, c);
 }
@@ -462,7 +368,7 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
   using C = Codes<Config<T, D>::kSplit>;
   constexpr float kZero = -8.f * (1 << C::kUnitLog) / 16777216.f;
   const int lane = threadIdx.x & 31, c = lane & 3;
-  const int32_t x = cur.row % cur.q.row_tiles * kRows + lane / 4, h = cur.row / cur.q.row_tiles;
+  const int32_t x = cur.row % row_tiles(cur.q) * kRows + lane / 4, h = cur.row / row_tiles(cur.q);
   const int32_t i = x / a.group;
   const bool live = i < cur.q.n;
   const int32_t pos = cur.q.pos0 + i;
@@ -532,7 +438,7 @@ __device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T,
   const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
   w.l += __shfl_xor_sync(~0u, w.l, 1);
   w.l += __shfl_xor_sync(~0u, w.l, 2);
-  const int32_t x0 = cur.row % cur.q.row_tiles * kRows, h = cur.row / cur.q.row_tiles;
+  const int32_t x0 = cur.row % row_tiles(cur.q) * kRows, h = cur.row / row_tiles(cur.q);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const float l = __shfl_sync(~0u, w.l, 8 * c + 4 * j);
@@ -593,6 +499,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   const int64_t run = (int64_t)me * kSms + blockIdx.x;
   const int chunks = (int)((a.requests + C::kThreads - 1) / C::kThreads);
   int64_t total = 0;
+  bool out_of_range = false;
   Cursor cur;
   cur.unit = cur.end = 0;
   for (int pass = 0; pass < (chunks > 1 ? 2 : 1); ++pass) {
@@ -601,7 +508,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       const int64_t r = (int64_t)ch * C::kThreads + tid;
       const bool mine = r < a.requests;
       int64_t u = 0;
-      if (mine) u = units_of(request_of(a, r, C::kTile, blockIdx.x == 0 && pass == 0), a.cache.kv_heads);
+      if (mine) u = units_of(a, request_of(a, r, C::kTile, &out_of_range));
       int64_t inc = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -622,7 +529,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       __syncthreads();
       if (pass == 0) total = sum;
       if (pass == 1 || chunks == 1) {
-        const Runs runs(total, (int64_t)kSms * C::kWarps);
+        const Runs runs(total, (int64_t)kSms * C::kWarps, kLeastRun);
         const int64_t u0 = runs.start(run), u1 = runs.start(run + 1);
         if (run < runs.count && u0 >= before && u0 < sum) {
           int l = 0, h = (int)min((int64_t)C::kThreads, a.requests - (int64_t)ch * C::kThreads);
@@ -632,7 +539,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
           }
           cur.unit = u0, cur.end = u1;
           cur.r = (int64_t)ch * C::kThreads + l;
-          cur.q = request_of(a, cur.r, C::kTile, false);
+          cur.q = request_of(a, cur.r, C::kTile);
           const int64_t in = u0 - s_first[l];
           cur.row = (int32_t)(in / cur.q.tiles);
           cur.tile = (int32_t)(in % cur.q.tiles);
@@ -641,7 +548,10 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       before = sum;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) a.base[a.requests] = total;
+  if (blockIdx.x == 0) {
+    if (tid == 0) a.base[a.requests] = total;
+    if (out_of_range) attn_flag(KQ_ERR_RANGE);
+  }
   if (cur.unit == cur.end) return;
   enter_row<C::kTile>(a, cur);
 
@@ -685,7 +595,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
           }
           const int32_t key = (g0 + i) * kGranule;
           if (id >= 0 && id < a.cache.pages) {
-            src[i] = ((int64_t)id * a.cache.kv_heads + cur.row / cur.q.row_tiles) * a.cache.block_bytes + sub * L::kBytes;
+            src[i] = ((int64_t)id * a.cache.kv_heads + cur.row / row_tiles(cur.q)) * a.cache.block_bytes + sub * L::kBytes;
             have |= 1u << i;
           } else if (key < cur.q.len && key + kGranule > cur.q.lo) {
             attn_flag(KQ_ERR_RANGE);  // (a page below a sliding window may be gone)
@@ -761,6 +671,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int heads_per_cta) {
   using C = Config<T, D>;
+  using P = PromptShape<D>;
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
   __shared__ int64_t s_request;
   __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
@@ -776,28 +687,43 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int he
   __syncthreads();
   const int64_t r = s_request;
   if (r < 0) return;
-  const Request q = request_of(a, r, C::kTile, false);
+  const Request q = request_of(a, r, C::kTile);
   const int32_t i = (int32_t)(t - q.first);
   if (i < 0 || i >= q.n) return;
-  const int64_t base = a.base[r];
-  const Runs runs(a.base[a.requests], (int64_t)kSms * C::kWarps);
+  const bool prompt = q.rows > a.few_rows;
+  const int rows = prompt ? P::kRows : kRows;  // of a partial result
+  const int64_t partial = prompt ? P::kPartial : kPartial<D>;
+  const float* parts = prompt ? a.prompt_partials : a.partials;
+  const Runs runs(prompt ? a.prompt_base[-1] : a.base[a.requests], prompt ? kSms : (int64_t)kSms * C::kWarps,
+                  prompt ? P::kLeastRun : kLeastRun);
+  const float unit = prompt ? 1.f : kOut<T, D>;
   const int h0 = (int)(blockIdx.x % per_token) * heads_per_cta;
   for (int h = h0; h < h0 + heads_per_cta; ++h) {
     const int32_t x = i * a.group + h % a.group;
     T* dst = static_cast<T*>(a.out) + t * a.out_token + (int64_t)h * a.out_head;
-    if (q.tiles == 0) {
+    // the units of the row tile that the query is in
+    int64_t lo;
+    int32_t tiles = q.tiles;
+    if (prompt) {
+      const int64_t block = a.prompt_first[r] + x / P::kRows;
+      if (block >= a.prompt_cap) return;  // overlapping requests, left out
+      tiles = row_block<D>(a, q, x / P::kRows).tiles;
+      lo = a.prompt_base[block] + (int64_t)(h / a.group) * tiles;
+    } else {
+      lo = a.base[r] + ((int64_t)(h / a.group) * row_tiles(q) + x / kRows) * tiles;
+    }
+    if (tiles == 0) {
       for (int e = tid; e < D; e += kCombineThreads) dst[e] = kv::from_float<T>(0.f);
       continue;
     }
-    const int64_t row = (int64_t)(h / a.group) * q.row_tiles + x / kRows;
-    const int64_t lo = base + row * q.tiles, hi = lo + q.tiles;
-    const int64_t w0 = runs.of(lo), w1 = runs.of(hi - 1);
+    const int64_t w0 = runs.of(lo), w1 = runs.of(lo + tiles - 1);
     if (w0 == w1) continue;
+    const int in = x % rows;
     float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
     for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
-      const float* p = a.partials + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * kPartial<D>;
-      const float m = p[kRows * D + x % kRows], l = p[kRows * D + kRows + x % kRows];
-      const float* o = p + (x % kRows) * D + lane * kPer;
+      const float* p = parts + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * partial;
+      const float m = p[rows * D + in], l = p[rows * D + rows + in];
+      const float* o = p + in * D + lane * kPer;
       const float now = fmaxf(ref, m);
       const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
       // a row of NaN scores keeps its reference at -inf and its weight NaN: it goes through
@@ -821,7 +747,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int he
         sum += s_sum[w][e] * f;
         l += s_ref[w] == -INFINITY ? s_weight[w] : s_weight[w] * f;
       }
-      dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (kOut<T, D> / l));
+      dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
     }
     __syncthreads();
   }
@@ -834,6 +760,9 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
       cudaFuncSetAttribute(attend_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (opted != cudaSuccess) return opted;
   if (cudaError_t e = launch_dependent(attend_kernel<T, D>, dim3(kSms), dim3(C::kThreads), C::kSmem, st, a)) return e;
+  if (a.few_rows != 0x7fffffff) {
+    if (cudaError_t e = launch_prompt(sizeof(T) == 4 ? -1 : (std::is_same_v<T, __half> ? KQ_F16 : KQ_BF16), D, a, st)) return e;
+  }
   const int heads = a.tokens * a.q_heads <= 4096 ? 1 : a.q_heads;
   return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(a.tokens * (a.q_heads / heads))), dim3(kCombineThreads), 0,
                           st, a, heads);
@@ -844,7 +773,36 @@ static cudaError_t launch(int d, const Args& a, cudaStream_t st) {
   return d == 64 ? launch<T, 64>(a, st) : (d == 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st));
 }
 
-static size_t base_bytes(int64_t requests) { return (size_t)((requests + 1) * 8 + 15) / 16 * 16; }
+// Query rows of a request from which on the prompt kernel takes it (16-bit queries).
+constexpr int32_t kFewRows = 32;
+
+// The workspace: byte offsets of its parts, and its size.
+struct Workspace {
+  size_t base, partials, prompt_first, prompt_base, prompt_partials, bytes;
+  int64_t prompt_cap;
+};
+static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t requests, int64_t tokens, int64_t max_new) {
+  const int d = c->head_dim;
+  const int64_t group = q_heads / c->kv_heads;
+  const bool prompts = std::min(max_new, tokens) > kFewRows / group;
+  const int64_t rows = d == 256 ? PromptShape<256>::kRows : PromptShape<128>::kRows;
+  const int64_t partial = d == 256 ? PromptShape<256>::kPartial : (d == 128 ? PromptShape<128>::kPartial : PromptShape<64>::kPartial);
+  Workspace w{};
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at += (size_t)round_up(bytes, 16);
+    return here;
+  };
+  w.base = take((requests + 1) * 8);
+  w.partials = take(2 * kSms * kMaxWarps * partial_floats(d) * 4);
+  w.prompt_first = take(prompts ? requests * 8 : 0);
+  w.prompt_cap = prompts ? tokens * group / rows + requests : 0;
+  w.prompt_base = take(prompts ? (w.prompt_cap + 1) * 8 : 0) + (prompts ? 8 : 0);
+  w.prompt_partials = take(prompts ? 2 * kSms * partial * 4 : 0);
+  w.bytes = at;
+  return w;
+}
 
 }  // namespace attn
 
@@ -879,8 +837,7 @@ size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_
                                int64_t max_new) {
   clear_error();
   if (check_attn(cache, q_heads, requests, tokens, max_new)) return 0;
-  const int d = cache->head_dim;
-  return attn::base_bytes(requests) + (size_t)(2 * attn::kSms * attn::kMaxWarps * attn::partial_floats(d)) * sizeof(float);
+  return attn::workspace(cache, q_heads, requests, tokens, max_new).bytes;
 }
 
 int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq_heads* q, const int32_t* d_q_start,
@@ -911,8 +868,16 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
   a.table_stride = table_stride, a.requests = requests, a.tokens = tokens, a.max_new = max_new;
   a.window = (int32_t)(window > 0x7fffffff ? 0x7fffffff : window);
   a.q_heads = q_heads, a.group = q_heads / cache->kv_heads, a.scale = scale;
-  a.base = static_cast<int64_t*>(d_ws);
-  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + attn::base_bytes(requests));
+  const attn::Workspace w = attn::workspace(cache, q_heads, requests, tokens, max_new);
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  a.base = reinterpret_cast<int64_t*>(ws + w.base);
+  a.partials = reinterpret_cast<float*>(ws + w.partials);
+  a.prompt_first = reinterpret_cast<int64_t*>(ws + w.prompt_first);
+  a.prompt_base = reinterpret_cast<int64_t*>(ws + w.prompt_base);
+  a.prompt_cap = w.prompt_cap;
+  a.prompt_partials = reinterpret_cast<float*>(ws + w.prompt_partials);
+  const bool prompts = dtype != KQ_F32 && std::min(max_new, tokens) > attn::kFewRows / a.group;
+  a.few_rows = prompts ? attn::kFewRows : 0x7fffffff;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32 ? attn::launch<float>(cache->head_dim, a, st)
                               : (dtype == KQ_F16 ? attn::launch<__half>(cache->head_dim, a, st)

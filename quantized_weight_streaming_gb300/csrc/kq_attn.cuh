@@ -1,0 +1,157 @@
+// What the attention kernels share: arguments, a request's extent, the cut of
+// the work into runs, small arithmetic.  kq_attn.cu: one to a few query rows a
+// request (and fp32 queries); kq_attn_prompt.cu: 16-bit prompts.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kq.h"
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace attn {
+
+using kv::Cache;
+using kv::kGranule;
+using kv::Layout;
+
+constexpr int kSms = 152;
+
+struct Args {
+  Cache cache;
+  const void* q;
+  void* out;
+  int64_t q_token, q_head, out_token, out_head;
+  const int32_t *q_start, *kv_len, *table;
+  int64_t table_stride, requests, tokens, max_new;
+  int32_t window;  // 0: none
+  int32_t q_heads, group;
+  float scale;
+  // requests with more query rows than this are the prompt kernel's
+  int32_t few_rows;
+  // workspace
+  int64_t* base;             // first work unit of each request, and the total
+  float* partials;           // two slots per run of kRows x D sums, kRows references, kRows weights
+  int64_t* prompt_first;     // first row block of each request
+  int64_t* prompt_base;      // first work unit of each row block; the total at [-1]
+  int64_t prompt_cap;        // row blocks that prompt_base has room for
+  float* prompt_partials;
+};
+
+// What a request asks for.  Tiles of `tile` keys from tile0 on cover every key
+// that one of its tokens sees.
+struct Request {
+  int32_t first, n;      // its new tokens
+  int32_t len, pos0;     // keys held; position of its first new token (negative: that token sees nothing)
+  int32_t lo;            // first key that one of its tokens sees
+  int32_t tile0, tiles;
+  int32_t rows;          // query rows of one key head
+};
+
+__device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile, bool* out_of_range = nullptr) {
+  Request q;
+  q.first = a.q_start[r];
+  const int32_t end = a.q_start[r + 1];
+  int32_t len = a.kv_len[r];
+  const int64_t room = a.table_stride * a.cache.page_size;
+  bool bad = len < 0 || len > room;
+  q.n = end - q.first;
+  if (q.first < 0 || end < q.first || end > a.tokens || q.n > a.max_new) bad = true, q.n = 0;
+  len = max(len, 0);
+  q.pos0 = len - q.n;
+  q.len = (int32_t)min((int64_t)len, room);
+  q.lo = a.window ? max(0, max(q.pos0, 0) - (a.window - 1)) : 0;
+  q.tile0 = q.lo / tile;
+  q.tiles = q.n > 0 && q.len > q.lo ? (q.len - 1) / tile - q.tile0 + 1 : 0;
+  q.rows = (int32_t)min((int64_t)0x7fffffff, (int64_t)q.n * a.group);
+  if (bad && out_of_range) *out_of_range = true;
+  return q;
+}
+
+// The prompt kernel's row blocks and key tiles (kq_attn_prompt.cu).
+template <int D>
+struct PromptShape {
+  static constexpr int kTiles = D == 256 ? 1 : 2;     // 128 query rows each
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kKeys = D == 256 ? 64 : 128;
+  static constexpr int kLeastRun = 4;                 // key tiles of a run
+  static constexpr int64_t kPartial = kRows * (int64_t)(D + 2);
+};
+
+// A block of query rows and the key tiles it looks at.
+struct RowBlock {
+  int32_t rows, lo, hi;  // keys lo .. hi - 1 are seen by some row
+  int32_t tile0, tiles;
+};
+template <int D>
+__device__ __forceinline__ RowBlock row_block(const Args& a, const Request& q, int32_t k) {
+  using S = PromptShape<D>;
+  RowBlock b;
+  const int32_t x0 = k * S::kRows;
+  b.rows = min(S::kRows, q.rows - x0);
+  const int32_t i0 = x0 / a.group, i1 = (x0 + b.rows - 1) / a.group;
+  b.hi = min(q.len, q.pos0 + i1 + 1);
+  b.lo = a.window ? max(0, q.pos0 + i0 - (a.window - 1)) : 0;
+  b.tile0 = b.lo / S::kKeys;
+  b.tiles = b.hi > b.lo ? (b.hi - 1) / S::kKeys - b.tile0 + 1 : 0;
+  return b;
+}
+
+// The work units cut into runs: the first `extra` of them per + 1 long, the others per.  No run is empty.
+struct Runs {
+  int64_t per, extra, count;
+  __device__ __forceinline__ Runs(int64_t total, int64_t most, int least) {
+    count = min(most, (total + least - 1) / least);
+    per = count ? total / count : 0;
+    extra = total - per * count;
+  }
+  __device__ __forceinline__ int64_t start(int64_t i) const { return i * per + min(i, extra); }
+  __device__ __forceinline__ int64_t of(int64_t unit) const {
+    const int64_t cut = extra * (per + 1);
+    return unit < cut ? unit / (per + 1) : extra + (unit - cut) / per;
+  }
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<__half2*>(&u)); }
+
+// Launches the prompt kernel for `dtype` KQ_F16 or KQ_BF16 (kq_attn_prompt.cu).
+cudaError_t launch_prompt(int dtype, int head_dim, const Args& a, cudaStream_t st);
+
+}  // namespace attn
+}  // namespace kq

@@ -1,0 +1,700 @@
+// Attention of prompts (16-bit queries, more than a few query rows a request)
+// over the paged 4-bit cache, on the 5th-generation tensor cores.
+//
+// With many query rows per key the work is a dense contraction: 4 D flops per
+// (query, key) pair against 4.5 bits per key value, so the tensor cores bound
+// it.  A CTA takes blocks of 256 query rows of one key head (two M tiles of
+// 128; at D = 256 one tile, for tensor memory holds 512 columns) and walks over
+// tiles of 128 keys (64 at D = 256):
+//
+//   S = Q K^T   tcgen05.mma, both operands in shared memory
+//   P = 2^(f S - m)  one thread per row, from and to tensor memory (fp16)
+//   O += P V    tcgen05.mma, P from tensor memory
+//
+// Keys and values become fp16 as they are unpacked (code - 8, exact, times the
+// scale, one rounding: the two roundings of K and V and that of P are each
+// 2^-12 at most, as the one of a 16-bit output, and independent); sums, maxima
+// and weights stay fp32.  Queries are scaled by a power of two per row, so bf16
+// loses nothing either.  Where a scale passes 8188 (the value would leave fp16)
+// the tile's keys or values are divided by 8, and scores or probabilities
+// multiplied by it.
+//
+// Roles: warp 0 copies granules into two raw stages; warp 1 issues the MMAs
+// (QK of the next item before PV of the last, so that the tensor cores work on
+// one M tile while the softmax of the other runs); warps 4-7 and 8-11 are the
+// softmax of the two M tiles; the rest unpack, into a ring of three buffers
+// that keys and values take in turn.  The reference m of a row moves only when
+// a score passes it by 8, and then its warp rescales O in tensor memory.
+//
+// Row blocks in order, each head's key tiles end to end, are cut into one run
+// of tiles per CTA, whatever the prompts' lengths and masks; a block cut
+// between CTAs leaves partial sums, which kq_attn.cu's combine kernel joins.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "kq_attn.cuh"
+#include "kq_device.cuh"
+#include "kq_internal.h"
+#include "kq_kv.cuh"
+#include "kq_tcgen05.cuh"
+
+namespace kq {
+namespace attn {
+
+using namespace tc;
+
+__device__ unsigned int g_prompt_status = 0;
+__device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_status, 1u << status); }
+
+constexpr int kPromptWarps = 14, kPromptThreads = 32 * kPromptWarps;
+constexpr float kPromptSlack = 8.f;
+
+template <int D>
+struct PromptConfig : PromptShape<D> {
+  using S = PromptShape<D>;
+  using L = Layout<D>;
+  static constexpr int kUnpackWarps = S::kTiles == 2 ? 4 : 8;
+  static constexpr int kGranules = S::kKeys / kGranule;          // of a key tile
+  static constexpr int kQBytes = 128 * D * 2;                    // one M tile
+  static constexpr int kBuffer = S::kKeys * D * 2;               // a tile of keys or values in fp16
+  static constexpr int kRaw = kGranules * L::kBytes;
+  static constexpr int kRing = S::kTiles * kQBytes;              // offsets
+  static constexpr int kRawAt = kRing + 3 * kBuffer;
+  static constexpr int kSmem = kRawAt + 2 * kRaw + 1024;         // and room to align to 1024
+  // tensor memory columns: S (and P over it), then O
+  static constexpr int kO = 2 * S::kKeys;
+  static constexpr int kColumns = 512;
+  static_assert(kO + S::kTiles * D <= kColumns, "tensor memory");
+};
+
+struct TileInfo {
+  float key_scale, value_scale;  // 1, or 8 where the tile was divided by 8
+  uint32_t nan;                  // a value scale of a visible key is not finite
+  uint32_t hidden;               // bit per granule whose page is missing
+};
+
+// Barriers that every role waits on with a limit; after one ran out all waits return at once, and the roles run through.
+struct Gate {
+  volatile int* abort;
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long start = clock64();
+    while (!mbar_try_wait_suspend(bar, parity)) {
+      if (*abort) return;
+      if (clock64() - start > kWaitLimitCycles) {
+        *abort = 1;
+        prompt_flag(KQ_ERR_TIMEOUT);
+        return;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+template <int N>
+__device__ __forceinline__ void load_raw(uint32_t (&w)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+// A pair of codes (low nibble of each half of v) minus 8, times d.
+__device__ __forceinline__ uint32_t value_pair(uint32_t v, __half2 d) {
+  const uint32_t magic = (v & 0x000F000Fu) | 0x64006400u;  // 1024 + q
+  return as_u32(__hmul2(__hsub2(as_h2(magic), as_h2(0x64086408u)), d));
+}
+
+// Keys of tokens 8 b .. 8 b + 7, slab sl: each lane a quarter of one token's groups, one 16-byte chunk a group.  The
+// eight dimensions of a chunk lie in the order 0 4 1 5 2 6 3 7, as the queries do.  Tokens of odd index take their
+// groups in the other order, so that a store's eight lanes fall on different banks.
+template <int D>
+__device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint8_t* buf, int b, int sl, float shrink) {
+  using C = PromptConfig<D>;
+  using L = Layout<D>;
+  constexpr int G = L::kGroups;
+  const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
+  const uint8_t* g0 = raw + (b / 2) * L::kBytes;
+  uint32_t w[G], ks[G / 2];
+  load_raw<G>(w, g0 + L::kKeys + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
+  const uint8_t* sp = g0 + L::kKeyScales + sl * L::kScaleSlab + ((b % 2) * 8 + r) * G * 2;
+  if constexpr (G == 4) {
+    load_raw<2>(ks, sp);
+  } else {
+    ks[0] = *reinterpret_cast<const uint32_t*>(sp);
+  }
+  const __half2 down = __float2half2_rn(shrink);
+#pragma unroll
+  for (int s = 0; s < G; ++s) {
+    const uint32_t v = r & 1 ? w[s ^ 1] : w[s];
+    const __half2 pair = __hmul2(as_h2(ks[s / 2]), down);
+    const __half2 d = ((r & 1) != 0) == (s % 2 == 0) ? __high2half2(pair) : __low2half2(pair);
+    uint4 o;
+    o.x = value_pair(v, d);
+    o.y = value_pair(v >> 4, d);
+    o.z = value_pair(v >> 8, d);
+    o.w = value_pair(v >> 12, d);
+    const int dim = sl * L::kSlabDim + 32 * (s ^ (r & 1));
+    const int chunk = (dim % 64) / 8 + c;
+    *reinterpret_cast<uint4*>(buf + (dim / 64) * (C::kKeys * 128) + (8 * b + r) * 128 + ((chunk ^ r) << 4)) = o;
+  }
+}
+
+// Values of tokens 8 b .. 8 b + 7, slab sl, transposed: row = dimension, the tile's keys along it.  A lane holds four
+// dimensions of two successive tokens and stores a pair of tokens a dimension; the lanes take their dimensions in
+// rotated order, so that a store's rows fall on different banks.
+template <int D>
+__device__ __forceinline__ void unpack_values(const uint8_t* raw, uint8_t* buf, int b, int sl, float shrink, uint32_t valid) {
+  using L = Layout<D>;
+  constexpr int G = L::kGroups;
+  const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
+  const uint8_t* g0 = raw + (b / 2) * L::kBytes;
+  uint32_t w[G], vs[G];
+  load_raw<G>(w, g0 + L::kValues + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
+  load_raw<G>(vs, g0 + L::kValueScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
+  const __half2 down = __float2half2_rn(shrink);
+  __half2 d[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const uint32_t u = __byte_perm(vs[g / 2], vs[G / 2 + g / 2], g % 2 ? 0x7632 : 0x5410);
+    // hidden keys and scales that are not finite count as zero (those keys' rows are marked by the softmax)
+    const uint32_t ok = __hle2_mask(__habs2(as_h2(u)), as_h2(0x7BFF7BFFu)) & valid;
+    d[g] = __hmul2(as_h2(u & ok), down);
+  }
+  uint8_t* base = buf + (b / 8) * (D * 128) + (sl * L::kSlabDim + 4 * r) * 128 + 4 * c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = (j + (r >> 1)) & 3, row = (4 * r + e) & 7;
+    uint8_t* at = base + e * 128 + (((b % 8) ^ row) << 4);
+#pragma unroll
+    for (int g = 0; g < G; ++g) *reinterpret_cast<uint32_t*>(at + g * 32 * 128) = value_pair(w[g] >> (4 * e), d[g]);
+  }
+}
+
+// The run's position: request, row block, key head, key tile.
+struct Place {
+  int64_t r;
+  int32_t k, h, tile;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
+  using C = PromptConfig<D>;
+  using L = Layout<D>;
+  constexpr int N = C::kKeys;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t raw_full[2], raw_empty[2], buf_full[3], buf_empty[3], s_full[2], p_full[2], pv_done[2];
+  __shared__ TileInfo s_info[4];
+  __shared__ uint8_t s_nan[4][N];     // groups of a key whose value scale is not finite
+  __shared__ uint32_t s_hidden[2];    // of a raw stage
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ int64_t s_entry[kPromptThreads];  // row blocks before each request of a chunk
+  __shared__ int64_t s_sum[kPromptWarps];
+  __shared__ Place s_place;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], C::kUnpackWarps);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&buf_full[i], C::kUnpackWarps);
+      mbar_init(&buf_empty[i], 1);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, C::kColumns);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+
+  // ---- the work units before each row block, and where this CTA's run begins ----
+  auto block_sum = [&](int64_t v, int64_t& before, int64_t& all) {  // exclusive sum over the CTA
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    before = inc - v, all = 0;
+    for (int i = 0; i < kPromptWarps; ++i) {
+      if (i < warp) before += s_sum[i];
+      all += s_sum[i];
+    }
+  };
+  int64_t unit = 0, end = 0;  // this CTA's run
+  {
+    int64_t total = 0;
+    const bool writer = blockIdx.x == 0;
+    for (int pass = 0; pass < 2; ++pass) {
+      int64_t units = 0, entries = 0;
+      for (int64_t r0 = 0; r0 < a.requests; r0 += kPromptThreads) {
+        int64_t blocks = 0;
+        if (r0 + tid < a.requests) {
+          const Request q = request_of(a, r0 + tid, N);
+          blocks = q.rows > a.few_rows ? (q.rows + C::kRows - 1) / C::kRows : 0;
+        }
+        int64_t before, all;
+        block_sum(blocks, before, all);
+        s_entry[tid] = before;
+        if (writer && pass == 0 && r0 + tid < a.requests) a.prompt_first[r0 + tid] = entries + before;
+        __syncthreads();
+        const int in_chunk = (int)min((int64_t)kPromptThreads, a.requests - r0);
+        for (int64_t e0 = 0; e0 < all; e0 += kPromptThreads) {
+          const int64_t e = e0 + tid;
+          int64_t u = 0, at, sum;
+          Place p{};
+          int32_t tiles = 0;
+          if (e < all && entries + e < a.prompt_cap) {
+            int l = 0, h = in_chunk;
+            while (h - l > 1) {  // the last request whose first row block is not after e
+              const int m = (l + h) >> 1;
+              if (s_entry[m] <= e) l = m; else h = m;
+            }
+            p.r = r0 + l, p.k = (int32_t)(e - s_entry[l]);
+            tiles = row_block<D>(a, request_of(a, p.r, N), p.k).tiles;
+            u = (int64_t)tiles * a.cache.kv_heads;
+          }
+          block_sum(u, at, sum);
+          if (writer && pass == 0 && e < all && entries + e < a.prompt_cap) a.prompt_base[entries + e] = units + at;
+          if (pass == 1 && u > 0 && unit >= units + at && unit < units + at + u) {
+            const int64_t in = unit - units - at;
+            p.h = (int32_t)(in / tiles), p.tile = (int32_t)(in % tiles);
+            s_place = p;
+          }
+          units += sum;
+        }
+        entries += all;
+        __syncthreads();  // s_entry has been read
+      }
+      if (pass == 0) {
+        total = units;
+        if (writer && tid == 0) a.prompt_base[-1] = total;
+        const Runs runs(total, kSms, C::kLeastRun);
+        if (blockIdx.x < runs.count) unit = runs.start(blockIdx.x), end = runs.start(blockIdx.x + 1);
+        if (unit == end) break;  // the same for the whole CTA
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  if (unit < end) {
+    const Gate gate{&s_abort};
+    Place at = s_place;
+    Request q = request_of(a, at.r, N);
+    RowBlock blk = row_block<D>(a, q, at.k);
+    // counts that the roles carry over the segments: raw stages (copies and unpacking), buffers, uses of the S buffers
+    uint32_t raws = 0, bufs = 0, uses[2] = {0, 0};
+    bool first = true;
+    while (unit < end) {
+      // next row: heads, then blocks, then requests
+      if (at.tile == blk.tiles) {
+        at.tile = 0;
+        if (++at.h == a.cache.kv_heads) {
+          at.h = 0;
+          do {
+            if (++at.k >= (q.rows + C::kRows - 1) / C::kRows || q.rows <= a.few_rows) {
+              at.k = 0;
+              do q = request_of(a, ++at.r, N);
+              while (q.rows <= a.few_rows);  // a unit remains, so some request has it
+            }
+            blk = row_block<D>(a, q, at.k);
+          } while (blk.tiles == 0);
+        }
+      }
+      const int32_t from = at.tile, to = (int32_t)min((int64_t)blk.tiles, from + (end - unit));
+      const int nm = blk.rows > 128 ? 2 : 1;
+      const int items = (to - from) * nm;
+
+      // ---- queries: one thread a row ----
+      const bool softmax = warp >= 4 && warp < 4 + 4 * C::kTiles;
+      const int m_tile = (warp - 4) / 4;
+      const int row = (warp & 3) * 32 + lane;       // tensor memory lane
+      const int32_t x = at.k * C::kRows + m_tile * 128 + row, i = x / a.group;
+      const bool live = softmax && m_tile * 128 + row < blk.rows;
+      const int32_t pos = q.pos0 + i;
+      const int32_t key_hi = live ? max(0, min(pos + 1, q.len)) : 0x7fffffff;
+      const int32_t key_lo = live && a.window ? max(0, pos - (a.window - 1)) : 0;
+      float factor = 0.f;
+      if (softmax && m_tile < nm) {
+        const T* src = static_cast<const T*>(a.q) + (int64_t)(q.first + i) * a.q_token +
+                       (int64_t)(at.h * a.group + x % a.group) * a.q_head;
+        float top = 0.f;
+        if (live) {
+          for (int e = 0; e < D; e += 8) {
+            float v[8];
+            kv::load8(src + e, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+          }
+        }
+        int e2 = 0;
+        if (top > 0.f && top <= 3.402823466e38f) frexpf(top, &e2);
+        e2 = min(max(8 - e2, -110), 110);  // the row times 2^e2 lies below 2^8
+        // the scale's sign goes with the queries, so that larger sums are larger scores
+        const float up = a.scale == 0.f ? 0.f : copysignf(ldexpf(1.f, e2), a.scale);
+        factor = ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2);
+        uint8_t* dst = smem + m_tile * C::kQBytes + row * 128;
+        for (int e = 0; e < D; e += 8) {
+          float v[8] = {};
+          if (live) kv::load8(src + e, v);
+          uint4 o;
+          o.x = pack2(v[0] * up, v[4] * up), o.y = pack2(v[1] * up, v[5] * up);
+          o.z = pack2(v[2] * up, v[6] * up), o.w = pack2(v[3] * up, v[7] * up);
+          *reinterpret_cast<uint4*>(dst + (e / 64) * (128 * 128) + (((e % 64 / 8) ^ (row & 7)) << 4)) = o;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncthreads();
+
+      if (warp == 0) {
+        // ---- copies ----
+        const uint64_t policy = l2_policy_evict_first();
+        const int per_page = a.cache.page_size / kGranule;
+        const int32_t pages = (q.len + a.cache.page_size - 1) / a.cache.page_size;
+        const int32_t* table = a.table + at.r * a.table_stride;
+        auto page_id = [&](int32_t t) -> int32_t {
+          const int32_t page = ((blk.tile0 + t) * C::kGranules + lane) / per_page;
+          return lane < C::kGranules && page < pages ? table[page] : -1;
+        };
+        int32_t next = page_id(from);
+        for (int32_t t = from; t < to; ++t, ++raws) {
+          const int st = raws & 1;
+          const int32_t id = next;
+          if (t + 1 < to) next = page_id(t + 1);
+          if (raws >= 2) gate.wait(&raw_empty[st], (raws / 2 - 1) & 1);
+          const int32_t granule = (blk.tile0 + t) * C::kGranules + lane, key = granule * kGranule;
+          const bool here = lane < C::kGranules && id >= 0 && id < a.cache.pages;
+          if (lane < C::kGranules && !here && key < blk.hi && key + kGranule > blk.lo) prompt_flag(KQ_ERR_RANGE);
+          const uint32_t have = __ballot_sync(~0u, here);
+          if (lane == 0) {
+            s_hidden[st] = ~have & ((1u << C::kGranules) - 1);
+            mbar_arrive_expect_tx(&raw_full[st], __popc(have) * L::kBytes);
+          }
+          __syncwarp();
+          if (here)
+            bulk_g2s(smem + C::kRawAt + st * C::kRaw + lane * L::kBytes,
+                     a.cache.data + ((int64_t)id * a.cache.kv_heads + at.h) * a.cache.block_bytes +
+                         (granule % per_page) * L::kBytes,
+                     L::kBytes, &raw_full[st], policy);
+        }
+      } else if (warp == 1) {
+        // ---- matrix products ----
+        if (elect_one()) {
+          const uint32_t qk = idesc_f16(128, N), pv = idesc_f16(128, D);
+          auto values = [&](int n) {  // O += P V of item n
+            const int j = n / nm, m = n % nm, b = n & 1;
+            const uint32_t vb = bufs + 2 * j + 1;
+            gate.wait(&p_full[b], (uses[b] + n / 2) & 1);
+            if (m == 0) gate.wait(&buf_full[vb % 3], (vb / 3) & 1);
+            tc_fence_after();
+            const uint64_t bd = sw128_desc(smem + C::kRing + (vb % 3) * C::kBuffer);
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k)
+              tc_mma_ts(tmem + C::kO + m * D, tmem + b * N + k * 8, bd + (uint64_t)(((k / 4) * D * 128 + (k % 4) * 32) >> 4), pv,
+                        j > 0 || k > 0);
+            tc_commit(&pv_done[b]);
+            if (m == nm - 1) tc_commit(&buf_empty[vb % 3]);
+          };
+          for (int n = 0; n < items; ++n) {
+            const int j = n / nm, m = n % nm, b = n & 1;
+            const uint32_t kb = bufs + 2 * j;
+            if (m == 0) gate.wait(&buf_full[kb % 3], (kb / 3) & 1);
+            if (n >= 2) gate.wait(&pv_done[b], (uses[b] + n / 2 - 1) & 1);  // S and P of the buffer's last item are read
+            tc_fence_after();
+            const uint64_t ad = sw128_desc(smem + m * C::kQBytes), bd = sw128_desc(smem + C::kRing + (kb % 3) * C::kBuffer);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc_mma_ss(tmem + b * N, ad + (uint64_t)(((k / 4) * 128 * 128 + (k % 4) * 32) >> 4),
+                        bd + (uint64_t)(((k / 4) * N * 128 + (k % 4) * 32) >> 4), qk, k > 0);
+            tc_commit(&s_full[b]);
+            if (m == nm - 1) tc_commit(&buf_empty[kb % 3]);
+            if (n >= 1) values(n - 1);
+          }
+          values(items - 1);
+        }
+        __syncwarp();
+      } else if (softmax) {
+        // ---- softmax ----
+        if (m_tile < nm) {
+          float ref = -INFINITY, weight = 0.f;
+          uint32_t nan_groups = 0;
+          const int32_t all_lo = __reduce_max_sync(~0u, key_lo), all_hi = __reduce_min_sync(~0u, key_hi);
+          const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor memory address of the warp's lanes
+          for (int n = m_tile; n < items; n += nm) {
+            const int b = n & 1;
+            const int32_t key0 = (blk.tile0 + from + n / nm) * N;
+            gate.wait(&s_full[b], (uses[b] + n / 2) & 1);
+            __syncwarp();
+            tc_fence_after();
+            const TileInfo info = s_info[(bufs / 2 + n / nm) & 3];
+            const float f = factor * info.key_scale;
+            const bool masked = info.hidden || key0 < all_lo || key0 + N > all_hi;
+            const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
+            uint32_t p[N / 2];
+            float sum = 0.f, top;
+            auto pass = [&]() {  // p = 2^(f S - ref), and the largest f S
+              const float minus = ref == -INFINITY ? 0.f : -ref;
+              float2 acc = make_float2(0.f, 0.f);
+              top = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < N / 32; ++c) {
+                uint32_t s[32];
+                tmem_ld32(tmem + lanes + b * N + 32 * c, s);
+                tmem_ld_wait();
+                if (masked) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) {
+                    const int key = 32 * c + e;
+                    if (key < rel_lo || key >= rel_hi || (info.hidden >> (key / kGranule) & 1u)) s[e] = 0xFF800000u;  // -inf
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const float2 v = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                  top = fmaxf(top, fmaxf(v.x, v.y));
+                  float2 y = fma2(v, make_float2(f, f), make_float2(minus, minus));
+                  y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                  acc = add2(acc, y);
+                  p[16 * c + e / 2] = pack2(y.x, y.y);
+                }
+              }
+              sum = acc.x + acc.y;
+              top *= f;
+            };
+            pass();
+            const bool moves = top > ref + kPromptSlack;
+            if (__any_sync(~0u, moves)) {
+              const float keep = !moves ? 1.f : (ref == -INFINITY ? 0.f : exp2_approx(ref - top));
+              if (moves) ref = top;
+              weight *= keep;
+              pass();
+              if (n >= nm) {  // rescale what earlier tiles left in O, once the last of them is in
+                const int before = n - nm;
+                gate.wait(&pv_done[before & 1], (uses[before & 1] + before / 2) & 1);
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
+                  tmem_ld_wait();
+                  uint32_t u[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * keep);
+                  tmem_st16(tmem + lanes + C::kO + m_tile * D + c, u);
+                }
+              }
+            }
+            weight += sum;
+            if (info.value_scale != 1.f) {
+#pragma unroll
+              for (int e = 0; e < N / 2; ++e) p[e] = as_u32(__hmul2(as_h2(p[e]), __float2half2_rn(8.f)));
+            }
+            if (info.nan) {
+              for (int e = 0; e < N; ++e)
+                if (e >= rel_lo && e < rel_hi) nan_groups |= s_nan[(bufs / 2 + n / nm) & 3][e];
+            }
+#pragma unroll
+            for (int c = 0; c < N / 2; c += 16) {
+              uint32_t u[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[e] = p[c + e];
+              tmem_st16(tmem + lanes + b * N + c, u);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[b]);
+          }
+          // ---- the block's rows ----
+          const int last = (items - 1 - m_tile) / nm * nm + m_tile;
+          gate.wait(&pv_done[last & 1], (uses[last & 1] + last / 2) & 1);
+          __syncwarp();
+          tc_fence_after();
+          const bool whole = from == 0 && to == blk.tiles;
+          const int in = m_tile * 128 + row;
+          float* part = a.prompt_partials + (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * C::kPartial;
+          T* dst = static_cast<T*>(a.out) + (int64_t)(q.first + i) * a.out_token +
+                   (int64_t)(at.h * a.group + x % a.group) * a.out_head;
+          const float scale = whole ? (weight == 0.f ? 0.f : 1.f / weight) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
+            tmem_ld_wait();
+            if (live) {
+              const float poison = nan_groups >> (c / 32) & 1u ? NAN : 0.f;
+              float lo[8], hi[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) lo[e] = o[e] * scale + poison, hi[e] = o[8 + e] * scale + poison;
+              if (whole) {
+                kv::store8(dst + c, lo);
+                kv::store8(dst + c + 8, hi);
+              } else {
+                kv::store8(part + in * D + c, lo);
+                kv::store8(part + in * D + c + 8, hi);
+              }
+            }
+            __syncwarp();
+          }
+          if (!whole && live) {
+            part[C::kRows * D + in] = ref;
+            part[C::kRows * D + C::kRows + in] = weight;
+          }
+          tc_fence_before();
+        }
+      } else {
+        // ---- unpacking ----
+        const int me = warp < 4 ? warp - 2 : warp - (C::kTiles == 2 ? 10 : 6);
+        for (int32_t t = from; t < to; ++t, ++raws) {
+          const int st = raws & 1;
+          const uint8_t* raw = smem + C::kRawAt + st * C::kRaw;
+          gate.wait(&raw_full[st], (raws / 2) & 1);
+          __syncwarp();
+          const uint32_t hidden = s_hidden[st];
+          const int32_t key0 = (blk.tile0 + t) * N;
+          const bool dirty = hidden || key0 < blk.lo || key0 + N > blk.hi;
+          // the largest scales of the tile (as bits: NaN above infinity above the numbers)
+          uint32_t top_k = 0, top_v = 0;
+          {
+            constexpr int kPer = C::kGranules * 2 * D / 32;  // bytes a lane
+            const int at_byte = lane * kPer, g = at_byte / (2 * D), in = at_byte % (2 * D);
+            const uint8_t* p = raw + g * L::kBytes + L::kKeyScales + in;
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < kPer; e += 4) {
+              uint32_t u = *reinterpret_cast<const uint32_t*>(p + e) & 0x7FFF7FFFu;
+              if (dirty) {  // hidden keys' scales may be anything; a word holds two groups of one token
+                const int32_t key = key0 + g * kGranule + (in + e) % D % L::kScaleSlab / (2 * L::kGroups);
+                if (key < blk.lo || key >= blk.hi || (hidden >> g & 1u)) u = 0;
+              }
+              top = __vmaxu2(top, u);
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            top_k = __reduce_max_sync(~0u, in < D ? top : 0u);
+            top_v = __reduce_max_sync(~0u, in < D ? 0u : top);
+          }
+          const float k_down = top_k > 0x6FFFu ? 0.125f : 1.f, v_down = top_v > 0x6FFFu ? 0.125f : 1.f;
+          if (me == 0) {
+            const int slot = (bufs / 2 + t - from) & 3;
+            if (top_v >= 0x7C00u) {
+              for (int e = lane; e < N; e += 32) {
+                uint32_t groups = 0;
+                const int32_t key = key0 + e;
+                if (key >= blk.lo && key < blk.hi && !(hidden >> (e / kGranule) & 1u)) {
+                  for (int gq = 0; gq < D / 32; ++gq) {
+                    const uint16_t u = *reinterpret_cast<const uint16_t*>(raw + (e / kGranule) * L::kBytes + D +
+                                                                          L::key_scale(e % kGranule, gq));
+                    groups |= (uint32_t)((u & 0x7FFFu) >= 0x7C00u) << gq;
+                  }
+                }
+                s_nan[slot][e] = (uint8_t)groups;
+              }
+            }
+            if (lane == 0) s_info[slot] = TileInfo{1.f / k_down, 1.f / v_down, top_v >= 0x7C00u, hidden};
+            __syncwarp();
+          }
+          const uint32_t kb = bufs + 2 * (t - from);
+          if (kb >= 3) gate.wait(&buf_empty[kb % 3], (kb / 3 - 1) & 1);
+          uint8_t* buf = smem + C::kRing + (kb % 3) * C::kBuffer;
+#pragma unroll 2
+          for (int w = me; w < N / 8 * L::kSlabs; w += C::kUnpackWarps) unpack_keys<D>(raw, buf, w / L::kSlabs, w % L::kSlabs, k_down);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&buf_full[kb % 3]);
+          const uint32_t vb = kb + 1;
+          if (vb >= 3) gate.wait(&buf_empty[vb % 3], (vb / 3 - 1) & 1);
+          buf = smem + C::kRing + (vb % 3) * C::kBuffer;
+#pragma unroll 2
+          for (int w = me; w < N / 8 * L::kSlabs; w += C::kUnpackWarps) {
+            const int b = w / L::kSlabs;
+            uint32_t valid = ~0u;
+            if (dirty) {
+              const int32_t key = key0 + 8 * b + 2 * (lane & 3);
+              const bool held = !(hidden >> (b / 2) & 1u);
+              valid = (held && key >= blk.lo && key < blk.hi ? 0xFFFFu : 0u) |
+                      (held && key + 1 >= blk.lo && key + 1 < blk.hi ? 0xFFFF0000u : 0u);
+            }
+            unpack_values<D>(raw, buf, b, w % L::kSlabs, v_down, valid);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&buf_full[vb % 3]);
+            mbar_arrive(&raw_empty[st]);
+          }
+        }
+      }
+      __syncthreads();
+      tc_fence_after();
+      bufs += 2 * (to - from);
+      uses[0] += (items + 1) / 2, uses[1] += items / 2;
+      first = false;
+      unit += to - from;
+      at.tile = to;
+    }
+    if (s_abort) {
+      // a wait ran out: give the copies and products in flight the same time before their memory goes away
+      if (tid == 0)
+        for (uint32_t n = raws > 2 ? raws - 2 : 0; n < raws; ++n) mbar_wait_bounded(&raw_full[n & 1], (n / 2) & 1);
+      if (warp == 1 && elect_one()) {
+        tc_commit(&pv_done[0]);
+        mbar_wait_bounded(&pv_done[0], uses[0] & 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::kColumns);
+}
+
+template <typename T, int D>
+static cudaError_t launch(const Args& a, cudaStream_t st) {
+  using C = PromptConfig<D>;
+  static const cudaError_t opted =
+      cudaFuncSetAttribute(prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (opted != cudaSuccess) return opted;
+  return launch_dependent(prompt_kernel<T, D>, dim3(kSms), dim3(kPromptThreads), C::kSmem, st, a);
+}
+
+template <typename T>
+static cudaError_t launch(int d, const Args& a, cudaStream_t st) {
+  return d == 64 ? launch<T, 64>(a, st) : (d == 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st));
+}
+
+cudaError_t launch_prompt(int dtype, int head_dim, const Args& a, cudaStream_t st) {
+  return dtype == KQ_F16 ? launch<__half>(head_dim, a, st) : launch<__nv_bfloat16>(head_dim, a, st);
+}
+
+}  // namespace attn
+
+int read_prompt_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, attn::g_prompt_status, sizeof(v)) != cudaSuccess) return -1;
+  if (clear && v) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(attn::g_prompt_status, &z, sizeof(z)) != cudaSuccess) return -1;
+  }
+  return (int)v;
+}
+
+}  // namespace kq

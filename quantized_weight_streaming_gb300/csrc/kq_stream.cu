@@ -1306,6 +1306,7 @@ int read_prep_status(int clear);     // kq_prep.cu
 int read_control_status(int clear);  // kq_control.cu
 int read_kv_status(int clear);       // kq_kv.cu
 int read_attn_status(int clear);     // kq_attn.cu
+int read_prompt_status(int clear);   // kq_attn_prompt.cu
 
 }  // namespace kq
 
@@ -1982,9 +1983,11 @@ int kq_device_status(int clear) {
   KQ_CUDA_TRY(cudaDeviceSynchronize());
   int a = read_stream_status(clear), b = read_prep_status(clear), c = read_tc_status(clear);
   int d = read_control_status(clear), t = read_tcs_status(clear), k = read_kv_status(clear), e = read_attn_status(clear);
-  if (a < 0 || b < 0 || c < 0 || d < 0 || t < 0 || k < 0 || e < 0)
+  int p = read_prompt_status(clear);
+  if (a < 0 || b < 0 || c < 0 || d < 0 || t < 0 || k < 0 || e < 0 || p < 0)
     return fail(KQ_ERR_CUDA, "reading the device status word failed");
-  const unsigned v = (unsigned)a | (unsigned)b | (unsigned)c | (unsigned)d | (unsigned)t | (unsigned)k | (unsigned)e;
+  const unsigned v = (unsigned)a | (unsigned)b | (unsigned)c | (unsigned)d | (unsigned)t | (unsigned)k | (unsigned)e |
+                     (unsigned)p;
   if (v & (1u << KQ_ERR_TIMEOUT)) return fail(KQ_ERR_TIMEOUT, "a bounded device wait expired");
   if (v & (1u << KQ_ERR_NONFINITE)) return fail(KQ_ERR_NONFINITE, "non-finite weight, key or value met on the device");
   if (v & (1u << KQ_ERR_RANGE)) return fail(KQ_ERR_RANGE, "scale overflowed fp16, or an id, length, position, slot or page out of range, on the device");
