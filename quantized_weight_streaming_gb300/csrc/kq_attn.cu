@@ -61,6 +61,7 @@ constexpr int kRows = 8;             // query rows of a tile
 constexpr float kSlack = 6.f;        // log2 by which a score may pass the reference
 constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
 constexpr int kCombineThreads = 256;
+constexpr int kWideRows = 2048;      // query rows up to which a CTA joins one
 constexpr int kLeastRun = 2;         // tiles of a run, where there are fewer than two for every warp
 
 template <typename T, int D>
@@ -665,21 +666,21 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   }
 }
 
-// Rows that were cut between warps: their parts joined in run order; rows that
-// see nothing: zeros.  One CTA per token (or, where these are few, per token
-// and head); the parts of a row are shared out over the CTA's warps.
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int heads_per_cta) {
+// Rows that were cut between runs: their parts joined in run order; rows that
+// see nothing: zeros.  kWide: a CTA per token and query head, whose warps share
+// out the parts of the row (a short list of rows, each in many parts).
+// Otherwise a CTA per token, a warp per key head (many rows, few of them cut).
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a) {
   using C = Config<T, D>;
   using P = PromptShape<D>;
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
   __shared__ int64_t s_request;
-  __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
+  __shared__ float s_sum[kWide ? kWarps : 1][D], s_ref[kWarps], s_weight[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int per_token = a.q_heads / heads_per_cta;
-  const int64_t t = blockIdx.x / per_token;
+  const int64_t t = kWide ? blockIdx.x / a.q_heads : blockIdx.x;
   if (tid == 0) s_request = -1;
   __syncthreads();
   for (int64_t r = tid; r < a.requests; r += kCombineThreads)
@@ -697,59 +698,68 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int he
   const Runs runs(prompt ? a.prompt_base[-1] : a.base[a.requests], prompt ? kSms : (int64_t)kSms * C::kWarps,
                   prompt ? P::kLeastRun : kLeastRun);
   const float unit = prompt ? 1.f : kOut<T, D>;
-  const int h0 = (int)(blockIdx.x % per_token) * heads_per_cta;
-  for (int h = h0; h < h0 + heads_per_cta; ++h) {
-    const int32_t x = i * a.group + h % a.group;
-    T* dst = static_cast<T*>(a.out) + t * a.out_token + (int64_t)h * a.out_head;
-    // the units of the row tile that the query is in
-    int64_t lo;
-    int32_t tiles = q.tiles;
-    if (prompt) {
-      const int64_t block = a.prompt_first[r] + x / P::kRows;
-      if (block >= a.prompt_cap) return;  // overlapping requests, left out
-      tiles = row_block<D>(a, q, x / P::kRows).tiles;
-      lo = a.prompt_base[block] + (int64_t)(h / a.group) * tiles;
-    } else {
-      lo = a.base[r] + ((int64_t)(h / a.group) * row_tiles(q) + x / kRows) * tiles;
-    }
-    if (tiles == 0) {
-      for (int e = tid; e < D; e += kCombineThreads) dst[e] = kv::from_float<T>(0.f);
-      continue;
-    }
-    const int64_t w0 = runs.of(lo), w1 = runs.of(lo + tiles - 1);
-    if (w0 == w1) continue;
-    const int in = x % rows;
-    float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
-    for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
-      const float* p = parts + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * partial;
-      const float m = p[rows * D + in], l = p[rows * D + rows + in];
-      const float* o = p + in * D + lane * kPer;
-      const float now = fmaxf(ref, m);
-      const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
-      // a row of NaN scores keeps its reference at -inf and its weight NaN: it goes through
-      weight = weight * keep + (m == -INFINITY ? l : l * f);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[e] * f;
-      ref = now;
-    }
-    if (lane == 0) s_ref[warp] = ref, s_weight[warp] = weight;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = acc[e];
-    __syncthreads();
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w]);
-    for (int e = tid; e < D; e += kCombineThreads) {
-      float sum = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = s_ref[w] == -INFINITY ? 0.f : exp2_approx(s_ref[w] - top);
-        sum += s_sum[w][e] * f;
-        l += s_ref[w] == -INFINITY ? s_weight[w] : s_weight[w] * f;
+  const int one = kWide ? blockIdx.x % a.q_heads : 0;
+  int64_t w0 = 0, w1 = 0, lo = 0;
+  int32_t tiles = 0, known = -1;  // of row tile `known` of key head hk
+  for (int hk = kWide ? one / a.group : warp; hk < (kWide ? one / a.group + 1 : a.cache.kv_heads); hk += kWarps, known = -1) {
+    for (int g = kWide ? one % a.group : 0; g < (kWide ? one % a.group + 1 : a.group); ++g) {
+      const int32_t x = i * a.group + g, tile = x / rows, in = x - tile * rows;
+      if (tile != known) {
+        known = tile;
+        tiles = q.tiles;
+        if (prompt) {
+          const int64_t block = a.prompt_first[r] + tile;
+          if (block >= a.prompt_cap) return;  // overlapping requests, left out
+          tiles = row_block<D>(a, q, tile).tiles;
+          lo = a.prompt_base[block] + (int64_t)hk * tiles;
+        } else {
+          lo = a.base[r] + ((int64_t)hk * row_tiles(q) + tile) * tiles;
+        }
+        if (tiles) w0 = runs.of(lo), w1 = runs.of(lo + tiles - 1);
       }
-      dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
+      T* dst = static_cast<T*>(a.out) + t * a.out_token + (int64_t)(hk * a.group + g) * a.out_head;
+      if (tiles == 0) {
+        for (int e = kWide ? tid : lane; e < D; e += kWide ? kCombineThreads : 32) dst[e] = kv::from_float<T>(0.f);
+        continue;
+      }
+      if (w0 == w1) continue;
+      float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
+      for (int64_t w = w0 + (kWide ? warp : 0); w <= w1; w += kWide ? kWarps : 1) {
+        const float* p = parts + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * partial;
+        const float m = p[rows * D + in], l = p[rows * D + rows + in];
+        const float* o = p + (int64_t)in * D + lane * kPer;
+        const float now = fmaxf(ref, m);
+        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
+        // a row of NaN scores keeps its reference at -inf and its weight NaN: it goes through
+        weight = weight * keep + (m == -INFINITY ? l : l * f);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[e] * f;
+        ref = now;
+      }
+      if constexpr (!kWide) {
+        const float f = weight == 0.f ? 0.f : unit / weight;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) dst[lane * kPer + e] = kv::from_float<T>(acc[e] * f);
+      } else {
+        if (lane == 0) s_ref[warp] = ref, s_weight[warp] = weight;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = acc[e];
+        __syncthreads();
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w]);
+        for (int e = tid; e < D; e += kCombineThreads) {
+          float sum = 0.f, l = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float f = s_ref[w] == -INFINITY ? 0.f : exp2_approx(s_ref[w] - top);
+            sum += s_sum[w][e] * f;
+            l += s_ref[w] == -INFINITY ? s_weight[w] : s_weight[w] * f;
+          }
+          dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
+        }
+      }
     }
-    __syncthreads();
   }
 }
 
@@ -763,9 +773,10 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   if (a.few_rows != 0x7fffffff) {
     if (cudaError_t e = launch_prompt(sizeof(T) == 4 ? -1 : (std::is_same_v<T, __half> ? KQ_F16 : KQ_BF16), D, a, st)) return e;
   }
-  const int heads = a.tokens * a.q_heads <= 4096 ? 1 : a.q_heads;
-  return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(a.tokens * (a.q_heads / heads))), dim3(kCombineThreads), 0,
-                          st, a, heads);
+  // few rows: each may be in many parts
+  if (a.tokens * a.q_heads <= kWideRows)
+    return launch_dependent(combine_kernel<T, D, true>, dim3((unsigned)(a.tokens * a.q_heads)), dim3(kCombineThreads), 0, st, a);
+  return launch_dependent(combine_kernel<T, D, false>, dim3((unsigned)a.tokens), dim3(kCombineThreads), 0, st, a);
 }
 
 template <typename T>
