@@ -177,6 +177,18 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint8_t* buf, 
   }
 }
 
+// Bits lo .. hi - 1 of 32.
+__device__ __forceinline__ uint32_t visible(int lo, int hi) {
+  const uint32_t below = hi <= 0 ? 0u : (hi >= 32 ? ~0u : (1u << hi) - 1);
+  const uint32_t skipped = lo <= 0 ? 0u : (lo >= 32 ? ~0u : (1u << lo) - 1);
+  return below & ~skipped;
+}
+// Keys c .. c + 31 of a tile whose granules (16 keys) are missing.
+__device__ __forceinline__ uint32_t hidden_keys(uint32_t hidden, int c) {
+  const uint32_t h = hidden >> (c / kGranule);
+  return (h & 1u ? 0xFFFFu : 0u) | (h & 2u ? 0xFFFF0000u : 0u);
+}
+
 // The run's position: request, row block, key head, key tile.
 struct Place {
   int64_t r;
@@ -451,44 +463,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
             const float f = factor * info.key_scale;
             const bool masked = info.hidden || key0 < all_lo || key0 + N > all_hi;
             const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
-            uint32_t p[N / 2];
-            float sum = 0.f, top;
-            auto pass = [&]() {  // p = 2^(f S - ref), and the largest f S
-              const float minus = ref == -INFINITY ? 0.f : -ref;
-              float2 acc = make_float2(0.f, 0.f);
-              top = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < N / 32; ++c) {
+            const uint32_t s_at = tmem + lanes + b * N;
+            // The largest score, and with it whether the reference moves, before any exponential.
+            float top = -INFINITY;
+            if (masked) {
+#pragma unroll 1
+              for (int c = 0; c < N; c += 32) {
                 uint32_t s[32];
-                tmem_ld32(tmem + lanes + b * N + 32 * c, s);
+                tmem_ld32(s_at + c, s);
                 tmem_ld_wait();
-                if (masked) {
+                const uint32_t see = visible(rel_lo - c, rel_hi - c) & ~hidden_keys(info.hidden, c);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) {
-                    const int key = 32 * c + e;
-                    if (key < rel_lo || key >= rel_hi || (info.hidden >> (key / kGranule) & 1u)) s[e] = 0xFF800000u;  // -inf
-                  }
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  const float2 v = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                  top = fmaxf(top, fmaxf(v.x, v.y));
-                  float2 y = fma2(v, make_float2(f, f), make_float2(minus, minus));
-                  y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                  acc = add2(acc, y);
-                  p[16 * c + e / 2] = pack2(y.x, y.y);
-                }
+                for (int e = 0; e < 32; ++e)
+                  if (see >> e & 1u) top = fmaxf(top, __uint_as_float(s[e]));
               }
-              sum = acc.x + acc.y;
-              top *= f;
-            };
-            pass();
+            } else {
+#pragma unroll
+              for (int c = 0; c < N; c += 32) {
+                uint32_t s[32];
+                tmem_ld32(s_at + c, s);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+              }
+            }
+            top *= f;
             const bool moves = top > ref + kPromptSlack;
             if (__any_sync(~0u, moves)) {
               const float keep = !moves ? 1.f : (ref == -INFINITY ? 0.f : exp2_approx(ref - top));
               if (moves) ref = top;
               weight *= keep;
-              pass();
               if (n >= nm) {  // rescale what earlier tiles left in O, once the last of them is in
                 const int before = n - nm;
                 gate.wait(&pv_done[before & 1], (uses[before & 1] + before / 2) & 1);
@@ -506,21 +510,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
                 }
               }
             }
-            weight += sum;
-            if (info.value_scale != 1.f) {
+            // p = 2^(f S - ref), 32 keys at a time; a chunk's p goes over scores that have been read
+            const float minus = ref == -INFINITY ? 0.f : -ref;
+            const __half2 times = __float2half2_rn(info.value_scale);
+            float2 acc = make_float2(0.f, 0.f);
+            auto chunk = [&](const uint32_t(&s)[32], uint32_t see, int c) {
+              uint32_t p[16];
 #pragma unroll
-              for (int e = 0; e < N / 2; ++e) p[e] = as_u32(__hmul2(as_h2(p[e]), __float2half2_rn(8.f)));
+              for (int e = 0; e < 32; e += 2) {
+                float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(f, f),
+                                make_float2(minus, minus));
+                y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                if (masked) {
+                  if (!(see >> e & 1u)) y.x = 0.f;
+                  if (!(see >> (e + 1) & 1u)) y.y = 0.f;
+                }
+                acc = add2(acc, y);
+                p[e / 2] = as_u32(__hmul2(as_h2(pack2(y.x, y.y)), times));
+              }
+              tmem_st16(s_at + c / 2, p);
+            };
+            if (masked) {
+#pragma unroll 1
+              for (int c = 0; c < N; c += 32) {
+                uint32_t s[32];
+                tmem_ld32(s_at + c, s);
+                tmem_ld_wait();
+                chunk(s, visible(rel_lo - c, rel_hi - c) & ~hidden_keys(info.hidden, c), c);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < N; c += 32) {
+                uint32_t s[32];
+                tmem_ld32(s_at + c, s);
+                tmem_ld_wait();
+                chunk(s, ~0u, c);
+              }
             }
+            weight += acc.x + acc.y;
             if (info.nan) {
               for (int e = 0; e < N; ++e)
                 if (e >= rel_lo && e < rel_hi) nan_groups |= s_nan[(bufs / 2 + n / nm) & 3][e];
-            }
-#pragma unroll
-            for (int c = 0; c < N / 2; c += 16) {
-              uint32_t u[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = p[c + e];
-              tmem_st16(tmem + lanes + b * N + c, u);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -577,22 +607,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           // the largest scales of the tile (as bits: NaN above infinity above the numbers)
           uint32_t top_k = 0, top_v = 0;
           {
-            constexpr int kPer = C::kGranules * 2 * D / 32;  // bytes a lane
-            const int at_byte = lane * kPer, g = at_byte / (2 * D), in = at_byte % (2 * D);
-            const uint8_t* p = raw + g * L::kBytes + L::kKeyScales + in;
-            uint32_t top = 0;
+            uint32_t top2[2] = {0, 0};  // of keys, of values
 #pragma unroll
-            for (int e = 0; e < kPer; e += 4) {
-              uint32_t u = *reinterpret_cast<const uint32_t*>(p + e) & 0x7FFF7FFFu;
+            for (int e = 0; e < C::kGranules * 2 * D / 128; ++e) {
+              const int byte = 128 * e + 4 * lane, g = byte / (2 * D), in = byte % (2 * D);
+              uint32_t u = *reinterpret_cast<const uint32_t*>(raw + g * L::kBytes + L::kKeyScales + in) & 0x7FFF7FFFu;
               if (dirty) {  // hidden keys' scales may be anything; a word holds two groups of one token
-                const int32_t key = key0 + g * kGranule + (in + e) % D % L::kScaleSlab / (2 * L::kGroups);
+                const int32_t key = key0 + g * kGranule + in % D % L::kScaleSlab / (2 * L::kGroups);
                 if (key < blk.lo || key >= blk.hi || (hidden >> g & 1u)) u = 0;
               }
-              top = __vmaxu2(top, u);
+              top2[in >= D] = __vmaxu2(top2[in >= D], u);
             }
-            top = max(top & 0xFFFFu, top >> 16);
-            top_k = __reduce_max_sync(~0u, in < D ? top : 0u);
-            top_v = __reduce_max_sync(~0u, in < D ? 0u : top);
+            top_k = __reduce_max_sync(~0u, max(top2[0] & 0xFFFFu, top2[0] >> 16));
+            top_v = __reduce_max_sync(~0u, max(top2[1] & 0xFFFFu, top2[1] >> 16));
           }
           const float k_down = top_k > 0x6FFFu ? 0.125f : 1.f, v_down = top_v > 0x6FFFu ? 0.125f : 1.f;
           if (me == 0) {
