@@ -75,8 +75,8 @@ template <int D>
 struct PromptShape {
   static constexpr int kTiles = D == 256 ? 1 : 2;     // 128 query rows each
   static constexpr int kRows = 128 * kTiles;
-  static constexpr int kKeys = D == 256 ? 64 : 128;
-  static constexpr int kLeastRun = 4;                 // key tiles of a run
+  static constexpr int kKeys = 64;
+  static constexpr int kLeastRun = 8;                 // key tiles of a run
   static constexpr int64_t kPartial = kRows * (int64_t)(D + 2);
 };
 

@@ -5,7 +5,7 @@
 // (query, key) pair against 4.5 bits per key value, so the tensor cores bound
 // it.  A CTA takes blocks of 256 query rows of one key head (two M tiles of
 // 128; at D = 256 one tile, for tensor memory holds 512 columns) and walks over
-// tiles of 128 keys (64 at D = 256):
+// tiles of 64 keys:
 //
 //   S = Q K^T   tcgen05.mma, both operands in shared memory
 //   P = 2^(f S - m)  one thread per row, from and to tensor memory (fp16)
@@ -19,12 +19,16 @@
 // the tile's keys or values are divided by 8, and scores or probabilities
 // multiplied by it.
 //
-// Roles: warp 0 copies granules into two raw stages; warp 1 issues the MMAs
-// (QK of the next item before PV of the last, so that the tensor cores work on
-// one M tile while the softmax of the other runs); warps 4-7 and 8-11 are the
-// softmax of the two M tiles; the rest unpack, into a ring of three buffers
-// that keys and values take in turn.  The reference m of a row moves only when
-// a score passes it by 8, and then its warp rescales O in tensor memory.
+// Roles: warp 0 copies granules into raw stages; warp 1 issues the MMAs; warp 2
+// looks at a stage's scales; warps 4-7 and 8-11 are the softmax of the two M
+// tiles; warps 12-19 unpack, into a ring of buffers that keys and values take
+// in turn (with four warps unpacking bound the kernel: 507 us against 309
+// without it).  Each M tile has two S buffers
+// (P replaces S in place), and QK of the next key tile is issued before PV of
+// this one, so that a softmax finds its next scores waiting: with one S buffer
+// of 128 keys per M tile the chain QK, softmax, PV bound the kernel (382 us for
+// 2048 tokens on 8192, 32 heads of 128).  The reference m of a row moves only
+// when a score passes it by 8, and then its warp rescales O in tensor memory.
 //
 // Row blocks in order, each head's key tiles end to end, are cut into one run
 // of tiles per CTA, whatever the prompts' lengths and masks; a block cut
@@ -47,23 +51,28 @@ using namespace tc;
 __device__ unsigned int g_prompt_status = 0;
 __device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_status, 1u << status); }
 
-constexpr int kPromptWarps = 14, kPromptThreads = 32 * kPromptWarps;
+// Five warpgroups of 96 registers a thread at launch: two that keep scores in registers take 144, the others give 32
+// back (2 x 144 + 3 x 64 = 5 x 96).
+constexpr int kPromptWarps = 20, kPromptThreads = 32 * kPromptWarps;
+constexpr int kUnpackFirst = 12, kUnpackWarps = 8;
 constexpr float kPromptSlack = 8.f;
+constexpr int kInfos = 8;            // key tiles between unpacking and softmax, and more
 
 template <int D>
 struct PromptConfig : PromptShape<D> {
   using S = PromptShape<D>;
   using L = Layout<D>;
-  static constexpr int kUnpackWarps = S::kTiles == 2 ? 4 : 8;
   static constexpr int kGranules = S::kKeys / kGranule;          // of a key tile
   static constexpr int kQBytes = 128 * D * 2;                    // one M tile
   static constexpr int kBuffer = S::kKeys * D * 2;               // a tile of keys or values in fp16
   static constexpr int kRaw = kGranules * L::kBytes;
+  static constexpr int kBuffers = D == 256 ? 3 : 6;
+  static constexpr int kStages = D == 256 ? 2 : 4;               // raw
   static constexpr int kRing = S::kTiles * kQBytes;              // offsets
-  static constexpr int kRawAt = kRing + 3 * kBuffer;
-  static constexpr int kSmem = kRawAt + 2 * kRaw + 1024;         // and room to align to 1024
-  // tensor memory columns: S (and P over it), then O
-  static constexpr int kO = 2 * S::kKeys;
+  static constexpr int kRawAt = kRing + kBuffers * kBuffer;
+  static constexpr int kSmem = kRawAt + kStages * kRaw + 1024;   // and room to align to 1024
+  // tensor memory columns: two S buffers of each M tile (P over them), then O
+  static constexpr int kO = 2 * S::kTiles * S::kKeys;
   static constexpr int kColumns = 512;
   static_assert(kO + S::kTiles * D <= kColumns, "tensor memory");
 };
@@ -72,6 +81,7 @@ struct TileInfo {
   float key_scale, value_scale;  // 1, or 8 where the tile was divided by 8
   uint32_t nan;                  // a value scale of a visible key is not finite
   uint32_t hidden;               // bit per granule whose page is missing
+  uint32_t special;              // values need a look: hidden or invisible keys, large or non-finite scales
 };
 
 // Barriers that every role waits on with a limit; after one ran out all waits return at once, and the roles run through.
@@ -111,11 +121,17 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t v, __half2 d) {
   return as_u32(__hmul2(__hsub2(as_h2(magic), as_h2(0x64086408u)), d));
 }
 
+// The same of the second nibble of each half.
+__device__ __forceinline__ uint32_t value_pair_up(uint32_t v, __half2 d) {
+  const uint32_t magic = (v & 0x00F000F0u) | 0x64006400u;  // 1024 + 16 q
+  return as_u32(__hmul2(__hfma2(as_h2(magic), as_h2(0x2C002C00u), as_h2(0xD480D480u)), d));
+}
+
 // Keys of tokens 8 b .. 8 b + 7, slab sl: each lane a quarter of one token's groups, one 16-byte chunk a group.  The
 // eight dimensions of a chunk lie in the order 0 4 1 5 2 6 3 7, as the queries do.  Tokens of odd index take their
 // groups in the other order, so that a store's eight lanes fall on different banks.
 template <int D>
-__device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint8_t* buf, int b, int sl, float shrink) {
+__device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint8_t* buf, int b, int sl, bool shrink) {
   using C = PromptConfig<D>;
   using L = Layout<D>;
   constexpr int G = L::kGroups;
@@ -129,17 +145,21 @@ __device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint8_t* buf, in
   } else {
     ks[0] = *reinterpret_cast<const uint32_t*>(sp);
   }
-  const __half2 down = __float2half2_rn(shrink);
+  if (shrink) {
+#pragma unroll
+    for (int i = 0; i < G / 2; ++i) ks[i] = as_u32(__hmul2(as_h2(ks[i]), __float2half2_rn(0.125f)));
+  }
+  const uint32_t pick = r & 1;
 #pragma unroll
   for (int s = 0; s < G; ++s) {
-    const uint32_t v = r & 1 ? w[s ^ 1] : w[s];
-    const __half2 pair = __hmul2(as_h2(ks[s / 2]), down);
-    const __half2 d = ((r & 1) != 0) == (s % 2 == 0) ? __high2half2(pair) : __low2half2(pair);
-    uint4 o;
+    const uint32_t v = pick ? w[s ^ 1] : w[s];
+    const __half2 d = as_h2(__byte_perm(ks[s / 2], 0, (s % 2) ^ pick ? 0x3232 : 0x1010));
+    const uint32_t u = v >> 8;
+    uint4 o;  // nibbles 1 and 3 stay 4 bits up: 1024 + 16 q, times 1/16, minus 72
     o.x = value_pair(v, d);
-    o.y = value_pair(v >> 4, d);
-    o.z = value_pair(v >> 8, d);
-    o.w = value_pair(v >> 12, d);
+    o.y = value_pair_up(v, d);
+    o.z = value_pair(u, d);
+    o.w = value_pair_up(u, d);
     const int dim = sl * L::kSlabDim + 32 * (s ^ (r & 1));
     const int chunk = (dim % 64) / 8 + c;
     *reinterpret_cast<uint4*>(buf + (dim / 64) * (C::kKeys * 128) + (8 * b + r) * 128 + ((chunk ^ r) << 4)) = o;
@@ -150,7 +170,8 @@ __device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint8_t* buf, in
 // dimensions of two successive tokens and stores a pair of tokens a dimension; the lanes take their dimensions in
 // rotated order, so that a store's rows fall on different banks.
 template <int D>
-__device__ __forceinline__ void unpack_values(const uint8_t* raw, uint8_t* buf, int b, int sl, float shrink, uint32_t valid) {
+__device__ __forceinline__ void unpack_values(const uint8_t* raw, uint8_t* buf, int b, int sl, bool special, bool shrink,
+                                              uint32_t valid) {
   using L = Layout<D>;
   constexpr int G = L::kGroups;
   const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
@@ -158,14 +179,16 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint8_t* buf, 
   uint32_t w[G], vs[G];
   load_raw<G>(w, g0 + L::kValues + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
   load_raw<G>(vs, g0 + L::kValueScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
-  const __half2 down = __float2half2_rn(shrink);
   __half2 d[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const uint32_t u = __byte_perm(vs[g / 2], vs[G / 2 + g / 2], g % 2 ? 0x7632 : 0x5410);
+  for (int g = 0; g < G; ++g) d[g] = as_h2(__byte_perm(vs[g / 2], vs[G / 2 + g / 2], g % 2 ? 0x7632 : 0x5410));
+  if (special) {
     // hidden keys and scales that are not finite count as zero (those keys' rows are marked by the softmax)
-    const uint32_t ok = __hle2_mask(__habs2(as_h2(u)), as_h2(0x7BFF7BFFu)) & valid;
-    d[g] = __hmul2(as_h2(u & ok), down);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      d[g] = as_h2(as_u32(d[g]) & __hle2_mask(__habs2(d[g]), as_h2(0x7BFF7BFFu)) & valid);
+      if (shrink) d[g] = __hmul2(d[g], __float2half2_rn(0.125f));
+    }
   }
   uint8_t* base = buf + (b / 8) * (D * 128) + (sl * L::kSlabDim + 4 * r) * 128 + 4 * c;
 #pragma unroll
@@ -195,16 +218,71 @@ struct Place {
   int32_t k, h, tile;
 };
 
+// A run's segments: row by row (request, row block, key head), the key tiles of it that the run holds.
+template <int D>
+struct Walk {
+  using S = PromptShape<D>;
+  const Args& a;
+  Place at;
+  int64_t unit, end;
+  Request q;
+  RowBlock blk;
+  int32_t from, to, tiles, nm;   // key tiles of the segment, its M tiles
+  uint32_t bufs;                 // buffers of keys and values used so far
+  uint32_t uses;                 // bit 2 m + b: how often S buffer b of M tile m has been used, modulo 2
+  bool first;
+
+  __device__ __forceinline__ Walk(const Args& args, const Place& p, int64_t u, int64_t e)
+      : a(args), at(p), unit(u), end(e), bufs(0), uses(0), first(true) {
+    if (unit < end) {
+      q = request_of(a, at.r, S::kKeys);
+      blk = row_block<D>(a, q, at.k);
+    }
+  }
+  // Parity of the barrier phase of M tile m's j-th score tile of the segment.
+  __device__ __forceinline__ uint32_t phase(int m, int j) const { return ((uses >> (2 * m + (j & 1))) + j / 2) & 1; }
+  __device__ __forceinline__ bool next() {
+    if (unit >= end) return false;
+    if (at.tile == blk.tiles) {  // heads, then blocks, then requests
+      at.tile = 0;
+      if (++at.h == a.cache.kv_heads) {
+        at.h = 0;
+        do {
+          if (++at.k >= (q.rows + S::kRows - 1) / S::kRows) {
+            at.k = 0;
+            do q = request_of(a, ++at.r, S::kKeys);
+            while (q.rows <= a.few_rows);  // a unit remains, so some request has it
+          }
+          blk = row_block<D>(a, q, at.k);
+        } while (blk.tiles == 0);
+      }
+    }
+    from = at.tile, to = (int32_t)min((int64_t)blk.tiles, from + (end - unit));
+    tiles = to - from;
+    nm = blk.rows > 128 ? 2 : 1;
+    return true;
+  }
+  __device__ __forceinline__ void done() {
+    bufs += 2 * tiles;
+    uses ^= ((((tiles + 1) / 2) & 1u) | ((tiles / 2) & 1u) << 1) * (nm == 2 ? 5u : 1u);
+    first = false;
+    unit += tiles;
+    at.tile = to;
+  }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   using C = PromptConfig<D>;
   using L = Layout<D>;
   constexpr int N = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t raw_full[2], raw_empty[2], buf_full[3], buf_empty[3], s_full[2], p_full[2], pv_done[2];
-  __shared__ TileInfo s_info[4];
-  __shared__ uint8_t s_nan[4][N];     // groups of a key whose value scale is not finite
-  __shared__ uint32_t s_hidden[2];    // of a raw stage
+  __shared__ uint64_t raw_full[C::kStages], raw_seen[C::kStages], raw_empty[C::kStages], buf_full[C::kBuffers], buf_empty[C::kBuffers];
+  __shared__ uint64_t s_full[C::kTiles][2], p_full[C::kTiles][2], pv_done[C::kTiles][2];
+  __shared__ TileInfo s_info[kInfos];
+  __shared__ uint8_t s_nan[kInfos][N];        // groups of a key whose value scale is not finite
+  __shared__ uint32_t s_hidden[C::kStages];   // of a raw stage
+  __shared__ uint64_t s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int64_t s_entry[kPromptThreads];  // row blocks before each request of a chunk
@@ -214,17 +292,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], C::kUnpackWarps);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&pv_done[i], 1);
+      mbar_init(&raw_seen[i], 1);
+      mbar_init(&raw_empty[i], kUnpackWarps);
     }
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&buf_full[i], C::kUnpackWarps);
+    for (int i = 0; i < 2 * C::kTiles; ++i) {
+      mbar_init(&s_full[i / 2][i & 1], 1);
+      mbar_init(&p_full[i / 2][i & 1], 128);
+      mbar_init(&pv_done[i / 2][i & 1], 1);
+    }
+    for (int i = 0; i < C::kBuffers; ++i) {
+      mbar_init(&buf_full[i], kUnpackWarps);
       mbar_init(&buf_empty[i], 1);
     }
+    mbar_init(&s_drain, 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -310,47 +392,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  if (unit < end) {
-    const Gate gate{&s_abort};
-    Place at = s_place;
-    Request q = request_of(a, at.r, N);
-    RowBlock blk = row_block<D>(a, q, at.k);
-    // counts that the roles carry over the segments: raw stages (copies and unpacking), buffers, uses of the S buffers
-    uint32_t raws = 0, bufs = 0, uses[2] = {0, 0};
-    bool first = true;
-    while (unit < end) {
-      // next row: heads, then blocks, then requests
-      if (at.tile == blk.tiles) {
-        at.tile = 0;
-        if (++at.h == a.cache.kv_heads) {
-          at.h = 0;
-          do {
-            if (++at.k >= (q.rows + C::kRows - 1) / C::kRows || q.rows <= a.few_rows) {
-              at.k = 0;
-              do q = request_of(a, ++at.r, N);
-              while (q.rows <= a.few_rows);  // a unit remains, so some request has it
-            }
-            blk = row_block<D>(a, q, at.k);
-          } while (blk.tiles == 0);
-        }
-      }
-      const int32_t from = at.tile, to = (int32_t)min((int64_t)blk.tiles, from + (end - unit));
-      const int nm = blk.rows > 128 ? 2 : 1;
-      const int items = (to - from) * nm;
-
+  const Gate gate{&s_abort};
+  Walk<D> w(a, s_place, unit, end);
+  uint32_t raws = 0;  // raw stages that a copying, looking or unpacking warp is through with
+  // Each role walks over the run's segments by itself; all meet when a segment's queries are in place, and at its end.
+  if (warp >= 4 && warp < 4 + 4 * C::kTiles) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    while (w.next()) {
       // ---- queries: one thread a row ----
-      const bool softmax = warp >= 4 && warp < 4 + 4 * C::kTiles;
       const int m_tile = (warp - 4) / 4;
       const int row = (warp & 3) * 32 + lane;       // tensor memory lane
-      const int32_t x = at.k * C::kRows + m_tile * 128 + row, i = x / a.group;
-      const bool live = softmax && m_tile * 128 + row < blk.rows;
-      const int32_t pos = q.pos0 + i;
-      const int32_t key_hi = live ? max(0, min(pos + 1, q.len)) : 0x7fffffff;
+      const int32_t x = w.at.k * C::kRows + m_tile * 128 + row, i = x / a.group;
+      const bool live = m_tile * 128 + row < w.blk.rows;
+      const int32_t pos = w.q.pos0 + i;
+      const int32_t key_hi = live ? max(0, min(pos + 1, w.q.len)) : 0x7fffffff;
       const int32_t key_lo = live && a.window ? max(0, pos - (a.window - 1)) : 0;
       float factor = 0.f;
-      if (softmax && m_tile < nm) {
-        const T* src = static_cast<const T*>(a.q) + (int64_t)(q.first + i) * a.q_token +
-                       (int64_t)(at.h * a.group + x % a.group) * a.q_head;
+      if (m_tile < w.nm) {
+        const T* src = static_cast<const T*>(a.q) + (int64_t)(w.q.first + i) * a.q_token +
+                       (int64_t)(w.at.h * a.group + x % a.group) * a.q_head;
         float top = 0.f;
         if (live) {
           for (int e = 0; e < D; e += 8) {
@@ -365,7 +425,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         e2 = min(max(8 - e2, -110), 110);  // the row times 2^e2 lies below 2^8
         // the scale's sign goes with the queries, so that larger sums are larger scores
         const float up = a.scale == 0.f ? 0.f : copysignf(ldexpf(1.f, e2), a.scale);
-        factor = ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2);
+        factor = fmaxf(ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2), 1e-37f);
         uint8_t* dst = smem + m_tile * C::kQBytes + row * 128;
         for (int e = 0; e < D; e += 8) {
           float v[8] = {};
@@ -378,26 +438,151 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       __syncthreads();
-
+      // ---- softmax ----
+      if (m_tile < w.nm) {
+        float ref = -INFINITY, weight = 0.f;
+        uint32_t nan_groups = 0;
+        const int32_t all_lo = __reduce_max_sync(~0u, key_lo), all_hi = __reduce_min_sync(~0u, key_hi);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor memory address of the warp's lanes
+        for (int j = 0; j < w.tiles; ++j) {
+          const int b = j & 1, slot = (w.bufs / 2 + j) % kInfos;
+          const int32_t key0 = (w.blk.tile0 + w.from + j) * N;
+          const uint32_t s_at = tmem + lanes + (2 * m_tile + b) * N;
+          gate.wait(&s_full[m_tile][b], w.phase(m_tile, j));
+          __syncwarp();
+          tc_fence_after();
+          uint32_t s[2][32];
+          tmem_ld32(s_at, s[0]);
+          tmem_ld32(s_at + 32, s[1]);
+          const TileInfo info = s_info[slot];
+          const float f = factor * info.key_scale;
+          const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
+          tmem_ld_wait();
+          if (info.hidden || key0 < all_lo || key0 + N > all_hi) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t see = visible(rel_lo - 32 * c, rel_hi - 32 * c) & ~hidden_keys(info.hidden, 32 * c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(see >> e & 1u)) s[c][e] = 0xFF800000u;  // -inf
+            }
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, fmaxf(__uint_as_float(s[0][e]), __uint_as_float(s[1][e])));
+          top *= f;
+          const bool moves = top > ref + kPromptSlack;
+          if (__any_sync(~0u, moves)) {
+            const float keep = !moves ? 1.f : (ref == -INFINITY ? 0.f : exp2_approx(ref - top));
+            if (moves) ref = top;
+            weight *= keep;
+            if (j > 0) {  // rescale what earlier w.tiles left in O, once the last of them is in
+              gate.wait(&pv_done[m_tile][b ^ 1], w.phase(m_tile, j - 1));
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
+                tmem_ld_wait();
+                uint32_t u[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * keep);
+                tmem_st16(tmem + lanes + C::kO + m_tile * D + c, u);
+              }
+            }
+          }
+          // p = 2^(f S - ref), over the scores
+          const float minus = ref == -INFINITY ? 0.f : -ref;
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 y = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(f, f),
+                              make_float2(minus, minus));
+              y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              acc = add2(acc, y);
+              p[e / 2] = pack2(y.x, y.y);
+            }
+            if (info.value_scale != 1.f) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = as_u32(__hmul2(as_h2(p[e]), __float2half2_rn(8.f)));
+            }
+            tmem_st16(s_at + 16 * c, p);
+          }
+          weight += acc.x + acc.y;
+          if (info.nan) {
+            for (int e = 0; e < N; ++e)
+              if (e >= rel_lo && e < rel_hi) nan_groups |= s_nan[slot][e];
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[m_tile][b]);
+        }
+        // ---- the block's rows ----
+        gate.wait(&pv_done[m_tile][(w.tiles - 1) & 1], w.phase(m_tile, w.tiles - 1));
+        __syncwarp();
+        tc_fence_after();
+        const bool whole = w.from == 0 && w.to == w.blk.tiles;
+        const int in = m_tile * 128 + row;
+        float* part = a.prompt_partials + (2 * (int64_t)blockIdx.x + (w.first ? 0 : 1)) * C::kPartial;
+        T* dst = static_cast<T*>(a.out) + (int64_t)(w.q.first + i) * a.out_token +
+                 (int64_t)(w.at.h * a.group + x % a.group) * a.out_head;
+        const float scale = whole ? (weight == 0.f ? 0.f : 1.f / weight) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
+          tmem_ld_wait();
+          if (live) {
+            const float poison = nan_groups >> (c / 32) & 1u ? NAN : 0.f;
+            float lo[8], hi[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lo[e] = o[e] * scale + poison, hi[e] = o[8 + e] * scale + poison;
+            if (whole) {
+              kv::store8(dst + c, lo);
+              kv::store8(dst + c + 8, hi);
+            } else {
+              kv::store8(part + in * D + c, lo);
+              kv::store8(part + in * D + c + 8, hi);
+            }
+          }
+          __syncwarp();
+        }
+        if (!whole && live) {
+          part[C::kRows * D + in] = ref;
+          part[C::kRows * D + C::kRows + in] = weight;
+        }
+        tc_fence_before();
+      }
+      __syncthreads();
+      w.done();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    while (w.next()) {
+      __syncthreads();
       if (warp == 0) {
         // ---- copies ----
         const uint64_t policy = l2_policy_evict_first();
         const int per_page = a.cache.page_size / kGranule;
-        const int32_t pages = (q.len + a.cache.page_size - 1) / a.cache.page_size;
-        const int32_t* table = a.table + at.r * a.table_stride;
+        const int32_t pages = (w.q.len + a.cache.page_size - 1) / a.cache.page_size;
+        const int32_t* table = a.table + w.at.r * a.table_stride;
         auto page_id = [&](int32_t t) -> int32_t {
-          const int32_t page = ((blk.tile0 + t) * C::kGranules + lane) / per_page;
+          const int32_t page = ((w.blk.tile0 + t) * C::kGranules + lane) / per_page;
           return lane < C::kGranules && page < pages ? table[page] : -1;
         };
-        int32_t next = page_id(from);
-        for (int32_t t = from; t < to; ++t, ++raws) {
-          const int st = raws & 1;
+        int32_t next = page_id(w.from);
+        for (int32_t t = w.from; t < w.to; ++t, ++raws) {
+          const int st = raws % C::kStages;
           const int32_t id = next;
-          if (t + 1 < to) next = page_id(t + 1);
-          if (raws >= 2) gate.wait(&raw_empty[st], (raws / 2 - 1) & 1);
-          const int32_t granule = (blk.tile0 + t) * C::kGranules + lane, key = granule * kGranule;
+          if (t + 1 < w.to) next = page_id(t + 1);
+          if (raws >= C::kStages) gate.wait(&raw_empty[st], (raws / C::kStages - 1) & 1);
+          const int32_t granule = (w.blk.tile0 + t) * C::kGranules + lane, key = granule * kGranule;
           const bool here = lane < C::kGranules && id >= 0 && id < a.cache.pages;
-          if (lane < C::kGranules && !here && key < blk.hi && key + kGranule > blk.lo) prompt_flag(KQ_ERR_RANGE);
+          if (lane < C::kGranules && !here && key < w.blk.hi && key + kGranule > w.blk.lo) prompt_flag(KQ_ERR_RANGE);
           const uint32_t have = __ballot_sync(~0u, here);
           if (lane == 0) {
             s_hidden[st] = ~have & ((1u << C::kGranules) - 1);
@@ -406,287 +591,148 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           __syncwarp();
           if (here)
             bulk_g2s(smem + C::kRawAt + st * C::kRaw + lane * L::kBytes,
-                     a.cache.data + ((int64_t)id * a.cache.kv_heads + at.h) * a.cache.block_bytes +
+                     a.cache.data + ((int64_t)id * a.cache.kv_heads + w.at.h) * a.cache.block_bytes +
                          (granule % per_page) * L::kBytes,
                      L::kBytes, &raw_full[st], policy);
         }
       } else if (warp == 1) {
         // ---- matrix products ----
+        tc_fence_after();
         if (elect_one()) {
           const uint32_t qk = idesc_f16(128, N), pv = idesc_f16(128, D);
-          auto values = [&](int n) {  // O += P V of item n
-            const int j = n / nm, m = n % nm, b = n & 1;
-            const uint32_t vb = bufs + 2 * j + 1;
-            gate.wait(&p_full[b], (uses[b] + n / 2) & 1);
-            if (m == 0) gate.wait(&buf_full[vb % 3], (vb / 3) & 1);
-            tc_fence_after();
-            const uint64_t bd = sw128_desc(smem + C::kRing + (vb % 3) * C::kBuffer);
+          for (int j = 0; j <= w.tiles; ++j) {
+            if (j < w.tiles) {  // S = Q K^T of tile j
+              const uint32_t kb = w.bufs + 2 * j;
+              const int b = j & 1, buf = kb % C::kBuffers;
+              gate.wait(&buf_full[buf], (kb / C::kBuffers) & 1);
+              const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
+              for (int m = 0; m < w.nm; ++m) {
+                // the buffer's last S and P are read
+                if (j >= 2) gate.wait(&pv_done[m][b], w.phase(m, j - 2));
+                tc_fence_after();
+                const uint64_t ad = sw128_desc(smem + m * C::kQBytes);
 #pragma unroll
-            for (int k = 0; k < N / 16; ++k)
-              tc_mma_ts(tmem + C::kO + m * D, tmem + b * N + k * 8, bd + (uint64_t)(((k / 4) * D * 128 + (k % 4) * 32) >> 4), pv,
-                        j > 0 || k > 0);
-            tc_commit(&pv_done[b]);
-            if (m == nm - 1) tc_commit(&buf_empty[vb % 3]);
-          };
-          for (int n = 0; n < items; ++n) {
-            const int j = n / nm, m = n % nm, b = n & 1;
-            const uint32_t kb = bufs + 2 * j;
-            if (m == 0) gate.wait(&buf_full[kb % 3], (kb / 3) & 1);
-            if (n >= 2) gate.wait(&pv_done[b], (uses[b] + n / 2 - 1) & 1);  // S and P of the buffer's last item are read
-            tc_fence_after();
-            const uint64_t ad = sw128_desc(smem + m * C::kQBytes), bd = sw128_desc(smem + C::kRing + (kb % 3) * C::kBuffer);
+                for (int k = 0; k < D / 16; ++k)
+                  tc_mma_ss(tmem + (2 * m + b) * N, ad + (uint64_t)(((k / 4) * 128 * 128 + (k % 4) * 32) >> 4),
+                            bd + (uint64_t)(((k / 4) * N * 128 + (k % 4) * 32) >> 4), qk, k > 0);
+                tc_commit(&s_full[m][b]);
+              }
+              tc_commit(&buf_empty[buf]);
+            }
+            if (j > 0) {  // O += P V of tile j - 1
+              const uint32_t vb = w.bufs + 2 * j - 1;
+              const int b = (j - 1) & 1, buf = vb % C::kBuffers;
+              gate.wait(&buf_full[buf], (vb / C::kBuffers) & 1);
+              const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
+              for (int m = 0; m < w.nm; ++m) {
+                gate.wait(&p_full[m][b], w.phase(m, j - 1));
+                tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              tc_mma_ss(tmem + b * N, ad + (uint64_t)(((k / 4) * 128 * 128 + (k % 4) * 32) >> 4),
-                        bd + (uint64_t)(((k / 4) * N * 128 + (k % 4) * 32) >> 4), qk, k > 0);
-            tc_commit(&s_full[b]);
-            if (m == nm - 1) tc_commit(&buf_empty[kb % 3]);
-            if (n >= 1) values(n - 1);
+                for (int k = 0; k < N / 16; ++k)
+                  tc_mma_ts(tmem + C::kO + m * D, tmem + (2 * m + b) * N + k * 8, bd + (uint64_t)((k * 32) >> 4), pv,
+                            j > 1 || k > 0);
+                tc_commit(&pv_done[m][b]);
+              }
+              tc_commit(&buf_empty[buf]);
+            }
           }
-          values(items - 1);
         }
         __syncwarp();
-      } else if (softmax) {
-        // ---- softmax ----
-        if (m_tile < nm) {
-          float ref = -INFINITY, weight = 0.f;
-          uint32_t nan_groups = 0;
-          const int32_t all_lo = __reduce_max_sync(~0u, key_lo), all_hi = __reduce_min_sync(~0u, key_hi);
-          const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor memory address of the warp's lanes
-          for (int n = m_tile; n < items; n += nm) {
-            const int b = n & 1;
-            const int32_t key0 = (blk.tile0 + from + n / nm) * N;
-            gate.wait(&s_full[b], (uses[b] + n / 2) & 1);
-            __syncwarp();
-            tc_fence_after();
-            const TileInfo info = s_info[(bufs / 2 + n / nm) & 3];
-            const float f = factor * info.key_scale;
-            const bool masked = info.hidden || key0 < all_lo || key0 + N > all_hi;
-            const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
-            const uint32_t s_at = tmem + lanes + b * N;
-            // The largest score, and with it whether the reference moves, before any exponential.
-            float top = -INFINITY;
-            if (masked) {
-#pragma unroll 1
-              for (int c = 0; c < N; c += 32) {
-                uint32_t s[32];
-                tmem_ld32(s_at + c, s);
-                tmem_ld_wait();
-                const uint32_t see = visible(rel_lo - c, rel_hi - c) & ~hidden_keys(info.hidden, c);
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (see >> e & 1u) top = fmaxf(top, __uint_as_float(s[e]));
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < N; c += 32) {
-                uint32_t s[32];
-                tmem_ld32(s_at + c, s);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-              }
-            }
-            top *= f;
-            const bool moves = top > ref + kPromptSlack;
-            if (__any_sync(~0u, moves)) {
-              const float keep = !moves ? 1.f : (ref == -INFINITY ? 0.f : exp2_approx(ref - top));
-              if (moves) ref = top;
-              weight *= keep;
-              if (n >= nm) {  // rescale what earlier tiles left in O, once the last of them is in
-                const int before = n - nm;
-                gate.wait(&pv_done[before & 1], (uses[before & 1] + before / 2) & 1);
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  float o[16];
-                  tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
-                  tmem_ld_wait();
-                  uint32_t u[16];
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * keep);
-                  tmem_st16(tmem + lanes + C::kO + m_tile * D + c, u);
-                }
-              }
-            }
-            // p = 2^(f S - ref), 32 keys at a time; a chunk's p goes over scores that have been read
-            const float minus = ref == -INFINITY ? 0.f : -ref;
-            const __half2 times = __float2half2_rn(info.value_scale);
-            float2 acc = make_float2(0.f, 0.f);
-            auto chunk = [&](const uint32_t(&s)[32], uint32_t see, int c) {
-              uint32_t p[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(f, f),
-                                make_float2(minus, minus));
-                y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                if (masked) {
-                  if (!(see >> e & 1u)) y.x = 0.f;
-                  if (!(see >> (e + 1) & 1u)) y.y = 0.f;
-                }
-                acc = add2(acc, y);
-                p[e / 2] = as_u32(__hmul2(as_h2(pack2(y.x, y.y)), times));
-              }
-              tmem_st16(s_at + c / 2, p);
-            };
-            if (masked) {
-#pragma unroll 1
-              for (int c = 0; c < N; c += 32) {
-                uint32_t s[32];
-                tmem_ld32(s_at + c, s);
-                tmem_ld_wait();
-                chunk(s, visible(rel_lo - c, rel_hi - c) & ~hidden_keys(info.hidden, c), c);
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < N; c += 32) {
-                uint32_t s[32];
-                tmem_ld32(s_at + c, s);
-                tmem_ld_wait();
-                chunk(s, ~0u, c);
-              }
-            }
-            weight += acc.x + acc.y;
-            if (info.nan) {
-              for (int e = 0; e < N; ++e)
-                if (e >= rel_lo && e < rel_hi) nan_groups |= s_nan[(bufs / 2 + n / nm) & 3][e];
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full[b]);
-          }
-          // ---- the block's rows ----
-          const int last = (items - 1 - m_tile) / nm * nm + m_tile;
-          gate.wait(&pv_done[last & 1], (uses[last & 1] + last / 2) & 1);
-          __syncwarp();
-          tc_fence_after();
-          const bool whole = from == 0 && to == blk.tiles;
-          const int in = m_tile * 128 + row;
-          float* part = a.prompt_partials + (2 * (int64_t)blockIdx.x + (first ? 0 : 1)) * C::kPartial;
-          T* dst = static_cast<T*>(a.out) + (int64_t)(q.first + i) * a.out_token +
-                   (int64_t)(at.h * a.group + x % a.group) * a.out_head;
-          const float scale = whole ? (weight == 0.f ? 0.f : 1.f / weight) : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
-            tmem_ld_wait();
-            if (live) {
-              const float poison = nan_groups >> (c / 32) & 1u ? NAN : 0.f;
-              float lo[8], hi[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) lo[e] = o[e] * scale + poison, hi[e] = o[8 + e] * scale + poison;
-              if (whole) {
-                kv::store8(dst + c, lo);
-                kv::store8(dst + c + 8, hi);
-              } else {
-                kv::store8(part + in * D + c, lo);
-                kv::store8(part + in * D + c + 8, hi);
-              }
-            }
-            __syncwarp();
-          }
-          if (!whole && live) {
-            part[C::kRows * D + in] = ref;
-            part[C::kRows * D + C::kRows + in] = weight;
-          }
-          tc_fence_before();
-        }
-      } else {
-        // ---- unpacking ----
-        const int me = warp < 4 ? warp - 2 : warp - (C::kTiles == 2 ? 10 : 6);
-        for (int32_t t = from; t < to; ++t, ++raws) {
-          const int st = raws & 1;
+      } else if (warp == 2) {
+        // ---- a look at the scales ----
+        for (int32_t t = w.from; t < w.to; ++t, ++raws) {
+          const int st = raws % C::kStages, slot = (w.bufs / 2 + t - w.from) % kInfos;
           const uint8_t* raw = smem + C::kRawAt + st * C::kRaw;
-          gate.wait(&raw_full[st], (raws / 2) & 1);
+          gate.wait(&raw_full[st], (raws / C::kStages) & 1);
           __syncwarp();
           const uint32_t hidden = s_hidden[st];
-          const int32_t key0 = (blk.tile0 + t) * N;
-          const bool dirty = hidden || key0 < blk.lo || key0 + N > blk.hi;
-          // the largest scales of the tile (as bits: NaN above infinity above the numbers)
-          uint32_t top_k = 0, top_v = 0;
-          {
-            uint32_t top2[2] = {0, 0};  // of keys, of values
+          const int32_t key0 = (w.blk.tile0 + t) * N;
+          const bool dirty = hidden || key0 < w.blk.lo || key0 + N > w.blk.hi;
+          uint32_t top[2] = {0, 0};  // the largest of the keys', of the values', as bits: NaN above infinity above the numbers
 #pragma unroll
-            for (int e = 0; e < C::kGranules * 2 * D / 128; ++e) {
-              const int byte = 128 * e + 4 * lane, g = byte / (2 * D), in = byte % (2 * D);
-              uint32_t u = *reinterpret_cast<const uint32_t*>(raw + g * L::kBytes + L::kKeyScales + in) & 0x7FFF7FFFu;
-              if (dirty) {  // hidden keys' scales may be anything; a word holds two groups of one token
-                const int32_t key = key0 + g * kGranule + in % D % L::kScaleSlab / (2 * L::kGroups);
-                if (key < blk.lo || key >= blk.hi || (hidden >> g & 1u)) u = 0;
-              }
-              top2[in >= D] = __vmaxu2(top2[in >= D], u);
+          for (int e = 0; e < C::kGranules * 2 * D / 128; ++e) {
+            const int byte = 128 * e + 4 * lane, g = byte / (2 * D), in = byte % (2 * D);
+            uint32_t u = *reinterpret_cast<const uint32_t*>(raw + g * L::kBytes + L::kKeyScales + in) & 0x7FFF7FFFu;
+            if (dirty) {  // hidden keys' scales may be anything; a word holds two groups of one token
+              const int32_t key = key0 + g * kGranule + in % D % L::kScaleSlab / (2 * L::kGroups);
+              if (key < w.blk.lo || key >= w.blk.hi || (hidden >> g & 1u)) u = 0;
             }
-            top_k = __reduce_max_sync(~0u, max(top2[0] & 0xFFFFu, top2[0] >> 16));
-            top_v = __reduce_max_sync(~0u, max(top2[1] & 0xFFFFu, top2[1] >> 16));
+            top[in >= D] = __vmaxu2(top[in >= D], u);
           }
-          const float k_down = top_k > 0x6FFFu ? 0.125f : 1.f, v_down = top_v > 0x6FFFu ? 0.125f : 1.f;
-          if (me == 0) {
-            const int slot = (bufs / 2 + t - from) & 3;
-            if (top_v >= 0x7C00u) {
-              for (int e = lane; e < N; e += 32) {
-                uint32_t groups = 0;
-                const int32_t key = key0 + e;
-                if (key >= blk.lo && key < blk.hi && !(hidden >> (e / kGranule) & 1u)) {
-                  for (int gq = 0; gq < D / 32; ++gq) {
-                    const uint16_t u = *reinterpret_cast<const uint16_t*>(raw + (e / kGranule) * L::kBytes + D +
-                                                                          L::key_scale(e % kGranule, gq));
-                    groups |= (uint32_t)((u & 0x7FFFu) >= 0x7C00u) << gq;
-                  }
+          const uint32_t top_k = __reduce_max_sync(~0u, max(top[0] & 0xFFFFu, top[0] >> 16));
+          const uint32_t top_v = __reduce_max_sync(~0u, max(top[1] & 0xFFFFu, top[1] >> 16));
+          const bool k_down = top_k > 0x6FFFu, v_down = top_v > 0x6FFFu, nan = top_v >= 0x7C00u;
+          if (nan) {
+            for (int e = lane; e < N; e += 32) {
+              uint32_t groups = 0;
+              const int32_t key = key0 + e;
+              if (key >= w.blk.lo && key < w.blk.hi && !(hidden >> (e / kGranule) & 1u)) {
+                for (int gq = 0; gq < D / 32; ++gq) {
+                  const uint16_t u = *reinterpret_cast<const uint16_t*>(raw + (e / kGranule) * L::kBytes + D +
+                                                                        L::key_scale(e % kGranule, gq));
+                  groups |= (uint32_t)((u & 0x7FFFu) >= 0x7C00u) << gq;
                 }
-                s_nan[slot][e] = (uint8_t)groups;
               }
+              s_nan[slot][e] = (uint8_t)groups;
             }
-            if (lane == 0) s_info[slot] = TileInfo{1.f / k_down, 1.f / v_down, top_v >= 0x7C00u, hidden};
-            __syncwarp();
           }
-          const uint32_t kb = bufs + 2 * (t - from);
-          if (kb >= 3) gate.wait(&buf_empty[kb % 3], (kb / 3 - 1) & 1);
-          uint8_t* buf = smem + C::kRing + (kb % 3) * C::kBuffer;
-#pragma unroll 2
-          for (int w = me; w < N / 8 * L::kSlabs; w += C::kUnpackWarps) unpack_keys<D>(raw, buf, w / L::kSlabs, w % L::kSlabs, k_down);
+          if (lane == 0) s_info[slot] = TileInfo{k_down ? 8.f : 1.f, v_down ? 8.f : 1.f, nan, hidden, dirty || v_down};
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_seen[st]);
+        }
+      } else if (warp >= kUnpackFirst) {
+        // ---- unpacking ----
+        const int me = warp - kUnpackFirst;
+        for (int32_t t = w.from; t < w.to; ++t, ++raws) {
+          const int st = raws % C::kStages;
+          const uint8_t* raw = smem + C::kRawAt + st * C::kRaw;
+          gate.wait(&raw_seen[st], (raws / C::kStages) & 1);
+          const TileInfo info = s_info[(w.bufs / 2 + t - w.from) % kInfos];
+          const uint32_t kb = w.bufs + 2 * (t - w.from);
+          if (kb >= C::kBuffers) gate.wait(&buf_empty[kb % C::kBuffers], (kb / C::kBuffers - 1) & 1);
+          __syncwarp();
+          uint8_t* buf = smem + C::kRing + (kb % C::kBuffers) * C::kBuffer;
+#pragma unroll
+          for (int task = me; task < N / 8 * L::kSlabs; task += kUnpackWarps)
+            unpack_keys<D>(raw, buf, task / L::kSlabs, task % L::kSlabs, info.key_scale != 1.f);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&buf_full[kb % 3]);
+          if (lane == 0) mbar_arrive(&buf_full[kb % C::kBuffers]);
           const uint32_t vb = kb + 1;
-          if (vb >= 3) gate.wait(&buf_empty[vb % 3], (vb / 3 - 1) & 1);
-          buf = smem + C::kRing + (vb % 3) * C::kBuffer;
-#pragma unroll 2
-          for (int w = me; w < N / 8 * L::kSlabs; w += C::kUnpackWarps) {
-            const int b = w / L::kSlabs;
+          if (vb >= C::kBuffers) gate.wait(&buf_empty[vb % C::kBuffers], (vb / C::kBuffers - 1) & 1);
+          __syncwarp();
+          buf = smem + C::kRing + (vb % C::kBuffers) * C::kBuffer;
+#pragma unroll
+          for (int task = me; task < N / 8 * L::kSlabs; task += kUnpackWarps) {
+            const int b = task / L::kSlabs;
             uint32_t valid = ~0u;
-            if (dirty) {
-              const int32_t key = key0 + 8 * b + 2 * (lane & 3);
-              const bool held = !(hidden >> (b / 2) & 1u);
-              valid = (held && key >= blk.lo && key < blk.hi ? 0xFFFFu : 0u) |
-                      (held && key + 1 >= blk.lo && key + 1 < blk.hi ? 0xFFFF0000u : 0u);
+            if (info.special) {
+              const int32_t key = (w.blk.tile0 + t) * N + 8 * b + 2 * (lane & 3);
+              const bool held = !(info.hidden >> (b / 2) & 1u);
+              valid = (held && key >= w.blk.lo && key < w.blk.hi ? 0xFFFFu : 0u) |
+                      (held && key + 1 >= w.blk.lo && key + 1 < w.blk.hi ? 0xFFFF0000u : 0u);
             }
-            unpack_values<D>(raw, buf, b, w % L::kSlabs, v_down, valid);
+            unpack_values<D>(raw, buf, b, task % L::kSlabs, info.special, info.value_scale != 1.f, valid);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&buf_full[vb % 3]);
+            mbar_arrive(&buf_full[vb % C::kBuffers]);
             mbar_arrive(&raw_empty[st]);
           }
         }
       }
       __syncthreads();
-      tc_fence_after();
-      bufs += 2 * (to - from);
-      uses[0] += (items + 1) / 2, uses[1] += items / 2;
-      first = false;
-      unit += to - from;
-      at.tile = to;
+      w.done();
     }
     if (s_abort) {
       // a wait ran out: give the copies and products in flight the same time before their memory goes away
       if (tid == 0)
-        for (uint32_t n = raws > 2 ? raws - 2 : 0; n < raws; ++n) mbar_wait_bounded(&raw_full[n & 1], (n / 2) & 1);
+        for (uint32_t n = raws > C::kStages ? raws - C::kStages : 0; n < raws; ++n)
+          mbar_wait_bounded(&raw_full[n % C::kStages], (n / C::kStages) & 1);
       if (warp == 1 && elect_one()) {
-        tc_commit(&pv_done[0]);
-        mbar_wait_bounded(&pv_done[0], uses[0] & 1);
+        tc_commit(&s_drain);
+        mbar_wait_bounded(&s_drain, 0);
       }
     }
   }
