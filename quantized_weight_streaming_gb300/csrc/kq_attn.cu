@@ -698,66 +698,115 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a) {
   const Runs runs(prompt ? a.prompt_base[-1] : a.base[a.requests], prompt ? kSms : (int64_t)kSms * C::kWarps,
                   prompt ? P::kLeastRun : kLeastRun);
   const float unit = prompt ? 1.f : kOut<T, D>;
-  const int one = kWide ? blockIdx.x % a.q_heads : 0;
-  int64_t w0 = 0, w1 = 0, lo = 0;
-  int32_t tiles = 0, known = -1;  // of row tile `known` of key head hk
-  for (int hk = kWide ? one / a.group : warp; hk < (kWide ? one / a.group + 1 : a.cache.kv_heads); hk += kWarps, known = -1) {
-    for (int g = kWide ? one % a.group : 0; g < (kWide ? one % a.group + 1 : a.group); ++g) {
-      const int32_t x = i * a.group + g, tile = x / rows, in = x - tile * rows;
-      if (tile != known) {
-        known = tile;
-        tiles = q.tiles;
-        if (prompt) {
-          const int64_t block = a.prompt_first[r] + tile;
-          if (block >= a.prompt_cap) return;  // overlapping requests, left out
-          tiles = row_block<D>(a, q, tile).tiles;
-          lo = a.prompt_base[block] + (int64_t)hk * tiles;
-        } else {
-          lo = a.base[r] + ((int64_t)hk * row_tiles(q) + tile) * tiles;
-        }
-        if (tiles) w0 = runs.of(lo), w1 = runs.of(lo + tiles - 1);
+  // the units of row tile `tile` of key head hk, and the runs that hold them
+  struct Row {
+    int32_t tiles;
+    int64_t lo, w0, w1;
+  };
+  auto row_of = [&](int32_t tile, int hk) -> Row {
+    Row w{q.tiles, 0, 0, 0};
+    if (prompt) {
+      const int64_t block = a.prompt_first[r] + tile;
+      if (block >= a.prompt_cap) return w;  // overlapping requests, left out
+      w.tiles = row_block<D>(a, q, tile).tiles;
+      w.lo = a.prompt_base[block] + (int64_t)hk * w.tiles;
+    } else {
+      w.lo = a.base[r] + ((int64_t)hk * row_tiles(q) + tile) * w.tiles;
+    }
+    if (w.tiles) w.w0 = runs.of(w.lo), w.w1 = runs.of(w.lo + w.tiles - 1);
+    return w;
+  };
+  auto row_out = [&](int h) { return static_cast<T*>(a.out) + t * a.out_token + (int64_t)h * a.out_head; };
+  // one part joined to what there is of a row (a row of NaN scores keeps its reference at -inf and its weight NaN)
+  struct Sum {
+    float ref, weight, acc[kPer];
+  };
+  auto join = [&](Sum& s, float m, float l, const float(&o)[kPer]) {
+    const float now = fmaxf(s.ref, m);
+    const float keep = s.ref == -INFINITY ? 0.f : exp2_approx(s.ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
+    s.weight = s.weight * keep + (m == -INFINITY ? l : l * f);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s.acc[e] = s.acc[e] * keep + o[e] * f;
+    s.ref = now;
+  };
+  auto part_of = [&](const Row& w, int64_t run) { return parts + (2 * run + (runs.start(run) >= w.lo ? 0 : 1)) * partial; };
+  if constexpr (kWide) {
+    const int h = blockIdx.x % a.q_heads, hk = h / a.group;
+    const int32_t x = i * a.group + h % a.group, in = x % rows;
+    const Row w = row_of(x / rows, hk);
+    if (w.tiles == 0) {
+      for (int e = tid; e < D; e += kCombineThreads) row_out(h)[e] = kv::from_float<T>(0.f);
+      return;
+    }
+    if (w.w0 == w.w1) return;
+    Sum s{-INFINITY, 0.f, {}};
+    for (int64_t run = w.w0 + warp; run <= w.w1; run += kWarps) {
+      const float* p = part_of(w, run);
+      float o[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = p[(int64_t)in * D + lane * kPer + e];
+      join(s, p[rows * D + in], p[rows * D + rows + in], o);
+    }
+    if (lane == 0) s_ref[warp] = s.ref, s_weight[warp] = s.weight;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = s.acc[e];
+    __syncthreads();
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_ref[v]);
+    for (int e = tid; e < D; e += kCombineThreads) {
+      float sum = 0.f, l = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float f = s_ref[v] == -INFINITY ? 0.f : exp2_approx(s_ref[v] - top);
+        sum += s_sum[v][e] * f;
+        l += s_ref[v] == -INFINITY ? s_weight[v] : s_weight[v] * f;
       }
-      T* dst = static_cast<T*>(a.out) + t * a.out_token + (int64_t)(hk * a.group + g) * a.out_head;
-      if (tiles == 0) {
-        for (int e = kWide ? tid : lane; e < D; e += kWide ? kCombineThreads : 32) dst[e] = kv::from_float<T>(0.f);
-        continue;
-      }
-      if (w0 == w1) continue;
-      float ref = -INFINITY, weight = 0.f, acc[kPer] = {};
-      for (int64_t w = w0 + (kWide ? warp : 0); w <= w1; w += kWide ? kWarps : 1) {
-        const float* p = parts + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * partial;
-        const float m = p[rows * D + in], l = p[rows * D + rows + in];
-        const float* o = p + (int64_t)in * D + lane * kPer;
-        const float now = fmaxf(ref, m);
-        const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
-        // a row of NaN scores keeps its reference at -inf and its weight NaN: it goes through
-        weight = weight * keep + (m == -INFINITY ? l : l * f);
+      row_out(h)[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
+    }
+  } else {
+    constexpr int kAtOnce = 4;  // heads whose parts are loaded together
+    for (int hk = warp; hk < a.cache.kv_heads; hk += kWarps) {
+      int32_t known = -1;
+      Row w{};
+      for (int g0 = 0; g0 < a.group;) {
+        const int32_t x = i * a.group + g0, tile = x / rows, in = x - tile * rows;
+        const int n = min(min(kAtOnce, a.group - g0), rows - in);  // of one row tile
+        if (tile != known) w = row_of(known = tile, hk);
+        if (w.tiles == 0) {
+          for (int g = 0; g < n; ++g)
+            for (int e = lane; e < D; e += 32) row_out(hk * a.group + g0 + g)[e] = kv::from_float<T>(0.f);
+        } else if (w.w0 != w.w1) {
+          Sum s[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * keep + o[e] * f;
-        ref = now;
-      }
-      if constexpr (!kWide) {
-        const float f = weight == 0.f ? 0.f : unit / weight;
+          for (int g = 0; g < kAtOnce; ++g) {
+            s[g].ref = -INFINITY, s[g].weight = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) dst[lane * kPer + e] = kv::from_float<T>(acc[e] * f);
-      } else {
-        if (lane == 0) s_ref[warp] = ref, s_weight[warp] = weight;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = acc[e];
-        __syncthreads();
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ref[w]);
-        for (int e = tid; e < D; e += kCombineThreads) {
-          float sum = 0.f, l = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float f = s_ref[w] == -INFINITY ? 0.f : exp2_approx(s_ref[w] - top);
-            sum += s_sum[w][e] * f;
-            l += s_ref[w] == -INFINITY ? s_weight[w] : s_weight[w] * f;
+            for (int e = 0; e < kPer; ++e) s[g].acc[e] = 0.f;
           }
-          dst[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
+          for (int64_t run = w.w0; run <= w.w1; ++run) {
+            const float* p = part_of(w, run);
+            float o[kAtOnce][kPer], m[kAtOnce], l[kAtOnce];
+#pragma unroll
+            for (int g = 0; g < kAtOnce; ++g) {
+              const int at = min(in + g, in + n - 1);
+              m[g] = p[rows * D + at], l[g] = p[rows * D + rows + at];
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) o[g][e] = p[(int64_t)at * D + lane * kPer + e];
+            }
+#pragma unroll
+            for (int g = 0; g < kAtOnce; ++g) join(s[g], m[g], l[g], o[g]);
+          }
+#pragma unroll
+          for (int g = 0; g < kAtOnce; ++g) {
+            if (g >= n) break;
+            const float f = s[g].weight == 0.f ? 0.f : unit / s[g].weight;
+            T* dst = row_out(hk * a.group + g0 + g);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) dst[lane * kPer + e] = kv::from_float<T>(s[g].acc[e] * f);
+          }
         }
+        g0 += n;
       }
     }
   }

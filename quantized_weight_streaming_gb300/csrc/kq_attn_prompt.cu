@@ -19,8 +19,8 @@
 // the tile's keys or values are divided by 8, and scores or probabilities
 // multiplied by it.
 //
-// Roles: warp 0 copies granules into raw stages; warp 1 issues the MMAs; warp 2
-// looks at a stage's scales; warps 4-7 and 8-11 are the softmax of the two M
+// Roles: warp 0 copies granules into raw stages; warps 1 and 3 issue the MMAs of
+// an M tile each; warp 2 looks at a stage's scales; warps 4-7 and 8-11 are the softmax of the two M
 // tiles; warps 12-19 unpack, into a ring of buffers that keys and values take
 // in turn (with four warps unpacking bound the kernel: 507 us against 309
 // without it).  Each M tile has two S buffers
@@ -229,11 +229,12 @@ struct Walk {
   RowBlock blk;
   int32_t from, to, tiles, nm;   // key tiles of the segment, its M tiles
   uint32_t bufs;                 // buffers of keys and values used so far
+  uint32_t queries;              // bit m: how many segments M tile m has been part of, modulo 2
   uint32_t uses;                 // bit 2 m + b: how often S buffer b of M tile m has been used, modulo 2
   bool first;
 
   __device__ __forceinline__ Walk(const Args& args, const Place& p, int64_t u, int64_t e)
-      : a(args), at(p), unit(u), end(e), bufs(0), uses(0), first(true) {
+      : a(args), at(p), unit(u), end(e), bufs(0), queries(0), uses(0), first(true) {
     if (unit < end) {
       q = request_of(a, at.r, S::kKeys);
       blk = row_block<D>(a, q, at.k);
@@ -265,6 +266,7 @@ struct Walk {
   __device__ __forceinline__ void done() {
     bufs += 2 * tiles;
     uses ^= ((((tiles + 1) / 2) & 1u) | ((tiles / 2) & 1u) << 1) * (nm == 2 ? 5u : 1u);
+    queries ^= nm == 2 ? 3u : 1u;
     first = false;
     unit += tiles;
     at.tile = to;
@@ -278,11 +280,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   constexpr int N = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t raw_full[C::kStages], raw_seen[C::kStages], raw_empty[C::kStages], buf_full[C::kBuffers], buf_empty[C::kBuffers];
-  __shared__ uint64_t s_full[C::kTiles][2], p_full[C::kTiles][2], pv_done[C::kTiles][2];
+  __shared__ uint64_t s_full[C::kTiles][2], p_full[C::kTiles][2], pv_done[C::kTiles][2], q_full[C::kTiles];
   __shared__ TileInfo s_info[kInfos];
   __shared__ uint8_t s_nan[kInfos][N];        // groups of a key whose value scale is not finite
   __shared__ uint32_t s_hidden[C::kStages];   // of a raw stage
-  __shared__ uint64_t s_drain;
+  __shared__ uint64_t s_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int64_t s_entry[kPromptThreads];  // row blocks before each request of a chunk
@@ -302,11 +304,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       mbar_init(&p_full[i / 2][i & 1], 128);
       mbar_init(&pv_done[i / 2][i & 1], 1);
     }
+    for (int i = 0; i < C::kTiles; ++i) mbar_init(&q_full[i], 128);
     for (int i = 0; i < C::kBuffers; ++i) {
       mbar_init(&buf_full[i], kUnpackWarps);
-      mbar_init(&buf_empty[i], 1);
+      mbar_init(&buf_empty[i], C::kTiles);
     }
-    mbar_init(&s_drain, 1);
+    mbar_init(&s_drain[0], 1);
+    mbar_init(&s_drain[1], 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -339,6 +343,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
     int64_t total = 0;
     const bool writer = blockIdx.x == 0;
     for (int pass = 0; pass < 2; ++pass) {
+      // the thread's last row block, whose place starts the run if the run starts in it
+      Place p{};
+      int64_t u = 0, first_unit = 0;
+      int32_t tiles = 0;
+      auto found = [&]() {
+        if (u > 0 && unit >= first_unit && unit < first_unit + u) {
+          const int64_t in = unit - first_unit;
+          p.h = (int32_t)(in / tiles), p.tile = (int32_t)(in % tiles);
+          s_place = p;
+        }
+      };
       int64_t units = 0, entries = 0;
       for (int64_t r0 = 0; r0 < a.requests; r0 += kPromptThreads) {
         int64_t blocks = 0;
@@ -354,9 +369,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         const int in_chunk = (int)min((int64_t)kPromptThreads, a.requests - r0);
         for (int64_t e0 = 0; e0 < all; e0 += kPromptThreads) {
           const int64_t e = e0 + tid;
-          int64_t u = 0, at, sum;
-          Place p{};
-          int32_t tiles = 0;
+          int64_t at, sum;
+          u = 0;
           if (e < all && entries + e < a.prompt_cap) {
             int l = 0, h = in_chunk;
             while (h - l > 1) {  // the last request whose first row block is not after e
@@ -369,11 +383,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           }
           block_sum(u, at, sum);
           if (writer && pass == 0 && e < all && entries + e < a.prompt_cap) a.prompt_base[entries + e] = units + at;
-          if (pass == 1 && u > 0 && unit >= units + at && unit < units + at + u) {
-            const int64_t in = unit - units - at;
-            p.h = (int32_t)(in / tiles), p.tile = (int32_t)(in % tiles);
-            s_place = p;
-          }
+          first_unit = units + at;
+          if (pass == 1) found();
           units += sum;
         }
         entries += all;
@@ -385,6 +396,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         const Runs runs(total, kSms, C::kLeastRun);
         if (blockIdx.x < runs.count) unit = runs.start(blockIdx.x), end = runs.start(blockIdx.x + 1);
         if (unit == end) break;  // the same for the whole CTA
+        if (a.requests <= kPromptThreads && entries <= kPromptThreads) {  // one look was enough
+          found();
+          break;
+        }
       }
     }
   }
@@ -395,7 +410,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   const Gate gate{&s_abort};
   Walk<D> w(a, s_place, unit, end);
   uint32_t raws = 0;  // raw stages that a copying, looking or unpacking warp is through with
-  // Each role walks over the run's segments by itself; all meet when a segment's queries are in place, and at its end.
+  // Each role walks over the run's segments by itself, copies and unpacking ahead into the next one as far as their
+  // rings go.
   if (warp >= 4 && warp < 4 + 4 * C::kTiles) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     while (w.next()) {
@@ -407,37 +423,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       const int32_t pos = w.q.pos0 + i;
       const int32_t key_hi = live ? max(0, min(pos + 1, w.q.len)) : 0x7fffffff;
       const int32_t key_lo = live && a.window ? max(0, pos - (a.window - 1)) : 0;
+      // A row's D / 8 lanes load it, eight dimensions each; the factor then goes to the row's own thread.
       float factor = 0.f;
       if (m_tile < w.nm) {
-        const T* src = static_cast<const T*>(a.q) + (int64_t)(w.q.first + i) * a.q_token +
-                       (int64_t)(w.at.h * a.group + x % a.group) * a.q_head;
-        float top = 0.f;
-        if (live) {
-          for (int e = 0; e < D; e += 8) {
-            float v[8];
-            kv::load8(src + e, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-          }
-        }
-        int e2 = 0;
-        if (top > 0.f && top <= 3.402823466e38f) frexpf(top, &e2);
-        e2 = min(max(8 - e2, -110), 110);  // the row times 2^e2 lies below 2^8
-        // the scale's sign goes with the queries, so that larger sums are larger scores
-        const float up = a.scale == 0.f ? 0.f : copysignf(ldexpf(1.f, e2), a.scale);
-        factor = fmaxf(ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2), 1e-37f);
-        uint8_t* dst = smem + m_tile * C::kQBytes + row * 128;
-        for (int e = 0; e < D; e += 8) {
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int l = lane % kLanes, sub = lane / kLanes;
+        uint8_t* tile = smem + m_tile * C::kQBytes + (l / 8) * (128 * 128);
+#pragma unroll 4
+        for (int it = 0; it < kLanes; ++it) {
+          const int rr = (warp & 3) * 32 + it * kAtOnce + sub;
+          const int32_t y = w.at.k * C::kRows + m_tile * 128 + rr, token = y / a.group;
           float v[8] = {};
-          if (live) kv::load8(src + e, v);
+          if (m_tile * 128 + rr < w.blk.rows)
+            kv::load8(static_cast<const T*>(a.q) + (int64_t)(w.q.first + token) * a.q_token +
+                          (int64_t)(w.at.h * a.group + y % a.group) * a.q_head + 8 * l,
+                      v);
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+          int e2 = 0;
+          if (top > 0.f && top <= 3.402823466e38f) frexpf(top, &e2);
+          e2 = min(max(8 - e2, -110), 110);  // the row times 2^e2 lies below 2^8
+          // the scale's sign goes with the queries, so that larger sums are larger scores
+          const float up = a.scale == 0.f ? 0.f : copysignf(ldexpf(1.f, e2), a.scale);
+          const float f = fmaxf(ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2), 1e-37f);
+          const float mine = __shfl_sync(~0u, f, (lane - it * kAtOnce) * kLanes);
+          if (lane / kAtOnce == it) factor = mine;
           uint4 o;
           o.x = pack2(v[0] * up, v[4] * up), o.y = pack2(v[1] * up, v[5] * up);
           o.z = pack2(v[2] * up, v[6] * up), o.w = pack2(v[3] * up, v[7] * up);
-          *reinterpret_cast<uint4*>(dst + (e / 64) * (128 * 128) + (((e % 64 / 8) ^ (row & 7)) << 4)) = o;
+          *reinterpret_cast<uint4*>(tile + rr * 128 + (((l % 8) ^ (rr & 7)) << 4)) = o;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      __syncthreads();
+      // the segment's queries are in place, and what the last one left in O has been read
+      if (m_tile < w.nm) mbar_arrive(&q_full[m_tile]);
       // ---- softmax ----
       if (m_tile < w.nm) {
         float ref = -INFINITY, weight = 0.f;
@@ -525,45 +547,58 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         gate.wait(&pv_done[m_tile][(w.tiles - 1) & 1], w.phase(m_tile, w.tiles - 1));
         __syncwarp();
         tc_fence_after();
-        const bool whole = w.from == 0 && w.to == w.blk.tiles;
-        const int in = m_tile * 128 + row;
-        float* part = a.prompt_partials + (2 * (int64_t)blockIdx.x + (w.first ? 0 : 1)) * C::kPartial;
-        T* dst = static_cast<T*>(a.out) + (int64_t)(w.q.first + i) * a.out_token +
-                 (int64_t)(w.at.h * a.group + x % a.group) * a.out_head;
-        const float scale = whole ? (weight == 0.f ? 0.f : 1.f / weight) : 1.f;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(tmem + lanes + C::kO + m_tile * D + c, o);
-          tmem_ld_wait();
-          if (live) {
-            const float poison = nan_groups >> (c / 32) & 1u ? NAN : 0.f;
-            float lo[8], hi[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) lo[e] = o[e] * scale + poison, hi[e] = o[8 + e] * scale + poison;
-            if (whole) {
-              kv::store8(dst + c, lo);
-              kv::store8(dst + c + 8, hi);
-            } else {
-              kv::store8(part + in * D + c, lo);
-              kv::store8(part + in * D + c + 8, hi);
-            }
+          const bool whole = w.from == 0 && w.to == w.blk.tiles;
+          float* part = a.prompt_partials + (2 * (int64_t)blockIdx.x + (w.first ? 0 : 1)) * C::kPartial;
+          const float scale = whole ? (weight == 0.f ? 0.f : 1.f / weight) : 1.f;
+          if (!whole && live) {
+            part[C::kRows * D + m_tile * 128 + row] = ref;
+            part[C::kRows * D + C::kRows + m_tile * 128 + row] = weight;
           }
-          __syncwarp();
-        }
-        if (!whole && live) {
-          part[C::kRows * D + in] = ref;
-          part[C::kRows * D + C::kRows + in] = weight;
-        }
+          // 32 dimensions at a time, turned in the warp's own part of the queries' place: a row's thread has its sums,
+          // eight lanes store them side by side
+          uint8_t* turn = smem + m_tile * C::kQBytes + (warp & 3) * 32 * 128;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanes + C::kO + m_tile * D + c, o);
+            tmem_ld_wait();
+            const float poison = nan_groups >> (c / 32) & 1u ? NAN : 0.f;
+            uint8_t* mine = turn + lane * 128;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float4 v;
+              v.x = __uint_as_float(o[4 * e]) * scale + poison, v.y = __uint_as_float(o[4 * e + 1]) * scale + poison;
+              v.z = __uint_as_float(o[4 * e + 2]) * scale + poison, v.w = __uint_as_float(o[4 * e + 3]) * scale + poison;
+              *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) << 4)) = v;
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int it = 0; it < 8; ++it) {
+              const int rr = 4 * it + lane / 8, in = m_tile * 128 + (warp & 3) * 32 + rr, e = lane & 7;
+              const float4 v = *reinterpret_cast<const float4*>(turn + rr * 128 + ((e ^ (rr & 7)) << 4));
+              if (in < w.blk.rows) {
+                if (whole) {
+                  const int32_t y = w.at.k * C::kRows + in;
+                  T* dst = static_cast<T*>(a.out) + (int64_t)(w.q.first + y / a.group) * a.out_token +
+                           (int64_t)(w.at.h * a.group + y % a.group) * a.out_head + c + 4 * e;
+                  union { uint2 u; T t[4]; } z;
+                  z.t[0] = kv::from_float<T>(v.x), z.t[1] = kv::from_float<T>(v.y);
+                  z.t[2] = kv::from_float<T>(v.z), z.t[3] = kv::from_float<T>(v.w);
+                  *reinterpret_cast<uint2*>(dst) = z.u;
+                } else {
+                  *reinterpret_cast<float4*>(part + (int64_t)in * D + c + 4 * e) = v;
+                }
+              }
+            }
+            __syncwarp();
+          }
         tc_fence_before();
       }
-      __syncthreads();
       w.done();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     while (w.next()) {
-      __syncthreads();
       if (warp == 0) {
         // ---- copies ----
         const uint64_t policy = l2_policy_evict_first();
@@ -595,45 +630,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
                          (granule % per_page) * L::kBytes,
                      L::kBytes, &raw_full[st], policy);
         }
-      } else if (warp == 1) {
-        // ---- matrix products ----
-        tc_fence_after();
+      } else if (warp == 1 || (warp == 3 && C::kTiles == 2)) {
+        // ---- matrix products, an issuing warp per M tile ----
+        const int m = warp / 2;
         if (elect_one()) {
+          const bool busy = m < w.nm;  // else only the buffers' turns are taken
+          if (busy) gate.wait(&q_full[m], (w.queries >> m) & 1);
           const uint32_t qk = idesc_f16(128, N), pv = idesc_f16(128, D);
+          const uint64_t ad = sw128_desc(smem + m * C::kQBytes);
           for (int j = 0; j <= w.tiles; ++j) {
             if (j < w.tiles) {  // S = Q K^T of tile j
               const uint32_t kb = w.bufs + 2 * j;
               const int b = j & 1, buf = kb % C::kBuffers;
+              // the buffer's last S and P are read
+              if (busy && j >= 2) gate.wait(&pv_done[m][b], w.phase(m, j - 2));
               gate.wait(&buf_full[buf], (kb / C::kBuffers) & 1);
-              const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
-              for (int m = 0; m < w.nm; ++m) {
-                // the buffer's last S and P are read
-                if (j >= 2) gate.wait(&pv_done[m][b], w.phase(m, j - 2));
+              if (busy) {
                 tc_fence_after();
-                const uint64_t ad = sw128_desc(smem + m * C::kQBytes);
+                const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                   tc_mma_ss(tmem + (2 * m + b) * N, ad + (uint64_t)(((k / 4) * 128 * 128 + (k % 4) * 32) >> 4),
                             bd + (uint64_t)(((k / 4) * N * 128 + (k % 4) * 32) >> 4), qk, k > 0);
                 tc_commit(&s_full[m][b]);
+                tc_commit(&buf_empty[buf]);
+              } else {
+                mbar_arrive(&buf_empty[buf]);
               }
-              tc_commit(&buf_empty[buf]);
             }
             if (j > 0) {  // O += P V of tile j - 1
               const uint32_t vb = w.bufs + 2 * j - 1;
               const int b = (j - 1) & 1, buf = vb % C::kBuffers;
               gate.wait(&buf_full[buf], (vb / C::kBuffers) & 1);
-              const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
-              for (int m = 0; m < w.nm; ++m) {
+              if (busy) {
                 gate.wait(&p_full[m][b], w.phase(m, j - 1));
                 tc_fence_after();
+                const uint64_t bd = sw128_desc(smem + C::kRing + buf * C::kBuffer);
 #pragma unroll
                 for (int k = 0; k < N / 16; ++k)
                   tc_mma_ts(tmem + C::kO + m * D, tmem + (2 * m + b) * N + k * 8, bd + (uint64_t)((k * 32) >> 4), pv,
                             j > 1 || k > 0);
                 tc_commit(&pv_done[m][b]);
+                tc_commit(&buf_empty[buf]);
+              } else {
+                mbar_arrive(&buf_empty[buf]);
               }
-              tc_commit(&buf_empty[buf]);
             }
           }
         }
@@ -722,7 +763,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           }
         }
       }
-      __syncthreads();
       w.done();
     }
     if (s_abort) {
@@ -730,9 +770,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       if (tid == 0)
         for (uint32_t n = raws > C::kStages ? raws - C::kStages : 0; n < raws; ++n)
           mbar_wait_bounded(&raw_full[n % C::kStages], (n / C::kStages) & 1);
-      if (warp == 1 && elect_one()) {
-        tc_commit(&s_drain);
-        mbar_wait_bounded(&s_drain, 0);
+      if ((warp == 1 || (warp == 3 && C::kTiles == 2)) && elect_one()) {
+        tc_commit(&s_drain[warp / 2]);
+        mbar_wait_bounded(&s_drain[warp / 2], 0);
       }
     }
   }
