@@ -21,9 +21,10 @@
 //
 // Roles: warp 0 copies granules into raw stages; warps 1 and 3 issue the MMAs of
 // an M tile each; warp 2 looks at a stage's scales; warps 4-7 and 8-11 are the softmax of the two M
-// tiles; warps 12-19 unpack, into a ring of buffers that keys and values take
-// in turn (with four warps unpacking bound the kernel: 507 us against 309
-// without it).  Each M tile has two S buffers
+// tiles; warps 12-15 and 16-19 unpack every other key tile, into a ring of
+// buffers that keys and values take in turn (one group of four warps bound the
+// kernel: 507 us, 309 without it; eight warps on every tile spent 750 of their
+// 2600 cycles a tile at barriers and had one chain of work at a time).  Each M tile has two S buffers
 // (P replaces S in place), and QK of the next key tile is issued before PV of
 // this one, so that a softmax finds its next scores waiting: with one S buffer
 // of 128 keys per M tile the chain QK, softmax, PV bound the kernel (382 us for
@@ -54,8 +55,8 @@ __device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_sta
 // Five warpgroups of 96 registers a thread at launch: two that keep scores in registers take 144, the others give 32
 // back (2 x 144 + 3 x 64 = 5 x 96).
 constexpr int kPromptWarps = 20, kPromptThreads = 32 * kPromptWarps;
-constexpr int kUnpackFirst = 12, kUnpackWarps = 8;
-constexpr float kPromptSlack = 8.f;
+constexpr int kUnpackFirst = 12, kUnpackWarps = 4;  // two groups of them, a key tile in turn each
+constexpr float kPromptMost = 4096.f;  // times 8 (see above) still fits fp16
 constexpr int kInfos = 8;            // key tiles between unpacking and softmax, and more
 
 template <int D>
@@ -212,6 +213,11 @@ __device__ __forceinline__ uint32_t hidden_keys(uint32_t hidden, int c) {
   return (h & 1u ? 0xFFFFu : 0u) | (h & 2u ? 0xFFFF0000u : 0u);
 }
 
+// A query row of a block: its token, and its head among those of the key head.
+struct RowAt {
+  int32_t token, head;
+};
+
 // The run's position: request, row block, key head, key tile.
 struct Place {
   int64_t r;
@@ -290,7 +296,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   __shared__ int64_t s_entry[kPromptThreads];  // row blocks before each request of a chunk
   __shared__ int64_t s_sum[kPromptWarps];
   __shared__ Place s_place;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset and not a rounded address: the compiler then still knows it for shared memory)
+  uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
@@ -414,6 +421,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   // rings go.
   if (warp >= 4 && warp < 4 + 4 * C::kTiles) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    // n / group = umulhi(n, per_group) for n below 2^32 / group: here n < group + 256
+    const uint32_t per_group = 0xFFFFFFFFu / (uint32_t)a.group + 1;
     while (w.next()) {
       // ---- queries: one thread a row ----
       const int m_tile = (warp - 4) / 4;
@@ -423,38 +432,56 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       const int32_t pos = w.q.pos0 + i;
       const int32_t key_hi = live ? max(0, min(pos + 1, w.q.len)) : 0x7fffffff;
       const int32_t key_lo = live && a.window ? max(0, pos - (a.window - 1)) : 0;
-      // A row's D / 8 lanes load it, eight dimensions each; the factor then goes to the row's own thread.
+      // A row's D / 8 lanes load it, eight dimensions each; the factor then goes to the row's own thread.  (The scale's
+      // sign goes with the queries, so that larger sums are larger scores.)
+      const int32_t token0 = w.q.first + w.at.k * C::kRows / a.group, head0 = w.at.k * C::kRows % a.group;
+      auto rows_at = [&](int in) {  // row `in` of the block
+        const uint32_t n = head0 + in, d = a.group == 1 ? n : __umulhi(n, per_group);
+        return RowAt{token0 + (int32_t)d, (int32_t)(n - d * a.group)};
+      };
       float factor = 0.f;
       if (m_tile < w.nm) {
+        // (Copied to their place first, then scaled there in a short loop: a segment runs this code once, so its
+        // instructions come from far away, and 16 rows unrolled took 15000 cycles.)
         constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
         const int l = lane % kLanes, sub = lane / kLanes;
         uint8_t* tile = smem + m_tile * C::kQBytes + (l / 8) * (128 * 128);
-#pragma unroll 4
+        const float score = a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f;
+        const float sign = a.scale == 0.f ? 0.f : copysignf(1.f, a.scale);
+        const T* src = static_cast<const T*>(a.q) + (int64_t)w.at.h * a.group * a.q_head + 8 * l;
+#pragma unroll 1
         for (int it = 0; it < kLanes; ++it) {
           const int rr = (warp & 3) * 32 + it * kAtOnce + sub;
-          const int32_t y = w.at.k * C::kRows + m_tile * 128 + rr, token = y / a.group;
-          float v[8] = {};
-          if (m_tile * 128 + rr < w.blk.rows)
-            kv::load8(static_cast<const T*>(a.q) + (int64_t)(w.q.first + token) * a.q_token +
-                          (int64_t)(w.at.h * a.group + y % a.group) * a.q_head + 8 * l,
-                      v);
-          float top = 0.f;
+          const bool held = m_tile * 128 + rr < w.blk.rows;
+          const RowAt y = rows_at(held ? m_tile * 128 + rr : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(tile + rr * 128 + (((l % 8) ^ (rr & 7)) << 4))),
+                       "l"(src + (int64_t)y.token * a.q_token + (int64_t)y.head * a.q_head), "r"(held ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int it = 0; it < kLanes; ++it) {
+          const int rr = (warp & 3) * 32 + it * kAtOnce + sub;
+          uint4* place = reinterpret_cast<uint4*>(tile + rr * 128 + (((l % 8) ^ (rr & 7)) << 4));
+          union { uint4 u; T t[8]; } in;
+          in.u = *place;
+          float v[8], top = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+          for (int e = 0; e < 8; ++e) v[e] = kv::to_float(in.t[e]), top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-          int e2 = 0;
-          if (top > 0.f && top <= 3.402823466e38f) frexpf(top, &e2);
-          e2 = min(max(8 - e2, -110), 110);  // the row times 2^e2 lies below 2^8
-          // the scale's sign goes with the queries, so that larger sums are larger scores
-          const float up = a.scale == 0.f ? 0.f : copysignf(ldexpf(1.f, e2), a.scale);
-          const float f = fmaxf(ldexpf(a.scale == 0.f ? 1.f : fabsf(a.scale) * 1.4426950408889634f, -e2), 1e-37f);
+          // 2^e2 brings the row's largest into [2^7, 2^8); an infinite row is left as it is
+          const int exponent = (int)(__float_as_uint(top) >> 23);
+          const int e2 = exponent == 255 ? 0 : min(max(134 - exponent, -110), 110);
+          const float up = sign * __uint_as_float((uint32_t)(127 + e2) << 23);
+          const float f = fmaxf(score * __uint_as_float((uint32_t)(127 - e2) << 23), 1e-37f);
           const float mine = __shfl_sync(~0u, f, (lane - it * kAtOnce) * kLanes);
           if (lane / kAtOnce == it) factor = mine;
           uint4 o;
           o.x = pack2(v[0] * up, v[4] * up), o.y = pack2(v[1] * up, v[5] * up);
           o.z = pack2(v[2] * up, v[6] * up), o.w = pack2(v[3] * up, v[7] * up);
-          *reinterpret_cast<uint4*>(tile + rr * 128 + (((l % 8) ^ (rr & 7)) << 4)) = o;
+          *place = o;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -489,16 +516,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
                 if (!(see >> e & 1u)) s[c][e] = 0xFF800000u;  // -inf
             }
           }
-          float top = -INFINITY;
+          auto largest = [&]() {  // of the row's scores, log2
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, fmaxf(__uint_as_float(s[0][e]), __uint_as_float(s[1][e])));
-          top *= f;
-          const bool moves = top > ref + kPromptSlack;
-          if (__any_sync(~0u, moves)) {
-            const float keep = !moves ? 1.f : (ref == -INFINITY ? 0.f : exp2_approx(ref - top));
+            for (int e = 0; e < 32; ++e)
+              top[e % 4] = fmaxf(top[e % 4], fmaxf(__uint_as_float(s[0][e]), __uint_as_float(s[1][e])));
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+          };
+          if (__any_sync(~0u, ref == -INFINITY)) {  // a row's first scores; nothing of it is in O yet
+            const float top = largest();
+            if (ref == -INFINITY) ref = top;
+          }
+          // p = 2^(f S - ref).  The reference stays while a tile's p add up to less than 2^12 (each then fits fp16): the
+          // exponentials wait for no maximum.
+          uint32_t p[32];
+          float2 acc;
+          while (true) {
+            const float minus = ref == -INFINITY ? 0.f : -ref;
+            float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              const float2 v = make_float2(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1]));
+              float2 y = fma2(v, make_float2(f, f), make_float2(minus, minus));
+              y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              sums[e / 2 % 2] = add2(sums[e / 2 % 2], y);
+              p[e / 2] = pack2(y.x, y.y);
+            }
+            acc = add2(sums[0], sums[1]);
+            const bool moves = acc.x + acc.y > kPromptMost;
+            if (!__any_sync(~0u, moves)) break;
+            const float top = largest(), keep = moves ? exp2_approx(ref - top) : 1.f;
             if (moves) ref = top;
             weight *= keep;
-            if (j > 0) {  // rescale what earlier w.tiles left in O, once the last of them is in
+            if (j > 0) {  // rescale what earlier tiles left in O, once the last of them is in
               gate.wait(&pv_done[m_tile][b ^ 1], w.phase(m_tile, j - 1));
               __syncwarp();
               tc_fence_after();
@@ -514,26 +564,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
               }
             }
           }
-          // p = 2^(f S - ref), over the scores
-          const float minus = ref == -INFINITY ? 0.f : -ref;
-          float2 acc = make_float2(0.f, 0.f);
+          if (info.value_scale != 1.f) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 y = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(f, f),
-                              make_float2(minus, minus));
-              y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-              acc = add2(acc, y);
-              p[e / 2] = pack2(y.x, y.y);
-            }
-            if (info.value_scale != 1.f) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) p[e] = as_u32(__hmul2(as_h2(p[e]), __float2half2_rn(8.f)));
-            }
-            tmem_st16(s_at + 16 * c, p);
+            for (int e = 0; e < 32; ++e) p[e] = as_u32(__hmul2(as_h2(p[e]), __float2half2_rn(8.f)));
           }
+          tmem_st32(s_at, p);
           weight += acc.x + acc.y;
           if (info.nan) {
             for (int e = 0; e < N; ++e)
@@ -578,9 +613,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
               const float4 v = *reinterpret_cast<const float4*>(turn + rr * 128 + ((e ^ (rr & 7)) << 4));
               if (in < w.blk.rows) {
                 if (whole) {
-                  const int32_t y = w.at.k * C::kRows + in;
-                  T* dst = static_cast<T*>(a.out) + (int64_t)(w.q.first + y / a.group) * a.out_token +
-                           (int64_t)(w.at.h * a.group + y % a.group) * a.out_head + c + 4 * e;
+                  const RowAt y = rows_at(in);
+                  T* dst = static_cast<T*>(a.out) + (int64_t)y.token * a.out_token +
+                           (int64_t)(w.at.h * a.group + y.head) * a.out_head + c + 4 * e;
                   union { uint2 u; T t[4]; } z;
                   z.t[0] = kv::from_float<T>(v.x), z.t[1] = kv::from_float<T>(v.y);
                   z.t[2] = kv::from_float<T>(v.z), z.t[3] = kv::from_float<T>(v.w);
@@ -723,8 +758,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         }
       } else if (warp >= kUnpackFirst) {
         // ---- unpacking ----
-        const int me = warp - kUnpackFirst;
+        const int me = (warp - kUnpackFirst) % kUnpackWarps;
+        const uint32_t group = (warp - kUnpackFirst) / kUnpackWarps;
         for (int32_t t = w.from; t < w.to; ++t, ++raws) {
+          if ((raws & 1) != group) continue;
           const int st = raws % C::kStages;
           const uint8_t* raw = smem + C::kRawAt + st * C::kRaw;
           gate.wait(&raw_seen[st], (raws / C::kStages) & 1);
