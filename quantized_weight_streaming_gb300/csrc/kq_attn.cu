@@ -61,7 +61,9 @@ constexpr int kRows = 8;             // query rows of a tile
 constexpr float kSlack = 6.f;        // log2 by which a score may pass the reference
 constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
 constexpr int kCombineThreads = 256;
-constexpr int kWideRows = 2048;      // query rows up to which a CTA joins one
+constexpr int kJoinRows = 16, kZeroCtas = 8;
+template <int D>
+constexpr int kJoinSlices = PromptShape<D>::kRows / kJoinRows;
 constexpr int kLeastRun = 2;         // tiles of a run, where there are fewer than two for every warp
 
 template <typename T, int D>
@@ -666,147 +668,144 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   }
 }
 
-// Rows that were cut between runs: their parts joined in run order; rows that
-// see nothing: zeros.  kWide: a CTA per token and query head, whose warps share
-// out the parts of the row (a short list of rows, each in many parts).
-// Otherwise a CTA per token, a warp per key head (many rows, few of them cut).
-template <typename T, int D, bool kWide>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a) {
+// One part of a row joined to what there is of it (a row of NaN scores keeps its reference at -inf and its weight NaN).
+template <int N>
+struct Sum {
+  float ref = -INFINITY, weight = 0.f, acc[N] = {};
+  __device__ __forceinline__ void join(float m, float l, const float (&o)[N]) {
+    const float now = fmaxf(ref, m);
+    const float keep = ref == -INFINITY ? 0.f : exp2_approx(ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
+    weight = weight * keep + (m == -INFINITY ? l : l * f);
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = acc[e] * keep + o[e] * f;
+    ref = now;
+  }
+};
+// N consecutive values, N = 2, 4 or 8.
+template <int N>
+__device__ __forceinline__ void load_part(float (&o)[N], const float* p) {
+  if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    o[0] = v.x, o[1] = v.y;
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + e);
+      o[e] = v.x, o[e + 1] = v.y, o[e + 2] = v.z, o[e + 3] = v.w;
+    }
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* p, const float (&o)[N], float f) {
+  union { uint32_t u[N * sizeof(T) / 4]; T t[N]; } y;
+#pragma unroll
+  for (int e = 0; e < N; ++e) y.t[e] = kv::from_float<T>(o[e] * f);
+#pragma unroll
+  for (int e = 0; e < (int)(N * sizeof(T) / 4); ++e) reinterpret_cast<uint32_t*>(p)[e] = y.u[e];
+}
+
+// Joins, in run order, the parts of rows that were cut between runs, and writes
+// zeros where a row sees nothing.
+//  - The first few_ctas CTAs: eight query rows of one request and key head each
+//    (a row tile of attend_kernel; its rows were cut at the same places).  The
+//    warps share out rows, and then the parts of a row.
+//  - The others: 16 rows of the row block that a boundary between two runs of
+//    the prompt kernel falls in.
+//  - The last kZeroCtas of them: prompts' row blocks that see nothing.
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int slices, int64_t few_ctas) {
   using C = Config<T, D>;
   using P = PromptShape<D>;
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
-  __shared__ int64_t s_request;
-  __shared__ float s_sum[kWide ? kWarps : 1][D], s_ref[kWarps], s_weight[kWarps];
+  __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t t = kWide ? blockIdx.x / a.q_heads : blockIdx.x;
-  if (tid == 0) s_request = -1;
-  __syncthreads();
-  for (int64_t r = tid; r < a.requests; r += kCombineThreads)
-    if (a.q_start[r] <= t && t < a.q_start[r + 1]) s_request = r;
-  __syncthreads();
-  const int64_t r = s_request;
-  if (r < 0) return;
-  const Request q = request_of(a, r, C::kTile);
-  const int32_t i = (int32_t)(t - q.first);
-  if (i < 0 || i >= q.n) return;
-  const bool prompt = q.rows > a.few_rows;
-  const int rows = prompt ? P::kRows : kRows;  // of a partial result
-  const int64_t partial = prompt ? P::kPartial : kPartial<D>;
-  const float* parts = prompt ? a.prompt_partials : a.partials;
-  const Runs runs(prompt ? a.prompt_base[-1] : a.base[a.requests], prompt ? kSms : (int64_t)kSms * C::kWarps,
-                  prompt ? P::kLeastRun : kLeastRun);
-  const float unit = prompt ? 1.f : kOut<T, D>;
-  // the units of row tile `tile` of key head hk, and the runs that hold them
-  struct Row {
-    int32_t tiles;
-    int64_t lo, w0, w1;
+  auto row_out = [&](const Request& q, int h, int32_t x) {
+    return static_cast<T*>(a.out) + (int64_t)(q.first + x / a.group) * a.out_token +
+           (int64_t)(h * a.group + x % a.group) * a.out_head;
   };
-  auto row_of = [&](int32_t tile, int hk) -> Row {
-    Row w{q.tiles, 0, 0, 0};
-    if (prompt) {
-      const int64_t block = a.prompt_first[r] + tile;
-      if (block >= a.prompt_cap) return w;  // overlapping requests, left out
-      w.tiles = row_block<D>(a, q, tile).tiles;
-      w.lo = a.prompt_base[block] + (int64_t)hk * w.tiles;
-    } else {
-      w.lo = a.base[r] + ((int64_t)hk * row_tiles(q) + tile) * w.tiles;
-    }
-    if (w.tiles) w.w0 = runs.of(w.lo), w.w1 = runs.of(w.lo + w.tiles - 1);
-    return w;
-  };
-  auto row_out = [&](int h) { return static_cast<T*>(a.out) + t * a.out_token + (int64_t)h * a.out_head; };
-  // one part joined to what there is of a row (a row of NaN scores keeps its reference at -inf and its weight NaN)
-  struct Sum {
-    float ref, weight, acc[kPer];
-  };
-  auto join = [&](Sum& s, float m, float l, const float(&o)[kPer]) {
-    const float now = fmaxf(s.ref, m);
-    const float keep = s.ref == -INFINITY ? 0.f : exp2_approx(s.ref - now), f = m == -INFINITY ? 0.f : exp2_approx(m - now);
-    s.weight = s.weight * keep + (m == -INFINITY ? l : l * f);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s.acc[e] = s.acc[e] * keep + o[e] * f;
-    s.ref = now;
-  };
-  auto part_of = [&](const Row& w, int64_t run) { return parts + (2 * run + (runs.start(run) >= w.lo ? 0 : 1)) * partial; };
-  if constexpr (kWide) {
-    const int h = blockIdx.x % a.q_heads, hk = h / a.group;
-    const int32_t x = i * a.group + h % a.group, in = x % rows;
-    const Row w = row_of(x / rows, hk);
-    if (w.tiles == 0) {
-      for (int e = tid; e < D; e += kCombineThreads) row_out(h)[e] = kv::from_float<T>(0.f);
+  if (blockIdx.x < few_ctas) {
+    const int slice = blockIdx.x % slices, h = blockIdx.x / slices % a.cache.kv_heads;
+    const int64_t r = blockIdx.x / slices / a.cache.kv_heads;
+    const Request q = request_of(a, r, C::kTile);
+    const int32_t x0 = slice * kRows;
+    if (q.rows > a.few_rows || x0 >= q.rows) return;
+    const int n = min(kRows, q.rows - x0);
+    if (q.tiles == 0) {
+      for (int e = tid; e < n * D; e += kCombineThreads) row_out(q, h, x0 + e / D)[e % D] = kv::from_float<T>(0.f);
       return;
     }
-    if (w.w0 == w.w1) return;
-    Sum s{-INFINITY, 0.f, {}};
-    for (int64_t run = w.w0 + warp; run <= w.w1; run += kWarps) {
-      const float* p = part_of(w, run);
-      float o[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = p[(int64_t)in * D + lane * kPer + e];
-      join(s, p[rows * D + in], p[rows * D + rows + in], o);
+    const Runs runs(a.base[a.requests], (int64_t)kSms * C::kWarps, kLeastRun);
+    const int64_t lo = a.base[r] + ((int64_t)h * row_tiles(q) + slice) * q.tiles;
+    const int64_t w0 = runs.of(lo), w1 = runs.of(lo + q.tiles - 1);
+    if (w0 == w1) return;
+    // a power of two of rows, the remaining factor of the warps on the parts of each
+    const int wide = n > 4 ? 8 : (n > 2 ? 4 : n), shares = kWarps / wide, in = warp % wide, share = warp / wide;
+    Sum<kPer> s;
+    if (in < n) {
+#pragma unroll 4
+      for (int64_t w = w0 + share; w <= w1; w += shares) {
+        const float* p = a.partials + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * kPartial<D>;
+        float o[kPer];
+        load_part<kPer>(o, p + in * D + lane * kPer);
+        s.join(p[kRows * D + in], p[kRows * D + kRows + in], o);
+      }
     }
     if (lane == 0) s_ref[warp] = s.ref, s_weight[warp] = s.weight;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = s.acc[e];
     __syncthreads();
-    float top = -INFINITY;
+    if (share > 0 || in >= n) return;
+    for (int v = 1; v < shares; ++v) {
+      float o[kPer];
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_ref[v]);
-    for (int e = tid; e < D; e += kCombineThreads) {
-      float sum = 0.f, l = 0.f;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        const float f = s_ref[v] == -INFINITY ? 0.f : exp2_approx(s_ref[v] - top);
-        sum += s_sum[v][e] * f;
-        l += s_ref[v] == -INFINITY ? s_weight[v] : s_weight[v] * f;
-      }
-      row_out(h)[e] = kv::from_float<T>(l == 0.f ? 0.f : sum * (unit / l));
+      for (int e = 0; e < kPer; ++e) o[e] = s_sum[in + v * wide][lane * kPer + e];
+      s.join(s_ref[in + v * wide], s_weight[in + v * wide], o);
     }
-  } else {
-    constexpr int kAtOnce = 4;  // heads whose parts are loaded together
-    for (int hk = warp; hk < a.cache.kv_heads; hk += kWarps) {
-      int32_t known = -1;
-      Row w{};
-      for (int g0 = 0; g0 < a.group;) {
-        const int32_t x = i * a.group + g0, tile = x / rows, in = x - tile * rows;
-        const int n = min(min(kAtOnce, a.group - g0), rows - in);  // of one row tile
-        if (tile != known) w = row_of(known = tile, hk);
-        if (w.tiles == 0) {
-          for (int g = 0; g < n; ++g)
-            for (int e = lane; e < D; e += 32) row_out(hk * a.group + g0 + g)[e] = kv::from_float<T>(0.f);
-        } else if (w.w0 != w.w1) {
-          Sum s[kAtOnce];
+    store_row<T, kPer>(row_out(q, h, x0 + in) + lane * kPer, s.acc, s.weight == 0.f ? 0.f : kOut<T, D> / s.weight);
+    return;
+  }
+  const int64_t at = blockIdx.x - few_ctas;
+  if (at < (int64_t)kJoinSlices<D> * (kSms - 1)) {
+    const int64_t b = at / kJoinSlices<D> + 1;
+    const Runs runs(*a.prompt_total, kSms, P::kLeastRun);
+    if (b >= runs.count) return;
+    const RunStart start = a.prompt_starts[b];
+    // a row block starts with the run, or an earlier boundary fell in it too
+    if (start.tile == 0 || start.lo < runs.start(b - 1)) return;
+    const Request q = request_of(a, start.r, P::kKeys);
+    const int32_t first = (int32_t)(at % kJoinSlices<D>) * kJoinRows;
+    const int32_t rows = min(P::kRows, q.rows - start.k * P::kRows);
+    const int64_t w1 = runs.of(start.lo + start.tiles - 1);
 #pragma unroll
-          for (int g = 0; g < kAtOnce; ++g) {
-            s[g].ref = -INFINITY, s[g].weight = 0.f;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) s[g].acc[e] = 0.f;
-          }
-          for (int64_t run = w.w0; run <= w.w1; ++run) {
-            const float* p = part_of(w, run);
-            float o[kAtOnce][kPer], m[kAtOnce], l[kAtOnce];
-#pragma unroll
-            for (int g = 0; g < kAtOnce; ++g) {
-              const int at = min(in + g, in + n - 1);
-              m[g] = p[rows * D + at], l[g] = p[rows * D + rows + at];
-#pragma unroll
-              for (int e = 0; e < kPer; ++e) o[g][e] = p[(int64_t)at * D + lane * kPer + e];
-            }
-#pragma unroll
-            for (int g = 0; g < kAtOnce; ++g) join(s[g], m[g], l[g], o[g]);
-          }
-#pragma unroll
-          for (int g = 0; g < kAtOnce; ++g) {
-            if (g >= n) break;
-            const float f = s[g].weight == 0.f ? 0.f : unit / s[g].weight;
-            T* dst = row_out(hk * a.group + g0 + g);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) dst[lane * kPer + e] = kv::from_float<T>(s[g].acc[e] * f);
-          }
-        }
-        g0 += n;
+    for (int i = 0; i < kJoinRows / kWarps; ++i) {
+      const int32_t in = first + i * kWarps + warp;
+      if (in >= rows) break;
+      Sum<kPer> s;
+#pragma unroll 2
+      for (int64_t w = b - 1; w <= w1; ++w) {
+        const float* p = a.prompt_partials + (2 * w + (runs.start(w) >= start.lo ? 0 : 1)) * P::kPartial;
+        float o[kPer];
+        load_part<kPer>(o, p + (int64_t)in * D + lane * kPer);
+        s.join(p[P::kRows * D + in], p[P::kRows * D + P::kRows + in], o);
+      }
+      store_row<T, kPer>(row_out(q, start.h, start.k * P::kRows + in) + lane * kPer, s.acc,
+                         s.weight == 0.f ? 0.f : 1.f / s.weight);
+    }
+    return;
+  }
+  for (int64_t r = at - (int64_t)kJoinSlices<D> * (kSms - 1); r < a.requests; r += kZeroCtas) {
+    const Request q = request_of(a, r, P::kKeys);
+    if (q.rows <= a.few_rows) continue;
+    // (only where the request brings more tokens than it holds, or its length was cut)
+    if (q.pos0 >= 0 && q.len == q.pos0 + q.n) continue;
+    for (int32_t k = 0; k * P::kRows < q.rows; ++k) {
+      const RowBlock blk = row_block<D>(a, q, k);
+      if (blk.tiles) continue;
+      for (int64_t e = tid; e < (int64_t)blk.rows * a.q_heads / a.group * D; e += kCombineThreads) {
+        const int32_t row = (int32_t)(e / D) % blk.rows;
+        row_out(q, (int)(e / D / blk.rows), k * P::kRows + row)[e % D] = kv::from_float<T>(0.f);
       }
     }
   }
@@ -822,10 +821,13 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   if (a.few_rows != 0x7fffffff) {
     if (cudaError_t e = launch_prompt(sizeof(T) == 4 ? -1 : (std::is_same_v<T, __half> ? KQ_F16 : KQ_BF16), D, a, st)) return e;
   }
-  // few rows: each may be in many parts
-  if (a.tokens * a.q_heads <= kWideRows)
-    return launch_dependent(combine_kernel<T, D, true>, dim3((unsigned)(a.tokens * a.q_heads)), dim3(kCombineThreads), 0, st, a);
-  return launch_dependent(combine_kernel<T, D, false>, dim3((unsigned)a.tokens), dim3(kCombineThreads), 0, st, a);
+  const bool prompts = a.few_rows != 0x7fffffff;
+  const int64_t rows = std::min<int64_t>(prompts ? a.few_rows : 0x7fffffff, std::min(a.max_new, a.tokens) * a.group);
+  const int slices = (int)((rows + kRows - 1) / kRows);
+  const int64_t few_ctas = a.requests * a.cache.kv_heads * slices;
+  const int64_t join_ctas = prompts ? (int64_t)kJoinSlices<D> * (kSms - 1) + kZeroCtas : 0;
+  return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(few_ctas + join_ctas)), dim3(kCombineThreads), 0, st, a, slices,
+                          few_ctas);
 }
 
 template <typename T>
@@ -838,14 +840,12 @@ constexpr int32_t kFewRows = 32;
 
 // The workspace: byte offsets of its parts, and its size.
 struct Workspace {
-  size_t base, partials, prompt_first, prompt_base, prompt_partials, bytes;
-  int64_t prompt_cap;
+  size_t base, partials, prompt_total, prompt_starts, prompt_partials, bytes;
 };
 static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t requests, int64_t tokens, int64_t max_new) {
   const int d = c->head_dim;
   const int64_t group = q_heads / c->kv_heads;
   const bool prompts = std::min(max_new, tokens) > kFewRows / group;
-  const int64_t rows = d == 256 ? PromptShape<256>::kRows : PromptShape<128>::kRows;
   const int64_t partial = d == 256 ? PromptShape<256>::kPartial : (d == 128 ? PromptShape<128>::kPartial : PromptShape<64>::kPartial);
   Workspace w{};
   size_t at = 0;
@@ -856,9 +856,8 @@ static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t reques
   };
   w.base = take((requests + 1) * 8);
   w.partials = take(2 * kSms * kMaxWarps * partial_floats(d) * 4);
-  w.prompt_first = take(prompts ? requests * 8 : 0);
-  w.prompt_cap = prompts ? tokens * group / rows + requests : 0;
-  w.prompt_base = take(prompts ? (w.prompt_cap + 1) * 8 : 0) + (prompts ? 8 : 0);
+  w.prompt_total = take(prompts ? 8 : 0);
+  w.prompt_starts = take(prompts ? kSms * (int64_t)sizeof(RunStart) : 0);
   w.prompt_partials = take(prompts ? 2 * kSms * partial * 4 : 0);
   w.bytes = at;
   return w;
@@ -932,9 +931,8 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
   a.base = reinterpret_cast<int64_t*>(ws + w.base);
   a.partials = reinterpret_cast<float*>(ws + w.partials);
-  a.prompt_first = reinterpret_cast<int64_t*>(ws + w.prompt_first);
-  a.prompt_base = reinterpret_cast<int64_t*>(ws + w.prompt_base);
-  a.prompt_cap = w.prompt_cap;
+  a.prompt_total = reinterpret_cast<int64_t*>(ws + w.prompt_total);
+  a.prompt_starts = reinterpret_cast<attn::RunStart*>(ws + w.prompt_starts);
   a.prompt_partials = reinterpret_cast<float*>(ws + w.prompt_partials);
   const bool prompts = dtype != KQ_F32 && std::min(max_new, tokens) > attn::kFewRows / a.group;
   a.few_rows = prompts ? attn::kFewRows : 0x7fffffff;

@@ -19,6 +19,13 @@ using kv::Layout;
 
 constexpr int kSms = 152;
 
+// Where a run of the prompt kernel begins: in key tile `tile` of the `tiles` that row block k of request r has for key
+// head h; the first of them is work unit `lo`.
+struct RunStart {
+  int64_t r, lo;
+  int32_t k, h, tile, tiles;
+};
+
 struct Args {
   Cache cache;
   const void* q;
@@ -34,9 +41,8 @@ struct Args {
   // workspace
   int64_t* base;             // first work unit of each request, and the total
   float* partials;           // two slots per run of kRows x D sums, kRows references, kRows weights
-  int64_t* prompt_first;     // first row block of each request
-  int64_t* prompt_base;      // first work unit of each row block; the total at [-1]
-  int64_t prompt_cap;        // row blocks that prompt_base has room for
+  int64_t* prompt_total;     // work units of the prompt kernel
+  RunStart* prompt_starts;   // of each of its runs
   float* prompt_partials;
 };
 

@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
   int64_t unit = 0, end = 0;  // this CTA's run
   {
     int64_t total = 0;
-    const bool writer = blockIdx.x == 0;
     for (int pass = 0; pass < 2; ++pass) {
       // the thread's last row block, whose place starts the run if the run starts in it
       Place p{};
@@ -359,6 +358,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           const int64_t in = unit - first_unit;
           p.h = (int32_t)(in / tiles), p.tile = (int32_t)(in % tiles);
           s_place = p;
+          a.prompt_starts[blockIdx.x] = RunStart{p.r, unit - p.tile, p.k, p.h, p.tile, tiles};
         }
       };
       int64_t units = 0, entries = 0;
@@ -371,14 +371,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         int64_t before, all;
         block_sum(blocks, before, all);
         s_entry[tid] = before;
-        if (writer && pass == 0 && r0 + tid < a.requests) a.prompt_first[r0 + tid] = entries + before;
         __syncthreads();
         const int in_chunk = (int)min((int64_t)kPromptThreads, a.requests - r0);
         for (int64_t e0 = 0; e0 < all; e0 += kPromptThreads) {
           const int64_t e = e0 + tid;
           int64_t at, sum;
           u = 0;
-          if (e < all && entries + e < a.prompt_cap) {
+          if (e < all) {
             int l = 0, h = in_chunk;
             while (h - l > 1) {  // the last request whose first row block is not after e
               const int m = (l + h) >> 1;
@@ -389,7 +388,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
             u = (int64_t)tiles * a.cache.kv_heads;
           }
           block_sum(u, at, sum);
-          if (writer && pass == 0 && e < all && entries + e < a.prompt_cap) a.prompt_base[entries + e] = units + at;
           first_unit = units + at;
           if (pass == 1) found();
           units += sum;
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       }
       if (pass == 0) {
         total = units;
-        if (writer && tid == 0) a.prompt_base[-1] = total;
+        if (blockIdx.x == 0 && tid == 0) *a.prompt_total = total;
         const Runs runs(total, kSms, C::kLeastRun);
         if (blockIdx.x < runs.count) unit = runs.start(blockIdx.x), end = runs.start(blockIdx.x + 1);
         if (unit == end) break;  // the same for the whole CTA
