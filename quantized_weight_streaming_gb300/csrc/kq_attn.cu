@@ -555,32 +555,30 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
     if (tid == 0) a.base[a.requests] = total;
     if (out_of_range) attn_flag(KQ_ERR_RANGE);
   }
-  if (cur.unit == cur.end) return;
-  enter_row<C::kTile>(a, cur);
+  if (!producer && cur.unit == cur.end) return;
+  if (cur.unit < cur.end) enter_row<C::kTile>(a, cur);
 
   if (producer) {
-    if (lane >= C::kWarps) return;
     const uint64_t policy = l2_policy_evict_first();
     const int per_page = a.cache.page_size / kGranule;
     const int32_t* row = nullptr;
     int64_t row_of = -1;
     int32_t at = -1, id = -1, next = -1;  // page `at` of the request, and the page after it in flight
     uint32_t made = 0;
+    // The lanes stay together: whichever find a free stage issue a tile, and only where none does the warp sleeps.  (With
+    // a wait per lane the slowest consumer held up all the others' copies.)
+    bool more = lane < C::kWarps && seek<C::kTile>(a, cur);
     long long since = clock64();
-    while (seek<C::kTile>(a, cur)) {
+    while (__any_sync(~0u, more)) {
       const int st = made % C::kStages;
-      if (made >= C::kStages) {
-        bool free = true;
-        while (!mbar_test_wait(&empty[st], (made / C::kStages - 1) & 1)) {
-          if (clock64() - since > kWaitLimitCycles) {
-            free = false;
-            break;
-          }
-          __nanosleep(64);
-        }
-        if (!free) break;  // the consumer reports it
-        since = clock64();
+      const bool free = more && (made < C::kStages || mbar_test_wait(&empty[st], (made / C::kStages - 1) & 1));
+      if (!__any_sync(~0u, free)) {
+        if (clock64() - since > kWaitLimitCycles) break;  // a consumer gave up, and reports it
+        __nanosleep(40);
+        continue;
       }
+      since = clock64();
+      if (!free) continue;
       if (cur.r != row_of) row_of = cur.r, row = a.table + cur.r * a.table_stride, at = -1;
       const int32_t pages = (cur.q.len + a.cache.page_size - 1) / a.cache.page_size;  // the table's row holds them
       const int32_t g0 = (cur.q.tile0 + cur.tile) * C::kTileGranules;
@@ -620,10 +618,12 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       ++made;
       ++cur.tile;
       ++cur.unit;
+      more = seek<C::kTile>(a, cur);
     }
     // the ring stays until the last copies have landed (they have, unless a consumer gave up)
-    for (uint32_t i = made > C::kStages ? made - C::kStages : 0; i < made; ++i)
-      mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1);
+    if (lane < C::kWarps)
+      for (uint32_t i = made > C::kStages ? made - C::kStages : 0; i < made; ++i)
+        mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1);
     return;
   }
 
@@ -706,14 +706,14 @@ __device__ __forceinline__ void store_row(T* p, const float (&o)[N], float f) {
 
 // Joins, in run order, the parts of rows that were cut between runs, and writes
 // zeros where a row sees nothing.
-//  - The first few_ctas CTAs: eight query rows of one request and key head each
-//    (a row tile of attend_kernel; its rows were cut at the same places).  The
-//    warps share out rows, and then the parts of a row.
+//  - The first few_ctas CTAs: rows_per_cta query rows of one row tile of
+//    attend_kernel each (eight rows of a request and key head, cut at the same
+//    places).  The warps share out rows, and then the parts of a row.
 //  - The others: 16 rows of the row block that a boundary between two runs of
 //    the prompt kernel falls in.
 //  - The last kZeroCtas of them: prompts' row blocks that see nothing.
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int slices, int64_t few_ctas) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int slices, int tile_rows, int rows_per_cta, int64_t few_ctas) {
   using C = Config<T, D>;
   using P = PromptShape<D>;
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
@@ -726,12 +726,15 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
            (int64_t)(h * a.group + x % a.group) * a.out_head;
   };
   if (blockIdx.x < few_ctas) {
-    const int slice = blockIdx.x % slices, h = blockIdx.x / slices % a.cache.kv_heads;
-    const int64_t r = blockIdx.x / slices / a.cache.kv_heads;
+    const int per_tile = (tile_rows + rows_per_cta - 1) / rows_per_cta, part = blockIdx.x % per_tile;
+    const int64_t tile = blockIdx.x / per_tile;
+    const int slice = (int)(tile % slices), h = (int)(tile / slices % a.cache.kv_heads);
+    const int64_t r = tile / slices / a.cache.kv_heads;
     const Request q = request_of(a, r, C::kTile);
-    const int32_t x0 = slice * kRows;
+    const int first = part * rows_per_cta;
+    const int32_t x0 = slice * kRows + first;
     if (q.rows > a.few_rows || x0 >= q.rows) return;
-    const int n = min(kRows, q.rows - x0);
+    const int n = min(rows_per_cta, q.rows - x0);
     if (q.tiles == 0) {
       for (int e = tid; e < n * D; e += kCombineThreads) row_out(q, h, x0 + e / D)[e % D] = kv::from_float<T>(0.f);
       return;
@@ -748,8 +751,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
       for (int64_t w = w0 + share; w <= w1; w += shares) {
         const float* p = a.partials + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * kPartial<D>;
         float o[kPer];
-        load_part<kPer>(o, p + in * D + lane * kPer);
-        s.join(p[kRows * D + in], p[kRows * D + kRows + in], o);
+        load_part<kPer>(o, p + (first + in) * D + lane * kPer);
+        s.join(p[kRows * D + first + in], p[kRows * D + kRows + first + in], o);
       }
     }
     if (lane == 0) s_ref[warp] = s.ref, s_weight[warp] = s.weight;
@@ -824,10 +827,14 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   const bool prompts = a.few_rows != 0x7fffffff;
   const int64_t rows = std::min<int64_t>(prompts ? a.few_rows : 0x7fffffff, std::min(a.max_new, a.tokens) * a.group);
   const int slices = (int)((rows + kRows - 1) / kRows);
-  const int64_t few_ctas = a.requests * a.cache.kv_heads * slices;
+  // a row a CTA while the GPU holds them at once (one long request's rows lie in a hundred parts), else more
+  const int64_t tiles = a.requests * a.cache.kv_heads * slices;
+  const int tile_rows = (int)std::min<int64_t>(rows, kRows);
+  const int rows_per_cta = tiles <= 64 ? 1 : kRows;
+  const int64_t few_ctas = tiles * ((tile_rows + rows_per_cta - 1) / rows_per_cta);
   const int64_t join_ctas = prompts ? (int64_t)kJoinSlices<D> * (kSms - 1) + kZeroCtas : 0;
   return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(few_ctas + join_ctas)), dim3(kCombineThreads), 0, st, a, slices,
-                          few_ctas);
+                          tile_rows, rows_per_cta, few_ctas);
 }
 
 template <typename T>
