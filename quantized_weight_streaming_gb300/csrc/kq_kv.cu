@@ -174,185 +174,417 @@ __device__ __forceinline__ int round_ratio(float a, float d, float inv) {
 
 // The four lanes of a 32-dimension group hold 8 values each: the group's scale
 // (SCALE4: the first value of largest magnitude over -8, rounded to fp16) and
-// this lane's eight codes, nibble j the j-th value.
+// this lane's eight codes, nibble j the j-th value.  The whole warp takes part.
+//
+// The codes come from the product with 1/d, rounded by adding 1.5 2^23 (+ 8:
+// the low bits are then the code).  x - n d, exact but for its own rounding,
+// shows whether n is beyond doubt, |x - n d| < |d| / 2; where it is not for
+// some value of the warp (a tie, or a quotient that its rounding moved), all
+// are decided by comparisons.  (Comparisons for every value made a prompt's
+// cache write bound by instructions: 230 a lane against 90.)
 __device__ __forceinline__ uint32_t quantize_group(const float (&x)[8], __half& scale) {
-  float m = x[0];
-  bool bad = !(fabsf(x[0]) <= 3.402823466e38f);
+  float hi = x[0], lo = x[0];
+  float2 none = make_float2(0.f, 0.f);  // 0 x: not 0 where x is not finite
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    bad |= !(fabsf(x[i]) <= 3.402823466e38f);
-    if (fabsf(x[i]) > fabsf(m)) m = x[i];
+  for (int i = 0; i < 8; i += 2) {
+    hi = fmaxf(hi, fmaxf(x[i], x[i + 1]));
+    lo = fminf(lo, fminf(x[i], x[i + 1]));
+    none = fma2(make_float2(x[i], x[i + 1]), make_float2(0.f, 0.f), none);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    const float y = __shfl_xor_sync(~0u, m, o);
-    const bool mine_first = (threadIdx.x & o) == 0;
-    if (mine_first ? fabsf(y) > fabsf(m) : fabsf(y) >= fabsf(m)) m = y;
+    hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
   }
-  bad = __shfl_xor_sync(~0u, (int)bad, 1) | (int)bad;
-  bad = __shfl_xor_sync(~0u, (int)bad, 2) | (int)bad;
+  const uint32_t strange = __ballot_sync(~0u, !(none.x + none.y == 0.f));
+  const bool bad = strange >> (threadIdx.x & 28) & 15u;
+  float m = hi > -lo ? hi : lo;
+  const bool tie = hi == -lo && hi > 0.f;
+  if (__any_sync(~0u, tie)) {  // both signs: the first one's counts
+    int at = 64;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+      if (fabsf(x[i]) == hi) at = (threadIdx.x & 3) * 8 + i, v = x[i];
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const int b = __shfl_xor_sync(~0u, at, o);
+      const float w = __shfl_xor_sync(~0u, v, o);
+      if (b < at) at = b, v = w;
+    }
+    if (tie) m = v;
+  }
   scale = __float2half_rn(m * -0.125f);
   if (bad) scale = __ushort_as_half((unsigned short)0x7FFF);
   const float d = __half2float(scale), mag = fabsf(d);
-  uint32_t w = 0x88888888u;
-  if (mag > 0.f && mag <= 65504.f) {
-    const float inv = 1.f / mag;
+  const bool plain = mag > 0.f && mag <= 65504.f;
+  const float inv = plain ? __fdividef(1.f, d) : 0.f, half = plain ? 0.5f * mag : 1.f, by = plain ? -d : 0.f;
+  constexpr float kMagic = 12582912.f + 8.f;
+  uint32_t w = 0;
+  bool doubt = mag < 6.104e-5f;  // a subnormal scale may leave quotients beyond -8
+#pragma unroll
+  for (int i = 6; i >= 0; i -= 2) {
+    const float2 v = plain ? make_float2(x[i], x[i + 1]) : make_float2(0.f, 0.f);
+    const float2 t = fma2(v, make_float2(inv, inv), make_float2(kMagic, kMagic));
+    const float2 e = fma2(add2(t, make_float2(-kMagic, -kMagic)), make_float2(by, by), v);
+    doubt |= !(fabsf(e.x) < half) || !(fabsf(e.y) < half);
+    const uint32_t q0 = min(__float_as_uint(t.x) & 31u, 15u), q1 = min(__float_as_uint(t.y) & 31u, 15u);
+    w = w << 8 | q1 << 4 | q0;
+  }
+  if (__any_sync(~0u, doubt) && plain) {
+    const float up = fabsf(inv);
     w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int n = round_ratio(fabsf(x[i]), mag, inv);
+      const int n = round_ratio(fabsf(x[i]), mag, up);
       const int q = (x[i] < 0.f) != (d < 0.f) ? 8 - n : 8 + n;
       w |= (uint32_t)min(max(q, 0), 15) << (4 * i);
     }
-  } else if (mag != 0.f) {
-    kv_flag(bad ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
   }
+  if (!plain && mag != 0.f) kv_flag(bad ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
   return w;
 }
 
-// Bound by the bytes of its rows.  A head row is spread over D / 8 lanes, 8
-// dimensions a lane (16 or 32 bytes), so its sum of squares is a few shuffles
-// and its other half for the rotation one shuffle a value.  A row group takes
-// kHeads heads of one token (kinds do not mix), loading all their rows before
-// the first is reduced, and keeps the token's cosines and sines in registers.
+// A head row is spread over D / 8 lanes ("row group"), eight dimensions a lane.
 constexpr int kQkThreads = 256;
+enum Mode { kNorm, kAppendEach, kAppendGranules };
 
-template <typename T, int D, int kHeads, bool kAppend>
-__global__ void __launch_bounds__(kQkThreads) qk_kernel(QkArgs a) {
+// The whole warp takes part; lanes without a row pass zeros.
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o, kLanes);
+  return v;
+}
+__device__ __forceinline__ void set2(float* p, float2 v) { p[0] = v.x, p[1] = v.y; }
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float u = a;
+  a = fmaf(u, c, -b * s);
+  b = fmaf(b, c, u * s);
+}
+// Whether the token's position lies in the table; `entry` is its row.
+__device__ __forceinline__ bool rope_row(const QkArgs& a, int64_t t, bool report, const float*& entry) {
+  const int32_t pos = a.positions[t];
+  if (pos < 0 || pos >= a.rope_positions) {
+    if (report) kv_flag(KQ_ERR_RANGE);
+    return false;
+  }
+  entry = a.rope + (int64_t)pos * a.rope_dim;
+  return true;
+}
+
+// Query rows (and key rows that are not quantized): kHeads heads of one token a
+// row group, all loaded before the first is reduced and held as they came: bound
+// by the bytes of the rows, so what counts is how many are on their way (four
+// heads, held in fp32 by 24 warps an SM, moved 3.4 TB/s).  A lane holds four dimensions and their four partners in the rotation
+// (what is not rotated: eight in a row), so that rotating takes no shuffles and
+// half the table loads: with eight dimensions in a row and shuffles 4099 tokens
+// of 28 heads of 256 took 35 us.
+template <typename T, int D, int kHeads>
+__device__ __forceinline__ void norm_rows(const QkArgs& a, const View& in, const View& out, const float* weight, int heads,
+                                          int64_t t0, int h0) {
+  constexpr int kLanes = D / 8;
+  const int row = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+  const int64_t t = t0 + row;
+  const bool live = t < a.tokens;
+  const int turning = a.rope_dim / 8, n = live ? min(kHeads, heads - h0) : 0;
+  const bool turns = l < turning, split = turns && !a.interleaved;
+  const int ea = split ? 4 * l : 8 * l, eb = split ? a.rope_dim / 2 + 4 * l : 8 * l + 4;
+  const T* src = static_cast<const T*>(in.data) + t * in.token + h0 * in.head;
+  Raw<T, 4> xa[kHeads], xb[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    xa[i].clear(), xb[i].clear();
+    if (i < n) xa[i].load(src + i * in.head + ea), xb[i].load(src + i * in.head + eb);
+  }
+  float w[8], c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = 1.f;
+  if (weight) load4(weight + ea, &w[0]), load4(weight + eb, &w[4]);
+  bool held = true;
+  if (a.rope_dim && live) {
+    const float* entry = nullptr;
+    held = rope_row(a, t, l == 0, entry);
+    if (held && turns) load4(entry + 4 * l, c), load4(entry + a.rope_dim / 2 + 4 * l, s);
+  }
+  // the rows' sums side by side: their shuffles overlap
+  float r[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    float v[8];
+    xa[i].get(v), xb[i].get(v + 4);
+    float2 ss = mul2(make_float2(v[0], v[1]), make_float2(v[0], v[1]));
+#pragma unroll
+    for (int j = 2; j < 8; j += 2) ss = fma2(make_float2(v[j], v[j + 1]), make_float2(v[j], v[j + 1]), ss);
+    r[i] = ss.x + ss.y;
+  }
+  if (a.norm) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) r[i] += __shfl_xor_sync(~0u, r[i], o, kLanes);
+    }
+  }
+  T* dst = static_cast<T*>(out.data) + t * out.token + h0 * out.head;
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (i >= n) break;
+    const float f = a.norm ? rsqrtf(r[i] * (1.f / D) + a.eps) : 1.f;
+    float v[8];
+    xa[i].get(v), xb[i].get(v + 4);
+    // weight, rotation, and the norm's factor last: it is common to a row
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) set2(v + j, mul2(make_float2(v[j], v[j + 1]), make_float2(w[j], w[j + 1])));
+    if (split) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 p = make_float2(v[j], v[j + 1]), q = make_float2(v[4 + j], v[5 + j]);
+        const float2 cc = make_float2(c[j], c[j + 1]), sn = make_float2(s[j], s[j + 1]);
+        set2(v + j, fma2(p, cc, mul2(make_float2(-q.x, -q.y), sn)));
+        set2(v + 4 + j, fma2(q, cc, mul2(p, sn)));
+      }
+    } else if (turns) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) turn(v[2 * j], v[2 * j + 1], c[j], s[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) set2(v + j, mul2(make_float2(v[j], v[j + 1]), make_float2(f, f)));
+    if (!held) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+    store4(dst + i * out.head + ea, v), store4(dst + i * out.head + eb, v + 4);
+  }
+}
+
+// Eight successive dimensions a lane of a key row (normed and rotated) or a value row (as it is) in fp32, for quantizing.
+template <typename T, int D>
+__device__ __forceinline__ Raw<T, 8> load_row(const QkArgs& a, bool key, int64_t t, int h, bool live) {
+  const View& in = key ? a.k : a.v;
+  Raw<T, 8> raw;
+  raw.clear();
+  if (live) raw.load(static_cast<const T*>(in.data) + t * in.token + h * in.head + 8 * (threadIdx.x % (D / 8)));
+  return raw;
+}
+// entry: the token's row of the rotation table; NULL: outside the table (or no rotation).
+template <typename T, int D>
+__device__ __forceinline__ void cache_row(const QkArgs& a, bool key, const float* entry, const Raw<T, 8>& raw, float (&x)[8]) {
+  constexpr int kLanes = D / 8;
+  const int l = threadIdx.x % kLanes, e0 = 8 * l, half_dim = a.rope_dim / 2;
+  raw.get(x);
+  if (!key) return;  // the same for the whole warp
+  float r = 1.f;
+  if (a.norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+    r = rsqrtf(row_sum<kLanes>(ss) * (1.f / D) + a.eps);
+  }
+  if (a.k_weight) {
+    float w[8];
+    load8(a.k_weight + e0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= w[j];
+  }
+  const bool held = entry || !a.rope_dim;
+  if (a.rope_dim) {
+    const bool turns = e0 < a.rope_dim, reads = entry && turns;
+    if (a.interleaved) {
+      if (reads) {
+        float c[4], s[4];
+        load4(entry + 4 * l, c), load4(entry + half_dim + 4 * l, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turn(x[2 * j], x[2 * j + 1], c[j], s[j]);
+      }
+    } else {
+      const bool low = e0 < half_dim;
+      const int i0 = low ? e0 : e0 - half_dim, partner = turns ? (low ? l + half_dim / 8 : l - half_dim / 8) : l;
+      float c[8], s[8];
+      if (reads) load8(entry + i0, c), load8(entry + half_dim + i0, s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float other = __shfl_sync(~0u, x[j], partner, kLanes);
+        if (reads) x[j] = low ? fmaf(x[j], c[j], -other * s[j]) : fmaf(x[j], c[j], other * s[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = held ? x[j] * r : 0.f;
+}
+
+// A lane's codes and (one lane of four) its group's scale, at `granule`.
+template <int D>
+__device__ __forceinline__ void put_row(uint8_t* granule, int token, bool key, uint32_t codes, __half scale) {
   using L = Layout<D>;
+  const int l = threadIdx.x % (D / 8);
+  if (key) {
+    *reinterpret_cast<uint32_t*>(granule + L::key_word(token, l)) = codes;
+  } else {
+    *reinterpret_cast<uint16_t*>(granule + L::value_unit(token, 2 * l)) = (uint16_t)codes;
+    *reinterpret_cast<uint16_t*>(granule + L::value_unit(token, 2 * l + 1)) = (uint16_t)(codes >> 16);
+  }
+  if (l % 4 == 0) *reinterpret_cast<__half*>(granule + L::key_scale(token, l / 4) + (key ? 0 : D)) = scale;
+}
+template <int D>
+__device__ __forceinline__ uint8_t* granule_of(const Cache& c, int32_t slot, int h) {
+  const int32_t page = slot / c.page_size, in_page = slot - page * c.page_size;
+  return c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes + (in_page / kGranule) * Layout<D>::kBytes;
+}
+__device__ __forceinline__ int32_t slot_of(const QkArgs& a, int64_t t) {
+  const int32_t slot = a.slots[t];
+  if (slot < a.cache.pages * a.cache.page_size) return slot;
+  kv_flag(KQ_ERR_RANGE);
+  return -1;
+}
+
+// Keys and values of a window of 32 (or 16) tokens of one head.  Where the tokens are
+// runs of successive slots (prompts), the rows are put together in shared memory
+// as the granules that they fill and go out word by word in memory order; a word
+// of two tokens' values of which one is not in the window, as half words.
+// Straight to the cache a token's values are 32 two-byte stores (8192 tokens of
+// 8 heads of 128, with their queries: 86 us).
+constexpr int kWindowGranules = 4;
+template <int D>
+constexpr int kWindow = D == 256 ? 16 : 32;
+
+template <typename T, int D>
+__device__ __forceinline__ void append_window(const QkArgs& a, int64_t t0, int h) {
+  using L = Layout<D>;
+  constexpr int kLanes = D / 8, kRows = kQkThreads / kLanes, W = kWindow<D>;
+  constexpr int kEach = W / kRows;  // key rows, and value rows, of a row group
+  __shared__ __align__(16) uint8_t image[kWindowGranules * L::kBytes];
+  __shared__ __align__(16) float s_table[W * D];
+  __shared__ int32_t s_slot[W], s_index[W], s_pos[W], s_first[kWindowGranules], s_count;
+  __shared__ uint32_t s_mask[kWindowGranules];
+  const int tid = threadIdx.x, row = tid / kLanes;
+  // all that the window reads is on its way before any of it is used
+  Raw<T, 8> keys[kEach], values[kEach];
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int64_t t = t0 + row + n * kRows;
+    keys[n] = load_row<T, D>(a, true, t, h, t < a.tokens);
+    values[n] = load_row<T, D>(a, false, t, h, t < a.tokens);
+  }
+  if (tid < kWindowGranules) s_mask[tid] = 0;
+  __syncthreads();
+  if (tid < 32) {
+    const bool in = tid < W && t0 + tid < a.tokens;
+    int32_t pos = in && a.rope_dim ? a.positions[t0 + tid] : -1;
+    const int32_t slot = in ? slot_of(a, t0 + tid) : -1;
+    if (pos >= a.rope_positions) pos = -1;
+    if (in && a.rope_dim && pos < 0) kv_flag(KQ_ERR_RANGE);
+    const int32_t granule = slot < 0 ? -1 : slot / kGranule;
+    const int32_t before = __shfl_up_sync(~0u, granule, 1);
+    const uint32_t starts = __ballot_sync(~0u, granule >= 0 && (tid == 0 || before != granule));
+    const int index = __popc(starts & (0xFFFFFFFFu >> (31 - tid))) - 1;
+    if (tid < W) s_slot[tid] = slot, s_index[tid] = index, s_pos[tid] = pos;
+    if (tid == 0) s_count = __popc(starts);
+    if (granule >= 0 && index < kWindowGranules) {
+      atomicOr(&s_mask[index], 1u << (slot % kGranule));
+      if (starts >> tid & 1u) s_first[index] = slot;
+    }
+  }
+  __syncthreads();
+  const int quarter = a.rope_dim / 4;  // of a table row, 16 bytes each
+  for (int i = tid; i < W * quarter; i += kQkThreads) {
+    const int in = i / quarter, at = i - in * quarter;
+    if (s_pos[in] >= 0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&s_table[in * a.rope_dim + 4 * at])),
+                   "l"(a.rope + (int64_t)s_pos[in] * a.rope_dim + 4 * at)
+                   : "memory");
+  }
+  const bool together = s_count <= kWindowGranules;
+  auto put = [&](int n, bool key, const float* entry, const Raw<T, 8>& raw) {
+    const int in = row + n * kRows;
+    const int32_t slot = s_slot[in];
+    float x[8];
+    cache_row<T, D>(a, key, entry, raw, x);
+    if (slot < 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;  // a skipped token's values ask nothing
+    }
+    __half scale;
+    const uint32_t codes = quantize_group(x, scale);
+    if (slot >= 0)
+      put_row<D>(together ? image + s_index[in] * L::kBytes : granule_of<D>(a.cache, slot, h), slot % kGranule, key, codes,
+                 scale);
+  };
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) put(n, false, nullptr, values[n]);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int in = row + n * kRows;
+    put(n, true, s_pos[in] >= 0 ? &s_table[in * a.rope_dim] : nullptr, keys[n]);
+  }
+  if (!together) return;
+  __syncthreads();
+  for (int g = 0; g < s_count; ++g) {
+    const uint32_t mask = s_mask[g];
+    const uint8_t* src = image + g * L::kBytes;
+    uint8_t* dst = granule_of<D>(a.cache, s_first[g], h);
+    if (mask == 0xFFFFu) {
+      for (int i = tid; i < L::kBytes / 16; i += kQkThreads)
+        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+      continue;
+    }
+    for (int i = tid; i < L::kBytes / 4; i += kQkThreads) {
+      const uint32_t word = reinterpret_cast<const uint32_t*>(src)[i];
+      const int byte = 4 * i;
+      uint32_t have;  // bit 0: the low half's token is there, bit 1: the high half's
+      if (byte < L::kValues) {
+        have = (mask >> (byte % L::kKeySlab / (L::kSlabDim / 2)) & 1u) * 3u;
+      } else if (byte < L::kKeyScales) {
+        const int in = (byte - L::kValues) % L::kKeySlab;
+        have = mask >> (in / L::kBlock * 8 + in % L::kBlock / (4 * L::kGroups) % 4 * 2) & 3u;
+      } else {
+        have = (mask >> ((byte - L::kKeyScales) % L::kScaleSlab / (2 * L::kGroups)) & 1u) * 3u;
+      }
+      if (have == 3u) {
+        reinterpret_cast<uint32_t*>(dst)[i] = word;
+      } else if (have) {
+        reinterpret_cast<uint16_t*>(dst)[2 * i + (have >> 1)] = (uint16_t)(have & 2u ? word >> 16 : word);
+      }
+    }
+  }
+}
+
+// CTAs [0, row_ctas): query rows (and, without a cache, key rows), kRows tokens
+// of one chunk of kHeads heads each.  The others: keys and values into the
+// cache, a row a row group or a window of tokens a CTA.
+template <typename T, int D, int kHeads, Mode kMode>
+__global__ void __launch_bounds__(kQkThreads) qk_kernel(QkArgs a, uint32_t row_ctas) {
   constexpr int kLanes = D / 8, kRows = kQkThreads / kLanes;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int row = threadIdx.x / kLanes, l = threadIdx.x % kLanes, e0 = 8 * l;
-  const int qc = (a.q_heads + kHeads - 1) / kHeads, kc = (a.kv_heads + kHeads - 1) / kHeads;
-  const int chunks = qc + kc + (kAppend ? kc : 0);
-  const int64_t item = (int64_t)blockIdx.x * kRows + row;
-  const bool live = item < a.tokens * chunks;  // whole warps stay for the shuffles
-  const int64_t t = live ? item / chunks : 0;
-  const int chunk = live ? (int)(item % chunks) : 0;
-  const int kind = chunk < qc ? 0 : (chunk < qc + kc ? 1 : 2);
-  const int h0 = (kind == 0 ? chunk : (kind == 1 ? chunk - qc : chunk - qc - kc)) * kHeads;
-  const int heads = live ? min(kHeads, (kind == 0 ? a.q_heads : a.kv_heads) - h0) : 0;
-  const View& in = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-  const T* src = static_cast<const T*>(in.data) + t * in.token + h0 * in.head + e0;
-  float x[kHeads][8];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (i < heads) {
-      load8(src + i * in.head, x[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-    }
+  const uint32_t along = (uint32_t)((a.tokens + kRows - 1) / kRows);
+  uint32_t b = blockIdx.x;
+  if (b < row_ctas) {
+    const int chunk = b / along, q_chunks = (a.q_heads + kHeads - 1) / kHeads;
+    const int64_t t0 = (int64_t)(b % along) * kRows;
+    if (kMode != kNorm || chunk < q_chunks)
+      norm_rows<T, D, kHeads>(a, a.q, a.q_out, a.q_weight, a.q_heads, t0, chunk * kHeads);
+    else
+      norm_rows<T, D, kHeads>(a, a.k, a.k_out, a.k_weight, a.kv_heads, t0, (chunk - q_chunks) * kHeads);
+    return;
   }
-  float w[8], cs[8], sn[8];
-  const int half_dim = a.rope_dim / 2;
-  const bool turns = e0 < a.rope_dim && kind < 2;
-  bool zero = false;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 1.f, cs[j] = 1.f, sn[j] = 0.f;
-  if (live && kind < 2) {
-    const float* wt = kind == 0 ? a.q_weight : a.k_weight;
-    if (wt) load8(wt + e0, w);
-    if (a.rope_dim) {
-      const int32_t pos = a.positions[t];
-      zero = pos < 0 || pos >= a.rope_positions;
-      if (zero) {
-        if (l == 0) kv_flag(KQ_ERR_RANGE);
-      } else if (turns) {
-        const float* tab = a.rope + (int64_t)pos * a.rope_dim;
-        if (a.interleaved) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            cs[2 * j] = cs[2 * j + 1] = tab[e0 / 2 + j];
-            const float s = tab[half_dim + e0 / 2 + j];
-            sn[2 * j] = -s, sn[2 * j + 1] = s;
-          }
-        } else {
-          const int i0 = e0 < half_dim ? e0 : e0 - half_dim;
-          load8(tab + i0, cs);
-          load8(tab + half_dim + i0, sn);
-          if (e0 < half_dim) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
-          }
-        }
-      }
-    }
-  }
-  const int partner = e0 < half_dim ? l + half_dim / 8 : l - half_dim / 8;
-  const View& outv = kind == 0 ? a.q_out : a.k_out;
-  int32_t slot = -1;
-  if (kAppend && live && kind > 0) {
-    slot = a.slots[t];
-    if (slot >= a.cache.pages * a.cache.page_size) {
-      if (l == 0) kv_flag(KQ_ERR_RANGE);
-      slot = -1;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (a.norm) {  // value rows share the warp's shuffles and stay as they are
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o, kLanes);
-      if (kind < 2) {
-        const float r = __frsqrt_rn(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = x[i][j] * r * w[j];
-      }
-    }
-    if (a.rope_dim) {
-      if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float u = x[i][j], v = x[i][j + 1];
-          if (turns) {
-            x[i][j] = fmaf(u, cs[j], v * sn[j]);
-            x[i][j + 1] = fmaf(v, cs[j + 1], u * sn[j + 1]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float other = __shfl_sync(~0u, x[i][j], turns ? partner : l, kLanes);
-          if (turns) x[i][j] = fmaf(x[i][j], cs[j], other * sn[j]);
-        }
-      }
-      if (zero) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-      }
-    }
-    if (kind == 0 || !kAppend) {
-      if (i < heads) store8(static_cast<T*>(outv.data) + t * outv.token + (h0 + i) * outv.head + e0, x[i]);
-    }
-    if constexpr (kAppend) {
-      __half scale;
-      const bool writes = kind > 0 && i < heads && slot >= 0;
-      if (!__any_sync(~0u, writes)) continue;
-      if (!writes) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = 0.f;  // no flag from rows that are not written
-      }
-      const uint32_t codes = quantize_group(x[i], scale);
-      if (writes) {
-        const int page = slot / a.cache.page_size, in_page = slot - page * a.cache.page_size;
-        uint8_t* g = a.cache.data + ((int64_t)page * a.cache.kv_heads + h0 + i) * a.cache.block_bytes +
-                     (in_page / kGranule) * L::kBytes;
-        const int tok = in_page % kGranule;
-        if (kind == 1) {
-          *reinterpret_cast<uint32_t*>(g + L::key_word(tok, l)) = codes;
-          if (l % 4 == 0) *reinterpret_cast<__half*>(g + L::key_scale(tok, l / 4)) = scale;
-        } else {
-          *reinterpret_cast<uint16_t*>(g + L::value_unit(tok, 2 * l)) = (uint16_t)codes;
-          *reinterpret_cast<uint16_t*>(g + L::value_unit(tok, 2 * l + 1)) = (uint16_t)(codes >> 16);
-          if (l % 4 == 0) *reinterpret_cast<__half*>(g + L::key_scale(tok, l / 4) + D) = scale;
-        }
-      }
-    }
+  b -= row_ctas;
+  if constexpr (kMode == kAppendEach) {
+    const int y = b / along, h = y % a.kv_heads;
+    const bool key = y < a.kv_heads;
+    const int64_t t = (int64_t)(b % along) * kRows + threadIdx.x / kLanes;
+    const int32_t slot = t < a.tokens ? slot_of(a, t) : -1;
+    const float* entry = nullptr;
+    if (key && slot >= 0 && a.rope_dim) rope_row(a, t, threadIdx.x % kLanes == 0, entry);
+    float x[8];
+    cache_row<T, D>(a, key, entry, load_row<T, D>(a, key, t, h, slot >= 0), x);
+    __half scale;
+    const uint32_t codes = quantize_group(x, scale);
+    if (slot >= 0) put_row<D>(granule_of<D>(a.cache, slot, h), slot % kGranule, key, codes, scale);
+  } else if constexpr (kMode == kAppendGranules) {
+    const uint32_t windows = (uint32_t)((a.tokens + kWindow<D> - 1) / kWindow<D>);
+    append_window<T, D>(a, (int64_t)(b % windows) * kWindow<D>, b / windows);
   }
 }
 
@@ -396,13 +628,27 @@ __global__ void __launch_bounds__(kQkThreads) read_kernel(Cache c, const int32_t
 template <typename T, int D, bool kAppend>
 static cudaError_t launch_qk(const QkArgs& a, cudaStream_t st) {
   constexpr int kRows = kQkThreads / (D / 8);
-  // Four heads a row group once that still fills the GPU, one below: a decode step is a few hundred rows.
-  const int64_t rows = a.tokens * (a.q_heads + (kAppend ? 2 : 1) * (int64_t)a.kv_heads);
-  const int heads = rows >= 4 * 152 * 2 * kRows ? 4 : 1;
-  const int64_t chunks = (a.q_heads + heads - 1) / heads + (kAppend ? 2 : 1) * ((a.kv_heads + heads - 1) / heads);
-  const int64_t grid = (a.tokens * chunks + kRows - 1) / kRows;
-  auto k = heads == 4 ? qk_kernel<T, D, 4, kAppend> : qk_kernel<T, D, 1, kAppend>;
-  return launch_dependent(k, dim3((unsigned)grid), dim3(kQkThreads), 0, st, a);
+  const int64_t along = (a.tokens + kRows - 1) / kRows;
+  // Several heads a row group (32 registers of rows) once that still fills the GPU, one below: a decode step is a few
+  // hundred rows.
+  constexpr int kMany = 4;
+  const int64_t rows = a.tokens * (a.q_heads + (kAppend ? 0 : 1) * (int64_t)a.kv_heads);
+  const int heads = rows >= kMany * 152 * 2 * kRows ? kMany : 1;
+  const int64_t chunks = (a.q_heads + heads - 1) / heads + (kAppend ? 0 : (a.kv_heads + heads - 1) / heads);
+  const int64_t row_ctas = along * chunks;
+  // Windows from four CTAs an SM of them on; below, a row a row group is nearer done.
+  const int64_t windows = (a.tokens + kWindow<D> - 1) / kWindow<D> * a.kv_heads;
+  const bool granules = kAppend && windows >= 4 * 152;
+  const int64_t ctas = row_ctas + (kAppend ? (granules ? windows : along * 2 * a.kv_heads) : 0);
+  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  void (*k)(QkArgs, uint32_t);
+  if constexpr (kAppend) {
+    k = granules ? (heads > 1 ? qk_kernel<T, D, kMany, kAppendGranules> : qk_kernel<T, D, 1, kAppendGranules>)
+                 : (heads > 1 ? qk_kernel<T, D, kMany, kAppendEach> : qk_kernel<T, D, 1, kAppendEach>);
+  } else {
+    k = heads > 1 ? qk_kernel<T, D, kMany, kNorm> : qk_kernel<T, D, 1, kNorm>;
+  }
+  return launch_dependent(k, dim3((unsigned)ctas), dim3(kQkThreads), 0, st, a, (uint32_t)row_ctas);
 }
 
 template <typename T, bool kAppend>

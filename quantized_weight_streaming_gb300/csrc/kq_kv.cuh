@@ -112,6 +112,67 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
+// Four or eight consecutive elements as they are in memory, to be held while others load.
+template <typename T, int N>
+struct Raw {
+  uint32_t u[N * sizeof(T) / 4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) u[i] = 0;
+  }
+  __device__ __forceinline__ void load(const T* p) {
+    constexpr int kBytes = N * sizeof(T);
+    if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        u[4 * i] = v.x, u[4 * i + 1] = v.y, u[4 * i + 2] = v.z, u[4 * i + 3] = v.w;
+      }
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      u[0] = v.x, u[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        union { uint32_t w; T t[2]; } y;
+        y.w = u[i];
+        v[2 * i] = to_float(y.t[0]), v[2 * i + 1] = to_float(y.t[1]);
+      }
+    }
+  }
+};
+
+// Four consecutive elements, aligned to their size.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  } else {
+    union { uint2 u; T t[4]; } x;
+    x.u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_float(x.t[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    union { uint2 u; T t[4]; } x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.t[i] = from_float<T>(v[i]);
+    *reinterpret_cast<uint2*>(p) = x.u;
+  }
+}
+
 }  // namespace kv
 
 // ---- host side -----------------------------------------------------------------
