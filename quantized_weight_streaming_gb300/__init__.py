@@ -480,6 +480,7 @@ class KVCache:
         self.data = data
         self.pages, self.page_size, self.kv_heads, self.head_dim = int(pages), int(page_size), int(kv_heads), int(head_dim)
         self.desc = kq_kv_cache(data.data_ptr(), self.pages, self.page_size, self.kv_heads, self.head_dim, 0)
+        self._ref = ctypes.byref(self.desc)
 
 
 class QKNorm:
@@ -490,8 +491,10 @@ class QKNorm:
     def __init__(self, q_heads, kv_heads, head_dim, rope_dim=0, q_weight=None, k_weight=None, rope=None, eps=1e-6,
                  interleaved=False, norm=True):
         self.q_weight, self.k_weight, self.rope = q_weight, k_weight, rope
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.desc = kq_qk_norm(q_heads, kv_heads, head_dim, rope_dim, int(interleaved), int(norm), eps, 0,
                                _ptr(q_weight), _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0])
+        self._ref = ctypes.byref(self.desc)
 
 
 _DTYPES = {}  # torch dtype -> (kq_dtype or -1, whether it is int32), filled on first use
@@ -557,45 +560,43 @@ def kq_rope_table_host(positions, rope_dim, base):
 
 def kq_qk_norm_rope(p, q, k, d_positions, q_out, k_out, stream=None):
     """Norm and rotation of q [tokens, q_heads, D] and k [tokens, kv_heads, D] (strided views) into q_out, k_out."""
-    d = p.desc
-    _check(_lib.kq_qk_norm_rope(ctypes.byref(d), _dtype(q), _heads(q, d.q_heads, d.head_dim, "q"),
-                                _heads(k, d.kv_heads, d.head_dim, "k", q), _ints(d_positions, q.shape[0], "d_positions"),
-                                q.shape[0], _heads(q_out, d.q_heads, d.head_dim, "q_out", q),
-                                _heads(k_out, d.kv_heads, d.head_dim, "k_out", q), _stream(stream)), "kq_qk_norm_rope")
+    hq, hk, d, t = p.q_heads, p.kv_heads, p.head_dim, q.shape[0]
+    _check(_lib.kq_qk_norm_rope(p._ref, _dtype(q), _heads(q, hq, d, "q"), _heads(k, hk, d, "k", q),
+                                _ints(d_positions, t, "d_positions"), t, _heads(q_out, hq, d, "q_out", q),
+                                _heads(k_out, hk, d, "k_out", q), _stream(stream)), "kq_qk_norm_rope")
 
 
 def kq_kv_append(p, cache, q, k, v, d_positions, d_slots, q_out, stream=None):
     """Norm and rotation of q into q_out; keys (normed, rotated) and values into the cache at d_slots, in 4 bits.
     q and q_out may be None."""
-    d, t = p.desc, k.shape[0]
-    _check(_lib.kq_kv_append(ctypes.byref(d), ctypes.byref(cache.desc), _dtype(k), _heads(q, d.q_heads, d.head_dim, "q", k),
-                             _heads(k, d.kv_heads, d.head_dim, "k"), _heads(v, d.kv_heads, d.head_dim, "v", k),
-                             _ints(d_positions, t, "d_positions"), _ints(d_slots, t, "d_slots"), t,
-                             _heads(q_out, d.q_heads, d.head_dim, "q_out", k), _stream(stream)), "kq_kv_append")
+    hq, hk, d, t = p.q_heads, p.kv_heads, p.head_dim, k.shape[0]
+    _check(_lib.kq_kv_append(p._ref, cache._ref, _dtype(k), _heads(q, hq, d, "q", k), _heads(k, hk, d, "k"),
+                             _heads(v, hk, d, "v", k), _ints(d_positions, t, "d_positions"), _ints(d_slots, t, "d_slots"), t,
+                             _heads(q_out, hq, d, "q_out", k), _stream(stream)), "kq_kv_append")
 
 
 def kq_kv_read(cache, d_slots, k_out, v_out, stream=None):
     """What the cache holds at d_slots, as values: k_out, v_out [count, kv_heads, D]."""
-    _check(_lib.kq_kv_read(ctypes.byref(cache.desc), _ints(d_slots, k_out.shape[0], "d_slots"), k_out.shape[0],
-                           _dtype(k_out), _heads(k_out, cache.kv_heads, cache.head_dim, "k_out"),
-                           _heads(v_out, cache.kv_heads, cache.head_dim, "v_out", k_out), _stream(stream)), "kq_kv_read")
+    h, d, n = cache.kv_heads, cache.head_dim, k_out.shape[0]
+    _check(_lib.kq_kv_read(cache._ref, _ints(d_slots, n, "d_slots"), n, _dtype(k_out), _heads(k_out, h, d, "k_out"),
+                           _heads(v_out, h, d, "v_out", k_out), _stream(stream)), "kq_kv_read")
 
 
 def kq_attn_workspace_bytes(cache, q_heads, requests, tokens, max_new):
-    return _lib.kq_attn_workspace_bytes(ctypes.byref(cache.desc), q_heads, requests, tokens, max_new)
+    return _lib.kq_attn_workspace_bytes(cache._ref, q_heads, requests, tokens, max_new)
 
 
 def kq_attn_paged(cache, q, d_q_start, d_kv_len, d_block_table, out, scale, max_new, window=0, ws=None, stream=None):
     """Attention of the step's new tokens q [tokens, q_heads, D] over the cache, causal, optionally over a sliding
     window; at most max_new new tokens a request."""
     p, nb = _ws(ws)
-    r, hq = d_kv_len.numel(), q.shape[1] if q.dim() == 3 else 0
-    if d_block_table.dim() != 2 or d_block_table.shape[0] < r:
-        raise KQError(KQ_ERR_SHAPE, f"block table {tuple(d_block_table.shape)} for {r} requests")
-    _check(_lib.kq_attn_paged(ctypes.byref(cache.desc), _dtype(q), hq, _heads(q, hq, cache.head_dim, "q"),
-                              _ints(d_q_start, r + 1, "d_q_start"), _ints(d_kv_len, r, "d_kv_len"),
-                              _ints(d_block_table, 0, "d_block_table"), d_block_table.shape[1], r, q.shape[0], max_new,
-                              scale, window, _heads(out, hq, cache.head_dim, "out", q), p, nb, _stream(stream)),
+    r, shape, table, d = d_kv_len.numel(), q.shape, d_block_table.shape, cache.head_dim
+    if len(table) != 2 or table[0] < r or len(shape) != 3:
+        raise KQError(KQ_ERR_SHAPE, f"block table {tuple(table)} for {r} requests, q {tuple(shape)}")
+    hq = shape[1]
+    _check(_lib.kq_attn_paged(cache._ref, _dtype(q), hq, _heads(q, hq, d, "q"), _ints(d_q_start, r + 1, "d_q_start"),
+                              _ints(d_kv_len, r, "d_kv_len"), _ints(d_block_table, 0, "d_block_table"), table[1], r,
+                              shape[0], max_new, scale, window, _heads(out, hq, d, "out", q), p, nb, _stream(stream)),
            "kq_attn_paged")
 
 
