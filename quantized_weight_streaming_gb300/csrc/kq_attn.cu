@@ -775,12 +775,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     const Runs runs(*a.prompt_total, kSms, P::kLeastRun);
     if (b >= runs.count) return;
     const RunStart start = a.prompt_starts[b];
-    // a row block starts with the run, or an earlier boundary fell in it too
-    if (start.tile == 0 || start.lo < runs.start(b - 1)) return;
+    // no tile of the row lies before this boundary, or an earlier boundary lies between its tiles too
+    const int64_t lo = start.lo + P::kRowCost;
+    if (start.at <= P::kRowCost || lo < runs.start(b - 1)) return;
     const Request q = request_of(a, start.r, P::kKeys);
     const int32_t first = (int32_t)(at % kJoinSlices<D>) * kJoinRows;
     const int32_t rows = min(P::kRows, q.rows - start.k * P::kRows);
-    const int64_t w1 = runs.of(start.lo + start.tiles - 1);
+    const int64_t w1 = runs.of(lo + start.tiles - 1);
 #pragma unroll
     for (int i = 0; i < kJoinRows / kWarps; ++i) {
       const int32_t in = first + i * kWarps + warp;

@@ -20,11 +20,11 @@ using kv::Layout;
 
 constexpr int kSms = 152;
 
-// Where a run of the prompt kernel begins: in key tile `tile` of the `tiles` that row block k of request r has for key
-// head h; the first of them is work unit `lo`.
+// Where a run of the prompt kernel begins: in unit `at` of row block k of request r and key head h, which looks at
+// `tiles` key tiles and whose first unit is work unit `lo`.
 struct RunStart {
   int64_t r, lo;
-  int32_t k, h, tile, tiles;
+  int32_t k, h, at, tiles;
 };
 
 struct Args {
@@ -83,7 +83,12 @@ struct PromptShape {
   static constexpr int kTiles = D == 256 ? 1 : 2;     // 128 query rows each
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = 64;
-  static constexpr int kLeastRun = 8;                 // key tiles of a run
+  // A row (a block of query rows of one key head) counts as its key tiles and so many units before them: fetching the
+  // queries and putting the rows away cost about 15000 cycles, a tile 1800 to 2400.  (Counted by tiles alone, ragged
+  // prompts left CTAs with nine short rows, 176000 cycles, beside others with two, 72000.)
+  static constexpr int kRowCost = 8;
+  static constexpr int kLeastRun = 12;                // units of a run
+  __device__ static int32_t units(int32_t tiles) { return tiles ? tiles + kRowCost : 0; }
   static constexpr int64_t kPartial = kRows * (int64_t)(D + 2);
 };
 
