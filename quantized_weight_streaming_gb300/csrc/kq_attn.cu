@@ -561,64 +561,84 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   if (producer) {
     const uint64_t policy = l2_policy_evict_first();
     const int per_page = a.cache.page_size / kGranule;
+    const int64_t page_bytes = a.cache.kv_heads * a.cache.block_bytes;
+    const bool in_one = per_page % C::kTileGranules == 0;  // a tile lies in one page
+    // The row's tiles that are left, the page and granule within it of the next one, and what a row fixes; page `at`
+    // of the request is `id`, the page after it in flight.
+    int32_t left = 0, page = 0, sub = 0, pages = 0, at = -1, id = -1, next = -1;
     const int32_t* row = nullptr;
+    const uint8_t* head = nullptr;
     int64_t row_of = -1;
-    int32_t at = -1, id = -1, next = -1;  // page `at` of the request, and the page after it in flight
     uint32_t made = 0;
+    bool more = lane < C::kWarps;
+    auto enter = [&]() {  // the next tile's row
+      more = more && seek<C::kTile>(a, cur);
+      if (!more) return;
+      left = (int32_t)min((int64_t)(min(cur.need_hi, cur.q.tiles) - cur.tile), cur.end - cur.unit);
+      if (cur.r != row_of) {
+        row_of = cur.r, row = a.table + cur.r * a.table_stride, at = -1;
+        pages = (cur.q.len + a.cache.page_size - 1) / a.cache.page_size;  // the table's row holds them
+      }
+      const int32_t g0 = (cur.q.tile0 + cur.tile) * C::kTileGranules;
+      page = g0 / per_page, sub = g0 - page * per_page;
+      head = a.cache.data + cur.row / row_tiles(cur.q) * a.cache.block_bytes;
+      // the tiles that follow are the row's
+      cur.tile += left;
+      cur.unit += left;
+    };
+    // The address of the granule at (page, sub), or NULL.
+    auto source = [&]() -> const uint8_t* {
+      if (page >= pages) return nullptr;
+      if (page != at) {
+        id = at >= 0 && page == at + 1 ? next : row[page];
+        at = page;
+        next = page + 1 < pages ? row[page + 1] : -1;
+      }
+      if (id >= 0 && id < a.cache.pages) return head + id * page_bytes + sub * L::kBytes;
+      const int32_t key = (page * per_page + sub) * kGranule;
+      if (key < cur.q.len && key + (in_one ? C::kTile : kGranule) > cur.q.lo) attn_flag(KQ_ERR_RANGE);
+      return nullptr;  // (a page below a sliding window may be gone)
+    };
+    enter();
     // The lanes stay together: whichever find a free stage issue a tile, and only where none does the warp sleeps.  (With
-    // a wait per lane the slowest consumer held up all the others' copies.)
-    bool more = lane < C::kWarps && seek<C::kTile>(a, cur);
+    // a wait per lane the slowest consumer held up all the others' copies; and a tile's own arithmetic has to stay
+    // short, or its stage comes back late: 11 or 7 lanes share the warp.)
     long long since = clock64();
     while (__any_sync(~0u, more)) {
       const int st = made % C::kStages;
       const bool free = more && (made < C::kStages || mbar_test_wait(&empty[st], (made / C::kStages - 1) & 1));
       if (!__any_sync(~0u, free)) {
-        if (clock64() - since > kWaitLimitCycles) break;  // a consumer gave up, and reports it
-        __nanosleep(40);
+        if (__any_sync(~0u, clock64() - since > kWaitLimitCycles)) break;  // a consumer gave up, and reports it
+        __nanosleep(20);
         continue;
       }
       since = clock64();
       if (!free) continue;
-      if (cur.r != row_of) row_of = cur.r, row = a.table + cur.r * a.table_stride, at = -1;
-      const int32_t pages = (cur.q.len + a.cache.page_size - 1) / a.cache.page_size;  // the table's row holds them
-      const int32_t g0 = (cur.q.tile0 + cur.tile) * C::kTileGranules;
-      int64_t src[C::kTileGranules];
-      uint32_t have = 0;
-      int32_t page = g0 / per_page, sub = g0 - page * per_page;
-#pragma unroll
-      for (int i = 0; i < C::kTileGranules; ++i) {
-        src[i] = -1;
-        if (page < pages) {
-          if (page != at) {
-            id = at >= 0 && page == at + 1 ? next : row[page];
-            at = page;
-            next = page + 1 < pages ? row[page + 1] : -1;
-          }
-          const int32_t key = (g0 + i) * kGranule;
-          if (id >= 0 && id < a.cache.pages) {
-            src[i] = ((int64_t)id * a.cache.kv_heads + cur.row / row_tiles(cur.q)) * a.cache.block_bytes + sub * L::kBytes;
-            have |= 1u << i;
-          } else if (key < cur.q.len && key + kGranule > cur.q.lo) {
-            attn_flag(KQ_ERR_RANGE);  // (a page below a sliding window may be gone)
-          }
-        }
-        if (++sub == per_page) sub = 0, ++page;
-      }
-      hidden[st] = ~have & ((1u << C::kTileGranules) - 1);
-      mbar_arrive_expect_tx(&full[st], __popc(have) * L::kBytes);
       uint8_t* dst = ring + st * C::kStageBytes;
-      if (C::kTileGranules > 1 && have == (1u << C::kTileGranules) - 1 &&
-          src[C::kTileGranules - 1] - src[0] == (C::kTileGranules - 1) * L::kBytes) {
-        bulk_g2s(dst, a.cache.data + src[0], C::kStageBytes, &full[st], policy);  // within one page: one copy
+      if (in_one) {
+        const uint8_t* src = source();
+        hidden[st] = src ? 0u : (1u << C::kTileGranules) - 1;
+        mbar_arrive_expect_tx(&full[st], src ? C::kStageBytes : 0);
+        if (src) bulk_g2s(dst, src, C::kStageBytes, &full[st], policy);
+        sub += C::kTileGranules;
+        if (sub == per_page) sub = 0, ++page;
       } else {
+        const uint8_t* src[C::kTileGranules];
+        uint32_t have = 0;
+#pragma unroll
+        for (int i = 0; i < C::kTileGranules; ++i) {
+          src[i] = source();
+          have |= (uint32_t)(src[i] != nullptr) << i;
+          if (++sub == per_page) sub = 0, ++page;
+        }
+        hidden[st] = ~have & ((1u << C::kTileGranules) - 1);
+        mbar_arrive_expect_tx(&full[st], __popc(have) * L::kBytes);
 #pragma unroll
         for (int i = 0; i < C::kTileGranules; ++i)
-          if (have >> i & 1u) bulk_g2s(dst + i * L::kBytes, a.cache.data + src[i], L::kBytes, &full[st], policy);
+          if (src[i]) bulk_g2s(dst + i * L::kBytes, src[i], L::kBytes, &full[st], policy);
       }
       ++made;
-      ++cur.tile;
-      ++cur.unit;
-      more = seek<C::kTile>(a, cur);
+      if (--left == 0) enter();
     }
     // the ring stays until the last copies have landed (they have, unless a consumer gave up)
     if (lane < C::kWarps)
