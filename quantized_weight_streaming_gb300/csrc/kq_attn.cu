@@ -69,18 +69,24 @@ constexpr int kLeastRun = 2;         // tiles of a run, where there are fewer th
 template <typename T, int D>
 struct Config {
   static constexpr bool kSplit = sizeof(T) == 4;        // two fp16 parts
-  static constexpr int kWarps = (D == 256 ? 8 : 12) - 1;
-  static constexpr int kStages = kWarps < 8 ? 6 : (kWarps < 12 ? 4 : 3);
+  // Consumer warps; with the copying warp two or three a scheduler, 255 or 168 registers.  At D = 256 the queries of
+  // 16-bit rows lie in shared memory (read once a tile), for three: sums and queries in registers leave room for two,
+  // which kept 4.5 TB/s busy.
+  static constexpr bool kQShared = D == 256 && !kSplit;
+  static constexpr int kWarps = (D == 256 && !kQShared ? 8 : 12) - 1;
+  static constexpr int kStages = kQShared ? 3 : (kWarps < 8 ? 6 : 4);
+  static constexpr int kQueries = kQShared ? kWarps * (D / 32) * 512 : 0;  // bytes
   static constexpr int kTileGranules = 256 / D;
   static constexpr int kTile = kTileGranules * kGranule;  // keys
   static constexpr int kStageBytes = kTileGranules * Layout<D>::kBytes;
   static constexpr int kThreads = 32 * (kWarps + 1);      // and the warp that issues the copies
   static constexpr int kRing = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRing + kWarps * kStages * 20;  // two barriers and a word a stage
+  static constexpr int kBarriers = kRing + kQueries;
+  static constexpr int kSmem = kBarriers + kWarps * kStages * 20;  // two barriers and a word a stage
 };
 // D = 256: one granule of 4608 bytes; 128: two; 64: four.
 
-constexpr int kMaxWarps = 15;
+constexpr int kMaxWarps = 11;
 // Floats of a partial result: 8 rows x D sums, 8 references, 8 weights.
 constexpr int64_t partial_floats(int d) { return kRows * (int64_t)d + 2 * kRows; }
 template <int D>
@@ -146,7 +152,8 @@ template <typename T, int D>
 struct Row {
   static constexpr int kQ = D / 32;  // groups
   static constexpr int kLo = Config<T, D>::kSplit ? kQ : 1;
-  uint32_t hi[kQ][4];                // operand A rows 0..7: dimensions (0,4), (1,5), (2,6), (3,7) of 8 c .., odd pairs / kOdd
+  // (kQShared: one group's at a time, the others in shared memory)
+  uint32_t hi[Config<T, D>::kQShared ? 1 : kQ][4];  // operand A rows 0..7: dimensions (0,4), (1,5), (2,6), (3,7) of 8 c .., odd pairs / kOdd
   uint32_t lo[kLo][4];               // rows 8..15
   float zero[kQ];                    // -8 sum(q) of each group
   float factor;                      // score in log2 units = factor * accumulated
@@ -184,7 +191,7 @@ __device__ __forceinline__ float reference(float m, int exponent) { return m + (
 
 template <typename T, int D, bool kMask>
 __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const uint8_t* stage, int32_t key0, uint32_t bad,
-                                            const Cursor& cur) {
+                                            const Cursor& cur, const uint8_t* queries) {
   using L = Layout<D>;
   using C = Config<T, D>;
   using Q = Codes<C::kSplit>;
@@ -210,30 +217,54 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
   float2 s[kBlocks];
   uint32_t seen = 0;  // bit 2 b + j: the row sees token 2 c + j of block b
   float top = -INFINITY;
-#pragma unroll
-  for (int b = 0; b < kBlocks; ++b) {
+  // scale * (q . code) of a group, for tokens 2 c and 2 c + 1 of a block, added to `sum`
+  auto score = [&](const uint32_t(&hi)[4], int q, uint32_t codes, uint32_t scale0, uint32_t scale1, float2& sum) {
+    float acc[4];
+    uint32_t l0 = 0, l1 = 0, l2 = 0, l3 = 0;
+    if constexpr (C::kSplit) l0 = w.lo[q][0], l1 = w.lo[q][1], l2 = w.lo[q][2], l3 = w.lo[q][3];
+    mma_from_zero(acc, hi[0], l0, hi[1], l1, Q::pair(codes, 0), Q::pair(codes, 1));
+    mma(acc, hi[2], l2, hi[3], l3, Q::pair(codes, 2), Q::pair(codes, 3));
+    float2 dot = add2(make_float2(acc[0], acc[1]), make_float2(w.zero[q], w.zero[q]));
+    if constexpr (C::kSplit) dot = add2(dot, make_float2(acc[2], acc[3]));
+    const float2 d0 = unpack2(scale0), d1 = unpack2(scale1);
+    sum = fma2(q % 2 ? make_float2(d0.y, d1.y) : make_float2(d0.x, d1.x), dot, sum);
+  };
+  auto block_words = [&](int b, int sl, uint32_t(&kw)[G], uint32_t(&ks)[G]) {  // ks: G scales of token 2 c, then of 2 c + 1
     const uint8_t* g0 = stage + (b / 2) * L::kBytes;
-    float2 sum = make_float2(0.f, 0.f);
+    load_words<G>(kw, g0 + L::kKeys + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
+    load_words<G>(ks, g0 + L::kKeyScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
+  };
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) s[b] = make_float2(0.f, 0.f);
+  if constexpr (C::kQShared) {
+    static_assert(kBlocks == 2, "one granule a tile");
 #pragma unroll
     for (int sl = 0; sl < L::kSlabs; ++sl) {
-      uint32_t kw[G], ks[G];  // ks: G scales of token 2 c, then of 2 c + 1
-      load_words<G>(kw, g0 + L::kKeys + sl * L::kKeySlab + (b % 2) * L::kBlock + lane * (L::kBlock / 32));
-      load_words<G>(ks, g0 + L::kKeyScales + sl * L::kScaleSlab + ((b % 2) * 8 + 2 * c) * G * 2);
+      uint32_t kw0[G], ks0[G], kw1[G], ks1[G];
+      block_words(0, sl, kw0, ks0);
+      block_words(1, sl, kw1, ks1);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int q = sl * G + g;
-        float acc[4];
-        uint32_t l0 = 0, l1 = 0, l2 = 0, l3 = 0;
-        if constexpr (C::kSplit) l0 = w.lo[q][0], l1 = w.lo[q][1], l2 = w.lo[q][2], l3 = w.lo[q][3];
-        mma_from_zero(acc, w.hi[q][0], l0, w.hi[q][1], l1, Q::pair(kw[g], 0), Q::pair(kw[g], 1));
-        mma(acc, w.hi[q][2], l2, w.hi[q][3], l3, Q::pair(kw[g], 2), Q::pair(kw[g], 3));
-        float2 dot = add2(make_float2(acc[0], acc[1]), make_float2(w.zero[q], w.zero[q]));
-        if constexpr (C::kSplit) dot = add2(dot, make_float2(acc[2], acc[3]));
-        const float2 d0 = unpack2(ks[g / 2]), d1 = unpack2(ks[G / 2 + g / 2]);
-        sum = fma2(g % 2 ? make_float2(d0.y, d1.y) : make_float2(d0.x, d1.x), dot, sum);
+        load_words<4>(w.hi[0], queries + ((sl * G + g) * 32 + lane) * 16);
+        score(w.hi[0], sl * G + g, kw0[g], ks0[g / 2], ks0[G / 2 + g / 2], s[0]);
+        score(w.hi[0], sl * G + g, kw1[g], ks1[g / 2], ks1[G / 2 + g / 2], s[1]);
       }
     }
-    s[b] = mul2(sum, make_float2(w.factor, w.factor));
+  } else {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+      for (int sl = 0; sl < L::kSlabs; ++sl) {
+        uint32_t kw[G], ks[G];
+        block_words(b, sl, kw, ks);
+#pragma unroll
+        for (int g = 0; g < G; ++g) score(w.hi[sl * G + g], sl * G + g, kw[g], ks[g / 2], ks[G / 2 + g / 2], s[b]);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b) {
+    s[b] = mul2(s[b], make_float2(w.factor, w.factor));
     if constexpr (kMask) {
       const int32_t key = key0 + 8 * b + 2 * c;
       const bool held = !(bad >> (b / 2) & 1u);
@@ -366,7 +397,7 @@ __device__ __forceinline__ bool seek(const Args& a, Cursor& c) {
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>& w) {
+__device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>& w, uint8_t* queries) {
   constexpr int kQ = D / 32;
   using C = Codes<Config<T, D>::kSplit>;
   constexpr float kZero = -8.f * (1 << C::kUnitLog) / 16777216.f;
@@ -406,12 +437,13 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
     float zh = 0.f, zl = 0.f;
+    uint32_t(&hi)[4] = w.hi[Config<T, D>::kQShared ? 0 : q];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const float f = p % 2 ? 1.f / C::kOdd : 1.f, back = p % 2 ? C::kOdd : 1.f;
       const float u = x8[q][p] * up * f, v = x8[q][p + 4] * up * f;
-      w.hi[q][p] = pack2(u, v);
-      const float2 r = unpack2(w.hi[q][p]);
+      hi[p] = pack2(u, v);
+      const float2 r = unpack2(hi[p]);
       zh += (r.x + r.y) * back;
       if constexpr (Config<T, D>::kSplit) {
         w.lo[q][p] = pack2(u - r.x, v - r.y);
@@ -419,6 +451,8 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
         zl += (t.x + t.y) * back;
       }
     }
+    if constexpr (Config<T, D>::kQShared)  // a lane reads back what it wrote
+      *reinterpret_cast<uint4*>(queries + (q * 32 + lane) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     zh += zl;
     zh += __shfl_xor_sync(~0u, zh, 1);
     zh += __shfl_xor_sync(~0u, zh, 2);
@@ -486,9 +520,9 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   const bool producer = warp == C::kWarps;
   const int me = producer ? min(lane, C::kWarps - 1) : warp;  // the consumer that this thread works for
   uint8_t* ring = smem + me * C::kStages * C::kStageBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing) + me * C::kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarriers) + me * C::kStages;
   uint64_t* empty = full + C::kWarps * C::kStages;
-  volatile uint32_t* hidden = reinterpret_cast<uint32_t*>(smem + C::kRing + C::kWarps * C::kStages * 16) + me * C::kStages;
+  volatile uint32_t* hidden = reinterpret_cast<uint32_t*>(smem + C::kBarriers + C::kWarps * C::kStages * 16) + me * C::kStages;
   if (!producer && lane < C::kStages) {
     mbar_init(&full[lane], 1);
     mbar_init(&empty[lane], 1);
@@ -649,12 +683,13 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
 
   // The cursor waits in shared memory while a row's tiles go by.
   Cursor& c = s_cursor[warp];
+  uint8_t* queries = smem + C::kRing + warp * (C::kQueries / C::kWarps);
   Row<T, D> w;
   bool first = true;
   uint32_t used = 0;
   while (cur.unit < cur.end) {
     if (cur.tile == cur.q.tiles) next_row<C::kTile>(a, cur);
-    begin_row<T, D>(a, cur, w);
+    begin_row<T, D>(a, cur, w, queries);
     __syncwarp();
     if (lane == 0) c = cur;
     __syncwarp();
@@ -671,9 +706,9 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       const uint32_t bad = hidden[st];
       const uint8_t* stage = ring + st * C::kStageBytes;
       if (bad || key0 < c.all_lo || key0 + C::kTile > c.all_hi)
-        attend_tile<T, D, true>(w, exponent, stage, key0, bad, c);
+        attend_tile<T, D, true>(w, exponent, stage, key0, bad, c, queries);
       else
-        attend_tile<T, D, false>(w, exponent, stage, key0, 0, c);
+        attend_tile<T, D, false>(w, exponent, stage, key0, 0, c, queries);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       ++used;
