@@ -414,6 +414,123 @@ def test_attention_value_scales_of_all_sizes(kq, dt):
         near(f64(out), s.want(), dt)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,d,page", [(8, 2, 128, 32), (7, 1, 64, 16), (6, 1, 256, 32)])
+def test_attention_long_prompt_in_many_parts(kq, dt, hq, hk, d, page):
+    """One prompt on a long context: its few row blocks are cut between all CTAs, some into more than two parts."""
+    rng = np.random.default_rng(21 + d)
+    s = Step(kq, rng, [2900], [150], hq, hk, d, page, dt)
+    s.check()
+    s.check(window=700)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_attention_mixed_batch(kq, dt):
+    """Single tokens, drafts, prompts and idle requests in one call; more of them than a CTA has threads."""
+    rng = np.random.default_rng(22)
+    new = rng.choice([0, 1, 1, 1, 3, 40], 700)
+    new[5], new[300] = 200, 90
+    lens = new + rng.integers(0, 60, 700)
+    lens[7] = new[7] + 900
+    s = Step(kq, rng, lens, new, 4, 2, 64, 16, dt)
+    s.check()
+    s.check(window=20)
+
+
+@pytest.mark.parametrize("sign", [-1.0, 0.0])
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attention_of_negative_and_zero_scale(kq, dt, sign):
+    rng = np.random.default_rng(23)
+    s = Step(kq, rng, [300, 90, 70], [70, 1, 3], 8, 2, 128, 32, dt)
+    s.scale *= sign
+    s.check()
+
+
+def test_attention_prompt_values_beyond_fp16(kq):
+    """Key and value scales above 8188 (8 steps leave fp16) in some tiles of a bf16 prompt."""
+    rng = np.random.default_rng(24)
+    s = Step(kq, rng, [400, 130], [90, 64], 8, 2, 128, 32, "bf16")
+    big = rng.random(s.vs.shape) < 0.02
+    s.vs = np.where(big & ~np.isnan(s.vs), np.float16(20000), s.vs)
+    s.ks = np.where(big & ~np.isnan(s.ks), np.float16(9000), s.ks)
+    s.q.mul_(1e-4)
+    s.cache.data.copy_(dev(ref.pack(s.kc, s.ks, s.vc, s.vs)))
+    out = s.run()
+    assert status(kq) == kq.KQ_OK
+    near(f64(out), s.want(), "bf16")
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attention_of_poisoned_values_stays_behind_the_mask(kq, dt):
+    """A visible key whose value scale is NaN: the rows that see it get NaN in its group of 32 dimensions, rows that the
+    causal mask or the window keeps from it nothing."""
+    rng = np.random.default_rng(25)
+    s = Step(kq, rng, [200, 40], [100, 4], 8, 2, 128, 32, dt)
+    want = s.want(window=60)
+    for r, j, g in ((0, 150, 1), (1, 37, 3)):
+        s.vs[s.table[r, j // 32], 0, j % 32, g] = np.nan
+    s.cache.data.copy_(dev(ref.pack(s.kc, s.ks, s.vc, s.vs)))
+    got = f64(s.run(window=60))
+    assert status(kq) == kq.KQ_OK
+    bad = np.zeros(got.shape, bool)
+    pos0 = np.concatenate([np.arange(100, 200), np.arange(36, 40)])
+    for r, j, g in ((0, 150, 1), (1, 37, 3)):
+        rows = (np.arange(104) >= 100) == (r == 1)
+        rows &= (pos0 >= j) & (pos0 < j + 60)
+        bad[np.ix_(rows, np.arange(4), np.arange(32 * g, 32 * g + 32))] = True
+    assert np.array_equal(np.isnan(got), bad)
+    norm = np.linalg.norm(want, axis=-1, keepdims=True)
+    assert np.all(np.abs(got - want)[~bad] <= (ATTN_TOL[dt] * norm * np.ones_like(want))[~bad])
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_attention_prompt_hides_bad_pages_and_freed_ones(kq, dt):
+    """Pages below a sliding window may be gone (no status, no effect); a missing page inside it hides its keys."""
+    rng = np.random.default_rng(26)
+    s = Step(kq, rng, [400], [80], 4, 2, 128, 32, dt)
+    table = s.table.copy()
+    table[0, :6] = -1  # keys 0..191; the window's first is 400 - 80 - 99 = 221
+    near(f64(s.run(window=100, table=table)), s.want(window=100), dt)
+    assert status(kq) == kq.KQ_OK
+    table[0, 9] = s.cache.pages + 3  # keys 288..319
+    got = f64(s.run(table=np.where(s.table < 0, -1, np.where(np.arange(s.table.shape[1]) == 9, table, s.table))))
+    assert status(kq) == kq.KQ_ERR_RANGE
+    k, v = (np.nan_to_num(ref.values(c, x)) for c, x in ((s.kc, s.ks), (s.vc, s.vs)))
+    for t in (0, 41, 79):
+        keys = np.array([j for j in range(320 + t + 1) if not 288 <= j < 320])
+        kk, vv = (x[s.table[0, keys // 32], :, keys % 32] for x in (k, v))
+        for h in range(4):
+            e = s.scale * kk[:, h // 2] @ f64(s.q)[t, h]
+            p = np.exp(e - e.max())
+            near(got[t, h], (p / p.sum()) @ vv[:, h // 2], dt)
+
+
+def test_attention_leaves_out_malformed_requests(kq):
+    """q_start that decreases or passes the tokens, and more new tokens than max_new: a status, the other requests'
+    rows as they should be."""
+    rng = np.random.default_rng(27)
+    s = Step(kq, rng, [100, 60, 90], [60, 4, 1], 8, 2, 128, 32, "f16")
+    want, good = s.want(), s.q_start
+    for q_start in ([0, 60, 64, 900], [0, 60, 20, 65], [-4, 60, 64, 65]):
+        s.q_start = np.array(q_start)
+        out = f64(s.run(max_new=60))
+        assert status(kq) == kq.KQ_ERR_RANGE
+        claims = np.zeros(65, int)  # well-formed requests that a row belongs to
+        for lo, hi in zip(q_start, q_start[1:]):
+            if 0 <= lo <= hi <= 65:
+                claims[lo:hi] += 1
+        for r in range(3):
+            lo, hi = q_start[r], q_start[r + 1]
+            if (lo, hi) == (good[r], good[r + 1]):
+                rows = lo + np.flatnonzero(claims[lo:hi] == 1)
+                near(out[rows], want[rows], "f16")
+    s.q_start = good
+    out = f64(s.run(max_new=10))
+    assert status(kq) == kq.KQ_ERR_RANGE
+    assert np.all(out[:60] == 7)
+    near(out[60:], want[60:], "f16")
+
+
 def test_attention_offsets_past_32_bits(kq):
     rng = np.random.default_rng(13)
     far = (5 << 30) // (2 * ref.block_bytes(32, 128))
