@@ -633,3 +633,15 @@ def test_whole_step(kq):
         want = ref.attention(f64(qo), ref.values(kc, ks), ref.values(vc, vs), q_start.cpu().numpy(), cached,
                              table.cpu().numpy(), page, d ** -0.5, 0)
         near(f64(out), want, "f32")
+
+
+def test_example_decode_layer(kq):
+    """The example's layer: prompt and steps through slot map, projections, append and attention, fp32 throughout."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_layer.py")
+    spec = importlib.util.spec_from_file_location("decode_layer", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.main(requests=3, prompt=21, steps=3) < ATTN_TOL["f32"]
