@@ -386,10 +386,11 @@ void kq_decode_plan_destroy(kq_plan* plan);
  * only after the matrices it depends on have written their outputs, while
  * the weight stream keeps running ahead across stage boundaries.
  *
- * The operations between projections that are not projections (attention,
- * normalisation, activation functions, residual adds) are outside this
- * library; the plainest stand-in is kept: the activation of a dependent
- * matrix is alpha times a prefix of an earlier matrix's output. */
+ * A linked plan knows projections only.  What lies between them (attention
+ * and the norm and rotation before it have entry points of their own, under
+ * or below; activation functions and residual adds are outside this library)
+ * is not part of the launch; the plainest stand-in is kept: the activation of
+ * a dependent matrix is alpha times a prefix of an earlier matrix's output. */
 typedef enum {
   KQ_SRC_PACKED = 0,    /* a fresh slot of d_x_packed, in list order over the matrices with this kind */
   KQ_SRC_INPUT_OF = 1,  /* the same activation as matrix `of` (k equal): a grouped matvec */

@@ -40,6 +40,16 @@
 // stages (bulk copies of whole granules, 4608 bytes a tile), so warps never
 // wait for one another.  A row cut between warps leaves partial sums in the
 // workspace; a second launch joins them in a fixed order.
+//
+// Measured (a replayed graph, both launches, 4 of them its own): 64 requests of
+// 16384 tokens, 24 query and 4 key heads of 256, fp16: 273 us, 1.21 GB of
+// cache; 32 ragged requests of 8000 on average, 32 and 8 heads of 128, bf16:
+// 51 us, 143 MB; 4 requests of 8 new tokens, fp32: 41 us.  The large ones move
+// 4.5 (D = 256) and 5.4 TB/s (D = 128) once they run, behind 12 us of finding
+// the runs, first copies, and joining.  Instructions bound them, not bytes: 51
+// to 55% of the issue slots taken with three warps a scheduler, tensor pipe 29
+// to 34%; per word of eight codes there are five to unpack, and the zero
+// points, scales and softmax.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -64,7 +74,9 @@ constexpr int kCombineThreads = 256;
 constexpr int kJoinRows = 16, kZeroCtas = 8;
 template <int D>
 constexpr int kJoinSlices = PromptShape<D>::kRows / kJoinRows;
-constexpr int kLeastRun = 2;         // tiles of a run, where there are fewer than two for every warp
+// Tiles of a run where there are fewer than one for every warp: one request of 1300 tokens (8 key heads of 128) takes
+// 16.4 us with one, 18.5 with two, 22.6 with eight; 32 requests of 1000 take 25 with any.
+constexpr int kLeastRun = 1;
 
 template <typename T, int D>
 struct Config {
@@ -883,7 +895,8 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
   const bool prompts = a.few_rows != 0x7fffffff;
   const int64_t rows = std::min<int64_t>(prompts ? a.few_rows : 0x7fffffff, std::min(a.max_new, a.tokens) * a.group);
   const int slices = (int)((rows + kRows - 1) / kRows);
-  // a row a CTA while the GPU holds them at once (one long request's rows lie in a hundred parts), else more
+  // A row a CTA where that stays few: one request of 20000 tokens, whose rows lie in a hundred parts, took 28 us instead
+  // of 52 with eight rows a CTA; with 256 row tiles a row a CTA cost 32 requests of 8000 tokens 4 us more.
   const int64_t tiles = a.requests * a.cache.kv_heads * slices;
   const int tile_rows = (int)std::min<int64_t>(rows, kRows);
   const int rows_per_cta = tiles <= 64 ? 1 : kRows;
@@ -898,8 +911,10 @@ static cudaError_t launch(int d, const Args& a, cudaStream_t st) {
   return d == 64 ? launch<T, 64>(a, st) : (d == 128 ? launch<T, 128>(a, st) : launch<T, 256>(a, st));
 }
 
-// Query rows of a request from which on the prompt kernel takes it (16-bit queries).
-constexpr int32_t kFewRows = 32;
+// Query rows of a request up to which attend_kernel takes it, with 16-bit queries; beyond, the prompt kernel.  8 requests
+// of 4096 tokens, 32 query and 8 key heads of 128: 32 rows 54 us here against 59, 64 rows 85 against 60; 24 and 4 heads of
+// 256: 24 rows 52 against 62, 48 rows 73 against 63; 14 and 2 heads of 64: 56 rows 31 against 35, 112 rows 39 against 36.
+constexpr int32_t few_rows_of(int d) { return d == 64 ? 64 : 40; }
 
 // The workspace: byte offsets of its parts, and its size.
 struct Workspace {
@@ -908,7 +923,7 @@ struct Workspace {
 static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t requests, int64_t tokens, int64_t max_new) {
   const int d = c->head_dim;
   const int64_t group = q_heads / c->kv_heads;
-  const bool prompts = std::min(max_new, tokens) > kFewRows / group;
+  const bool prompts = std::min(max_new, tokens) > few_rows_of(d) / group;
   const int64_t partial = d == 256 ? PromptShape<256>::kPartial : (d == 128 ? PromptShape<128>::kPartial : PromptShape<64>::kPartial);
   Workspace w{};
   size_t at = 0;
@@ -997,8 +1012,8 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
   a.prompt_total = reinterpret_cast<int64_t*>(ws + w.prompt_total);
   a.prompt_starts = reinterpret_cast<attn::RunStart*>(ws + w.prompt_starts);
   a.prompt_partials = reinterpret_cast<float*>(ws + w.prompt_partials);
-  const bool prompts = dtype != KQ_F32 && std::min(max_new, tokens) > attn::kFewRows / a.group;
-  a.few_rows = prompts ? attn::kFewRows : 0x7fffffff;
+  const bool prompts = dtype != KQ_F32 && std::min(max_new, tokens) > attn::few_rows_of(cache->head_dim) / a.group;
+  a.few_rows = prompts ? attn::few_rows_of(cache->head_dim) : 0x7fffffff;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32 ? attn::launch<float>(cache->head_dim, a, st)
                               : (dtype == KQ_F16 ? attn::launch<__half>(cache->head_dim, a, st)

@@ -19,17 +19,26 @@
 // the tile's keys or values are divided by 8, and scores or probabilities
 // multiplied by it.
 //
-// Roles: warp 0 copies granules into raw stages; warps 1 and 3 issue the MMAs of
-// an M tile each; warp 2 looks at a stage's scales; warps 4-7 and 8-11 are the softmax of the two M
-// tiles; warps 12-15 and 16-19 unpack every other key tile, into a ring of
-// buffers that keys and values take in turn (one group of four warps bound the
-// kernel: 507 us, 309 without it; eight warps on every tile spent 750 of their
-// 2600 cycles a tile at barriers and had one chain of work at a time).  Each M tile has two S buffers
-// (P replaces S in place), and QK of the next key tile is issued before PV of
-// this one, so that a softmax finds its next scores waiting: with one S buffer
-// of 128 keys per M tile the chain QK, softmax, PV bound the kernel (382 us for
-// 2048 tokens on 8192, 32 heads of 128).  The reference m of a row moves only
-// when a score passes it by 8, and then its warp rescales O in tensor memory.
+// Roles: warp 0 copies granules into raw stages; warps 1 and 3 issue the MMAs
+// of an M tile each; warp 2 looks at a stage's scales; warps 4-7 and 8-11 are
+// the softmax of the two M tiles; warps 12-15 and 16-19 unpack every other key
+// tile, into a ring of buffers that keys and values take in turn (one group of
+// four warps bound the kernel: 507 us, 309 without it; eight warps on every
+// tile spent 750 of their 2600 cycles a tile at barriers and had one chain of
+// work at a time).  Each M tile has two S buffers (P replaces S in place), and
+// QK of the next key tile is issued before PV of this one, so that a softmax
+// finds its next scores waiting: with one S buffer of 128 keys per M tile the
+// chain QK, softmax, PV bound the kernel (382 us).  The reference m of a row is
+// the largest score of the first tile it sees; it moves when a tile's sum of p
+// passes 2^12, and then its warp rescales O in tensor memory.  The loops are
+// unrolled no further than the instruction cache takes with five roles running
+// (378 us with the unpacking loops unrolled, 266 without).
+//
+// Measured: 2048 tokens on 8192 already held, 32 query and 8 key heads of 128,
+// bf16: 260 to 266 us, 905 to 925 TFLOP/s of what the mask leaves.  Issue slots
+// bound it (64% taken; tensor pipe 40%): unpacking, which each row block does
+// anew, and the softmax.  Rounding K, V and P to fp16 costs rows of fp16 output
+// an error of 3.6e-4 where rounding the output alone costs 2.1e-4.
 //
 // Row blocks in order, each head's key tiles end to end, are cut into one run
 // of tiles per CTA, whatever the prompts' lengths and masks; a block cut

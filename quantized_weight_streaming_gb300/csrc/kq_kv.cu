@@ -26,7 +26,9 @@ __device__ __forceinline__ void kv_flag(int status) { atomicOr(&g_kv_status, 1u 
 // tokens and runs the sum itself, kScan requests at a time, up to the chunk that
 // ends its range (CTA 0 runs it to the end and writes the per-request outputs),
 // so the whole map is one launch with no pass over intermediate sums.  A page
-// is entered in the table by the one token that opens it.
+// is entered in the table by the one token that opens it.  Bound by latency: 90k
+// tokens of 61 requests take 3.4 us beyond an empty launch (2048 tokens a CTA
+// instead of 512 took 9.5), 256 requests of one token 1.4.
 constexpr int kScanThreads = 256;
 constexpr int kScan = 4 * kScanThreads;
 constexpr int kMapTokens = 512;  // tokens of a CTA
@@ -276,10 +278,11 @@ __device__ __forceinline__ bool rope_row(const QkArgs& a, int64_t t, bool report
 // Query rows (and key rows that are not quantized): kHeads heads of one token a
 // row group, all loaded before the first is reduced and held as they came: bound
 // by the bytes of the rows, so what counts is how many are on their way (four
-// heads, held in fp32 by 24 warps an SM, moved 3.4 TB/s).  A lane holds four dimensions and their four partners in the rotation
-// (what is not rotated: eight in a row), so that rotating takes no shuffles and
-// half the table loads: with eight dimensions in a row and shuffles 4099 tokens
-// of 28 heads of 256 took 35 us.
+// heads, held in fp32 by 24 warps an SM, moved 3.4 TB/s).  A lane holds four
+// dimensions and their four partners in the rotation (what is not rotated:
+// eight in a row), so that rotating takes no shuffles and half the table loads.
+// 4099 tokens of 28 heads of 256 in bf16: 24 us, 4.9 TB/s (35 us with eight
+// dimensions in a row, shuffles and rows held in fp32).
 template <typename T, int D, int kHeads>
 __device__ __forceinline__ void norm_rows(const QkArgs& a, const View& in, const View& out, const float* weight, int heads,
                                           int64_t t0, int h0) {
@@ -441,8 +444,10 @@ __device__ __forceinline__ int32_t slot_of(const QkArgs& a, int64_t t) {
 // runs of successive slots (prompts), the rows are put together in shared memory
 // as the granules that they fill and go out word by word in memory order; a word
 // of two tokens' values of which one is not in the window, as half words.
-// Straight to the cache a token's values are 32 two-byte stores (8192 tokens of
-// 8 heads of 128, with their queries: 86 us).
+// Straight to the cache a token's values are 32 two-byte stores.  8192 tokens of
+// 8 key and 32 query heads of 128 in bf16: 58 us (3.0 TB/s; 86 before, straight
+// and with 230 instructions to quantize a lane's values); what bounds it is the
+// issue of instructions, 70% of the slots.
 constexpr int kWindowGranules = 4;
 template <int D>
 constexpr int kWindow = D == 256 ? 16 : 32;
@@ -588,7 +593,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkArgs a, uint32_t row_c
   }
 }
 
-// One row of one slot a row group: its codes' values in `T`.
+// One row of one slot a row group: its codes' values in `T`.  8192 tokens of 8
+// heads of 128 to fp16: 12 us, 3.5 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(kQkThreads) read_kernel(Cache c, const int32_t* slots, int64_t count, View k, View v) {
   using L = Layout<D>;
@@ -629,14 +635,15 @@ template <typename T, int D, bool kAppend>
 static cudaError_t launch_qk(const QkArgs& a, cudaStream_t st) {
   constexpr int kRows = kQkThreads / (D / 8);
   const int64_t along = (a.tokens + kRows - 1) / kRows;
-  // Several heads a row group (32 registers of rows) once that still fills the GPU, one below: a decode step is a few
-  // hundred rows.
+  // Four heads a row group once that still fills the GPU, one below: 1024 tokens of 28 heads of 256 take 9.0 us with
+  // four, 12.3 with one; 64 tokens 5.5 and 4.8.  (Eight held too many registers: 35 us against 29 for 4099 tokens.)
   constexpr int kMany = 4;
   const int64_t rows = a.tokens * (a.q_heads + (kAppend ? 0 : 1) * (int64_t)a.kv_heads);
   const int heads = rows >= kMany * 152 * 2 * kRows ? kMany : 1;
   const int64_t chunks = (a.q_heads + heads - 1) / heads + (kAppend ? 0 : (a.kv_heads + heads - 1) / heads);
   const int64_t row_ctas = along * chunks;
-  // Windows from four CTAs an SM of them on; below, a row a row group is nearer done.
+  // Windows from four CTAs an SM of them on: 2432 tokens of 8 heads of 128 take 28.8 us with their queries against 30.8 a
+  // row a row group, 4096 tokens 43.0 against 47.2, but 1024 tokens 18.5 against 16.5 and 64 tokens 12.3 against 8.2.
   const int64_t windows = (a.tokens + kWindow<D> - 1) / kWindow<D> * a.kv_heads;
   const bool granules = kAppend && windows >= 4 * 152;
   const int64_t ctas = row_ctas + (kAppend ? (granules ? windows : along * 2 * a.kv_heads) : 0);
