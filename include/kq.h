@@ -387,8 +387,8 @@ void kq_decode_plan_destroy(kq_plan* plan);
  * the weight stream keeps running ahead across stage boundaries.
  *
  * A linked plan knows projections only.  What lies between them (attention
- * and the norm and rotation before it have entry points of their own, under
- * or below; activation functions and residual adds are outside this library)
+ * and the norm and rotation before it have entry points of their own further
+ * down; activation functions and residual adds are outside this library)
  * is not part of the launch; the plainest stand-in is kept: the activation of
  * a dependent matrix is alpha times a prefix of an earlier matrix's output. */
 typedef enum {

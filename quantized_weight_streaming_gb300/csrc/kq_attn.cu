@@ -42,9 +42,8 @@
 // workspace; a second launch joins them in a fixed order.
 //
 // Measured (a replayed graph, both launches, 4 of them its own): 64 requests of
-// 16384 tokens, 24 query and 4 key heads of 256, fp16: 273 us, 1.21 GB of
-// cache; 32 ragged requests of 8000 on average, 32 and 8 heads of 128, bf16:
-// 51 us, 143 MB; 4 requests of 8 new tokens, fp32: 41 us.  The large ones move
+// 16384 tokens, 24 query and 4 key heads of 256, fp16: 273 us, 1.21 GB of cache; 32 ragged requests of up to 8000, 32 and 8 heads of 128, bf16: 51 us,
+// 143 MB; 8 requests of 4 new tokens on 4100, fp32: 41 us.  The large ones move
 // 4.5 (D = 256) and 5.4 TB/s (D = 128) once they run, behind 12 us of finding
 // the runs, first copies, and joining.  Instructions bound them, not bytes: 51
 // to 55% of the issue slots taken with three warps a scheduler, tensor pipe 29
