@@ -554,7 +554,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
                 if (!(see >> e & 1u)) s[c][e] = 0xFF800000u;  // -inf
             }
           }
-          auto largest = [&]() {  // of the row's scores, log2
+          // Of the row's scores, log2.  (Needed in a row's first tile and when the reference moves: without the fence the
+          // compiler worked it out before the branches, 61 of a tile's 430 instructions.)
+          auto largest = [&]() {
+            asm volatile("" : "+r"(s[0][0]));
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < 32; ++e)
