@@ -41,14 +41,15 @@
 // wait for one another.  A row cut between warps leaves partial sums in the
 // workspace; a second launch joins them in a fixed order.
 //
-// Measured (a replayed graph, both launches, 4 of them its own): 64 requests of
-// 16384 tokens, 24 query and 4 key heads of 256, fp16: 273 us, 1.21 GB of cache; 32 ragged requests of up to 8000, 32 and 8 heads of 128, bf16: 51 us,
-// 143 MB; 8 requests of 4 new tokens on 4100, fp32: 41 us.  The large ones move
-// 4.5 (D = 256) and 5.4 TB/s (D = 128) once they run, behind 12 us of finding
+// Measured (a replayed graph, both launches, 4 us of them its own): 64 requests
+// of 16384 tokens, 24 query and 4 key heads of 256, fp16: 266 us, 1.21 GB of
+// cache; 32 ragged requests of up to 8000, 32 and 8 heads of 128, bf16: 50 us,
+// 143 MB; 8 requests of 4 new tokens on 4100, fp32: 40 us.  The large ones move
+// 4.6 (D = 256) and 5.4 TB/s (D = 128) once they run, behind 12 us of finding
 // the runs, first copies, and joining.  Instructions bound them, not bytes: 51
-// to 55% of the issue slots taken with three warps a scheduler, tensor pipe 29
-// to 34%; per word of eight codes there are five to unpack, and the zero
-// points, scales and softmax.
+// to 55% of the issue slots taken (with three warps a scheduler; a fourth gave
+// 2%), tensor pipe 29 to 34%; per word of eight codes there are five to unpack,
+// and the zero points, scales and softmax.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -80,12 +81,13 @@ constexpr int kLeastRun = 1;
 template <typename T, int D>
 struct Config {
   static constexpr bool kSplit = sizeof(T) == 4;        // two fp16 parts
-  // Consumer warps; with the copying warp two or three a scheduler, 255 or 168 registers.  At D = 256 the queries of
-  // 16-bit rows lie in shared memory (read once a tile), for three: sums and queries in registers leave room for two,
-  // which kept 4.5 TB/s busy.
+  // Consumer warps; with the copying warp four a scheduler and 128 registers for 16-bit queries, three and 168 or two and
+  // 255 for fp32.  (Three a scheduler with 16-bit queries: 64 requests of 16384 tokens, 4 key heads of 256, took 273 us
+  // instead of 266, and 32 ragged ones on 8 heads of 128 51.5 instead of 50.7.)  At D = 256 the queries of 16-bit rows lie
+  // in shared memory, read once a tile: sums and queries in registers leave room for two, 283 us.
   static constexpr bool kQShared = D == 256 && !kSplit;
-  static constexpr int kWarps = (D == 256 && !kQShared ? 8 : 12) - 1;
-  static constexpr int kStages = kQShared ? 3 : (kWarps < 8 ? 6 : 4);
+  static constexpr int kWarps = (!kSplit ? 16 : (D == 256 ? 8 : 12)) - 1;
+  static constexpr int kStages = kQShared ? 2 : (kWarps > 11 ? 3 : (kWarps < 8 ? 6 : 4));  // what fits beside them
   static constexpr int kQueries = kQShared ? kWarps * (D / 32) * 512 : 0;  // bytes
   static constexpr int kTileGranules = 256 / D;
   static constexpr int kTile = kTileGranules * kGranule;  // keys
@@ -97,7 +99,7 @@ struct Config {
 };
 // D = 256: one granule of 4608 bytes; 128: two; 64: four.
 
-constexpr int kMaxWarps = 11;
+constexpr int kMaxWarps = 15;
 // Floats of a partial result: 8 rows x D sums, 8 references, 8 weights.
 constexpr int64_t partial_floats(int d) { return kRows * (int64_t)d + 2 * kRows; }
 template <int D>
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
     enter();
     // The lanes stay together: whichever find a free stage issue a tile, and only where none does the warp sleeps.  (With
     // a wait per lane the slowest consumer held up all the others' copies; and a tile's own arithmetic has to stay
-    // short, or its stage comes back late: 11 or 7 lanes share the warp.)
+    // short, or its stage comes back late: up to 15 lanes share the warp.)
     long long since = clock64();
     while (__any_sync(~0u, more)) {
       const int st = made % C::kStages;
@@ -785,8 +787,12 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
   __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_dependency_wait();
-  allow_dependent_launch();
+  // (What the call was given may be read before the launch in front is done: that one let this one start after all
+  // before it were.)
+  auto launches_before = []() {
+    grid_dependency_wait();
+    allow_dependent_launch();
+  };
   auto row_out = [&](const Request& q, int h, int32_t x) {
     return static_cast<T*>(a.out) + (int64_t)(q.first + x / a.group) * a.out_token +
            (int64_t)(h * a.group + x % a.group) * a.out_head;
@@ -797,6 +803,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     const int slice = (int)(tile % slices), h = (int)(tile / slices % a.cache.kv_heads);
     const int64_t r = tile / slices / a.cache.kv_heads;
     const Request q = request_of(a, r, C::kTile);
+    launches_before();
     const int first = part * rows_per_cta;
     const int32_t x0 = slice * kRows + first;
     if (q.rows > a.few_rows || x0 >= q.rows) return;
@@ -835,6 +842,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     store_row<T, kPer>(row_out(q, h, x0 + in) + lane * kPer, s.acc, s.weight == 0.f ? 0.f : kOut<T, D> / s.weight);
     return;
   }
+  launches_before();
   const int64_t at = blockIdx.x - few_ctas;
   if (at < (int64_t)kJoinSlices<D> * (kSms - 1)) {
     const int64_t b = at / kJoinSlices<D> + 1;
