@@ -787,8 +787,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
   __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // (What the call was given may be read before the launch in front is done: that one let this one start after all
-  // before it were.)
+  // (What the call was given may be read before the launch in front is done, from L2: that one let this one start after
+  // all before it were.)
   auto launches_before = []() {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     const int64_t tile = blockIdx.x / per_tile;
     const int slice = (int)(tile % slices), h = (int)(tile / slices % a.cache.kv_heads);
     const int64_t r = tile / slices / a.cache.kv_heads;
-    const Request q = request_of(a, r, C::kTile);
+    const Request q = request_of<true>(a, r, C::kTile);
     launches_before();
     const int first = part * rows_per_cta;
     const int32_t x0 = slice * kRows + first;

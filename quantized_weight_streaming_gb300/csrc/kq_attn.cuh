@@ -57,11 +57,14 @@ struct Request {
   int32_t rows;          // query rows of one key head
 };
 
+// kFromL2: read past the SM's own cache.
+template <bool kFromL2 = false>
 __device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile, bool* out_of_range = nullptr) {
+  auto load = [](const int32_t* p) { return kFromL2 ? __ldcg(p) : *p; };
   Request q;
-  q.first = a.q_start[r];
-  const int32_t end = a.q_start[r + 1];
-  int32_t len = a.kv_len[r];
+  q.first = load(a.q_start + r);
+  const int32_t end = load(a.q_start + r + 1);
+  int32_t len = load(a.kv_len + r);
   const int64_t room = a.table_stride * a.cache.page_size;
   bool bad = len < 0 || len > room;
   q.n = end - q.first;

@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
                        : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
+#pragma unroll 2
         for (int it = 0; it < kLanes; ++it) {
           const int rr = (warp & 3) * 32 + it * kAtOnce + sub;
           uint4* place = reinterpret_cast<uint4*>(tile + rr * 128 + (((l % 8) ^ (rr & 7)) << 4));
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
               *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) << 4)) = v;
             }
             __syncwarp();
-#pragma unroll 2
+#pragma unroll 8
             for (int it = 0; it < 8; ++it) {
               const int rr = 4 * it + lane / 8, in = m_tile * 128 + (warp & 3) * 32 + rr, e = lane & 7;
               const float4 v = *reinterpret_cast<const float4*>(turn + rr * 128 + ((e ^ (rr & 7)) << 4));
