@@ -87,7 +87,7 @@ struct PromptShape {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = 64;
   // A row (a block of query rows of one key head) counts as its key tiles and so many units before them: fetching the
-  // queries and putting the rows away cost about 15000 cycles, a tile 1800 to 2400.  (Counted by tiles alone, ragged
+  // queries and putting the rows away cost about 15000 cycles, a tile 1900.  (Counted by tiles alone, ragged
   // prompts left CTAs with nine short rows, 176000 cycles, beside others with two, 72000.)
   static constexpr int kRowCost = 8;
   static constexpr int kLeastRun = 12;                // units of a run

@@ -35,7 +35,7 @@
 // (378 us with the unpacking loops unrolled, 266 without).
 //
 // Measured: the last 2048 of 8192 tokens, 32 query and 8 key heads of 128,
-// bf16: 260 to 266 us, 905 to 925 TFLOP/s of what the mask leaves.  Issue slots
+// bf16: 251 to 261 us, 920 to 957 TFLOP/s of what the mask leaves.  Issue slots
 // bound it (64% taken; tensor pipe 40%): unpacking, which each row block does
 // anew, and the softmax.  Rounding K, V and P to fp16 costs rows of fp16 output
 // an error of 3.6e-4 where rounding the output alone costs 2.1e-4.
