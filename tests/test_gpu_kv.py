@@ -424,6 +424,21 @@ def test_attention_long_prompt_in_many_parts(kq, dt, hq, hk, d, page):
     s.check(window=700)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 1, 256), (7, 1, 64), (41, 1, 128), (65, 1, 64), (48, 1, 256)])
+def test_attention_on_both_sides_of_the_change_of_kernels(kq, dt, hq, hk, d):
+    """Requests of a few more and a few less than 40 or 64 query rows a key head, in one call and each alone; one key head
+    for so many query heads that a single token has them."""
+    rng = np.random.default_rng(23 + hq + d)
+    new = np.array([6, 7, 9, 10, 11, 1])
+    lens = np.array([6, 90, 300, 33, 1000, 513])
+    s = Step(kq, rng, lens, new, hq, hk, d, 32, dt)
+    s.check()
+    s.check(window=8)
+    for n, length in ((1, 1), (1, 700), (10, 200), (11, 200)):
+        Step(kq, rng, [length], [n], hq, hk, d, 16, dt).check()
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 def test_attention_mixed_batch(kq, dt):
     """Single tokens, drafts, prompts and idle requests in one call; more of them than a CTA has threads."""
