@@ -87,10 +87,12 @@ struct PromptShape {
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = 64;
   // A row (a block of query rows of one key head) counts as its key tiles and so many units before them: fetching the
-  // queries and putting the rows away cost about 15000 cycles, a tile 1900.  (Counted by tiles alone, ragged
-  // prompts left CTAs with nine short rows, 176000 cycles, beside others with two, 72000.)
-  static constexpr int kRowCost = 8;
-  static constexpr int kLeastRun = 12;                // units of a run
+  // queries and putting the rows away cost 15000 to 18000 cycles, a tile 1900.  (Counted by tiles alone, ragged prompts
+  // left CTAs with nine short rows, 176000 cycles, beside others with two, 72000.  6 ragged prompts of up to 700 of 1500
+  // tokens, 8 key heads of 128: 90.9 us with six units, 84.5 with ten, 89.2 with 14.)
+  static constexpr int kRowCost = 10;
+  // Units of a run: two tiles.  The last 300 of 2000 tokens: 43.2 us; with twelve more units a run 9 us more.
+  static constexpr int kLeastRun = kRowCost + 2;
   __device__ static int32_t units(int32_t tiles) { return tiles ? tiles + kRowCost : 0; }
   static constexpr int64_t kPartial = kRows * (int64_t)(D + 2);
 };
