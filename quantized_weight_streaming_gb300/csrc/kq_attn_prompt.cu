@@ -66,6 +66,7 @@ __device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_sta
 constexpr int kPromptWarps = 20, kPromptThreads = 32 * kPromptWarps;
 constexpr int kUnpackFirst = 12, kUnpackWarps = 4;  // two groups of them, a key tile in turn each
 constexpr float kPromptMost = 4096.f;  // times 8 (see above) still fits fp16
+constexpr float kCoarse = 16777216.f;  // 2^24: numbers from here on lie two or more apart
 constexpr int kInfos = 8;            // key tiles between unpacking and softmax, and more
 
 template <int D>
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           tmem_ld32(s_at, s[0]);
           tmem_ld32(s_at + 32, s[1]);
           const TileInfo info = s_info[slot];
-          const float f = factor * info.key_scale;
+          float f = factor * info.key_scale;
           const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
           tmem_ld_wait();
           if (info.hidden || key0 < all_lo || key0 + N > all_hi) {
@@ -569,11 +570,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
             if (ref == -INFINITY) ref = top;
           }
           // p = 2^(f S - ref).  The reference stays while a tile's p add up to less than 2^12 (each then fits fp16): the
-          // exponentials wait for no maximum.
+          // exponentials wait for no maximum.  f S - ref is rounded once, so a reference that is the row's own largest
+          // score, rounded, leaves that one 2^r, r what its rounding took: a fraction, but from 2^28 on r passes 12
+          // either way, and p overflows or the row's weight vanishes.  From 2^24 on the scores are therefore rounded as
+          // the reference was, before the subtraction; the largest p is then 1.  After a move every p is 2 at most, so
+          // there is no third round.
           uint32_t p[32];
           float2 acc;
-          while (true) {
+#pragma unroll 1
+          for (int round = 0;; ++round) {
             const float minus = ref == -INFINITY ? 0.f : -ref;
+            if (fabsf(minus) >= kCoarse) {
+#pragma unroll
+              for (int e = 0; e < 64; ++e) s[e / 32][e % 32] = __float_as_uint(__uint_as_float(s[e / 32][e % 32]) * f);
+              f = 1.f;
+            }
             float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
@@ -585,7 +596,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
             }
             acc = add2(sums[0], sums[1]);
             const bool moves = acc.x + acc.y > kPromptMost;
-            if (!__any_sync(~0u, moves)) break;
+            if (round == 1 || !__any_sync(~0u, moves)) break;
             const float top = largest(), keep = moves ? exp2_approx(ref - top) : 1.f;
             if (moves) ref = top;
             weight *= keep;

@@ -1,0 +1,95 @@
+"""GPU checks of the attention-step operators at the far ends of what they take:
+scores beyond fp32's whole numbers, pages and lengths near 31 bits, windows as
+long as an int, grids that the caller's bounds make large, and the paths that
+only long prompts reach.  Statements and tolerances are those of test_gpu_kv.py
+unless a test says otherwise."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+import kv_reference as ref  # noqa: E402
+from test_gpu_kv import ATTN_TOL, Step, dev, f64, ints, kq, near, status  # noqa: E402,F401
+
+
+def repack(s):
+    s.cache.data.copy_(dev(ref.pack(s.kc, s.ks, s.vc, s.vs)))
+
+
+# ---- scores of any size ---------------------------------------------------------------
+
+
+def _one_key_rows(s, window=0):
+    """(rows whose largest score stands out, the value row of that key): FP64 scores a fraction 2^-16 of the row's largest
+    magnitude apart, 16 times what fp32 products of exact operands can lose.  Where that is 100 or more, every other key's
+    weight is below 2^-100 and the output is the key's value."""
+    group = s.hq // s.kc.shape[1]
+    k, v = (np.nan_to_num(ref.values(c, x)) for c, x in ((s.kc, s.ks), (s.vc, s.vs)))
+    q = f64(s.q)
+    stands, want = np.zeros(q.shape[:2], bool), np.zeros(q.shape)
+    for r, total in enumerate(s.kv_len):
+        at = np.arange(total)
+        kk, vv = (x[s.table[r, at // s.page], :, at % s.page] for x in (k, v))
+        lo, hi = s.q_start[r], s.q_start[r + 1]
+        for t in range(lo, hi):
+            pos = total - (hi - lo) + (t - lo)
+            first = max(0, pos - window + 1) if window else 0
+            for h in range(s.hq):
+                e = s.scale * (kk[first: pos + 1, h // group] @ q[t, h])
+                order = np.argsort(e)
+                gap = e[order[-1]] - e[order[-2]] if len(e) > 1 else np.inf
+                stands[t, h] = gap > max(100.0, 2.0**-16 * np.abs(e).max())
+                want[t, h] = vv[first + order[-1], h // group]
+    return stands, want
+
+
+def _large(kq, rng, dt, hq, hk, d, size, side, new, lens):
+    """A step whose scores are `size` and more: key scales powers of two (their products with codes are exact in fp16);
+    `side` 1 or -1: every score of that sign."""
+    s = Step(kq, rng, lens, new, hq, hk, d, 32, dt)
+    s.ks = np.where(np.isnan(s.ks), s.ks, np.sign(s.ks) * np.float16(0.25))
+    if side:
+        s.ks = np.abs(s.ks)
+        s.kc = np.maximum(s.kc, 9)
+        s.q = (s.q.abs() * side).contiguous()
+    if dt == "f16":
+        s.scale *= size
+    else:
+        s.q = (s.q.float() * size).to(s.q.dtype)
+    repack(s)
+    return s
+
+
+@pytest.mark.parametrize("side", [0, 1, -1])
+@pytest.mark.parametrize("dt,size", [("bf16", 1e7), ("bf16", 1e8), ("bf16", 3e8), ("bf16", 1e12), ("bf16", 1e30), ("f16", 1e8), ("f16", 1e20)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 1, 256), (14, 2, 64)])
+def test_prompt_of_very_large_scores(kq, hq, hk, d, dt, size, side):
+    """The softmax of 16-bit prompts ends and stays finite whatever the scores' size; where one key stands out, its value
+    is the output."""
+    rng = np.random.default_rng(31 + d)
+    s = _large(kq, rng, dt, hq, hk, d, size, side, [70, 45], [170, 45])
+    for window in (0, 30):
+        out = f64(s.run(window))
+        assert status(kq) == kq.KQ_OK
+        assert np.all(np.isfinite(out))
+        stands, want = _one_key_rows(s, window)
+        assert stands.mean() > 0.5
+        near(out[stands], want[stands], dt)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 1, 256), (14, 2, 64)])
+def test_prompt_of_non_finite_queries_stays_in_its_rows(kq, dt, hq, hk, d):
+    rng = np.random.default_rng(32 + d)
+    s = Step(kq, rng, [300, 90], [100, 60], hq, hk, d, 32, dt)
+    a = s.check()
+    bad = torch.zeros(a.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h, e, x in ((0, 3, 5, "nan"), (37, 0, 0, "inf"), (99, hq - 1, d - 1, "-inf"), (150, 1, 7, "nan")):
+        s.q[t, h, e] = float(x)
+        bad[t, h] = True
+    b = s.run()
+    assert status(kq) == kq.KQ_OK
+    assert torch.equal(a[~bad], b[~bad])
+    assert not torch.any(torch.isfinite(b[bad]))
