@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
         at = page;
         next = page + 1 < pages ? row[page + 1] : -1;
       }
-      if (id >= 0 && id < a.cache.pages) return head + id * page_bytes + sub * L::kBytes;
+      if (id >= 0 && id < a.cache.pages) return head + id * page_bytes + (int64_t)sub * L::kBytes;
       const int32_t key = (page * per_page + sub) * kGranule;
       if (key < cur.q.len && key + (in_one ? C::kTile : kGranule) > cur.q.lo) attn_flag(KQ_ERR_RANGE);
       return nullptr;  // (a page below a sliding window may be gone)

@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           if (here)
             bulk_g2s(smem + C::kRawAt + st * C::kRaw + lane * L::kBytes,
                      a.cache.data + ((int64_t)id * a.cache.kv_heads + w.at.h) * a.cache.block_bytes +
-                         (granule % per_page) * L::kBytes,
+                         (int64_t)(granule % per_page) * L::kBytes,
                      L::kBytes, &raw_full[st], policy);
         }
       } else if (warp == 1 || (warp == 3 && C::kTiles == 2)) {

@@ -431,7 +431,8 @@ __device__ __forceinline__ void put_row(uint8_t* granule, int token, bool key, u
 template <int D>
 __device__ __forceinline__ uint8_t* granule_of(const Cache& c, int32_t slot, int h) {
   const int32_t page = slot / c.page_size, in_page = slot - page * c.page_size;
-  return c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes + (in_page / kGranule) * Layout<D>::kBytes;
+  return c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes +
+         (int64_t)(in_page / kGranule) * Layout<D>::kBytes;
 }
 __device__ __forceinline__ int32_t slot_of(const QkArgs& a, int64_t t) {
   const int32_t slot = a.slots[t];
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kQkThreads) read_kernel(Cache c, const int32_t
   if (slot >= 0) {
     const int page = slot / c.page_size, in_page = slot - page * c.page_size, tok = in_page % kGranule;
     const uint8_t* g =
-        c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes + (in_page / kGranule) * L::kBytes;
+        c.data + ((int64_t)page * c.kv_heads + h) * c.block_bytes + (int64_t)(in_page / kGranule) * L::kBytes;
     const uint32_t kw = *reinterpret_cast<const uint32_t*>(g + L::key_word(tok, l));
     const uint32_t vw = *reinterpret_cast<const uint16_t*>(g + L::value_unit(tok, 2 * l)) |
                         (uint32_t)*reinterpret_cast<const uint16_t*>(g + L::value_unit(tok, 2 * l + 1)) << 16;

@@ -93,3 +93,38 @@ def test_prompt_of_non_finite_queries_stays_in_its_rows(kq, dt, hq, hk, d):
     assert status(kq) == kq.KQ_OK
     assert torch.equal(a[~bad], b[~bad])
     assert not torch.any(torch.isfinite(b[bad]))
+
+
+# ---- pages and lengths near 31 bits -------------------------------------------------------
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_page_of_more_than_2_31_bytes(kq, d):
+    """One page whose granules pass 32-bit byte offsets, as where a cache is used as one contiguous block: the write
+    (row by row and by windows), reading back, and both attention kernels, at its last slots."""
+    rng = np.random.default_rng(41 + d)
+    page = 16 * ((1 << 31) // (18 * d) + 100)
+    cache = kq.KVCache(1, page, 1, d)
+    assert cache.data.numel() > 1 << 31
+    p = kq.QKNorm(4, 1, d, norm=False)
+    for n in (30, 20000):  # 20000: more than 4 windows an SM
+        x = dev(rng.standard_normal((2, n, 1, d)).astype(np.float32))
+        small = kq.KVCache(-(-n // 16), 16, 1, d)
+        kq.kq_kv_append(p, small, None, x[0], x[1], None, ints(np.arange(n)), None)
+        slots = ints(page - n + np.arange(n))
+        kq.kq_kv_append(p, cache, None, x[0], x[1], None, slots, None)
+        got, want = (torch.empty(2, n, 1, d, device="cuda") for _ in range(2))
+        kq.kq_kv_read(cache, slots, got[0], got[1])
+        kq.kq_kv_read(small, ints(np.arange(n)), want[0], want[1])
+        assert status(kq) == kq.KQ_OK
+        assert torch.equal(got, want)
+    k, v = f64(got)  # [n, 1, d]
+    for dt, new, window in (("f32", 1, 400), ("bf16", 2, 33), ("bf16", 60, 100)):
+        q = dev(rng.standard_normal((new, 4, d)).astype(np.float32)).to({"f32": torch.float32, "bf16": torch.bfloat16}[dt])
+        out = torch.empty_like(q)
+        ws = torch.empty(kq.kq_attn_workspace_bytes(cache, 4, 1, new, new), dtype=torch.uint8, device="cuda")
+        kq.kq_attn_paged(cache, q, ints([0, new]), ints([page]), ints([[0]]), out, d ** -0.5, new, window=window, ws=ws)
+        assert status(kq) == kq.KQ_OK
+        want = ref.attention(f64(q), k.transpose(1, 0, 2)[None], v.transpose(1, 0, 2)[None], [0, new], [n], np.array([[0]]),
+                             n, d ** -0.5, window)
+        near(f64(out), want, dt)
