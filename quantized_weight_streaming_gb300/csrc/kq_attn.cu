@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       left = (int32_t)min((int64_t)(min(cur.need_hi, cur.q.tiles) - cur.tile), cur.end - cur.unit);
       if (cur.r != row_of) {
         row_of = cur.r, row = a.table + cur.r * a.table_stride, at = -1;
-        pages = (cur.q.len + a.cache.page_size - 1) / a.cache.page_size;  // the table's row holds them
+        pages = pages_of(cur.q.len, a.cache.page_size);  // the table's row holds them
       }
       const int32_t g0 = (cur.q.tile0 + cur.tile) * C::kTileGranules;
       page = g0 / per_page, sub = g0 - page * per_page;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       }
       if (id >= 0 && id < a.cache.pages) return head + id * page_bytes + (int64_t)sub * L::kBytes;
       const int32_t key = (page * per_page + sub) * kGranule;
-      if (key < cur.q.len && key + (in_one ? C::kTile : kGranule) > cur.q.lo) attn_flag(KQ_ERR_RANGE);
+      if (key < cur.q.len && key > cur.q.lo - (in_one ? C::kTile : kGranule)) attn_flag(KQ_ERR_RANGE);
       return nullptr;  // (a page below a sliding window may be gone)
     };
     enter();
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       const int32_t key0 = (c.q.tile0 + t) * C::kTile;
       const uint32_t bad = hidden[st];
       const uint8_t* stage = ring + st * C::kStageBytes;
-      if (bad || key0 < c.all_lo || key0 + C::kTile > c.all_hi)
+      if (bad || key0 < c.all_lo || key0 > c.all_hi - C::kTile)
         attend_tile<T, D, true>(w, exponent, stage, key0, bad, c, queries);
       else
         attend_tile<T, D, false>(w, exponent, stage, key0, 0, c, queries);

@@ -80,6 +80,10 @@ __device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile
   return q;
 }
 
+// Pages of `len` keys.  (Lengths go up to 2^31 - 1: neither this sum nor the end of the last key tile fits 32 bits, so
+// tiles are compared by their first key.)
+__device__ __forceinline__ int32_t pages_of(int32_t len, int32_t page_size) { return len / page_size + (len % page_size != 0); }
+
 // The prompt kernel's row blocks and key tiles (kq_attn_prompt.cu).
 template <int D>
 struct PromptShape {

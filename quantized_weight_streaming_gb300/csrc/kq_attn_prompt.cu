@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           float f = factor * info.key_scale;
           const int32_t rel_lo = key_lo - key0, rel_hi = key_hi - key0;
           tmem_ld_wait();
-          if (info.hidden || key0 < all_lo || key0 + N > all_hi) {
+          if (info.hidden || key0 < all_lo || key0 > all_hi - N) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const uint32_t see = visible(rel_lo - 32 * c, rel_hi - 32 * c) & ~hidden_keys(info.hidden, 32 * c);
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
         // ---- copies ----
         const uint64_t policy = l2_policy_evict_first();
         const int per_page = a.cache.page_size / kGranule;
-        const int32_t pages = (w.q.len + a.cache.page_size - 1) / a.cache.page_size;
+        const int32_t pages = pages_of(w.q.len, a.cache.page_size);
         const int32_t* table = a.table + w.at.r * a.table_stride;
         auto page_id = [&](int32_t t) -> int32_t {
           const int32_t page = ((w.blk.tile0 + t) * C::kGranules + lane) / per_page;
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           if (raws >= C::kStages) gate.wait(&raw_empty[st], (raws / C::kStages - 1) & 1);
           const int32_t granule = (w.blk.tile0 + t) * C::kGranules + lane, key = granule * kGranule;
           const bool here = lane < C::kGranules && id >= 0 && id < a.cache.pages;
-          if (lane < C::kGranules && !here && key < w.blk.hi && key + kGranule > w.blk.lo) prompt_flag(KQ_ERR_RANGE);
+          if (lane < C::kGranules && !here && key < w.blk.hi && key > w.blk.lo - kGranule) prompt_flag(KQ_ERR_RANGE);
           const uint32_t have = __ballot_sync(~0u, here);
           if (lane == 0) {
             s_hidden[st] = ~have & ((1u << C::kGranules) - 1);
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
           __syncwarp();
           const uint32_t hidden = s_hidden[st];
           const int32_t key0 = (w.blk.tile0 + t) * N;
-          const bool dirty = hidden || key0 < w.blk.lo || key0 + N > w.blk.hi;
+          const bool dirty = hidden || key0 < w.blk.lo || key0 > w.blk.hi - N;
           uint32_t top[2] = {0, 0};  // the largest of the keys', of the values', as bits: NaN above infinity above the numbers
 #pragma unroll
           for (int e = 0; e < C::kGranules * 2 * D / 128; ++e) {

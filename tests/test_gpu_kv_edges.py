@@ -128,3 +128,31 @@ def test_page_of_more_than_2_31_bytes(kq, d):
         want = ref.attention(f64(q), k.transpose(1, 0, 2)[None], v.transpose(1, 0, 2)[None], [0, new], [n], np.array([[0]]),
                              n, d ** -0.5, window)
         near(f64(out), want, dt)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_lengths_up_to_2_31(kq, d):
+    """Requests of 2^31 - 1 and a few less keys (a table that names one page again and again), seen through a window; the
+    slots behind the length and before the window hold NaN."""
+    rng = np.random.default_rng(42)
+    page, window = 1 << 20, 90
+    kc, vc = (rng.integers(0, 16, (1, 1, page, d)).astype(np.uint8) for _ in range(2))
+    ks, vs = (rng.uniform(0.05, 0.4, (1, 1, page, d // 32)).astype(np.float16) for _ in range(2))
+    ks[:, :, : page - 400] = vs[:, :, : page - 400] = np.nan
+    for length in ((1 << 31) - 1, (1 << 31) - 17, (1 << 31) - 64):
+        cut = page - ((1 << 31) - length)
+        s = [x.copy() for x in (ks, vs)]
+        for x in s:
+            x[:, :, cut:] = np.nan
+        cache = kq.KVCache(1, page, 1, d, data=dev(ref.pack(kc, s[0], vc, s[1])))
+        table = torch.zeros(1, 2048, dtype=torch.int32, device="cuda")
+        k, v = (ref.values(c, x)[:, :, cut - 300: cut] for c, x in zip((kc, vc), s))
+        for dt, new in (("f32", 1), ("f16", 2), ("bf16", 130)):
+            q = dev(rng.standard_normal((new, 4, d)).astype(np.float32)).to(
+                {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dt])
+            out = torch.empty_like(q)
+            ws = torch.empty(kq.kq_attn_workspace_bytes(cache, 4, 1, new, new), dtype=torch.uint8, device="cuda")
+            kq.kq_attn_paged(cache, q, ints([0, new]), ints([length]), table, out, d ** -0.5, new, window=window, ws=ws)
+            assert status(kq) == kq.KQ_OK
+            want = ref.attention(f64(q), k, v, [0, new], [300], np.array([[0]]), 300, d ** -0.5, window)
+            near(f64(out), want, dt)
