@@ -381,7 +381,7 @@ __device__ __forceinline__ void enter_row(const Args& a, Cursor& c) {
   const int32_t x = c.row % row_tiles(c.q) * kRows;
   const int32_t i0 = x / a.group, i1 = min(c.q.n - 1, (x + kRows - 1) / a.group);
   const int32_t hi = min(c.q.len, c.q.pos0 + i1 + 1);
-  const int32_t lo = a.window ? max(0, c.q.pos0 + i0 - (a.window - 1)) : 0;
+  const int32_t lo = first_key(a, c.q.pos0 + i0);
   c.need_lo = lo / kTile - c.q.tile0;
   c.need_hi = hi > lo ? (hi - 1) / kTile + 1 - c.q.tile0 : 0;
 }
@@ -420,7 +420,7 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
   const bool live = i < cur.q.n;
   const int32_t pos = cur.q.pos0 + i;
   // rows past the last one hold zeros and see everything: they never ask for the masked path
-  w.key_lo = live ? (a.window ? max(0, pos - (a.window - 1)) : 0) : 0;
+  w.key_lo = live ? first_key(a, pos) : 0;
   w.key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
   cur.all_lo = __reduce_max_sync(~0u, w.key_lo), cur.all_hi = __reduce_min_sync(~0u, w.key_hi);
   cur.any_lo = __reduce_min_sync(~0u, live ? w.key_lo : 0x7fffffff);

@@ -57,6 +57,11 @@ struct Request {
   int32_t rows;          // query rows of one key head
 };
 
+// First key that a token at `pos` sees.  (pos - (window - 1) would pass -2^31 for a negative position and the longest window.)
+__device__ __forceinline__ int32_t first_key(const Args& a, int32_t pos) {
+  return a.window ? max(0, max(pos, 0) - (a.window - 1)) : 0;
+}
+
 // kFromL2: read past the SM's own cache.
 template <bool kFromL2 = false>
 __device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile, bool* out_of_range = nullptr) {
@@ -72,7 +77,7 @@ __device__ __forceinline__ Request request_of(const Args& a, int64_t r, int tile
   len = max(len, 0);
   q.pos0 = len - q.n;
   q.len = (int32_t)min((int64_t)len, room);
-  q.lo = a.window ? max(0, max(q.pos0, 0) - (a.window - 1)) : 0;
+  q.lo = first_key(a, q.pos0);
   q.tile0 = q.lo / tile;
   q.tiles = q.n > 0 && q.len > q.lo ? (q.len - 1) / tile - q.tile0 + 1 : 0;
   q.rows = (int32_t)min((int64_t)0x7fffffff, (int64_t)q.n * a.group);
@@ -114,7 +119,7 @@ __device__ __forceinline__ RowBlock row_block(const Args& a, const Request& q, i
   b.rows = min(S::kRows, q.rows - x0);
   const int32_t i0 = x0 / a.group, i1 = (x0 + b.rows - 1) / a.group;
   b.hi = min(q.len, q.pos0 + i1 + 1);
-  b.lo = a.window ? max(0, q.pos0 + i0 - (a.window - 1)) : 0;
+  b.lo = first_key(a, q.pos0 + i0);
   b.tile0 = b.lo / S::kKeys;
   b.tiles = b.hi > b.lo ? (b.hi - 1) / S::kKeys - b.tile0 + 1 : 0;
   return b;

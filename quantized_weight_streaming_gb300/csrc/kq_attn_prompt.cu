@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(Args a) {
       const bool live = m_tile * 128 + row < w.blk.rows;
       const int32_t pos = w.q.pos0 + i;
       const int32_t key_hi = live ? max(0, min(pos + 1, w.q.len)) : 0x7fffffff;
-      const int32_t key_lo = live && a.window ? max(0, pos - (a.window - 1)) : 0;
+      const int32_t key_lo = live ? first_key(a, pos) : 0;
       // A row's D / 8 lanes load it, eight dimensions each; the factor then goes to the row's own thread.  (The scale's
       // sign goes with the queries, so that larger sums are larger scores.)
       const int32_t token0 = w.q.first + w.at.k * C::kRows / a.group, head0 = w.at.k * C::kRows % a.group;

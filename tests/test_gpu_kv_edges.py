@@ -156,3 +156,15 @@ def test_lengths_up_to_2_31(kq, d):
             assert status(kq) == kq.KQ_OK
             want = ref.attention(f64(q), k, v, [0, new], [300], np.array([[0]]), 300, d ** -0.5, window)
             near(f64(out), want, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 128), (14, 2, 64), (6, 1, 256), (2, 2, 128)])
+def test_longest_windows_over_requests_of_more_tokens_than_keys(kq, dt, hq, hk, d):
+    """A window of 2^31 - 1 keys and more is no window, also where a request's first tokens stand before its first key."""
+    rng = np.random.default_rng(43 + d)
+    s = Step(kq, rng, [5, 100, 1, 40, 0], [6, 150, 90, 41, 3], hq, hk, d, 32, dt)
+    for window in ((1 << 31) - 1, (1 << 31) - 2, 1 << 40):
+        s.check(window=window)
+    few = Step(kq, rng, [5, 3, 1], [11, 7, 2], hq, hk, d, 32, dt)
+    few.check(window=(1 << 31) - 1)
