@@ -585,6 +585,10 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(QkArgs a, uint32_t row_c
     if (key && slot >= 0 && a.rope_dim) rope_row(a, t, threadIdx.x % kLanes == 0, entry);
     float x[8];
     cache_row<T, D>(a, key, entry, load_row<T, D>(a, key, t, h, slot >= 0), x);
+    if (slot < 0) {  // nothing is asked of a lane without a row (a norm with eps = 0 makes NaN of its zeros)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    }
     __half scale;
     const uint32_t codes = quantize_group(x, scale);
     if (slot >= 0) put_row<D>(granule_of<D>(a.cache, slot, h), slot % kGranule, key, codes, scale);

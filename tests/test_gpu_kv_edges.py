@@ -168,3 +168,23 @@ def test_longest_windows_over_requests_of_more_tokens_than_keys(kq, dt, hq, hk, 
         s.check(window=window)
     few = Step(kq, rng, [5, 3, 1], [11, 7, 2], hq, hk, d, 32, dt)
     few.check(window=(1 << 31) - 1)
+
+
+# ---- the cache write ----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_append_without_eps_reports_nothing_for_rows_that_are_not_there(kq, d):
+    """eps = 0 and no rotation: tokens that are skipped, and the lanes past the last token, are no zero rows to norm."""
+    rng = np.random.default_rng(51)
+    p = kq.QKNorm(2, 2, d, eps=0.0)
+    for n in (1, 3, 16, 41):
+        cache = kq.KVCache(8, 16, 2, d)
+        x = dev(rng.standard_normal((n, 2, d)).astype(np.float32))
+        slots = np.arange(n)
+        slots[n // 2] = -1
+        kq.kq_kv_append(p, cache, None, x, x, None, ints(slots), None)
+        assert status(kq) == kq.KQ_OK
+    x[:] = 0  # a zero row that is there: 0 / 0
+    kq.kq_kv_append(p, cache, None, x, x, None, ints(slots), None)
+    assert status(kq) == kq.KQ_ERR_NONFINITE
