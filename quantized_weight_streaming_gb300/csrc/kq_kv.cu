@@ -478,7 +478,7 @@ __device__ __forceinline__ void append_window(const QkArgs& a, int64_t t0, int h
     int32_t pos = in && a.rope_dim ? a.positions[t0 + tid] : -1;
     const int32_t slot = in ? slot_of(a, t0 + tid) : -1;
     if (pos >= a.rope_positions) pos = -1;
-    if (in && a.rope_dim && pos < 0) kv_flag(KQ_ERR_RANGE);
+    if (slot >= 0 && a.rope_dim && pos < 0) kv_flag(KQ_ERR_RANGE);
     const int32_t granule = slot < 0 ? -1 : slot / kGranule;
     const int32_t before = __shfl_up_sync(~0u, granule, 1);
     const uint32_t starts = __ballot_sync(~0u, granule >= 0 && (tid == 0 || before != granule));

@@ -188,3 +188,25 @@ def test_append_without_eps_reports_nothing_for_rows_that_are_not_there(kq, d):
     x[:] = 0  # a zero row that is there: 0 / 0
     kq.kq_kv_append(p, cache, None, x, x, None, ints(slots), None)
     assert status(kq) == kq.KQ_ERR_NONFINITE
+
+
+def test_append_of_skipped_tokens_asks_for_no_position(kq):
+    """Keys and values alone: a skipped token's position is not looked at, however many tokens there are; a written one's is,
+    and its key is zero."""
+    rng = np.random.default_rng(52)
+    hk, d = 64, 64
+    p = kq.QKNorm(hk, hk, d, d, None, None, dev(kq.kq_rope_table_host(10, d, 1e4)))
+    for n in (20, 330):  # 330: windows of tokens, more than four an SM
+        cache = kq.KVCache(24, 16, hk, d)
+        x = dev(rng.standard_normal((n, hk, d)).astype(np.float32))
+        slots, pos = np.arange(n), rng.integers(0, 10, n)
+        slots[[3, 11]] = -1
+        pos[[3, 11]] = -1, 10
+        kq.kq_kv_append(p, cache, None, x, x, ints(pos), ints(slots), None)
+        assert status(kq) == kq.KQ_OK
+        pos[7] = 10
+        kq.kq_kv_append(p, cache, None, x, x, ints(pos), ints(slots), None)
+        assert status(kq) == kq.KQ_ERR_RANGE
+        k, v = (torch.empty(n, hk, d, device="cuda") for _ in range(2))
+        kq.kq_kv_read(cache, ints(slots), k, v)
+        assert torch.all(k[7] == 0) and torch.all(k[8].abs().amax(-1) > 0) and torch.all(v[7].abs().amax(-1) > 0)
