@@ -556,8 +556,8 @@ int64_t kq_kv_block_bytes(int32_t page_size, int32_t head_dim);
  * total get position 0 and slot -1, which kq_kv_append skips.
  *  - All arrays int32, 16-byte aligned.  requests >= 1, tokens >= 0 (a step may
  *    have none), free_count >= 0 (d_free_pages may then be NULL).
- *  - On the device: a negative length counts as 0; new tokens past the
- *    capacity are dropped; a token whose page the free list or the table's row
+ *  - On the device: a negative length counts as 0; lengths and totals past
+ *    2^31 - 1 are cut to it; new tokens past the capacity are dropped; a token whose page the free list or the table's row
  *    cannot hold gets slot -1 (and -1 in the table where the row has room).
  *    Each sets KQ_ERR_RANGE for kq_device_status.
  *  - Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */

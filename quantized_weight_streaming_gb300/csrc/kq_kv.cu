@@ -40,6 +40,11 @@ struct SlotArgs {
   int32_t page_size;
 };
 
+// Sum of counts, held at 2^31 - 1: lengths that no cache holds then pass the capacity instead of wrapping around it.
+__device__ __forceinline__ int32_t sum_held(int32_t a, int32_t b) {
+  return (int32_t)min((uint32_t)a + (uint32_t)b, 0x7fffffffu);
+}
+
 __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
   __shared__ int32_t s_first[kScan + 1];  // first token of each request of the chunk
   __shared__ int32_t s_pages[kScan];      // pages taken before it
@@ -67,25 +72,27 @@ __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
       n[i] = min(max(n[i], 0), 0x7fffffff - c[i]);
       const int64_t end = (int64_t)c[i] + n[i];
       need[i] = (int32_t)((end + P - 1) / P - ((int64_t)c[i] + P - 1) / P);
-      sum.x += n[i];
-      sum.y += need[i];
+      sum.x = sum_held(sum.x, n[i]);
+      sum.y = sum_held(sum.y, need[i]);
     }
     int2 inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(~0u, inc.x, o), y = __shfl_up_sync(~0u, inc.y, o);
-      if (lane >= o) inc.x += x, inc.y += y;
+      if (lane >= o) inc.x = sum_held(inc.x, x), inc.y = sum_held(inc.y, y);
     }
+    int2 earlier = make_int2(__shfl_up_sync(~0u, inc.x, 1), __shfl_up_sync(~0u, inc.y, 1));  // the warp's lanes before
+    if (lane == 0) earlier = make_int2(0, 0);
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
     int2 before = make_int2(run_tokens, run_pages), total = before;
 #pragma unroll
     for (int w = 0; w < kScanThreads / 32; ++w) {
-      if (w < warp) before.x += s_warp[w].x, before.y += s_warp[w].y;
-      total.x += s_warp[w].x, total.y += s_warp[w].y;
+      total.x = sum_held(total.x, s_warp[w].x), total.y = sum_held(total.y, s_warp[w].y);
+      if (w + 1 == warp) before = total;
     }
-    before.x += inc.x - sum.x;
-    before.y += inc.y - sum.y;
+    before.x = sum_held(before.x, earlier.x);
+    before.y = sum_held(before.y, earlier.y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 4 * tid + i;
@@ -96,8 +103,8 @@ __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
         a.q_start[base + j] = before.x;
         a.kv_len[base + j] = c[i] + n[i];
       }
-      before.x += n[i];
-      before.y += need[i];
+      before.x = sum_held(before.x, n[i]);
+      before.y = sum_held(before.y, need[i]);
     }
     if (tid == kScanThreads - 1) s_first[kScan] = before.x;
     __syncthreads();
@@ -114,13 +121,13 @@ __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
       const int32_t old = (int32_t)(((int64_t)s_cached[l] + P - 1) / P), at = pos / P;
       int32_t* row = a.table + (base + l) * a.table_stride;
       int32_t page = -1;
-      if (pos < 0 || at >= a.table_stride) {  // pos < 0: the lengths' sum left 31 bits
+      if (at >= a.table_stride) {
         range = true;
       } else if (at < old) {
         page = row[at];
       } else {
         const int64_t f = (int64_t)s_pages[l] + (at - old);
-        if (f >= 0 && f < a.free_count) page = a.free_pages[f]; else range = true;
+        if (f < a.free_count) page = a.free_pages[f]; else range = true;
         if (pos % P == 0) row[at] = page;
       }
       const int64_t slot = page < 0 ? -1 : (int64_t)page * P + pos % P;
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kScanThreads) slot_map_kernel(SlotArgs a) {
   if (writer && tid == 0) {
     a.q_start[a.requests] = run_tokens;
     a.used[0] = run_pages;
-    if (run_tokens > a.tokens) range = true;
+    if (run_tokens > a.tokens || run_tokens == 0x7fffffff) range = true;
   }
   for (int64_t t = max(t0, (int64_t)run_tokens) + tid; t < t1; t += kScanThreads) {
     a.positions[t] = 0;

@@ -210,3 +210,41 @@ def test_append_of_skipped_tokens_asks_for_no_position(kq):
         k, v = (torch.empty(n, hk, d, device="cuda") for _ in range(2))
         kq.kq_kv_read(cache, ints(slots), k, v)
         assert torch.all(k[7] == 0) and torch.all(k[8].abs().amax(-1) > 0) and torch.all(v[7].abs().amax(-1) > 0)
+
+
+# ---- slot maps -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("cached,new", [([3, 0, 7], [1_200_000_000, 1_200_000_000, 2]),
+                                        ([3] + [0] * 2499, [1_000_000] * 2500),
+                                        ([3, 0, 0, 2147483640, 5], [30, 2147483647, 2147483647, 7, 2147483647]),
+                                        ([3, 16], [2147483640, 2147483640])])
+def test_slot_map_of_lengths_past_31_bits(kq, cached, new):
+    """Totals past 2^31 - 1 are held there and reported; the tokens within the capacity get their places."""
+    page, stride, capacity = 16, 4, 50
+    free = np.arange(50, 57)
+    table = np.full((len(cached), stride), 9)
+    o = [ints(np.full(n, -7)) for n in (len(cached) + 1, len(cached), capacity, capacity, 1)]
+    t = ints(table)
+    kq.kq_slot_map(ints(cached), ints(new), page, ints(free), t, *o)
+    assert status(kq) == kq.KQ_ERR_RANGE
+    q_start, kv_len, positions, slots, used = (x.cpu().numpy().astype(np.int64) for x in o)
+    most = (1 << 31) - 1
+    cut = np.minimum(new, most - np.asarray(cached))  # a length of its own past 31 bits is cut, too
+    assert np.array_equal(q_start, np.minimum(np.concatenate([[0], np.cumsum(cut)]), most))
+    assert np.array_equal(kv_len, np.asarray(cached) + cut)
+    need = -(-kv_len // page) - (-(-np.asarray(cached) // page))
+    assert used[0] == min(need.sum(), most)
+    t = t.cpu().numpy()
+    for i in range(capacity):
+        r = int(np.searchsorted(q_start, i, side="right")) - 1
+        pos = cached[r] + i - q_start[r]
+        assert positions[i] == pos
+        at = pos // page
+        old = -(-cached[r] // page)
+        first = int(need[:r].sum())
+        want = -1
+        if at < stride:
+            want = 9 if at < old else (free[first + at - old] if first + at - old < len(free) else -1)
+            assert t[r, at] == want
+        assert slots[i] == (-1 if want < 0 else want * page + pos % page)
