@@ -483,6 +483,16 @@ class KVCache:
         self._ref = ctypes.byref(self.desc)
 
 
+def _floats(t, name, shape):
+    """Address of a contiguous fp32 tensor that fills `shape` in its last dimensions (None -> NULL)."""
+    if t is None:
+        return None
+    if str(t.dtype) == "torch.float32" and t.is_contiguous() and t.dim() >= len(shape) and \
+            tuple(t.shape[t.dim() - len(shape):]) == shape:
+        return t.data_ptr()
+    raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous fp32 tensor of {shape} is needed, not {tuple(t.shape)} {t.dtype}")
+
+
 class QKNorm:
     """A kq_qk_norm descriptor and the device tensors it points at: fp32
     weights [head_dim] (None: ones), the fp32 rotation table [positions,
@@ -492,8 +502,10 @@ class QKNorm:
                  interleaved=False, norm=True):
         self.q_weight, self.k_weight, self.rope = q_weight, k_weight, rope
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        rows = 0 if rope is None else rope.shape[0]
         self.desc = kq_qk_norm(q_heads, kv_heads, head_dim, rope_dim, int(interleaved), int(norm), eps, 0,
-                               _ptr(q_weight), _ptr(k_weight), _ptr(rope), 0 if rope is None else rope.shape[0])
+                               _floats(q_weight, "q_weight", (head_dim,)), _floats(k_weight, "k_weight", (head_dim,)),
+                               _floats(rope, "rope", (rows, rope_dim)) if rope_dim else None, rows)
         self._ref = ctypes.byref(self.desc)
 
 
