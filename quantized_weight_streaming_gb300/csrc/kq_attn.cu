@@ -32,7 +32,8 @@
 //    the two accumulators of a score lie in one lane.  fp32 probabilities are
 //    split the same way into two products.
 //  - m moves only when a score passes it by 6 (p' then reaches 2^15 at most),
-//    so that the accumulators are rarely rescaled.
+//    so that the accumulators are rarely rescaled.  The power of two that brings
+//    p' there is a factor of its own: as part of m it would be lost beyond 2^24.
 //
 // Work is counted in tiles of keys per (request, key head, eight query rows),
 // laid end to end and cut into equal runs, one per warp, whatever the requests'
@@ -170,9 +171,9 @@ struct Row {
   uint32_t lo[kLo][4];               // rows 8..15
   float zero[kQ];                    // -8 sum(q) of each group
   float factor;                      // score in log2 units = factor * accumulated
-  float m, l;                        // reference (log2), this lane's share of the weight
-  float dmax;                        // power of two that no value scale so far passes
-  int32_t key_lo, key_hi;            // keys that the lane's row sees
+  float m, l;                        // reference (log2), this lane's share of the weight; both it and o are sums of
+                                     // p = 2^(score - m) up (up is not added to m, which beyond 2^24 would lose it)
+  float up;                          // 2^kHeadroom over a power of two that no value scale so far passes
   float o[kQ][2][4];                 // sums: dimensions 4 r + {0, 2} (and one further, times kOdd), rows 2 c, 2 c + 1
 
   __device__ __forceinline__ void add(int q, int j, const float (&t)[4]) {
@@ -199,12 +200,13 @@ struct Cursor {
   int32_t any_lo, any_hi;      // keys that one of them sees
 };
 
-// Joins m and the exponent of the largest value scale: true sum = stored * 2^reference.
-__device__ __forceinline__ float reference(float m, int exponent) { return m + (float)(exponent - kHeadroom); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// 1 / x of a power of two.
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 template <typename T, int D, bool kMask>
-__device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const uint8_t* stage, int32_t key0, uint32_t bad,
-                                            const Cursor& cur, const uint8_t* queries) {
+__device__ __forceinline__ void attend_tile(Row<T, D>& w, const uint8_t* stage, int32_t key0, uint32_t bad,
+                                            const Cursor& cur, const uint8_t* queries, const int2* sees) {
   using L = Layout<D>;
   using C = Config<T, D>;
   using Q = Codes<C::kSplit>;
@@ -275,13 +277,15 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
       }
     }
   }
+  int2 row_sees;
+  if constexpr (kMask) row_sees = sees[lane];
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) {
     s[b] = mul2(s[b], make_float2(w.factor, w.factor));
     if constexpr (kMask) {
       const int32_t key = key0 + 8 * b + 2 * c;
       const bool held = !(bad >> (b / 2) & 1u);
-      const bool s0 = held && key >= w.key_lo && key < w.key_hi, s1 = held && key + 1 >= w.key_lo && key + 1 < w.key_hi;
+      const bool s0 = held && key >= row_sees.x && key < row_sees.y, s1 = held && key + 1 >= row_sees.x && key + 1 < row_sees.y;
       seen |= (uint32_t)s0 << (2 * b) | (uint32_t)s1 << (2 * b + 1);
       if (!s0) s[b].x = -INFINITY;
       if (!s1) s[b].y = -INFINITY;
@@ -289,7 +293,7 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
     top = fmaxf(top, fmaxf(s[b].x, s[b].y));
   }
   // whether a reference has to move
-  const bool moves = top > w.m + kSlack, grows = dmax > w.dmax;
+  const bool moves = top - w.m > kSlack, grows = dmax * w.up > pow2(kHeadroom);  // (exact where they are close)
   if (__any_sync(~0u, moves || grows)) {
     // every lane of a row agrees on whether it moves: a row's own scores alone decide its reference
     float row = top;
@@ -298,16 +302,17 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
     float d = dmax;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) d = fmaxf(d, __shfl_xor_sync(~0u, d, o));
-    const float before = reference(w.m, exponent);
-    const bool fresh = w.m == -INFINITY;
-    if (row > w.m + kSlack) w.m = row;
-    if (d > w.dmax) {
+    const float before = w.m;
+    float keep_up = 1.f;
+    if (row - w.m > kSlack) w.m = row;
+    if (d * w.up > pow2(kHeadroom)) {
       int e;
       frexpf(d, &e);  // d <= 2^e
-      exponent = max(exponent, min(e, 17));
-      w.dmax = ldexpf(1.f, exponent);
+      const float up = fminf(w.up, pow2(kHeadroom - min(e, 17)));
+      keep_up = up * inverse_pow2(w.up);
+      w.up = up;
     }
-    const float keep = fresh ? 0.f : exp2_approx(before - reference(w.m, exponent));
+    const float keep = before == -INFINITY ? 0.f : exp2_approx(before - w.m) * keep_up;
     w.l *= keep;
     const float k0 = __shfl_sync(~0u, keep, 8 * c), k1 = __shfl_sync(~0u, keep, 8 * c + 4);
 #pragma unroll
@@ -316,11 +321,11 @@ __device__ __forceinline__ void attend_tile(Row<T, D>& w, int& exponent, const u
       for (int j = 0; j < 2; ++j) w.o[q][j][0] *= k0, w.o[q][j][1] *= k1, w.o[q][j][2] *= k0, w.o[q][j][3] *= k1;
     }
   }
-  const float ref = w.m == -INFINITY ? 0.f : -reference(w.m, exponent);
+  const float minus = w.m == -INFINITY ? 0.f : -w.m, up = w.up;
 #pragma unroll
   for (int b = 0; b < kBlocks; ++b) {
-    s[b] = add2(s[b], make_float2(ref, ref));
-    s[b] = make_float2(exp2_approx(s[b].x), exp2_approx(s[b].y));
+    s[b] = add2(s[b], make_float2(minus, minus));
+    s[b] = mul2(make_float2(exp2_approx(s[b].x), exp2_approx(s[b].y)), make_float2(up, up));
     w.l += s[b].x + s[b].y;
   }
 #pragma unroll
@@ -410,7 +415,7 @@ __device__ __forceinline__ bool seek(const Args& a, Cursor& c) {
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>& w, uint8_t* queries) {
+__device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>& w, uint8_t* queries, int2* sees) {
   constexpr int kQ = D / 32;
   using C = Codes<Config<T, D>::kSplit>;
   constexpr float kZero = -8.f * (1 << C::kUnitLog) / 16777216.f;
@@ -420,11 +425,11 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
   const bool live = i < cur.q.n;
   const int32_t pos = cur.q.pos0 + i;
   // rows past the last one hold zeros and see everything: they never ask for the masked path
-  w.key_lo = live ? first_key(a, pos) : 0;
-  w.key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
-  cur.all_lo = __reduce_max_sync(~0u, w.key_lo), cur.all_hi = __reduce_min_sync(~0u, w.key_hi);
-  cur.any_lo = __reduce_min_sync(~0u, live ? w.key_lo : 0x7fffffff);
-  cur.any_hi = __reduce_max_sync(~0u, live ? w.key_hi : 0);
+  const int32_t key_lo = live ? first_key(a, pos) : 0, key_hi = live ? max(0, min(pos + 1, cur.q.len)) : 0x7fffffff;
+  sees[lane] = make_int2(key_lo, key_hi);  // a lane reads back what it wrote
+  cur.all_lo = __reduce_max_sync(~0u, key_lo), cur.all_hi = __reduce_min_sync(~0u, key_hi);
+  cur.any_lo = __reduce_min_sync(~0u, live ? key_lo : 0x7fffffff);
+  cur.any_hi = __reduce_max_sync(~0u, live ? key_hi : 0);
   const T* src = static_cast<const T*>(a.q) + (int64_t)(cur.q.first + i) * a.q_token +
                  (int64_t)(h * a.group + x % a.group) * a.q_head + 8 * c;
   float x8[kQ][8], top = 0.f;
@@ -473,7 +478,7 @@ __device__ __forceinline__ void begin_row(const Args& a, Cursor& cur, Row<T, D>&
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.o[q][0][j] = w.o[q][1][j] = 0.f;
   }
-  w.dmax = 0.f;
+  w.up = pow2(kHeadroom + 24);
   w.m = live ? -INFINITY : 0.f;
   w.l = 0.f;
 }
@@ -484,7 +489,7 @@ constexpr float kOut = 16777216.f / (1 << Codes<Config<T, D>::kSplit>::kUnitLog)
 
 // Ends a row (whole: the output itself) or this warp's part of it.
 template <typename T, int D>
-__device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T, D>& w, int exponent, float* partial) {
+__device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T, D>& w, float* partial) {
   const int lane = threadIdx.x & 31, r = lane / 4, c = lane & 3;
   w.l += __shfl_xor_sync(~0u, w.l, 1);
   w.l += __shfl_xor_sync(~0u, w.l, 2);
@@ -494,7 +499,7 @@ __device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T,
     const float l = __shfl_sync(~0u, w.l, 8 * c + 4 * j);
     const int32_t x = x0 + 2 * c + j, i = x / a.group;
     if (i >= cur.q.n) continue;
-    const float f = partial ? 1.f : (l == 0.f ? 0.f : kOut<T, D> / l);
+    const float f = partial ? inverse_pow2(w.up) : (l == 0.f ? 0.f : kOut<T, D> / l);
     T* dst = static_cast<T*>(a.out) + (int64_t)(cur.q.first + i) * a.out_token +
              (int64_t)(h * a.group + x % a.group) * a.out_head;
 #pragma unroll
@@ -514,8 +519,8 @@ __device__ __forceinline__ void end_row(const Args& a, const Cursor& cur, Row<T,
     }
   }
   if (partial && c == 0) {
-    partial[kRows * D + r] = w.m == -INFINITY ? -INFINITY : reference(w.m, exponent);
-    partial[kRows * D + kRows + r] = w.l;
+    partial[kRows * D + r] = w.m;
+    partial[kRows * D + kRows + r] = w.l * inverse_pow2(w.up);
   }
 }
 
@@ -529,6 +534,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   __shared__ int64_t s_first[C::kThreads];  // units before each request of a chunk
   __shared__ int64_t s_warp[C::kWarps + 1];
   __shared__ Cursor s_cursor[C::kWarps];
+  __shared__ int2 s_sees[C::kWarps][32];  // keys that a lane's row sees
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool producer = warp == C::kWarps;
   const int me = producer ? min(lane, C::kWarps - 1) : warp;  // the consumer that this thread works for
@@ -702,13 +708,12 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
   uint32_t used = 0;
   while (cur.unit < cur.end) {
     if (cur.tile == cur.q.tiles) next_row<C::kTile>(a, cur);
-    begin_row<T, D>(a, cur, w, queries);
+    begin_row<T, D>(a, cur, w, queries, s_sees[warp]);
     __syncwarp();
     if (lane == 0) c = cur;
     __syncwarp();
     const int32_t from = c.tile;
     const int32_t to = (int32_t)min((int64_t)c.q.tiles, from + (c.end - c.unit));
-    int exponent = -24;  // of the value scales so far
     for (int32_t t = max(from, c.need_lo); t < min(to, c.need_hi); ++t) {
       const int st = used % C::kStages;
       if (!mbar_wait_suspend(&full[st], (used / C::kStages) & 1)) {
@@ -719,16 +724,16 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
       const uint32_t bad = hidden[st];
       const uint8_t* stage = ring + st * C::kStageBytes;
       if (bad || key0 < c.all_lo || key0 > c.all_hi - C::kTile)
-        attend_tile<T, D, true>(w, exponent, stage, key0, bad, c, queries);
+        attend_tile<T, D, true>(w, stage, key0, bad, c, queries, s_sees[warp]);
       else
-        attend_tile<T, D, false>(w, exponent, stage, key0, 0, c, queries);
+        attend_tile<T, D, false>(w, stage, key0, 0, c, queries, s_sees[warp]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
       ++used;
     }
     const bool whole = from == 0 && to == c.q.tiles;
     float* partial = whole ? nullptr : a.partials + (2 * run + (first ? 0 : 1)) * kPartial<D>;
-    end_row<T, D>(a, c, w, exponent, partial);
+    end_row<T, D>(a, c, w, partial);
     first = false;
     cur = c;
     cur.unit += to - from;

@@ -21,10 +21,10 @@ def repack(s):
 # ---- scores of any size ---------------------------------------------------------------
 
 
-def _one_key_rows(s, window=0):
-    """(rows whose largest score stands out, the value row of that key): FP64 scores a fraction 2^-16 of the row's largest
-    magnitude apart, 16 times what fp32 products of exact operands can lose.  Where that is 100 or more, every other key's
-    weight is below 2^-100 and the output is the key's value."""
+def _one_key_rows(s, window=0, apart=2.0**-16):
+    """(rows whose largest score stands out, the value row of that key): FP64 scores a fraction `apart` of the row's largest
+    magnitude apart; 2^-16 is 16 times what fp32 products of exact operands can lose.  Where that is 100 or more, every
+    other key's weight is below 2^-100 and the output is the key's value."""
     group = s.hq // s.kc.shape[1]
     k, v = (np.nan_to_num(ref.values(c, x)) for c, x in ((s.kc, s.ks), (s.vc, s.vs)))
     q = f64(s.q)
@@ -40,7 +40,7 @@ def _one_key_rows(s, window=0):
                 e = s.scale * (kk[first: pos + 1, h // group] @ q[t, h])
                 order = np.argsort(e)
                 gap = e[order[-1]] - e[order[-2]] if len(e) > 1 else np.inf
-                stands[t, h] = gap > max(100.0, 2.0**-16 * np.abs(e).max())
+                stands[t, h] = gap > max(100.0, apart * np.abs(e).max())
                 want[t, h] = vv[first + order[-1], h // group]
     return stands, want
 
@@ -75,6 +75,27 @@ def test_prompt_of_very_large_scores(kq, hq, hk, d, dt, size, side):
         assert status(kq) == kq.KQ_OK
         assert np.all(np.isfinite(out))
         stands, want = _one_key_rows(s, window)
+        assert stands.mean() > 0.5
+        near(out[stands], want[stands], dt)
+
+
+@pytest.mark.parametrize("side", [0, 1, -1])
+@pytest.mark.parametrize("dt,size", [("f32", 1e6), ("f32", 1e7), ("f32", 5e7), ("f32", 1e8), ("f32", 1e12), ("f32", 1e30),
+                                     ("bf16", 1e7), ("bf16", 1e8), ("bf16", 1e30), ("f16", 1e8), ("f16", 1e20)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 1, 256), (14, 2, 64)])
+@pytest.mark.parametrize("values", [0, -10])
+def test_decode_of_very_large_scores(kq, hq, hk, d, dt, size, side, values):
+    """The same of the kernel for few query rows, in rows that one warp ends and rows that several share.  (16-bit rows: the
+    tensor instruction keeps 13 bits or more of a product with a code, so scores a fraction 2^-9 apart stand out.)"""
+    rng = np.random.default_rng(33 + d)
+    s = _large(kq, rng, dt, hq, hk, d, size, side, [1, 2, 3, 1], [170, 45, 30, 2000])
+    s.vs = (s.vs.astype(np.float32) * 2.0**values).astype(np.float16)
+    repack(s)
+    for window in (0, 30):
+        out = f64(s.run(window))
+        assert status(kq) == kq.KQ_OK
+        assert np.all(np.isfinite(out))
+        stands, want = _one_key_rows(s, window, 2.0**-16 if dt == "f32" else 2.0**-9)
         assert stands.mean() > 0.5
         near(out[stands], want[stands], dt)
 
