@@ -73,6 +73,11 @@ constexpr float kSlack = 6.f;        // log2 by which a score may pass the refer
 constexpr int kHeadroom = 9;         // p' <= 2^(6 + 9)
 constexpr int kCombineThreads = 256;
 constexpr int kJoinRows = 16, kZeroCtas = 8;
+// Row tiles, as the arguments bound them, up to which cut rows are found by a CTA a row tile, which can read its request
+// before attend_kernel is done; beyond, by the runs.  8 key heads of 128, 32 requests of 8000 tokens, bf16: 256 row tiles,
+// 50.6 us against 53.1 by the runs; 256 of 1000: 2048, 73.1 against 73.4; 512 of 500: 4096, 97.5 against 92.0; 32 of 1000 in
+// fp32 under a max_new of 512, 65536 row tiles: 252 against 29.
+constexpr int64_t kManyTiles = 2048;
 template <int D>
 constexpr int kJoinSlices = PromptShape<D>::kRows / kJoinRows;
 // Tiles of a run where there are fewer than one for every warp: one request of 1300 tokens (8 key heads of 128) takes
@@ -581,7 +586,7 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
         sum += s_warp[i];
       }
       s_first[tid] = at;
-      if (blockIdx.x == 0 && pass == 0 && mine) a.base[r] = at;
+      if (blockIdx.x == 0 && pass == 0 && mine && !a.by_runs) a.base[r] = at;
       __syncthreads();
       if (pass == 0) total = sum;
       if (pass == 1 || chunks == 1) {
@@ -605,11 +610,24 @@ __global__ void __launch_bounds__(Config<T, D>::kThreads, 1) attend_kernel(Args 
     }
   }
   if (blockIdx.x == 0) {
-    if (tid == 0) a.base[a.requests] = total;
+    if (tid == 0 && !a.by_runs) a.base[a.requests] = total;
     if (out_of_range) attn_flag(KQ_ERR_RANGE);
   }
-  if (!producer && cur.unit == cur.end) return;
   if (cur.unit < cur.end) enter_row<C::kTile>(a, cur);
+  if (a.by_runs && !producer && lane == 0) {  // (while the first tiles are on their way)
+    TileStart start{};
+    start.from = start.to = (int32_t)run;
+    if (cur.unit < cur.end) {
+      const Runs runs(total, (int64_t)kSms * C::kWarps, kLeastRun);
+      const int64_t lo = cur.unit - cur.tile;
+      start.from = (int32_t)runs.of(lo), start.to = (int32_t)runs.of(lo + cur.q.tiles - 1);
+      start.later = runs.start(start.from) < lo;
+      start.first = cur.q.first, start.rows = cur.q.rows;
+      start.x0 = cur.row % row_tiles(cur.q) * kRows, start.h = cur.row / row_tiles(cur.q);
+    }
+    a.starts[run] = start;
+  }
+  if (!producer && cur.unit == cur.end) return;
 
   if (producer) {
     const uint64_t policy = l2_policy_evict_first();
@@ -779,18 +797,61 @@ __device__ __forceinline__ void store_row(T* p, const float (&o)[N], float f) {
 
 // Joins, in run order, the parts of rows that were cut between runs, and writes
 // zeros where a row sees nothing.
-//  - The first few_ctas CTAs: rows_per_cta query rows of one row tile of
-//    attend_kernel each (eight rows of a request and key head, cut at the same
-//    places).  The warps share out rows, and then the parts of a row.
-//  - The others: 16 rows of the row block that a boundary between two runs of
-//    the prompt kernel falls in.
-//  - The last kZeroCtas of them: prompts' row blocks that see nothing.
-template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int slices, int tile_rows, int rows_per_cta, int64_t few_ctas) {
+//  - The first few_ctas CTAs: rows of row tiles of attend_kernel (eight rows of a
+//    request and key head, cut at the same places).  The warps share out rows,
+//    and then the parts of a row.
+//    Without kByRuns, rows_per_cta rows of one row tile each, whether they were
+//    cut or not, as many CTAs as requests of max_new tokens would have.
+//    With it, eight boundaries between runs each, and the row tiles whose first
+//    boundary is among them: a grid that follows from the number of runs,
+//    whatever the caller's bounds are.
+//  - The next: 16 rows of the row block that a boundary between two runs of the
+//    prompt kernel falls in.
+//  - The last kZeroCtas: what sees nothing of prompts (with kByRuns, of all requests).
+constexpr int kBoundaries = 8;
+
+// Rows first .. first + n - 1 of a row tile that runs `from` .. `to` hold, by the whole CTA; out(row): where a row goes.  Its
+// sums lie in a run's first slot, in the second of run `from` where the run began with another row (`later`).
+template <typename T, int D, typename Out>
+__device__ __forceinline__ void join_rows(const Args& a, int first, int n, int32_t from, int32_t to, int32_t later, const Out& out,
+                                          float (*s_sum)[D], float* s_ref, float* s_weight) {
+  constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a power of two of rows, the remaining factor of the warps on the parts of each
+  const int wide = n > 4 ? 8 : (n > 2 ? 4 : n), shares = kWarps / wide, in = warp % wide, share = warp / wide;
+  Sum<kPer> s;
+  if (in < n) {
+#pragma unroll 4
+    for (int32_t w = from + share; w <= to; w += shares) {
+      const float* p = a.partials + (2 * (int64_t)w + (w == from ? later : 0)) * kPartial<D>;
+      float o[kPer];
+      load_part<kPer>(o, p + (first + in) * D + lane * kPer);
+      s.join(p[kRows * D + first + in], p[kRows * D + kRows + first + in], o);
+    }
+  }
+  if (lane == 0) s_ref[warp] = s.ref, s_weight[warp] = s.weight;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = s.acc[e];
+  __syncthreads();
+  if (share > 0 || in >= n) return;
+  for (int v = 1; v < shares; ++v) {
+    float o[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = s_sum[in + v * wide][lane * kPer + e];
+    s.join(s_ref[in + v * wide], s_weight[in + v * wide], o);
+  }
+  store_row<T, kPer>(out(first + in) + lane * kPer, s.acc, s.weight == 0.f ? 0.f : kOut<T, D> / s.weight);
+}
+
+template <typename T, int D, bool kByRuns>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int slices, int tile_rows, int rows_per_cta, int few_ctas,
+                                                                  int prompt_ctas) {
   using C = Config<T, D>;
   using P = PromptShape<D>;
   constexpr int kPer = D / 32, kWarps = kCombineThreads / 32;
   __shared__ float s_sum[kWarps][D], s_ref[kWarps], s_weight[kWarps];
+  __shared__ int64_t s_list[kCombineThreads];
+  __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // (What the call was given may be read before the launch in front is done, from L2: that one let this one start after
   // all before it were.)
@@ -798,14 +859,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     grid_dependency_wait();
     allow_dependent_launch();
   };
-  auto row_out = [&](const Request& q, int h, int32_t x) {
-    return static_cast<T*>(a.out) + (int64_t)(q.first + x / a.group) * a.out_token +
+  auto row_out = [&](int32_t token0, int h, int32_t x) {
+    return static_cast<T*>(a.out) + (int64_t)(token0 + x / a.group) * a.out_token +
            (int64_t)(h * a.group + x % a.group) * a.out_head;
   };
-  if (blockIdx.x < few_ctas) {
+  if (!kByRuns && blockIdx.x < few_ctas) {
     const int per_tile = (tile_rows + rows_per_cta - 1) / rows_per_cta, part = blockIdx.x % per_tile;
-    const int64_t tile = blockIdx.x / per_tile;
-    const int slice = (int)(tile % slices), h = (int)(tile / slices % a.cache.kv_heads);
+    const int tile = blockIdx.x / per_tile;
+    const int slice = tile % slices, h = tile / slices % a.cache.kv_heads;
     const int64_t r = tile / slices / a.cache.kv_heads;
     const Request q = request_of<true>(a, r, C::kTile);
     launches_before();
@@ -814,42 +875,37 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     if (q.rows > a.few_rows || x0 >= q.rows) return;
     const int n = min(rows_per_cta, q.rows - x0);
     if (q.tiles == 0) {
-      for (int e = tid; e < n * D; e += kCombineThreads) row_out(q, h, x0 + e / D)[e % D] = kv::from_float<T>(0.f);
+      for (int e = tid; e < n * D; e += kCombineThreads) row_out(q.first, h, x0 + e / D)[e % D] = kv::from_float<T>(0.f);
       return;
     }
     const Runs runs(a.base[a.requests], (int64_t)kSms * C::kWarps, kLeastRun);
     const int64_t lo = a.base[r] + ((int64_t)h * row_tiles(q) + slice) * q.tiles;
-    const int64_t w0 = runs.of(lo), w1 = runs.of(lo + q.tiles - 1);
-    if (w0 == w1) return;
-    // a power of two of rows, the remaining factor of the warps on the parts of each
-    const int wide = n > 4 ? 8 : (n > 2 ? 4 : n), shares = kWarps / wide, in = warp % wide, share = warp / wide;
-    Sum<kPer> s;
-    if (in < n) {
-#pragma unroll 4
-      for (int64_t w = w0 + share; w <= w1; w += shares) {
-        const float* p = a.partials + (2 * w + (runs.start(w) >= lo ? 0 : 1)) * kPartial<D>;
-        float o[kPer];
-        load_part<kPer>(o, p + (first + in) * D + lane * kPer);
-        s.join(p[kRows * D + first + in], p[kRows * D + kRows + first + in], o);
-      }
-    }
-    if (lane == 0) s_ref[warp] = s.ref, s_weight[warp] = s.weight;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s_sum[warp][lane * kPer + e] = s.acc[e];
-    __syncthreads();
-    if (share > 0 || in >= n) return;
-    for (int v = 1; v < shares; ++v) {
-      float o[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = s_sum[in + v * wide][lane * kPer + e];
-      s.join(s_ref[in + v * wide], s_weight[in + v * wide], o);
-    }
-    store_row<T, kPer>(row_out(q, h, x0 + in) + lane * kPer, s.acc, s.weight == 0.f ? 0.f : kOut<T, D> / s.weight);
+    const int32_t from = (int32_t)runs.of(lo), to = (int32_t)runs.of(lo + q.tiles - 1);
+    if (from == to) return;
+    join_rows<T, D>(a, first, n, from, to, runs.start(from) >= lo ? 0 : 1,
+                    [&](int row) { return row_out(q.first, h, slice * kRows + row); }, s_sum, s_ref, s_weight);
     return;
   }
   launches_before();
-  const int64_t at = blockIdx.x - few_ctas;
-  if (at < (int64_t)kJoinSlices<D> * (kSms - 1)) {
+  if (kByRuns && blockIdx.x < few_ctas) {
+    // lane i of every warp looks at the i-th boundary
+    const int32_t b0 = 1 + kBoundaries * blockIdx.x, b = b0 + lane % kBoundaries;
+    TileStart start{};
+    if (b < kSms * C::kWarps) start = a.starts[b];
+    const uint32_t firsts = __ballot_sync(~0u, b == start.from + 1 && b <= start.to) & ((1u << kBoundaries) - 1);
+    for (uint32_t left = firsts; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const int32_t from = __shfl_sync(~0u, start.from, i), to = __shfl_sync(~0u, start.to, i);
+      const int32_t later = __shfl_sync(~0u, start.later, i), token0 = __shfl_sync(~0u, start.first, i);
+      const int32_t x0 = __shfl_sync(~0u, start.x0, i), rows = __shfl_sync(~0u, start.rows, i), h = __shfl_sync(~0u, start.h, i);
+      join_rows<T, D>(a, 0, min(kRows, rows - x0), from, to, later, [&](int row) { return row_out(token0, h, x0 + row); }, s_sum,
+                      s_ref, s_weight);
+      __syncthreads();
+    }
+    return;
+  }
+  const int at = blockIdx.x - few_ctas;
+  if (at < prompt_ctas) {
     const int64_t b = at / kJoinSlices<D> + 1;
     const Runs runs(*a.prompt_total, kSms, P::kLeastRun);
     if (b >= runs.count) return;
@@ -858,7 +914,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
     const int64_t lo = start.lo + P::kRowCost;
     if (start.at <= P::kRowCost || lo < runs.start(b - 1)) return;
     const Request q = request_of(a, start.r, P::kKeys);
-    const int32_t first = (int32_t)(at % kJoinSlices<D>) * kJoinRows;
+    const int32_t first = at % kJoinSlices<D> * kJoinRows;
     const int32_t rows = min(P::kRows, q.rows - start.k * P::kRows);
     const int64_t w1 = runs.of(lo + start.tiles - 1);
 #pragma unroll
@@ -873,25 +929,43 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(Args a, int sl
         load_part<kPer>(o, p + (int64_t)in * D + lane * kPer);
         s.join(p[P::kRows * D + in], p[P::kRows * D + P::kRows + in], o);
       }
-      store_row<T, kPer>(row_out(q, start.h, start.k * P::kRows + in) + lane * kPer, s.acc,
+      store_row<T, kPer>(row_out(q.first, start.h, start.k * P::kRows + in) + lane * kPer, s.acc,
                          s.weight == 0.f ? 0.f : 1.f / s.weight);
     }
     return;
   }
-  for (int64_t r = at - (int64_t)kJoinSlices<D> * (kSms - 1); r < a.requests; r += kZeroCtas) {
-    const Request q = request_of(a, r, P::kKeys);
-    if (q.rows <= a.few_rows) continue;
-    // (only where the request brings more tokens than it holds, or its length was cut)
-    if (q.pos0 >= 0 && q.len == q.pos0 + q.n) continue;
-    for (int32_t k = 0; k * P::kRows < q.rows; ++k) {
-      const RowBlock blk = row_block<D>(a, q, k);
-      if (blk.tiles) continue;
-      for (int64_t e = tid; e < (int64_t)blk.rows * a.q_heads / a.group * D; e += kCombineThreads) {
-        const int32_t row = (int32_t)(e / D) % blk.rows;
-        row_out(q, (int)(e / D / blk.rows), k * P::kRows + row)[e % D] = kv::from_float<T>(0.f);
+  // Every thread looks at a request; the CTA then writes the rows of those that were found.
+  for (int64_t r0 = at - prompt_ctas; r0 < a.requests; r0 += (int64_t)kZeroCtas * kCombineThreads) {
+    const int64_t mine = r0 + (int64_t)kZeroCtas * tid;
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    if (mine < a.requests) {
+      const Request q = request_of(a, mine, C::kTile);
+      // (of a prompt only where it brings more tokens than it holds, or its length was cut)
+      if (q.rows > a.few_rows ? q.pos0 < 0 || q.len != q.pos0 + q.n : kByRuns && q.n > 0 && q.tiles == 0)
+        s_list[atomicAdd(&s_count, 1)] = mine;
+    }
+    __syncthreads();
+    for (int i = 0; i < s_count; ++i) {
+      const int64_t r = s_list[i];
+      const Request q = request_of(a, r, P::kKeys);
+      for (int32_t x0 = 0; x0 < q.rows; x0 += P::kRows) {
+        if (q.rows > a.few_rows && row_block<D>(a, q, x0 / P::kRows).tiles) continue;
+        const int32_t rows = min(P::kRows, q.rows - x0);
+        for (int64_t e = tid; e < (int64_t)rows * a.cache.kv_heads * D; e += kCombineThreads)
+          row_out(q.first, (int)(e / D / rows), x0 + (int32_t)(e / D % rows))[e % D] = kv::from_float<T>(0.f);
       }
     }
+    __syncthreads();
   }
+}
+
+// Bounds from the call's arguments: query rows of a key head that one request brings to attend_kernel, and row tiles of all
+// requests and key heads (2^40 stands for anything large).
+static int64_t query_rows_of(const Args& a) { return std::min<int64_t>(a.few_rows, std::min(a.max_new, a.tokens) * a.group); }
+static int64_t row_tiles_of(const Args& a) {
+  const int64_t slices = (query_rows_of(a) + kRows - 1) / kRows * a.cache.kv_heads, most = (int64_t)1 << 40;
+  return slices > most / a.requests ? most : slices * a.requests;
 }
 
 template <typename T, int D>
@@ -905,17 +979,17 @@ static cudaError_t launch(const Args& a, cudaStream_t st) {
     if (cudaError_t e = launch_prompt(sizeof(T) == 4 ? -1 : (std::is_same_v<T, __half> ? KQ_F16 : KQ_BF16), D, a, st)) return e;
   }
   const bool prompts = a.few_rows != 0x7fffffff;
-  const int64_t rows = std::min<int64_t>(prompts ? a.few_rows : 0x7fffffff, std::min(a.max_new, a.tokens) * a.group);
-  const int slices = (int)((rows + kRows - 1) / kRows);
   // A row a CTA where that stays few: one request of 20000 tokens, whose rows lie in a hundred parts, took 28 us instead
   // of 52 with eight rows a CTA; with 256 row tiles a row a CTA cost 32 requests of 8000 tokens 4 us more.
-  const int64_t tiles = a.requests * a.cache.kv_heads * slices;
-  const int tile_rows = (int)std::min<int64_t>(rows, kRows);
+  const int64_t tiles = row_tiles_of(a);
+  const int slices = (int)(query_rows_of(a) + kRows - 1) / kRows, tile_rows = (int)std::min<int64_t>(query_rows_of(a), kRows);
   const int rows_per_cta = tiles <= 64 ? 1 : kRows;
-  const int64_t few_ctas = tiles * ((tile_rows + rows_per_cta - 1) / rows_per_cta);
-  const int64_t join_ctas = prompts ? (int64_t)kJoinSlices<D> * (kSms - 1) + kZeroCtas : 0;
-  return launch_dependent(combine_kernel<T, D>, dim3((unsigned)(few_ctas + join_ctas)), dim3(kCombineThreads), 0, st, a, slices,
-                          tile_rows, rows_per_cta, few_ctas);
+  const int few_ctas = a.by_runs ? ((int)kSms * C::kWarps + kBoundaries - 2) / kBoundaries
+                                 : (int)tiles * ((tile_rows + rows_per_cta - 1) / rows_per_cta);
+  const int prompt_ctas = prompts ? kJoinSlices<D> * (kSms - 1) : 0;
+  return launch_dependent(a.by_runs ? combine_kernel<T, D, true> : combine_kernel<T, D, false>,
+                          dim3((unsigned)(few_ctas + prompt_ctas + (prompts || a.by_runs ? kZeroCtas : 0))), dim3(kCombineThreads), 0,
+                          st, a, slices, tile_rows, rows_per_cta, few_ctas, prompt_ctas);
 }
 
 template <typename T>
@@ -930,7 +1004,7 @@ constexpr int32_t few_rows_of(int d) { return d == 64 ? 64 : 40; }
 
 // The workspace: byte offsets of its parts, and its size.
 struct Workspace {
-  size_t base, partials, prompt_total, prompt_starts, prompt_partials, bytes;
+  size_t base, starts, partials, prompt_total, prompt_starts, prompt_partials, bytes;
 };
 static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t requests, int64_t tokens, int64_t max_new) {
   const int d = c->head_dim;
@@ -945,6 +1019,7 @@ static Workspace workspace(const kq_kv_cache* c, int32_t q_heads, int64_t reques
     return here;
   };
   w.base = take((requests + 1) * 8);
+  w.starts = take(kSms * kMaxWarps * (int64_t)sizeof(TileStart));
   w.partials = take(2 * kSms * kMaxWarps * partial_floats(d) * 4);
   w.prompt_total = take(prompts ? 8 : 0);
   w.prompt_starts = take(prompts ? kSms * (int64_t)sizeof(RunStart) : 0);
@@ -1020,12 +1095,14 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
   const attn::Workspace w = attn::workspace(cache, q_heads, requests, tokens, max_new);
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
   a.base = reinterpret_cast<int64_t*>(ws + w.base);
+  a.starts = reinterpret_cast<attn::TileStart*>(ws + w.starts);
   a.partials = reinterpret_cast<float*>(ws + w.partials);
   a.prompt_total = reinterpret_cast<int64_t*>(ws + w.prompt_total);
   a.prompt_starts = reinterpret_cast<attn::RunStart*>(ws + w.prompt_starts);
   a.prompt_partials = reinterpret_cast<float*>(ws + w.prompt_partials);
   const bool prompts = dtype != KQ_F32 && std::min(max_new, tokens) > attn::few_rows_of(cache->head_dim) / a.group;
   a.few_rows = prompts ? attn::few_rows_of(cache->head_dim) : 0x7fffffff;
+  a.by_runs = attn::row_tiles_of(a) > attn::kManyTiles;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32 ? attn::launch<float>(cache->head_dim, a, st)
                               : (dtype == KQ_F16 ? attn::launch<__half>(cache->head_dim, a, st)

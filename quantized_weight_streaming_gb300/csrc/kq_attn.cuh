@@ -27,6 +27,14 @@ struct RunStart {
   int32_t k, h, at, tiles;
 };
 
+// The row tile that a run of attend_kernel begins in: the runs from .. to hold it, `from` as its first or a later row.  (A
+// run without work: from = to.)
+struct alignas(16) TileStart {
+  int32_t from, to, later;
+  int32_t first, x0, rows, h;  // the request's first token, the row tile's first row and all rows of the key head
+  int32_t reserved;
+};
+
 struct Args {
   Cache cache;
   const void* q;
@@ -39,8 +47,10 @@ struct Args {
   float scale;
   // requests with more query rows than this are the prompt kernel's
   int32_t few_rows;
+  int32_t by_runs;  // how cut rows are found again (combine_kernel)
   // workspace
-  int64_t* base;             // first work unit of each request, and the total
+  int64_t* base;             // first work unit of each request, and the total (with by_runs: not written)
+  TileStart* starts;         // of each run of attend_kernel (with by_runs alone)
   float* partials;           // two slots per run of kRows x D sums, kRows references, kRows weights
   int64_t* prompt_total;     // work units of the prompt kernel
   RunStart* prompt_starts;   // of each of its runs

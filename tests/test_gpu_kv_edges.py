@@ -269,3 +269,59 @@ def test_slot_map_of_lengths_past_31_bits(kq, cached, new):
             want = 9 if at < old else (free[first + at - old] if first + at - old < len(free) else -1)
             assert t[r, at] == want
         assert slots[i] == (-1 if want < 0 else want * page + pos % page)
+
+
+# ---- bounds of lengths that are far from the lengths -----------------------------------------
+
+
+@pytest.mark.parametrize("requests,longest", [(1025, 300), (600, 300), (7, 3000)])
+def test_attention_of_few_tokens_under_large_bounds(kq, requests, longest):
+    """tokens and max_new are a capacity and an upper bound: as large as they may be, with 128 query heads on one key head,
+    cut rows are joined as with the smallest that fit, bit by bit (7 requests: by other CTAs)."""
+    import ctypes
+
+    rng = np.random.default_rng(61)
+    s = Step(kq, rng, rng.integers(0, longest, requests), [1] * requests, 128, 1, 64, 16, "f32")
+    want = s.run()
+    assert status(kq) == kq.KQ_OK
+    first = ref.attention(f64(s.q[:7]), np.nan_to_num(ref.values(s.kc, s.ks)), np.nan_to_num(ref.values(s.vc, s.vs)),
+                          s.q_start[:8], s.kv_len[:7], s.table, 16, s.scale, 0)
+    near(f64(want[:7]), first, "f32")
+    tokens = (1 << 31) // 8192 - 1
+    n = kq.kq_attn_workspace_bytes(s.cache, 128, requests, tokens, tokens)
+    assert n > 0
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full(s.q.shape, 7.0, device="cuda")
+    q_start, kv_len, table = ints(s.q_start), ints(s.kv_len), ints(s.table)
+    view = lambda t: ctypes.byref(kq.kq_heads(t.data_ptr(), t.stride(0), t.stride(1)))  # noqa: E731
+    assert kq.lib().kq_attn_paged(ctypes.byref(s.cache.desc), kq.KQ_F32, 128, view(s.q), q_start.data_ptr(), kv_len.data_ptr(),
+                                  table.data_ptr(), table.shape[1], requests, tokens, tokens, s.scale, 0, view(out),
+                                  ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == kq.KQ_OK
+    assert status(kq) == kq.KQ_OK
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (6, 1, 256), (14, 2, 64)])
+def test_attention_under_large_bounds(kq, dt, hq, hk, d):
+    """Rows in few and in many parts, requests that see nothing, a malformed one and prompts, where the bounds allow a
+    hundred thousand row tiles."""
+    rng = np.random.default_rng(62 + d)
+    lens = np.array([5000, 1, 0, 77, 3, 640, 0, 300] + [20] * 60)
+    new = np.array([1, 1, 2, 3, 9, 70, 5, 1] + [1] * 60)
+    s = Step(kq, rng, lens, new, hq, hk, d, 32, dt)
+    q = s.q
+    s.q = torch.cat([q, q.new_zeros(9000, hq, d)])
+    out = s.run(max_new=9000)
+    assert status(kq) == kq.KQ_OK
+    assert torch.all(out[len(q):] == 7)
+    s.q = q
+    want = s.want()
+    near(f64(out[: len(q)]), want, dt)
+    one = Step(kq, rng, [20000], [1], hq, hk, d, 32, dt)  # one row tile in a thousand parts
+    q = one.q
+    one.q = torch.cat([q, q.new_zeros(60000, hq, d)])
+    out = one.run(max_new=60000)
+    assert status(kq) == kq.KQ_OK
+    one.q = q
+    near(f64(out[:1]), one.want(), dt)
