@@ -325,3 +325,152 @@ def test_attention_under_large_bounds(kq, dt, hq, hk, d):
     assert status(kq) == kq.KQ_OK
     one.q = q
     near(f64(out[:1]), one.want(), dt)
+
+
+# ---- paths that only long prompts reach, and what else a step promises --------------------------
+
+
+def _prompt_slots(rng, tokens, page, pages):
+    """Slots of a prompt step: requests that go on in the middle of a granule, tokens skipped within a run, and a stretch in
+    no order at all (a window of 32 tokens then falls on more granules than it gathers)."""
+    order = rng.permutation(pages)
+    slots, at = np.full(tokens, -1), 0
+    i = 0
+    while i < tokens:
+        n = int(min(tokens - i, rng.integers(1, 120)))
+        first = int(rng.integers(0, page))
+        need = -(-(first + n) // page)
+        pos = first + np.arange(n)
+        slots[i: i + n] = order[at + pos // page] * page + pos % page
+        at += need
+        i += n
+    mixed = slice(tokens // 2, tokens // 2 + 100)
+    slots[mixed] = rng.permutation(slots[mixed])
+    slots[rng.random(tokens) < 0.05] = -1
+    slots[-1] = -1
+    return slots
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,rd,inter,tokens,page", [(128, 128, False, 700, 32), (128, 64, True, 613, 48), (64, 64, False, 650, 16),
+                                                   (64, 32, True, 621, 32), (256, 64, False, 330, 16), (256, 256, True, 313, 64),
+                                                   (128, 0, False, 641, 16)])
+def test_append_of_prompts(kq, dt, d, rd, inter, tokens, page):
+    """The windowed write (from 608 windows of 32 or 16 tokens of a head on): values are the host SCALE4 quantizer's bytes,
+    keys within half a step of FP64, every byte that of the same tokens written in small calls, other slots untouched."""
+    rng = np.random.default_rng(71 + d + tokens)
+    hq, hk = 5, 32
+    assert -(-tokens // (16 if d == 256 else 32)) * hk >= 608
+    x = dev(rng.standard_normal((tokens, (2 * hq + 2 * hk) * d)).astype(np.float32) * 1.7,
+            {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dt])
+    q = x[:, : 2 * hq * d].unflatten(1, (hq, 2 * d))[:, :, :d]
+    k, v = x[:, 2 * hq * d: (2 * hq + hk) * d].unflatten(1, (hk, d)), x[:, (2 * hq + hk) * d:].unflatten(1, (hk, d))
+    v[3, 1, :32] = 0
+    v[3, 1, 7], v[3, 1, 20] = -2.0, 2.0
+    pages = tokens // 4
+    slots, pos = _prompt_slots(rng, tokens, page, pages), rng.integers(0, 300, tokens)
+    table = kq.kq_rope_table_host(300, rd, 1e4) if rd else None
+    w = rng.uniform(0.5, 1.5, d).astype(np.float32)
+    p = kq.QKNorm(hq, hk, d, rd, None, dev(w), dev(table) if rd else None, interleaved=inter)
+    cache, small = (kq.KVCache(pages, page, hk, d) for _ in range(2))
+    for c in (cache, small):
+        c.data.fill_(0x5A)
+    qo, q2, k2 = (torch.empty(tokens, h, d, dtype=x.dtype, device="cuda") for h in (hq, hq, hk))
+    kq.kq_kv_append(p, cache, q, k, v, ints(pos), ints(slots), qo)
+    assert status(kq) == kq.KQ_OK
+    for i in range(0, tokens, 64):
+        j = min(tokens, i + 64)
+        kq.kq_kv_append(p, small, None, k[i:j], v[i:j], ints(pos[i:j]), ints(slots[i:j]), None)
+    kq.kq_qk_norm_rope(p, q, k, ints(pos), q2, k2)
+    assert status(kq) == kq.KQ_OK
+    assert torch.equal(qo, q2)
+    assert torch.equal(cache.data, small.data)
+    live = slots >= 0
+    at = slots[live]
+    kc, ks, vc, vs = (y[at // page, :, at % page] for y in ref.unpack(cache.data.cpu().numpy(), page, d))
+    blocks = kq.kq_quantize_scale4(v.float().cpu().numpy()[live].reshape(-1, d)).reshape(live.sum(), hk, d // 32, 18)
+    assert np.array_equal(vs.view(np.uint16), blocks[..., :2].copy().view(np.uint16)[..., 0])
+    assert np.array_equal(vc, np.stack([blocks[..., 2:] & 15, blocks[..., 2:] >> 4], -1).reshape(live.sum(), hk, d))
+    want = ref.norm_rope(f64(k), w, table, pos, rd, 1e-6, True, inter)[live]
+    step = np.repeat(np.abs(ks.astype(np.float64)), 32, -1)
+    # half a step, or up to one where 8 steps is the clamped end, and the fp16 rounding of the scale (8 steps of 2^-11)
+    assert np.all(np.abs(ref.values(kc, ks) - want) <= step * np.where(kc == 15, 1.01, 0.505) + 1e-6)
+    rest = np.ones(pages * page, bool)
+    rest[at] = False
+    blank = kq.KVCache(pages, page, hk, d)
+    blank.data.fill_(0x5A)
+    for y, z in zip(ref.unpack(cache.data.cpu().numpy(), page, d), ref.unpack(blank.data.cpu().numpy(), page, d)):
+        y, z = (a.transpose(0, 2, 1, 3).reshape(pages * page, -1)[rest] for a in (y, z))
+        assert np.array_equal(y.view(np.uint16) if y.dtype == np.float16 else y, z.view(np.uint16) if z.dtype == np.float16 else z)
+
+
+def test_slot_map_repeated_writes_the_same(kq):
+    rng = np.random.default_rng(72)
+    cached, new = rng.integers(0, 300, 300), rng.integers(0, 40, 300)
+    t, stride = int(new.sum()), 30
+    need = int((-(-(cached + new) // 16) - (-(-cached // 16))).sum())
+    args = [ints(cached), ints(new), 16, ints(rng.permutation(need))]
+    table = ints(rng.integers(0, 1000, (300, stride)))
+    o = [ints(np.zeros(n)) for n in (301, 300, t, t, 1)]
+    kq.kq_slot_map(*args, table, *o)
+    first = [x.clone() for x in (table, *o)]
+    for x in o:
+        x.fill_(-3)
+    kq.kq_slot_map(*args, table, *o)
+    assert status(kq) == kq.KQ_OK
+    assert all(torch.equal(x, y) for x, y in zip(first, (table, *o)))
+
+
+@pytest.mark.parametrize("dt,new", [("f32", [1, 1, 1, 1]), ("bf16", [1, 3, 1, 0]), ("f16", [90, 1, 200, 7])])
+def test_whole_step_in_a_cuda_graph(kq, dt, new):
+    """slot map -> append -> attention captured once and replayed over other lengths and values: the same bits as the calls."""
+    rng = np.random.default_rng(73)
+    hq, hk, d, page, pages, t, r = 8, 2, 128, 16, 200, sum(new), len(new)
+    typ = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[dt]
+    rope = dev(kq.kq_rope_table_host(900, d, 1e4))
+    p = kq.QKNorm(hq, hk, d, d, None, None, rope)
+
+    class State:
+        def __init__(self):
+            self.cache = kq.KVCache(pages, page, hk, d)
+            self.cached, self.new, self.free = ints(np.zeros(r)), ints(new), ints(np.arange(pages))
+            self.table = ints(np.zeros((r, 60)))
+            self.o = [ints(np.zeros(n)) for n in (r + 1, r, t, t, 1)]
+            self.x = torch.zeros(t, hq + 2 * hk, d, dtype=typ, device="cuda")
+            self.qo, self.out = (torch.zeros(t, hq, d, dtype=typ, device="cuda") for _ in range(2))
+            n = kq.kq_attn_workspace_bytes(self.cache, hq, r, t, max(new))
+            self.ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+        def step(self):
+            q_start, kv_len, positions, slots, used = self.o
+            kq.kq_slot_map(self.cached, self.new, page, self.free, self.table, *self.o)
+            kq.kq_kv_append(p, self.cache, self.x[:, :hq], self.x[:, hq: hq + hk], self.x[:, hq + hk:], positions, slots, self.qo)
+            kq.kq_attn_paged(self.cache, self.qo, q_start, kv_len, self.table, self.out, d ** -0.5, max(new), ws=self.ws)
+
+    plain, captured = State(), State()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        captured.step()  # first launches of the kernels, outside the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured.step()
+    done, total = 0, np.zeros(r, int)
+    for i in range(4):
+        x = dev(rng.standard_normal((t, hq + 2 * hk, d)).astype(np.float32), typ)
+        free = np.concatenate([np.arange(done, pages), np.arange(done)])
+        for s in (plain, captured):
+            s.x.copy_(x)
+            s.cached.copy_(ints(total))
+            s.free.copy_(ints(free))
+        plain.step()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(plain.out, captured.out) and torch.equal(plain.table, captured.table)
+        kc, ks, vc, vs = ref.unpack(plain.cache.data.cpu().numpy(), page, d)
+        want = ref.attention(f64(plain.qo), ref.values(kc, ks), ref.values(vc, vs), plain.o[0].cpu().numpy(), total + new,
+                             plain.table.cpu().numpy(), page, d ** -0.5, 0)
+        near(f64(plain.out), want, dt)
+        total += new
+        done += int(plain.o[4].item())
+    assert status(kq) == kq.KQ_OK
