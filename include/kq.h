@@ -636,9 +636,14 @@ int kq_kv_read(const kq_kv_cache* cache, const int32_t* d_slots, int64_t count, 
  *  - d_q_start [requests + 1], d_kv_len [requests], d_block_table
  *    [requests][table_stride]: int32, as kq_slot_map writes them.
  *  - max_new: an upper bound of the requests' new tokens (1 for a decode step).
- *  - Scores, softmax statistics and sums in fp32, codes exact.  fp32 queries
- *    and the probabilities that go with them enter the tensor cores as two
- *    fp16 parts.
+ *  - Scores, softmax statistics and sums are fp32.  With fp32 queries the
+ *    result is one of fp32: codes stay exact, queries and probabilities enter
+ *    the tensor cores as two fp16 parts.  With 16-bit queries probabilities are
+ *    rounded to fp16, and a product of query and code keeps 13 bits or more;
+ *    requests of more than 40 query rows a key head (64 at head_dim 64) round
+ *    code times scale of keys and values to fp16, too: 2^-11 at most each, in
+ *    all 2.9e-4 and 3.8e-4 of a row's size at scores of about 1, where the fp16
+ *    output's own rounding is 2.1e-4.  What a score loses grows with its size.
  *  - On the device: a page id outside the cache hides its keys; a length past
  *    the table's row is cut to it; a request whose q_start passes `tokens` or
  *    decreases, or that brings more than max_new tokens, is left out (its rows

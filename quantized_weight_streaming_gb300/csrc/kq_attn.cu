@@ -43,14 +43,20 @@
 // workspace; a second launch joins them in a fixed order.
 //
 // Measured (a replayed graph, both launches, 4 us of them its own): 64 requests
-// of 16384 tokens, 24 query and 4 key heads of 256, fp16: 266 us, 1.21 GB of
+// of 16384 tokens, 24 query and 4 key heads of 256, fp16: 261 us, 1.21 GB of
 // cache; 32 ragged requests of up to 8000, 32 and 8 heads of 128, bf16: 50 us,
-// 143 MB; 8 requests of 4 new tokens on 4100, fp32: 40 us.  The large ones move
-// 4.6 (D = 256) and 5.4 TB/s (D = 128) once they run, behind 12 us of finding
-// the runs, first copies, and joining.  Instructions bound them, not bytes: 51
-// to 55% of the issue slots taken (with three warps a scheduler; a fourth gave
-// 2%), tensor pipe 29 to 34%; per word of eight codes there are five to unpack,
-// and the zero points, scales and softmax.
+// 143 MB, the same in fp32: 53 us; 8 requests of 4 new tokens on 4100, fp32: 39
+// us (each eight rows unpack the keys anew).  A further byte of cache comes at
+// 5.1 (D = 256) and 4.8 TB/s (D = 128); finding the runs, first copies, uneven
+// ends and joining are 20 to 25 us.  Neither bytes nor issue slots are used up:
+// 59 and 52% of the slots are taken while warps run (per word of eight codes five
+// instructions unpack, and there are the zero points, scales and softmax),
+// tensor pipe 34 and 28%; warps wait for the fixed latency of the instructions
+// before (1.6 cycles of 6.5 to 7 between two) and for the pipes that unpacking
+// and products share (1.0 to 1.1).
+//
+// 16-bit rows are 2.9e-4 from exact at fp16 where rounding the output alone is
+// 2.1e-4: p' is rounded to fp16, and score products keep 13 bits or more.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -89,8 +95,9 @@ struct Config {
   static constexpr bool kSplit = sizeof(T) == 4;        // two fp16 parts
   // Consumer warps; with the copying warp four a scheduler and 128 registers for 16-bit queries, three and 168 or two and
   // 255 for fp32.  (Three a scheduler with 16-bit queries: 64 requests of 16384 tokens, 4 key heads of 256, took 273 us
-  // instead of 266, and 32 ragged ones on 8 heads of 128 51.5 instead of 50.7.)  At D = 256 the queries of 16-bit rows lie
-  // in shared memory, read once a tile: sums and queries in registers leave room for two, 283 us.
+  // instead of 266, and 32 ragged ones on 8 heads of 128 51.5 instead of 50.7; at 128 registers 136 bytes spill at D = 128,
+  // 48 at 256.)  At D = 256 the queries of 16-bit rows lie in shared memory, read once a tile: sums and queries in
+  // registers leave room for two, 283 us.
   static constexpr bool kQShared = D == 256 && !kSplit;
   static constexpr int kWarps = (!kSplit ? 16 : (D == 256 ? 8 : 12)) - 1;
   static constexpr int kStages = kQShared ? 2 : (kWarps > 11 ? 3 : (kWarps < 8 ? 6 : 4));  // what fits beside them

@@ -110,7 +110,9 @@ struct PromptShape {
   // left CTAs with nine short rows, 176000 cycles, beside others with two, 72000.  6 ragged prompts of up to 700 of 1500
   // tokens, 8 key heads of 128: 90.9 us with six units, 84.5 with ten, 89.2 with 14.)
   static constexpr int kRowCost = 10;
-  // Units of a run: two tiles.  The last 300 of 2000 tokens: 43.2 us; with twelve more units a run 9 us more.
+  // Units that a run is worth: two tiles of a row.  (Runs share the units evenly, so one more than this many make two
+  // runs of half as many, of which the first may hold no tile.)  The last 300 of 2000 tokens: 43.2 us; with twelve more
+  // units a run 9 us more.
   static constexpr int kLeastRun = kRowCost + 2;
   __device__ static int32_t units(int32_t tiles) { return tiles ? tiles + kRowCost : 0; }
   static constexpr int64_t kPartial = kRows * (int64_t)(D + 2);

@@ -13,7 +13,7 @@
 //
 // Keys and values become fp16 as they are unpacked (code - 8, exact, times the
 // scale, one rounding: the two roundings of K and V and that of P are each
-// 2^-12 at most, as the one of a 16-bit output, and independent); sums, maxima
+// 2^-11 at most, as the one of a 16-bit output, and independent); sums, maxima
 // and weights stay fp32.  Queries are scaled by a power of two per row, so bf16
 // loses nothing either.  Where a scale passes 8188 (the value would leave fp16)
 // the tile's keys or values are divided by 8, and scores or probabilities
@@ -35,10 +35,12 @@
 // (378 us with the unpacking loops unrolled, 266 without).
 //
 // Measured: the last 2048 of 8192 tokens, 32 query and 8 key heads of 128,
-// bf16: 251 to 261 us, 920 to 957 TFLOP/s of what the mask leaves.  Issue slots
-// bound it (64% taken; tensor pipe 40%): unpacking, which each row block does
+// bf16: 249 to 255 us, 945 to 966 TFLOP/s of what the mask leaves.  Issue slots
+// bound it (63% taken; tensor pipe 42%): unpacking, which each row block does
 // anew, and the softmax.  Rounding K, V and P to fp16 costs rows of fp16 output
-// an error of 3.6e-4 where rounding the output alone costs 2.1e-4.
+// an error of 3.6e-4 to 3.8e-4 where rounding the output alone costs 2.1e-4.  (P
+// as two fp16 parts left 3.2e-4 and took 300 us instead of 255 in fp16.)  The
+// scores' rounding goes into the exponent: it grows with their size.
 //
 // Row blocks in order, each head's key tiles end to end, are cut into one run
 // of tiles per CTA, whatever the prompts' lengths and masks; a block cut
