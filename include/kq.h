@@ -388,7 +388,8 @@ void kq_decode_plan_destroy(kq_plan* plan);
  *
  * A linked plan knows projections only.  What lies between them (attention
  * and the norm and rotation before it have entry points of their own further
- * down; activation functions and residual adds are outside this library)
+ * down, as have residual adds with the norm after them; the FFN's activation
+ * function is outside this library)
  * is not part of the launch; the plainest stand-in is kept: the activation of
  * a dependent matrix is alpha times a prefix of an earlier matrix's output. */
 typedef enum {
@@ -660,6 +661,157 @@ int kq_attn_paged(const kq_kv_cache* cache, int dtype, int32_t q_heads, const kq
 /* Workspace bytes of kq_attn_paged; 0 for arguments it does not take. */
 size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_t requests, int64_t tokens,
                                int64_t max_new);
+
+/* ---- norms, gated-delta layers and sampling ------------------------------------ */
+
+/* What a decode or prompt step runs beside its attention layers: the norm of
+ * the residual stream between two projections, the layers that keep a state
+ * instead of a cache (a short convolution, the gated delta rule, a gated norm:
+ * "Bonsai 2 27B", section 7, 48 of whose 64 layers are such), and the choice of
+ * a token from the head's logits.
+ *
+ * A delta layer: (projections) -> kq_causal_conv -> kq_gdn -> kq_rms_norm with
+ * the gate -> (output projection).  Requests are given as in kq_attn_paged, by
+ * the q_start and kv_len that kq_slot_map writes; beside them each has a state
+ * slot.  Nothing is read back, so a step can be captured in a CUDA graph. */
+
+/* RMS norm of rows.  A row is one head of one token: heads rows of dim elements
+ * a token (a residual stream is one head of its hidden size).
+ *   s = x + residual   (rounded to dtype, written back to residual; s = x without)
+ *   y = s / sqrt(mean(s^2) + eps) * weight * silu(gate)
+ * weight fp32 [dim] (NULL: ones), silu(z) = z / (1 + e^-z), left out without a
+ * gate.  fp32 arithmetic whatever the types, one rounding at the end.
+ *   heads 1 to 4096; dim a multiple of 8 up to 32768; eps >= 0. */
+typedef struct {
+  int32_t heads, dim;
+  float eps;
+  int32_t reserved; /* 0 */
+  const float* weight;
+} kq_rms;
+
+/* y of `tokens` tokens to out (rows of `dtype` elements), to out_q8, or to both.
+ *  - x, residual (in and out, or NULL), gate (or NULL), out (or NULL): rows of
+ *    heads.  out may be x's, the residual's or the gate's own view; other
+ *    overlaps are not allowed.
+ *  - out_q8 (or NULL): planes of KQ_Q8_0 with n = tokens * heads rows (token by
+ *    token) and k = dim (then a multiple of 32), written by the rules of
+ *    kq_quantize_q8_0 from the fp32 y, scale padding included.  A block that
+ *    holds a NaN or infinity reads back as NaN and sets KQ_ERR_NONFINITE for
+ *    kq_device_status; one whose scale overflows fp16 as well, with KQ_ERR_RANGE.
+ *  - tokens = 0 is a no-op; tokens * heads < 2^31.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
+int kq_rms_norm(const kq_rms* p, int dtype, const kq_heads* x, const kq_heads* residual, const kq_heads* gate,
+                int64_t tokens, const kq_heads* out, const kq_qmat* out_q8, void* stream);
+
+/* The causal convolution of each channel over a request's tokens, and a SiLU:
+ *   y[t] = silu(bias + sum_{j < width} weight[j] x[t - (width - 1) + j])
+ * with the inputs before the request's new tokens taken from its state.
+ *   channels a multiple of 8 up to 2^20; width 2 to 4; weight fp32
+ *   [channels][width], bias fp32 [channels] (NULL: none); silu = 0 leaves the
+ *   SiLU out. */
+typedef struct {
+  int32_t channels, width;
+  int32_t silu;
+  int32_t reserved; /* 0 */
+  const float* weight;
+  const float* bias;
+} kq_conv;
+
+/* The step's requests, of kq_causal_conv and kq_gdn.  Request r has the tokens
+ * q_start[r] .. q_start[r + 1] - 1 of the token rows and the state d_slot[r].
+ *  - d_q_start [requests + 1], d_kv_len [requests] (NULL: every state goes on),
+ *    d_slot [requests]: int32.  A request whose kv_len equals its new tokens
+ *    begins: its state counts as zero, whatever the slot holds.
+ *  - A request without tokens, or with a negative slot, is skipped: its output
+ *    rows and its state stay as they are.  Rows past q_start[requests] are left
+ *    alone.
+ *  - On the device: a slot past the states, a q_start that decreases, is
+ *    negative or passes `tokens` (or more new tokens than max_new, where there is one) sets
+ *    KQ_ERR_RANGE for kq_device_status; the request is left out, and of the
+ *    others of a call with such a q_start any may be.
+ *  - Two requests of one call must not share a slot. */
+
+/* x, out: rows of `channels` elements of `dtype` (head_stride unused), `tokens`
+ * of them; out must not overlap x.  d_state: `dtype` [slots][width - 1]
+ * [channels], the last inputs, oldest first, 16-byte aligned; updated.
+ * requests >= 1; tokens = 0 is a no-op.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
+int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t* d_q_start, const int32_t* d_kv_len,
+                   const int32_t* d_slot, int64_t requests, int64_t tokens, void* d_state, int64_t slots,
+                   const kq_heads* out, void* stream);
+
+/* The gated delta rule.  Each value head h keeps a state S [D][D] (key
+ * dimension by value dimension); key head h / (v_heads / k_heads) serves it.
+ * Token by token, with a decay g and a strength beta per value head:
+ *   S <- g S;  u = beta (v - S^T k);  S <- S + k u^T;  out = S^T q
+ *  - unit = 1: q and k are scaled to x / sqrt(sum(x^2) + eps) first; q is then
+ *    multiplied by `scale` in any case.
+ *  - gates = 1: g = exp(-exp(a_log) softplus(a + dt_bias)), beta = sigmoid(b),
+ *    a_log, dt_bias fp32 [v_heads]; gates = 0: g = exp(a), beta = b (a_log and
+ *    dt_bias NULL).  a > 0 is then a growth, and is taken as it is.
+ *   head_dim 64 or 128; v_heads a multiple of k_heads, 1 to 4096. */
+typedef struct {
+  int32_t k_heads, v_heads, head_dim;
+  int32_t unit, gates;
+  float eps, scale;
+  int32_t reserved; /* 0 */
+  const float* a_log;
+  const float* dt_bias;
+} kq_gdn_rule;
+
+/* out of the step's tokens, and the states after them.
+ *  - q, k [tokens][k_heads][D], v, out [tokens][v_heads][D]: rows of heads of
+ *    `dtype`; out may be v's own view.  a, b: `dtype` [tokens][v_heads] with
+ *    token strides of a_stride, b_stride elements (any alignment of a dtype's).
+ *  - d_state: fp32 [slots][v_heads][D][D], 16-byte aligned; updated.
+ *  - max_new: an upper bound of the requests' new tokens (1 for a decode step).
+ *  - fp32 arithmetic and states whatever the types, one rounding of the output.
+ *    Prompts of 16-bit types go in chunks of 64 tokens whose products run on the
+ *    tensor cores, with every factor that is not exact in fp16 as two fp16 parts
+ *    (22 bits): states and outputs are ones of fp32 there too.
+ *  - A NaN or infinity in a token's q, k, v or gates makes what it reaches
+ *    unspecified: its heads' outputs from that token on (in a chunk, from the
+ *    chunk's first on), and their state.
+ *  - Workspace: kq_gdn_workspace_bytes, 16-byte aligned (0 where none is
+ *    needed); everything in it is written before it is read.
+ *  - requests >= 1; tokens = 0 is a no-op.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_WORKSPACE,
+ * KQ_ERR_CUDA. */
+int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k, const kq_heads* v, const void* d_a,
+           int64_t a_stride, const void* d_b, int64_t b_stride, const int32_t* d_q_start, const int32_t* d_kv_len,
+           const int32_t* d_slot, int64_t requests, int64_t tokens, int64_t max_new, float* d_state, int64_t slots,
+           const kq_heads* out, void* d_ws, size_t ws_bytes, void* stream);
+/* Workspace bytes of kq_gdn; 0 for arguments it does not take. */
+size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests, int64_t tokens, int64_t max_new);
+
+/* A token from each row of logits.  With the row's settings, e_i = exp((l_i -
+ * max l) / temperature):
+ *   top_k > 0 keeps the top_k largest logits (of equal ones the lowest ids);
+ *   top_p < 1 keeps, of these in falling order, the fewest whose e sum to at
+ *   least top_p of theirs (one at least); min_p > 0 keeps those with e >= min_p
+ *   (the largest in any case).
+ * The token is the first id, in the order of the vocabulary, at which the
+ * running sum of the kept e exceeds u times their sum; prob is its e over that
+ * sum.  temperature = 0 takes the largest logit, the lowest id of equal ones
+ * (prob 1).
+ *  - d_logits: `dtype` [rows][vocab], rows row_stride elements apart, aligned to
+ *    the type's size (16-byte rows load faster).
+ *  - d_temperature, d_top_p, d_min_p, d_u fp32 [rows], d_top_k int32 [rows]; a
+ *    NULL one stands for 1, 1, 0, (d_u is needed) and 0 for every row.  u lies in
+ *    [0, 1); what lies outside counts as the nearest end.
+ *  - d_token int32 [rows], d_prob fp32 [rows] (NULL: not written).
+ *  - A logit of -infinity is never chosen.  A row whose largest is infinity
+ *    chooses among those alone.  A row that holds a NaN or nothing but
+ *    -infinity, or whose temperature or top_p or min_p is a NaN or whose temperature is
+ *    negative or infinite, gets token -1 and prob 0, and sets
+ *    KQ_ERR_NONFINITE for kq_device_status.
+ *  - exp is one of fp32, of an argument kept to 2^-40; sums are of 64-bit
+ *    integers, so the order of work changes no token.
+ *  - vocab 1 to 393216; rows = 0 is a no-op.
+ * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
+int kq_sample(int dtype, const void* d_logits, int64_t row_stride, int64_t rows, int64_t vocab,
+              const float* d_temperature, const int32_t* d_top_k, const float* d_top_p, const float* d_min_p,
+              const float* d_u, int32_t* d_token, float* d_prob, void* stream);
 
 /* ---- device status --------------------------------------------------------- */
 

@@ -87,6 +87,22 @@ class kq_qk_norm(ctypes.Structure):
                 ("k_weight", ctypes.c_void_p), ("d_rope", ctypes.c_void_p), ("rope_positions", ctypes.c_int64)]
 
 
+class kq_rms(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("weight", ctypes.c_void_p)]
+
+
+class kq_conv(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("width", ctypes.c_int32), ("silu", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class kq_gdn_rule(ctypes.Structure):
+    _fields_ = [("k_heads", ctypes.c_int32), ("v_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("unit", ctypes.c_int32), ("gates", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("a_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -95,6 +111,9 @@ _QP = ctypes.POINTER(kq_qmat)
 _HP = ctypes.POINTER(kq_heads)
 _CP = ctypes.POINTER(kq_kv_cache)
 _NP = ctypes.POINTER(kq_qk_norm)
+_RP = ctypes.POINTER(kq_rms)
+_VP = ctypes.POINTER(kq_conv)
+_GP = ctypes.POINTER(kq_gdn_rule)
 
 # name -> (restype, argtypes); every symbol declared in include/kq.h
 SIGNATURES = {
@@ -151,6 +170,12 @@ SIGNATURES = {
     "kq_attn_paged": (ctypes.c_int, [_CP, ctypes.c_int, _I32, _HP, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_float,
                                      _I64, _HP, _P, _SZ, _P]),
     "kq_attn_workspace_bytes": (_SZ, [_CP, _I32, _I64, _I64, _I64]),
+    "kq_rms_norm": (ctypes.c_int, [_RP, ctypes.c_int, _HP, _HP, _HP, _I64, _HP, _QP, _P]),
+    "kq_causal_conv": (ctypes.c_int, [_VP, ctypes.c_int, _HP, _P, _P, _P, _I64, _I64, _P, _I64, _HP, _P]),
+    "kq_gdn": (ctypes.c_int, [_GP, ctypes.c_int, _HP, _HP, _HP, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64,
+                              _HP, _P, _SZ, _P]),
+    "kq_gdn_workspace_bytes": (_SZ, [_GP, ctypes.c_int, _I64, _I64, _I64]),
+    "kq_sample": (ctypes.c_int, [ctypes.c_int, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P]),
     "kq_device_status": (ctypes.c_int, [ctypes.c_int]),
     "kq_set_pq2_0_consumer": (ctypes.c_int, [ctypes.c_int]),
     "kq_get_pq2_0_consumer": (ctypes.c_int, []),
@@ -610,6 +635,140 @@ def kq_attn_paged(cache, q, d_q_start, d_kv_len, d_block_table, out, scale, max_
                               _ints(d_kv_len, r, "d_kv_len"), _ints(d_block_table, 0, "d_block_table"), table[1], r,
                               shape[0], max_new, scale, window, _heads(out, hq, d, "out", q), p, nb, _stream(stream)),
            "kq_attn_paged")
+
+
+# ---- norms, gated-delta layers and sampling ------------------------------------------
+
+class RMSNorm:
+    """A kq_rms descriptor and the fp32 weight [dim] (None: ones) that it points at."""
+
+    def __init__(self, heads, dim, weight=None, eps=1e-6):
+        self.weight, self.heads, self.dim = weight, heads, dim
+        self.desc = kq_rms(heads, dim, eps, 0, _floats(weight, "weight", (dim,)))
+        self._ref = ctypes.byref(self.desc)
+
+
+def kq_rms_norm(p, x, out=None, residual=None, gate=None, out_q8=None, stream=None):
+    """RMS norm of the rows of x [tokens, heads, dim] (strided views): of x + residual, which residual then holds, where one
+    is given; times silu(gate) where one is.  To out, to the Q8_0 planes of out_q8 (a QMatrix of tokens * heads rows), or
+    both."""
+    h, d, t = p.heads, p.dim, x.shape[0]
+    _check(_lib.kq_rms_norm(p._ref, _dtype(x), _heads(x, h, d, "x"), _heads(residual, h, d, "residual", x),
+                            _heads(gate, h, d, "gate", x), t, _heads(out, h, d, "out", x),
+                            None if out_q8 is None else ctypes.byref(out_q8.desc), _stream(stream)), "kq_rms_norm")
+
+
+class CausalConv:
+    """A kq_conv descriptor and the fp32 tensors that it points at: weight [channels, width], bias [channels] or None."""
+
+    def __init__(self, weight, bias=None, silu=True):
+        if weight.dim() != 2:
+            raise KQError(KQ_ERR_SHAPE, f"weight {tuple(weight.shape)}: [channels, width] is needed")
+        self.weight, self.bias = weight, bias
+        self.channels, self.width = weight.shape
+        self.desc = kq_conv(self.channels, self.width, int(silu), 0, _floats(weight, "weight", tuple(weight.shape)),
+                            _floats(bias, "bias", (self.channels,)))
+        self._ref = ctypes.byref(self.desc)
+
+
+def _wide_rows(t, wide, name, like=None):
+    """kq_heads of a [tokens, wide] view whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) == 2:
+        n, c = shape
+        st, sc = t.stride()
+        if c == wide and (sc == 1 or n == 0) and (like is None or (n == like.shape[0] and t.dtype is like.dtype)):
+            return kq_heads(t.data_ptr(), st if n > 1 else 0, 0)
+    raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(shape)} {t.dtype} strides {t.stride()}: [tokens, {wide}] of one type for "
+                                "all, innermost contiguous, is needed")
+
+
+def _states(t, like, shape, name):
+    """(address, slots) of a contiguous tensor [slots, *shape] of the type `like`."""
+    if t.dtype is like and t.is_contiguous() and tuple(t.shape[1:]) == shape:
+        return t.data_ptr(), t.shape[0]
+    raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(t.shape)} {t.dtype}: a contiguous {like} tensor [slots, "
+                                f"{', '.join(map(str, shape))}] is needed")
+
+
+def kq_causal_conv(p, x, d_q_start, d_kv_len, d_slot, state, out, stream=None):
+    """The short causal convolution of x [tokens, channels] into out, request by request; state [slots, width - 1,
+    channels] of x's type holds each slot's last inputs.  d_kv_len may be None: then every state goes on."""
+    r, t, c = d_slot.numel(), x.shape[0], p.channels
+    at, slots = _states(state, x.dtype, (p.width - 1, c), "state")
+    _check(_lib.kq_causal_conv(p._ref, _dtype(x), _wide_rows(x, c, "x"), _ints(d_q_start, r + 1, "d_q_start"),
+                               _ints(d_kv_len, r, "d_kv_len"), _ints(d_slot, r, "d_slot"), r, t, at, slots,
+                               _wide_rows(out, c, "out", x), _stream(stream)), "kq_causal_conv")
+
+
+class GatedDelta:
+    """A kq_gdn_rule descriptor and the fp32 tensors a_log, dt_bias [v_heads] that it points at (both None: the gates given
+    to kq_gdn are log decays and strengths as they are).  scale: None for head_dim ** -0.5."""
+
+    def __init__(self, k_heads, v_heads, head_dim, a_log=None, dt_bias=None, unit=True, eps=1e-6, scale=None):
+        self.a_log, self.dt_bias = a_log, dt_bias
+        self.k_heads, self.v_heads, self.head_dim = k_heads, v_heads, head_dim
+        self.desc = kq_gdn_rule(k_heads, v_heads, head_dim, int(unit), int(a_log is not None), eps,
+                                head_dim ** -0.5 if scale is None else scale, 0, _floats(a_log, "a_log", (v_heads,)),
+                                _floats(dt_bias, "dt_bias", (v_heads,)))
+        self._ref = ctypes.byref(self.desc)
+
+
+def kq_gdn_workspace_bytes(p, dtype, requests, tokens, max_new):
+    """Workspace bytes of kq_gdn; dtype a torch dtype."""
+    return _lib.kq_gdn_workspace_bytes(p._ref, _kind(dtype)[0], requests, tokens, max_new)
+
+
+def _gate(t, heads, name, like):
+    """(address, token stride) of a [tokens, heads] view whose rows are contiguous."""
+    if t.dim() == 2 and t.shape[0] == like.shape[0] and t.shape[1] == heads and t.dtype is like.dtype and \
+            (t.stride(1) == 1 or heads == 1 or t.shape[0] == 0):
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    raise KQError(KQ_ERR_SHAPE, f"{name} {tuple(t.shape)} {t.dtype} strides {t.stride()}: [{like.shape[0]}, {heads}] of "
+                                "q's type, innermost contiguous, is needed")
+
+
+_FLOAT32 = None
+
+
+def kq_gdn(p, q, k, v, a, b, d_q_start, d_kv_len, d_slot, state, out, max_new, ws=None, stream=None):
+    """The gated delta rule over the step's new tokens: q, k [tokens, k_heads, D], v, out [tokens, v_heads, D], gates a, b
+    [tokens, v_heads]; state fp32 [slots, v_heads, D, D], updated.  d_kv_len may be None: then every state goes on."""
+    global _FLOAT32
+    if _FLOAT32 is None:
+        import torch
+
+        _FLOAT32 = torch.float32
+    hk, hv, d, r, t = p.k_heads, p.v_heads, p.head_dim, d_slot.numel(), q.shape[0]
+    at, slots = _states(state, _FLOAT32, (hv, d, d), "state")
+    a_at, a_stride = _gate(a, hv, "a", q)
+    b_at, b_stride = _gate(b, hv, "b", q)
+    w, nb = _ws(ws)
+    _check(_lib.kq_gdn(p._ref, _dtype(q), _heads(q, hk, d, "q"), _heads(k, hk, d, "k", q), _heads(v, hv, d, "v", q), a_at,
+                       a_stride, b_at, b_stride, _ints(d_q_start, r + 1, "d_q_start"), _ints(d_kv_len, r, "d_kv_len"),
+                       _ints(d_slot, r, "d_slot"), r, t, max_new, at, slots, _heads(out, hv, d, "out", q), w, nb,
+                       _stream(stream)), "kq_gdn")
+
+
+def _per_row(t, rows, name):
+    if t is None:
+        return None
+    if str(t.dtype) == "torch.float32" and t.is_contiguous() and t.numel() >= rows:
+        return t.data_ptr()
+    raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous fp32 tensor of {rows} elements is needed, not {tuple(t.shape)} {t.dtype}")
+
+
+def kq_sample(logits, u, d_token, d_prob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """A token from each row of logits [rows, vocab] (rows may be strided) by the random numbers u [rows]; the settings are
+    device tensors [rows] (top_k int32, the others fp32) or None."""
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise KQError(KQ_ERR_SHAPE, f"logits {tuple(logits.shape)} strides {logits.stride()}: [rows, vocab], innermost "
+                                    "contiguous, is needed")
+    r, v = logits.shape
+    _check(_lib.kq_sample(_dtype(logits), logits.data_ptr(), logits.stride(0) if r > 1 else 0, r, v,
+                          _per_row(temperature, r, "temperature"), _ints(top_k, r, "top_k"), _per_row(top_p, r, "top_p"),
+                          _per_row(min_p, r, "min_p"), _per_row(u, r, "u"), _ints(d_token, r, "d_token"),
+                          _per_row(d_prob, r, "d_prob"), _stream(stream)), "kq_sample")
 
 
 KQ_PQ2_0_MMA_SYNC = 0

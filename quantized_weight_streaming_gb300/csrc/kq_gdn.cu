@@ -1,0 +1,457 @@
+// The gated-delta layers' operators beside their projections: the short causal
+// convolution with its rolling state, and the gated delta rule token by token.
+// (Long prompts of 16-bit types go to kq_gdn_prompt.cu.)
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kq_device.cuh"
+#include "kq_gdn.cuh"
+#include "kq_internal.h"
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace gdn {
+
+__device__ unsigned int g_gdn_status = 0;
+__device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1u << status); }
+
+// ---- the causal convolution -----------------------------------------------------
+//
+// y[t] = silu(bias + sum_j w[j] x[t - W + 1 + j]), channel by channel: two flops a
+// byte or less, so memory bounds it.  A warp takes 256 channels, eight a lane, and
+// walks down a piece of a request's tokens with the last W - 1 inputs in registers:
+// each input is read once but for the W - 1 before a piece.  Pieces begin at the
+// request's first token and every `piece` tokens from there, so only a request's
+// first piece reads its state, and the same lanes write the new one: nothing is
+// read after another CTA wrote it.  A warp owns the pieces that begin in its window
+// of token rows: it finds the request there by a 32-way search of q_start.
+
+constexpr int kConvWarps = 4;
+
+struct ConvArgs {
+  Rows x, out;
+  Requests s;
+  char* state;
+  const float* weight;
+  const float* bias;
+  int32_t channels, silu;
+  int32_t piece, window;
+  int64_t windows;
+};
+
+template <typename T, int W>
+struct ConvLane {
+  const ConvArgs& a;
+  const int channel;
+  float w[W][8], bias[8];
+  float past[W - 1][8];
+
+  __device__ __forceinline__ const T* row(int64_t t) const { return reinterpret_cast<const T*>(a.x.at(t, 0)) + channel; }
+  __device__ __forceinline__ T* kept(int32_t slot, int j) const {
+    return reinterpret_cast<T*>(a.state) + ((int64_t)slot * (W - 1) + j) * a.channels + channel;
+  }
+
+  __device__ void piece(const Request& q, int32_t from) {
+    const int32_t end = min(q.count, from + a.piece);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int32_t at = from - (W - 1) + j;
+      if (from > 0) {
+        kv::load8(row((int64_t)q.first + at), past[j]);  // a piece is W - 1 tokens long at least
+      } else if (q.fresh) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) past[j][e] = 0.f;
+      } else {
+        kv::load8(kept(q.slot, j), past[j]);
+      }
+    }
+    if (from == 0) {  // the new state: the last inputs, those of the old one among them where there are fewer
+      float next[W - 1][8];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        const int32_t at = q.count - (W - 1) + j;
+        if (at >= 0) {
+          kv::load8(row((int64_t)q.first + at), next[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < W - 1; ++i)
+            if (i == q.count + j) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) next[j][e] = past[i][e];
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) kv::store8(kept(q.slot, j), next[j]);
+    }
+    for (int32_t t = from; t < end; t += 4) {
+      kv::Raw<T, 8> raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < end) raw[i].load(row((int64_t)q.first + t + i));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t + i >= end) break;
+        float v[8], y[8];
+        raw[i].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float s = bias[e];
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][e], past[j][e], s);
+          s = fmaf(w[W - 1][e], v[e], s);
+          y[e] = a.silu ? s / (1.0f + expf(-s)) : s;
+#pragma unroll
+          for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
+          past[W - 2][e] = v[e];
+        }
+        kv::store8(reinterpret_cast<T*>(a.out.at((int64_t)q.first + t + i, 0)) + channel, y);
+      }
+    }
+  }
+};
+
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x % 32;
+  const int64_t window = (int64_t)blockIdx.x * kConvWarps + threadIdx.x / 32;
+  if (window >= a.windows) return;
+  const int64_t lo = window * a.window, hi = lo + a.window;
+  // the last request that begins at or before lo
+  int64_t r = 0, span = a.s.requests;
+  bool before = false;
+  while (span > 0) {
+    const int64_t step = (span + 31) / 32, at = r + lane * step;
+    const unsigned some = __ballot_sync(~0u, lane * step < span && a.s.q_start[at] <= lo);
+    if (!some) break;
+    before = true;
+    const int last = 31 - __clz(some);
+    if (step == 1) {
+      r += last;
+      break;
+    }
+    r += last * step;
+    span = min(step, span - last * step);
+  }
+  const int channel = blockIdx.y * 256 + 8 * lane;
+  const bool here = channel < a.channels;
+  ConvLane<T, W> c{a, channel};
+  if (here) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c.bias[e] = a.bias ? a.bias[channel + e] : 0.f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) c.w[j][e] = a.weight[(int64_t)(channel + e) * W + j];
+    }
+  }
+  if (window == 0 && lane == 0 && blockIdx.y == 0 && (a.s.q_start[0] < 0 || a.s.q_start[0] > a.s.tokens)) gdn_flag(KQ_ERR_RANGE);
+  if (before) {
+    const Request q = read_request(a.s, r, a.s.tokens);
+    if (q.status && lane == 0) gdn_flag(q.status);
+    if (q.count) {
+      const int64_t from = (lo - q.first + a.piece - 1) / a.piece * a.piece;
+      if (q.first + from < hi && from < q.count && here) c.piece(q, (int32_t)from);
+    }
+    ++r;
+  }
+  for (; r < a.s.requests; ++r) {
+    const int32_t first = a.s.q_start[r];
+    if (first >= hi) break;
+    const Request q = read_request(a.s, r, a.s.tokens);
+    if (q.status && lane == 0) gdn_flag(q.status);
+    if (q.count && q.first >= lo && here) c.piece(q, 0);
+  }
+}
+
+template <typename T>
+static cudaError_t launch_conv(const ConvArgs& a, int width, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.windows + kConvWarps - 1) / kConvWarps), (unsigned)((a.channels + 255) / 256));
+  const auto k = width == 2 ? conv_kernel<T, 2> : width == 3 ? conv_kernel<T, 3> : conv_kernel<T, 4>;
+  return launch_dependent(k, grid, dim3(32 * kConvWarps), 0, st, a);
+}
+
+// ---- the gated delta rule, token by token ------------------------------------------
+//
+// A state's columns do not know of one another: u_c = beta (v_c - g S_c . k),
+// S_c <- g S_c + k u_c, out_c = S_c . q = g S_c . q + (k . q) u_c with S before.  So
+// a CTA keeps 32 columns of one state in registers, eight rows of four columns a
+// thread, from the first token of its request to the last: the state is read and
+// written once however many tokens there are.  Both products with S before the
+// update are made in the same pass over the registers, and one barrier a token
+// joins the four warps' sums.
+//
+// A decode step is bound by the states' bytes (128 KB a value head read and written
+// at D = 128).
+
+constexpr int kStepThreads = 128, kStepCols = 32;
+constexpr int kStepTokens = 8;  // staged at a time
+
+struct RuleArgs {
+  Rows q, k, v, out;
+  const char* a;
+  const char* b;
+  int64_t a_stride, b_stride;  // bytes
+  Requests s;
+  float* state;
+  const float* a_log;
+  const float* dt_bias;
+  int64_t max_new;
+  int32_t k_heads, v_heads, unit, gates;
+  float eps, scale;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kStepThreads) gdn_step_kernel(const RuleArgs p) {
+  constexpr int kSlices = D / kStepCols, kRows = D / 16;
+  __shared__ __align__(16) float s_k[kStepTokens][D], s_q[kStepTokens][D], s_v[kStepTokens][kStepCols];
+  __shared__ float s_g[kStepTokens], s_beta[kStepTokens], s_kq[kStepTokens];
+  __shared__ __align__(16) float s_part[2][4][2][kStepCols];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int slice = blockIdx.x % kSlices, h = blockIdx.x / kSlices % p.v_heads;
+  const int64_t r = blockIdx.x / kSlices / p.v_heads;
+  const Request req = read_request(p.s, r, p.max_new);
+  if (req.status && tid == 0) gdn_flag(req.status);
+  if (!req.count) return;
+  const int hk = h / (p.v_heads / p.k_heads);
+  const int row0 = (warp * 4 + lane / 8) * kRows, col = (lane % 8) * 4, col0 = slice * kStepCols;
+  float* state = p.state + ((int64_t)req.slot * p.v_heads + h) * D * D + (int64_t)row0 * D + col0 + col;
+  float4 S[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    S[i] = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(state + (int64_t)i * D);
+  int turn = 0;
+  for (int32_t t0 = 0; t0 < req.count; t0 += kStepTokens) {
+    const int n = min(kStepTokens, req.count - t0);
+    __syncthreads();  // the tokens before are done with
+    for (int e = tid; e < kStepTokens * (D / 8); e += kStepThreads) {
+      const int t = e / (D / 8), vec = e % (D / 8);
+      const int64_t token = (int64_t)req.first + t0 + t;
+      float kk[8], qq[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) kk[i] = qq[i] = 0.f;
+      if (t < n) {
+        kv::load8(reinterpret_cast<const T*>(p.k.at(token, hk)) + 8 * vec, kk);
+        kv::load8(reinterpret_cast<const T*>(p.q.at(token, hk)) + 8 * vec, qq);
+      }
+      float k2 = 0.f, q2 = 0.f, kq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k2 = fmaf(kk[i], kk[i], k2), q2 = fmaf(qq[i], qq[i], q2), kq = fmaf(kk[i], qq[i], kq);
+#pragma unroll
+      for (int o = D / 16; o; o >>= 1) {
+        k2 += __shfl_xor_sync(~0u, k2, o);
+        q2 += __shfl_xor_sync(~0u, q2, o);
+        kq += __shfl_xor_sync(~0u, kq, o);
+      }
+      const float fk = p.unit ? 1.0f / sqrtf(k2 + p.eps) : 1.f, fq = p.unit ? p.scale / sqrtf(q2 + p.eps) : p.scale;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) kk[i] *= fk, qq[i] *= fq;
+      kv::store8(&s_k[t][8 * vec], kk);
+      kv::store8(&s_q[t][8 * vec], qq);
+      if (vec == 0) s_kq[t] = kq * fk * fq;
+    }
+    for (int e = tid; e < kStepTokens * kStepCols; e += kStepThreads) {
+      const int t = e / kStepCols, c = e % kStepCols;
+      if (t < n)
+        s_v[t][c] = kv::to_float(reinterpret_cast<const T*>(p.v.at((int64_t)req.first + t0 + t, h))[col0 + c]);
+    }
+    if (tid < n) {
+      const int64_t token = (int64_t)req.first + t0 + tid;
+      const float a = kv::to_float(reinterpret_cast<const T*>(p.a + token * p.a_stride)[h]);
+      const float b = kv::to_float(reinterpret_cast<const T*>(p.b + token * p.b_stride)[h]);
+      s_g[tid] = expf(p.gates ? log_decay(a, p.a_log[h], p.dt_bias[h]) : a);
+      s_beta[tid] = p.gates ? sigmoid(b) : b;
+    }
+    __syncthreads();
+    for (int t = 0; t < n; ++t, turn ^= 1) {
+      float kr[kRows], qr[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; i += 4) kv::load4(&s_k[t][row0 + i], kr + i), kv::load4(&s_q[t][row0 + i], qr + i);
+      float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), qs = ks;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        ks.x = fmaf(kr[i], S[i].x, ks.x), ks.y = fmaf(kr[i], S[i].y, ks.y);
+        ks.z = fmaf(kr[i], S[i].z, ks.z), ks.w = fmaf(kr[i], S[i].w, ks.w);
+        qs.x = fmaf(qr[i], S[i].x, qs.x), qs.y = fmaf(qr[i], S[i].y, qs.y);
+        qs.z = fmaf(qr[i], S[i].z, qs.z), qs.w = fmaf(qr[i], S[i].w, qs.w);
+      }
+#pragma unroll
+      for (int o = 8; o < 32; o *= 2) {
+        ks.x += __shfl_xor_sync(~0u, ks.x, o), ks.y += __shfl_xor_sync(~0u, ks.y, o);
+        ks.z += __shfl_xor_sync(~0u, ks.z, o), ks.w += __shfl_xor_sync(~0u, ks.w, o);
+        qs.x += __shfl_xor_sync(~0u, qs.x, o), qs.y += __shfl_xor_sync(~0u, qs.y, o);
+        qs.z += __shfl_xor_sync(~0u, qs.z, o), qs.w += __shfl_xor_sync(~0u, qs.w, o);
+      }
+      if (lane < 8) {
+        *reinterpret_cast<float4*>(&s_part[turn][warp][0][col]) = ks;
+        *reinterpret_cast<float4*>(&s_part[turn][warp][1][col]) = qs;
+      }
+      __syncthreads();
+      ks = qs = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&s_part[turn][w][0][col]);
+        const float4 y = *reinterpret_cast<const float4*>(&s_part[turn][w][1][col]);
+        ks.x += x.x, ks.y += x.y, ks.z += x.z, ks.w += x.w;
+        qs.x += y.x, qs.y += y.y, qs.z += y.z, qs.w += y.w;
+      }
+      const float g = s_g[t], beta = s_beta[t], kq = s_kq[t];
+      float4 u = *reinterpret_cast<const float4*>(&s_v[t][col]);
+      u.x = beta * fmaf(-g, ks.x, u.x), u.y = beta * fmaf(-g, ks.y, u.y);
+      u.z = beta * fmaf(-g, ks.z, u.z), u.w = beta * fmaf(-g, ks.w, u.w);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        S[i].x = fmaf(kr[i], u.x, g * S[i].x), S[i].y = fmaf(kr[i], u.y, g * S[i].y);
+        S[i].z = fmaf(kr[i], u.z, g * S[i].z), S[i].w = fmaf(kr[i], u.w, g * S[i].w);
+      }
+      if (tid < 8) {
+        const float o[4] = {fmaf(kq, u.x, g * qs.x), fmaf(kq, u.y, g * qs.y), fmaf(kq, u.z, g * qs.z),
+                            fmaf(kq, u.w, g * qs.w)};
+        kv::store4(reinterpret_cast<T*>(p.out.at((int64_t)req.first + t0 + t, h)) + col0 + col, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(state + (int64_t)i * D) = S[i];
+}
+
+template <typename T>
+static cudaError_t launch_step(const RuleArgs& a, int head_dim, cudaStream_t st) {
+  const int64_t grid = a.s.requests * a.v_heads * (head_dim / kStepCols);
+  const auto k = head_dim == 64 ? gdn_step_kernel<T, 64> : gdn_step_kernel<T, 128>;
+  return launch_dependent(k, dim3((unsigned)grid), dim3(kStepThreads), 0, st, a);
+}
+
+}  // namespace gdn
+
+int read_gdn_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, gdn::g_gdn_status, sizeof(v)) != cudaSuccess) return -1;
+  if (clear && v) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(gdn::g_gdn_status, &z, sizeof(z)) != cudaSuccess) return -1;
+  }
+  return (int)v;
+}
+
+static int check_requests(const int32_t* q_start, const int32_t* kv_len, const int32_t* slot, int64_t requests,
+                          int64_t tokens, const void* state, int64_t slots) {
+  if (requests < 1 || requests > 0x7fffffffll - 1 || tokens < 0 || tokens > 0x7fffffffll || slots < 1 || slots > 0x7fffffffll)
+    return fail(KQ_ERR_SHAPE, "requests = %lld, tokens = %lld, slots = %lld", (long long)requests, (long long)tokens,
+                (long long)slots);
+  if (!q_start || !slot || !state) return fail(KQ_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(q_start) || !aligned16(kv_len) || !aligned16(slot) || !aligned16(state))
+    return fail(KQ_ERR_ALIGNMENT, "q_start, kv_len, slot or state not 16-byte aligned");
+  return KQ_OK;
+}
+
+// Whether rows of `wide` bytes of the two views share a byte; side by side in rows of one stride they do not.
+static bool overlap(const gdn::Rows& x, const gdn::Rows& y, int64_t rows, int64_t wide) {
+  const char* x1 = x.data + (rows - 1) * x.token_stride + wide;
+  const char* y1 = y.data + (rows - 1) * y.token_stride + wide;
+  if (x.data >= y1 || y.data >= x1) return false;
+  const int64_t stride = x.token_stride;
+  if (rows == 1 || stride != y.token_stride || stride == 0) return true;
+  const int64_t off = ((y.data - x.data) % stride + stride) % stride;
+  return off < wide || off + wide > stride;
+}
+
+static int check_rule(const kq_gdn_rule* p) {
+  if (!p) return fail(KQ_ERR_INVALID_ARG, "p is NULL");
+  if (p->reserved != 0 || (p->unit != 0 && p->unit != 1) || (p->gates != 0 && p->gates != 1))
+    return fail(KQ_ERR_INVALID_ARG, "unit and gates are 0 or 1, reserved is 0");
+  if (p->head_dim != 64 && p->head_dim != 128) return fail(KQ_ERR_SHAPE, "head_dim = %d (64 or 128)", p->head_dim);
+  if (p->k_heads < 1 || p->v_heads < 1 || p->v_heads > 4096 || p->v_heads % p->k_heads)
+    return fail(KQ_ERR_SHAPE, "%d value heads on %d key heads", p->v_heads, p->k_heads);
+  if (!(p->eps >= 0.f && std::isfinite(p->eps)) || !std::isfinite(p->scale))
+    return fail(KQ_ERR_INVALID_ARG, "eps is negative, or eps or scale not finite");
+  if (p->gates != (p->a_log != nullptr) || p->gates != (p->dt_bias != nullptr))
+    return fail(KQ_ERR_INVALID_ARG, "a_log and dt_bias come with gates = 1, and only then");
+  if ((p->a_log && !aligned16(p->a_log)) || (p->dt_bias && !aligned16(p->dt_bias)))
+    return fail(KQ_ERR_ALIGNMENT, "a_log or dt_bias not 16-byte aligned");
+  return KQ_OK;
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" {
+
+int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t* d_q_start, const int32_t* d_kv_len,
+                   const int32_t* d_slot, int64_t requests, int64_t tokens, void* d_state, int64_t slots,
+                   const kq_heads* out, void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (!p || !p->weight) return fail(KQ_ERR_INVALID_ARG, "p or its weight is NULL");
+  if (p->reserved != 0 || (p->silu != 0 && p->silu != 1)) return fail(KQ_ERR_INVALID_ARG, "silu is 0 or 1, reserved is 0");
+  if (p->channels < 8 || p->channels % 8 || p->channels > (1 << 20) || p->width < 2 || p->width > 4)
+    return fail(KQ_ERR_SHAPE, "%d channels (a multiple of 8 up to 2^20), width %d (2 to 4)", p->channels, p->width);
+  if (!aligned16(p->weight) || !aligned16(p->bias)) return fail(KQ_ERR_ALIGNMENT, "weight or bias not 16-byte aligned");
+  if (int s = check_requests(d_q_start, d_kv_len, d_slot, requests, tokens, d_state, slots)) return s;
+  if (tokens == 0) return KQ_OK;
+  if (int s = check_heads(x, "x", dtype)) return s;
+  if (int s = check_out_rows(out, "out", dtype, tokens, 1, p->channels)) return s;
+  const int size = dtype == KQ_F32 ? 4 : 2;
+  gdn::ConvArgs a{};
+  a.x = gdn::rows_of(x, size), a.out = gdn::rows_of(out, size);
+  if (overlap(a.x, a.out, tokens, (int64_t)p->channels * size)) return fail(KQ_ERR_INVALID_ARG, "out overlaps x");
+  a.s = gdn::Requests{d_q_start, d_kv_len, d_slot, requests, tokens, slots};
+  a.state = static_cast<char*>(d_state), a.weight = p->weight, a.bias = p->bias;
+  a.channels = p->channels, a.silu = p->silu;
+  // few tokens: a piece a warp, so that no request waits for another; many: pieces long enough that what lies before them
+  // is read again for a tenth
+  a.piece = tokens <= 1024 ? 4 : 32, a.window = tokens <= 1024 ? 1 : 32;
+  a.windows = (tokens + a.window - 1) / a.window;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_conv<float>(a, p->width, st)
+              : dtype == KQ_F16 ? gdn::launch_conv<__half>(a, p->width, st)
+                                : gdn::launch_conv<__nv_bfloat16>(a, p->width, st));
+  return KQ_OK;
+}
+
+size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests, int64_t tokens, int64_t max_new) {
+  (void)p, (void)dtype, (void)requests, (void)tokens, (void)max_new;
+  return 0;
+}
+
+int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k, const kq_heads* v, const void* d_a,
+           int64_t a_stride, const void* d_b, int64_t b_stride, const int32_t* d_q_start, const int32_t* d_kv_len,
+           const int32_t* d_slot, int64_t requests, int64_t tokens, int64_t max_new, float* d_state, int64_t slots,
+           const kq_heads* out, void* d_ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (int s = check_rule(p)) return s;
+  if (int s = check_requests(d_q_start, d_kv_len, d_slot, requests, tokens, d_state, slots)) return s;
+  if (max_new < 0 || a_stride < 0 || b_stride < 0 || requests > 0x7fffffffll / (4 * p->v_heads))
+    return fail(KQ_ERR_SHAPE, "max_new = %lld, a_stride = %lld, b_stride = %lld, %lld requests of %d heads",
+                (long long)max_new, (long long)a_stride, (long long)b_stride, (long long)requests, p->v_heads);
+  if (tokens == 0) return KQ_OK;
+  if (!d_a || !d_b) return fail(KQ_ERR_INVALID_ARG, "a or b is NULL");
+  const int size = dtype == KQ_F32 ? 4 : 2;
+  if ((uintptr_t)d_a % size || (uintptr_t)d_b % size) return fail(KQ_ERR_ALIGNMENT, "a or b not aligned to its type");
+  if (int s = check_heads(q, "q", dtype)) return s;
+  if (int s = check_heads(k, "k", dtype)) return s;
+  if (int s = check_heads(v, "v", dtype)) return s;
+  if (int s = check_out_rows(out, "out", dtype, tokens, p->v_heads, p->head_dim)) return s;
+  gdn::RuleArgs a{};
+  a.q = gdn::rows_of(q, size), a.k = gdn::rows_of(k, size), a.v = gdn::rows_of(v, size), a.out = gdn::rows_of(out, size);
+  a.a = static_cast<const char*>(d_a), a.b = static_cast<const char*>(d_b);
+  a.a_stride = a_stride * size, a.b_stride = b_stride * size;
+  a.s = gdn::Requests{d_q_start, d_kv_len, d_slot, requests, tokens, slots};
+  a.state = d_state, a.a_log = p->a_log, a.dt_bias = p->dt_bias, a.max_new = max_new;
+  a.k_heads = p->k_heads, a.v_heads = p->v_heads, a.unit = p->unit, a.gates = p->gates, a.eps = p->eps, a.scale = p->scale;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_step<float>(a, p->head_dim, st)
+              : dtype == KQ_F16 ? gdn::launch_step<__half>(a, p->head_dim, st)
+                                : gdn::launch_step<__nv_bfloat16>(a, p->head_dim, st));
+  (void)d_ws, (void)ws_bytes;
+  return KQ_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,66 @@
+// What the delta layers' kernels share: strided rows and the step's requests.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kq.h"
+
+namespace kq {
+namespace gdn {
+
+// Rows of heads in bytes (data null: not there).
+struct Rows {
+  char* data;
+  int64_t token_stride, head_stride;
+  __device__ __forceinline__ char* at(int64_t token, int head) const {
+    return data + token * token_stride + head * head_stride;
+  }
+};
+inline Rows rows_of(const kq_heads* h, int size) {
+  return h ? Rows{static_cast<char*>(h->data), h->token_stride * size, h->head_stride * size} : Rows{nullptr, 0, 0};
+}
+
+struct Requests {
+  const int32_t* q_start;
+  const int32_t* kv_len;  // or null
+  const int32_t* slot;
+  int64_t requests, tokens, slots;
+};
+
+// A request as it is computed: tokens first .. first + count - 1, none where it is skipped or left out.
+struct Request {
+  int32_t first, count, slot;
+  bool fresh;
+  int status;  // what the device status is told: 0 or KQ_ERR_RANGE
+};
+__device__ __forceinline__ Request read_request(const Requests& s, int64_t r, int64_t max_new) {
+  Request q{};
+  const int32_t lo = s.q_start[r], hi = s.q_start[r + 1], slot = s.slot[r];
+  const int64_t n = (int64_t)hi - lo;
+  if (lo < 0 || n < 0 || hi > s.tokens || n > max_new || slot >= s.slots) {
+    q.status = KQ_ERR_RANGE;
+    return q;
+  }
+  if (slot < 0 || n == 0) return q;
+  q.first = lo, q.count = (int32_t)n, q.slot = slot;
+  q.fresh = s.kv_len && s.kv_len[r] == q.count;
+  return q;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// The logarithm of a token's decay from its gate.
+__device__ __forceinline__ float log_decay(float a, float a_log, float dt_bias) {
+  const float x = a + dt_bias;
+  return -expf(a_log) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
+}
+
+}  // namespace gdn
+
+// check_heads of rows that are written: no two may share an element (kq_norm.cu).
+int check_out_rows(const kq_heads* h, const char* name, int dtype, int64_t tokens, int heads, int dim);
+int read_norm_status(int clear);
+int read_gdn_status(int clear);
+int read_sample_status(int clear);
+
+}  // namespace kq

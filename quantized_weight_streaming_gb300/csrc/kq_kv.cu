@@ -722,7 +722,7 @@ kv::Cache cache_view(const kq_kv_cache* c) {
                    c->kv_heads};
 }
 
-static int check_dtype(int dtype) {
+int check_dtype(int dtype) {
   if (dtype != KQ_F32 && dtype != KQ_F16 && dtype != KQ_BF16) return fail(KQ_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   return KQ_OK;
 }

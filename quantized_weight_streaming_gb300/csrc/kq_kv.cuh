@@ -177,7 +177,8 @@ __device__ __forceinline__ void store4(T* p, const float* v) {
 
 // ---- host side -----------------------------------------------------------------
 
-// Checks a cache descriptor / a heads view of `dtype` elements (kq_kv.cu).
+// Checks an activation type / a cache descriptor / a heads view of `dtype` elements (kq_kv.cu).
+int check_dtype(int dtype);
 int check_cache(const kq_kv_cache* c);
 int check_heads(const kq_heads* h, const char* name, int dtype);
 kv::Cache cache_view(const kq_kv_cache* c);

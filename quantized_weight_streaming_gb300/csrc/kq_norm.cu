@@ -1,0 +1,259 @@
+// RMS norm of rows, with the residual's addition before it, a gate after it and
+// an output in Q8_0 beside the one in the activations' type.
+//
+//   s = x + residual;  y = s / sqrt(mean(s^2) + eps) * weight * silu(gate)
+//
+// Two flops a byte: memory bounds it, so a row is read once and stays in
+// registers between the sum of its squares and the output.  A thread holds
+// vectors of eight elements.  A row of up to 256 elements (a head) belongs to 8,
+// 16 or 32 lanes, who add their squares by shuffles; a longer one to a CTA, with
+// one barrier a row.  Rows are walked with the grid's stride, so that the weight
+// (which, in fp32, is as long as a row of 16-bit activations and its output
+// together) is read once a CTA and kept.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kq_device.cuh"
+#include "kq_gdn.cuh"
+#include "kq_internal.h"
+#include "kq_kv.cuh"
+
+namespace kq {
+namespace norm {
+
+using gdn::Rows;
+
+__device__ unsigned int g_norm_status = 0;
+__device__ __forceinline__ void norm_flag(int status) { atomicOr(&g_norm_status, 1u << status); }
+
+struct Args {
+  Rows x, residual, gate, out;
+  int8_t* codes;     // of Q8_0, or null
+  uint16_t* scales;
+  const float* weight;
+  int64_t rows;
+  int32_t heads, dim;
+  int32_t scale_stride;
+  float eps;
+};
+
+// Code of |v| / d, rounded half away from zero by what the quotient is and not what a division rounds it to: the
+// estimate is moved by one where the exact sign of |v| - (n - 1/2) d (20 bits of product, one rounding) says so.
+__device__ __forceinline__ int q8_code(float v, float d, float inverse) {
+  const float m = fabsf(v);
+  float n = floorf(fmaf(m, inverse, 0.5f));
+  n = fminf(n, 128.f);
+  if (fmaf(-(n - 0.5f), d, m) < 0.f) n -= 1.f;
+  if (fmaf(-(n + 0.5f), d, m) >= 0.f) n += 1.f;
+  const int q = (int)fminf(n, 127.f);
+  return v < 0.f ? -q : q;
+}
+
+// Eight values of a block of 32, its other 24 in the three neighbouring lanes; `valid` is the same in all four.
+__device__ __forceinline__ void store_q8(const Args& a, int64_t row, int vec, const float (&y)[8], bool valid) {
+  float most = 0.f;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(y[i])), odd |= !isfinite(y[i]);
+  most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+  most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+  const unsigned bad = __ballot_sync(~0u, odd && valid) >> (threadIdx.x & 28) & 15u;
+  if (!valid) return;
+  __half s = __float2half_rn(most / 127.0f);
+  if (bad || __hisinf(s)) {
+    norm_flag(bad ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
+    s = __ushort_as_half(0x7E00);
+  }
+  const float d = __half2float(s);
+  union { int8_t c[8]; uint2 u; } q;
+  if (d > 0.f) {
+    const float inverse = 1.0f / d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q.c[i] = (int8_t)q8_code(y[i], d, inverse);
+  } else {
+    q.u = make_uint2(0, 0);
+  }
+  *reinterpret_cast<uint2*>(a.codes + row * a.dim + 8 * vec) = q.u;
+  if ((threadIdx.x & 3) == 0) {
+    uint16_t* at = a.scales + row * a.scale_stride;
+    at[vec / 4] = __half_as_ushort(s);
+    if (8 * vec + 32 == a.dim)
+      for (int i = a.dim / 32; i < a.scale_stride; ++i) at[i] = 0;
+  }
+}
+
+// LANES: lanes of a row, 0 for the whole CTA.  N vectors a thread.
+template <typename T, int LANES, int N>
+__global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args a) {
+  __shared__ float s_part[2][32];
+  constexpr int kRows = LANES ? 256 / (LANES ? LANES : 1) : 1;  // rows that a CTA has at a time
+  const int step = LANES ? LANES : blockDim.x;
+  const int first = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
+  const int vecs = a.dim / 8;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  float w[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
+    if (a.weight && first + i * step < vecs) kv::load8(a.weight + 8 * (first + i * step), w[i]);
+  }
+  const int64_t ahead = (int64_t)gridDim.x * kRows;
+  int turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += ahead, turn ^= 1) {
+    const int64_t row = base + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
+    const bool here = row < a.rows;
+    const int64_t token = row / a.heads;
+    const int head = (int)(row - token * a.heads);
+    const T* x = reinterpret_cast<const T*>(a.x.at(token, head));
+    T* res = reinterpret_cast<T*>(a.residual.at(token, head));
+    const T* gate = reinterpret_cast<const T*>(a.gate.at(token, head));
+    kv::Raw<T, 8> raw[N], other[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int vec = first + i * step;
+      raw[i].clear();
+      other[i].clear();
+      if (!here || vec >= vecs) continue;
+      raw[i].load(x + 8 * vec);
+      if (a.residual.data) other[i].load(res + 8 * vec);
+      else if (a.gate.data) other[i].load(gate + 8 * vec);
+    }
+    float v[N][8], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int vec = first + i * step;
+      raw[i].get(v[i]);
+      if (a.residual.data) {
+        float r[8];
+        other[i].get(r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = kv::to_float(kv::from_float<T>(v[i][e] + r[e]));
+        if (here && vec < vecs) kv::store8(res + 8 * vec, v[i]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
+    }
+#pragma unroll
+    for (int o = (LANES ? LANES : 32) / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (!LANES) {
+      if (threadIdx.x % 32 == 0) s_part[turn][threadIdx.x / 32] = sum;
+      __syncthreads();
+      sum = 0.f;
+      const int warps = blockDim.x / 32;
+      if (threadIdx.x % 32 < warps) sum = s_part[turn][threadIdx.x % 32];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    }
+    const float f = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int vec = first + i * step;
+      const bool mine = here && vec < vecs;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[i][e];
+      if (a.gate.data) {
+        float z[8];
+        if (a.residual.data && mine) other[i].load(gate + 8 * vec);
+        other[i].get(z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] *= z[e] / (1.0f + expf(-z[e]));
+      }
+      if (a.codes) store_q8(a, row, vec, v[i], mine);
+      if (a.out.data && mine) kv::store8(reinterpret_cast<T*>(a.out.at(token, head)) + 8 * vec, v[i]);
+    }
+  }
+}
+
+template <typename T, int LANES, int N>
+static cudaError_t launch(const Args& a, int64_t ctas, int threads, cudaStream_t st) {
+  if (ctas <= 304) return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)ctas), dim3(threads), 0, st, a);
+  int resident = 0;
+  if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, rms_norm_kernel<T, LANES, N>, threads, 0))
+    return e;
+  const int64_t most = 152ll * std::max(1, resident);
+  // every CTA the same number of rows, as near as it goes
+  const int64_t turns = (ctas + most - 1) / most;
+  const int64_t grid = (ctas + turns - 1) / turns;
+  return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)grid), dim3(threads), 0, st, a);
+}
+
+template <typename T>
+static cudaError_t launch_norm(const Args& a, cudaStream_t st) {
+  const int vecs = a.dim / 8;
+  if (vecs <= 8) return launch<T, 8, 1>(a, (a.rows + 31) / 32, 256, st);
+  if (vecs <= 16) return launch<T, 16, 1>(a, (a.rows + 15) / 16, 256, st);
+  if (vecs <= 32) return launch<T, 32, 1>(a, (a.rows + 7) / 8, 256, st);
+  auto threads = [&](int n) { return (vecs + 32 * n - 1) / (32 * n) * 32; };
+  if (vecs <= 1024 && (a.rows <= 304 || vecs <= 128)) return launch<T, 0, 1>(a, a.rows, threads(1), st);
+  if (vecs <= 2048) return launch<T, 0, 2>(a, a.rows, threads(2), st);
+  return launch<T, 0, 4>(a, a.rows, threads(4), st);
+}
+
+}  // namespace norm
+
+int check_out_rows(const kq_heads* h, const char* name, int dtype, int64_t tokens, int heads, int dim) {
+  if (int s = check_heads(h, name, dtype)) return s;
+  if ((tokens > 1 && h->token_stride < dim) || (heads > 1 && h->head_stride < dim))
+    return fail(KQ_ERR_SHAPE, "rows of %s overlap", name);
+  return KQ_OK;
+}
+
+int read_norm_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, norm::g_norm_status, sizeof(v)) != cudaSuccess) return -1;
+  if (clear && v) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(norm::g_norm_status, &z, sizeof(z)) != cudaSuccess) return -1;
+  }
+  return (int)v;
+}
+
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" int kq_rms_norm(const kq_rms* p, int dtype, const kq_heads* x, const kq_heads* residual,
+                           const kq_heads* gate, int64_t tokens, const kq_heads* out, const kq_qmat* out_q8,
+                           void* stream) {
+  clear_error();
+  if (int s = check_dtype(dtype)) return s;
+  if (!p) return fail(KQ_ERR_INVALID_ARG, "p is NULL");
+  if (p->reserved != 0) return fail(KQ_ERR_INVALID_ARG, "reserved is not 0");
+  if (p->heads < 1 || p->heads > 4096 || p->dim < 8 || p->dim % 8 || p->dim > 32768)
+    return fail(KQ_ERR_SHAPE, "%d heads of %d (1 to 4096, a multiple of 8 up to 32768)", p->heads, p->dim);
+  if (!(p->eps >= 0.f && std::isfinite(p->eps))) return fail(KQ_ERR_INVALID_ARG, "eps is negative or not finite");
+  if (p->weight && !aligned16(p->weight)) return fail(KQ_ERR_ALIGNMENT, "weight not 16-byte aligned");
+  if (tokens < 0 || tokens > 0x7fffffffll / p->heads) return fail(KQ_ERR_SHAPE, "tokens = %lld", (long long)tokens);
+  if (tokens == 0) return KQ_OK;
+  if (!out && !out_q8) return fail(KQ_ERR_INVALID_ARG, "neither out nor out_q8");
+  if (int s = check_heads(x, "x", dtype)) return s;
+  if (residual)
+    if (int s = check_out_rows(residual, "residual", dtype, tokens, p->heads, p->dim)) return s;
+  if (gate)
+    if (int s = check_heads(gate, "gate", dtype)) return s;
+  if (out)
+    if (int s = check_out_rows(out, "out", dtype, tokens, p->heads, p->dim)) return s;
+  norm::Args a{};
+  if (out_q8) {
+    if (int s = check_qmat(out_q8, KQ_Q8_0)) return s;
+    if (out_q8->n != tokens * p->heads || out_q8->k != p->dim)
+      return fail(KQ_ERR_SHAPE, "out_q8 is %lld x %lld, %lld rows of %d are written", (long long)out_q8->n,
+                  (long long)out_q8->k, (long long)(tokens * p->heads), p->dim);
+    a.codes = static_cast<int8_t*>(const_cast<void*>(static_cast<const void*>(out_q8->codes)));
+    a.scales = static_cast<uint16_t*>(const_cast<void*>(static_cast<const void*>(out_q8->scales)));
+    a.scale_stride = (int32_t)scale_stride(KQ_Q8_0, p->dim);
+  }
+  const int size = dtype == KQ_F32 ? 4 : 2;
+  a.x = gdn::rows_of(x, size), a.residual = gdn::rows_of(residual, size), a.gate = gdn::rows_of(gate, size);
+  a.out = gdn::rows_of(out, size);
+  a.weight = p->weight, a.rows = tokens * p->heads, a.heads = p->heads, a.dim = p->dim, a.eps = p->eps;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  KQ_CUDA_TRY(dtype == KQ_F32   ? norm::launch_norm<float>(a, st)
+              : dtype == KQ_F16 ? norm::launch_norm<__half>(a, st)
+                                : norm::launch_norm<__nv_bfloat16>(a, st));
+  return KQ_OK;
+}
