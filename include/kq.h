@@ -727,8 +727,8 @@ typedef struct {
  *    alone.
  *  - On the device: a slot past the states, a q_start that decreases, is
  *    negative or passes `tokens` (or more new tokens than max_new, where there is one) sets
- *    KQ_ERR_RANGE for kq_device_status; the request is left out, and of the
- *    others of a call with such a q_start any may be.
+ *    KQ_ERR_RANGE for kq_device_status; the request is left out, and what the
+ *    others of a call with such a q_start get is unspecified.
  *  - Two requests of one call must not share a slot. */
 
 /* x, out: rows of `channels` elements of `dtype` (head_stride unused), `tokens`

@@ -190,20 +190,6 @@ static cudaError_t launch_conv(const ConvArgs& a, int width, cudaStream_t st) {
 constexpr int kStepThreads = 128, kStepCols = 32;
 constexpr int kStepTokens = 8;  // staged at a time
 
-struct RuleArgs {
-  Rows q, k, v, out;
-  const char* a;
-  const char* b;
-  int64_t a_stride, b_stride;  // bytes
-  Requests s;
-  float* state;
-  const float* a_log;
-  const float* dt_bias;
-  int64_t max_new;
-  int32_t k_heads, v_heads, unit, gates;
-  float eps, scale;
-};
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kStepThreads) gdn_step_kernel(const RuleArgs p) {
   constexpr int kSlices = D / kStepCols, kRows = D / 16;
@@ -217,7 +203,7 @@ __global__ void __launch_bounds__(kStepThreads) gdn_step_kernel(const RuleArgs p
   const int64_t r = blockIdx.x / kSlices / p.v_heads;
   const Request req = read_request(p.s, r, p.max_new);
   if (req.status && tid == 0) gdn_flag(req.status);
-  if (!req.count) return;
+  if (!req.count || req.count > p.short_most) return;
   const int hk = h / (p.v_heads / p.k_heads);
   const int row0 = (warp * 4 + lane / 8) * kRows, col = (lane % 8) * 4, col0 = slice * kStepCols;
   float* state = p.state + ((int64_t)req.slot * p.v_heads + h) * D * D + (int64_t)row0 * D + col0 + col;
@@ -336,7 +322,8 @@ int read_gdn_status(int clear) {
     const unsigned int z = 0;
     if (cudaMemcpyToSymbol(gdn::g_gdn_status, &z, sizeof(z)) != cudaSuccess) return -1;
   }
-  return (int)v;
+  const int w = gdn::prompt_status(clear);
+  return w < 0 ? -1 : (int)v | w;
 }
 
 static int check_requests(const int32_t* q_start, const int32_t* kv_len, const int32_t* slot, int64_t requests,
@@ -375,6 +362,21 @@ static int check_rule(const kq_gdn_rule* p) {
   if ((p->a_log && !aligned16(p->a_log)) || (p->dt_bias && !aligned16(p->dt_bias)))
     return fail(KQ_ERR_ALIGNMENT, "a_log or dt_bias not 16-byte aligned");
   return KQ_OK;
+}
+
+static int check_sizes(const kq_gdn_rule* p, int64_t requests, int64_t tokens, int64_t max_new) {
+  const int64_t most = 0x7fffffffll / (4 * p->v_heads);  // CTAs
+  if (requests < 1 || requests > most / 2 || tokens < 0 || tokens / gdn::kChunk > most / 2 || max_new < 0)
+    return fail(KQ_ERR_SHAPE, "%lld requests, %lld tokens, max_new = %lld, %d heads", (long long)requests, (long long)tokens,
+                (long long)max_new, p->v_heads);
+  return KQ_OK;
+}
+
+// Whether runs longer than kShortRun tokens go in chunks on the tensor cores: 16-bit keys and queries are exact in fp16 but
+// for a power of two, and what is solved and summed in fp16 parts is bounded where keys have unit length and strengths and
+// decays are at most 1.
+static bool in_chunks(const kq_gdn_rule* p, int dtype, int64_t max_new) {
+  return dtype != KQ_F32 && p->head_dim == 128 && p->unit && p->gates && max_new > gdn::kShortRun;
 }
 
 }  // namespace kq
@@ -416,8 +418,9 @@ int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t
 }
 
 size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests, int64_t tokens, int64_t max_new) {
-  (void)p, (void)dtype, (void)requests, (void)tokens, (void)max_new;
-  return 0;
+  clear_error();
+  if (check_dtype(dtype) || check_rule(p) || check_sizes(p, requests, tokens, max_new)) return 0;
+  return in_chunks(p, dtype, max_new) ? (size_t)gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens) : 0;
 }
 
 int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k, const kq_heads* v, const void* d_a,
@@ -428,9 +431,9 @@ int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k
   if (int s = check_dtype(dtype)) return s;
   if (int s = check_rule(p)) return s;
   if (int s = check_requests(d_q_start, d_kv_len, d_slot, requests, tokens, d_state, slots)) return s;
-  if (max_new < 0 || a_stride < 0 || b_stride < 0 || requests > 0x7fffffffll / (4 * p->v_heads))
-    return fail(KQ_ERR_SHAPE, "max_new = %lld, a_stride = %lld, b_stride = %lld, %lld requests of %d heads",
-                (long long)max_new, (long long)a_stride, (long long)b_stride, (long long)requests, p->v_heads);
+  if (int s = check_sizes(p, requests, tokens, max_new)) return s;
+  if (a_stride < 0 || b_stride < 0)
+    return fail(KQ_ERR_SHAPE, "a_stride = %lld, b_stride = %lld", (long long)a_stride, (long long)b_stride);
   if (tokens == 0) return KQ_OK;
   if (!d_a || !d_b) return fail(KQ_ERR_INVALID_ARG, "a or b is NULL");
   const int size = dtype == KQ_F32 ? 4 : 2;
@@ -447,10 +450,19 @@ int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k
   a.state = d_state, a.a_log = p->a_log, a.dt_bias = p->dt_bias, a.max_new = max_new;
   a.k_heads = p->k_heads, a.v_heads = p->v_heads, a.unit = p->unit, a.gates = p->gates, a.eps = p->eps, a.scale = p->scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.short_most = 0x7fffffff;
+  if (in_chunks(p, dtype, max_new)) {
+    const size_t need = gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens);
+    if (!d_ws || ws_bytes < need)
+      return fail(KQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", d_ws ? ws_bytes : (size_t)0, need);
+    if (!aligned16(d_ws)) return fail(KQ_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+    a.short_most = requests == 1 ? 0 : gdn::kShortRun;
+    KQ_CUDA_TRY(gdn::launch_prompt(a, dtype, d_ws, st));
+    if (requests == 1) return KQ_OK;
+  }
   KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_step<float>(a, p->head_dim, st)
               : dtype == KQ_F16 ? gdn::launch_step<__half>(a, p->head_dim, st)
                                 : gdn::launch_step<__nv_bfloat16>(a, p->head_dim, st));
-  (void)d_ws, (void)ws_bytes;
   return KQ_OK;
 }
 

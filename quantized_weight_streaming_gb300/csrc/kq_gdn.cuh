@@ -48,6 +48,28 @@ __device__ __forceinline__ Request read_request(const Requests& s, int64_t r, in
   return q;
 }
 
+struct RuleArgs {
+  Rows q, k, v, out;
+  const char* a;
+  const char* b;
+  int64_t a_stride, b_stride;  // bytes
+  Requests s;
+  float* state;
+  const float* a_log;
+  const float* dt_bias;
+  int64_t max_new;
+  int32_t k_heads, v_heads, unit, gates;
+  float eps, scale;
+  int32_t short_most;  // runs of up to so many tokens go token by token, longer ones in chunks
+};
+
+constexpr int kChunk = 64;     // tokens that a prompt is worked through in at a time
+constexpr int kShortRun = 16;  // tokens that are faster one by one
+
+int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens);
+cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st);
+int prompt_status(int clear);
+
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 // The logarithm of a token's decay from its gate.
 __device__ __forceinline__ float log_decay(float a, float a_log, float dt_bias) {

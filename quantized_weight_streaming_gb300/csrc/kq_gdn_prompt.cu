@@ -1,0 +1,590 @@
+// The gated delta rule over prompts of 16-bit types, in chunks of 64 tokens, on
+// the 5th-generation tensor cores.
+//
+// Within a chunk, with G_i the product of the decays up to token i and k, q unit
+// rows, the updates u of all tokens solve one triangular system:
+//
+//   U = T R,  R_i = beta_i (v_i - G_i S^T k_i),  T = (1 + L)^-1,
+//   L_ij = beta_i (G_i / G_j) k_i . k_j  for j < i
+//   O_i = G_i S^T q_i + (X R)_i,  X = P T,  P_ij = (G_i / G_j) q_i . k_j  for j <= i
+//   S <- G_64 S + sum_j (G_64 / G_j) k_j u_j^T
+//
+// T and X do not depend on the state: gdn_chunk_kernel makes them for all chunks of
+// a call at once.  gdn_prompt_kernel then walks down each request's chunks with a
+// state's columns (64 of 128 a CTA) in registers, three matrix products a chunk:
+//
+//   D1 = [K; Q] S      128 x 64 x 128
+//   D2 = [T; X] R      128 x 64 x 64     U over its first rows, the rest of O below
+//   D3 = K^T (w U)     128 x 64 x 64
+//
+// The states are fp32 and stay so.  K and Q enter as they came (a power of two per
+// row away: exact in fp16), their norms and decays as fp32 factors of rows; what is
+// not exact in fp16 (S, T, X, R, U) enters as two fp16 parts, 22 bits.  Products of
+// two such leave out the one of the low parts.  D3 is added to S in registers, with
+// fp32's rounding (the tensor cores' sums cut off instead, and a state that adds
+// up over thousands of tokens would drift).  S, R and U share a power of two per
+// chunk and CTA that keeps them within fp16: |u_i| <= 64 max|v| + |S| because no
+// step of the rule lets a column grow by more than |v| (|k| <= 1, beta < 1, decays
+// of at most 1).
+//
+// T's columns and X's rows (x (1 + L) = p) are solved by a thread each, side by
+// side in four warps, in registers.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "kq_device.cuh"
+#include "kq_gdn.cuh"
+#include "kq_internal.h"
+#include "kq_kv.cuh"
+#include "kq_tcgen05.cuh"
+
+namespace kq {
+namespace gdn {
+
+using namespace tc;
+
+__device__ unsigned int g_prompt_status = 0;
+__device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_status, 1u << status); }
+
+constexpr int kD = 128, kCols = 64;     // head dimension; a CTA's columns
+constexpr int kTile = 32768;            // bytes of [K; Q], or of [T; X] in two parts
+constexpr int kRowFactors = 4 * kChunk + 4;
+
+struct PromptArgs {
+  RuleArgs r;
+  uint8_t* kq;      // [slot][key head] tiles
+  uint8_t* tx;      // [slot][value head] tiles
+  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64
+};
+
+// Where a request's chunks lie among the slots: q_start / 64 + r is at least the slots of the requests before it.
+__device__ __forceinline__ int64_t chunk_base(int64_t first, int64_t r) { return first / kChunk + r; }
+
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two numbers as high and low fp16 parts.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  hi = h2_bits(h);
+  lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+}
+
+constexpr int kStride = kChunk + 4;  // of the triangular matrices' rows, in floats
+constexpr int kTriangle = kChunk * kStride * 4;
+constexpr int kChunkSmem = 3 * kTriangle;
+static_assert(kChunkSmem >= kTile, "the triangles lie over the tile");
+
+// One chunk and value head: the tile of its keys and queries, T and X, the rows' factors.
+template <typename T>
+__global__ void __launch_bounds__(128) gdn_chunk_kernel(const PromptArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
+  __shared__ double s_first;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const RuleArgs& a = p.r;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.x % a.v_heads;
+  const int64_t slot = blockIdx.x / a.v_heads;
+  // the last request whose chunks begin at or before this slot
+  int64_t r = 0, span = a.s.requests;
+  while (span > 0) {
+    const int64_t step = (span + 31) / 32, at = r + lane * step;
+    const unsigned some = __ballot_sync(~0u, lane * step < span && chunk_base(max(a.s.q_start[at], 0), at) <= slot);
+    if (!some) return;
+    const int last = 31 - __clz(some);
+    r += last * step;
+    if (step == 1) break;
+    span = min(step, span - last * step);
+  }
+  const Request req = read_request(a.s, r, a.max_new);
+  if (req.status && tid == 0) prompt_flag(req.status);
+  if (!req.count || req.count <= a.short_most) return;
+  const int64_t c = slot - chunk_base(req.first, r);
+  if (c < 0 || c * kChunk >= req.count) return;
+  const int group = a.v_heads / a.k_heads, hk = h / group, n = (int)min((int64_t)kChunk, req.count - c * kChunk);
+  const int64_t first = req.first + c * kChunk;
+  uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kTile;
+
+  for (int e = tid; e < 2 * kChunk * 16; e += 128) {
+    const int row = e / 16, vec = e % 16, i = row % kChunk;
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = 0.f;
+    if (i < n) kv::load8(reinterpret_cast<const T*>((row < kChunk ? a.k : a.q).at(first + i, hk)) + 8 * vec, v);
+    float most = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) most = fmaxf(most, fabsf(v[x]));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    const int power = (int)(__float_as_uint(most) >> 23);
+    const float f = power == 255 || most == 0.f ? 1.f : __uint_as_float((uint32_t)max(254 - power, 1) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] *= f, sum = fmaf(v[x], v[x], sum);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    uint4 u;
+    u.x = h2_bits(__floats2half2_rn(v[0], v[1])), u.y = h2_bits(__floats2half2_rn(v[2], v[3]));
+    u.z = h2_bits(__floats2half2_rn(v[4], v[5])), u.w = h2_bits(__floats2half2_rn(v[6], v[7]));
+    const uint32_t at = vec / 8 * 16384 + swizzled(row, vec % 8);
+    *reinterpret_cast<uint4*>(smem + at) = u;
+    if (h % group == 0) *reinterpret_cast<uint4*>(kq + at) = u;
+    if (vec == 0) (row < kChunk ? s_fk : s_fq)[i] = i < n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
+  }
+
+  // decays: running sums in 64 bits, kept as two floats, for what counts is the difference of two that may be large
+  double g = 0.0;
+  float beta = 0.f;
+  if (tid < kChunk) {
+    if (tid < n) {
+      const int64_t token = first + tid;
+      // e^-200 is nothing in fp32, and sums of 64 such keep 2^-38 of what follows them
+      g = fmaxf(log_decay(kv::to_float(reinterpret_cast<const T*>(a.a + token * a.a_stride)[h]), a.a_log[h], a.dt_bias[h]), -200.f);
+      beta = sigmoid(kv::to_float(reinterpret_cast<const T*>(a.b + token * a.b_stride)[h]));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const double x = __shfl_up_sync(~0u, g, o);
+      if (lane >= o) g += x;
+    }
+    if (tid == 31) s_first = g;
+  }
+  __syncthreads();
+  if (tid < kChunk) {
+    if (tid >= 32) g += s_first;
+    const float hi = (float)g;
+    s_hi[tid] = hi, s_lo[tid] = (float)(g - (double)hi);
+    s_beta[tid] = beta;
+  }
+  __syncthreads();
+
+  // products of keys and of queries with keys: a warp 32 rows
+  float acc[2][8][4] = {};
+  {
+    const uint32_t base = smem_u32(smem);
+#pragma unroll
+    for (int k = 0; k < kD / 16; ++k) {
+      const uint32_t half = base + k / 4 * 16384;
+      uint32_t fa[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        ldmatrix4(fa[m], half + swizzled(warp * 32 + m * 16 + lane % 16, k % 4 * 2 + lane / 16));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
+        uint32_t fb[4];
+        ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma_f16(acc[m][2 * b], fa[m], fb[0], fb[1]);
+          mma_f16(acc[m][2 * b + 1], fa[m], fb[2], fb[3]);
+        }
+      }
+    }
+  }
+  __syncthreads();  // the tile is read: the triangles go over it
+  float* nl = reinterpret_cast<float*>(smem);           // -L, by rows
+  float* nt = nl + kChunk * kStride;                    // -L, by columns
+  float* pp = nt + kChunk * kStride;                    // P, by rows
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = warp * 32 + m * 16 + lane / 4 + e / 2 * 8, i = row % kChunk, j = b * 8 + lane % 4 * 2 + e % 2;
+        const bool keys = row < kChunk;
+        float x = 0.f;
+        if (keys ? j < i : j <= i) {
+          const float ratio = expf((s_hi[i] - s_hi[j]) + (s_lo[i] - s_lo[j]));
+          x = acc[m][b][e] * s_fk[j] * ratio * (keys ? -s_beta[i] * s_fk[i] : a.scale * s_fq[i]);
+        }
+        if (keys) nl[i * kStride + j] = x, nt[j * kStride + i] = x;
+        else pp[i * kStride + j] = x;
+      }
+  __syncthreads();
+
+  uint8_t* tx = p.tx + (slot * a.v_heads + h) * kTile;
+  if (warp < 2) {  // column j of T from its first row down: t_i = [i = j] - sum_m L_im t_m
+    const int j = tid;
+    float2 t[kChunk / 2];
+#pragma unroll
+    for (int m = 0; m < kChunk / 2; ++m) t[m] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      float2 s0 = make_float2(i == j ? 1.f : 0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int m = 0; m < i; m += 4) {  // what lies at and past i is zero
+        const float4 l = *reinterpret_cast<const float4*>(nl + i * kStride + m);
+        s0 = fma2(make_float2(l.x, l.y), t[m / 2], s0);
+        s1 = fma2(make_float2(l.z, l.w), t[m / 2 + 1], s1);
+      }
+      const float x = (s0.x + s1.x) + (s0.y + s1.y);
+      (i % 2 ? t[i / 2].y : t[i / 2].x) = x;
+      const __half hi = __float2half_rn(x);
+      const uint32_t at = swizzled(i, j / 8) + j % 8 * 2;
+      *reinterpret_cast<__half*>(tx + at) = hi;
+      *reinterpret_cast<__half*>(tx + kTile / 2 + at) = __float2half_rn(x - __half2float(hi));
+    }
+  } else {  // row i of X from its last column down: x_j = P_ij - sum_{m > j} x_m L_mj
+    const int i = tid - 64;
+    float2 x[kChunk / 2];
+#pragma unroll
+    for (int m = 0; m < kChunk / 2; ++m) x[m] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = kChunk - 1; j >= 0; --j) {
+      float2 s0 = make_float2(pp[i * kStride + j], 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int m = j / 4 * 4; m < kChunk; m += 4) {  // what lies at and before j is zero
+        const float4 l = *reinterpret_cast<const float4*>(nt + j * kStride + m);
+        s0 = fma2(make_float2(l.x, l.y), x[m / 2], s0);
+        s1 = fma2(make_float2(l.z, l.w), x[m / 2 + 1], s1);
+      }
+      (j % 2 ? x[j / 2].y : x[j / 2].x) = (s0.x + s1.x) + (s0.y + s1.y);
+      if (j % 8 == 0) {
+        uint4 hi, lo;
+        split2(x[j / 2].x, x[j / 2].y, hi.x, lo.x), split2(x[j / 2 + 1].x, x[j / 2 + 1].y, hi.y, lo.y);
+        split2(x[j / 2 + 2].x, x[j / 2 + 2].y, hi.z, lo.z), split2(x[j / 2 + 3].x, x[j / 2 + 3].y, hi.w, lo.w);
+        const uint32_t at = swizzled(64 + i, j / 8);
+        *reinterpret_cast<uint4*>(tx + at) = hi;
+        *reinterpret_cast<uint4*>(tx + kTile / 2 + at) = lo;
+      }
+    }
+  }
+  if (tid < kChunk) {
+    float* f = p.factors + (slot * a.v_heads + h) * kRowFactors;
+    const float decay = expf(s_hi[tid]), beta_i = s_beta[tid], fk = s_fk[tid];
+    f[tid] = beta_i * decay * fk;
+    f[kChunk + tid] = beta_i;
+    f[2 * kChunk + tid] = fk * expf((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
+    f[3 * kChunk + tid] = a.scale * decay * s_fq[tid];
+    if (tid == 0) f[4 * kChunk] = expf(s_hi[kChunk - 1]);
+  }
+}
+
+// ---- the walk down the chunks --------------------------------------------------------
+
+constexpr int kWalkWarps = 9, kWorkers = 256;  // eight warps compute, one copies and issues the products
+constexpr int kStages = 2;
+constexpr int kStagesAt = 0;                          // [stage]: [K; Q], [T; X]
+constexpr int kStateAt = kStages * 2 * kTile;         // S: high part, low part, [128][64]
+constexpr int kPartsAt = kStateAt + 2 * kD * kCols * 2;  // R, then w U: high part, low part, [64][64]
+constexpr int kWalkSmem = kPartsAt + 2 * kChunk * kCols * 2 + 1024;  // and room to align
+constexpr int kD1 = 0, kD2 = 64, kD3 = 128, kColumns = 256;  // tensor memory
+
+// Barriers that are waited on with a limit; after one ran out all waits return at once, and the warps run through.
+struct Gate {
+  volatile int* abort;
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return;
+    const long long start = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*abort) return;
+      if (clock64() - start > kWaitLimitCycles) {
+        *abort = 1;
+        prompt_flag(KQ_ERR_TIMEOUT);
+        return;
+      }
+    }
+  }
+};
+
+// Descriptor of an operand whose rows (128 bytes, 128-byte swizzle) run along K and whose M or N lies along the row: groups
+// of 64 of M or N `wide` bytes apart, of eight K 1024.
+__device__ __forceinline__ uint64_t across_desc(const void* at, uint32_t wide) {
+  const uint64_t start = (uint64_t)((smem_u32(at) >> 4) & 0x3FFF);
+  return start | ((uint64_t)(wide >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 numbers of a row of a [rows][64] operand, columns 32 half .., as two fp16 parts `low` bytes apart.
+__device__ __forceinline__ void put_row(uint8_t* tile, int low, int row, int half, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4 hi, lo;
+    split2(v[8 * c], v[8 * c + 1], hi.x, lo.x), split2(v[8 * c + 2], v[8 * c + 3], hi.y, lo.y);
+    split2(v[8 * c + 4], v[8 * c + 5], hi.z, lo.z), split2(v[8 * c + 6], v[8 * c + 7], hi.w, lo.w);
+    const uint32_t at = swizzled(row, half * 4 + c);
+    *reinterpret_cast<uint4*>(tile + at) = hi;
+    *reinterpret_cast<uint4*>(tile + low + at) = lo;
+  }
+}
+
+__device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[32]) {
+  uint32_t u[32];
+  tmem_ld32(taddr, u);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const PromptArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kStages], s_ready, r_ready, u_ready, d1_full, d2_full, d3_full;
+  __shared__ uint32_t s_tmem, s_most[8], s_vmost[4];
+  __shared__ int s_abort;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const RuleArgs& a = p.r;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int part = blockIdx.x % (kD / kCols), h = blockIdx.x / (kD / kCols) % a.v_heads;
+  const int64_t r = blockIdx.x / (kD / kCols) / a.v_heads;
+  const Request req = read_request(a.s, r, a.max_new);
+  if (req.status && tid == 0) prompt_flag(req.status);
+  if (!req.count || req.count <= a.short_most) return;
+  const int chunks = (req.count + kChunk - 1) / kChunk;
+  const int64_t slot0 = chunk_base(req.first, r);
+  const int hk = h / (a.v_heads / a.k_heads);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    mbar_init(&s_ready, kWorkers);
+    mbar_init(&r_ready, kWorkers / 2);
+    mbar_init(&u_ready, kWorkers / 2);
+    mbar_init(&d1_full, 1);
+    mbar_init(&d2_full, 1);
+    mbar_init(&d3_full, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s_tmem, kColumns);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const Gate gate{&s_abort};
+
+  if (warp == 8) {
+    if (elect_one()) {
+      const uint64_t policy = l2_policy_evict_first();
+      auto copy = [&](int c) {
+        uint8_t* at = smem + kStagesAt + c % kStages * 2 * kTile;
+        uint64_t* bar = &full[c % kStages];
+        mbar_arrive_expect_tx(bar, 2 * kTile);
+        bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kTile, kTile, bar, policy);
+        bulk_g2s(at + kTile, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
+      };
+      const uint32_t id1 = idesc_f16(128, kCols) | kAcrossB, id3 = id1 | kAcrossA;
+      const uint64_t sd = across_desc(smem + kStateAt, 0), ud = across_desc(smem + kPartsAt, 0);
+      constexpr uint64_t kStateLow = (kD * kCols * 2) >> 4, kPartLow = (kChunk * kCols * 2) >> 4;
+      copy(0);
+      for (int c = 0; c < chunks; ++c) {
+        const uint8_t* at = smem + kStagesAt + c % kStages * 2 * kTile;
+        gate.wait(&s_ready, c & 1);  // the chunk before is done with, its stage is free
+        if (c + 1 < chunks) copy(c + 1);
+        gate.wait(&full[c % kStages], c / kStages & 1);
+        tc_fence_after();
+        const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile);
+#pragma unroll
+        for (int low = 0; low < 2; ++low)
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k)
+            tc_mma_ss(tmem + kD1, kd + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4),
+                      sd + low * kStateLow + (uint64_t)(k * 2048 >> 4), id1, low || k);
+        tc_commit(&d1_full);
+        gate.wait(&r_ready, c & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass)  // high x high, high x low, low x high
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            tc_mma_ss(tmem + kD2, td + (uint64_t)(((pass == 2 ? kTile / 2 : 0) + k * 32) >> 4),
+                      ud + (pass == 1 ? kPartLow : 0) + (uint64_t)(k * 2048 >> 4), id1, pass || k);
+        tc_commit(&d2_full);
+        gate.wait(&u_ready, c & 1);
+        tc_fence_after();
+        const uint64_t kt = across_desc(at, 16384);
+#pragma unroll
+        for (int low = 0; low < 2; ++low)
+#pragma unroll
+          for (int k = 0; k < kChunk / 16; ++k)
+            tc_mma_ss(tmem + kD3, kt + (uint64_t)(k * 2048 >> 4), ud + low * kPartLow + (uint64_t)(k * 2048 >> 4), id3, low || k);
+        tc_commit(&d3_full);
+      }
+      gate.wait(&d3_full, chunks - 1 & 1);  // nothing is in flight when the memory goes
+    }
+    __syncwarp();
+  } else {
+    // lane `row` of tensor memory, columns 32 half ..
+    const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane, i = row % kChunk;
+    const bool keys = quarter < 2;  // rows of keys (R, U), or of queries (O)
+    const uint32_t mine = tmem + (quarter << 21) + half * 32;
+    const int col = part * kCols + half * 32;
+    float* state = a.state + (((int64_t)req.slot * a.v_heads + h) * kD + row) * kD + col;
+    float S[32];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float4 x = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(state)[e];
+      S[4 * e] = x.x, S[4 * e + 1] = x.y, S[4 * e + 2] = x.z, S[4 * e + 3] = x.w;
+    }
+    // of the next chunk: values of this row, the rows' factors
+    kv::Raw<T, 32> value;
+    float f0 = 0.f, f1 = 0.f, f2 = 0.f, last = 1.f;
+    auto fetch = [&](int c) {
+      value.clear();
+      if (c >= chunks) return;
+      const float* f = p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors;
+      last = f[4 * kChunk];
+      if (keys) {
+        f0 = f[i], f1 = f[kChunk + i], f2 = f[2 * kChunk + i];
+        const int64_t t = (int64_t)c * kChunk + i;
+        if (t < req.count) value.load(reinterpret_cast<const T*>(a.v.at(req.first + t, h)) + col);
+      } else {
+        f0 = f[3 * kChunk + i];
+      }
+    };
+    fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+      const float k0 = f0, k1 = f1, k2 = f2, decay = last;
+      // the power of two that S, R and U are taken at: 64 max|v| + 12 max|S| comes to 2^14 at most
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) most = max(most, __float_as_uint(S[e]) & 0x7FFFFFFFu);
+      most = __reduce_max_sync(~0u, most);
+      if (lane == 0) s_most[warp] = most;
+      if (keys) {
+        float v[32];
+        value.get(v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(~0u, top);
+        if (lane == 0) s_vmost[quarter * 2 + half] = top;
+      }
+      named_barrier(1, kWorkers);
+      uint32_t sm = 0, vm = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sm = max(sm, s_most[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) vm = max(vm, s_vmost[e]);
+      // exponents of bounds: 64 max|v| < 2^(ev + 7), 12 max|S| < 2^(es + 5)
+      const int bound = max((int)(vm >> 23) + 7, (int)(sm >> 23) + 5) - 127 + 1;
+      const int power = min(max(14 - bound, -126), 120);
+      const float up = __uint_as_float((uint32_t)(127 + power) << 23), down = __uint_as_float((uint32_t)(127 - power) << 23);
+      {
+        float s[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = S[e] * up;
+        put_row(smem + kStateAt, kD * kCols * 2, row, half, s);
+      }
+      fence_async();
+      tc_fence_before();
+      mbar_arrive(&s_ready);
+      float d[32], o[32];
+      gate.wait(&d1_full, c & 1);
+      tc_fence_after();
+      read_columns(mine + kD1, d);
+      if (keys) {
+        float v[32];
+        value.get(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) d[e] = fmaf(-k0, d[e], k1 * up * v[e]);
+        put_row(smem + kPartsAt, kChunk * kCols * 2, i, half, d);
+        fence_async();
+        tc_fence_before();
+        mbar_arrive(&r_ready);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = k0 * d[e];
+      }
+      fetch(c + 1);
+      gate.wait(&d2_full, c & 1);
+      tc_fence_after();
+      read_columns(mine + kD2, d);
+      if (keys) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) d[e] *= k2;
+        put_row(smem + kPartsAt, kChunk * kCols * 2, i, half, d);
+        fence_async();
+        tc_fence_before();
+        mbar_arrive(&u_ready);
+      } else {
+        const int64_t t = (int64_t)c * kChunk + i;
+        if (t < req.count) {
+          T* out = reinterpret_cast<T*>(a.out.at(req.first + t, h)) + col;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float y[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) y[x] = (o[e + x] + d[e + x]) * down;
+            kv::store8(out + e, y);
+          }
+        }
+      }
+      gate.wait(&d3_full, c & 1);
+      tc_fence_after();
+      read_columns(mine + kD3, d);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S[e] = fmaf(decay, S[e], down * d[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      reinterpret_cast<float4*>(state)[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kColumns);
+  }
+}
+
+static int64_t prompt_slots(int64_t requests, int64_t tokens) { return tokens / kChunk + requests; }
+static int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens) {
+  const int64_t slots = prompt_slots(requests, tokens);
+  return slots * (k_heads + v_heads) * (int64_t)kTile + align256(slots * v_heads * kRowFactors * 4);
+}
+
+template <typename T>
+static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
+  const int64_t slots = prompt_slots(a.s.requests, a.s.tokens);
+  PromptArgs p{};
+  p.r = a;
+  p.kq = static_cast<uint8_t*>(ws);
+  p.tx = p.kq + slots * a.k_heads * kTile;
+  p.factors = reinterpret_cast<float*>(p.tx + slots * a.v_heads * kTile);
+  if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalkSmem)) return e;
+  if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
+    return e;
+  const int64_t grid = a.s.requests * a.v_heads * (kD / kCols);
+  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(32 * kWalkWarps), kWalkSmem, st, p);
+}
+
+cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
+  return dtype == KQ_F16 ? launch<__half>(a, ws, st) : launch<__nv_bfloat16>(a, ws, st);
+}
+
+int prompt_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prompt_status, sizeof(v)) != cudaSuccess) return -1;
+  if (clear && v) {
+    const unsigned int z = 0;
+    if (cudaMemcpyToSymbol(g_prompt_status, &z, sizeof(z)) != cudaSuccess) return -1;
+  }
+  return (int)v;
+}
+
+}  // namespace gdn
+}  // namespace kq
