@@ -20,15 +20,17 @@ __device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1
 // ---- the causal convolution -----------------------------------------------------
 //
 // y[t] = silu(bias + sum_j w[j] x[t - W + 1 + j]), channel by channel: two flops a
-// byte or less, so memory bounds it.  A warp takes 256 channels, eight a lane, and
+// byte or less, so memory bounds it.  A warp takes 16 bytes of channels a lane and
 // walks down a piece of a request's tokens with the last W - 1 inputs in registers:
 // each input is read once but for the W - 1 before a piece.  Pieces begin at the
-// request's first token and every `piece` tokens from there, so only a request's
+// request's first token and every kPiece tokens from there, so only a request's
 // first piece reads its state, and the same lanes write the new one: nothing is
-// read after another CTA wrote it.  A warp owns the pieces that begin in its window
-// of token rows: it finds the request there by a 32-way search of q_start.
+// read after another CTA wrote it.  Each request has a warp for its first piece,
+// which finds it without a search (a decode step is all such); the pieces after it
+// belong to the window of kPiece token rows they begin in, one at most in each,
+// whose warp finds the request by a 32-way search of q_start.
 
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 4, kConvAhead = 4;
 
 struct ConvArgs {
   Rows x, out;
@@ -37,139 +39,120 @@ struct ConvArgs {
   const float* weight;
   const float* bias;
   int32_t channels, silu;
-  int32_t piece, window;
+  int32_t piece;
   int64_t windows;
 };
 
 template <typename T, int W>
-struct ConvLane {
-  const ConvArgs& a;
-  const int channel;
-  float w[W][8], bias[8];
-  float past[W - 1][8];
-
-  __device__ __forceinline__ const T* row(int64_t t) const { return reinterpret_cast<const T*>(a.x.at(t, 0)) + channel; }
-  __device__ __forceinline__ T* kept(int32_t slot, int j) const {
-    return reinterpret_cast<T*>(a.state) + ((int64_t)slot * (W - 1) + j) * a.channels + channel;
-  }
-
-  __device__ void piece(const Request& q, int32_t from) {
-    const int32_t end = min(q.count, from + a.piece);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-      const int32_t at = from - (W - 1) + j;
-      if (from > 0) {
-        kv::load8(row((int64_t)q.first + at), past[j]);  // a piece is W - 1 tokens long at least
-      } else if (q.fresh) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) past[j][e] = 0.f;
-      } else {
-        kv::load8(kept(q.slot, j), past[j]);
-      }
-    }
-    if (from == 0) {  // the new state: the last inputs, those of the old one among them where there are fewer
-      float next[W - 1][8];
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        const int32_t at = q.count - (W - 1) + j;
-        if (at >= 0) {
-          kv::load8(row((int64_t)q.first + at), next[j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < W - 1; ++i)
-            if (i == q.count + j) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) next[j][e] = past[i][e];
-            }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) kv::store8(kept(q.slot, j), next[j]);
-    }
-    for (int32_t t = from; t < end; t += 4) {
-      kv::Raw<T, 8> raw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < end) raw[i].load(row((int64_t)q.first + t + i));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (t + i >= end) break;
-        float v[8], y[8];
-        raw[i].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float s = bias[e];
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][e], past[j][e], s);
-          s = fmaf(w[W - 1][e], v[e], s);
-          y[e] = a.silu ? s / (1.0f + expf(-s)) : s;
-#pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
-          past[W - 2][e] = v[e];
-        }
-        kv::store8(reinterpret_cast<T*>(a.out.at((int64_t)q.first + t + i, 0)) + channel, y);
-      }
-    }
-  }
-};
-
-template <typename T, int W>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a) {
+  constexpr int V = 16 / sizeof(T);  // channels of a lane
+  const int lane = threadIdx.x % 32;
+  const int64_t unit = (int64_t)blockIdx.x * kConvWarps + threadIdx.x / 32;
+  const int channel = (blockIdx.y * 32 + lane) * V;
+  const bool here = channel < a.channels;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int lane = threadIdx.x % 32;
-  const int64_t window = (int64_t)blockIdx.x * kConvWarps + threadIdx.x / 32;
-  if (window >= a.windows) return;
-  const int64_t lo = window * a.window, hi = lo + a.window;
-  // the last request that begins at or before lo
-  int64_t r = 0, span = a.s.requests;
-  bool before = false;
-  while (span > 0) {
-    const int64_t step = (span + 31) / 32, at = r + lane * step;
-    const unsigned some = __ballot_sync(~0u, lane * step < span && a.s.q_start[at] <= lo);
-    if (!some) break;
-    before = true;
-    const int last = 31 - __clz(some);
-    if (step == 1) {
-      r += last;
-      break;
-    }
-    r += last * step;
-    span = min(step, span - last * step);
-  }
-  const int channel = blockIdx.y * 256 + 8 * lane;
-  const bool here = channel < a.channels;
-  ConvLane<T, W> c{a, channel};
+  float w[W][V], bias[V];
   if (here) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c.bias[e] = a.bias ? a.bias[channel + e] : 0.f;
+    for (int e = 0; e < V; ++e) {
+      const float* from = a.weight + (int64_t)(channel + e) * W;
+      if constexpr (W == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from);
+        w[0][e] = x.x, w[1][e] = x.y, w[2][e] = x.z, w[3][e] = x.w;
+      } else {
 #pragma unroll
-      for (int j = 0; j < W; ++j) c.w[j][e] = a.weight[(int64_t)(channel + e) * W + j];
+        for (int j = 0; j < W; ++j) w[j][e] = from[j];
+      }
+      bias[e] = a.bias ? a.bias[channel + e] : 0.f;
     }
   }
-  if (window == 0 && lane == 0 && blockIdx.y == 0 && (a.s.q_start[0] < 0 || a.s.q_start[0] > a.s.tokens)) gdn_flag(KQ_ERR_RANGE);
-  if (before) {
-    const Request q = read_request(a.s, r, a.s.tokens);
-    if (q.status && lane == 0) gdn_flag(q.status);
-    if (q.count) {
-      const int64_t from = (lo - q.first + a.piece - 1) / a.piece * a.piece;
-      if (q.first + from < hi && from < q.count && here) c.piece(q, (int32_t)from);
+  int64_t r = unit, begin = 0;
+  if (unit >= a.s.requests) {  // the last request that begins at or before the window
+    const int64_t window = unit - a.s.requests, lo = window * a.piece;
+    if (window >= a.windows) return;
+    if (window == 0 && lane == 0 && (a.s.q_start[0] < 0 || a.s.q_start[0] > a.s.tokens)) gdn_flag(KQ_ERR_RANGE);
+    r = 0;
+    for (int64_t span = a.s.requests;;) {
+      const int64_t step = (span + 31) / 32, at = r + lane * step;
+      const unsigned some = __ballot_sync(~0u, lane * step < span && a.s.q_start[at] <= lo);
+      if (!some) return;
+      const int last = 31 - __clz(some);
+      r += last * step;
+      if (step == 1) break;
+      span = min(step, span - last * step);
     }
-    ++r;
+    begin = (lo - a.s.q_start[r] + a.piece - 1) / a.piece * a.piece;
+    if (begin <= 0) return;  // that is its first piece
   }
-  for (; r < a.s.requests; ++r) {
-    const int32_t first = a.s.q_start[r];
-    if (first >= hi) break;
-    const Request q = read_request(a.s, r, a.s.tokens);
-    if (q.status && lane == 0) gdn_flag(q.status);
-    if (q.count && q.first >= lo && here) c.piece(q, 0);
+  const Request q = read_request(a.s, r, a.s.tokens);
+  if (q.status && lane == 0) gdn_flag(q.status);
+  if (begin >= q.count || !here) return;
+  const int32_t from = (int32_t)begin, end = min(q.count, from + a.piece);
+  const char* x = a.x.at(q.first, 0) + channel * sizeof(T);
+  char* out = a.out.at(q.first, 0) + channel * sizeof(T);
+  T* kept = reinterpret_cast<T*>(a.state) + (int64_t)q.slot * (W - 1) * a.channels + channel;
+  kv::Raw<T, V> raw[kConvAhead];
+  auto load = [&](int32_t t) {
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i)
+      if (t + i < end) raw[i].load(reinterpret_cast<const T*>(x + (t + i) * a.x.token_stride));
+  };
+  load(from);
+  kv::Raw<T, V> old[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    old[j].clear();
+    if (from > 0) old[j].load(reinterpret_cast<const T*>(x + (from - (W - 1) + j) * a.x.token_stride));
+    else if (!q.fresh) old[j].load(kept + (int64_t)j * a.channels);
+  }
+  if (from == 0) {  // the new state: the last inputs, those of the old one among them where there are fewer
+    kv::Raw<T, V> next[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int32_t at = q.count - (W - 1) + j;
+      if (at >= 0) next[j].load(reinterpret_cast<const T*>(x + at * a.x.token_stride));
+      else if (q.count == 1) next[j] = old[j + 1 < W - 1 ? j + 1 : W - 2];
+      else next[j] = old[j + 2 < W - 1 ? j + 2 : W - 2];  // fewer than W - 1 are one or two
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      *reinterpret_cast<uint4*>(kept + (int64_t)j * a.channels) = make_uint4(next[j].u[0], next[j].u[1], next[j].u[2], next[j].u[3]);
+  }
+  float past[W - 1][V];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) old[j].get(past[j]);
+  for (int32_t t = from; t < end; t += kConvAhead) {
+    kv::Raw<T, V> now[kConvAhead];
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i) now[i] = raw[i];
+    load(t + kConvAhead);
+#pragma unroll
+    for (int i = 0; i < kConvAhead; ++i) {
+      float v[V], y[V];
+      now[i].get(v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float s = bias[e];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][e], past[j][e], s);
+        s = fmaf(w[W - 1][e], v[e], s);
+        y[e] = a.silu ? silu(s) : s;
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
+        past[W - 2][e] = v[e];
+      }
+      if (t + i >= end) continue;
+      if constexpr (sizeof(T) == 4) kv::store4(reinterpret_cast<T*>(out + (t + i) * a.out.token_stride), y);
+      else kv::store8(reinterpret_cast<T*>(out + (t + i) * a.out.token_stride), y);
+    }
   }
 }
 
 template <typename T>
 static cudaError_t launch_conv(const ConvArgs& a, int width, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.windows + kConvWarps - 1) / kConvWarps), (unsigned)((a.channels + 255) / 256));
+  const int wide = 32 * 16 / sizeof(T);
+  const dim3 grid((unsigned)((a.s.requests + a.windows + kConvWarps - 1) / kConvWarps), (unsigned)((a.channels + wide - 1) / wide));
   const auto k = width == 2 ? conv_kernel<T, 2> : width == 3 ? conv_kernel<T, 3> : conv_kernel<T, 4>;
   return launch_dependent(k, grid, dim3(32 * kConvWarps), 0, st, a);
 }
@@ -406,10 +389,10 @@ int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t
   a.s = gdn::Requests{d_q_start, d_kv_len, d_slot, requests, tokens, slots};
   a.state = static_cast<char*>(d_state), a.weight = p->weight, a.bias = p->bias;
   a.channels = p->channels, a.silu = p->silu;
-  // few tokens: a piece a warp, so that no request waits for another; many: pieces long enough that what lies before them
-  // is read again for a tenth
-  a.piece = tokens <= 1024 ? 4 : 32, a.window = tokens <= 1024 ? 1 : 32;
-  a.windows = (tokens + a.window - 1) / a.window;
+  // short pieces where there are few, or the last wave of warps would be a long one; long ones where there are many, for
+  // the inputs before a piece are read again
+  a.piece = tokens <= 2048 ? 8 : 32;
+  a.windows = (tokens + a.piece - 1) / a.piece;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_conv<float>(a, p->width, st)
               : dtype == KQ_F16 ? gdn::launch_conv<__half>(a, p->width, st)

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args
         if (a.residual.data && mine) other[i].load(gate + 8 * vec);
         other[i].get(z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= z[e] / (1.0f + expf(-z[e]));
+        for (int e = 0; e < 8; ++e) v[i][e] *= gdn::silu(z[e]);
       }
       if (a.codes) store_q8(a, row, vec, v[i], mine);
       if (a.out.data && mine) kv::store8(reinterpret_cast<T*>(a.out.at(token, head)) + 8 * vec, v[i]);
