@@ -20,7 +20,7 @@ __device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1
 // ---- the causal convolution -----------------------------------------------------
 //
 // y[t] = silu(bias + sum_j w[j] x[t - W + 1 + j]), channel by channel: two flops a
-// byte or less, so memory bounds it.  A warp takes 16 bytes of channels a lane and
+// byte or less, so memory bounds it.  A warp takes four channels a lane and
 // walks down a piece of a request's tokens with the last W - 1 inputs in registers:
 // each input is read once but for the W - 1 before a piece.  Pieces begin at the
 // request's first token and every kPiece tokens from there, so only a request's
@@ -30,7 +30,7 @@ __device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1
 // belong to the window of kPiece token rows they begin in, one at most in each,
 // whose warp finds the request by a 32-way search of q_start.
 
-constexpr int kConvWarps = 4, kConvAhead = 4;
+constexpr int kConvWarps = 4, kConvAhead = 4, kConvWide = 4;
 
 struct ConvArgs {
   Rows x, out;
@@ -45,7 +45,7 @@ struct ConvArgs {
 
 template <typename T, int W>
 __global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a) {
-  constexpr int V = 16 / sizeof(T);  // channels of a lane
+  constexpr int V = kConvWide;  // channels of a lane
   const int lane = threadIdx.x % 32;
   const int64_t unit = (int64_t)blockIdx.x * kConvWarps + threadIdx.x / 32;
   const int channel = (blockIdx.y * 32 + lane) * V;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a)
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      *reinterpret_cast<uint4*>(kept + (int64_t)j * a.channels) = make_uint4(next[j].u[0], next[j].u[1], next[j].u[2], next[j].u[3]);
+      next[j].store(kept + (int64_t)j * a.channels);
   }
   float past[W - 1][V];
 #pragma unroll
@@ -143,15 +143,14 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a)
         past[W - 2][e] = v[e];
       }
       if (t + i >= end) continue;
-      if constexpr (sizeof(T) == 4) kv::store4(reinterpret_cast<T*>(out + (t + i) * a.out.token_stride), y);
-      else kv::store8(reinterpret_cast<T*>(out + (t + i) * a.out.token_stride), y);
+      kv::store4(reinterpret_cast<T*>(out + (t + i) * a.out.token_stride), y);
     }
   }
 }
 
 template <typename T>
 static cudaError_t launch_conv(const ConvArgs& a, int width, cudaStream_t st) {
-  const int wide = 32 * 16 / sizeof(T);
+  const int wide = 32 * kConvWide;
   const dim3 grid((unsigned)((a.s.requests + a.windows + kConvWarps - 1) / kConvWarps), (unsigned)((a.channels + wide - 1) / wide));
   const auto k = width == 2 ? conv_kernel<T, 2> : width == 3 ? conv_kernel<T, 3> : conv_kernel<T, 4>;
   return launch_dependent(k, grid, dim3(32 * kConvWarps), 0, st, a);

@@ -133,6 +133,16 @@ struct Raw {
       u[0] = v.x, u[1] = v.y;
     }
   }
+  __device__ __forceinline__ void store(T* p) const {
+    constexpr int kBytes = N * sizeof(T);
+    if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    }
+  }
   __device__ __forceinline__ void get(float* v) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
