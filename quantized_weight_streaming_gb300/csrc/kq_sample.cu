@@ -4,10 +4,15 @@
 // The kept tokens are those above a border: a logit K, and how many of the equal
 // ones at it (the lowest ids) still belong.  Top-k looks for the border by counts,
 // top-p by masses; neither sorts.  A row's logits are read once and stay in the
-// shared memory of a cluster of CTAs, a slice each; a border is found by
-// histograms over ever finer parts of the value range, summed over the cluster.
-// The token then is the first id, in the vocabulary's order, where the running sum
-// of the kept weights passes u times their sum.
+// shared memory of a cluster of CTAs, a slice each.  A histogram of 2048 equal
+// steps of (max - l) / temperature, summed over the cluster, says in which step the
+// border lies; that step's logits, some hundreds at most in a vocabulary's usual
+// spread, are gathered from all slices and compared with one another.  (Bins of the
+// numbers' leading bits, as a radix sort has them, put most of a row into a dozen
+// bins, and their atomics took 200 of 237 us for one row of 248320.)  Where more
+// than 1024 lie in the step, as where logits are equal, the border is found digit by
+// digit.  The token then is the first id, in the vocabulary's order, where the
+// running sum of the kept weights passes u times their sum.
 //
 // A weight is exp((l - max) / temperature) in fixed point, 44 bits behind the
 // point, and sums are of 64-bit integers: a row of 2^18 equal ones still fits, sums
@@ -52,17 +57,28 @@ struct Args {
 
 typedef unsigned long long u64;
 
+constexpr int kList = 1024;
+
 // What the CTAs of a cluster show one another.
 struct Shared {
-  u64 hist[kBins];
-  u64 total[kBins];     // the cluster's sums, the same in every CTA
+  union {
+    struct {
+      uint32_t low[kBins], high[kBins];  // sums of 64 bits
+    } hist;
+    struct {
+      u64 weight[kList];
+      uint32_t key[kList];  // of all slices
+    } all;
+  };
+  uint32_t list[kList];  // keys of this slice's logits in the border's step
   u64 part[kMostWarps];
-  u64 kept;             // this slice's kept weight
-  float most;
-  int32_t nan, ties, lowest;
+  u64 kept;              // this slice's kept weight
+  float most, least;
+  int32_t nan, ties, lowest, listed;
   int32_t bin;
-  u64 above;
-  u64 found;
+  u64 above, inside;
+  uint32_t key;
+  u64 equal, need;
 };
 
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -119,11 +135,12 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
 
   // the slice, its largest
   const T* src = static_cast<const T*>(a.logits) + row * a.row_stride + first;
-  float most = -INFINITY;
+  float most = -INFINITY, lowest = INFINITY;
   int nan = 0;
   auto see = [&](T x) {
     const float v = kv::to_float(x);
     most = fmaxf(most, v);
+    lowest = fminf(lowest, v);
     nan |= isnan(v);
   };
   constexpr int kVec = 16 / sizeof(T);
@@ -142,12 +159,14 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   float* fpart = reinterpret_cast<float*>(s.part);
   int* ipart = reinterpret_cast<int*>(s.part);
   most = block_reduce(most, fpart, [](float x, float y) { return fmaxf(x, y); }, -INFINITY);
+  lowest = block_reduce(lowest, fpart, [](float x, float y) { return fminf(x, y); }, INFINITY);
   nan = __syncthreads_or(nan);
-  if (tid == 0) s.most = most, s.nan = nan;
+  if (tid == 0) s.most = most, s.least = lowest, s.nan = nan;
   cluster.sync();
   for (int c = 0; c < ranks; ++c) {
     const Shared* o = cluster.map_shared_rank(&s, c);
     most = fmaxf(most, o->most);
+    lowest = fminf(lowest, o->least);
     nan |= o->nan;
   }
 
@@ -187,130 +206,189 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   w.hi = (float)fmin(factor, 3.0e38);
   w.lo = (float)fmin(factor - (double)w.hi, 1.0e30);
 
-  // Sums s.hist over the cluster and finds, from the highest of `bins` bins down, the one in which the running sum comes
-  // to `target`; `above` gets what lies over it.
-  auto find = [&](int bins, u64 target, u64 above, int& bin, u64& over) {
+  auto add = [&](int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
+    const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.low[bin], lo);
+    const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < old);
+    if (hi) atomicAdd(&s.hist.high[bin], hi);
+  };
+  auto clear = [&](int bins) {
+    for (int b = tid; b < bins; b += blockDim.x) s.hist.low[b] = s.hist.high[b] = 0;
+    __syncthreads();
+  };
+  // Sums the histogram over the cluster and finds the bin, from the first on, in which the running sum comes to `target`:
+  // s.bin, what lies before it (s.above) and in it (s.inside).  Returns the sum of all bins.  share >= 0: the target is that
+  // share of the sum of all, rounded up, one at least.
+  auto find = [&](int bins, u64& target, double share) -> u64 {
     cluster.sync();
-    for (int b = tid; b < bins; b += blockDim.x) {
+    const int per = (bins + blockDim.x - 1) / blockDim.x, from = min(bins, tid * per), to = min(bins, from + per);
+    auto bin_sum = [&](int b) {
       u64 sum = 0;
-      for (int c = 0; c < ranks; ++c) sum += cluster.map_shared_rank(&s, c)->hist[b];
-      s.total[b] = sum;
+      for (int c = 0; c < ranks; ++c) {
+        const Shared* o = cluster.map_shared_rank(&s, c);
+        sum += (u64)o->hist.high[b] << 32 | o->hist.low[b];
+      }
+      return sum;
+    };
+    u64 bin0 = from < to ? bin_sum(from) : 0, own = bin0;
+    for (int b = from + 1; b < to; ++b) own += bin_sum(b);
+    u64 x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const u64 y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s.part[warp] = x;
+    __syncthreads();
+    u64 all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w == warp) x += all;
+      all += s.part[w];
+    }
+    if (share >= 0.0) target = max((u64)ceil(share * (double)all), (u64)1);
+    if (x - own < target && target <= x) {
+      u64 before = x - own, in = bin0;
+      int b = from;
+      while (before + in < target) before += in, in = bin_sum(++b);
+      s.bin = b, s.above = before, s.inside = in;
     }
     __syncthreads();
-    if (warp == 0) {  // 32 bins at a time, the highest first
-      u64 run = above;
-      int hit = -1;
-      for (int b0 = bins - 32; b0 >= 0; b0 -= 32) {
-        u64 x = s.total[b0 + 31 - lane];
-        const u64 own = x;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const u64 y = __shfl_up_sync(~0u, x, o);
-          if (lane >= o) x += y;
-        }
-        const unsigned m = __ballot_sync(~0u, run + x >= target);
-        if (m) {
-          const int l = __ffs(m) - 1;
-          hit = b0 + 31 - l;
-          run += __shfl_sync(~0u, x - own, l);
-          break;
-        }
-        run += __shfl_sync(~0u, x, 31);
-      }
-      if (lane == 0) s.bin = hit, s.above = run;
-    }
-    cluster.sync();
-    bin = s.bin;
-    over = s.above;
+    return all;
   };
 
-  // The border at which the running sum, from the largest logit down, of one each (MASS false) or of the weights comes to
-  // `target`: the key there, and how many of the equal ones belong.
-  auto border = [&](bool mass, u64 target, uint32_t& key, u64& ties, u64& over) {
-    uint32_t prefix = 0;
-    over = 0;
-    int shift = 32;
-    for (int bits : {11, 11, 10}) {
-      shift -= bits;
-      const int bins = 1 << bits;
-      for (int b = tid; b < bins; b += blockDim.x) s.hist[b] = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += blockDim.x) {
-        const float v = kv::to_float(s_l[i]);
-        const uint32_t k = key_of(v);
-        if (shift + bits < 32 && k >> (shift + bits) != prefix) continue;
-        const u64 x = mass ? w.weight(v) : 1;
-        if (x) atomicAdd(&s.hist[k >> shift & (bins - 1)], x);
-      }
-      int bin;
-      u64 now;
-      find(bins, target, over, bin, now);
-      over = now;
-      prefix = prefix << bits | (uint32_t)bin;
+  // The border at which the running sum, from the largest logit down, of one each (MASS false) or of the weights of those at
+  // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.
+  const float steps = w.infinite ? 1.f : 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
+  auto step_of = [&](float v) { return (int)fminf((most - v) * steps, 2047.f); };  // falls as v grows (NaN, of infinities: the last, as all are then)
+  auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) {
+    auto one = [&](float v) { return mass ? w.weight(v) : (u64)1; };
+    clear(kBins);
+    for (int i = tid; i < n; i += blockDim.x) {
+      const float v = kv::to_float(s_l[i]);
+      if (key_of(v) <= least) continue;
+      const u64 x = one(v);
+      if (x) add(step_of(v), x);
     }
-    key = prefix;
-    const u64 one = mass ? w.weight(value_of(key)) : 1;
-    ties = (target - over + one - 1) / one;
+    if (least_ties && rank == 0 && tid == 0) add(step_of(value_of(least)), least_ties * one(value_of(least)));
+    find(kBins, target, share);
+    const int bin = s.bin;
+    u64 rest = target - s.above;
+    if (tid == 0) s.listed = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += blockDim.x) {
+      const float v = kv::to_float(s_l[i]);
+      if (key_of(v) < least || step_of(v) != bin) continue;
+      const int at = atomicAdd(&s.listed, 1);
+      if (at < kList) s.list[at] = key_of(v);
+    }
+    cluster.sync();
+    int count = 0;
+    for (int c = 0; c < ranks; ++c) count += cluster.map_shared_rank(&s, c)->listed;
+    if (count <= kList) {
+      int at = 0;
+      for (int c = 0; c < ranks; ++c) {
+        const Shared* o = cluster.map_shared_rank(&s, c);
+        const int m = o->listed;
+        for (int i = tid; i < m; i += blockDim.x) {
+          const uint32_t k = o->list[i];
+          s.all.key[at + i] = k;
+          s.all.weight[at + i] = one(value_of(k));
+        }
+        at += m;
+      }
+      __syncthreads();
+      for (int i = tid; i < count; i += blockDim.x) {
+        const uint32_t k = s.all.key[i];
+        u64 over = 0;
+        uint32_t same = 0;
+        for (int j = 0; j < count; ++j) {
+          const uint32_t o = s.all.key[j];
+          if (o > k) over += s.all.weight[j];
+          same += o == k;
+        }
+        const u64 x = s.all.weight[i];
+        if (over < rest && rest <= over + same * x) s.key = k, s.equal = same, s.need = (rest - over + x - 1) / x;
+      }
+      __syncthreads();
+      key = s.key, ties = s.need, equal = s.equal;
+    } else {
+      uint32_t prefix = 0;
+      int shift = 32;
+      rest = target;
+      for (int bits : {11, 11, 10}) {
+        shift -= bits;
+        const int bins = 1 << bits;
+        cluster.sync();  // nobody reads what is cleared
+        clear(bins);
+        for (int i = tid; i < n; i += blockDim.x) {
+          const float v = kv::to_float(s_l[i]);
+          const uint32_t k = key_of(v);
+          if (k < least || (shift + bits < 32 && k >> (shift + bits) != prefix)) continue;
+          const u64 x = one(v);
+          if (x) add(bins - 1 - (k >> shift & (bins - 1)), x);
+        }
+        find(bins, rest, -1.0);
+        rest -= s.above;
+        prefix = prefix << bits | (uint32_t)(bins - 1 - s.bin);
+        if (shift == 0) equal = s.inside;
+        __syncthreads();
+      }
+      key = prefix;
+      const u64 x = one(value_of(key));
+      ties = (rest + x - 1) / x;
+      equal /= x;
+    }
+    cluster.sync();
   };
 
   uint32_t key = 0;  // below every logit: all belong
-  u64 ties = ~0ull, over = 0, total = 0;
+  u64 ties = 0, equal = 0;
   const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
-  if (by_k) border(false, (u64)top_k, key, ties, over);
-  auto kept_mass = [&]() {  // of all that belong so far
-    u64 sum = 0;
-    for (int i = tid; i < n; i += blockDim.x) {
-      const float v = kv::to_float(s_l[i]);
-      if (key_of(v) > key) sum += w.weight(v);
-    }
-    sum = block_reduce(sum, s.part, [](u64 x, u64 y) { return x + y; }, (u64)0);
-    if (tid == 0) s.kept = sum;
-    cluster.sync();
-    sum = 0;
-    for (int c = 0; c < ranks; ++c) sum += cluster.map_shared_rank(&s, c)->kept;
-    cluster.sync();
-    return by_k ? sum + ties * w.weight(value_of(key)) : sum;
-  };
-  if (by_p) {
-    total = kept_mass();
-    const u64 target = (u64)ceil((double)top_p * (double)total);
-    border(true, max(target, (u64)1), key, ties, over);
-  }
+  if (by_k) border(false, (u64)top_k, -1.0, 0, 0, key, ties, equal);
+  if (by_p) border(true, 0, (double)top_p, key, ties, key, ties, equal);
+  const bool at_border = by_k || by_p, some = at_border && ties < equal;  // some of the equal ones only
+  if (!some) ties = ~0ull;
 
-  // The kept weight of each warp's run of the slice; equal ones at the border are counted off in order.
+  // The kept weight of each warp's run of the slice; where some of the equal ones at the border belong, they are counted off
+  // in order.
   const int run = (n + 32 * warps - 1) / (32 * warps) * 32, lo = min(n, warp * run), hi = min(n, lo + run);
-  const bool at_border = by_k || by_p;
-  int mine = 0;
-  if (at_border)
+  u64 ahead = 0;
+  if (some) {
+    int mine = 0;
     for (int i = lo; i < hi; i += 32) {
       const bool tie = i + lane < hi && key_of(kv::to_float(s_l[i + lane])) == key;
       mine += __popc(__ballot_sync(~0u, tie));
     }
-  __syncthreads();
-  if (lane == 0) ipart[warp] = mine;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < warps; ++i) {
-    if (i < warp) before += ipart[i];
-    all += ipart[i];
+    __syncthreads();
+    if (lane == 0) ipart[warp] = mine;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < warps; ++i) {
+      if (i < warp) before += ipart[i];
+      all += ipart[i];
+    }
+    if (tid == 0) s.ties = all;
+    cluster.sync();
+    ahead = before;
+    for (int c = 0; c < rank; ++c) ahead += cluster.map_shared_rank(&s, c)->ties;
   }
-  if (tid == 0) s.ties = all;
-  cluster.sync();
-  u64 ahead = before;
-  for (int c = 0; c < rank; ++c) ahead += cluster.map_shared_rank(&s, c)->ties;
-  auto weigh = [&](int i, u64& seen) -> u64 {  // element i of the warp's run, all lanes together
-    const bool here = i < hi;
-    const float v = here ? kv::to_float(s_l[i]) : -INFINITY;
-    const uint32_t k = key_of(v);
-    const unsigned m = __ballot_sync(~0u, here && at_border && k == key);
-    const bool in = here && (!at_border || k > key || (k == key && seen + __popc(m & ((1u << lane) - 1)) < ties));
-    seen += __popc(m);
-    if (!in) return 0;
+  auto kept = [&](float v) -> u64 {
     const float e = w.exp_of(v);
     return e >= min_p || v == most ? (u64)__float2ull_rn(e * kOne) : 0;
   };
+  // element i of a warp's run, which ends at `end`; all lanes together
+  auto weigh = [&](int i, int end, u64& seen) -> u64 {
+    const float v = i < end ? kv::to_float(s_l[i]) : -INFINITY;
+    const uint32_t k = i < end ? key_of(v) : 0;
+    bool in = i < end && k >= key;
+    if (some) {
+      const unsigned m = __ballot_sync(~0u, in && k == key);
+      in = in && (k > key || seen + __popc(m & ((1u << lane) - 1)) < ties);
+      seen += __popc(m);
+    }
+    return in ? kept(v) : 0;
+  };
   u64 sum = 0, seen = ahead;
-  for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, seen);
+  for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   __syncthreads();
@@ -337,7 +415,8 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
     seen = ahead;
     u64 at = lower;
     for (int i = lo; i < hi; i += 32) {
-      const u64 own = weigh(i + lane, seen);
+      const u64 own = weigh(i + lane, hi, seen);
+      if (!__ballot_sync(~0u, own != 0)) continue;
       u64 x = own;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
