@@ -36,10 +36,10 @@ __device__ unsigned int g_sample_status = 0;
 __device__ __forceinline__ void sample_flag(int status) { atomicOr(&g_sample_status, 1u << status); }
 
 constexpr int kMostVocab = 393216;
-constexpr int kMostCluster = 8;
-constexpr int kMostSlice = kMostVocab / kMostCluster;
-constexpr int kMostThreads = 1024, kMostWarps = kMostThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kPortable = 8, kMostCluster = 16;
+constexpr int kMostSlice = kMostVocab / kPortable;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kSubs = 1024;
 constexpr float kOne = 17592186044416.f;  // 2^44
 
 struct Args {
@@ -60,7 +60,7 @@ typedef unsigned long long u64;
 constexpr int kList = 1024;
 
 // What the CTAs of a cluster show one another.
-struct Shared {
+struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
   union {
     struct {
       uint32_t low[kBins], high[kBins];  // sums of 64 bits
@@ -70,13 +70,17 @@ struct Shared {
       uint32_t key[kList];  // of all slices
     } all;
   };
+  struct {
+    uint32_t low[kSubs], high[kSubs];
+  } sub;
   uint32_t list[kList];  // keys of this slice's logits in the border's step
-  u64 part[kMostWarps];
+  u64 part[kWarps];
   u64 kept;              // this slice's kept weight
+  u64 bins;              // the sum of this CTA's share of the bins
   float most, least;
-  int32_t nan, ties, lowest, listed;
-  int32_t bin;
-  u64 above, inside;
+  int32_t nan, ties, lowest, listed, members;
+  int32_t bin, subbin;
+  u64 above, inside, rest;
   uint32_t key;
   u64 equal, need;
 };
@@ -110,7 +114,8 @@ template <typename V, typename F>
 __device__ __forceinline__ V block_reduce(V v, V* part, F join, V none) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = join(v, __shfl_xor_sync(~0u, v, o));
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int warps = kWarps;
   __syncthreads();
   if (lane == 0) part[warp] = v;
   __syncthreads();
@@ -121,14 +126,15 @@ __device__ __forceinline__ V block_reduce(V v, V* part, F join, V none) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   Shared& s = *reinterpret_cast<Shared*>(s_raw);
   T* s_l = reinterpret_cast<T*>(s_raw + sizeof(Shared));
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int64_t row = blockIdx.x / ranks;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, warps = blockDim.x / 32;
+  constexpr int warps = kWarps;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int first = rank * a.slice, n = max(0, min(a.slice, a.vocab - first));
   grid_dependency_wait();
   allow_dependent_launch();
@@ -145,16 +151,16 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   };
   constexpr int kVec = 16 / sizeof(T);
   if (((uintptr_t)src & 15) == 0) {
-    for (int i = tid; i < n / kVec; i += blockDim.x) {
+    for (int i = tid; i < n / kVec; i += kThreads) {
       union { uint4 u; T t[kVec]; } x;
       x.u = __ldg(reinterpret_cast<const uint4*>(src) + i);
       reinterpret_cast<uint4*>(s_l)[i] = x.u;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) see(x.t[e]);
     }
-    for (int i = n / kVec * kVec + tid; i < n; i += blockDim.x) see(s_l[i] = src[i]);
+    for (int i = n / kVec * kVec + tid; i < n; i += kThreads) see(s_l[i] = src[i]);
   } else {
-    for (int i = tid; i < n; i += blockDim.x) see(s_l[i] = src[i]);
+    for (int i = tid; i < n; i += kThreads) see(s_l[i] = src[i]);
   }
   float* fpart = reinterpret_cast<float*>(s.part);
   int* ipart = reinterpret_cast<int*>(s.part);
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   w.infinite = isinf(most);
   if (t == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f) {  // the largest alone, its lowest id
     int at = 0x7fffffff;
-    for (int i = tid; i < n; i += blockDim.x)
+    for (int i = tid; i < n; i += kThreads)
       if (kv::to_float(s_l[i]) == most) at = min(at, first + i);
     at = block_reduce(at, ipart, [](int x, int y) { return min(x, y); }, 0x7fffffff);
     if (tid == 0) s.lowest = at;
@@ -206,32 +212,17 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   w.hi = (float)fmin(factor, 3.0e38);
   w.lo = (float)fmin(factor - (double)w.hi, 1.0e30);
 
-  auto add = [&](int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
-    const uint32_t lo = (uint32_t)x, old = atomicAdd(&s.hist.low[bin], lo);
+  auto add = [&](uint32_t* low, uint32_t* high, int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
+    const uint32_t lo = (uint32_t)x, old = atomicAdd(&low[bin], lo);
     const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < old);
-    if (hi) atomicAdd(&s.hist.high[bin], hi);
+    if (hi) atomicAdd(&high[bin], hi);
   };
   auto clear = [&](int bins) {
-    for (int b = tid; b < bins; b += blockDim.x) s.hist.low[b] = s.hist.high[b] = 0;
+    for (int b = tid; b < bins; b += kThreads) s.hist.low[b] = s.hist.high[b] = 0;
     __syncthreads();
   };
-  // Sums the histogram over the cluster and finds the bin, from the first on, in which the running sum comes to `target`:
-  // s.bin, what lies before it (s.above) and in it (s.inside).  Returns the sum of all bins.  share >= 0: the target is that
-  // share of the sum of all, rounded up, one at least.
-  auto find = [&](int bins, u64& target, double share) -> u64 {
-    cluster.sync();
-    const int per = (bins + blockDim.x - 1) / blockDim.x, from = min(bins, tid * per), to = min(bins, from + per);
-    auto bin_sum = [&](int b) {
-      u64 sum = 0;
-      for (int c = 0; c < ranks; ++c) {
-        const Shared* o = cluster.map_shared_rank(&s, c);
-        sum += (u64)o->hist.high[b] << 32 | o->hist.low[b];
-      }
-      return sum;
-    };
-    u64 bin0 = from < to ? bin_sum(from) : 0, own = bin0;
-    for (int b = from + 1; b < to; ++b) own += bin_sum(b);
-    u64 x = own;
+  // This thread's running sum of x over the CTA, and the sum of all.
+  auto scan = [&](u64 x, u64& all) {
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const u64 y = __shfl_up_sync(~0u, x, o);
@@ -239,20 +230,62 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
     }
     if (lane == 31) s.part[warp] = x;
     __syncthreads();
-    u64 all = 0;
-    for (int w = 0; w < warps; ++w) {
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
       if (w == warp) x += all;
       all += s.part[w];
     }
-    if (share >= 0.0) target = max((u64)ceil(share * (double)all), (u64)1);
-    if (x - own < target && target <= x) {
-      u64 before = x - own, in = bin0;
-      int b = from;
-      while (before + in < target) before += in, in = bin_sum(++b);
-      s.bin = b, s.above = before, s.inside = in;
-    }
     __syncthreads();
-    return all;
+    return x;
+  };
+  // Sums the histogram over the cluster, a share of the bins in each CTA, and finds the bin, from the first on, in which the
+  // running sum comes to `target`: s.bin, what lies before it (s.above) and in it (s.inside).  share >= 0: the target is that
+  // share of the sum of all, rounded up, one at least.
+  auto find = [&](int bins, u64& target, double share) {
+    cluster.sync();
+    const int mine = bins / ranks, per = (mine + kThreads - 1) / kThreads;
+    const int from = rank * mine + min(mine, tid * per), to = rank * mine + min(mine, tid * per + per);
+    u64 bin[4], own = 0;  // 2048 bins and 512 threads at most
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bin[i] = 0;
+      if (from + i >= to) continue;
+#pragma unroll
+      for (int c = 0; c < kMostCluster; ++c) {
+        if (c >= ranks) break;
+        const Shared* o = cluster.map_shared_rank(&s, c);
+        bin[i] += (u64)o->hist.high[from + i] << 32 | o->hist.low[from + i];
+      }
+      own += bin[i];
+    }
+    u64 all = 0, x = scan(own, all);
+    if (tid == 0) s.bins = all;
+    cluster.sync();
+    u64 lower = 0;
+    all = 0;
+#pragma unroll
+    for (int c = 0; c < kMostCluster; ++c) {
+      if (c >= ranks) break;
+      const u64 y = cluster.map_shared_rank(&s, c)->bins;
+      if (c < rank) lower += y;
+      all += y;
+    }
+    if (share >= 0.0) target = max((u64)ceil(share * (double)all), (u64)1);
+    x += lower;
+    if (x - own < target && target <= x) {
+      u64 before = x - own;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (before < target && target <= before + bin[i])
+          for (int c = 0; c < ranks; ++c) {
+            Shared* o = cluster.map_shared_rank(&s, c);
+            o->bin = from + i, o->above = before, o->inside = bin[i];
+          }
+        before += bin[i];
+      }
+    }
+    cluster.sync();
   };
 
   // The border at which the running sum, from the largest logit down, of one each (MASS false) or of the weights of those at
@@ -262,19 +295,21 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
   auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) {
     auto one = [&](float v) { return mass ? w.weight(v) : (u64)1; };
     clear(kBins);
-    for (int i = tid; i < n; i += blockDim.x) {
+    for (int i = tid; i < n; i += kThreads) {
       const float v = kv::to_float(s_l[i]);
       if (key_of(v) <= least) continue;
       const u64 x = one(v);
-      if (x) add(step_of(v), x);
+      if (!mass) atomicAdd(&s.hist.low[step_of(v)], 1u);
+      else if (x) add(s.hist.low, s.hist.high, step_of(v), x);
     }
-    if (least_ties && rank == 0 && tid == 0) add(step_of(value_of(least)), least_ties * one(value_of(least)));
+    if (least_ties && rank == 0 && tid == 0)
+      add(s.hist.low, s.hist.high, step_of(value_of(least)), least_ties * one(value_of(least)));
     find(kBins, target, share);
     const int bin = s.bin;
     u64 rest = target - s.above;
     if (tid == 0) s.listed = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += blockDim.x) {
+    for (int i = tid; i < n; i += kThreads) {
       const float v = kv::to_float(s_l[i]);
       if (key_of(v) < least || step_of(v) != bin) continue;
       const int at = atomicAdd(&s.listed, 1);
@@ -288,25 +323,46 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
       for (int c = 0; c < ranks; ++c) {
         const Shared* o = cluster.map_shared_rank(&s, c);
         const int m = o->listed;
-        for (int i = tid; i < m; i += blockDim.x) {
+        for (int i = tid; i < m; i += kThreads) {
           const uint32_t k = o->list[i];
           s.all.key[at + i] = k;
           s.all.weight[at + i] = one(value_of(k));
         }
         at += m;
       }
+      for (int i = tid; i < kSubs; i += kThreads) s.sub.low[i] = s.sub.high[i] = 0;
+      if (tid == 0) s.members = 0;
+      cluster.sync();  // the lists are read: they are used again
+      // 1024 steps within the step; of the one that the border lies in, each with each
+      auto sub_of = [&](uint32_t k) { return (int)(((most - value_of(k)) * steps - (float)bin) * (float)kSubs); };
+      auto sub = [&](uint32_t k) { return bin == kBins - 1 ? 0 : min(max(sub_of(k), 0), kSubs - 1); };
+      for (int i = tid; i < count; i += kThreads) add(s.sub.low, s.sub.high, sub(s.all.key[i]), s.all.weight[i]);
       __syncthreads();
-      for (int i = tid; i < count; i += blockDim.x) {
-        const uint32_t k = s.all.key[i];
+      u64 bins[2], all;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) bins[i] = (u64)s.sub.high[2 * tid + i] << 32 | s.sub.low[2 * tid + i];
+      const u64 x = scan(bins[0] + bins[1], all), before = x - bins[0] - bins[1];
+      if (before < rest && rest <= x) {
+        const bool second = before + bins[0] < rest;
+        s.subbin = 2 * tid + second, s.rest = rest - before - (second ? bins[0] : 0);
+      }
+      __syncthreads();
+      rest = s.rest;
+      for (int i = tid; i < count; i += kThreads)
+        if (sub(s.all.key[i]) == s.subbin) s.list[atomicAdd(&s.members, 1)] = i;
+      __syncthreads();
+      const int members = s.members;
+      for (int i = tid; i < members; i += kThreads) {
+        const uint32_t k = s.all.key[s.list[i]];
         u64 over = 0;
         uint32_t same = 0;
-        for (int j = 0; j < count; ++j) {
-          const uint32_t o = s.all.key[j];
-          if (o > k) over += s.all.weight[j];
+        for (int j = 0; j < members; ++j) {
+          const uint32_t o = s.all.key[s.list[j]];
+          if (o > k) over += s.all.weight[s.list[j]];
           same += o == k;
         }
-        const u64 x = s.all.weight[i];
-        if (over < rest && rest <= over + same * x) s.key = k, s.equal = same, s.need = (rest - over + x - 1) / x;
+        const u64 w1 = s.all.weight[s.list[i]];
+        if (over < rest && rest <= over + same * w1) s.key = k, s.equal = same, s.need = (rest - over + w1 - 1) / w1;
       }
       __syncthreads();
       key = s.key, ties = s.need, equal = s.equal;
@@ -319,12 +375,12 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
         const int bins = 1 << bits;
         cluster.sync();  // nobody reads what is cleared
         clear(bins);
-        for (int i = tid; i < n; i += blockDim.x) {
+        for (int i = tid; i < n; i += kThreads) {
           const float v = kv::to_float(s_l[i]);
           const uint32_t k = key_of(v);
           if (k < least || (shift + bits < 32 && k >> (shift + bits) != prefix)) continue;
           const u64 x = one(v);
-          if (x) add(bins - 1 - (k >> shift & (bins - 1)), x);
+          if (x) add(s.hist.low, s.hist.high, bins - 1 - (k >> shift & (bins - 1)), x);
         }
         find(bins, rest, -1.0);
         rest -= s.above;
@@ -440,16 +496,20 @@ __global__ void __launch_bounds__(kMostThreads) sample_kernel(const Args a) {
 template <typename T>
 static cudaError_t launch(const Args& a0, int64_t rows, cudaStream_t st) {
   Args a = a0;
+  // slices of 4096 logits at least; beyond 8 CTAs a row where rows leave most of the GPU idle
+  const int most = rows * kMostCluster <= 152 ? kMostCluster : kPortable;
   int ranks = 1;
-  while (ranks < kMostCluster && a.vocab > ranks * 4096) ranks *= 2;
+  while (ranks < most && a.vocab > ranks * 4096) ranks *= 2;
   a.slice = ((a.vocab + ranks - 1) / ranks + 7) / 8 * 8;
   const size_t smem = sizeof(Shared) + (size_t)a.slice * sizeof(T);
   if (cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)(sizeof(Shared) + kMostSlice * sizeof(T))))
     return e;
+  if (ranks > kPortable)
+    if (cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(rows * ranks));
-  cfg.blockDim = dim3(kMostThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -485,7 +545,7 @@ extern "C" int kq_sample(int dtype, const void* d_logits, int64_t row_stride, in
   if (int s = check_dtype(dtype)) return s;
   if (vocab < 1 || vocab > sample::kMostVocab)
     return fail(KQ_ERR_SHAPE, "vocab = %lld (1 to %d)", (long long)vocab, sample::kMostVocab);
-  if (rows < 0 || rows > 0x7fffffffll / sample::kMostCluster || row_stride < 0 || (rows > 1 && row_stride < vocab))
+  if (rows < 0 || rows > 0x7fffffffll / sample::kPortable || row_stride < 0 || (rows > 1 && row_stride < vocab))
     return fail(KQ_ERR_SHAPE, "rows = %lld, row_stride = %lld", (long long)rows, (long long)row_stride);
   if (rows == 0) return KQ_OK;
   if (!d_logits || !d_u || !d_token) return fail(KQ_ERR_INVALID_ARG, "NULL pointer");
