@@ -805,7 +805,7 @@ size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests,
  *    -infinity, or whose temperature or top_p or min_p is a NaN or whose temperature is
  *    negative or infinite, gets token -1 and prob 0, and sets
  *    KQ_ERR_NONFINITE for kq_device_status.
- *  - exp is one of fp32, of an argument kept to 2^-40; sums are of 64-bit
+ *  - exp is good to 2^-21 however large its argument; sums are of 64-bit
  *    integers, so the order of work changes no token.
  *  - vocab 1 to 393216; rows = 0 is a no-op.
  * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */

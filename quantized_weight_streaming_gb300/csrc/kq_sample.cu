@@ -93,19 +93,29 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// A row's weights.  EXACT: the difference from the largest is kept to its rounding error too (of 16-bit logits it has none
+// that matters: 2^-20 at worst, where logits are 2^20 steps apart).
+template <bool EXACT>
 struct Row {
-  float most;         // the largest logit
-  float hi, lo;       // log2(e) / temperature in two floats
-  bool infinite;      // the largest is infinity: those alone weigh, one each
-  // exp((v - most) / temperature): the difference and its product with the factor are kept to twice fp32's bits, so the
-  // error is that of exp2f alone however large the argument is.
+  float most;      // the largest logit
+  float hi, lo;    // log2(e) / temperature in two floats
+  float low;       // differences below it weigh nothing
+  bool infinite;   // the largest is infinity: those alone weigh, one each
+  // exp((v - most) / temperature): the product with the factor is kept to twice fp32's bits, so the error is that of the
+  // exponential instruction (2^-22) however large the argument is.
   __device__ __forceinline__ float exp_of(float v) const {
-    if (infinite) return v == most ? 1.f : 0.f;
-    const float d = v - most, b = d - v, err = (v - (d - b)) - (most + b);  // v - most = d + err exactly
+    const float d = fmaxf(v - most, low);
+    float rest = d * lo;
+    if (EXACT) {
+      const float b = d - v, err = (v - (d - b)) - (most + b);  // v - most = d + err exactly
+      rest = fmaf(d > low ? err : 0.f, hi, rest);
+    }
     const float p = d * hi;
-    if (!(p > -160.f)) return 0.f;
-    const float rest = fmaf(d, hi, -p) + fmaf(d, lo, err * hi);
-    return exp2f(p) * fmaf(rest, 0.69314718f, 1.f);
+    rest += fmaf(d, hi, -p);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
+    e = fmaf(e * rest, 0.69314718f, e);
+    return infinite ? (v == most ? 1.f : 0.f) : e;
   }
   __device__ __forceinline__ u64 weight(float v) const { return (u64)__float2ull_rn(exp_of(v) * kOne); }
 };
@@ -162,6 +172,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   } else {
     for (int i = tid; i < n; i += kThreads) see(s_l[i] = src[i]);
   }
+  const int vecs = (n + kVec - 1) / kVec;
+  for (int i = n + tid; i < vecs * kVec; i += kThreads) s_l[i] = kv::from_float<T>(-INFINITY);  // weighs nothing
+  // f(value) of each logit of the slice, in any order
+  auto each = [&](auto f) {
+    for (int i = tid; i < vecs; i += kThreads) {
+      union { uint4 u; T t[kVec]; } x;
+      x.u = reinterpret_cast<const uint4*>(s_l)[i];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) f(kv::to_float(x.t[e]));
+    }
+  };
+  // x of the cluster's CTAs, each lane that of one
+  auto of_lane = [&](const auto Shared::*field, auto none) {
+    auto v = none;
+    if (lane < ranks) v = cluster.map_shared_rank(&s, lane)->*field;
+    return v;
+  };
   float* fpart = reinterpret_cast<float*>(s.part);
   int* ipart = reinterpret_cast<int*>(s.part);
   most = block_reduce(most, fpart, [](float x, float y) { return fmaxf(x, y); }, -INFINITY);
@@ -169,12 +196,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   nan = __syncthreads_or(nan);
   if (tid == 0) s.most = most, s.least = lowest, s.nan = nan;
   cluster.sync();
-  for (int c = 0; c < ranks; ++c) {
-    const Shared* o = cluster.map_shared_rank(&s, c);
-    most = fmaxf(most, o->most);
-    lowest = fminf(lowest, o->least);
-    nan |= o->nan;
+  most = of_lane(&Shared::most, -INFINITY), lowest = of_lane(&Shared::least, INFINITY);
+  nan = of_lane(&Shared::nan, 0);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    lowest = fminf(lowest, __shfl_xor_sync(~0u, lowest, o));
   }
+  most = __shfl_sync(~0u, most, 0), lowest = __shfl_sync(~0u, lowest, 0);
+  nan = __any_sync(~0u, nan);
 
   const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
   const float min_p = a.min_p ? a.min_p[row] : 0.f;
@@ -190,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return;
   }
 
-  Row w;
+  Row<sizeof(T) == 4> w;
   w.most = most;
   w.infinite = isinf(most);
   if (t == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f) {  // the largest alone, its lowest id
@@ -210,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
   const double factor = 1.4426950408889634 / (double)t;
   w.hi = (float)fmin(factor, 3.0e38);
-  w.lo = (float)fmin(factor - (double)w.hi, 1.0e30);
+  w.lo = (float)(factor - (double)w.hi);
+  if (!(fabsf(w.lo) < 1.0e30f)) w.lo = 0.f;
+  w.low = fmaxf(-200.f / w.hi, -3.0e38f);
 
   auto add = [&](uint32_t* low, uint32_t* high, int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
     const uint32_t lo = (uint32_t)x, old = atomicAdd(&low[bin], lo);
@@ -239,38 +271,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     __syncthreads();
     return x;
   };
+  // The cluster's sum of a field, and that of the CTAs before this one.
+  auto ranks_sum = [&](const u64 Shared::*field, u64& lower, u64& all) {
+    const u64 own = of_lane(field, (u64)0);
+    u64 x = own;
+#pragma unroll
+    for (int o = 1; o < kMostCluster; o *= 2) {
+      const u64 y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    all = __shfl_sync(~0u, x, kMostCluster - 1);
+    lower = __shfl_sync(~0u, x - own, rank);
+  };
   // Sums the histogram over the cluster, a share of the bins in each CTA, and finds the bin, from the first on, in which the
   // running sum comes to `target`: s.bin, what lies before it (s.above) and in it (s.inside).  share >= 0: the target is that
   // share of the sum of all, rounded up, one at least.
   auto find = [&](int bins, u64& target, double share) {
     cluster.sync();
-    const int mine = bins / ranks, per = (mine + kThreads - 1) / kThreads;
-    const int from = rank * mine + min(mine, tid * per), to = rank * mine + min(mine, tid * per + per);
-    u64 bin[4], own = 0;  // 2048 bins and 512 threads at most
+    // four words of each kind a thread: four CTAs' of a bin, or fewer CTAs' of two or four bins
+    const int mine = bins / ranks, threads = max(1, ranks / 4), wide = max(1, 4 / ranks);
+    const int from = rank * mine + tid / threads * wide;
+    const bool here = tid / threads * wide < mine;
+    u64 bin[4] = {0, 0, 0, 0};
+    if (here) {
+      uint32_t low[4], high[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      bin[i] = 0;
-      if (from + i >= to) continue;
-#pragma unroll
-      for (int c = 0; c < kMostCluster; ++c) {
-        if (c >= ranks) break;
+      for (int i = 0; i < 4; ++i) {
+        const int c = ranks >= 4 ? tid % threads * 4 + i : i % ranks, b = from + (ranks >= 4 ? 0 : i / ranks);
         const Shared* o = cluster.map_shared_rank(&s, c);
-        bin[i] += (u64)o->hist.high[from + i] << 32 | o->hist.low[from + i];
+        low[i] = o->hist.low[b], high[i] = o->hist.high[b];
       }
-      own += bin[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bin[i] = (u64)high[i] << 32 | low[i];
+      if (ranks == 2) bin[0] += bin[1], bin[1] = bin[2] + bin[3], bin[2] = bin[3] = 0;
+      if (ranks >= 4) bin[0] += bin[1] + bin[2] + bin[3], bin[1] = bin[2] = bin[3] = 0;
     }
+    for (int o = threads / 2; o; o >>= 1) bin[0] += __shfl_xor_sync(~0u, bin[0], o);
+    if (tid % threads) bin[0] = 0;
+    const u64 own = bin[0] + bin[1] + bin[2] + bin[3];
     u64 all = 0, x = scan(own, all);
     if (tid == 0) s.bins = all;
     cluster.sync();
-    u64 lower = 0;
-    all = 0;
-#pragma unroll
-    for (int c = 0; c < kMostCluster; ++c) {
-      if (c >= ranks) break;
-      const u64 y = cluster.map_shared_rank(&s, c)->bins;
-      if (c < rank) lower += y;
-      all += y;
-    }
+    u64 lower;
+    ranks_sum(&Shared::bins, lower, all);
     if (share >= 0.0) target = max((u64)ceil(share * (double)all), (u64)1);
     x += lower;
     if (x - own < target && target <= x) {
@@ -295,13 +338,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) {
     auto one = [&](float v) { return mass ? w.weight(v) : (u64)1; };
     clear(kBins);
-    for (int i = tid; i < n; i += kThreads) {
-      const float v = kv::to_float(s_l[i]);
-      if (key_of(v) <= least) continue;
-      const u64 x = one(v);
-      if (!mass) atomicAdd(&s.hist.low[step_of(v)], 1u);
-      else if (x) add(s.hist.low, s.hist.high, step_of(v), x);
-    }
+    const float above_value = least ? value_of(least) : -INFINITY;
+    if (mass)
+      each([&](float v) {
+        if (least && v <= above_value) return;
+        const u64 x = w.weight(v);
+        if (x) add(s.hist.low, s.hist.high, step_of(v), x);
+      });
+    else
+      each([&](float v) { atomicAdd(&s.hist.low[step_of(v)], 1u); });
     if (least_ties && rank == 0 && tid == 0)
       add(s.hist.low, s.hist.high, step_of(value_of(least)), least_ties * one(value_of(least)));
     find(kBins, target, share);
@@ -309,26 +354,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     u64 rest = target - s.above;
     if (tid == 0) s.listed = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const float v = kv::to_float(s_l[i]);
-      if (key_of(v) < least || step_of(v) != bin) continue;
+    each([&](float v) {
+      if (v < above_value || step_of(v) != bin) return;
       const int at = atomicAdd(&s.listed, 1);
       if (at < kList) s.list[at] = key_of(v);
-    }
+    });
     cluster.sync();
-    int count = 0;
-    for (int c = 0; c < ranks; ++c) count += cluster.map_shared_rank(&s, c)->listed;
+    const int part = of_lane(&Shared::listed, 0);
+    const int count = __reduce_add_sync(~0u, part);
     if (count <= kList) {
-      int at = 0;
-      for (int c = 0; c < ranks; ++c) {
-        const Shared* o = cluster.map_shared_rank(&s, c);
-        const int m = o->listed;
-        for (int i = tid; i < m; i += kThreads) {
+      if (warp < ranks) {  // a warp copies a CTA's
+        const Shared* o = cluster.map_shared_rank(&s, warp);
+        const int at = __reduce_add_sync(~0u, lane < warp ? part : 0), m = __shfl_sync(~0u, part, warp);
+        for (int i = lane; i < m; i += 32) {
           const uint32_t k = o->list[i];
           s.all.key[at + i] = k;
           s.all.weight[at + i] = one(value_of(k));
         }
-        at += m;
       }
       for (int i = tid; i < kSubs; i += kThreads) s.sub.low[i] = s.sub.high[i] = 0;
       if (tid == 0) s.members = 0;
@@ -393,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       ties = (rest + x - 1) / x;
       equal /= x;
     }
-    cluster.sync();
   };
 
   uint32_t key = 0;  // below every logit: all belong
@@ -424,8 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     }
     if (tid == 0) s.ties = all;
     cluster.sync();
-    ahead = before;
-    for (int c = 0; c < rank; ++c) ahead += cluster.map_shared_rank(&s, c)->ties;
+    ahead = before + __reduce_add_sync(~0u, lane < rank ? of_lane(&Shared::ties, 0) : 0);
   }
   auto kept = [&](float v) -> u64 {
     const float e = w.exp_of(v);
@@ -444,7 +484,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return in ? kept(v) : 0;
   };
   u64 sum = 0, seen = ahead;
-  for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
+  int i0 = lo;
+  if (!some) {  // four at a time, for they do not wait for one another
+    const float border_value = at_border ? value_of(key) : -INFINITY;
+    for (; i0 + 128 <= hi; i0 += 128) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = kv::to_float(s_l[i0 + 32 * e + lane]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v[e] >= border_value) sum += kept(v[e]);
+    }
+  }
+  for (int i = i0; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   __syncthreads();
@@ -457,12 +509,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
   if (tid == 0) s.kept = slice;
   cluster.sync();
-  u64 grand = 0;
-  for (int c = 0; c < ranks; ++c) {
-    const u64 x = cluster.map_shared_rank(&s, c)->kept;
-    if (c < rank) lower += x;
-    grand += x;
-  }
+  u64 grand, others;
+  ranks_sum(&Shared::kept, others, grand);
+  lower += others;
   const float u = a.u[row];
   const double part = (double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)grand;
   // the first whose running sum is over `part`; u = 1, or a product that rounds up to all, takes the last
