@@ -58,6 +58,7 @@ struct Args {
 typedef unsigned long long u64;
 
 constexpr int kList = 1024;
+constexpr int kFewK = 256;  // top_k up to which the candidates are gathered without a histogram
 
 // What the CTAs of a cluster show one another.
 struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
@@ -69,15 +70,20 @@ struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
       u64 weight[kList];
       uint32_t key[kList];  // of all slices
     } all;
+    u64 sorted[kList];      // key above the complement of the id
   };
   struct {
     uint32_t low[kSubs], high[kSubs];
   } sub;
-  uint32_t list[kList];  // keys of this slice's logits in the border's step
+  union {
+    uint32_t list[kList];  // keys of this slice's logits in the border's step
+    u64 top[kList];        // of those that may be among the top_k, each above the complement of its id
+  };
   u64 part[kWarps];
   u64 kept;              // this slice's kept weight
   u64 bins;              // the sum of this CTA's share of the bins
   float most, least;
+  uint32_t at_k, at_share;
   int32_t nan, ties, lowest, listed, members;
   int32_t bin, subbin;
   u64 above, inside, rest;
@@ -100,7 +106,6 @@ struct Row {
   float most;      // the largest logit
   float hi, lo;    // log2(e) / temperature in two floats
   float low;       // differences below it weigh nothing
-  bool infinite;   // the largest is infinity: those alone weigh, one each
   // exp((v - most) / temperature): the product with the factor is kept to twice fp32's bits, so the error is that of the
   // exponential instruction (2^-22) however large the argument is.
   __device__ __forceinline__ float exp_of(float v) const {
@@ -114,11 +119,50 @@ struct Row {
     rest += fmaf(d, hi, -p);
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
-    e = fmaf(e * rest, 0.69314718f, e);
-    return infinite ? (v == most ? 1.f : 0.f) : e;
+    return fmaf(e * rest, 0.69314718f, e);
   }
-  __device__ __forceinline__ u64 weight(float v) const { return (u64)__float2ull_rn(exp_of(v) * kOne); }
+  // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest.
+  static __device__ __forceinline__ u64 fixed(float e) {
+    const float top = e + 2.0f, rest = fmaf(e - (top - 2.0f), kOne, 12582912.0f);
+    const int32_t hi = (int32_t)__float_as_uint(top) - 0x40000000, lo = (int32_t)__float_as_uint(rest) - 0x4B400000;
+    return (u64)((int64_t)hi * (1 << 22) + lo);
+  }
+  __device__ __forceinline__ u64 weight(float v) const { return fixed(exp_of(v)); }
 };
+
+// Sorts 512 keys, one a thread, the largest first.
+__device__ __forceinline__ uint32_t sort_threads(uint32_t k, uint32_t* swap) {
+  const int tid = threadIdx.x;
+  for (int size = 2; size <= kThreads; size *= 2)
+    for (int stride = size / 2; stride; stride /= 2) {
+      uint32_t o;
+      if (stride < 32) {
+        o = __shfl_xor_sync(~0u, k, stride);
+      } else {
+        __syncthreads();
+        swap[tid] = k;
+        __syncthreads();
+        o = swap[tid ^ stride];
+      }
+      const bool larger = ((tid & size) == 0) == ((tid & stride) == 0);
+      k = larger ? max(k, o) : min(k, o);
+    }
+  return k;
+}
+
+// Sorts the first `count` (a power of two up to kList) of v, the largest first.
+__device__ __forceinline__ void sort_list(u64* v, int count) {
+  for (int size = 2; size <= count; size *= 2)
+    for (int stride = size / 2; stride; stride /= 2) {
+      __syncthreads();
+      const int i = threadIdx.x / stride * 2 * stride + threadIdx.x % stride;  // kThreads = kList / 2
+      if (i < count) {
+        const u64 x = v[i], y = v[i + stride];
+        if ((x < y) == ((i & size) == 0)) v[i] = y, v[i + stride] = x;
+      }
+    }
+  __syncthreads();
+}
 
 template <typename V, typename F>
 __device__ __forceinline__ V block_reduce(V v, V* part, F join, V none) {
@@ -148,6 +192,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const int first = rank * a.slice, n = max(0, min(a.slice, a.vocab - first));
   grid_dependency_wait();
   allow_dependent_launch();
+
+  const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
+  const float min_p = a.min_p ? a.min_p[row] : 0.f;
+  const int32_t top_k = a.top_k ? a.top_k[row] : 0;
+  const float u = a.u[row];
+  const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f, few = by_k && top_k <= kFewK;
 
   // the slice, its largest
   const T* src = static_cast<const T*>(a.logits) + row * a.row_stride + first;
@@ -191,6 +241,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   };
   float* fpart = reinterpret_cast<float*>(s.part);
   int* ipart = reinterpret_cast<int*>(s.part);
+  if (few) {  // what the top_k-th largest of all cannot lie below: a CTA's own, or the least of the CTAs' shares of top_k
+    const uint32_t k = sort_threads(most == -INFINITY ? 0 : key_of(most), s.list);
+    if (tid == top_k - 1) s.at_k = k;
+    if (tid == (top_k + ranks - 1) / ranks - 1) s.at_share = k;
+  }
   most = block_reduce(most, fpart, [](float x, float y) { return fmaxf(x, y); }, -INFINITY);
   lowest = block_reduce(lowest, fpart, [](float x, float y) { return fminf(x, y); }, INFINITY);
   nan = __syncthreads_or(nan);
@@ -205,10 +260,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
   most = __shfl_sync(~0u, most, 0), lowest = __shfl_sync(~0u, lowest, 0);
   nan = __any_sync(~0u, nan);
+  uint32_t bound = 0;
+  if (few) bound = max(__reduce_max_sync(~0u, of_lane(&Shared::at_k, 0u)), __reduce_min_sync(~0u, of_lane(&Shared::at_share, ~0u)));
 
-  const float t = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
-  const int32_t top_k = a.top_k ? a.top_k[row] : 0;
   const bool bad = nan || most == -INFINITY || !(t >= 0.f) || isinf(t) || isnan(top_p) || isnan(min_p);
   if (bad) {
     if (rank == 0 && tid == 0) {
@@ -220,9 +274,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return;
   }
 
-  Row<sizeof(T) == 4> w;
-  w.most = most;
-  w.infinite = isinf(most);
   if (t == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f) {  // the largest alone, its lowest id
     int at = 0x7fffffff;
     for (int i = tid; i < n; i += kThreads)
@@ -238,21 +289,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     cluster.sync();
     return;
   }
+  if (isinf(most)) {  // those alone weigh, one each
+    for (int i = tid; i < vecs * kVec; i += kThreads) s_l[i] = kv::from_float<T>(kv::to_float(s_l[i]) == most ? 0.f : -INFINITY);
+    most = 0.f;
+    bound = min(bound, key_of(0.f));
+    __syncthreads();
+  }
+  Row<sizeof(T) == 4> w;
+  w.most = most;
   const double factor = 1.4426950408889634 / (double)t;
   w.hi = (float)fmin(factor, 3.0e38);
   w.lo = (float)(factor - (double)w.hi);
   if (!(fabsf(w.lo) < 1.0e30f)) w.lo = 0.f;
   w.low = fmaxf(-200.f / w.hi, -3.0e38f);
 
-  auto add = [&](uint32_t* low, uint32_t* high, int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
-    const uint32_t lo = (uint32_t)x, old = atomicAdd(&low[bin], lo);
-    const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < old);
-    if (hi) atomicAdd(&high[bin], hi);
-  };
-  auto clear = [&](int bins) {
-    for (int b = tid; b < bins; b += kThreads) s.hist.low[b] = s.hist.high[b] = 0;
-    __syncthreads();
-  };
   // This thread's running sum of x over the CTA, and the sum of all.
   auto scan = [&](u64 x, u64& all) {
 #pragma unroll
@@ -270,6 +320,93 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     }
     __syncthreads();
     return x;
+  };
+  auto target_of = [&](double share, u64 all) {  // the least sum that is over that share, all at most
+    return min((u64)(share * (double)all) + 1, all);
+  };
+  const double share = (double)(u > 0.f ? fminf(u, 1.f) : 0.f);
+
+  if (few) {
+    if (tid == 0) s.listed = 0;
+    __syncthreads();
+    const float from = bound ? value_of(bound) : -INFINITY;
+    for (int i = tid; i < vecs; i += kThreads) {
+      union { uint4 u; T t[kVec]; } x;
+      x.u = reinterpret_cast<const uint4*>(s_l)[i];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float v = kv::to_float(x.t[e]);
+        if (!(v >= from) || v == -INFINITY) continue;
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kList) s.top[at] = (u64)key_of(v) << 32 | (uint32_t)~(first + i * kVec + e);
+      }
+    }
+    cluster.sync();
+    const int part = of_lane(&Shared::listed, 0);
+    const int count = __reduce_add_sync(~0u, part);
+    if (count <= kList) {  // the first CTA has them all then, and does the rest by itself
+      if (rank == 0) {
+        if (warp < ranks) {
+          const Shared* o = cluster.map_shared_rank(&s, warp);
+          const int at = __reduce_add_sync(~0u, lane < warp ? part : 0), m = __shfl_sync(~0u, part, warp);
+          for (int i = lane; i < m; i += 32) s.sorted[at + i] = o->top[i];
+        }
+        int wide = 2;
+        while (wide < count) wide *= 2;
+        for (int i = count + tid; i < wide; i += kThreads) s.sorted[i] = 0;
+        sort_list(s.sorted, wide);
+        const int most_kept = min(count, top_k);
+        u64 x[2], y[2], all;
+        bool in[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = 2 * tid + i;
+          y[i] = at < most_kept ? s.sorted[at] : 0;
+          in[i] = at < most_kept;
+          x[i] = in[i] ? w.weight(value_of((uint32_t)(y[i] >> 32))) : 0;
+        }
+        u64 run = scan(x[0] + x[1], all) - x[0] - x[1];
+        const u64 target = by_p ? max((u64)ceil((double)top_p * (double)all), (u64)1) : ~0ull;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          in[i] = in[i] && run < target && (2 * tid + i == 0 || w.exp_of(value_of((uint32_t)(y[i] >> 32))) >= min_p);
+          run += x[i];
+        }
+        // in the vocabulary's order: the id's complement in front
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (2 * tid + i < wide) s.sorted[2 * tid + i] = in[i] ? y[i] << 32 | y[i] >> 32 : 0;
+        sort_list(s.sorted, wide);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          y[i] = 2 * tid + i < wide ? s.sorted[2 * tid + i] : 0;
+          x[i] = y[i] ? w.weight(value_of((uint32_t)y[i])) : 0;
+        }
+        run = scan(x[0] + x[1], all) - x[0] - x[1];
+        const u64 at = target_of(share, all);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (run < at && at <= run + x[i]) {
+            a.token[row] = (int32_t)~(uint32_t)(y[i] >> 32);
+            if (a.prob) a.prob[row] = (float)((double)x[i] / (double)all);
+          }
+          run += x[i];
+        }
+      }
+      cluster.sync();
+      return;
+    }
+  }
+
+  auto add = [&](uint32_t* low, uint32_t* high, int bin, u64 x) {  // 64 bits by two words: the carry goes with the high one
+    const uint32_t lo = (uint32_t)x, old = atomicAdd(&low[bin], lo);
+    const uint32_t hi = (uint32_t)(x >> 32) + (old + lo < old);
+    if (hi) atomicAdd(&high[bin], hi);
+  };
+  auto clear = [&](int bins) {
+    for (int b = tid; b < bins; b += kThreads) s.hist.low[b] = s.hist.high[b] = 0;
+    __syncthreads();
   };
   // The cluster's sum of a field, and that of the CTAs before this one.
   auto ranks_sum = [&](const u64 Shared::*field, u64& lower, u64& all) {
@@ -333,8 +470,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 
   // The border at which the running sum, from the largest logit down, of one each (MASS false) or of the weights of those at
   // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.
-  const float steps = w.infinite ? 1.f : 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
-  auto step_of = [&](float v) { return (int)fminf((most - v) * steps, 2047.f); };  // falls as v grows (NaN, of infinities: the last, as all are then)
+  const float steps = 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
+  auto step_of = [&](float v) {  // falls as v grows
+    return (int)(__float_as_uint(fminf((most - v) * steps, 2047.f) + 8388608.f) & (kBins - 1));
+  };
   auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) {
     auto one = [&](float v) { return mass ? w.weight(v) : (u64)1; };
     clear(kBins);
@@ -376,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       if (tid == 0) s.members = 0;
       cluster.sync();  // the lists are read: they are used again
       // 1024 steps within the step; of the one that the border lies in, each with each
-      auto sub_of = [&](uint32_t k) { return (int)(((most - value_of(k)) * steps - (float)bin) * (float)kSubs); };
+      auto sub_of = [&](uint32_t k) { return (int)(((most - value_of(k)) * steps - ((float)bin - 0.5f)) * (float)kSubs); };
       auto sub = [&](uint32_t k) { return bin == kBins - 1 ? 0 : min(max(sub_of(k), 0), kSubs - 1); };
       for (int i = tid; i < count; i += kThreads) add(s.sub.low, s.sub.high, sub(s.all.key[i]), s.all.weight[i]);
       __syncthreads();
@@ -439,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 
   uint32_t key = 0;  // below every logit: all belong
   u64 ties = 0, equal = 0;
-  const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
   if (by_k) border(false, (u64)top_k, -1.0, 0, 0, key, ties, equal);
   if (by_p) border(true, 0, (double)top_p, key, ties, key, ties, equal);
   const bool at_border = by_k || by_p, some = at_border && ties < equal;  // some of the equal ones only
@@ -447,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 
   // The kept weight of each warp's run of the slice; where some of the equal ones at the border belong, they are counted off
   // in order.
-  const int run = (n + 32 * warps - 1) / (32 * warps) * 32, lo = min(n, warp * run), hi = min(n, lo + run);
+  const int run = (n + 32 * kVec * warps - 1) / (32 * kVec * warps) * (32 * kVec), lo = min(n, warp * run), hi = min(n, lo + run);
   u64 ahead = 0;
   if (some) {
     int mine = 0;
@@ -469,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
   auto kept = [&](float v) -> u64 {
     const float e = w.exp_of(v);
-    return e >= min_p || v == most ? (u64)__float2ull_rn(e * kOne) : 0;
+    return e >= min_p || v == most ? w.fixed(e) : 0;
   };
   // element i of a warp's run, which ends at `end`; all lanes together
   auto weigh = [&](int i, int end, u64& seen) -> u64 {
@@ -484,19 +622,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     return in ? kept(v) : 0;
   };
   u64 sum = 0, seen = ahead;
-  int i0 = lo;
-  if (!some) {  // four at a time, for they do not wait for one another
-    const float border_value = at_border ? value_of(key) : -INFINITY;
-    for (; i0 + 128 <= hi; i0 += 128) {
-      float v[4];
+  const float border_value = at_border ? value_of(key) : -INFINITY;
+  auto group = [&](int i) -> u64 {  // this lane's share of the kept weight of 32 kVec logits from i on
+    u64 x = 0;
+    if (i + lane * kVec >= hi) return x;
+    union { uint4 u; T t[kVec]; } l;
+    l.u = *reinterpret_cast<const uint4*>(s_l + i + lane * kVec);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = kv::to_float(s_l[i0 + 32 * e + lane]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (v[e] >= border_value) sum += kept(v[e]);
+    for (int e = 0; e < kVec; ++e) {
+      const float v = kv::to_float(l.t[e]);
+      if (v >= border_value) x += kept(v);
     }
-  }
-  for (int i = i0; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
+    return x;
+  };
+  if (some)
+    for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
+  else
+    for (int i = lo; i < hi; i += 32 * kVec) sum += group(i);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   __syncthreads();
@@ -512,14 +654,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   u64 grand, others;
   ranks_sum(&Shared::kept, others, grand);
   lower += others;
-  const float u = a.u[row];
-  const double part = (double)(u > 0.f ? fminf(u, 1.f) : 0.f) * (double)grand;
-  // the first whose running sum is over `part`; u = 1, or a product that rounds up to all, takes the last
-  const u64 target = min((u64)part + 1, grand);
+  const u64 target = target_of(share, grand);
   if (lower < target && target <= lower + sum) {
     seen = ahead;
     u64 at = lower;
-    for (int i = lo; i < hi; i += 32) {
+    int i = lo;
+    if (!some)
+      for (; i + 32 * kVec < hi; i += 32 * kVec) {
+        u64 x = group(i);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+        if (at + x >= target) break;
+        at += x;
+      }
+    for (; i < hi; i += 32) {
       const u64 own = weigh(i + lane, hi, seen);
       if (!__ballot_sync(~0u, own != 0)) continue;
       u64 x = own;
@@ -545,10 +693,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 template <typename T>
 static cudaError_t launch(const Args& a0, int64_t rows, cudaStream_t st) {
   Args a = a0;
-  // slices of 4096 logits at least; beyond 8 CTAs a row where rows leave most of the GPU idle
-  const int most = rows * kMostCluster <= 152 ? kMostCluster : kPortable;
+  // Slices of 4096 logits at least, and no more CTAs than the GPU takes at a time (two an SM), for much of a pass is waiting
+  // for one another (64 rows of 151936: 4 CTAs a row XX us, 8 YY us); more than 8 a row only where an SM has one.
   int ranks = 1;
-  while (ranks < most && a.vocab > ranks * 4096) ranks *= 2;
+  while (ranks < kMostCluster && a.vocab > ranks * 4096 && rows * 2 * ranks <= (ranks < kPortable ? 304 : 152)) ranks *= 2;
+  while ((int64_t)ranks * kMostSlice < a.vocab) ranks *= 2;
   a.slice = ((a.vocab + ranks - 1) / ranks + 7) / 8 * 8;
   const size_t smem = sizeof(Shared) + (size_t)a.slice * sizeof(T);
   if (cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
