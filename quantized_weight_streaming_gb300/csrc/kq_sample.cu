@@ -121,11 +121,16 @@ struct Row {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
     return fmaf(e * rest, 0.69314718f, e);
   }
-  // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest.
-  static __device__ __forceinline__ u64 fixed(float e) {
+  // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest (signed).
+  static __device__ __forceinline__ void fixed(float e, uint32_t& hi, int32_t& lo) {
     const float top = e + 2.0f, rest = fmaf(e - (top - 2.0f), kOne, 12582912.0f);
-    const int32_t hi = (int32_t)__float_as_uint(top) - 0x40000000, lo = (int32_t)__float_as_uint(rest) - 0x4B400000;
-    return (u64)((int64_t)hi * (1 << 22) + lo);
+    hi = __float_as_uint(top) - 0x40000000u, lo = (int32_t)(__float_as_uint(rest) - 0x4B400000u);
+  }
+  static __device__ __forceinline__ u64 fixed(float e) {
+    uint32_t hi;
+    int32_t lo;
+    fixed(e, hi, lo);
+    return ((u64)hi << 22) + (int64_t)lo;
   }
   __device__ __forceinline__ u64 weight(float v) const { return fixed(exp_of(v)); }
 };
@@ -150,17 +155,39 @@ __device__ __forceinline__ uint32_t sort_threads(uint32_t k, uint32_t* swap) {
   return k;
 }
 
-// Sorts the first `count` (a power of two up to kList) of v, the largest first.
+// Sorts the first `count` (a power of two up to kList) of v, the largest first; v is written before and read after by any
+// thread.  Up to 512 a thread has one in registers, and lanes exchange theirs where they can.
 __device__ __forceinline__ void sort_list(u64* v, int count) {
-  for (int size = 2; size <= count; size *= 2)
-    for (int stride = size / 2; stride; stride /= 2) {
-      __syncthreads();
-      const int i = threadIdx.x / stride * 2 * stride + threadIdx.x % stride;  // kThreads = kList / 2
-      if (i < count) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (count <= kThreads) {
+    u64 k = tid < count ? v[tid] : 0;
+    for (int size = 2; size <= count; size *= 2)
+      for (int stride = size / 2; stride; stride /= 2) {
+        u64 o;
+        if (stride < 32) {
+          if (tid / 32 * 32 >= count) continue;
+          o = __shfl_xor_sync(~0u, k, stride);
+        } else {
+          __syncthreads();
+          if (tid < count) v[tid] = k;
+          __syncthreads();
+          o = tid < count ? v[tid ^ stride] : 0;
+        }
+        const bool larger = ((tid & size) == 0) == ((tid & stride) == 0);
+        k = (k < o) == larger ? o : k;
+      }
+    __syncthreads();
+    if (tid < count) v[tid] = k;
+  } else {
+    for (int size = 2; size <= count; size *= 2)
+      for (int stride = size / 2; stride; stride /= 2) {
+        __syncthreads();
+        const int i = tid / stride * 2 * stride + tid % stride;  // kThreads = kList / 2
         const u64 x = v[i], y = v[i + stride];
         if ((x < y) == ((i & size) == 0)) v[i] = y, v[i + stride] = x;
       }
-    }
+  }
   __syncthreads();
 }
 
@@ -297,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   }
   Row<sizeof(T) == 4> w;
   w.most = most;
-  const double factor = 1.4426950408889634 / (double)t;
-  w.hi = (float)fmin(factor, 3.0e38);
-  w.lo = (float)(factor - (double)w.hi);
+  // log2(e) / t: the quotient, and what it lacks (1.44269502 + 1.925963e-8 is log2(e) to 48 bits)
+  w.hi = fminf(1.44269502f / t, 3.0e38f);
+  w.lo = (fmaf(-w.hi, t, 1.44269502f) + 1.92596303e-8f) / t;
   if (!(fabsf(w.lo) < 1.0e30f)) w.lo = 0.f;
   w.low = fmaxf(-200.f / w.hi, -3.0e38f);
 
@@ -374,6 +401,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         }
         // in the vocabulary's order: the id's complement in front
         __syncthreads();
+        wide = 2;
+        while (wide < most_kept) wide *= 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if (2 * tid + i < wide) s.sorted[2 * tid + i] = in[i] ? y[i] << 32 | y[i] >> 32 : 0;
@@ -624,16 +653,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   u64 sum = 0, seen = ahead;
   const float border_value = at_border ? value_of(key) : -INFINITY;
   auto group = [&](int i) -> u64 {  // this lane's share of the kept weight of 32 kVec logits from i on
-    u64 x = 0;
-    if (i + lane * kVec >= hi) return x;
     union { uint4 u; T t[kVec]; } l;
-    l.u = *reinterpret_cast<const uint4*>(s_l + i + lane * kVec);
+    const bool here = i + lane * kVec < hi;
+    if (here) l.u = *reinterpret_cast<const uint4*>(s_l + i + lane * kVec);
+    float v[kVec], top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[e] = here ? kv::to_float(l.t[e]) : -INFINITY, top = fmaxf(top, v[e]);
+    if (!__any_sync(~0u, top >= border_value)) return 0;
+    uint32_t hi_sum = 0;
+    int32_t lo_sum = 0;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      const float v = kv::to_float(l.t[e]);
-      if (v >= border_value) x += kept(v);
+      const float x = w.exp_of(v[e]);
+      uint32_t a;
+      int32_t b;
+      w.fixed(v[e] >= border_value && (x >= min_p || v[e] == most) ? x : 0.f, a, b);
+      hi_sum += a, lo_sum += b;
     }
-    return x;
+    return ((u64)hi_sum << 22) + (int64_t)lo_sum;
   };
   if (some)
     for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
