@@ -612,28 +612,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   const bool at_border = by_k || by_p, some = at_border && ties < equal;  // some of the equal ones only
   if (!some) ties = ~0ull;
 
-  // The kept weight of each warp's run of the slice; where some of the equal ones at the border belong, they are counted off
-  // in order.
+  // The kept weight of each warp's run of the slice; where only some of the equal ones at the border belong, these are counted
+  // off from one run to the next.
   const int run = (n + 32 * kVec * warps - 1) / (32 * kVec * warps) * (32 * kVec), lo = min(n, warp * run), hi = min(n, lo + run);
-  u64 ahead = 0;
-  if (some) {
-    int mine = 0;
-    for (int i = lo; i < hi; i += 32) {
-      const bool tie = i + lane < hi && key_of(kv::to_float(s_l[i + lane])) == key;
-      mine += __popc(__ballot_sync(~0u, tie));
-    }
-    __syncthreads();
-    if (lane == 0) ipart[warp] = mine;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int i = 0; i < warps; ++i) {
-      if (i < warp) before += ipart[i];
-      all += ipart[i];
-    }
-    if (tid == 0) s.ties = all;
-    cluster.sync();
-    ahead = before + __reduce_add_sync(~0u, lane < rank ? of_lane(&Shared::ties, 0) : 0);
-  }
   auto kept = [&](float v) -> u64 {
     const float e = w.exp_of(v);
     return e >= min_p || v == most ? w.fixed(e) : 0;
@@ -650,9 +631,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     }
     return in ? kept(v) : 0;
   };
-  u64 sum = 0, seen = ahead;
   const float border_value = at_border ? value_of(key) : -INFINITY;
-  auto group = [&](int i) -> u64 {  // this lane's share of the kept weight of 32 kVec logits from i on
+  const u64 tie_weight = some ? kept(border_value) : 0;
+  // This lane's share of the kept weight of 32 kVec logits from i on, those at the border left out where only some of them
+  // belong, and how many these are.
+  auto group = [&](int i, int& tied) -> u64 {
     union { uint4 u; T t[kVec]; } l;
     const bool here = i + lane * kVec < hi;
     if (here) l.u = *reinterpret_cast<const uint4*>(s_l + i + lane * kVec);
@@ -665,17 +648,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       const float x = w.exp_of(v[e]);
+      const bool tie = some && v[e] == border_value;
       uint32_t a;
       int32_t b;
-      w.fixed(v[e] >= border_value && (x >= min_p || v[e] == most) ? x : 0.f, a, b);
-      hi_sum += a, lo_sum += b;
+      w.fixed(v[e] >= border_value && !tie && (x >= min_p || v[e] == most) ? x : 0.f, a, b);
+      hi_sum += a, lo_sum += b, tied += tie;
     }
     return ((u64)hi_sum << 22) + (int64_t)lo_sum;
   };
-  if (some)
-    for (int i = lo; i < hi; i += 32) sum += weigh(i + lane, hi, seen);
-  else
-    for (int i = lo; i < hi; i += 32 * kVec) sum += group(i);
+  auto of_ties = [&](u64 before, int count) { return before < ties ? min(ties - before, (u64)count) * tie_weight : 0; };
+  u64 sum = 0, ahead = 0;
+  int tied = 0;
+  for (int i = lo; i < hi; i += 32 * kVec) sum += group(i, tied);
+  if (some) {
+    tied = __reduce_add_sync(~0u, tied);
+    __syncthreads();
+    if (lane == 0) ipart[warp] = tied;
+    __syncthreads();
+    int all = 0;
+    for (int i = 0; i < warps; ++i) {
+      if (i < warp) ahead += ipart[i];
+      all += ipart[i];
+    }
+    if (tid == 0) s.ties = all;
+    cluster.sync();
+    ahead += __reduce_add_sync(~0u, lane < rank ? of_lane(&Shared::ties, 0) : 0);
+    if (lane == 0) sum += of_ties(ahead, tied);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   __syncthreads();
@@ -693,17 +692,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   lower += others;
   const u64 target = target_of(share, grand);
   if (lower < target && target <= lower + sum) {
-    seen = ahead;
-    u64 at = lower;
+    u64 at = lower, seen = ahead;
     int i = lo;
-    if (!some)
-      for (; i + 32 * kVec < hi; i += 32 * kVec) {
-        u64 x = group(i);
+    for (; i + 32 * kVec < hi; i += 32 * kVec) {
+      int tied = 0;
+      u64 x = group(i, tied);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-        if (at + x >= target) break;
-        at += x;
-      }
+      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+      tied = __reduce_add_sync(~0u, tied);
+      x += of_ties(seen, tied);
+      if (at + x >= target) break;
+      at += x, seen += tied;
+    }
     for (; i < hi; i += 32) {
       const u64 own = weigh(i + lane, hi, seen);
       if (!__ballot_sync(~0u, own != 0)) continue;
