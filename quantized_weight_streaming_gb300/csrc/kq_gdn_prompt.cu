@@ -27,8 +27,7 @@
 // step of the rule lets a column grow by more than |v| (|k| <= 1, beta < 1, decays
 // of at most 1).
 //
-// T's columns and X's rows (x (1 + L) = p) are solved by a thread each, side by
-// side in four warps, in registers.
+// Measured: see DESIGN
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -55,7 +54,7 @@ struct PromptArgs {
   RuleArgs r;
   uint8_t* kq;      // [slot][key head] tiles
   uint8_t* tx;      // [slot][value head] tiles
-  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64
+  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64, the largest value
 };
 
 // Where a request's chunks lie among the slots: q_start / 64 + r is at least the slots of the requests before it.
@@ -83,17 +82,43 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
 }
 
-constexpr int kStride = kChunk + 4;  // of the triangular matrices' rows, in floats
-constexpr int kTriangle = kChunk * kStride * 4;
-constexpr int kChunkSmem = 3 * kTriangle;
-static_assert(kChunkSmem >= kTile, "the triangles lie over the tile");
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// c += (a_hi + a_lo) (b_hi + b_lo) of a 16 x 16 by 16 x 16 product, without that of the low parts.
+__device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
+  mma_f16(c0, ah, bh[0], bh[1]);
+  mma_f16(c1, ah, bh[2], bh[3]);
+  mma_f16(c0, ah, bl[0], bl[1]);
+  mma_f16(c1, ah, bl[2], bl[3]);
+  mma_f16(c0, al, bh[0], bh[1]);
+  mma_f16(c1, al, bh[2], bh[3]);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kStride = kChunk + 4;                  // of -L's rows, in floats
+constexpr int kSide = 80;                            // bytes between rows of the 32 x 32 product in between
+constexpr int kLAt = kTile, kSideAt = kLAt + kChunk * kStride * 4, kChunkSmem = kSideAt + 2 * 32 * kSide;
 
 // One chunk and value head: the tile of its keys and queries, T and X, the rows' factors.
+//
+// T is solved by blocks of 32: the two on the diagonal column by column, a thread each, then the one below by two products
+// with the tensor cores, T21 = T22 (-L21) T11.  X = P T follows from the products' own layout: what a warp's mma leaves of
+// its queries' rows is, times the decays, the operand of the next.  (Solving all of T and X in threads' registers took twice
+// the instructions: 382 us for 129 chunks of 48 heads.)
 template <typename T>
-__global__ void __launch_bounds__(128) gdn_chunk_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
+  __shared__ __align__(16) float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
   __shared__ double s_first;
+  __shared__ uint32_t s_vmax[4];
   grid_dependency_wait();
   allow_dependent_launch();
   const RuleArgs& a = p.r;
@@ -119,17 +144,23 @@ __global__ void __launch_bounds__(128) gdn_chunk_kernel(const PromptArgs p) {
   const int64_t first = req.first + c * kChunk;
   uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kTile;
 
+  // keys and queries: a power of two per row that brings its largest to [1, 2), then fp16; the rows' norms
+#pragma unroll 4
   for (int e = tid; e < 2 * kChunk * 16; e += 128) {
     const int row = e / 16, vec = e % 16, i = row % kChunk;
+    kv::Raw<T, 8> raw;
+    raw.clear();
+    if (i < n) raw.load(reinterpret_cast<const T*>((row < kChunk ? a.k : a.q).at(first + i, hk)) + 8 * vec);
     float v[8];
+    raw.get(v);
+    uint32_t most2 = 0;  // of 16-bit patterns without their signs, which order as the numbers do
 #pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] = 0.f;
-    if (i < n) kv::load8(reinterpret_cast<const T*>((row < kChunk ? a.k : a.q).at(first + i, hk)) + 8 * vec, v);
-    float most = 0.f;
+    for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw.u[x] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) most = fmaxf(most, fabsf(v[x]));
-#pragma unroll
-    for (int o = 8; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+    for (int o = 8; o; o >>= 1) most2 = __vmaxu2(most2, __shfl_xor_sync(~0u, most2, o));
+    union { uint16_t b; T t; } top;
+    top.b = (uint16_t)max(most2 >> 16, most2 & 0xFFFFu);
+    const float most = kv::to_float(top.t);
     const int power = (int)(__float_as_uint(most) >> 23);
     const float f = power == 255 || most == 0.f ? 1.f : __uint_as_float((uint32_t)max(254 - power, 1) << 23);
     float sum = 0.f;
@@ -145,15 +176,30 @@ __global__ void __launch_bounds__(128) gdn_chunk_kernel(const PromptArgs p) {
     if (h % group == 0) *reinterpret_cast<uint4*>(kq + at) = u;
     if (vec == 0) (row < kChunk ? s_fk : s_fq)[i] = i < n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
   }
+  {  // the largest value
+    uint32_t most2 = 0;
+#pragma unroll
+    for (int e = tid; e < kChunk * 16; e += 128) {
+      kv::Raw<T, 8> raw;
+      raw.clear();
+      if (e / 16 < n) raw.load(reinterpret_cast<const T*>(a.v.at(first + e / 16, h)) + 8 * (e % 16));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw.u[x] & 0x7FFF7FFFu);
+    }
+    const uint32_t top = __reduce_max_sync(~0u, max(most2 >> 16, most2 & 0xFFFFu));
+    if (lane == 0) s_vmax[warp] = top;
+  }
 
-  // decays: running sums in 64 bits, kept as two floats, for what counts is the difference of two that may be large
+  // decays: running sums of their base-2 logarithms in 64 bits, kept as two floats, for what counts is the difference of two
+  // that may be large
   double g = 0.0;
   float beta = 0.f;
   if (tid < kChunk) {
     if (tid < n) {
       const int64_t token = first + tid;
       // e^-200 is nothing in fp32, and sums of 64 such keep 2^-38 of what follows them
-      g = fmaxf(log_decay(kv::to_float(reinterpret_cast<const T*>(a.a + token * a.a_stride)[h]), a.a_log[h], a.dt_bias[h]), -200.f);
+      g = 1.4426950408889634 * (double)fmaxf(log_decay(kv::to_float(reinterpret_cast<const T*>(a.a + token * a.a_stride)[h]),
+                                                       a.a_log[h], a.dt_bias[h]), -200.f);
       beta = sigmoid(kv::to_float(reinterpret_cast<const T*>(a.b + token * a.b_stride)[h]));
     }
 #pragma unroll
@@ -170,114 +216,187 @@ __global__ void __launch_bounds__(128) gdn_chunk_kernel(const PromptArgs p) {
     s_hi[tid] = hi, s_lo[tid] = (float)(g - (double)hi);
     s_beta[tid] = beta;
   }
-  __syncthreads();
 
-  // products of keys and of queries with keys: a warp 32 rows
+  // products of 16 rows of keys and 16 of queries a warp with the keys that they look back on
+  const uint32_t base = smem_u32(smem);
   float acc[2][8][4] = {};
-  {
-    const uint32_t base = smem_u32(smem);
 #pragma unroll
-    for (int k = 0; k < kD / 16; ++k) {
-      const uint32_t half = base + k / 4 * 16384;
-      uint32_t fa[2][4];
+  for (int k = 0; k < kD / 16; ++k) {
+    const uint32_t half = base + k / 4 * 16384;
+    uint32_t fa[2][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        ldmatrix4(fa[m], half + swizzled(warp * 32 + m * 16 + lane % 16, k % 4 * 2 + lane / 16));
+    for (int m = 0; m < 2; ++m) ldmatrix4(fa[m], half + swizzled(m * kChunk + warp * 16 + lane % 16, k % 4 * 2 + lane / 16));
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
-        uint32_t fb[4];
-        ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
+    for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
+      if (b > warp) continue;
+      uint32_t fb[4];
+      ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_f16(acc[m][2 * b], fa[m], fb[0], fb[1]);
-          mma_f16(acc[m][2 * b + 1], fa[m], fb[2], fb[3]);
-        }
+      for (int m = 0; m < 2; ++m) {
+        mma_f16(acc[m][2 * b], fa[m], fb[0], fb[1]);
+        mma_f16(acc[m][2 * b + 1], fa[m], fb[2], fb[3]);
       }
     }
   }
-  __syncthreads();  // the tile is read: the triangles go over it
-  float* nl = reinterpret_cast<float*>(smem);           // -L, by rows
-  float* nt = nl + kChunk * kStride;                    // -L, by columns
-  float* pp = nt + kChunk * kStride;                    // P, by rows
+  __syncthreads();  // the tile is read: T and X go over it
+  float* nl = reinterpret_cast<float*>(smem + kLAt);  // -L
+  uint32_t ph[4][4], pl[4][4];                        // P as operands of 16 x 16
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int e = 0; e < 2; ++e) {
+    const int i = warp * 16 + lane / 4 + e * 8;
+    const float hi = s_hi[i], lo = s_lo[i], fl = -s_beta[i] * s_fk[i], fp = a.scale * s_fq[i];
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = warp * 32 + m * 16 + lane / 4 + e / 2 * 8, i = row % kChunk, j = b * 8 + lane % 4 * 2 + e % 2;
-        const bool keys = row < kChunk;
-        float x = 0.f;
-        if (keys ? j < i : j <= i) {
-          const float ratio = expf((s_hi[i] - s_hi[j]) + (s_lo[i] - s_lo[j]));
-          x = acc[m][b][e] * s_fk[j] * ratio * (keys ? -s_beta[i] * s_fk[i] : a.scale * s_fq[i]);
-        }
-        if (keys) nl[i * kStride + j] = x, nt[j * kStride + i] = x;
-        else pp[i * kStride + j] = x;
-      }
+    for (int b = 0; b < 8; ++b) {
+      if (b / 2 > warp) continue;
+      const int j = b * 8 + lane % 4 * 2;
+      const float2 hj = *reinterpret_cast<const float2*>(s_hi + j), lj = *reinterpret_cast<const float2*>(s_lo + j);
+      const float2 fj = *reinterpret_cast<const float2*>(s_fk + j);
+      const float r0 = fj.x * exp2_fast((hi - hj.x) + (lo - lj.x)), r1 = fj.y * exp2_fast((hi - hj.y) + (lo - lj.y));
+      *reinterpret_cast<float2*>(nl + i * kStride + j) =
+          make_float2(j < i ? acc[0][b][2 * e] * r0 * fl : 0.f, j + 1 < i ? acc[0][b][2 * e + 1] * r1 * fl : 0.f);
+      split2(j <= i ? acc[1][b][2 * e] * r0 * fp : 0.f, j + 1 <= i ? acc[1][b][2 * e + 1] * r1 * fp : 0.f,
+             ph[b / 2][b % 2 * 2 + e], pl[b / 2][b % 2 * 2 + e]);
+    }
+  }
   __syncthreads();
 
-  uint8_t* tx = p.tx + (slot * a.v_heads + h) * kTile;
-  if (warp < 2) {  // column j of T from its first row down: t_i = [i = j] - sum_m L_im t_m
-    const int j = tid;
-    float2 t[kChunk / 2];
+  uint8_t* lowpart = smem + kTile / 2;
+  if (warp < 2) {  // column j of a diagonal block, from the first row down: t_i = [i = j] - sum_m L_im t_m
+    const int j = lane, at0 = 32 * warp;
+    const float* l0 = nl + at0 * kStride + at0;
+    float2 t[16];
 #pragma unroll
-    for (int m = 0; m < kChunk / 2; ++m) t[m] = make_float2(0.f, 0.f);
+    for (int m = 0; m < 16; ++m) t[m] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
+    for (int i = 0; i < 32; ++i) {
       float2 s0 = make_float2(i == j ? 1.f : 0.f, 0.f), s1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < i; m += 4) {  // what lies at and past i is zero
-        const float4 l = *reinterpret_cast<const float4*>(nl + i * kStride + m);
+        const float4 l = *reinterpret_cast<const float4*>(l0 + i * kStride + m);
         s0 = fma2(make_float2(l.x, l.y), t[m / 2], s0);
         s1 = fma2(make_float2(l.z, l.w), t[m / 2 + 1], s1);
       }
       const float x = (s0.x + s1.x) + (s0.y + s1.y);
       (i % 2 ? t[i / 2].y : t[i / 2].x) = x;
       const __half hi = __float2half_rn(x);
-      const uint32_t at = swizzled(i, j / 8) + j % 8 * 2;
-      *reinterpret_cast<__half*>(tx + at) = hi;
-      *reinterpret_cast<__half*>(tx + kTile / 2 + at) = __float2half_rn(x - __half2float(hi));
+      const uint32_t at = swizzled(at0 + i, (at0 + j) / 8) + j % 8 * 2;
+      *reinterpret_cast<__half*>(smem + at) = hi;
+      *reinterpret_cast<__half*>(lowpart + at) = __float2half_rn(x - __half2float(hi));
     }
-  } else {  // row i of X from its last column down: x_j = P_ij - sum_{m > j} x_m L_mj
-    const int i = tid - 64;
-    float2 x[kChunk / 2];
+  } else {  // zeros above the diagonal blocks
+    for (int e = tid - 64; e < 32 * 4 * 2; e += 64)
+      *reinterpret_cast<uint4*>((e & 1 ? lowpart : smem) + swizzled(e / 8, 4 + e / 2 % 4)) = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+
+  // the block below: a warp 16 of its 32 rows and 16 of its 32 columns
+  const int m0 = 32 + warp / 2 * 16, n0 = warp % 2 * 16;
+  const uint32_t low = base + kTile / 2, side = base + kSideAt;
+  {
+    float x0[4] = {}, x1[4] = {};
 #pragma unroll
-    for (int m = 0; m < kChunk / 2; ++m) x[m] = make_float2(0.f, 0.f);
+    for (int k = 0; k < 2; ++k) {
+      uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
-    for (int j = kChunk - 1; j >= 0; --j) {
-      float2 s0 = make_float2(pp[i * kStride + j], 0.f), s1 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int m = j / 4 * 4; m < kChunk; m += 4) {  // what lies at and before j is zero
-        const float4 l = *reinterpret_cast<const float4*>(nt + j * kStride + m);
-        s0 = fma2(make_float2(l.x, l.y), x[m / 2], s0);
-        s1 = fma2(make_float2(l.z, l.w), x[m / 2 + 1], s1);
+      for (int e = 0; e < 4; ++e) {
+        const float2 l = *reinterpret_cast<const float2*>(nl + (m0 + lane / 4 + e % 2 * 8) * kStride + k * 16 + lane % 4 * 2 + e / 2 * 8);
+        split2(l.x, l.y, ah[e], al[e]);
       }
-      (j % 2 ? x[j / 2].y : x[j / 2].x) = (s0.x + s1.x) + (s0.y + s1.y);
-      if (j % 8 == 0) {
-        uint4 hi, lo;
-        split2(x[j / 2].x, x[j / 2].y, hi.x, lo.x), split2(x[j / 2 + 1].x, x[j / 2 + 1].y, hi.y, lo.y);
-        split2(x[j / 2 + 2].x, x[j / 2 + 2].y, hi.z, lo.z), split2(x[j / 2 + 3].x, x[j / 2 + 3].y, hi.w, lo.w);
-        const uint32_t at = swizzled(64 + i, j / 8);
-        *reinterpret_cast<uint4*>(tx + at) = hi;
-        *reinterpret_cast<uint4*>(tx + kTile / 2 + at) = lo;
-      }
+      const uint32_t at = swizzled(k * 16 + lane % 16, n0 / 8 + lane / 16);
+      ldmatrix4_t(bh, base + at);
+      ldmatrix4_t(bl, low + at);
+      mma_parts(x0, x1, ah, al, bh, bl);
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      uint8_t* to = smem + kSideAt + (m0 - 32 + lane / 4 + e * 8) * kSide + (n0 + lane % 4 * 2) * 2;
+      split2(x0[2 * e], x0[2 * e + 1], hi, lo);
+      *reinterpret_cast<uint32_t*>(to) = hi, *reinterpret_cast<uint32_t*>(to + 32 * kSide) = lo;
+      split2(x1[2 * e], x1[2 * e + 1], hi, lo);
+      *reinterpret_cast<uint32_t*>(to + 16) = hi, *reinterpret_cast<uint32_t*>(to + 32 * kSide + 16) = lo;
+    }
+  }
+  __syncthreads();
+  {
+    float x0[4] = {}, x1[4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t ah[4], al[4], bh[4], bl[4];
+      const uint32_t at = swizzled(m0 + lane % 16, 4 + k * 2 + lane / 16);
+      ldmatrix4(ah, base + at);
+      ldmatrix4(al, low + at);
+      const uint32_t from = side + (k * 16 + lane % 16) * kSide + (n0 + lane / 16 * 8) * 2;
+      ldmatrix4_t(bh, from);
+      ldmatrix4_t(bl, from + 32 * kSide);
+      mma_parts(x0, x1, ah, al, bh, bl);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      const int row = m0 + lane / 4 + e * 8;
+      uint32_t at = swizzled(row, n0 / 8) + lane % 4 * 4;
+      split2(x0[2 * e], x0[2 * e + 1], hi, lo);
+      *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
+      at = swizzled(row, n0 / 8 + 1) + lane % 4 * 4;
+      split2(x1[2 * e], x1[2 * e + 1], hi, lo);
+      *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
+    }
+  }
+  __syncthreads();
+
+  // X = P T
+  float x[8][4] = {};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k > warp) continue;
+#pragma unroll
+    for (int b = 0; b <= k; ++b) {
+      uint32_t bh[4], bl[4];
+      const uint32_t at = swizzled(k * 16 + lane % 16, b * 2 + lane / 16);
+      ldmatrix4_t(bh, base + at);
+      ldmatrix4_t(bl, low + at);
+      mma_parts(x[2 * b], x[2 * b + 1], ph[k], pl[k], bh, bl);
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 8; ++b)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t hi, lo;
+      const uint32_t at = swizzled(kChunk + warp * 16 + lane / 4 + e * 8, b) + lane % 4 * 4;
+      split2(x[b][2 * e], x[b][2 * e + 1], hi, lo);
+      *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
+    }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
+  if (tid == 0) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.tx + (slot * a.v_heads + h) * kTile),
+                 "r"(base), "r"(kTile)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
   if (tid < kChunk) {
     float* f = p.factors + (slot * a.v_heads + h) * kRowFactors;
-    const float decay = expf(s_hi[tid]), beta_i = s_beta[tid], fk = s_fk[tid];
+    const float decay = exp2_fast(s_hi[tid]), beta_i = s_beta[tid], fk = s_fk[tid];
     f[tid] = beta_i * decay * fk;
     f[kChunk + tid] = beta_i;
-    f[2 * kChunk + tid] = fk * expf((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
+    f[2 * kChunk + tid] = fk * exp2_fast((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
     f[3 * kChunk + tid] = a.scale * decay * s_fq[tid];
-    if (tid == 0) f[4 * kChunk] = expf(s_hi[kChunk - 1]);
+    if (tid == 0) {
+      union { uint16_t b; T t; } top;
+      top.b = (uint16_t)max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3]));
+      f[4 * kChunk] = exp2_fast(s_hi[kChunk - 1]);
+      f[4 * kChunk + 1] = kv::to_float(top.t);
+    }
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- the walk down the chunks --------------------------------------------------------
 
-constexpr int kWalkWarps = 9, kWorkers = 256;  // eight warps compute, one copies and issues the products
+constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;  // and one warp more, which copies and issues the products
+constexpr int kWide = kCols / (kWorkWarps / 4);             // columns of a thread: a lane of tensor memory has four threads
 constexpr int kStages = 2;
 constexpr int kStagesAt = 0;                          // [stage]: [K; Q], [T; X]
 constexpr int kStateAt = kStages * 2 * kTile;         // S: high part, low part, [128][64]
@@ -312,32 +431,36 @@ constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 32 numbers of a row of a [rows][64] operand, columns 32 half .., as two fp16 parts `low` bytes apart.
-__device__ __forceinline__ void put_row(uint8_t* tile, int low, int row, int half, const float (&v)[32]) {
+// kWide numbers of a row of a [rows][64] operand, columns kWide part .., as two fp16 parts `low` bytes apart.
+__device__ __forceinline__ void put_row(uint8_t* tile, int low, int row, int part, const float2 (&v)[kWide / 2]) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < kWide / 8; ++c) {
     uint4 hi, lo;
-    split2(v[8 * c], v[8 * c + 1], hi.x, lo.x), split2(v[8 * c + 2], v[8 * c + 3], hi.y, lo.y);
-    split2(v[8 * c + 4], v[8 * c + 5], hi.z, lo.z), split2(v[8 * c + 6], v[8 * c + 7], hi.w, lo.w);
-    const uint32_t at = swizzled(row, half * 4 + c);
+    split2(v[4 * c].x, v[4 * c].y, hi.x, lo.x), split2(v[4 * c + 1].x, v[4 * c + 1].y, hi.y, lo.y);
+    split2(v[4 * c + 2].x, v[4 * c + 2].y, hi.z, lo.z), split2(v[4 * c + 3].x, v[4 * c + 3].y, hi.w, lo.w);
+    const uint32_t at = swizzled(row, part * (kWide / 8) + c);
     *reinterpret_cast<uint4*>(tile + at) = hi;
     *reinterpret_cast<uint4*>(tile + low + at) = lo;
   }
 }
 
-__device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[32]) {
-  uint32_t u[32];
-  tmem_ld32(taddr, u);
+__device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[kWide / 2]) {
+  float f[kWide];
+  static_assert(kWide == 16, "one load");
+  tmem_ld16(taddr, f);
   tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+  for (int i = 0; i < kWide / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
 }
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 template <typename T>
-__global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], s_ready, r_ready, u_ready, d1_full, d2_full, d3_full;
-  __shared__ uint32_t s_tmem, s_most[8], s_vmost[4];
+  __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   grid_dependency_wait();
@@ -363,7 +486,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const Pr
     s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == kWorkWarps) {
     tmem_alloc(&s_tmem, kColumns);
     tmem_relinquish();
     tc_fence_before();
@@ -373,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const Pr
   const uint32_t tmem = s_tmem;
   const Gate gate{&s_abort};
 
-  if (warp == 8) {
+  if (warp == kWorkWarps) {
     if (elect_one()) {
       const uint64_t policy = l2_policy_evict_first();
       auto copy = [&](int c) {
@@ -424,26 +547,26 @@ __global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const Pr
     }
     __syncwarp();
   } else {
-    // lane `row` of tensor memory, columns 32 half ..
-    const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane, i = row % kChunk;
+    // lane `row` of tensor memory, columns kWide sub ..
+    const int quarter = warp % 4, sub = warp / 4, row = quarter * 32 + lane, i = row % kChunk;
     const bool keys = quarter < 2;  // rows of keys (R, U), or of queries (O)
-    const uint32_t mine = tmem + (quarter << 21) + half * 32;
-    const int col = part * kCols + half * 32;
+    const uint32_t mine = tmem + (quarter << 21) + sub * kWide;
+    const int col = part * kCols + sub * kWide;
     float* state = a.state + (((int64_t)req.slot * a.v_heads + h) * kD + row) * kD + col;
-    float S[32];
+    float2 S[kWide / 2];  // times 2^power
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kWide / 4; ++e) {
       const float4 x = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(state)[e];
-      S[4 * e] = x.x, S[4 * e + 1] = x.y, S[4 * e + 2] = x.z, S[4 * e + 3] = x.w;
+      S[2 * e] = make_float2(x.x, x.y), S[2 * e + 1] = make_float2(x.z, x.w);
     }
     // of the next chunk: values of this row, the rows' factors
-    kv::Raw<T, 32> value;
-    float f0 = 0.f, f1 = 0.f, f2 = 0.f, last = 1.f;
+    kv::Raw<T, kWide> value;
+    float f0 = 0.f, f1 = 0.f, f2 = 0.f, last = 1.f, vmax = 0.f;
     auto fetch = [&](int c) {
       value.clear();
       if (c >= chunks) return;
       const float* f = p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors;
-      last = f[4 * kChunk];
+      last = f[4 * kChunk], vmax = f[4 * kChunk + 1];
       if (keys) {
         f0 = f[i], f1 = f[kChunk + i], f2 = f[2 * kChunk + i];
         const int64_t t = (int64_t)c * kChunk + i;
@@ -452,97 +575,110 @@ __global__ void __launch_bounds__(32 * kWalkWarps, 1) gdn_prompt_kernel(const Pr
         f0 = f[3 * kChunk + i];
       }
     };
+    // x such that 64 max|v| + |s| < 2^x, given |s| < 2^s; and the power of two that brings that to 2^15
+    auto bound_of = [&](float v, int s) { return max((int)(__float_as_uint(v) >> 23) - 127 + 7, s) + 1; };
+    auto power_of = [&](int bound) { return min(max(15 - bound, -120), 120); };
     fetch(0);
-    for (int c = 0; c < chunks; ++c) {
-      const float k0 = f0, k1 = f1, k2 = f2, decay = last;
-      // the power of two that S, R and U are taken at: 64 max|v| + 12 max|S| comes to 2^14 at most
+    int power = 0;
+    // the first chunk: the largest of S, known to all
+    {
       uint32_t most = 0;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) most = max(most, __float_as_uint(S[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < kWide / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
       most = __reduce_max_sync(~0u, most);
-      if (lane == 0) s_most[warp] = most;
-      if (keys) {
-        float v[32];
-        value.get(v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(~0u, top);
-        if (lane == 0) s_vmost[quarter * 2 + half] = top;
-      }
+      if (lane == 0) s_most[1][warp] = most;
       named_barrier(1, kWorkers);
-      uint32_t sm = 0, vm = 0;
+      most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[1][lane] : 0u);
+      power = power_of(bound_of(vmax, (int)(most >> 23) - 127 + 5));  // a column is 12 entries long at most
+      const float2 up = both(power_of_two(power));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sm = max(sm, s_most[e]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) vm = max(vm, s_vmost[e]);
-      // exponents of bounds: 64 max|v| < 2^(ev + 7), 12 max|S| < 2^(es + 5)
-      const int bound = max((int)(vm >> 23) + 7, (int)(sm >> 23) + 5) - 127 + 1;
-      const int power = min(max(14 - bound, -126), 120);
-      const float up = __uint_as_float((uint32_t)(127 + power) << 23), down = __uint_as_float((uint32_t)(127 - power) << 23);
-      {
-        float s[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = S[e] * up;
-        put_row(smem + kStateAt, kD * kCols * 2, row, half, s);
-      }
+      for (int e = 0; e < kWide / 2; ++e) S[e] = mul2(S[e], up);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      const float k0 = f0, k1 = f1 * power_of_two(power), k2 = f2, decay = last, vnow = vmax;
+      put_row(smem + kStateAt, kD * kCols * 2, row, sub, S);
       fence_async();
-      tc_fence_before();
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < kWide / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
+      most = __reduce_max_sync(~0u, most);
+      if (lane == 0) s_most[c & 1][warp] = most;
+      __syncwarp();
       mbar_arrive(&s_ready);
-      float d[32], o[32];
+      float2 d[kWide / 2], o[kWide / 2];
       gate.wait(&d1_full, c & 1);
       tc_fence_after();
       read_columns(mine + kD1, d);
       if (keys) {
-        float v[32];
+        float v[kWide];
         value.get(v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) d[e] = fmaf(-k0, d[e], k1 * up * v[e]);
-        put_row(smem + kPartsAt, kChunk * kCols * 2, i, half, d);
+        for (int e = 0; e < kWide / 2; ++e)
+          d[e] = fma2(d[e], both(-k0), mul2(make_float2(v[2 * e], v[2 * e + 1]), both(k1)));
+        put_row(smem + kPartsAt, kChunk * kCols * 2, i, sub, d);
         fence_async();
         tc_fence_before();
         mbar_arrive(&r_ready);
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = k0 * d[e];
+        for (int e = 0; e < kWide / 2; ++e) o[e] = mul2(d[e], both(k0));
       }
       fetch(c + 1);
+      // The power of two of the next chunk: no column of S grows past 12 max|S| + 64 max|v| in this one.  It stays where the
+      // bound stays within fp16 and not too far below.
+      gate.wait(&s_ready, c & 1);  // passed by then: what the others wrote is seen
+      most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[c & 1][lane] : 0u);
+      const int grown = bound_of(vnow, (int)(most >> 23) - 127 - power + 5);
       gate.wait(&d2_full, c & 1);
       tc_fence_after();
       read_columns(mine + kD2, d);
       if (keys) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) d[e] *= k2;
-        put_row(smem + kPartsAt, kChunk * kCols * 2, i, half, d);
+        for (int e = 0; e < kWide / 2; ++e) d[e] = mul2(d[e], both(k2));
+        put_row(smem + kPartsAt, kChunk * kCols * 2, i, sub, d);
         fence_async();
         tc_fence_before();
         mbar_arrive(&u_ready);
       } else {
         const int64_t t = (int64_t)c * kChunk + i;
         if (t < req.count) {
+          const float2 down = both(power_of_two(-power));
           T* out = reinterpret_cast<T*>(a.out.at(req.first + t, h)) + col;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < kWide / 2; e += 4) {
             float y[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) y[x] = (o[e + x] + d[e + x]) * down;
-            kv::store8(out + e, y);
+            for (int x = 0; x < 4; ++x) {
+              const float2 z = mul2(add2(o[e + x], d[e + x]), down);
+              y[2 * x] = z.x, y[2 * x + 1] = z.y;
+            }
+            kv::store8(out + 2 * e, y);
           }
         }
       }
+      const int want = power_of(bound_of(vmax, grown));
+      const int move = c + 1 < chunks && (want < power || want > power + 3) ? min(max(want - power, -120), 120) : 0;
       gate.wait(&d3_full, c & 1);
       tc_fence_after();
       read_columns(mine + kD3, d);
+      tc_fence_before();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) S[e] = fmaf(decay, S[e], down * d[e]);
+      for (int e = 0; e < kWide / 2; ++e) S[e] = fma2(S[e], both(decay), d[e]);
+      if (move) {
+        const float2 by = both(power_of_two(move));
+#pragma unroll
+        for (int e = 0; e < kWide / 2; ++e) S[e] = mul2(S[e], by);
+        power += move;
+      }
     }
+    const float down = power_of_two(-power);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      reinterpret_cast<float4*>(state)[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+    for (int e = 0; e < kWide / 4; ++e)
+      reinterpret_cast<float4*>(state)[e] = make_float4(S[2 * e].x * down, S[2 * e].y * down, S[2 * e + 1].x * down, S[2 * e + 1].y * down);
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kWorkWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, kColumns);
   }
@@ -569,7 +705,7 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
     return e;
   const int64_t grid = a.s.requests * a.v_heads * (kD / kCols);
-  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(32 * kWalkWarps), kWalkSmem, st, p);
+  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 32), kWalkSmem, st, p);
 }
 
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
