@@ -46,7 +46,7 @@ using namespace tc;
 __device__ unsigned int g_prompt_status = 0;
 __device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_status, 1u << status); }
 
-constexpr int kD = 128, kCols = 64;     // head dimension; a CTA's columns
+constexpr int kD = 128;                 // head dimension
 constexpr int kTile = 32768;            // bytes of [K; Q], or of [T; X] in two parts
 constexpr int kRowFactors = 4 * kChunk + 4;
 
@@ -395,14 +395,27 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
 
 // ---- the walk down the chunks --------------------------------------------------------
 
-constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;  // and one warp more, which copies and issues the products
-constexpr int kWide = kCols / (kWorkWarps / 4);             // columns of a thread: a lane of tensor memory has four threads
+//
+// Everything is turned over here: a lane of tensor memory is a value dimension, so that S^T, R^T and (w U)^T are left
+// operands, which tensor memory holds, straight from the registers that made them, and the chunk's tiles are right ones:
+//
+//   D1 = S^T [K; Q]^T    D2 = R^T [T; X]^T    D3 = (w U)^T K
+//
+// With S, R and U as right operands in shared memory (64 value dimensions a CTA) each product read its left one, 4 KB, anew
+// for 64 columns: 80 cycles each where the tensor core needs 32, and half a head took 6900 cycles a chunk.
+//
+// Sixteen warps compute: a warp has 32 value dimensions (lanes) and a quarter of the columns (32 of S's rows, 16 tokens).  One
+// warp more copies tiles and issues products.  What the next step waits for goes first: S^T K, T's part of D2, D3; the part of
+// the queries fills the gaps, and a chunk's outputs are written while the next one's first product runs.
+
+constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;
+constexpr int kRows = kD / 4, kToks = kChunk / 4;  // a thread's key dimensions of S, and its tokens
 constexpr int kStages = 2;
-constexpr int kStagesAt = 0;                          // [stage]: [K; Q], [T; X]
-constexpr int kStateAt = kStages * 2 * kTile;         // S: high part, low part, [128][64]
-constexpr int kPartsAt = kStateAt + 2 * kD * kCols * 2;  // R, then w U: high part, low part, [64][64]
-constexpr int kWalkSmem = kPartsAt + 2 * kChunk * kCols * 2 + 1024;  // and room to align
-constexpr int kD1 = 0, kD2 = 64, kD3 = 128, kColumns = 256;  // tensor memory
+constexpr int kFactorBytes = kRowFactors * 4;
+constexpr int kStage = 2 * kTile + 2048;           // [K; Q], [T; X], factors
+constexpr int kWalkSmem = kStages * kStage + 1024;  // and room to align
+// tensor memory: S^T K and then U; S^T Q; the rest of O; R's parts; D3; S's parts, U's over the first of them
+constexpr int kDk = 0, kDq = 64, kDx = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
 
 // Barriers that are waited on with a limit; after one ran out all waits return at once, and the warps run through.
 struct Gate {
@@ -421,45 +434,54 @@ struct Gate {
   }
 };
 
-// Descriptor of an operand whose rows (128 bytes, 128-byte swizzle) run along K and whose M or N lies along the row: groups
-// of 64 of M or N `wide` bytes apart, of eight K 1024.
+// Descriptor of an operand whose rows (128 bytes, 128-byte swizzle) run along K and whose N lies along the row: groups of 64
+// of N `wide` bytes apart, of eight K 1024.
 __device__ __forceinline__ uint64_t across_desc(const void* at, uint32_t wide) {
   const uint64_t start = (uint64_t)((smem_u32(at) >> 4) & 0x3FFF);
   return start | ((uint64_t)(wide >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-constexpr uint32_t kAcrossA = 1u << 15, kAcrossB = 1u << 16;
-
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// kWide numbers of a row of a [rows][64] operand, columns kWide part .., as two fp16 parts `low` bytes apart.
-__device__ __forceinline__ void put_row(uint8_t* tile, int low, int row, int part, const float2 (&v)[kWide / 2]) {
-#pragma unroll
-  for (int c = 0; c < kWide / 8; ++c) {
-    uint4 hi, lo;
-    split2(v[4 * c].x, v[4 * c].y, hi.x, lo.x), split2(v[4 * c + 1].x, v[4 * c + 1].y, hi.y, lo.y);
-    split2(v[4 * c + 2].x, v[4 * c + 2].y, hi.z, lo.z), split2(v[4 * c + 3].x, v[4 * c + 3].y, hi.w, lo.w);
-    const uint32_t at = swizzled(row, part * (kWide / 8) + c);
-    *reinterpret_cast<uint4*>(tile + at) = hi;
-    *reinterpret_cast<uint4*>(tile + low + at) = lo;
-  }
-}
-
-__device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[kWide / 2]) {
-  float f[kWide];
-  static_assert(kWide == 16, "one load");
-  tmem_ld16(taddr, f);
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < kWide / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
-}
+constexpr uint32_t kAcross = 1u << 16;  // of an instruction whose right operand lies so
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// 2 N numbers of a lane as two fp16 parts, in N columns each.
+template <int N>
+__device__ __forceinline__ void put_parts(uint32_t hi_at, uint32_t lo_at, const float2 (&v)[N]) {
+  static_assert(N % 8 == 0, "stores of eight columns");
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split2(v[c + e].x, v[c + e].y, hi[e], lo[e]);
+    tmem_st8(hi_at + c, hi);
+    tmem_st8(lo_at + c, lo);
+  }
+  tmem_st_wait();
+}
+
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[N]) {
+  static_assert(N == 8 || N == 16, "one load");
+  if constexpr (N == 8) {
+    float f[16];
+    tmem_ld16(taddr, f);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  } else {
+    uint32_t f[32];
+    tmem_ld32(taddr, f);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1]));
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], s_ready, r_ready, u_ready, d1_full, d2_full, d3_full;
+  __shared__ __align__(8) uint64_t full[kStages], s_ready, r_ready, u_ready, o_read, k_done, u_done, s_done, x_done;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -467,8 +489,8 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
   allow_dependent_launch();
   const RuleArgs& a = p.r;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int part = blockIdx.x % (kD / kCols), h = blockIdx.x / (kD / kCols) % a.v_heads;
-  const int64_t r = blockIdx.x / (kD / kCols) / a.v_heads;
+  const int h = blockIdx.x % a.v_heads;
+  const int64_t r = blockIdx.x / a.v_heads;
   const Request req = read_request(a.s, r, a.max_new);
   if (req.status && tid == 0) prompt_flag(req.status);
   if (!req.count || req.count <= a.short_most) return;
@@ -477,12 +499,8 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
   const int hk = h / (a.v_heads / a.k_heads);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
-    mbar_init(&s_ready, kWorkers);
-    mbar_init(&r_ready, kWorkers / 2);
-    mbar_init(&u_ready, kWorkers / 2);
-    mbar_init(&d1_full, 1);
-    mbar_init(&d2_full, 1);
-    mbar_init(&d3_full, 1);
+    for (uint64_t* b : {&s_ready, &r_ready, &u_ready, &o_read}) mbar_init(b, kWorkers);
+    for (uint64_t* b : {&k_done, &u_done, &s_done, &x_done}) mbar_init(b, 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -500,182 +518,202 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
     if (elect_one()) {
       const uint64_t policy = l2_policy_evict_first();
       auto copy = [&](int c) {
-        uint8_t* at = smem + kStagesAt + c % kStages * 2 * kTile;
+        uint8_t* at = smem + c % kStages * kStage;
         uint64_t* bar = &full[c % kStages];
-        mbar_arrive_expect_tx(bar, 2 * kTile);
+        mbar_arrive_expect_tx(bar, 2 * kTile + kFactorBytes);
         bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kTile, kTile, bar, policy);
         bulk_g2s(at + kTile, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
+        bulk_g2s(at + 2 * kTile, p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors, kFactorBytes, bar, policy);
       };
-      const uint32_t id1 = idesc_f16(128, kCols) | kAcrossB, id3 = id1 | kAcrossA;
-      const uint64_t sd = across_desc(smem + kStateAt, 0), ud = across_desc(smem + kPartsAt, 0);
-      constexpr uint64_t kStateLow = (kD * kCols * 2) >> 4, kPartLow = (kChunk * kCols * 2) >> 4;
+      const uint32_t narrow = idesc_f16(128, kChunk), wide = idesc_f16(128, kD) | kAcross;
+      constexpr uint64_t kLower = (kChunk * 128) >> 4, kLowPart = (kTile / 2) >> 4;  // a tile's rows 64.., its low parts
       copy(0);
       for (int c = 0; c < chunks; ++c) {
-        const uint8_t* at = smem + kStagesAt + c % kStages * 2 * kTile;
-        gate.wait(&s_ready, c & 1);  // the chunk before is done with, its stage is free
-        if (c + 1 < chunks) copy(c + 1);
-        gate.wait(&full[c % kStages], c / kStages & 1);
-        tc_fence_after();
-        const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile);
-#pragma unroll
-        for (int low = 0; low < 2; ++low)
+        const uint8_t* at = smem + c % kStages * kStage;
+        const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile), kt = across_desc(at, 16384);
+        auto state = [&](uint32_t to, uint64_t rows, int low) {
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k)
-            tc_mma_ss(tmem + kD1, kd + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4),
-                      sd + low * kStateLow + (uint64_t)(k * 2048 >> 4), id1, low || k);
-        tc_commit(&d1_full);
+            tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow,
+                      low || k);
+        };
+        auto solved = [&](uint32_t to, uint64_t rows) {
+#pragma unroll
+          for (int pass = 0; pass < 3; ++pass)  // high x high, low x high, high x low
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+              tc_mma_ts(tmem + to, tmem + kR + (pass == 1 ? kChunk / 2 : 0) + k * 8,
+                        rows + (pass == 2 ? kLowPart : 0) + (uint64_t)(k * 32 >> 4), narrow, pass || k);
+        };
+        gate.wait(&full[c % kStages], c / kStages & 1);
+        gate.wait(&s_ready, c & 1);
+        tc_fence_after();
+        state(kDk, kd, 0);
+        state(kDk, kd, 1);
+        tc_commit(&k_done);
+        gate.wait(&o_read, c & 1);  // the last chunk's outputs are in registers, its stage is free
+        if (c + 1 < chunks) copy(c + 1);
+        tc_fence_after();
+        state(kDq, kd + kLower, 0);
         gate.wait(&r_ready, c & 1);
         tc_fence_after();
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass)  // high x high, high x low, low x high
-#pragma unroll
-          for (int k = 0; k < kChunk / 16; ++k)
-            tc_mma_ss(tmem + kD2, td + (uint64_t)(((pass == 2 ? kTile / 2 : 0) + k * 32) >> 4),
-                      ud + (pass == 1 ? kPartLow : 0) + (uint64_t)(k * 2048 >> 4), id1, pass || k);
-        tc_commit(&d2_full);
+        solved(kDk, td);
+        tc_commit(&u_done);
+        state(kDq, kd + kLower, 1);
         gate.wait(&u_ready, c & 1);
         tc_fence_after();
-        const uint64_t kt = across_desc(at, 16384);
 #pragma unroll
         for (int low = 0; low < 2; ++low)
 #pragma unroll
           for (int k = 0; k < kChunk / 16; ++k)
-            tc_mma_ss(tmem + kD3, kt + (uint64_t)(k * 2048 >> 4), ud + low * kPartLow + (uint64_t)(k * 2048 >> 4), id3, low || k);
-        tc_commit(&d3_full);
+            tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
+        tc_commit(&s_done);
+        solved(kDx, td + kLower);
+        tc_commit(&x_done);
       }
-      gate.wait(&d3_full, chunks - 1 & 1);  // nothing is in flight when the memory goes
+      gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
     }
     __syncwarp();
   } else {
-    // lane `row` of tensor memory, columns kWide sub ..
-    const int quarter = warp % 4, sub = warp / 4, row = quarter * 32 + lane, i = row % kChunk;
-    const bool keys = quarter < 2;  // rows of keys (R, U), or of queries (O)
-    const uint32_t mine = tmem + (quarter << 21) + sub * kWide;
-    const int col = part * kCols + sub * kWide;
-    float* state = a.state + (((int64_t)req.slot * a.v_heads + h) * kD + row) * kD + col;
-    float2 S[kWide / 2];  // times 2^power
+    const int quarter = warp % 4, sub = warp / 4, dim = quarter * 32 + lane;  // a value dimension; which quarter of the columns
+    const uint32_t mine = tmem + (quarter << 21);
+    float* state = a.state + (((int64_t)req.slot * a.v_heads + h) * kD + sub * kRows) * kD + dim;
+    float2 S[kRows / 2];  // rows of two successive key dimensions, times 2^power
 #pragma unroll
-    for (int e = 0; e < kWide / 4; ++e) {
-      const float4 x = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(state)[e];
-      S[2 * e] = make_float2(x.x, x.y), S[2 * e + 1] = make_float2(x.z, x.w);
-    }
-    // of the next chunk: values of this row, the rows' factors
-    kv::Raw<T, kWide> value;
-    float f0 = 0.f, f1 = 0.f, f2 = 0.f, last = 1.f, vmax = 0.f;
+    for (int e = 0; e < kRows / 2; ++e)
+      S[e] = req.fresh ? make_float2(0.f, 0.f) : make_float2(state[2 * e * kD], state[(2 * e + 1) * kD]);
+    T value[kToks];  // of the next chunk
     auto fetch = [&](int c) {
-      value.clear();
-      if (c >= chunks) return;
-      const float* f = p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors;
-      last = f[4 * kChunk], vmax = f[4 * kChunk + 1];
-      if (keys) {
-        f0 = f[i], f1 = f[kChunk + i], f2 = f[2 * kChunk + i];
-        const int64_t t = (int64_t)c * kChunk + i;
-        if (t < req.count) value.load(reinterpret_cast<const T*>(a.v.at(req.first + t, h)) + col);
-      } else {
-        f0 = f[3 * kChunk + i];
-      }
+      const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
+      const char* from = a.v.at(req.first + t0, h) + dim * sizeof(T);
+#pragma unroll
+      for (int e = 0; e < kToks; ++e)
+        value[e] = t0 + e < req.count ? *reinterpret_cast<const T*>(from + e * a.v.token_stride) : kv::from_float<T>(0.f);
+    };
+    auto factors = [&](int c, int which) {  // of this warp's tokens
+      return reinterpret_cast<const float*>(smem + c % kStages * kStage + 2 * kTile) + which * kChunk + sub * kToks;
+    };
+    auto largest = [&]() {
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < kRows / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
+      return __reduce_max_sync(~0u, most);
     };
     // x such that 64 max|v| + |s| < 2^x, given |s| < 2^s; and the power of two that brings that to 2^15
     auto bound_of = [&](float v, int s) { return max((int)(__float_as_uint(v) >> 23) - 127 + 7, s) + 1; };
     auto power_of = [&](int bound) { return min(max(15 - bound, -120), 120); };
     fetch(0);
     int power = 0;
-    // the first chunk: the largest of S, known to all
+    float vmax = p.factors[(slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1], down = 1.f;
     {
-      uint32_t most = 0;
-#pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
-      most = __reduce_max_sync(~0u, most);
+      uint32_t most = largest();
       if (lane == 0) s_most[1][warp] = most;
       named_barrier(1, kWorkers);
       most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[1][lane] : 0u);
       power = power_of(bound_of(vmax, (int)(most >> 23) - 127 + 5));  // a column is 12 entries long at most
       const float2 up = both(power_of_two(power));
 #pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) S[e] = mul2(S[e], up);
+      for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(S[e], up);
     }
-    for (int c = 0; c < chunks; ++c) {
-      const float k0 = f0, k1 = f1 * power_of_two(power), k2 = f2, decay = last, vnow = vmax;
-      put_row(smem + kStateAt, kD * kCols * 2, row, sub, S);
-      fence_async();
-      uint32_t most = 0;
-#pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
-      most = __reduce_max_sync(~0u, most);
-      if (lane == 0) s_most[c & 1][warp] = most;
-      __syncwarp();
-      mbar_arrive(&s_ready);
-      float2 d[kWide / 2], o[kWide / 2];
-      gate.wait(&d1_full, c & 1);
+    // the outputs of chunk c, which were taken at 1 / down; the barrier tells that they and the chunk's factors are read
+    auto outputs = [&](int c) {
+      float2 q[kToks / 2], x[kToks / 2];
+      gate.wait(&x_done, c & 1);
       tc_fence_after();
-      read_columns(mine + kD1, d);
-      if (keys) {
-        float v[kWide];
-        value.get(v);
+      read_columns(mine + kDq + sub * kToks, q);
+      read_columns(mine + kDx + sub * kToks, x);
+      const float* f = factors(c, 3);
 #pragma unroll
-        for (int e = 0; e < kWide / 2; ++e)
-          d[e] = fma2(d[e], both(-k0), mul2(make_float2(v[2 * e], v[2 * e + 1]), both(k1)));
-        put_row(smem + kPartsAt, kChunk * kCols * 2, i, sub, d);
-        fence_async();
-        tc_fence_before();
-        mbar_arrive(&r_ready);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kWide / 2; ++e) o[e] = mul2(d[e], both(k0));
+      for (int e = 0; e < kToks / 2; e += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(f + 2 * e);
+        x[e] = mul2(fma2(q[e], make_float2(w.x, w.y), x[e]), both(down));
+        x[e + 1] = mul2(fma2(q[e + 1], make_float2(w.z, w.w), x[e + 1]), both(down));
       }
-      fetch(c + 1);
+      tc_fence_before();
+      mbar_arrive(&o_read);
+      const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
+      char* out = a.out.at(req.first + t0, h) + dim * sizeof(T);
+#pragma unroll
+      for (int e = 0; e < kToks; ++e)
+        if (t0 + e < req.count)
+          *reinterpret_cast<T*>(out + e * a.out.token_stride) = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
+    };
+    for (int c = 0; c < chunks; ++c) {
+      put_parts(mine + kS + sub * (kRows / 2), mine + kS + kD / 2 + sub * (kRows / 2), S);
+      tc_fence_before();
+      {
+        const uint32_t most = largest();
+        if (lane == 0) s_most[c & 1][warp] = most;
+        __syncwarp();
+      }
+      mbar_arrive(&s_ready);
+      if (c) outputs(c - 1);
+      else mbar_arrive(&o_read);
+      down = power_of_two(-power);
+      gate.wait(&full[c % kStages], c / kStages & 1);  // the factors
+      const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vnow = vmax;
+      float2 d[kToks / 2];
+      gate.wait(&k_done, c & 1);
+      tc_fence_after();
+      read_columns(mine + kDk + sub * kToks, d);
+      {
+        const float *f0 = factors(c, 0), *f1 = factors(c, 1);
+        const float2 up = both(power_of_two(power));
+#pragma unroll
+        for (int e = 0; e < kToks / 2; e += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(f0 + 2 * e), y = *reinterpret_cast<const float4*>(f1 + 2 * e);
+          const float2 v0 = mul2(make_float2(kv::to_float(value[2 * e]), kv::to_float(value[2 * e + 1])), up);
+          const float2 v1 = mul2(make_float2(kv::to_float(value[2 * e + 2]), kv::to_float(value[2 * e + 3])), up);
+          d[e] = fma2(d[e], make_float2(-x.x, -x.y), mul2(v0, make_float2(y.x, y.y)));
+          d[e + 1] = fma2(d[e + 1], make_float2(-x.z, -x.w), mul2(v1, make_float2(y.z, y.w)));
+        }
+      }
+      put_parts(mine + kR + sub * (kToks / 2), mine + kR + kChunk / 2 + sub * (kToks / 2), d);
+      tc_fence_before();
+      mbar_arrive(&r_ready);
+      if (c + 1 < chunks) {
+        fetch(c + 1);
+        vmax = p.factors[((slot0 + c + 1) * a.v_heads + h) * kRowFactors + 4 * kChunk + 1];
+      }
       // The power of two of the next chunk: no column of S grows past 12 max|S| + 64 max|v| in this one.  It stays where the
       // bound stays within fp16 and not too far below.
       gate.wait(&s_ready, c & 1);  // passed by then: what the others wrote is seen
-      most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[c & 1][lane] : 0u);
+      const uint32_t most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[c & 1][lane] : 0u);
       const int grown = bound_of(vnow, (int)(most >> 23) - 127 - power + 5);
-      gate.wait(&d2_full, c & 1);
+      gate.wait(&u_done, c & 1);
       tc_fence_after();
-      read_columns(mine + kD2, d);
-      if (keys) {
+      read_columns(mine + kDk + sub * kToks, d);
+      {
+        const float* f2 = factors(c, 2);
 #pragma unroll
-        for (int e = 0; e < kWide / 2; ++e) d[e] = mul2(d[e], both(k2));
-        put_row(smem + kPartsAt, kChunk * kCols * 2, i, sub, d);
-        fence_async();
-        tc_fence_before();
-        mbar_arrive(&u_ready);
-      } else {
-        const int64_t t = (int64_t)c * kChunk + i;
-        if (t < req.count) {
-          const float2 down = both(power_of_two(-power));
-          T* out = reinterpret_cast<T*>(a.out.at(req.first + t, h)) + col;
-#pragma unroll
-          for (int e = 0; e < kWide / 2; e += 4) {
-            float y[8];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 z = mul2(add2(o[e + x], d[e + x]), down);
-              y[2 * x] = z.x, y[2 * x + 1] = z.y;
-            }
-            kv::store8(out + 2 * e, y);
-          }
+        for (int e = 0; e < kToks / 2; e += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(f2 + 2 * e);
+          d[e] = mul2(d[e], make_float2(x.x, x.y)), d[e + 1] = mul2(d[e + 1], make_float2(x.z, x.w));
         }
       }
+      put_parts(mine + kS + sub * (kToks / 2), mine + kS + kChunk / 2 + sub * (kToks / 2), d);
+      tc_fence_before();
+      mbar_arrive(&u_ready);
       const int want = power_of(bound_of(vmax, grown));
       const int move = c + 1 < chunks && (want < power || want > power + 3) ? min(max(want - power, -120), 120) : 0;
-      gate.wait(&d3_full, c & 1);
+      gate.wait(&s_done, c & 1);
       tc_fence_after();
-      read_columns(mine + kD3, d);
+      float2 g[kRows / 2];
+      read_columns(mine + kD3 + sub * kRows, g);
       tc_fence_before();
 #pragma unroll
-      for (int e = 0; e < kWide / 2; ++e) S[e] = fma2(S[e], both(decay), d[e]);
+      for (int e = 0; e < kRows / 2; ++e) S[e] = fma2(S[e], both(decay), g[e]);
       if (move) {
         const float2 by = both(power_of_two(move));
 #pragma unroll
-        for (int e = 0; e < kWide / 2; ++e) S[e] = mul2(S[e], by);
+        for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(S[e], by);
         power += move;
       }
     }
-    const float down = power_of_two(-power);
+    outputs(chunks - 1);
+    const float back = power_of_two(-power);
 #pragma unroll
-    for (int e = 0; e < kWide / 4; ++e)
-      reinterpret_cast<float4*>(state)[e] = make_float4(S[2 * e].x * down, S[2 * e].y * down, S[2 * e + 1].x * down, S[2 * e + 1].y * down);
-    tc_fence_before();
+    for (int e = 0; e < kRows / 2; ++e) state[2 * e * kD] = S[e].x * back, state[(2 * e + 1) * kD] = S[e].y * back;
   }
   __syncthreads();
   if (warp == kWorkWarps) {
@@ -704,7 +742,7 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalkSmem)) return e;
   if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
     return e;
-  const int64_t grid = a.s.requests * a.v_heads * (kD / kCols);
+  const int64_t grid = a.s.requests * a.v_heads;
   return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 32), kWalkSmem, st, p);
 }
 
