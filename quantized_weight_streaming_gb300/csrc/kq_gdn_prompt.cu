@@ -405,14 +405,15 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
 // for 64 columns: 80 cycles each where the tensor core needs 32, and half a head took 6900 cycles a chunk.
 //
 // Sixteen warps compute: a warp has 32 value dimensions (lanes) and a quarter of the columns (32 of S's rows, 16 tokens).  One
-// warp more copies tiles and issues products.  What the next step waits for goes first: S^T K, T's part of D2, D3; the part of
-// the queries fills the gaps, and a chunk's outputs are written while the next one's first product runs.
+// warp more issues products, another copies tiles and the values' rows.  What the next step waits for goes first: S^T K, T's
+// part of D2; the queries' parts run while R and U are made, and the outputs are written while D3 runs.
 
 constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;
 constexpr int kRows = kD / 4, kToks = kChunk / 4;  // a thread's key dimensions of S, and its tokens
 constexpr int kStages = 2;
 constexpr int kFactorBytes = kRowFactors * 4;
-constexpr int kStage = 2 * kTile + 2048;           // [K; Q], [T; X], factors
+constexpr int kValuesAt = 2 * kTile, kFactorsAt = kValuesAt + kChunk * kD * 2;
+constexpr int kStage = kFactorsAt + 2048;          // [K; Q], [T; X], values, factors
 constexpr int kWalkSmem = kStages * kStage + 1024;  // and room to align
 // tensor memory: S^T K and then U; S^T Q; the rest of O; R's parts; D3; S's parts, U's over the first of them
 constexpr int kDk = 0, kDq = 64, kDx = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
@@ -479,9 +480,9 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[N]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], s_ready, r_ready, u_ready, o_read, k_done, u_done, s_done, x_done;
+  __shared__ __align__(8) uint64_t full[kStages], free[kStages], s_ready, r_ready, u_ready, k_done, u_done, s_done, x_done;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -498,8 +499,8 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
   const int64_t slot0 = chunk_base(req.first, r);
   const int hk = h / (a.v_heads / a.k_heads);
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
-    for (uint64_t* b : {&s_ready, &r_ready, &u_ready, &o_read}) mbar_init(b, kWorkers);
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&free[i], kWorkers + 1);
+    for (uint64_t* b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, kWorkers);
     for (uint64_t* b : {&k_done, &u_done, &s_done, &x_done}) mbar_init(b, 1);
     s_abort = 0;
     fence_barrier_init();
@@ -514,28 +515,37 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
   const uint32_t tmem = s_tmem;
   const Gate gate{&s_abort};
 
-  if (warp == kWorkWarps) {
-    if (elect_one()) {
-      const uint64_t policy = l2_policy_evict_first();
-      auto copy = [&](int c) {
-        uint8_t* at = smem + c % kStages * kStage;
-        uint64_t* bar = &full[c % kStages];
-        mbar_arrive_expect_tx(bar, 2 * kTile + kFactorBytes);
+  if (warp == kWorkWarps + 1) {  // copies
+    const uint64_t policy = l2_policy_evict_first();
+    for (int c = 0; c < chunks; ++c) {
+      if (c >= kStages) gate.wait(&free[c % kStages], c / kStages - 1 & 1);
+      uint8_t* at = smem + c % kStages * kStage;
+      uint64_t* bar = &full[c % kStages];
+      const int count = min(kChunk, req.count - c * kChunk);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, 2 * kTile + kFactorBytes + count * kD * (int)sizeof(T));
         bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kTile, kTile, bar, policy);
         bulk_g2s(at + kTile, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
-        bulk_g2s(at + 2 * kTile, p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors, kFactorBytes, bar, policy);
-      };
+        bulk_g2s(at + kFactorsAt, p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors, kFactorBytes, bar, policy);
+      }
+      __syncwarp();
+      for (int t = lane; t < count; t += 32)
+        bulk_g2s(at + kValuesAt + t * kD * sizeof(T), a.v.at(req.first + (int64_t)c * kChunk + t, h), kD * sizeof(T), bar, policy);
+    }
+  } else if (warp == kWorkWarps) {  // products
+    if (elect_one()) {
       const uint32_t narrow = idesc_f16(128, kChunk), wide = idesc_f16(128, kD) | kAcross;
       constexpr uint64_t kLower = (kChunk * 128) >> 4, kLowPart = (kTile / 2) >> 4;  // a tile's rows 64.., its low parts
-      copy(0);
       for (int c = 0; c < chunks; ++c) {
         const uint8_t* at = smem + c % kStages * kStage;
         const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile), kt = across_desc(at, 16384);
-        auto state = [&](uint32_t to, uint64_t rows, int low) {
+        auto state = [&](uint32_t to, uint64_t rows) {
 #pragma unroll
-          for (int k = 0; k < kD / 16; ++k)
-            tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow,
-                      low || k);
+          for (int low = 0; low < 2; ++low)
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k)
+              tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow,
+                        low || k);
         };
         auto solved = [&](uint32_t to, uint64_t rows) {
 #pragma unroll
@@ -548,18 +558,15 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
         gate.wait(&full[c % kStages], c / kStages & 1);
         gate.wait(&s_ready, c & 1);
         tc_fence_after();
-        state(kDk, kd, 0);
-        state(kDk, kd, 1);
+        state(kDk, kd);
         tc_commit(&k_done);
-        gate.wait(&o_read, c & 1);  // the last chunk's outputs are in registers, its stage is free
-        if (c + 1 < chunks) copy(c + 1);
-        tc_fence_after();
-        state(kDq, kd + kLower, 0);
+        state(kDq, kd + kLower);
         gate.wait(&r_ready, c & 1);
         tc_fence_after();
         solved(kDk, td);
         tc_commit(&u_done);
-        state(kDq, kd + kLower, 1);
+        solved(kDx, td + kLower);
+        tc_commit(&x_done);
         gate.wait(&u_ready, c & 1);
         tc_fence_after();
 #pragma unroll
@@ -568,10 +575,9 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
           for (int k = 0; k < kChunk / 16; ++k)
             tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
         tc_commit(&s_done);
-        solved(kDx, td + kLower);
-        tc_commit(&x_done);
+        tc_commit(&free[c % kStages]);
       }
-      gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
+      gate.wait(&s_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
     }
     __syncwarp();
   } else {
@@ -582,16 +588,8 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
 #pragma unroll
     for (int e = 0; e < kRows / 2; ++e)
       S[e] = req.fresh ? make_float2(0.f, 0.f) : make_float2(state[2 * e * kD], state[(2 * e + 1) * kD]);
-    T value[kToks];  // of the next chunk
-    auto fetch = [&](int c) {
-      const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
-      const char* from = a.v.at(req.first + t0, h) + dim * sizeof(T);
-#pragma unroll
-      for (int e = 0; e < kToks; ++e)
-        value[e] = t0 + e < req.count ? *reinterpret_cast<const T*>(from + e * a.v.token_stride) : kv::from_float<T>(0.f);
-    };
     auto factors = [&](int c, int which) {  // of this warp's tokens
-      return reinterpret_cast<const float*>(smem + c % kStages * kStage + 2 * kTile) + which * kChunk + sub * kToks;
+      return reinterpret_cast<const float*>(smem + c % kStages * kStage + kFactorsAt) + which * kChunk + sub * kToks;
     };
     auto largest = [&]() {
       uint32_t most = 0;
@@ -602,9 +600,9 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
     // x such that 64 max|v| + |s| < 2^x, given |s| < 2^s; and the power of two that brings that to 2^15
     auto bound_of = [&](float v, int s) { return max((int)(__float_as_uint(v) >> 23) - 127 + 7, s) + 1; };
     auto power_of = [&](int bound) { return min(max(15 - bound, -120), 120); };
-    fetch(0);
     int power = 0;
-    float vmax = p.factors[(slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1], down = 1.f;
+    const float* vmaxes = p.factors + (slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1;  // a chunk's largest value
+    float vmax = *vmaxes;
     {
       uint32_t most = largest();
       if (lane == 0) s_most[1][warp] = most;
@@ -615,29 +613,6 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
 #pragma unroll
       for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(S[e], up);
     }
-    // the outputs of chunk c, which were taken at 1 / down; the barrier tells that they and the chunk's factors are read
-    auto outputs = [&](int c) {
-      float2 q[kToks / 2], x[kToks / 2];
-      gate.wait(&x_done, c & 1);
-      tc_fence_after();
-      read_columns(mine + kDq + sub * kToks, q);
-      read_columns(mine + kDx + sub * kToks, x);
-      const float* f = factors(c, 3);
-#pragma unroll
-      for (int e = 0; e < kToks / 2; e += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(f + 2 * e);
-        x[e] = mul2(fma2(q[e], make_float2(w.x, w.y), x[e]), both(down));
-        x[e + 1] = mul2(fma2(q[e + 1], make_float2(w.z, w.w), x[e + 1]), both(down));
-      }
-      tc_fence_before();
-      mbar_arrive(&o_read);
-      const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
-      char* out = a.out.at(req.first + t0, h) + dim * sizeof(T);
-#pragma unroll
-      for (int e = 0; e < kToks; ++e)
-        if (t0 + e < req.count)
-          *reinterpret_cast<T*>(out + e * a.out.token_stride) = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
-    };
     for (int c = 0; c < chunks; ++c) {
       put_parts(mine + kS + sub * (kRows / 2), mine + kS + kD / 2 + sub * (kRows / 2), S);
       tc_fence_before();
@@ -647,34 +622,29 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
         __syncwarp();
       }
       mbar_arrive(&s_ready);
-      if (c) outputs(c - 1);
-      else mbar_arrive(&o_read);
-      down = power_of_two(-power);
-      gate.wait(&full[c % kStages], c / kStages & 1);  // the factors
+      gate.wait(&full[c % kStages], c / kStages & 1);  // factors and values
       const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vnow = vmax;
+      if (c + 1 < chunks) vmaxes += a.v_heads * kRowFactors, vmax = *vmaxes;
       float2 d[kToks / 2];
       gate.wait(&k_done, c & 1);
       tc_fence_after();
       read_columns(mine + kDk + sub * kToks, d);
       {
         const float *f0 = factors(c, 0), *f1 = factors(c, 1);
+        const T* value = reinterpret_cast<const T*>(smem + c % kStages * kStage + kValuesAt) + sub * kToks * kD + dim;
+        const int count = req.count - c * kChunk - sub * kToks;
         const float2 up = both(power_of_two(power));
+        auto v = [&](int t) { return t < count ? kv::to_float(value[t * kD]) : 0.f; };
 #pragma unroll
         for (int e = 0; e < kToks / 2; e += 2) {
           const float4 x = *reinterpret_cast<const float4*>(f0 + 2 * e), y = *reinterpret_cast<const float4*>(f1 + 2 * e);
-          const float2 v0 = mul2(make_float2(kv::to_float(value[2 * e]), kv::to_float(value[2 * e + 1])), up);
-          const float2 v1 = mul2(make_float2(kv::to_float(value[2 * e + 2]), kv::to_float(value[2 * e + 3])), up);
-          d[e] = fma2(d[e], make_float2(-x.x, -x.y), mul2(v0, make_float2(y.x, y.y)));
-          d[e + 1] = fma2(d[e + 1], make_float2(-x.z, -x.w), mul2(v1, make_float2(y.z, y.w)));
+          d[e] = fma2(d[e], make_float2(-x.x, -x.y), mul2(mul2(make_float2(v(2 * e), v(2 * e + 1)), up), make_float2(y.x, y.y)));
+          d[e + 1] = fma2(d[e + 1], make_float2(-x.z, -x.w), mul2(mul2(make_float2(v(2 * e + 2), v(2 * e + 3)), up), make_float2(y.z, y.w)));
         }
       }
       put_parts(mine + kR + sub * (kToks / 2), mine + kR + kChunk / 2 + sub * (kToks / 2), d);
       tc_fence_before();
       mbar_arrive(&r_ready);
-      if (c + 1 < chunks) {
-        fetch(c + 1);
-        vmax = p.factors[((slot0 + c + 1) * a.v_heads + h) * kRowFactors + 4 * kChunk + 1];
-      }
       // The power of two of the next chunk: no column of S grows past 12 max|S| + 64 max|v| in this one.  It stays where the
       // bound stays within fp16 and not too far below.
       gate.wait(&s_ready, c & 1);  // passed by then: what the others wrote is seen
@@ -696,6 +666,28 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
       mbar_arrive(&u_ready);
       const int want = power_of(bound_of(vmax, grown));
       const int move = c + 1 < chunks && (want < power || want > power + 3) ? min(max(want - power, -120), 120) : 0;
+      {  // outputs
+        gate.wait(&x_done, c & 1);
+        tc_fence_after();
+        const float2 down = both(power_of_two(-power));
+        float2 x[kToks / 2];
+        read_columns(mine + kDq + sub * kToks, d);
+        read_columns(mine + kDx + sub * kToks, x);
+        const float* f3 = factors(c, 3);
+#pragma unroll
+        for (int e = 0; e < kToks / 2; e += 2) {
+          const float4 w = *reinterpret_cast<const float4*>(f3 + 2 * e);
+          x[e] = mul2(fma2(d[e], make_float2(w.x, w.y), x[e]), down);
+          x[e + 1] = mul2(fma2(d[e + 1], make_float2(w.z, w.w), x[e + 1]), down);
+        }
+        mbar_arrive(&free[c % kStages]);  // factors and values are read
+        const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
+        char* out = a.out.at(req.first + t0, h) + dim * sizeof(T);
+#pragma unroll
+        for (int e = 0; e < kToks; ++e)
+          if (t0 + e < req.count)
+            *reinterpret_cast<T*>(out + e * a.out.token_stride) = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
+      }
       gate.wait(&s_done, c & 1);
       tc_fence_after();
       float2 g[kRows / 2];
@@ -710,7 +702,6 @@ __global__ void __launch_bounds__(kWorkers + 32, 1) gdn_prompt_kernel(const Prom
         power += move;
       }
     }
-    outputs(chunks - 1);
     const float back = power_of_two(-power);
 #pragma unroll
     for (int e = 0; e < kRows / 2; ++e) state[2 * e * kD] = S[e].x * back, state[(2 * e + 1) * kD] = S[e].y * back;
@@ -743,7 +734,7 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
     return e;
   const int64_t grid = a.s.requests * a.v_heads;
-  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 32), kWalkSmem, st, p);
+  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 64), kWalkSmem, st, p);
 }
 
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
