@@ -405,16 +405,17 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
 // for 64 columns: 80 cycles each where the tensor core needs 32, and half a head took 6900 cycles a chunk.
 //
 // Sixteen warps compute: a warp has 32 value dimensions (lanes) and a quarter of the columns (32 of S's rows, 16 tokens).  One
-// warp more issues products, another copies tiles and the values' rows.  What the next step waits for goes first: S^T K, T's
+// warp more issues products, one copies tiles, one fetches values' rows, one writes outputs' rows (as bulk copies of 256 bytes
+// these two took 60 cycles a row, 7700 a chunk).  What the next step waits for goes first: S^T K, T's
 // part of D2; the queries' parts run while R and U are made, and the outputs are written while D3 runs.
 
 constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;
 constexpr int kRows = kD / 4, kToks = kChunk / 4;  // a thread's key dimensions of S, and its tokens
-constexpr int kStages = 2;
 constexpr int kFactorBytes = kRowFactors * 4;
-constexpr int kValuesAt = 2 * kTile, kFactorsAt = kValuesAt + kChunk * kD * 2;
-constexpr int kStage = kFactorsAt + 2048;          // [K; Q], [T; X], values, factors
-constexpr int kWalkSmem = kStages * kStage + 1024;  // and room to align
+constexpr int kStages = 2, kStage = 2 * kTile;                           // [K; Q], [T; X]
+constexpr int kSlots = 3, kSlot = kChunk * kD * 2 + 2048;                // values and then outputs, factors
+constexpr int kSlotsAt = kStages * kStage, kFactorsAt = kChunk * kD * 2;
+constexpr int kWalkSmem = kSlotsAt + kSlots * kSlot + 1024;              // and room to align
 // tensor memory: S^T K and then U; S^T Q; the rest of O; R's parts; D3; S's parts, U's over the first of them
 constexpr int kDk = 0, kDq = 64, kDx = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
 
@@ -442,6 +443,11 @@ __device__ __forceinline__ uint64_t across_desc(const void* at, uint32_t wide) {
   return start | ((uint64_t)(wide >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 constexpr uint32_t kAcross = 1u << 16;  // of an instruction whose right operand lies so
+
+// 16 bytes to shared memory, or as many zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -480,9 +486,9 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[N]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], free[kStages], s_ready, r_ready, u_ready, k_done, u_done, s_done, x_done;
+  __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready, r_ready, u_ready, k_done, u_done, s_done, x_done;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -499,7 +505,8 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
   const int64_t slot0 = chunk_base(req.first, r);
   const int hk = h / (a.v_heads / a.k_heads);
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&free[i], kWorkers + 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&tiles_free[i], 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&slot_full[i], 32), mbar_init(&slot_out[i], kWorkers), mbar_init(&slot_free[i], 32);
     for (uint64_t* b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, kWorkers);
     for (uint64_t* b : {&k_done, &u_done, &s_done, &x_done}) mbar_init(b, 1);
     s_abort = 0;
@@ -515,22 +522,43 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
   const uint32_t tmem = s_tmem;
   const Gate gate{&s_abort};
 
-  if (warp == kWorkWarps + 1) {  // copies
-    const uint64_t policy = l2_policy_evict_first();
-    for (int c = 0; c < chunks; ++c) {
-      if (c >= kStages) gate.wait(&free[c % kStages], c / kStages - 1 & 1);
-      uint8_t* at = smem + c % kStages * kStage;
-      uint64_t* bar = &full[c % kStages];
-      const int count = min(kChunk, req.count - c * kChunk);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, 2 * kTile + kFactorBytes + count * kD * (int)sizeof(T));
+  if (warp == kWorkWarps + 1) {  // tiles
+    if (elect_one()) {
+      const uint64_t policy = l2_policy_evict_first();
+      for (int c = 0; c < chunks; ++c) {
+        uint8_t* at = smem + c % kStages * kStage;
+        uint64_t* bar = &full[c % kStages];
+        if (c >= kStages) gate.wait(&tiles_free[c % kStages], c / kStages - 1 & 1);
+        mbar_arrive_expect_tx(bar, 2 * kTile);
         bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kTile, kTile, bar, policy);
         bulk_g2s(at + kTile, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
-        bulk_g2s(at + kFactorsAt, p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors, kFactorBytes, bar, policy);
       }
-      __syncwarp();
-      for (int t = lane; t < count; t += 32)
-        bulk_g2s(at + kValuesAt + t * kD * sizeof(T), a.v.at(req.first + (int64_t)c * kChunk + t, h), kD * sizeof(T), bar, policy);
+    }
+    __syncwarp();
+  } else if (warp == kWorkWarps + 2) {  // values, none past the last token, and factors
+    for (int c = 0; c < chunks; ++c) {
+      if (c >= kSlots) gate.wait(&slot_free[c % kSlots], c / kSlots - 1 & 1);
+      const uint32_t at = smem_u32(smem + kSlotsAt + c % kSlots * kSlot);
+      const int count = req.count - c * kChunk;
+      const char* from = a.v.at(req.first + (int64_t)c * kChunk, h) + lane % 16 * 16;
+#pragma unroll 8
+      for (int t = lane / 16; t < kChunk; t += 2)
+        copy16(at + t * (kD * (int)sizeof(T)) + lane % 16 * 16, t < count ? from + t * a.v.token_stride : from, t < count ? 16 : 0);
+      const float* f = p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors;
+      for (int t = lane; t < kFactorBytes / 16; t += 32) copy16(at + kFactorsAt + t * 16, f + t * 4, 16);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&slot_full[c % kSlots])) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kWorkWarps + 3) {  // outputs, which lie where the values were
+    for (int c = 0; c < chunks; ++c) {
+      gate.wait(&slot_out[c % kSlots], c / kSlots & 1);
+      const uint8_t* from = smem + kSlotsAt + c % kSlots * kSlot + lane % 16 * 16;
+      const int count = min(kChunk, req.count - c * kChunk);
+      char* to = a.out.at(req.first + (int64_t)c * kChunk, h) + lane % 16 * 16;
+#pragma unroll 8
+      for (int t = lane / 16; t < count; t += 2)
+        *reinterpret_cast<uint4*>(to + t * a.out.token_stride) = *reinterpret_cast<const uint4*>(from + t * (kD * (int)sizeof(T)));
+      mbar_arrive(&slot_free[c % kSlots]);
     }
   } else if (warp == kWorkWarps) {  // products
     if (elect_one()) {
@@ -575,7 +603,7 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
           for (int k = 0; k < kChunk / 16; ++k)
             tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
         tc_commit(&s_done);
-        tc_commit(&free[c % kStages]);
+        tc_commit(&tiles_free[c % kStages]);
       }
       gate.wait(&s_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
     }
@@ -589,7 +617,10 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
     for (int e = 0; e < kRows / 2; ++e)
       S[e] = req.fresh ? make_float2(0.f, 0.f) : make_float2(state[2 * e * kD], state[(2 * e + 1) * kD]);
     auto factors = [&](int c, int which) {  // of this warp's tokens
-      return reinterpret_cast<const float*>(smem + c % kStages * kStage + kFactorsAt) + which * kChunk + sub * kToks;
+      return reinterpret_cast<const float*>(smem + kSlotsAt + c % kSlots * kSlot + kFactorsAt) + which * kChunk + sub * kToks;
+    };
+    auto values = [&](int c) {  // of this thread's tokens, and then their outputs
+      return reinterpret_cast<T*>(smem + kSlotsAt + c % kSlots * kSlot) + sub * kToks * kD + dim;
     };
     auto largest = [&]() {
       uint32_t most = 0;
@@ -622,7 +653,7 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
         __syncwarp();
       }
       mbar_arrive(&s_ready);
-      gate.wait(&full[c % kStages], c / kStages & 1);  // factors and values
+      gate.wait(&slot_full[c % kSlots], c / kSlots & 1);  // factors and values
       const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vnow = vmax;
       if (c + 1 < chunks) vmaxes += a.v_heads * kRowFactors, vmax = *vmaxes;
       float2 d[kToks / 2];
@@ -631,10 +662,9 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
       read_columns(mine + kDk + sub * kToks, d);
       {
         const float *f0 = factors(c, 0), *f1 = factors(c, 1);
-        const T* value = reinterpret_cast<const T*>(smem + c % kStages * kStage + kValuesAt) + sub * kToks * kD + dim;
-        const int count = req.count - c * kChunk - sub * kToks;
+        const T* value = values(c);
         const float2 up = both(power_of_two(power));
-        auto v = [&](int t) { return t < count ? kv::to_float(value[t * kD]) : 0.f; };
+        auto v = [&](int t) { return kv::to_float(value[t * kD]); };
 #pragma unroll
         for (int e = 0; e < kToks / 2; e += 2) {
           const float4 x = *reinterpret_cast<const float4*>(f0 + 2 * e), y = *reinterpret_cast<const float4*>(f1 + 2 * e);
@@ -680,13 +710,10 @@ __global__ void __launch_bounds__(kWorkers + 64, 1) gdn_prompt_kernel(const Prom
           x[e] = mul2(fma2(d[e], make_float2(w.x, w.y), x[e]), down);
           x[e + 1] = mul2(fma2(d[e + 1], make_float2(w.z, w.w), x[e + 1]), down);
         }
-        mbar_arrive(&free[c % kStages]);  // factors and values are read
-        const int64_t t0 = (int64_t)c * kChunk + sub * kToks;
-        char* out = a.out.at(req.first + t0, h) + dim * sizeof(T);
+        T* out = values(c);
 #pragma unroll
-        for (int e = 0; e < kToks; ++e)
-          if (t0 + e < req.count)
-            *reinterpret_cast<T*>(out + e * a.out.token_stride) = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
+        for (int e = 0; e < kToks; ++e) out[e * kD] = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
+        mbar_arrive(&slot_out[c % kSlots]);  // factors and values are read, outputs written
       }
       gate.wait(&s_done, c & 1);
       tc_fence_after();
@@ -734,7 +761,7 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
     return e;
   const int64_t grid = a.s.requests * a.v_heads;
-  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 64), kWalkSmem, st, p);
+  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 128), kWalkSmem, st, p);
 }
 
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
