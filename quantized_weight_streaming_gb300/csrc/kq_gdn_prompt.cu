@@ -54,6 +54,7 @@ struct PromptArgs {
   RuleArgs r;
   uint8_t* kq;      // [slot][key head] tiles
   uint8_t* tx;      // [slot][value head] tiles
+  float* norms;     // [slot][key head]: of 64 keys and of 64 queries, what their rows are multiplied by to have unit length
   float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64, the largest value
 };
 
@@ -103,59 +104,60 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-constexpr int kStride = kChunk + 4;                  // of -L's rows, in floats
-constexpr int kSide = 80;                            // bytes between rows of the 32 x 32 product in between
-constexpr int kLAt = kTile, kSideAt = kLAt + kChunk * kStride * 4, kChunkSmem = kSideAt + 2 * 32 * kSide;
-
-// One chunk and value head: the tile of its keys and queries, T and X, the rows' factors.
-//
-// T is solved by blocks of 32: the two on the diagonal column by column, a thread each, then the one below by two products
-// with the tensor cores, T21 = T22 (-L21) T11.  X = P T follows from the products' own layout: what a warp's mma leaves of
-// its queries' rows is, times the decays, the operand of the next.  (Solving all of T and X in threads' registers took twice
-// the instructions: 382 us for 129 chunks of 48 heads.)
-template <typename T>
-__global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
-  extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(16) float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
-  __shared__ double s_first;
-  __shared__ uint32_t s_vmax[4];
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const RuleArgs& a = p.r;
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.x % a.v_heads;
-  const int64_t slot = blockIdx.x / a.v_heads;
-  // the last request whose chunks begin at or before this slot
+// The last request whose chunks begin at or before this slot, and the chunk that lies there.
+struct Place {
+  Request req;
+  int64_t first;  // token
+  int n;          // tokens, 0 where the slot is empty
+};
+__device__ __forceinline__ Place place_of(const RuleArgs& a, int64_t slot) {
+  const int lane = threadIdx.x % 32;
+  Place p{};
   int64_t r = 0, span = a.s.requests;
-  while (span > 0) {
+  while (true) {
     const int64_t step = (span + 31) / 32, at = r + lane * step;
     const unsigned some = __ballot_sync(~0u, lane * step < span && chunk_base(max(a.s.q_start[at], 0), at) <= slot);
-    if (!some) return;
+    if (!some) return p;
     const int last = 31 - __clz(some);
     r += last * step;
     if (step == 1) break;
     span = min(step, span - last * step);
   }
-  const Request req = read_request(a.s, r, a.max_new);
-  if (req.status && tid == 0) prompt_flag(req.status);
-  if (!req.count || req.count <= a.short_most) return;
-  const int64_t c = slot - chunk_base(req.first, r);
-  if (c < 0 || c * kChunk >= req.count) return;
-  const int group = a.v_heads / a.k_heads, hk = h / group, n = (int)min((int64_t)kChunk, req.count - c * kChunk);
-  const int64_t first = req.first + c * kChunk;
-  uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kTile;
+  p.req = read_request(a.s, r, a.max_new);
+  if (p.req.status && threadIdx.x == 0) prompt_flag(p.req.status);
+  if (!p.req.count || p.req.count <= a.short_most) return p;
+  const int64_t c = slot - chunk_base(p.req.first, r);
+  if (c < 0 || c * kChunk >= p.req.count) return p;
+  p.first = p.req.first + c * kChunk, p.n = (int)min((int64_t)kChunk, p.req.count - c * kChunk);
+  return p;
+}
 
-  // keys and queries: a power of two per row that brings its largest to [1, 2), then fp16; the rows' norms
-#pragma unroll 4
-  for (int e = tid; e < 2 * kChunk * 16; e += 128) {
-    const int row = e / 16, vec = e % 16, i = row % kChunk;
-    kv::Raw<T, 8> raw;
-    raw.clear();
-    if (i < n) raw.load(reinterpret_cast<const T*>((row < kChunk ? a.k : a.q).at(first + i, hk)) + 8 * vec);
-    float v[8];
-    raw.get(v);
+// One chunk and key head: the tile of its keys and queries, each row brought to [1, 2) by a power of two and then fp16 (the
+// rows' values stay what they are), and the rows' norms.
+template <typename T>
+__global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const RuleArgs& a = p.r;
+  const int hk = blockIdx.x % a.k_heads;
+  const int64_t slot = blockIdx.x / a.k_heads;
+  const Place at = place_of(a, slot);
+  if (!at.n) return;
+  uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kTile;
+  float* norms = p.norms + (slot * a.k_heads + hk) * 2 * kChunk;
+  kv::Raw<T, 8> raw[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int e = threadIdx.x + x * 256, row = e / 16, i = row % kChunk;
+    raw[x].clear();
+    if (i < at.n) raw[x].load(reinterpret_cast<const T*>((row < kChunk ? a.k : a.q).at(at.first + i, hk)) + 8 * (e % 16));
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int e = threadIdx.x + x * 256, row = e / 16, vec = e % 16, i = row % kChunk;
     uint32_t most2 = 0;  // of 16-bit patterns without their signs, which order as the numbers do
 #pragma unroll
-    for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw.u[x] & 0x7FFF7FFFu);
+    for (int y = 0; y < 4; ++y) most2 = __vmaxu2(most2, raw[x].u[y] & 0x7FFF7FFFu);
 #pragma unroll
     for (int o = 8; o; o >>= 1) most2 = __vmaxu2(most2, __shfl_xor_sync(~0u, most2, o));
     union { uint16_t b; T t; } top;
@@ -163,29 +165,70 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
     const float most = kv::to_float(top.t);
     const int power = (int)(__float_as_uint(most) >> 23);
     const float f = power == 255 || most == 0.f ? 1.f : __uint_as_float((uint32_t)max(254 - power, 1) << 23);
-    float sum = 0.f;
+    float v[8], sum = 0.f;
+    raw[x].get(v);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] *= f, sum = fmaf(v[x], v[x], sum);
+    for (int y = 0; y < 8; ++y) v[y] *= f, sum = fmaf(v[y], v[y], sum);
 #pragma unroll
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     uint4 u;
     u.x = h2_bits(__floats2half2_rn(v[0], v[1])), u.y = h2_bits(__floats2half2_rn(v[2], v[3]));
     u.z = h2_bits(__floats2half2_rn(v[4], v[5])), u.w = h2_bits(__floats2half2_rn(v[6], v[7]));
-    const uint32_t at = vec / 8 * 16384 + swizzled(row, vec % 8);
-    *reinterpret_cast<uint4*>(smem + at) = u;
-    if (h % group == 0) *reinterpret_cast<uint4*>(kq + at) = u;
-    if (vec == 0) (row < kChunk ? s_fk : s_fq)[i] = i < n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
+    *reinterpret_cast<uint4*>(kq + vec / 8 * 16384 + swizzled(row, vec % 8)) = u;
+    if (vec == 0) norms[row] = i < at.n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
   }
+}
+
+// -L in fp32 over the tile's rows 64.., which the queries leave and X takes: rows of 256 bytes, 32 in each half of the tile,
+// in words of 16 bytes that lie apart for eight successive rows.
+__device__ __forceinline__ uint32_t lower_at(int i, int j) {
+  return i / 32 * 16384 + 8192 + i % 32 * 256 + (((j / 4) ^ ((i & 7) << 1)) << 4) + j % 4 * 4;
+}
+constexpr int kSide = 80;                                       // bytes between rows of the 32 x 32 product in between
+constexpr int kSideAt = kTile, kChunkSmem = kSideAt + 2 * 32 * kSide;
+
+// One chunk and value head: T and X, the rows' factors.
+//
+// T is solved by blocks of 32: the two on the diagonal column by column, a thread each, then the one below by two products
+// with the tensor cores, T21 = T22 (-L21) T11.  X = P T follows from the products' own layout: what a warp's mma leaves of
+// its queries' rows is, times the decays, the operand of the next.  (Solving all of T and X in threads' registers took twice
+// the instructions: 382 us for 129 chunks of 48 heads.)
+template <typename T>
+__global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(16) float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
+  __shared__ __align__(8) uint64_t s_full;
+  __shared__ double s_first;
+  __shared__ uint32_t s_vmax[4];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const RuleArgs& a = p.r;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.x % a.v_heads;
+  const int64_t slot = blockIdx.x / a.v_heads;
+  const Place place = place_of(a, slot);
+  if (!place.n) return;
+  const int n = place.n, hk = h / (a.v_heads / a.k_heads);
+  const int64_t first = place.first;
+  if (tid == 0) {
+    mbar_init(&s_full, 1);
+    fence_barrier_init();
+    mbar_arrive_expect_tx(&s_full, kTile);
+    bulk_g2s(smem, p.kq + (slot * a.k_heads + hk) * kTile, kTile, &s_full, l2_policy_evict_first());
+  }
+  if (tid < 2 * kChunk) (tid < kChunk ? s_fk : s_fq)[tid % kChunk] = p.norms[(slot * a.k_heads + hk) * 2 * kChunk + tid];
   {  // the largest value
+    kv::Raw<T, 8> raw[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = tid / 16 + e * 8;
+      raw[e].clear();
+      if (t < n) raw[e].load(reinterpret_cast<const T*>(a.v.at(first + t, h)) + 8 * (tid % 16));
+    }
     uint32_t most2 = 0;
 #pragma unroll
-    for (int e = tid; e < kChunk * 16; e += 128) {
-      kv::Raw<T, 8> raw;
-      raw.clear();
-      if (e / 16 < n) raw.load(reinterpret_cast<const T*>(a.v.at(first + e / 16, h)) + 8 * (e % 16));
+    for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw.u[x] & 0x7FFF7FFFu);
-    }
+      for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw[e].u[x] & 0x7FFF7FFFu);
     const uint32_t top = __reduce_max_sync(~0u, max(most2 >> 16, most2 & 0xFFFFu));
     if (lane == 0) s_vmax[warp] = top;
   }
@@ -217,45 +260,67 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
     s_beta[tid] = beta;
   }
 
-  // products of 16 rows of keys and 16 of queries a warp with the keys that they look back on
+  __syncthreads();
+  if (!mbar_wait_bounded(&s_full, 0)) prompt_flag(KQ_ERR_TIMEOUT);
+
+  // products of 16 rows a warp, of queries and then of keys, with the keys that they look back on
   const uint32_t base = smem_u32(smem);
-  float acc[2][8][4] = {};
+  auto products = [&](float (&acc)[8][4], int rows) {
 #pragma unroll
-  for (int k = 0; k < kD / 16; ++k) {
-    const uint32_t half = base + k / 4 * 16384;
-    uint32_t fa[2][4];
+    for (int b = 0; b < 8; ++b)
 #pragma unroll
-    for (int m = 0; m < 2; ++m) ldmatrix4(fa[m], half + swizzled(m * kChunk + warp * 16 + lane % 16, k % 4 * 2 + lane / 16));
+      for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
-      if (b > warp) continue;
-      uint32_t fb[4];
-      ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
+    for (int k = 0; k < kD / 16; ++k) {
+      const uint32_t half = base + k / 4 * 16384;
+      uint32_t fa[4];
+      ldmatrix4(fa, half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16));
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        mma_f16(acc[m][2 * b], fa[m], fb[0], fb[1]);
-        mma_f16(acc[m][2 * b + 1], fa[m], fb[2], fb[3]);
+      for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
+        if (b > warp) continue;
+        uint32_t fb[4];
+        ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
+        mma_f16(acc[2 * b], fa, fb[0], fb[1]);
+        mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
       }
     }
-  }
-  __syncthreads();  // the tile is read: T and X go over it
-  float* nl = reinterpret_cast<float*>(smem + kLAt);  // -L
-  uint32_t ph[4][4], pl[4][4];                        // P as operands of 16 x 16
+  };
+  // of row i and the two columns from j on: the decays between, times the keys' norms
+  auto decays = [&](int i, int j) {
+    const float hi = s_hi[i], lo = s_lo[i];
+    const float2 hj = *reinterpret_cast<const float2*>(s_hi + j), lj = *reinterpret_cast<const float2*>(s_lo + j);
+    const float2 fj = *reinterpret_cast<const float2*>(s_fk + j);
+    return make_float2(fj.x * exp2_fast((hi - hj.x) + (lo - lj.x)), fj.y * exp2_fast((hi - hj.y) + (lo - lj.y)));
+  };
+  float acc[8][4];
+  uint32_t ph[4][4], pl[4][4];  // P as operands of 16 x 16
+  products(acc, kChunk);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = warp * 16 + lane / 4 + e * 8;
-    const float hi = s_hi[i], lo = s_lo[i], fl = -s_beta[i] * s_fk[i], fp = a.scale * s_fq[i];
+    const float f = a.scale * s_fq[i];
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       if (b / 2 > warp) continue;
       const int j = b * 8 + lane % 4 * 2;
-      const float2 hj = *reinterpret_cast<const float2*>(s_hi + j), lj = *reinterpret_cast<const float2*>(s_lo + j);
-      const float2 fj = *reinterpret_cast<const float2*>(s_fk + j);
-      const float r0 = fj.x * exp2_fast((hi - hj.x) + (lo - lj.x)), r1 = fj.y * exp2_fast((hi - hj.y) + (lo - lj.y));
-      *reinterpret_cast<float2*>(nl + i * kStride + j) =
-          make_float2(j < i ? acc[0][b][2 * e] * r0 * fl : 0.f, j + 1 < i ? acc[0][b][2 * e + 1] * r1 * fl : 0.f);
-      split2(j <= i ? acc[1][b][2 * e] * r0 * fp : 0.f, j + 1 <= i ? acc[1][b][2 * e + 1] * r1 * fp : 0.f,
-             ph[b / 2][b % 2 * 2 + e], pl[b / 2][b % 2 * 2 + e]);
+      const float2 r = decays(i, j);
+      split2(j <= i ? acc[b][2 * e] * r.x * f : 0.f, j + 1 <= i ? acc[b][2 * e + 1] * r.y * f : 0.f, ph[b / 2][b % 2 * 2 + e],
+             pl[b / 2][b % 2 * 2 + e]);
+    }
+  }
+  products(acc, 0);
+  __syncthreads();  // the tile is read: -L goes over its queries, T over its keys
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = warp * 16 + lane / 4 + e * 8;
+    const float f = -s_beta[i] * s_fk[i];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (b / 2 > warp) continue;
+      const int j = b * 8 + lane % 4 * 2;
+      const float2 r = decays(i, j);
+      *reinterpret_cast<float2*>(smem + lower_at(i, j)) =
+          make_float2(j < i ? acc[b][2 * e] * r.x * f : 0.f, j + 1 < i ? acc[b][2 * e + 1] * r.y * f : 0.f);
     }
   }
   __syncthreads();
@@ -263,7 +328,7 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
   uint8_t* lowpart = smem + kTile / 2;
   if (warp < 2) {  // column j of a diagonal block, from the first row down: t_i = [i = j] - sum_m L_im t_m
     const int j = lane, at0 = 32 * warp;
-    const float* l0 = nl + at0 * kStride + at0;
+    const uint32_t turn = warp * 128;  // column 32 + m of row 32 + i lies where column m of row i does, but for this bit
     float2 t[16];
 #pragma unroll
     for (int m = 0; m < 16; ++m) t[m] = make_float2(0.f, 0.f);
@@ -272,7 +337,7 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
       float2 s0 = make_float2(i == j ? 1.f : 0.f, 0.f), s1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < i; m += 4) {  // what lies at and past i is zero
-        const float4 l = *reinterpret_cast<const float4*>(l0 + i * kStride + m);
+        const float4 l = *reinterpret_cast<const float4*>(smem + ((lower_at(i, m) ^ turn) + warp * 16384));
         s0 = fma2(make_float2(l.x, l.y), t[m / 2], s0);
         s1 = fma2(make_float2(l.z, l.w), t[m / 2 + 1], s1);
       }
@@ -299,7 +364,7 @@ __global__ void __launch_bounds__(128, 4) gdn_chunk_kernel(const PromptArgs p) {
       uint32_t ah[4], al[4], bh[4], bl[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 l = *reinterpret_cast<const float2*>(nl + (m0 + lane / 4 + e % 2 * 8) * kStride + k * 16 + lane % 4 * 2 + e / 2 * 8);
+        const float2 l = *reinterpret_cast<const float2*>(smem + lower_at(m0 + lane / 4 + e % 2 * 8, k * 16 + lane % 4 * 2 + e / 2 * 8));
         split2(l.x, l.y, ah[e], al[e]);
       }
       const uint32_t at = swizzled(k * 16 + lane % 16, n0 / 8 + lane / 16);
@@ -745,7 +810,8 @@ static int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens) {
   const int64_t slots = prompt_slots(requests, tokens);
-  return slots * (k_heads + v_heads) * (int64_t)kTile + align256(slots * v_heads * kRowFactors * 4);
+  return slots * (k_heads + v_heads) * (int64_t)kTile + align256(slots * k_heads * 2 * kChunk * 4) +
+         align256(slots * v_heads * kRowFactors * 4);
 }
 
 template <typename T>
@@ -755,9 +821,11 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   p.r = a;
   p.kq = static_cast<uint8_t*>(ws);
   p.tx = p.kq + slots * a.k_heads * kTile;
-  p.factors = reinterpret_cast<float*>(p.tx + slots * a.v_heads * kTile);
+  p.norms = reinterpret_cast<float*>(p.tx + slots * a.v_heads * kTile);
+  p.factors = p.norms + align256(slots * a.k_heads * 2 * kChunk * 4) / 4;
   if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem)) return e;
   if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalkSmem)) return e;
+  if (cudaError_t e = launch_dependent(gdn_rows_kernel<T>, dim3((unsigned)(slots * a.k_heads)), dim3(256), 0, st, p)) return e;
   if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
     return e;
   const int64_t grid = a.s.requests * a.v_heads;
