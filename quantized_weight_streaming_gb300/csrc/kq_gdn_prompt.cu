@@ -466,13 +466,15 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
 //
 //   D1 = S^T [K; Q]^T    D2 = R^T [T; X]^T    D3 = (w U)^T K
 //
+// A warp has 32 value dimensions (lanes) and a quarter of the columns (32 of S's rows, 16 tokens), and what a quarter made is
+// one or two steps of K of the next product: products begin with the first quarter, and T's being triangular lets a quarter
+// have its U when the quarters up to it have their R.  The queries' part of D1 and X's of D2 fill the gaps.
+//
 // With S, R and U as right operands in shared memory (64 value dimensions a CTA) each product read its left one, 4 KB, anew
 // for 64 columns: 80 cycles each where the tensor core needs 32, and half a head took 6900 cycles a chunk.
 //
-// Sixteen warps compute: a warp has 32 value dimensions (lanes) and a quarter of the columns (32 of S's rows, 16 tokens).  One
-// warp more issues products, one copies tiles, one fetches values' rows, one writes outputs' rows (as bulk copies of 256 bytes
-// these two took 60 cycles a row, 7700 a chunk).  What the next step waits for goes first: S^T K, T's
-// part of D2; the queries' parts run while R and U are made, and the outputs are written while D3 runs.
+// Sixteen warps compute, one issues products, one copies tiles, one fetches values' rows, one writes outputs' rows (as bulk
+// copies of 256 bytes these two took 60 cycles a row, 7700 a chunk).
 
 constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;
 constexpr int kRows = kD / 4, kToks = kChunk / 4;  // a thread's key dimensions of S, and its tokens
@@ -481,8 +483,8 @@ constexpr int kStages = 2, kStage = 2 * kTile;                           // [K; 
 constexpr int kSlots = 3, kSlot = kChunk * kD * 2 + 2048;                // values and then outputs, factors
 constexpr int kSlotsAt = kStages * kStage, kFactorsAt = kChunk * kD * 2;
 constexpr int kWalkSmem = kSlotsAt + kSlots * kSlot + 1024;              // and room to align
-// tensor memory: S^T K and then U; S^T Q; the rest of O; R's parts; D3; S's parts, U's over the first of them
-constexpr int kDk = 0, kDq = 64, kDx = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
+// tensor memory: S^T K; S^T Q; U and then X's part of O; R's parts; D3; S's parts, U's over the first of them
+constexpr int kDk = 0, kDq = 64, kDu = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
 
 // Barriers that are waited on with a limit; after one ran out all waits return at once, and the warps run through.
 struct Gate {
@@ -553,7 +555,8 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[N]) {
 template <typename T>
 __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const PromptArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready, r_ready, u_ready, k_done, u_done, s_done, x_done;
+  __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready[4], r_ready[4], u_ready[4],
+      u_done[4], o_read, k_done, s_done, x_done;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -572,8 +575,10 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&tiles_free[i], 1);
     for (int i = 0; i < kSlots; ++i) mbar_init(&slot_full[i], 32), mbar_init(&slot_out[i], kWorkers), mbar_init(&slot_free[i], 32);
-    for (uint64_t* b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, kWorkers);
-    for (uint64_t* b : {&k_done, &u_done, &s_done, &x_done}) mbar_init(b, 1);
+    for (int i = 0; i < 4; ++i)
+      mbar_init(&s_ready[i], kWorkers / 4), mbar_init(&r_ready[i], kWorkers / 4), mbar_init(&u_ready[i], kWorkers / 4), mbar_init(&u_done[i], 1);
+    mbar_init(&o_read, kWorkers);
+    for (uint64_t* b : {&k_done, &s_done, &x_done}) mbar_init(b, 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -632,45 +637,57 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       for (int c = 0; c < chunks; ++c) {
         const uint8_t* at = smem + c % kStages * kStage;
         const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile), kt = across_desc(at, 16384);
-        auto state = [&](uint32_t to, uint64_t rows) {
-#pragma unroll
-          for (int low = 0; low < 2; ++low)
-#pragma unroll
-            for (int k = 0; k < kD / 16; ++k)
-              tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow,
-                        low || k);
+        auto state = [&](uint32_t to, uint64_t rows, int k, int low, uint32_t add) {  // 16 of S's key dimensions
+          tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow, add);
         };
-        auto solved = [&](uint32_t to, uint64_t rows) {
+        auto solved = [&](uint32_t to, uint64_t rows, int k) {  // 16 tokens' R, and the tokens from there on
 #pragma unroll
           for (int pass = 0; pass < 3; ++pass)  // high x high, low x high, high x low
+            tc_mma_ts(tmem + to + 16 * k, tmem + kR + (pass == 1 ? kChunk / 2 : 0) + k * 8,
+                      rows + (pass == 2 ? kLowPart : 0) + (uint64_t)((k * 16 * 128 + k * 32) >> 4), idesc_f16(128, kChunk - 16 * k),
+                      pass || k);
+        };
+        auto update = [&](int k) {  // 16 tokens' U
+          gate.wait(&u_ready[k], c & 1);
+          tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kChunk / 16; ++k)
-              tc_mma_ts(tmem + to, tmem + kR + (pass == 1 ? kChunk / 2 : 0) + k * 8,
-                        rows + (pass == 2 ? kLowPart : 0) + (uint64_t)(k * 32 >> 4), narrow, pass || k);
+          for (int low = 0; low < 2; ++low)
+            tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
         };
         gate.wait(&full[c % kStages], c / kStages & 1);
-        gate.wait(&s_ready, c & 1);
-        tc_fence_after();
-        state(kDk, kd);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          gate.wait(&s_ready[j], c & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 2 * j; k < 2 * j + 2; ++k) state(kDk, kd, k, 0, k), state(kDk, kd, k, 1, 1);
+        }
         tc_commit(&k_done);
-        state(kDq, kd + kLower);
-        gate.wait(&r_ready, c & 1);
-        tc_fence_after();
-        solved(kDk, td);
-        tc_commit(&u_done);
-        solved(kDx, td + kLower);
-        tc_commit(&x_done);
-        gate.wait(&u_ready, c & 1);
-        tc_fence_after();
+        if (c) {  // the last chunk's outputs are in registers
+          gate.wait(&o_read, c - 1 & 1);
+          tc_fence_after();
+        }
 #pragma unroll
-        for (int low = 0; low < 2; ++low)
+        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 0, k);
 #pragma unroll
-          for (int k = 0; k < kChunk / 16; ++k)
-            tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
+        for (int j = 0; j < 4; ++j) {
+          gate.wait(&r_ready[j], c & 1);
+          tc_fence_after();
+          solved(kDu, td, j);
+          tc_commit(&u_done[j]);
+        }
+        update(0);
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 1, 1);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) update(j);
         tc_commit(&s_done);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j);
+        tc_commit(&x_done);
         tc_commit(&tiles_free[c % kStages]);
       }
-      gate.wait(&s_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
+      gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
     }
     __syncwarp();
   } else {
@@ -693,34 +710,58 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       for (int e = 0; e < kRows / 2; ++e) most = max(most, max(__float_as_uint(fabsf(S[e].x)), __float_as_uint(fabsf(S[e].y))));
       return __reduce_max_sync(~0u, most);
     };
-    // x such that 64 max|v| + |s| < 2^x, given |s| < 2^s; and the power of two that brings that to 2^15
-    auto bound_of = [&](float v, int s) { return max((int)(__float_as_uint(v) >> 23) - 127 + 7, s) + 1; };
-    auto power_of = [&](int bound) { return min(max(15 - bound, -120), 120); };
-    int power = 0;
-    const float* vmaxes = p.factors + (slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1;  // a chunk's largest value
-    float vmax = *vmaxes;
-    {
-      uint32_t most = largest();
-      if (lane == 0) s_most[1][warp] = most;
-      named_barrier(1, kWorkers);
-      most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[1][lane] : 0u);
-      power = power_of(bound_of(vmax, (int)(most >> 23) - 127 + 5));  // a column is 12 entries long at most
-      const float2 up = both(power_of_two(power));
+    float down = 1.f;
+    auto outputs = [&](int c) {  // of a chunk whose S was taken at 1 / down
+      float2 q[kToks / 2], x[kToks / 2];
+      gate.wait(&x_done, c & 1);
+      tc_fence_after();
+      read_columns(mine + kDq + sub * kToks, q);
+      read_columns(mine + kDu + sub * kToks, x);
+      tc_fence_before();
+      mbar_arrive(&o_read);
+      const float* f3 = factors(c, 3);
 #pragma unroll
-      for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(S[e], up);
-    }
+      for (int e = 0; e < kToks / 2; e += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(f3 + 2 * e);
+        x[e] = mul2(fma2(q[e], make_float2(w.x, w.y), x[e]), both(down));
+        x[e + 1] = mul2(fma2(q[e + 1], make_float2(w.z, w.w), x[e + 1]), both(down));
+      }
+      T* out = values(c);
+#pragma unroll
+      for (int e = 0; e < kToks; ++e) out[e * kD] = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
+      mbar_arrive(&slot_out[c % kSlots]);  // factors and values are read, outputs written
+    };
+    const float* vmaxes = p.factors + (slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1;  // a chunk's largest value
+    int power = 0;  // S is kept times 2^power, so that it, R and U stay within 2^15
+    float reach = 0.f;  // no column of S is longer (a column has 128 entries, so 12 times the largest at most)
+    auto measure = [&](int turn) {  // reach from S as it is; all warps together
+      const uint32_t most = largest();
+      if (lane == 0) s_most[turn][warp] = most;
+      named_barrier(1, kWorkers);
+      reach = 12.f * __uint_as_float(__reduce_max_sync(~0u, lane < kWorkWarps ? s_most[turn][lane] : 0u)) * power_of_two(-power);
+    };
+    auto rescale = [&](float vmax) {  // |R| and |U| of a chunk are at most 64 max|v| + the longest column
+      const int bound = (int)(__float_as_uint(fmaf(64.f, vmax, reach)) >> 23) - 126;  // 2^bound is more
+      const int want = min(max(15 - bound, -120), 120);
+      if (want >= power && want <= power + 3) return;
+      const int half = (want - power) / 2;  // in two steps, for the whole may be no number
+      const float2 by = both(power_of_two(half)), on = both(power_of_two(want - power - half));
+#pragma unroll
+      for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(mul2(S[e], by), on);
+      power = want;
+    };
+    measure(0);
+    rescale(*vmaxes);
     for (int c = 0; c < chunks; ++c) {
       put_parts(mine + kS + sub * (kRows / 2), mine + kS + kD / 2 + sub * (kRows / 2), S);
       tc_fence_before();
-      {
-        const uint32_t most = largest();
-        if (lane == 0) s_most[c & 1][warp] = most;
-        __syncwarp();
-      }
-      mbar_arrive(&s_ready);
+      mbar_arrive(&s_ready[sub]);
+      if (c) outputs(c - 1);
+      down = power_of_two(-power);
       gate.wait(&slot_full[c % kSlots], c / kSlots & 1);  // factors and values
-      const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vnow = vmax;
-      if (c + 1 < chunks) vmaxes += a.v_heads * kRowFactors, vmax = *vmaxes;
+      const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vmax = factors(c, 0)[4 * kChunk + 1 - sub * kToks];
+      if (c + 1 < chunks) vmaxes += a.v_heads * kRowFactors;
+      const float vnext = *vmaxes;
       float2 d[kToks / 2];
       gate.wait(&k_done, c & 1);
       tc_fence_after();
@@ -739,15 +780,10 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       }
       put_parts(mine + kR + sub * (kToks / 2), mine + kR + kChunk / 2 + sub * (kToks / 2), d);
       tc_fence_before();
-      mbar_arrive(&r_ready);
-      // The power of two of the next chunk: no column of S grows past 12 max|S| + 64 max|v| in this one.  It stays where the
-      // bound stays within fp16 and not too far below.
-      gate.wait(&s_ready, c & 1);  // passed by then: what the others wrote is seen
-      const uint32_t most = __reduce_max_sync(~0u, lane < kWorkWarps ? s_most[c & 1][lane] : 0u);
-      const int grown = bound_of(vnow, (int)(most >> 23) - 127 - power + 5);
-      gate.wait(&u_done, c & 1);
+      mbar_arrive(&r_ready[sub]);
+      gate.wait(&u_done[sub], c & 1);
       tc_fence_after();
-      read_columns(mine + kDk + sub * kToks, d);
+      read_columns(mine + kDu + sub * kToks, d);
       {
         const float* f2 = factors(c, 2);
 #pragma unroll
@@ -758,28 +794,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       }
       put_parts(mine + kS + sub * (kToks / 2), mine + kS + kChunk / 2 + sub * (kToks / 2), d);
       tc_fence_before();
-      mbar_arrive(&u_ready);
-      const int want = power_of(bound_of(vmax, grown));
-      const int move = c + 1 < chunks && (want < power || want > power + 3) ? min(max(want - power, -120), 120) : 0;
-      {  // outputs
-        gate.wait(&x_done, c & 1);
-        tc_fence_after();
-        const float2 down = both(power_of_two(-power));
-        float2 x[kToks / 2];
-        read_columns(mine + kDq + sub * kToks, d);
-        read_columns(mine + kDx + sub * kToks, x);
-        const float* f3 = factors(c, 3);
-#pragma unroll
-        for (int e = 0; e < kToks / 2; e += 2) {
-          const float4 w = *reinterpret_cast<const float4*>(f3 + 2 * e);
-          x[e] = mul2(fma2(d[e], make_float2(w.x, w.y), x[e]), down);
-          x[e + 1] = mul2(fma2(d[e + 1], make_float2(w.z, w.w), x[e + 1]), down);
-        }
-        T* out = values(c);
-#pragma unroll
-        for (int e = 0; e < kToks; ++e) out[e * kD] = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
-        mbar_arrive(&slot_out[c % kSlots]);  // factors and values are read, outputs written
-      }
+      mbar_arrive(&u_ready[sub]);
       gate.wait(&s_done, c & 1);
       tc_fence_after();
       float2 g[kRows / 2];
@@ -787,13 +802,12 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       tc_fence_before();
 #pragma unroll
       for (int e = 0; e < kRows / 2; ++e) S[e] = fma2(S[e], both(decay), g[e]);
-      if (move) {
-        const float2 by = both(power_of_two(move));
-#pragma unroll
-        for (int e = 0; e < kRows / 2; ++e) S[e] = mul2(S[e], by);
-        power += move;
-      }
+      // S's columns have grown by 64 max|v| at most; what they came to is looked at now and then
+      reach = fmaf(64.f, vmax, reach);
+      if (c % 8 == 7 && c + 1 < chunks) measure(c / 8 & 1);
+      rescale(vnext);
     }
+    outputs(chunks - 1);
     const float back = power_of_two(-power);
 #pragma unroll
     for (int e = 0; e < kRows / 2; ++e) state[2 * e * kD] = S[e].x * back, state[(2 * e + 1) * kD] = S[e].y * back;
