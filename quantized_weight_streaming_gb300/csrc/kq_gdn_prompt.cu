@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           tc_fence_after();
         }
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 0, k);
+        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 0, k), state(kDq, kd + kLower, k, 1, 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           gate.wait(&r_ready[j], c & 1);
@@ -676,11 +676,8 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           solved(kDu, td, j);
           tc_commit(&u_done[j]);
         }
-        update(0);
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 1, 1);
-#pragma unroll
-        for (int j = 1; j < 4; ++j) update(j);
+        for (int j = 0; j < 4; ++j) update(j);
         tc_commit(&s_done);
 #pragma unroll
         for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j);
@@ -731,7 +728,21 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       for (int e = 0; e < kToks; ++e) out[e * kD] = kv::from_float<T>(e % 2 ? x[e / 2].y : x[e / 2].x);
       mbar_arrive(&slot_out[c % kSlots]);  // factors and values are read, outputs written
     };
-    const float* vmaxes = p.factors + (slot0 * a.v_heads + h) * kRowFactors + 4 * kChunk + 1;  // a chunk's largest value
+    // A chunk's values times their strengths, made while the chunk before is waited for; returns the largest value.
+    float2 strong[kToks / 2];
+    auto strengthen = [&](int c) {
+      gate.wait(&slot_full[c % kSlots], c / kSlots & 1);
+      const float* f1 = factors(c, 1);
+      const T* value = values(c);
+      auto v = [&](int t) { return kv::to_float(value[t * kD]); };
+#pragma unroll
+      for (int e = 0; e < kToks / 2; e += 2) {
+        const float4 y = *reinterpret_cast<const float4*>(f1 + 2 * e);
+        strong[e] = mul2(make_float2(v(2 * e), v(2 * e + 1)), make_float2(y.x, y.y));
+        strong[e + 1] = mul2(make_float2(v(2 * e + 2), v(2 * e + 3)), make_float2(y.z, y.w));
+      }
+      return factors(c, 0)[4 * kChunk + 1 - sub * kToks];
+    };
     int power = 0;  // S is kept times 2^power, so that it, R and U stay within 2^15
     float reach = 0.f;  // no column of S is longer (a column has 128 entries, so 12 times the largest at most)
     auto measure = [&](int turn) {  // reach from S as it is; all warps together
@@ -751,31 +762,25 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       power = want;
     };
     measure(0);
-    rescale(*vmaxes);
+    rescale(strengthen(0));
     for (int c = 0; c < chunks; ++c) {
       put_parts(mine + kS + sub * (kRows / 2), mine + kS + kD / 2 + sub * (kRows / 2), S);
       tc_fence_before();
       mbar_arrive(&s_ready[sub]);
       if (c) outputs(c - 1);
       down = power_of_two(-power);
-      gate.wait(&slot_full[c % kSlots], c / kSlots & 1);  // factors and values
-      const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vmax = factors(c, 0)[4 * kChunk + 1 - sub * kToks];
-      if (c + 1 < chunks) vmaxes += a.v_heads * kRowFactors;
-      const float vnext = *vmaxes;
       float2 d[kToks / 2];
       gate.wait(&k_done, c & 1);
       tc_fence_after();
       read_columns(mine + kDk + sub * kToks, d);
       {
-        const float *f0 = factors(c, 0), *f1 = factors(c, 1);
-        const T* value = values(c);
+        const float* f0 = factors(c, 0);
         const float2 up = both(power_of_two(power));
-        auto v = [&](int t) { return kv::to_float(value[t * kD]); };
 #pragma unroll
         for (int e = 0; e < kToks / 2; e += 2) {
-          const float4 x = *reinterpret_cast<const float4*>(f0 + 2 * e), y = *reinterpret_cast<const float4*>(f1 + 2 * e);
-          d[e] = fma2(d[e], make_float2(-x.x, -x.y), mul2(mul2(make_float2(v(2 * e), v(2 * e + 1)), up), make_float2(y.x, y.y)));
-          d[e + 1] = fma2(d[e + 1], make_float2(-x.z, -x.w), mul2(mul2(make_float2(v(2 * e + 2), v(2 * e + 3)), up), make_float2(y.z, y.w)));
+          const float4 x = *reinterpret_cast<const float4*>(f0 + 2 * e);
+          d[e] = fma2(d[e], make_float2(-x.x, -x.y), mul2(strong[e], up));
+          d[e + 1] = fma2(d[e + 1], make_float2(-x.z, -x.w), mul2(strong[e + 1], up));
         }
       }
       put_parts(mine + kR + sub * (kToks / 2), mine + kR + kChunk / 2 + sub * (kToks / 2), d);
@@ -795,13 +800,17 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       put_parts(mine + kS + sub * (kToks / 2), mine + kS + kChunk / 2 + sub * (kToks / 2), d);
       tc_fence_before();
       mbar_arrive(&u_ready[sub]);
+      const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vmax = factors(c, 0)[4 * kChunk + 1 - sub * kToks];
+      const float vnext = c + 1 < chunks ? strengthen(c + 1) : vmax;
       gate.wait(&s_done, c & 1);
       tc_fence_after();
-      float2 g[kRows / 2];
-      read_columns(mine + kD3 + sub * kRows, g);
-      tc_fence_before();
 #pragma unroll
-      for (int e = 0; e < kRows / 2; ++e) S[e] = fma2(S[e], both(decay), g[e]);
+      for (int half = 0; half < 2; ++half) {
+        read_columns(mine + kD3 + sub * kRows + half * 16, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) S[8 * half + e] = fma2(S[8 * half + e], both(decay), d[e]);
+      }
+      tc_fence_before();
       // S's columns have grown by 64 max|v| at most; what they came to is looked at now and then
       reach = fmaf(64.f, vmax, reach);
       if (c % 8 == 7 && c + 1 < chunks) measure(c / 8 & 1);
