@@ -133,6 +133,19 @@ struct Raw {
       u[0] = v.x, u[1] = v.y;
     }
   }
+  __device__ __forceinline__ void set(const float* v) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) u[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        union { uint32_t w; T t[2]; } y;
+        y.t[0] = from_float<T>(v[2 * i]), y.t[1] = from_float<T>(v[2 * i + 1]);
+        u[i] = y.w;
+      }
+    }
+  }
   __device__ __forceinline__ void store(T* p) const {
     constexpr int kBytes = N * sizeof(T);
     if constexpr (kBytes % 16 == 0) {

@@ -39,12 +39,11 @@ struct Args {
   float eps;
 };
 
-// Code of |v| / d, rounded half away from zero by what the quotient is and not what a division rounds it to: the
-// estimate is moved by one where the exact sign of |v| - (n - 1/2) d (20 bits of product, one rounding) says so.
-__device__ __forceinline__ int q8_code(float v, float d, float inverse) {
+// v / d rounded half away from zero by what the quotient is and not what a division rounds it to: the estimate is moved by
+// one where the exact sign of |v| - (n - 1/2) d (20 bits of product, one rounding) says so.
+__device__ __noinline__ int q8_border(float v, float d, float inverse) {
   const float m = fabsf(v);
-  float n = floorf(fmaf(m, inverse, 0.5f));
-  n = fminf(n, 128.f);
+  float n = fminf(floorf(fmaf(m, inverse, 0.5f)), 128.f);
   if (fmaf(-(n - 0.5f), d, m) < 0.f) n -= 1.f;
   if (fmaf(-(n + 0.5f), d, m) >= 0.f) n += 1.f;
   const int q = (int)fminf(n, 127.f);
@@ -53,27 +52,36 @@ __device__ __forceinline__ int q8_code(float v, float d, float inverse) {
 
 // Eight values of a block of 32, its other 24 in the three neighbouring lanes; `valid` is the same in all four.
 __device__ __forceinline__ void store_q8(const Args& a, int64_t row, int vec, const float (&y)[8], bool valid) {
-  float most = 0.f;
-  bool odd = false;
+  uint32_t top = 0;  // of the magnitudes' patterns, which order as the numbers do, infinity and NaN above them
 #pragma unroll
-  for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(y[i])), odd |= !isfinite(y[i]);
-  most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
-  most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
-  const unsigned bad = __ballot_sync(~0u, odd && valid) >> (threadIdx.x & 28) & 15u;
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  top = max(top, __shfl_xor_sync(~0u, top, 1));
+  top = max(top, __shfl_xor_sync(~0u, top, 2));
   if (!valid) return;
-  __half s = __float2half_rn(most / 127.0f);
-  if (bad || __hisinf(s)) {
-    norm_flag(bad ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
+  __half s = __float2half_rn(__uint_as_float(top) / 127.0f);
+  if (top >= 0x7F800000u || __hisinf(s)) {
+    norm_flag(top >= 0x7F800000u ? KQ_ERR_NONFINITE : KQ_ERR_RANGE);
     s = __ushort_as_half(0x7E00);
   }
   const float d = __half2float(s);
   union { int8_t c[8]; uint2 u; } q;
+  q.u = make_uint2(0, 0);
   if (d > 0.f) {
     const float inverse = 1.0f / d;
+    float off = 0.f;
+    uint32_t n[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q.c[i] = (int8_t)q8_code(y[i], d, inverse);
-  } else {
-    q.u = make_uint2(0, 0);
+    for (int i = 0; i < 8; ++i) {  // the nearest whole number, in the low bits of 1.5 * 2^23 + it
+      const float r = y[i] * inverse, w = r + 12582912.f;
+      n[i] = __float_as_uint(w);
+      off = fmaxf(off, fabsf(r - (w - 12582912.f)));
+    }
+    q.u.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+    q.u.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
+    if (!(off < 0.4999f && __uint_as_float(top) * inverse < 127.4f)) {  // a quotient near a border between two codes, or past the last
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q.c[i] = (int8_t)q8_border(y[i], d, inverse);
+    }
   }
   *reinterpret_cast<uint2*>(a.codes + row * a.dim + 8 * vec) = q.u;
   if ((threadIdx.x & 3) == 0) {
@@ -94,19 +102,12 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args
   const int vecs = a.dim / 8;
   grid_dependency_wait();
   allow_dependent_launch();
-  float w[N][8];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
-    if (a.weight && first + i * step < vecs) kv::load8(a.weight + 8 * (first + i * step), w[i]);
-  }
   const int64_t ahead = (int64_t)gridDim.x * kRows;
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += ahead, turn ^= 1) {
     const int64_t row = base + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
     const bool here = row < a.rows;
-    const int64_t token = row / a.heads;
+    const int64_t token = a.heads == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)a.heads);
     const int head = (int)(row - token * a.heads);
     const T* x = reinterpret_cast<const T*>(a.x.at(token, head));
     T* res = reinterpret_cast<T*>(a.residual.at(token, head));
@@ -131,8 +132,10 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args
         float r[8];
         other[i].get(r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = kv::to_float(kv::from_float<T>(v[i][e] + r[e]));
-        if (here && vec < vecs) kv::store8(res + 8 * vec, v[i]);
+        for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+        raw[i].set(v[i]);
+        if (here && vec < vecs) raw[i].store(res + 8 * vec);
+        raw[i].get(v[i]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
@@ -153,8 +156,10 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args
     for (int i = 0; i < N; ++i) {
       const int vec = first + i * step;
       const bool mine = here && vec < vecs;
+      float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      if (a.weight && mine) kv::load8(a.weight + 8 * vec, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[i][e];
+      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[e];
       if (a.gate.data) {
         float z[8];
         if (a.residual.data && mine) other[i].load(gate + 8 * vec);
