@@ -95,95 +95,83 @@ __device__ __forceinline__ void store_q8(const Args& a, int64_t row, int vec, co
 // LANES: lanes of a row, 0 for the whole CTA.  N vectors a thread.
 template <typename T, int LANES, int N>
 __global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args a) {
-  __shared__ float s_part[2][32];
+  __shared__ float s_part[32];
   constexpr int kRows = LANES ? 256 / (LANES ? LANES : 1) : 1;  // rows that a CTA has at a time
   const int step = LANES ? LANES : blockDim.x;
   const int first = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
   const int vecs = a.dim / 8;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t ahead = (int64_t)gridDim.x * kRows;
-  int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.rows; base += ahead, turn ^= 1) {
-    const int64_t row = base + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-    const bool here = row < a.rows;
-    const int64_t token = a.heads == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)a.heads);
-    const int head = (int)(row - token * a.heads);
-    const T* x = reinterpret_cast<const T*>(a.x.at(token, head));
-    T* res = reinterpret_cast<T*>(a.residual.at(token, head));
-    const T* gate = reinterpret_cast<const T*>(a.gate.at(token, head));
-    kv::Raw<T, 8> raw[N], other[N];
+  const int64_t row = (int64_t)blockIdx.x * kRows + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
+  const bool here = row < a.rows;
+  const int64_t token = a.heads == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)a.heads);
+  const int head = (int)(row - token * a.heads);
+  const T* x = reinterpret_cast<const T*>(a.x.at(token, head));
+  T* res = reinterpret_cast<T*>(a.residual.at(token, head));
+  const T* gate = reinterpret_cast<const T*>(a.gate.at(token, head));
+  kv::Raw<T, 8> raw[N], other[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int vec = first + i * step;
-      raw[i].clear();
-      other[i].clear();
-      if (!here || vec >= vecs) continue;
-      raw[i].load(x + 8 * vec);
-      if (a.residual.data) other[i].load(res + 8 * vec);
-      else if (a.gate.data) other[i].load(gate + 8 * vec);
-    }
-    float v[N][8], sum = 0.f;
+  for (int i = 0; i < N; ++i) {
+    const int vec = first + i * step;
+    raw[i].clear();
+    other[i].clear();
+    if (!here || vec >= vecs) continue;
+    raw[i].load(x + 8 * vec);
+    if (a.residual.data) other[i].load(res + 8 * vec);
+    else if (a.gate.data) other[i].load(gate + 8 * vec);
+  }
+  float v[N][8], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int vec = first + i * step;
+  for (int i = 0; i < N; ++i) {
+    const int vec = first + i * step;
+    raw[i].get(v[i]);
+    if (a.residual.data) {
+      float r[8];
+      other[i].get(r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+      raw[i].set(v[i]);
+      if (here && vec < vecs) raw[i].store(res + 8 * vec);
       raw[i].get(v[i]);
-      if (a.residual.data) {
-        float r[8];
-        other[i].get(r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] += r[e];
-        raw[i].set(v[i]);
-        if (here && vec < vecs) raw[i].store(res + 8 * vec);
-        raw[i].get(v[i]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
     }
 #pragma unroll
-    for (int o = (LANES ? LANES : 32) / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (!LANES) {
-      if (threadIdx.x % 32 == 0) s_part[turn][threadIdx.x / 32] = sum;
-      __syncthreads();
-      sum = 0.f;
-      const int warps = blockDim.x / 32;
-      if (threadIdx.x % 32 < warps) sum = s_part[turn][threadIdx.x % 32];
+    for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
+  }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  for (int o = (LANES ? LANES : 32) / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (!LANES) {
+    if (threadIdx.x % 32 == 0) s_part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.f;
+    const int warps = blockDim.x / 32;
+    if (threadIdx.x % 32 < warps) sum = s_part[threadIdx.x % 32];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  }
+  const float f = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int vec = first + i * step;
+    const bool mine = here && vec < vecs;
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (a.weight && mine) kv::load8(a.weight + 8 * vec, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[e];
+    if (a.gate.data) {
+      float z[8];
+      if (a.residual.data && mine) other[i].load(gate + 8 * vec);
+      other[i].get(z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= gdn::silu(z[e]);
     }
-    const float f = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int vec = first + i * step;
-      const bool mine = here && vec < vecs;
-      float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-      if (a.weight && mine) kv::load8(a.weight + 8 * vec, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[e];
-      if (a.gate.data) {
-        float z[8];
-        if (a.residual.data && mine) other[i].load(gate + 8 * vec);
-        other[i].get(z);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] *= gdn::silu(z[e]);
-      }
-      if (a.codes) store_q8(a, row, vec, v[i], mine);
-      if (a.out.data && mine) kv::store8(reinterpret_cast<T*>(a.out.at(token, head)) + 8 * vec, v[i]);
-    }
+    if (a.codes) store_q8(a, row, vec, v[i], mine);
+    if (a.out.data && mine) kv::store8(reinterpret_cast<T*>(a.out.at(token, head)) + 8 * vec, v[i]);
   }
 }
 
 template <typename T, int LANES, int N>
 static cudaError_t launch(const Args& a, int64_t ctas, int threads, cudaStream_t st) {
-  if (ctas <= 304) return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)ctas), dim3(threads), 0, st, a);
-  int resident = 0;
-  if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, rms_norm_kernel<T, LANES, N>, threads, 0))
-    return e;
-  const int64_t most = 152ll * std::max(1, resident);
-  // every CTA the same number of rows, as near as it goes
-  const int64_t turns = (ctas + most - 1) / most;
-  const int64_t grid = (ctas + turns - 1) / turns;
-  return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)grid), dim3(threads), 0, st, a);
+  return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)ctas), dim3(threads), 0, st, a);
 }
 
 template <typename T>
