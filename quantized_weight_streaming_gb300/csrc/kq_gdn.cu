@@ -535,11 +535,10 @@ static int check_sizes(const kq_gdn_rule* p, int64_t requests, int64_t tokens, i
   return KQ_OK;
 }
 
-// Whether runs longer than kShortRun tokens go in chunks on the tensor cores: 16-bit keys and queries are exact in fp16 but
-// for a power of two, and what is solved and summed in fp16 parts is bounded where keys have unit length and strengths and
-// decays are at most 1.
-static bool in_chunks(const kq_gdn_rule* p, int dtype, int64_t max_new) {
-  return dtype != KQ_F32 && p->head_dim == 128 && p->unit && p->gates && max_new > gdn::kShortRun;
+// Whether runs longer than kShortRun tokens go in chunks on the tensor cores: what is solved and summed in fp16 parts is
+// bounded where keys have unit length and strengths and decays are at most 1.
+static bool in_chunks(const kq_gdn_rule* p, int64_t max_new) {
+  return p->head_dim == 128 && p->unit && p->gates && max_new > gdn::kShortRun;
 }
 
 }  // namespace kq
@@ -583,7 +582,7 @@ int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t
 size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests, int64_t tokens, int64_t max_new) {
   clear_error();
   if (check_dtype(dtype) || check_rule(p) || check_sizes(p, requests, tokens, max_new)) return 0;
-  return in_chunks(p, dtype, max_new) ? (size_t)gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens) : 0;
+  return in_chunks(p, max_new) ? (size_t)gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens, dtype) : 0;
 }
 
 int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k, const kq_heads* v, const void* d_a,
@@ -614,8 +613,8 @@ int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k
   a.k_heads = p->k_heads, a.v_heads = p->v_heads, a.unit = p->unit, a.gates = p->gates, a.eps = p->eps, a.scale = p->scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.short_most = 0x7fffffff;
-  if (in_chunks(p, dtype, max_new)) {
-    const size_t need = gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens);
+  if (in_chunks(p, max_new)) {
+    const size_t need = gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens, dtype);
     if (!d_ws || ws_bytes < need)
       return fail(KQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", d_ws ? ws_bytes : (size_t)0, need);
     if (!aligned16(d_ws)) return fail(KQ_ERR_ALIGNMENT, "workspace not 16-byte aligned");

@@ -66,7 +66,7 @@ struct RuleArgs {
 constexpr int kChunk = 64;     // tokens that a prompt is worked through in at a time
 constexpr int kShortRun = 32;  // tokens that are faster one by one
 
-int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens);
+int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens, int dtype);
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st);
 int prompt_status(int clear);
 

@@ -47,7 +47,12 @@ __device__ unsigned int g_prompt_status = 0;
 __device__ __forceinline__ void prompt_flag(int status) { atomicOr(&g_prompt_status, 1u << status); }
 
 constexpr int kD = 128;                 // head dimension
-constexpr int kTile = 32768;            // bytes of [K; Q], or of [T; X] in two parts
+constexpr int kTile = 32768;            // bytes of [K; Q] in fp16, or of [T; X] in two parts
+// [K; Q] of fp32 has two parts as well, a tile each.
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+template <typename T>
+constexpr int kKqTile = kParts<T> * kTile;
 constexpr int kRowFactors = 4 * kChunk + 4;
 
 struct PromptArgs {
@@ -104,6 +109,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// The largest magnitude of eight numbers as its pattern without the sign, which orders as the numbers do; and its value.
+template <typename T>
+__device__ __forceinline__ uint32_t pattern_max(const kv::Raw<T, 8>& raw) {
+  uint32_t most = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) most = max(most, raw.u[x] & 0x7FFFFFFFu);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) most = __vmaxu2(most, raw.u[x] & 0x7FFF7FFFu);
+    most = max(most >> 16, most & 0xFFFFu);
+  }
+  return most;
+}
+template <typename T>
+__device__ __forceinline__ float pattern_value(uint32_t pattern) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(pattern);
+  union { uint16_t b; T t; } top;
+  top.b = (uint16_t)pattern;
+  return kv::to_float(top.t);
+}
+
 // The last request whose chunks begin at or before this slot, and the chunk that lies there.
 struct Place {
   Request req;
@@ -143,7 +170,7 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
   const int64_t slot = blockIdx.x / a.k_heads;
   const Place at = place_of(a, slot);
   if (!at.n) return;
-  uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kTile;
+  uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kKqTile<T>;
   float* norms = p.norms + (slot * a.k_heads + hk) * 2 * kChunk;
   kv::Raw<T, 8> raw[8];
 #pragma unroll
@@ -155,14 +182,10 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     const int e = threadIdx.x + x * 256, row = e / 16, vec = e % 16, i = row % kChunk;
-    uint32_t most2 = 0;  // of 16-bit patterns without their signs, which order as the numbers do
+    uint32_t top = pattern_max(raw[x]);
 #pragma unroll
-    for (int y = 0; y < 4; ++y) most2 = __vmaxu2(most2, raw[x].u[y] & 0x7FFF7FFFu);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) most2 = __vmaxu2(most2, __shfl_xor_sync(~0u, most2, o));
-    union { uint16_t b; T t; } top;
-    top.b = (uint16_t)max(most2 >> 16, most2 & 0xFFFFu);
-    const float most = kv::to_float(top.t);
+    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+    const float most = pattern_value<T>(top);
     const int power = (int)(__float_as_uint(most) >> 23);
     const float f = power == 255 || most == 0.f ? 1.f : __uint_as_float((uint32_t)max(254 - power, 1) << 23);
     float v[8], sum = 0.f;
@@ -171,10 +194,11 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
     for (int y = 0; y < 8; ++y) v[y] *= f, sum = fmaf(v[y], v[y], sum);
 #pragma unroll
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    uint4 u;
-    u.x = h2_bits(__floats2half2_rn(v[0], v[1])), u.y = h2_bits(__floats2half2_rn(v[2], v[3]));
-    u.z = h2_bits(__floats2half2_rn(v[4], v[5])), u.w = h2_bits(__floats2half2_rn(v[6], v[7]));
-    *reinterpret_cast<uint4*>(kq + vec / 8 * 16384 + swizzled(row, vec % 8)) = u;
+    uint4 hi, lo;
+    split2(v[0], v[1], hi.x, lo.x), split2(v[2], v[3], hi.y, lo.y), split2(v[4], v[5], hi.z, lo.z), split2(v[6], v[7], hi.w, lo.w);
+    uint8_t* to = kq + vec / 8 * 16384 + swizzled(row, vec % 8);
+    *reinterpret_cast<uint4*>(to) = hi;
+    if (kParts<T> == 2) *reinterpret_cast<uint4*>(to + kTile) = lo;  // of 16-bit types it is zero
     if (vec == 0) norms[row] = i < at.n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
   }
 }
@@ -184,8 +208,9 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
 __device__ __forceinline__ uint32_t lower_at(int i, int j) {
   return i / 32 * 16384 + 8192 + i % 32 * 256 + (((j / 4) ^ ((i & 7) << 1)) << 4) + j % 4 * 4;
 }
-constexpr int kSide = 80;                                       // bytes between rows of the 32 x 32 product in between
-constexpr int kSideAt = kTile, kChunkSmem = kSideAt + 2 * 32 * kSide;
+constexpr int kSide = 80;  // bytes between rows of the 32 x 32 product in between, which lies behind the tile
+template <typename T>
+constexpr int kChunkSmem = kKqTile<T> + 2 * 32 * kSide;
 
 // One chunk and value head: T and X, the rows' factors.
 //
@@ -194,7 +219,8 @@ constexpr int kSideAt = kTile, kChunkSmem = kSideAt + 2 * 32 * kSide;
 // its queries' rows is, times the decays, the operand of the next.  (Solving all of T and X in threads' registers took twice
 // the instructions: 382 us for 129 chunks of 48 heads.)
 template <typename T>
-__global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
+__global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(const PromptArgs p) {
+  constexpr int kSideAt = kKqTile<T>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
   __shared__ __align__(8) uint64_t s_full;
@@ -212,8 +238,8 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
   if (tid == 0) {
     mbar_init(&s_full, 1);
     fence_barrier_init();
-    mbar_arrive_expect_tx(&s_full, kTile);
-    bulk_g2s(smem, p.kq + (slot * a.k_heads + hk) * kTile, kTile, &s_full, l2_policy_evict_first());
+    mbar_arrive_expect_tx(&s_full, kKqTile<T>);
+    bulk_g2s(smem, p.kq + (slot * a.k_heads + hk) * kKqTile<T>, kKqTile<T>, &s_full, l2_policy_evict_first());
   }
   if (tid < 2 * kChunk) (tid < kChunk ? s_fk : s_fq)[tid % kChunk] = p.norms[(slot * a.k_heads + hk) * 2 * kChunk + tid];
   {  // the largest value
@@ -224,12 +250,10 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
       raw[e].clear();
       if (t < n) raw[e].load(reinterpret_cast<const T*>(a.v.at(first + t, h)) + 8 * (tid % 16));
     }
-    uint32_t most2 = 0;
+    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) most2 = __vmaxu2(most2, raw[e].u[x] & 0x7FFF7FFFu);
-    const uint32_t top = __reduce_max_sync(~0u, max(most2 >> 16, most2 & 0xFFFFu));
+    for (int e = 0; e < 8; ++e) top = max(top, pattern_max(raw[e]));
+    top = __reduce_max_sync(~0u, top);
     if (lane == 0) s_vmax[warp] = top;
   }
 
@@ -273,15 +297,24 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
 #pragma unroll
     for (int k = 0; k < kD / 16; ++k) {
       const uint32_t half = base + k / 4 * 16384;
-      uint32_t fa[4];
-      ldmatrix4(fa, half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16));
+      const uint32_t mine = half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16);
+      uint32_t fa[4], fa_low[4];
+      ldmatrix4(fa, mine);
+      if constexpr (kParts<T> == 2) ldmatrix4(fa_low, mine + kTile);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
         if (b > warp) continue;
+        const uint32_t keys = half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2);
         uint32_t fb[4];
-        ldmatrix4(fb, half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2));
-        mma_f16(acc[2 * b], fa, fb[0], fb[1]);
-        mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
+        ldmatrix4(fb, keys);
+        if constexpr (kParts<T> == 2) {
+          uint32_t fb_low[4];
+          ldmatrix4(fb_low, keys + kTile);
+          mma_parts(acc[2 * b], acc[2 * b + 1], fa, fa_low, fb, fb_low);
+        } else {
+          mma_f16(acc[2 * b], fa, fb[0], fb[1]);
+          mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
+        }
       }
     }
   };
@@ -449,10 +482,8 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
     f[2 * kChunk + tid] = fk * exp2_fast((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
     f[3 * kChunk + tid] = a.scale * decay * s_fq[tid];
     if (tid == 0) {
-      union { uint16_t b; T t; } top;
-      top.b = (uint16_t)max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3]));
       f[4 * kChunk] = exp2_fast(s_hi[kChunk - 1]);
-      f[4 * kChunk + 1] = kv::to_float(top.t);
+      f[4 * kChunk + 1] = pattern_value<T>(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])));
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -479,10 +510,16 @@ __global__ void __launch_bounds__(128, 5) gdn_chunk_kernel(const PromptArgs p) {
 constexpr int kWorkWarps = 16, kWorkers = 32 * kWorkWarps;
 constexpr int kRows = kD / 4, kToks = kChunk / 4;  // a thread's key dimensions of S, and its tokens
 constexpr int kFactorBytes = kRowFactors * 4;
-constexpr int kStages = 2, kStage = 2 * kTile;                           // [K; Q], [T; X]
-constexpr int kSlots = 3, kSlot = kChunk * kD * 2 + 2048;                // values and then outputs, factors
-constexpr int kSlotsAt = kStages * kStage, kFactorsAt = kChunk * kD * 2;
-constexpr int kWalkSmem = kSlotsAt + kSlots * kSlot + 1024;              // and room to align
+constexpr int kSlots = 3;  // of values and then outputs, and factors
+// Two stages of tiles; one where [K; Q] has two parts, for shared memory holds no more.
+template <typename T>
+struct Walk {
+  static constexpr int kStages = kParts<T> == 2 ? 1 : 2, kStage = kKqTile<T> + kTile;  // [K; Q], [T; X]
+  static constexpr int kFactorsAt = kChunk * kD * (int)sizeof(T), kSlot = kFactorsAt + 2048;
+  static constexpr int kSlotsAt = kStages * kStage;
+  static constexpr int kSmem = kSlotsAt + kSlots * kSlot + 1024;  // and room to align
+  static_assert(kSmem <= 232448 - 1024, "shared memory");
+};
 // tensor memory: S^T K; S^T Q; U and then X's part of O; R's parts; D3; S's parts, U's over the first of them
 constexpr int kDk = 0, kDq = 64, kDu = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
 
@@ -554,6 +591,9 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float2 (&v)[N]) {
 
 template <typename T>
 __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const PromptArgs p) {
+  using W = Walk<T>;
+  constexpr int kStages = W::kStages, kStage = W::kStage, kSlotsAt = W::kSlotsAt, kSlot = W::kSlot, kFactorsAt = W::kFactorsAt;
+  constexpr int kRowWords = kD * (int)sizeof(T) / 16;  // of 16 bytes, of a row of values
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready[4], r_ready[4], u_ready[4],
       u_done[4], o_read, k_done, s_done, x_done;
@@ -599,9 +639,9 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
         uint8_t* at = smem + c % kStages * kStage;
         uint64_t* bar = &full[c % kStages];
         if (c >= kStages) gate.wait(&tiles_free[c % kStages], c / kStages - 1 & 1);
-        mbar_arrive_expect_tx(bar, 2 * kTile);
-        bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kTile, kTile, bar, policy);
-        bulk_g2s(at + kTile, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
+        mbar_arrive_expect_tx(bar, kStage);
+        bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kKqTile<T>, kKqTile<T>, bar, policy);
+        bulk_g2s(at + kKqTile<T>, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
       }
     }
     __syncwarp();
@@ -610,10 +650,10 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       if (c >= kSlots) gate.wait(&slot_free[c % kSlots], c / kSlots - 1 & 1);
       const uint32_t at = smem_u32(smem + kSlotsAt + c % kSlots * kSlot);
       const int count = req.count - c * kChunk;
-      const char* from = a.v.at(req.first + (int64_t)c * kChunk, h) + lane % 16 * 16;
+      const char* from = a.v.at(req.first + (int64_t)c * kChunk, h) + lane % kRowWords * 16;
 #pragma unroll 8
-      for (int t = lane / 16; t < kChunk; t += 2)
-        copy16(at + t * (kD * (int)sizeof(T)) + lane % 16 * 16, t < count ? from + t * a.v.token_stride : from, t < count ? 16 : 0);
+      for (int t = lane / kRowWords; t < kChunk; t += 32 / kRowWords)
+        copy16(at + (t * kRowWords + lane % kRowWords) * 16, t < count ? from + t * a.v.token_stride : from, t < count ? 16 : 0);
       const float* f = p.factors + ((slot0 + c) * a.v_heads + h) * kRowFactors;
       for (int t = lane; t < kFactorBytes / 16; t += 32) copy16(at + kFactorsAt + t * 16, f + t * 4, 16);
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&slot_full[c % kSlots])) : "memory");
@@ -622,12 +662,12 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   } else if (warp == kWorkWarps + 3) {  // outputs, which lie where the values were
     for (int c = 0; c < chunks; ++c) {
       gate.wait(&slot_out[c % kSlots], c / kSlots & 1);
-      const uint8_t* from = smem + kSlotsAt + c % kSlots * kSlot + lane % 16 * 16;
+      const uint8_t* from = smem + kSlotsAt + c % kSlots * kSlot + lane % kRowWords * 16;
       const int count = min(kChunk, req.count - c * kChunk);
-      char* to = a.out.at(req.first + (int64_t)c * kChunk, h) + lane % 16 * 16;
+      char* to = a.out.at(req.first + (int64_t)c * kChunk, h) + lane % kRowWords * 16;
 #pragma unroll 8
-      for (int t = lane / 16; t < count; t += 2)
-        *reinterpret_cast<uint4*>(to + t * a.out.token_stride) = *reinterpret_cast<const uint4*>(from + t * (kD * (int)sizeof(T)));
+      for (int t = lane / kRowWords; t < count; t += 32 / kRowWords)
+        *reinterpret_cast<uint4*>(to + t * a.out.token_stride) = *reinterpret_cast<const uint4*>(from + t * kRowWords * 16);
       mbar_arrive(&slot_free[c % kSlots]);
     }
   } else if (warp == kWorkWarps) {  // products
@@ -636,9 +676,12 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       constexpr uint64_t kLower = (kChunk * 128) >> 4, kLowPart = (kTile / 2) >> 4;  // a tile's rows 64.., its low parts
       for (int c = 0; c < chunks; ++c) {
         const uint8_t* at = smem + c % kStages * kStage;
-        const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kTile), kt = across_desc(at, 16384);
-        auto state = [&](uint32_t to, uint64_t rows, int k, int low, uint32_t add) {  // 16 of S's key dimensions
-          tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8, rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4), narrow, add);
+        const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kKqTile<T>), kt = across_desc(at, 16384);
+        auto state = [&](uint32_t to, uint64_t rows, int k) {  // 16 of S's key dimensions: high and low parts, and K's low ones
+          rows += (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4);
+          tc_mma_ts(tmem + to, tmem + kS + k * 8, rows, narrow, k);
+          tc_mma_ts(tmem + to, tmem + kS + kD / 2 + k * 8, rows, narrow, 1);
+          if (kParts<T> == 2) tc_mma_ts(tmem + to, tmem + kS + k * 8, rows + (kTile >> 4), narrow, 1);
         };
         auto solved = [&](uint32_t to, uint64_t rows, int k) {  // 16 tokens' R, and the tokens from there on
 #pragma unroll
@@ -653,6 +696,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
 #pragma unroll
           for (int low = 0; low < 2; ++low)
             tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
+          if (kParts<T> == 2) tc_mma_ts(tmem + kD3, tmem + kS + k * 8, kt + (uint64_t)((kTile + k * 2048) >> 4), wide, 1);
         };
         gate.wait(&full[c % kStages], c / kStages & 1);
 #pragma unroll
@@ -660,7 +704,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           gate.wait(&s_ready[j], c & 1);
           tc_fence_after();
 #pragma unroll
-          for (int k = 2 * j; k < 2 * j + 2; ++k) state(kDk, kd, k, 0, k), state(kDk, kd, k, 1, 1);
+          for (int k = 2 * j; k < 2 * j + 2; ++k) state(kDk, kd, k);
         }
         tc_commit(&k_done);
         if (c) {  // the last chunk's outputs are in registers
@@ -668,7 +712,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           tc_fence_after();
         }
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, 0, k), state(kDq, kd + kLower, k, 1, 1);
+        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           gate.wait(&r_ready[j], c & 1);
@@ -831,9 +875,9 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
 static int64_t prompt_slots(int64_t requests, int64_t tokens) { return tokens / kChunk + requests; }
 static int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens) {
-  const int64_t slots = prompt_slots(requests, tokens);
-  return slots * (k_heads + v_heads) * (int64_t)kTile + align256(slots * k_heads * 2 * kChunk * 4) +
+int64_t prompt_workspace(int k_heads, int v_heads, int64_t requests, int64_t tokens, int dtype) {
+  const int64_t slots = prompt_slots(requests, tokens), kq = dtype == KQ_F32 ? kKqTile<float> : kKqTile<__half>;
+  return slots * (k_heads * kq + v_heads * (int64_t)kTile) + align256(slots * k_heads * 2 * kChunk * 4) +
          align256(slots * v_heads * kRowFactors * 4);
 }
 
@@ -843,20 +887,19 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   PromptArgs p{};
   p.r = a;
   p.kq = static_cast<uint8_t*>(ws);
-  p.tx = p.kq + slots * a.k_heads * kTile;
+  p.tx = p.kq + slots * a.k_heads * kKqTile<T>;
   p.norms = reinterpret_cast<float*>(p.tx + slots * a.v_heads * kTile);
   p.factors = p.norms + align256(slots * a.k_heads * 2 * kChunk * 4) / 4;
-  if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem)) return e;
-  if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWalkSmem)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<T>)) return e;
+  if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk<T>::kSmem)) return e;
   if (cudaError_t e = launch_dependent(gdn_rows_kernel<T>, dim3((unsigned)(slots * a.k_heads)), dim3(256), 0, st, p)) return e;
-  if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem, st, p))
+  if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem<T>, st, p))
     return e;
-  const int64_t grid = a.s.requests * a.v_heads;
-  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)grid), dim3(kWorkers + 128), kWalkSmem, st, p);
+  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)(a.s.requests * a.v_heads)), dim3(kWorkers + 128), Walk<T>::kSmem, st, p);
 }
 
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
-  return dtype == KQ_F16 ? launch<__half>(a, ws, st) : launch<__nv_bfloat16>(a, ws, st);
+  return dtype == KQ_F32 ? launch<float>(a, ws, st) : dtype == KQ_F16 ? launch<__half>(a, ws, st) : launch<__nv_bfloat16>(a, ws, st);
 }
 
 int prompt_status(int clear) {
