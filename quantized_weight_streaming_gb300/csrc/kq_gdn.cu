@@ -264,28 +264,18 @@ __global__ void __launch_bounds__(kStepThreads) gdn_step_kernel(const RuleArgs p
   }
 }
 
-// Runs of tokens, four at a time: with S before the four and the decays' products G,
-//
-//   u_i = beta_i (v_i - G_i S . k_i - sum_{j < i} (G_i / G_j) (k_i . k_j) u_j)
-//   out_i = G_i S . q_i + sum_{j <= i} (G_i / G_j) (q_i . k_j) u_j,   S <- G_4 S + sum_j (G_4 / G_j) k_j u_j
-//
-// so all eight products with S are made in one pass and joined together: a lane pair exchanges halves of what it has, which
-// leaves a lane eight of 32 sums, and two barriers do for four tokens.  A warp then has eight columns and a token for every
-// eight lanes, and the tokens' u follow by shuffles.  (One token a pass: 0.57 us each where one request's 192 CTAs are too
-// few to hide the barriers, against YY us.)  Keys and queries of the next eight tokens are fetched while these are worked on.
+// Runs of tokens, one after the other, eight staged at a time; one barrier a token.  (Four tokens a pass, with their u from
+// one another's products, took fewer instructions and barriers but twice the registers: eight runs of up to 5 fp32 tokens
+// 20 us against 14, 16 runs of 33 154 against 129.)
 
-constexpr int kRunTokens = 8, kBlock = 4;  // staged at a time; of a pass
+constexpr int kStepTokens = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kStepThreads) gdn_run_kernel(const RuleArgs p) {
-  constexpr int kSlices = D / kStepCols, kRows = D / 16, kWide = D + 4;  // a row's floats in shared memory, apart by a bank group
-  constexpr int kVecs = kRunTokens * D / 8 / kStepThreads;               // of keys (and of queries) a thread stages; 1 at D = 128
-  constexpr int kLoads = kVecs ? kVecs : 1;
-  __shared__ __align__(16) float s_k[kRunTokens][kWide], s_q[kRunTokens][kWide], s_v[kRunTokens][kStepCols];
-  __shared__ float s_g[kRunTokens], s_beta[kRunTokens];
-  __shared__ float s_low[2][kBlock][kBlock], s_in[2][kBlock][kBlock];  // of u_j in u_i, in out_i
-  __shared__ float s_decay[2][kBlock], s_rest[2][kBlock];              // G_i, G_4 / G_j
-  __shared__ __align__(16) float s_part[4][2][kBlock][kStepCols], s_u[kBlock][kStepCols];
+  constexpr int kSlices = D / kStepCols, kRows = D / 16;
+  __shared__ __align__(16) float s_k[kStepTokens][D], s_q[kStepTokens][D], s_v[kStepTokens][kStepCols];
+  __shared__ float s_g[kStepTokens], s_beta[kStepTokens], s_kq[kStepTokens];
+  __shared__ __align__(16) float s_part[2][4][2][kStepCols];
   grid_dependency_wait();
   allow_dependent_launch();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -297,175 +287,103 @@ __global__ void __launch_bounds__(kStepThreads) gdn_run_kernel(const RuleArgs p)
   const int hk = h / (p.v_heads / p.k_heads);
   const int row0 = (warp * 4 + lane / 8) * kRows, col = (lane % 8) * 4, col0 = slice * kStepCols;
   float* state = p.state + ((int64_t)req.slot * p.v_heads + h) * D * D + (int64_t)row0 * D + col0 + col;
-  float2 S[kRows][2];
+  float4 S[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const float4 x = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(state + (int64_t)i * D);
-    S[i][0] = make_float2(x.x, x.y), S[i][1] = make_float2(x.z, x.w);
-  }
-  // a thread's vector of eight of a token's keys and queries, two of its values, and a token's gates
-  kv::Raw<T, 8> rk[kLoads], rq[kLoads];
-  T rv[2], ra = kv::from_float<T>(0.f), rb = ra;
-  auto fetch = [&](int32_t t0) {
+  for (int i = 0; i < kRows; ++i)
+    S[i] = req.fresh ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(state + (int64_t)i * D);
+  int turn = 0;
+  for (int32_t t0 = 0; t0 < req.count; t0 += kStepTokens) {
+    const int n = min(kStepTokens, req.count - t0);
+    __syncthreads();  // the tokens before are done with
+    for (int e = tid; e < kStepTokens * (D / 8); e += kStepThreads) {
+      const int t = e / (D / 8), vec = e % (D / 8);
+      const int64_t token = (int64_t)req.first + t0 + t;
+      float kk[8], qq[8];
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) {
-      const int e = tid + x * kStepThreads, t = e / (D / 8), vec = e % (D / 8);
-      rk[x].clear();
-      rq[x].clear();
-      if (t >= kRunTokens || t0 + t >= req.count) continue;
-      rk[x].load(reinterpret_cast<const T*>(p.k.at((int64_t)req.first + t0 + t, hk)) + 8 * vec);
-      rq[x].load(reinterpret_cast<const T*>(p.q.at((int64_t)req.first + t0 + t, hk)) + 8 * vec);
-    }
+      for (int i = 0; i < 8; ++i) kk[i] = qq[i] = 0.f;
+      if (t < n) {
+        kv::load8(reinterpret_cast<const T*>(p.k.at(token, hk)) + 8 * vec, kk);
+        kv::load8(reinterpret_cast<const T*>(p.q.at(token, hk)) + 8 * vec, qq);
+      }
+      float k2 = 0.f, q2 = 0.f, kq = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int t = warp + 4 * x;
-      rv[x] = kv::from_float<T>(0.f);
-      if (t0 + t < req.count) rv[x] = reinterpret_cast<const T*>(p.v.at((int64_t)req.first + t0 + t, h))[col0 + lane];
-    }
-    if (tid < kRunTokens && t0 + tid < req.count) {
-      const int64_t token = (int64_t)req.first + t0 + tid;
-      ra = reinterpret_cast<const T*>(p.a + token * p.a_stride)[h], rb = reinterpret_cast<const T*>(p.b + token * p.b_stride)[h];
-    }
-  };
-  const float a_log = p.gates ? p.a_log[h] : 0.f, dt_bias = p.gates ? p.dt_bias[h] : 0.f;
-  fetch(0);
-  for (int32_t t0 = 0; t0 < req.count; t0 += kRunTokens) {
-    const int n = min(kRunTokens, req.count - t0);
-#pragma unroll
-    for (int x = 0; x < kLoads; ++x) {  // what lies past the last token is zero, and stays so
-      const int e = tid + x * kStepThreads, t = e / (D / 8), vec = e % (D / 8);
-      float kk[8], qq[8], k2 = 0.f, q2 = 0.f;
-      rk[x].get(kk);
-      rq[x].get(qq);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) k2 = fmaf(kk[i], kk[i], k2), q2 = fmaf(qq[i], qq[i], q2);
+      for (int i = 0; i < 8; ++i) k2 = fmaf(kk[i], kk[i], k2), q2 = fmaf(qq[i], qq[i], q2), kq = fmaf(kk[i], qq[i], kq);
 #pragma unroll
       for (int o = D / 16; o; o >>= 1) {
         k2 += __shfl_xor_sync(~0u, k2, o);
         q2 += __shfl_xor_sync(~0u, q2, o);
+        kq += __shfl_xor_sync(~0u, kq, o);
       }
-      const bool here = t < n;
       const float fk = p.unit ? 1.0f / sqrtf(k2 + p.eps) : 1.f, fq = p.unit ? p.scale / sqrtf(q2 + p.eps) : p.scale;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) kk[i] = here ? kk[i] * fk : 0.f, qq[i] = here ? qq[i] * fq : 0.f;
-      if (t < kRunTokens) kv::store8(&s_k[t][8 * vec], kk), kv::store8(&s_q[t][8 * vec], qq);
+      for (int i = 0; i < 8; ++i) kk[i] *= fk, qq[i] *= fq;
+      kv::store8(&s_k[t][8 * vec], kk);
+      kv::store8(&s_q[t][8 * vec], qq);
+      if (vec == 0) s_kq[t] = kq * fk * fq;
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) s_v[warp + 4 * x][lane] = kv::to_float(rv[x]);
-    if (tid < kRunTokens) {
-      const float a = kv::to_float(ra), b = kv::to_float(rb);
-      s_g[tid] = tid < n ? expf(p.gates ? log_decay(a, a_log, dt_bias) : a) : 1.f;
-      s_beta[tid] = tid < n ? (p.gates ? sigmoid(b) : b) : 0.f;
+    for (int e = tid; e < kStepTokens * kStepCols; e += kStepThreads) {
+      const int t = e / kStepCols, c = e % kStepCols;
+      if (t < n)
+        s_v[t][c] = kv::to_float(reinterpret_cast<const T*>(p.v.at((int64_t)req.first + t0 + t, h))[col0 + c]);
+    }
+    if (tid < n) {
+      const int64_t token = (int64_t)req.first + t0 + tid;
+      const float a = kv::to_float(reinterpret_cast<const T*>(p.a + token * p.a_stride)[h]);
+      const float b = kv::to_float(reinterpret_cast<const T*>(p.b + token * p.b_stride)[h]);
+      s_g[tid] = expf(p.gates ? log_decay(a, p.a_log[h], p.dt_bias[h]) : a);
+      s_beta[tid] = p.gates ? sigmoid(b) : b;
     }
     __syncthreads();
-    if (t0 + kRunTokens < req.count) fetch(t0 + kRunTokens);
-    {  // products of the fours' keys and queries: four threads each
-      const int which = tid / 4, four = which / 16, i = which / 4 % 4, j = which % 4;
-      const bool low = j < i;  // keys with keys below the diagonal; what is above it does for queries with the same keys, turned
-      const int ii = low ? i : j, jj = low ? j : i;  // ii >= jj
-      const float* left = low ? s_k[4 * four + ii] : s_q[4 * four + ii];
-      const float* right = s_k[4 * four + jj];
-      float sum = 0.f, sum2 = 0.f;
+    for (int t = 0; t < n; ++t, turn ^= 1) {
+      float kr[kRows], qr[kRows];
 #pragma unroll
-      for (int m = 0; m < D / 16; ++m) {
-        const float4 x = *reinterpret_cast<const float4*>(left + 4 * (tid % 4 + 4 * m));
-        const float4 y = *reinterpret_cast<const float4*>(right + 4 * (tid % 4 + 4 * m));
-        sum = fmaf(x.x, y.x, sum), sum2 = fmaf(x.y, y.y, sum2), sum = fmaf(x.z, y.z, sum), sum2 = fmaf(x.w, y.w, sum2);
-      }
-      sum += sum2;
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
-      if (tid % 4 == 0) {
-        const float* g = s_g + 4 * four;
-        float decay = 1.f;
-        for (int m = jj + 1; m <= ii; ++m) decay *= g[m];
-        if (low) s_low[four][ii][jj] = -s_beta[4 * four + ii] * decay * sum;
-        else s_in[four][ii][jj] = decay * sum;
-        if (i == j) {
-          float all = 1.f, rest = 1.f;
-          for (int m = 0; m <= i; ++m) all *= g[m];
-          for (int m = i + 1; m < kBlock; ++m) rest *= g[m];
-          s_decay[four][i] = all, s_rest[four][i] = rest;
-        }
-      }
-    }
-    for (int f = 0; f < kRunTokens / kBlock; ++f) {
-      if (f * kBlock >= n) break;
-      float kr[kBlock][kRows];
-      float2 part[2 * kBlock][2];  // S . k and S . q of the four
-#pragma unroll
-      for (int t = 0; t < kBlock; ++t) {
-        float qr[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; i += 4)
-          kv::load4(&s_k[f * kBlock + t][row0 + i], kr[t] + i), kv::load4(&s_q[f * kBlock + t][row0 + i], qr + i);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) part[t][c] = part[kBlock + t][c] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            part[t][c] = fma2(make_float2(kr[t][i], kr[t][i]), S[i][c], part[t][c]);
-            part[kBlock + t][c] = fma2(make_float2(qr[i], qr[i]), S[i][c], part[kBlock + t][c]);
-          }
-      }
-      // lanes 8 apart keep one of the two kinds each, lanes 16 apart one of the two pairs of tokens each
-      const bool kind = lane & 8, pair = lane & 16;
-      float2 kept[kBlock][2];
-#pragma unroll
-      for (int t = 0; t < kBlock; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 mine = kind ? part[kBlock + t][c] : part[t][c], give = kind ? part[t][c] : part[kBlock + t][c];
-          kept[t][c] = add2(mine, make_float2(__shfl_xor_sync(~0u, give.x, 8), __shfl_xor_sync(~0u, give.y, 8)));
-        }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float2 sum[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 mine = pair ? kept[t + 2][c] : kept[t][c], give = pair ? kept[t][c] : kept[t + 2][c];
-          sum[c] = add2(mine, make_float2(__shfl_xor_sync(~0u, give.x, 16), __shfl_xor_sync(~0u, give.y, 16)));
-        }
-        *reinterpret_cast<float4*>(&s_part[warp][kind][t + (pair ? 2 : 0)][col]) = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
-      }
-      __syncthreads();
-      {  // token i of the four, a column: what S gives, then the tokens before it
-        const int i = lane / 8, c = warp * 8 + lane % 8, t = f * kBlock + i;
-        float ks = 0.f, qs = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) ks += s_part[w][0][i][c], qs += s_part[w][1][i][c];
-        const float g = s_decay[f][i];
-        float u = s_beta[t] * fmaf(-g, ks, s_v[t][c]), o = g * qs;
-#pragma unroll
-        for (int j = 0; j < kBlock; ++j) {
-          const float before = __shfl_sync(~0u, u, j * 8 + lane % 8);  // whole by then
-          if (j < i) u = fmaf(s_low[f][i][j], before, u);
-          if (j <= i) o = fmaf(s_in[f][i][j], before, o);
-        }
-        s_u[i][c] = s_rest[f][i] * u;
-        if (t < n) reinterpret_cast<T*>(p.out.at((int64_t)req.first + t0 + t, h))[col0 + c] = kv::from_float<T>(o);
-      }
-      __syncthreads();
-      const float all = s_decay[f][kBlock - 1];
-      float4 u[kBlock];
-#pragma unroll
-      for (int t = 0; t < kBlock; ++t) u[t] = *reinterpret_cast<const float4*>(&s_u[t][col]);
+      for (int i = 0; i < kRows; i += 4) kv::load4(&s_k[t][row0 + i], kr + i), kv::load4(&s_q[t][row0 + i], qr + i);
+      float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), qs = ks;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        S[i][0] = mul2(S[i][0], make_float2(all, all)), S[i][1] = mul2(S[i][1], make_float2(all, all));
+        ks.x = fmaf(kr[i], S[i].x, ks.x), ks.y = fmaf(kr[i], S[i].y, ks.y);
+        ks.z = fmaf(kr[i], S[i].z, ks.z), ks.w = fmaf(kr[i], S[i].w, ks.w);
+        qs.x = fmaf(qr[i], S[i].x, qs.x), qs.y = fmaf(qr[i], S[i].y, qs.y);
+        qs.z = fmaf(qr[i], S[i].z, qs.z), qs.w = fmaf(qr[i], S[i].w, qs.w);
+      }
 #pragma unroll
-        for (int t = 0; t < kBlock; ++t) {
-          S[i][0] = fma2(make_float2(kr[t][i], kr[t][i]), make_float2(u[t].x, u[t].y), S[i][0]);
-          S[i][1] = fma2(make_float2(kr[t][i], kr[t][i]), make_float2(u[t].z, u[t].w), S[i][1]);
-        }
+      for (int o = 8; o < 32; o *= 2) {
+        ks.x += __shfl_xor_sync(~0u, ks.x, o), ks.y += __shfl_xor_sync(~0u, ks.y, o);
+        ks.z += __shfl_xor_sync(~0u, ks.z, o), ks.w += __shfl_xor_sync(~0u, ks.w, o);
+        qs.x += __shfl_xor_sync(~0u, qs.x, o), qs.y += __shfl_xor_sync(~0u, qs.y, o);
+        qs.z += __shfl_xor_sync(~0u, qs.z, o), qs.w += __shfl_xor_sync(~0u, qs.w, o);
+      }
+      if (lane < 8) {
+        *reinterpret_cast<float4*>(&s_part[turn][warp][0][col]) = ks;
+        *reinterpret_cast<float4*>(&s_part[turn][warp][1][col]) = qs;
+      }
+      __syncthreads();
+      ks = qs = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(&s_part[turn][w][0][col]);
+        const float4 y = *reinterpret_cast<const float4*>(&s_part[turn][w][1][col]);
+        ks.x += x.x, ks.y += x.y, ks.z += x.z, ks.w += x.w;
+        qs.x += y.x, qs.y += y.y, qs.z += y.z, qs.w += y.w;
+      }
+      const float g = s_g[t], beta = s_beta[t], kq = s_kq[t];
+      float4 u = *reinterpret_cast<const float4*>(&s_v[t][col]);
+      u.x = beta * fmaf(-g, ks.x, u.x), u.y = beta * fmaf(-g, ks.y, u.y);
+      u.z = beta * fmaf(-g, ks.z, u.z), u.w = beta * fmaf(-g, ks.w, u.w);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        S[i].x = fmaf(kr[i], u.x, g * S[i].x), S[i].y = fmaf(kr[i], u.y, g * S[i].y);
+        S[i].z = fmaf(kr[i], u.z, g * S[i].z), S[i].w = fmaf(kr[i], u.w, g * S[i].w);
+      }
+      if (tid < 8) {
+        const float o[4] = {fmaf(kq, u.x, g * qs.x), fmaf(kq, u.y, g * qs.y), fmaf(kq, u.z, g * qs.z),
+                            fmaf(kq, u.w, g * qs.w)};
+        kv::store4(reinterpret_cast<T*>(p.out.at((int64_t)req.first + t0 + t, h)) + col0 + col, o);
       }
     }
-    __syncthreads();  // these tokens are done with
   }
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    *reinterpret_cast<float4*>(state + (int64_t)i * D) = make_float4(S[i][0].x, S[i][0].y, S[i][1].x, S[i][1].y);
+  for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(state + (int64_t)i * D) = S[i];
 }
 
 template <typename T>
