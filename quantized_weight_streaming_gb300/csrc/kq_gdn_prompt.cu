@@ -80,12 +80,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two numbers as high and low fp16 parts.
+// Two numbers as high and low fp16 parts: the first eleven bits, and what is left rounded to eleven more.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  hi = h2_bits(h);
-  lo = h2_bits(__floats2half2_rn(a - f.x, b - f.y));
+  const float2 x = make_float2(a, b);
+  const float2 h = make_float2(__uint_as_float(__float_as_uint(a) & 0xFFFFE000u), __uint_as_float(__float_as_uint(b) & 0xFFFFE000u));
+  const float2 l = fma2(h, make_float2(-1.f, -1.f), x);
+  hi = h2_bits(__floats2half2_rn(h.x, h.y));
+  lo = h2_bits(__floats2half2_rn(l.x, l.y));
 }
 
 __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
