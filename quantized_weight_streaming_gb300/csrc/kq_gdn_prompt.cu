@@ -60,6 +60,10 @@ struct PromptArgs {
   uint8_t* kq;      // [slot][key head] tiles
   uint8_t* tx;      // [slot][value head] tiles
   float* norms;     // [slot][key head]: of 64 keys and of 64 queries, what their rows are multiplied by to have unit length
+  // Of each request's chunks: those that are walked down, and those that chunk tasks are done for, where these are not all
+  // slots' (tasks_from < 0); `beside` where tasks run beside the walk launched before them.
+  int64_t from, to, tasks_from;
+  int32_t beside;
   float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64, the largest value
 };
 
@@ -227,13 +231,19 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   __shared__ __align__(8) uint64_t s_full;
   __shared__ double s_first;
   __shared__ uint32_t s_vmax[4];
-  grid_dependency_wait();
+  // Beside a walk this grid reads what grids before that walk wrote (it waited for them) and writes what none before it
+  // touches; that it ends after the walk does, its last CTA sees to.
+  const bool last = blockIdx.x == gridDim.x - 1;
+  if (!p.beside) grid_dependency_wait();
   allow_dependent_launch();
   const RuleArgs& a = p.r;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.x % a.v_heads;
-  const int64_t slot = blockIdx.x / a.v_heads;
+  const int64_t slot = blockIdx.x / a.v_heads + (p.tasks_from < 0 ? 0 : p.tasks_from + chunk_base(max(a.s.q_start[0], 0), 0));
   const Place place = place_of(a, slot);
-  if (!place.n) return;
+  if (!place.n) {
+    if (p.beside && last) grid_dependency_wait();
+    return;
+  }
   const int n = place.n, hk = h / (a.v_heads / a.k_heads);
   const int64_t first = place.first;
   if (tid == 0) {
@@ -488,6 +498,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (p.beside && last) grid_dependency_wait();
 }
 
 // ---- the walk down the chunks --------------------------------------------------------
@@ -607,11 +618,14 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int h = blockIdx.x % a.v_heads;
   const int64_t r = blockIdx.x / a.v_heads;
-  const Request req = read_request(a.s, r, a.max_new);
+  Request req = read_request(a.s, r, a.max_new);
   if (req.status && tid == 0) prompt_flag(req.status);
-  if (!req.count || req.count <= a.short_most) return;
+  if (!req.count || req.count <= a.short_most || p.from * kChunk >= req.count) return;
+  const int64_t slot0 = chunk_base(req.first, r) + p.from;
+  // from here on the request is the part of it that is walked down
+  req.fresh = req.fresh && p.from == 0;
+  req.first += (int32_t)(p.from * kChunk), req.count = (int32_t)(min((int64_t)req.count, p.to * kChunk) - p.from * kChunk);
   const int chunks = (req.count + kChunk - 1) / kChunk;
-  const int64_t slot0 = chunk_base(req.first, r);
   const int hk = h / (a.v_heads / a.k_heads);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1), mbar_init(&tiles_free[i], 1);
@@ -873,6 +887,8 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   }
 }
 
+constexpr int kFirstPart = 12;  // chunks
+
 static int64_t prompt_slots(int64_t requests, int64_t tokens) { return tokens / kChunk + requests; }
 static int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -894,9 +910,32 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<T>)) return e;
   if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk<T>::kSmem)) return e;
   if (cudaError_t e = launch_dependent(gdn_rows_kernel<T>, dim3((unsigned)(slots * a.k_heads)), dim3(256), 0, st, p)) return e;
-  if (cudaError_t e = launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(slots * a.v_heads)), dim3(128), kChunkSmem<T>, st, p))
-    return e;
-  return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)(a.s.requests * a.v_heads)), dim3(kWorkers + 128), Walk<T>::kSmem, st, p);
+  const auto tasks = [&](int64_t chunks) {
+    return launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(chunks * a.v_heads)), dim3(128), kChunkSmem<T>, st, p);
+  };
+  const auto walk = [&]() {
+    return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)(a.s.requests * a.v_heads)), dim3(kWorkers + 128), Walk<T>::kSmem, st, p);
+  };
+  // One request's heads leave SMs idle: its chunks go in parts, and while one part is walked down, the next one's chunk tasks
+  // run on the other SMs (1.5 us a chunk on what 48 heads leave, against 2.6 of walking, so parts may grow).
+  const int64_t chunks = (std::min(a.max_new, a.s.tokens) + kChunk - 1) / kChunk;
+  if (a.s.requests == 1 && 2 * a.v_heads <= 152 && chunks >= 2 * kFirstPart) {
+    p.tasks_from = 0;
+    if (cudaError_t e = tasks(kFirstPart)) return e;
+    p.beside = 1;
+    for (int64_t from = 0, size = kFirstPart; from < chunks;) {
+      const int64_t next = from + size, left = chunks - next, then = left < 2 * size ? left : size * 3 / 2;
+      p.from = from, p.to = next, p.tasks_from = next;
+      if (cudaError_t e = walk()) return e;
+      if (left > 0)
+        if (cudaError_t e = tasks(then)) return e;
+      from = next, size = then;
+    }
+    return cudaSuccess;
+  }
+  p.to = INT64_MAX / kChunk, p.tasks_from = -1;
+  if (cudaError_t e = tasks(slots)) return e;
+  return walk();
 }
 
 cudaError_t launch_prompt(const RuleArgs& a, int dtype, void* ws, cudaStream_t st) {
