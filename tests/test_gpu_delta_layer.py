@@ -145,3 +145,24 @@ def test_gdn_prompts_share_no_workspace_state(kq, dt):  # noqa: F811
     big.check(*one)
     assert all(torch.equal(a, b) for a, b in zip(one, again))
     _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("new,cached,before", [(1537, 0, 0), (2100, 3, 71)])
+def test_gdn_long_prompt_of_one_request(kq, dt, new, cached, before):  # noqa: F811
+    """Prompts long enough that their chunks go in parts; one begins behind rows that are no request's."""
+    c = Delta(dt, ([before, new], [0, cached], [-1, 2]), 1, 2, 128, seed=51, decay=-9.0)
+    p = c.rule(kq)
+    q, k, v, a, b = [x.cuda() for x in (c.q, c.k, c.v, c.a, c.b)]
+    for _ in range(3):
+        state, out = c.state.cuda(), torch.full(c.v.shape, 7.0, dtype=c.dt, device="cuda")
+        n = kq.kq_gdn_workspace_bytes(p, c.dt, 1, v.shape[0], new)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        kq.kq_gdn(p, q, k, v, a, b, _int([before, before + new]), _int([new + cached]), _int([2]), state, out, new, ws=ws)
+        c.check(out.cpu(), state.cpu(), longest=new)
+    # a bound far above the tokens that there are
+    ws = torch.full((kq.kq_gdn_workspace_bytes(p, c.dt, 1, v.shape[0], 100000),), 255, dtype=torch.uint8, device="cuda")
+    state, again = c.state.cuda(), torch.full(c.v.shape, 7.0, dtype=c.dt, device="cuda")
+    kq.kq_gdn(p, q, k, v, a, b, _int([before, before + new]), _int([new + cached]), _int([2]), state, again, 100000, ws=ws)
+    assert torch.equal(again, out)
+    _ok(kq)
