@@ -409,7 +409,9 @@ int read_gdn_status(int clear) {
 
 static int check_requests(const int32_t* q_start, const int32_t* kv_len, const int32_t* slot, int64_t requests,
                           int64_t tokens, const void* state, int64_t slots) {
-  if (requests < 1 || requests > 0x7fffffffll - 1 || tokens < 0 || tokens > 0x7fffffffll || slots < 1 || slots > 0x7fffffffll)
+  // (a token's index, and that of a few past the last, fits 32 bits)
+  if (requests < 1 || requests > 0x7fffffffll - 1 || tokens < 0 || tokens > 0x7fffffffll - gdn::kChunk || slots < 1 ||
+      slots > 0x7fffffffll)
     return fail(KQ_ERR_SHAPE, "requests = %lld, tokens = %lld, slots = %lld", (long long)requests, (long long)tokens,
                 (long long)slots);
   if (!q_start || !slot || !state) return fail(KQ_ERR_INVALID_ARG, "NULL pointer");

@@ -190,7 +190,11 @@ static cudaError_t launch_norm(const Args& a, cudaStream_t st) {
 
 int check_out_rows(const kq_heads* h, const char* name, int dtype, int64_t tokens, int heads, int dim) {
   if (int s = check_heads(h, name, dtype)) return s;
-  if ((tokens > 1 && h->token_stride < dim) || (heads > 1 && h->head_stride < dim))
+  // the rows along the smaller stride lie apart, and those along the larger one past all of them
+  const bool by_head = tokens <= 1 || (heads > 1 && h->head_stride <= h->token_stride);
+  const int64_t near = by_head ? h->head_stride : h->token_stride, far = by_head ? h->token_stride : h->head_stride;
+  const int64_t near_rows = by_head ? heads : tokens, far_rows = by_head ? tokens : heads;
+  if ((near_rows > 1 && near < dim) || (far_rows > 1 && (far < dim || (far - dim) / std::max<int64_t>(near, 1) < near_rows - 1)))
     return fail(KQ_ERR_SHAPE, "rows of %s overlap", name);
   return KQ_OK;
 }

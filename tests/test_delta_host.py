@@ -44,7 +44,9 @@ def test_norm_refusals(kq):
         assert call(**over) == kq.KQ_ERR_INVALID_ARG, over
     for over in (dict(heads=0), dict(heads=5000), dict(dim=0), dict(dim=12), dict(dim=32776), dict(tokens=-1),
                  dict(tokens=1 << 30), dict(out=_view(kq, token=120)), dict(out=_view(kq, head=64)), dict(out=_view(kq, token=0)),
-                 dict(residual=_view(kq, token=0)), dict(x=_view(kq, token=-8))):
+                 dict(residual=_view(kq, token=0)), dict(x=_view(kq, token=-8)),
+                 dict(out=_view(kq, token=128, head=128)), dict(out=_view(kq, token=504, head=128)), dict(out=_view(kq, token=128, head=256)),
+                 dict(residual=_view(kq, token=256, head=256))):
         assert call(**over) == kq.KQ_ERR_SHAPE, over
     for over in (dict(weight=FAKE + 4), dict(x=_view(kq, FAKE + 2)), dict(out=_view(kq, token=8196)), dict(gate=_view(kq, head=132)),
                  dict(residual=_view(kq, FAKE + 8))):
@@ -69,7 +71,7 @@ def test_conv_refusals(kq):
                  dict(out=_view(kq, FAKE + 8192 * 2)), dict(out=_view(kq, FAKE + 16, token=4096))):
         assert call(**over) == kq.KQ_ERR_INVALID_ARG, over
     for over in (dict(channels=0), dict(channels=12), dict(channels=(1 << 20) + 8), dict(width=1), dict(width=5), dict(requests=0),
-                 dict(tokens=-1), dict(slots=0), dict(out=_view(kq, FAKE + (1 << 24), token=56))):
+                 dict(tokens=-1), dict(tokens=(1 << 31) - 1), dict(slots=0), dict(out=_view(kq, FAKE + (1 << 24), token=56))):
         assert call(**over) == kq.KQ_ERR_SHAPE, over
     for over in (dict(weight=FAKE + 4), dict(bias=FAKE + 4), dict(q_start=FAKE + 4), dict(kv_len=FAKE + 4), dict(slot=FAKE + 8),
                  dict(state=FAKE + 2), dict(x=_view(kq, FAKE + 2))):
@@ -92,7 +94,8 @@ def test_gdn_refusals_and_workspace(kq):
         assert call(**over) == kq.KQ_ERR_INVALID_ARG, over
     for over in (dict(head_dim=96), dict(head_dim=256), dict(k_heads=0), dict(k_heads=3), dict(v_heads=0), dict(v_heads=8192, k_heads=1),
                  dict(requests=0), dict(requests=1 << 30), dict(tokens=-1), dict(max_new=-1), dict(slots=0), dict(a_stride=-1),
-                 dict(b_stride=-4), dict(out=_view(kq, token=64)), dict(out=_view(kq, head=0))):
+                 dict(b_stride=-4), dict(out=_view(kq, token=64)), dict(out=_view(kq, head=0)), dict(out=_view(kq, token=256)),
+                 dict(v_heads=2, tokens=(1 << 31) - 1)):
         assert call(**over) == kq.KQ_ERR_SHAPE, over
     for over in (dict(a=FAKE + 2), dict(b=FAKE + 1), dict(a_log=FAKE + 4), dict(dt_bias=FAKE + 4), dict(state=FAKE + 4),
                  dict(q_start=FAKE + 4), dict(kv_len=FAKE + 4), dict(slot=FAKE + 4), dict(q=_view(kq, FAKE + 4))):
