@@ -64,7 +64,7 @@ struct PromptArgs {
   // slots' (tasks_from < 0); `beside` where tasks run beside the walk launched before them.
   int64_t from, to, tasks_from;
   int32_t beside;
-  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, scale G fq; G64, the largest value
+  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, G fq; G64, the largest value
 };
 
 // Where a request's chunks lie among the slots: q_start / 64 + r is at least the slots of the requests before it.
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = warp * 16 + lane / 4 + e * 8;
-    const float f = a.scale * s_fq[i];
+    const float f = s_fq[i];  // the scale, which no fp16 part may have to hold, comes with the outputs
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       if (b / 2 > warp) continue;
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     f[tid] = beta_i * decay * fk;
     f[kChunk + tid] = beta_i;
     f[2 * kChunk + tid] = fk * exp2_fast((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
-    f[3 * kChunk + tid] = a.scale * decay * s_fq[tid];
+    f[3 * kChunk + tid] = decay * s_fq[tid];
     if (tid == 0) {
       f[4 * kChunk] = exp2_fast(s_hi[kChunk - 1]);
       f[4 * kChunk + 1] = pattern_value<T>(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])));
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       return __reduce_max_sync(~0u, most);
     };
     float down = 1.f;
-    auto outputs = [&](int c) {  // of a chunk whose S was taken at 1 / down
+    auto outputs = [&](int c) {  // of a chunk whose S was taken at scale / down
       float2 q[kToks / 2], x[kToks / 2];
       gate.wait(&x_done, c & 1);
       tc_fence_after();
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       tc_fence_before();
       mbar_arrive(&s_ready[sub]);
       if (c) outputs(c - 1);
-      down = power_of_two(-power);
+      down = a.scale * power_of_two(-power);
       float2 d[kToks / 2];
       gate.wait(&k_done, c & 1);
       tc_fence_after();

@@ -234,7 +234,8 @@ def test_conv_malformed_requests(kq):
 class Delta:
     """Inputs of a step on the CPU, and what the rule makes of them in 64 bits."""
 
-    def __init__(self, dt, kind, hk, hv, d, seed=0, unit=True, gates=True, strided=True, size=1.0, common=0.3, decay=None):
+    def __init__(self, dt, kind, hk, hv, d, seed=0, unit=True, gates=True, strided=True, size=1.0, common=0.3, decay=None,
+                 scale=None):
         t, g = TYPES[dt], _gen(seed)
         new, cached, slot = kind if isinstance(kind, tuple) else _steps(kind, seed + d)
         self.q_start, self.kv_len, self.slot = _arrays(new, cached, slot)
@@ -263,13 +264,14 @@ class Delta:
         self.state = size * torch.randn(len(slot) + 3, hv, d, d, generator=g) * 0.3
         self.shape = (hk, hv, d)
         self.unit = unit
-        self.eps, self.scale = 1e-6, d ** -0.5
+        self.eps, self.scale = 1e-6, d ** -0.5 if scale is None else scale
         self.want, self.after = ref.gdn(self.q, self.k, self.v, self.a, self.b, self.a_log, self.dt_bias, unit, self.eps,
                                         self.scale, self.q_start, self.kv_len, self.slot, self.state)
 
     def rule(self, kq):
         cuda = lambda t: None if t is None else t.cuda()  # noqa: E731
-        return kq.GatedDelta(*self.shape, cuda(self.a_log), cuda(self.dt_bias), unit=self.unit, eps=self.eps)
+        return kq.GatedDelta(*self.shape, cuda(self.a_log), cuda(self.dt_bias), unit=self.unit, eps=self.eps,
+                             scale=self.scale)
 
     def run(self, kq, max_new=None, ws=None, stream=None):
         p = self.rule(kq)
@@ -362,6 +364,16 @@ def test_gdn_values_of_any_size(kq, size):
         assert float((state[used].double() - c.after[used]).norm() / c.after[used].norm()) <= 4 * (16 + 2 * math.sqrt(128 * 130)) * H
     else:
         c.check(*c.run(kq))
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["short", "mid"])
+@pytest.mark.parametrize("scale", [1e-6, -1e6])
+def test_gdn_scales_of_any_size(kq, dt, kind, scale):
+    """Factors that no fp16 number comes near: a query's scale is the caller's."""
+    c = Delta(dt, kind, 1, 2, 128, seed=14, scale=scale)
+    c.check(*c.run(kq))
     _ok(kq)
 
 
