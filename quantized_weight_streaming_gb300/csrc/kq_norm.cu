@@ -6,10 +6,16 @@
 // Two flops a byte: memory bounds it, so a row is read once and stays in
 // registers between the sum of its squares and the output.  A thread holds
 // vectors of eight elements.  A row of up to 256 elements (a head) belongs to 8,
-// 16 or 32 lanes, who add their squares by shuffles; a longer one to a CTA, with
-// one barrier a row.  Rows are walked with the grid's stride, so that the weight
-// (which, in fp32, is as long as a row of 16-bit activations and its output
-// together) is read once a CTA and kept.
+// 16 or 32 lanes, who add their squares by shuffles; a longer one to a CTA of its
+// own, with one barrier.  The weight comes from L2 each time: CTAs that kept it in
+// registers and walked rows with the grid's stride, with or without the next row's
+// loads ahead, had fewer bytes in flight (4099 rows of 5120 bf16 with a residual,
+// an output and codes: 61 and 49 us against 39 with as many vectors a thread).
+//
+// Measured on 4099 rows of 5120 bf16: 27.6 us with a residual and an output (168
+// MB, 6.1 TB/s, 0.90 of a copy's rate), 36.3 with codes too (191 MB, 5.3 TB/s: the
+// codes' arithmetic shows); one row of fp32 2.8 us, the time of a launch that loads
+// twice.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -180,9 +186,13 @@ static cudaError_t launch_norm(const Args& a, cudaStream_t st) {
   if (vecs <= 8) return launch<T, 8, 1>(a, (a.rows + 31) / 32, 256, st);
   if (vecs <= 16) return launch<T, 16, 1>(a, (a.rows + 15) / 16, 256, st);
   if (vecs <= 32) return launch<T, 32, 1>(a, (a.rows + 7) / 8, 256, st);
+  // Few rows, of up to a wave of CTAs, want many threads (one row of 5120 bf16 with a residual: 2.0, 2.3, 3.1 us with 1, 2, 4
+  // vectors a thread; 304 rows 4.2, 4.7, 5.1).  Many want fewer that have more in flight each (4096 rows of 5120: 36, 30, 28 us;
+  // of 8192: 71, 47, 42), but for short ones (8192 rows of 2048: 26, 22, 23) and fp32, whose four vectors are more than a
+  // thread's 64 registers hold (4096 rows of 5120: 54, 51, 61).
   auto threads = [&](int n) { return (vecs + 32 * n - 1) / (32 * n) * 32; };
-  if (vecs <= 1024 && (a.rows <= 304 || vecs <= 128)) return launch<T, 0, 1>(a, a.rows, threads(1), st);
-  if (vecs <= 2048) return launch<T, 0, 2>(a, a.rows, threads(2), st);
+  if (vecs <= 1024 && a.rows <= 304) return launch<T, 0, 1>(a, a.rows, threads(1), st);
+  if (vecs <= (a.rows <= 304 || sizeof(T) == 4 ? 2048 : 512)) return launch<T, 0, 2>(a, a.rows, threads(2), st);
   return launch<T, 0, 4>(a, a.rows, threads(4), st);
 }
 
