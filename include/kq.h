@@ -692,7 +692,9 @@ typedef struct {
 /* y of `tokens` tokens to out (rows of `dtype` elements), to out_q8, or to both.
  *  - x, residual (in and out, or NULL), gate (or NULL), out (or NULL): rows of
  *    heads.  out may be x's, the residual's or the gate's own view; other
- *    overlaps are not allowed.
+ *    overlaps are not allowed.  Rows that are written lie apart: along the
+ *    smaller of their strides by dim at least, and along the larger past all
+ *    of those (so too where kq_gdn writes).
  *  - out_q8 (or NULL): planes of KQ_Q8_0 with n = tokens * heads rows (token by
  *    token) and k = dim (then a multiple of 32), written by the rules of
  *    kq_quantize_q8_0 from the fp32 y, scale padding included.  A block that
@@ -732,7 +734,7 @@ typedef struct {
  *  - Two requests of one call must not share a slot. */
 
 /* x, out: rows of `channels` elements of `dtype` (head_stride unused), `tokens`
- * of them; out must not overlap x.  d_state: `dtype` [slots][width - 1]
+ * of them, less than 2^31 - 64; out must not overlap x.  d_state: `dtype` [slots][width - 1]
  * [channels], the last inputs, oldest first, 16-byte aligned; updated.
  * requests >= 1; tokens = 0 is a no-op.
  * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
@@ -766,15 +768,18 @@ typedef struct {
  *  - d_state: fp32 [slots][v_heads][D][D], 16-byte aligned; updated.
  *  - max_new: an upper bound of the requests' new tokens (1 for a decode step).
  *  - fp32 arithmetic and states whatever the types, one rounding of the output.
- *    Prompts of 16-bit types go in chunks of 64 tokens whose products run on the
- *    tensor cores, with every factor that is not exact in fp16 as two fp16 parts
- *    (22 bits): states and outputs are ones of fp32 there too.
+ *    With head_dim 128, unit = 1, gates = 1 and max_new > 32, runs of more than
+ *    32 tokens (a single request's whatever its length) go in chunks of 64
+ *    tokens whose products run on the tensor cores, with every factor that is
+ *    not a 16-bit number as two fp16 parts (22 bits): what they err by is of the
+ *    order of fp32's rounding of the largest value and state of a head's chunk.
  *  - A NaN or infinity in a token's q, k, v or gates makes what it reaches
  *    unspecified: its heads' outputs from that token on (in a chunk, from the
  *    chunk's first on), and their state.
  *  - Workspace: kq_gdn_workspace_bytes, 16-byte aligned (0 where none is
  *    needed); everything in it is written before it is read.
- *  - requests >= 1; tokens = 0 is a no-op.
+ *  - requests >= 1; tokens = 0 is a no-op.  A chunk or step that waits for
+ *    longer than its limit sets KQ_ERR_TIMEOUT for kq_device_status.
  * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_WORKSPACE,
  * KQ_ERR_CUDA. */
 int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k, const kq_heads* v, const void* d_a,
@@ -822,7 +827,8 @@ int kq_kernel_binary_version(int* version);
 
 /* Synchronises the current device and returns the status word that kernels
  * set when a bounded wait expired (KQ_ERR_TIMEOUT) or a device quantizer met
- * a non-finite weight (KQ_ERR_NONFINITE) or an fp16 overflow (KQ_ERR_RANGE);
+ * a non-finite weight (KQ_ERR_NONFINITE) or an fp16 overflow (KQ_ERR_RANGE),
+ * and what the operators above report by these;
  * KQ_OK if none.  clear != 0 resets the word. */
 int kq_device_status(int clear);
 

@@ -1,6 +1,6 @@
 // The gated-delta layers' operators beside their projections: the short causal
 // convolution with its rolling state, and the gated delta rule token by token.
-// (Long prompts of 16-bit types go to kq_gdn_prompt.cu.)
+// (kq_gdn_prompt.cu has the runs of more than kShortRun tokens.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,6 +29,11 @@ __device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1
 // which finds it without a search (a decode step is all such); the pieces after it
 // belong to the window of kPiece token rows they begin in, one at most in each,
 // whose warp finds the request by a 32-way search of q_start.
+//
+// Measured: 64 requests' tokens of 10240 f16 channels 6.7 us (1.6 of bytes, the rest
+// two loads that wait for one another and a launch); 7 ragged requests of 5900 tokens
+// together, bf16, 52 us, 4.7 TB/s.  Eight channels a lane, or eight tokens' loads ahead, took
+// more registers and as long.
 
 constexpr int kConvWarps = 4, kConvAhead = 4, kConvWide = 4;
 
@@ -166,7 +171,8 @@ static cudaError_t launch_conv(const ConvArgs& a, int width, cudaStream_t st) {
 //
 // A decode step (gdn_step_kernel, one token a request) is bound by the states' bytes
 // (128 KB a value head read and written at D = 128); both products with S are made in
-// one pass over the registers, and one barrier joins the four warps' sums.
+// one pass over the registers, and one barrier joins the four warps' sums.  Measured:
+// 128 requests of 48 heads (806 MB) 120 us, 6.7 TB/s, what a copy reaches.
 
 constexpr int kStepThreads = 128, kStepCols = 32;
 

@@ -1,5 +1,5 @@
-// The gated delta rule over prompts of 16-bit types, in chunks of 64 tokens, on
-// the 5th-generation tensor cores.
+// The gated delta rule over prompts, in chunks of 64 tokens, on the 5th-generation
+// tensor cores.
 //
 // Within a chunk, with G_i the product of the decays up to token i and k, q unit
 // rows, the updates u of all tokens solve one triangular system:
@@ -9,25 +9,31 @@
 //   O_i = G_i S^T q_i + (X R)_i,  X = P T,  P_ij = (G_i / G_j) q_i . k_j  for j <= i
 //   S <- G_64 S + sum_j (G_64 / G_j) k_j u_j^T
 //
-// T and X do not depend on the state: gdn_chunk_kernel makes them for all chunks of
-// a call at once.  gdn_prompt_kernel then walks down each request's chunks with a
-// state's columns (64 of 128 a CTA) in registers, three matrix products a chunk:
+// Token by token a state's 128 x 128 numbers take part in two products and a sum
+// each: 8192 tokens of 48 heads took 4931 us so, bound by a token's two passes over
+// the registers and its barrier.  In chunks the same work is matrix products.  T and X do not depend on the
+// state: gdn_rows_kernel lays out each key head's rows, gdn_chunk_kernel makes T and X
+// for all chunks, and gdn_prompt_kernel walks down each request's chunks, a CTA a
+// head, with its state in registers.
 //
-//   D1 = [K; Q] S      128 x 64 x 128
-//   D2 = [T; X] R      128 x 64 x 64     U over its first rows, the rest of O below
-//   D3 = K^T (w U)     128 x 64 x 64
+// The states are fp32 and stay so.  K and Q enter as fp16 with a power of two per row
+// taken out, so that an element is off by at most 2^-25 of its row's largest (fp32
+// rows as two parts), their norms and decays as fp32 factors of rows; what is not a
+// 16-bit number to begin with (S, T, X, R, U) enters as two fp16 parts, 22 bits.
+// Products of two such leave out the one of the low parts.  The update of S is added
+// in registers, with fp32's rounding (the tensor cores' sums cut off instead, and a
+// state that adds up over thousands of tokens would drift).  S, R and U share a power
+// of two per chunk and head that keeps them within fp16: |u_i| <= 64 max|v| + |S|
+// because no step of the rule lets a column grow by more than |v| (|k| <= 1, beta <
+// 1, decays of at most 1).  By the same bound no element of T or X passes 1.
 //
-// The states are fp32 and stay so.  K and Q enter as they came (a power of two per
-// row away: exact in fp16), their norms and decays as fp32 factors of rows; what is
-// not exact in fp16 (S, T, X, R, U) enters as two fp16 parts, 22 bits.  Products of
-// two such leave out the one of the low parts.  D3 is added to S in registers, with
-// fp32's rounding (the tensor cores' sums cut off instead, and a state that adds
-// up over thousands of tokens would drift).  S, R and U share a power of two per
-// chunk and CTA that keeps them within fp16: |u_i| <= 64 max|v| + |S| because no
-// step of the rule lets a column grow by more than |v| (|k| <= 1, beta < 1, decays
-// of at most 1).
-//
-// Measured: see DESIGN
+// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 438 us (the
+// bytes alone 40; 118 TFLOP/s of the rule's own operations); six ragged requests of
+// 4613 tokens together, f16: 221.  Of the first, the rows take 26 us, the chunk
+// tasks 136, the walk 2.6 us a chunk, in which five waits follow one another (S^T K,
+// R, U, the update, S again), each a product of 100 to 500 cycles, its signal (150) and
+// a turn through registers: neither bytes nor products bound it but their latency.
+// States are within 2e-7 of 64-bit ones, fp32 outputs too.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -503,9 +509,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
 
 // ---- the walk down the chunks --------------------------------------------------------
 
-//
 // Everything is turned over here: a lane of tensor memory is a value dimension, so that S^T, R^T and (w U)^T are left
-// operands, which tensor memory holds, straight from the registers that made them, and the chunk's tiles are right ones:
+// operands, which tensor memory holds, straight from the registers that made them, and the chunk's tiles are right ones
+// (128 value dimensions by 128, 128 and 128 columns, K = 128, 64 and 64):
 //
 //   D1 = S^T [K; Q]^T    D2 = R^T [T; X]^T    D3 = (w U)^T K
 //
