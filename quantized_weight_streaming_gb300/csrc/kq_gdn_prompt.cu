@@ -923,7 +923,9 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
     return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)(a.s.requests * a.v_heads)), dim3(kWorkers + 128), Walk<T>::kSmem, st, p);
   };
   // One request's heads leave SMs idle: its chunks go in parts, and while one part is walked down, the next one's chunk tasks
-  // run on the other SMs (1.5 us a chunk on what 48 heads leave, against 2.6 of walking, so parts may grow).
+  // run on the other SMs (1.5 us a chunk on what 48 heads leave, against 2.6 of walking, so parts may grow).  8192 tokens of
+  // 48 heads: 503 us at once, 439 in parts; tasks and walk as CTAs of one kernel, which then held the registers of the larger,
+  // 500.
   const int64_t chunks = (std::min(a.max_new, a.s.tokens) + kChunk - 1) / kChunk;
   if (a.s.requests == 1 && 2 * a.v_heads <= 152 && chunks >= 2 * kFirstPart) {
     p.tasks_from = 0;
