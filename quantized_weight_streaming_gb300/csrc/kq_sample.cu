@@ -81,6 +81,7 @@ struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
   };
   u64 part[kWarps];
   u64 kept;              // this slice's kept weight
+  u64 whole, over;       // this slice's weight, and of those that min_p leaves
   u64 bins;              // the sum of this CTA's share of the bins
   float most, least;
   uint32_t at_k, at_share;
@@ -106,31 +107,43 @@ struct Row {
   float most;      // the largest logit
   float hi, lo;    // log2(e) / temperature in two floats
   float low;       // differences below it weigh nothing
-  // exp((v - most) / temperature): the product with the factor is kept to twice fp32's bits, so the error is that of the
-  // exponential instruction (2^-22) however large the argument is.
-  __device__ __forceinline__ float exp_of(float v) const {
-    const float d = fmaxf(v - most, low);
-    float rest = d * lo;
+  // exp((v - most) / temperature) of two logits, in packed operations: the product with the factor is kept to twice fp32's
+  // bits, so the error is that of the exponential instruction (2^-22) however large the argument is.
+  __device__ __forceinline__ float2 exp_of(float2 v) const {
+    float2 d = add2(v, make_float2(-most, -most));
+    d.x = fmaxf(d.x, low), d.y = fmaxf(d.y, low);
+    const float2 h = make_float2(hi, hi), p = mul2(d, h);
+    float2 rest = fma2(d, make_float2(lo, lo), fma2(d, h, make_float2(-p.x, -p.y)));
     if (EXACT) {
-      const float b = d - v, err = (v - (d - b)) - (most + b);  // v - most = d + err exactly
-      rest = fmaf(d > low ? err : 0.f, hi, rest);
+      const float2 minus = make_float2(-1.f, -1.f), b = fma2(v, minus, d);  // v - most = d + err exactly
+      float2 err = add2(fma2(fma2(b, minus, d), minus, v), fma2(b, minus, make_float2(-most, -most)));
+      err.x = d.x > low ? err.x : 0.f, err.y = d.y > low ? err.y : 0.f;
+      rest = fma2(err, h, rest);
     }
-    const float p = d * hi;
-    rest += fmaf(d, hi, -p);
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
-    return fmaf(e * rest, 0.69314718f, e);
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(p.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(p.y));
+    return fma2(mul2(e, rest), make_float2(0.69314718f, 0.69314718f), e);
   }
-  // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest (signed).
-  static __device__ __forceinline__ void fixed(float e, uint32_t& hi, int32_t& lo) {
-    const float top = e + 2.0f, rest = fmaf(e - (top - 2.0f), kOne, 12582912.0f);
-    hi = __float_as_uint(top) - 0x40000000u, lo = (int32_t)(__float_as_uint(rest) - 0x4B400000u);
+  __device__ __forceinline__ float exp_of(float v) const { return exp_of(make_float2(v, v)).x; }
+  // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest (signed),
+  // each above what `none` has.
+  static __device__ __forceinline__ void fixed(float2 e, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+    const float2 top = add2(e, make_float2(2.0f, 2.0f)), less = add2(top, make_float2(-2.0f, -2.0f));
+    const float2 rest = fma2(fma2(less, make_float2(-1.f, -1.f), e), make_float2(kOne, kOne), make_float2(12582912.0f, 12582912.0f));
+    hi[0] = __float_as_uint(top.x), hi[1] = __float_as_uint(top.y);
+    lo[0] = __float_as_uint(rest.x), lo[1] = __float_as_uint(rest.y);
+  }
+  static constexpr uint32_t kNoneHi = 0x40000000u, kNoneLo = 0x4B400000u;  // of a weight of zero
+  // The sum of `count` weights from the sums of their parts, which so many as a thread sees do not carry over 32 bits but for
+  // the multiples of `none`.
+  static __device__ __forceinline__ u64 joined(uint32_t hi, uint32_t lo, uint32_t count) {
+    return ((u64)(hi - count * kNoneHi) << 22) + (int64_t)(int32_t)(lo - count * kNoneLo);
   }
   static __device__ __forceinline__ u64 fixed(float e) {
-    uint32_t hi;
-    int32_t lo;
-    fixed(e, hi, lo);
-    return ((u64)hi << 22) + (int64_t)lo;
+    uint32_t hi[2], lo[2];
+    fixed(make_float2(e, e), hi, lo);
+    return joined(hi[0], lo[0], 1);
   }
   __device__ __forceinline__ u64 weight(float v) const { return fixed(exp_of(v)); }
 };
@@ -258,6 +271,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       x.u = reinterpret_cast<const uint4*>(s_l)[i];
 #pragma unroll
       for (int e = 0; e < kVec; ++e) f(kv::to_float(x.t[e]));
+    }
+  };
+  auto each2 = [&](auto f) {
+    for (int i = tid; i < vecs; i += kThreads) {
+      union { uint4 u; T t[kVec]; } x;
+      x.u = reinterpret_cast<const uint4*>(s_l)[i];
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) f(make_float2(kv::to_float(x.t[e]), kv::to_float(x.t[e + 1])));
     }
   };
   // x of the cluster's CTAs, each lane that of one
@@ -497,36 +518,75 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     cluster.sync();
   };
 
-  // The border at which the running sum, from the largest logit down, of one each (MASS false) or of the weights of those at
-  // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.
+  // The border at which the running sum, from the largest logit down, of one each (mass false) or of the weights of those at
+  // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.  False
+  // where it lies below what min_p leaves, and so moves nothing: what min_p takes is summed, but neither binned nor gathered
+  // (64 rows of 151936 with top_p 0.95: NEWA us with min_p 0.02, NEWB without).
   const float steps = 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
   auto step_of = [&](float v) {  // falls as v grows
     return (int)(__float_as_uint(fminf((most - v) * steps, 2047.f) + 8388608.f) & (kBins - 1));
   };
-  auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) {
+  auto border = [&](bool mass, u64 target, double share, uint32_t least, u64 least_ties, uint32_t& key, u64& ties, u64& equal) -> bool {
     auto one = [&](float v) { return mass ? w.weight(v) : (u64)1; };
     clear(kBins);
-    const float above_value = least ? value_of(least) : -INFINITY;
-    if (mass)
-      each([&](float v) {
-        if (least && v <= above_value) return;
-        const u64 x = w.weight(v);
-        if (x) add(s.hist.low, s.hist.high, step_of(v), x);
+    const float above_value = least ? value_of(least) : -INFINITY, least_e = fmaxf(min_p, 0x1p-45f);  // below weighs nothing
+    if (mass) {
+      uint32_t hi_sum = 0, lo_sum = 0, seen = 0;  // of all that `least` leaves
+      u64 over = 0;                               // of those that min_p leaves too
+      each2([&](float2 v) {
+        float2 e = w.exp_of(v);
+        if (least) e.x = v.x > above_value ? e.x : 0.f, e.y = v.y > above_value ? e.y : 0.f;
+        uint32_t hi[2], lo[2];
+        w.fixed(e, hi, lo);
+        hi_sum += hi[0] + hi[1], lo_sum += lo[0] + lo[1], seen += 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!((i ? e.y : e.x) >= least_e)) continue;
+          const u64 x = w.joined(hi[i], lo[i], 1);
+          add(s.hist.low, s.hist.high, step_of(i ? v.y : v.x), x);
+          over += x;
+        }
       });
-    else
+      u64 whole = w.joined(hi_sum, lo_sum, seen), lower;
+      if (least_ties && rank == 0 && tid == 0) {
+        const u64 x = least_ties * one(above_value);
+        whole += x;
+        if (w.exp_of(above_value) >= least_e) add(s.hist.low, s.hist.high, step_of(above_value), x), over += x;
+      }
+      if (min_p > 0.f) {
+        scan(whole, whole), scan(over, over);
+        if (tid == 0) s.whole = whole, s.over = over;
+        cluster.sync();
+        ranks_sum(&Shared::whole, lower, whole);
+        ranks_sum(&Shared::over, lower, over);
+        target = max((u64)ceil(share * (double)whole), (u64)1), share = -1.0;
+        if (target > over) return false;
+      }
+    } else {
       each([&](float v) { atomicAdd(&s.hist.low[step_of(v)], 1u); });
-    if (least_ties && rank == 0 && tid == 0)
-      add(s.hist.low, s.hist.high, step_of(value_of(least)), least_ties * one(value_of(least)));
+    }
     find(kBins, target, share);
     const int bin = s.bin;
     u64 rest = target - s.above;
     if (tid == 0) s.listed = 0;
     __syncthreads();
-    each([&](float v) {
-      if (v < above_value || step_of(v) != bin) return;
-      const int at = atomicAdd(&s.listed, 1);
-      if (at < kList) s.list[at] = key_of(v);
-    });
+    // the step's values, and some more for the roundings
+    const float middle = most - (float)bin / steps, half = bin == kBins - 1 ? INFINITY : 0.51f / steps + 1e-6f * fabsf(most);
+    for (int i = tid; i < vecs; i += kThreads) {
+      union { uint4 u; T t[kVec]; } x;
+      x.u = reinterpret_cast<const uint4*>(s_l)[i];
+      bool some = false;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) some |= fabsf(kv::to_float(x.t[e]) - middle) <= half;
+      if (!some) continue;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const float v = kv::to_float(x.t[e]);
+        if (v < above_value || step_of(v) != bin) continue;
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kList) s.list[at] = key_of(v);
+      }
+    }
     cluster.sync();
     const int part = of_lane(&Shared::listed, 0);
     const int count = __reduce_add_sync(~0u, part);
@@ -603,13 +663,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       ties = (rest + x - 1) / x;
       equal /= x;
     }
+    return true;
   };
 
   uint32_t key = 0;  // below every logit: all belong
   u64 ties = 0, equal = 0;
   if (by_k) border(false, (u64)top_k, -1.0, 0, 0, key, ties, equal);
-  if (by_p) border(true, 0, (double)top_p, key, ties, key, ties, equal);
-  const bool at_border = by_k || by_p, some = at_border && ties < equal;  // some of the equal ones only
+  const bool by_mass = by_p && border(true, 0, (double)top_p, key, ties, key, ties, equal);
+  const bool at_border = by_k || by_mass, some = at_border && ties < equal;  // some of the equal ones only
   if (!some) ties = ~0ull;
 
   // The kept weight of each warp's run of the slice; where only some of the equal ones at the border belong, these are counted
@@ -631,35 +692,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     }
     return in ? kept(v) : 0;
   };
-  const float border_value = at_border ? value_of(key) : -INFINITY;
+  const float border_value = at_border ? value_of(key) : -INFINITY, inside = some ? value_of(key + 1) : border_value;
   const u64 tie_weight = some ? kept(border_value) : 0;
+  // below it no logit is kept: of min_p, a little lower than its own border
+  const float filter = min_p > 0.f ? fmaxf(border_value, most - t * (0.01f - logf(min_p)) - 1e-5f * fabsf(most)) : border_value;
   // This lane's share of the kept weight of 32 kVec logits from i on, those at the border left out where only some of them
   // belong, and how many these are.
-  auto group = [&](int i, int& tied) -> u64 {
+  struct Parts {
+    uint32_t hi = 0, lo = 0, seen = 0;
+    int tied = 0;
+    __device__ __forceinline__ u64 weight() const { return decltype(w)::joined(hi, lo, seen); }
+  };
+  auto group = [&](int i, Parts& sum) {
     union { uint4 u; T t[kVec]; } l;
     const bool here = i + lane * kVec < hi;
     if (here) l.u = *reinterpret_cast<const uint4*>(s_l + i + lane * kVec);
-    float v[kVec], top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = here ? kv::to_float(l.t[e]) : -INFINITY, top = fmaxf(top, v[e]);
-    if (!__any_sync(~0u, top >= border_value)) return 0;
-    uint32_t hi_sum = 0;
-    int32_t lo_sum = 0;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const float x = w.exp_of(v[e]);
-      const bool tie = some && v[e] == border_value;
-      uint32_t a;
-      int32_t b;
-      w.fixed(v[e] >= border_value && !tie && (x >= min_p || v[e] == most) ? x : 0.f, a, b);
-      hi_sum += a, lo_sum += b, tied += tie;
+    for (int e = 0; e < kVec; e += 2) {
+      const float2 v = here ? make_float2(kv::to_float(l.t[e]), kv::to_float(l.t[e + 1])) : make_float2(-INFINITY, -INFINITY);
+      if (!__any_sync(~0u, fmaxf(v.x, v.y) >= filter)) continue;
+      const float2 x = w.exp_of(v);
+      uint32_t a[2], b[2];
+      w.fixed(make_float2(v.x >= inside && x.x >= min_p ? x.x : 0.f, v.y >= inside && x.y >= min_p ? x.y : 0.f), a, b);
+      sum.hi += a[0] + a[1], sum.lo += b[0] + b[1], sum.seen += 2;
+      if (some) sum.tied += (v.x == border_value) + (v.y == border_value);
     }
-    return ((u64)hi_sum << 22) + (int64_t)lo_sum;
   };
   auto of_ties = [&](u64 before, int count) { return before < ties ? min(ties - before, (u64)count) * tie_weight : 0; };
-  u64 sum = 0, ahead = 0;
-  int tied = 0;
-  for (int i = lo; i < hi; i += 32 * kVec) sum += group(i, tied);
+  Parts parts;
+  for (int i = lo; i < hi; i += 32 * kVec) group(i, parts);
+  u64 sum = parts.weight(), ahead = 0;
+  int tied = parts.tied;
   if (some) {
     tied = __reduce_add_sync(~0u, tied);
     __syncthreads();
@@ -695,8 +758,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     u64 at = lower, seen = ahead;
     int i = lo;
     for (; i + 32 * kVec < hi; i += 32 * kVec) {
-      int tied = 0;
-      u64 x = group(i, tied);
+      Parts parts;
+      group(i, parts);
+      int tied = parts.tied;
+      u64 x = parts.weight();
 #pragma unroll
       for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
       tied = __reduce_add_sync(~0u, tied);
