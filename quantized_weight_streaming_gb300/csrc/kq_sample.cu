@@ -17,6 +17,12 @@
 // A weight is exp((l - max) / temperature) in fixed point, 44 bits behind the
 // point, and sums are of 64-bit integers: a row of 2^18 equal ones still fits, sums
 // are exact, and no order of atomics or CTAs moves a border or a token.
+//
+// Measured: one row of 248320 fp32 with top_k 20 and top_p 0.8 18 us, 64 rows of 151936
+// fp16 with top_p 0.95 and min_p 0.02 28 us.  Bytes (0.15 and 2.9 us) bound neither:
+// a row's path is a handful of passes over shared memory with a wait for the whole
+// cluster after each (1000 to 2500 cycles), and of a batch the weights' arithmetic
+// (15 instructions a logit and pass) and, without min_p, the bins' atomics.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   // The border at which the running sum, from the largest logit down, of one each (mass false) or of the weights of those at
   // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.  False
   // where it lies below what min_p leaves, and so moves nothing: what min_p takes is summed, but neither binned nor gathered
-  // (64 rows of 151936 with top_p 0.95: NEWA us with min_p 0.02, NEWB without).
+  // (64 rows of 151936 with top_p 0.95: 28 us with min_p 0.02, 54 without).
   const float steps = 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
   auto step_of = [&](float v) {  // falls as v grows
     return (int)(__float_as_uint(fminf((most - v) * steps, 2047.f) + 8388608.f) & (kBins - 1));
