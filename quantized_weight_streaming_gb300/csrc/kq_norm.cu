@@ -7,7 +7,9 @@
 // registers between the sum of its squares and the output.  A thread holds
 // vectors of eight elements.  A row of up to 256 elements (a head) belongs to 8,
 // 16 or 32 lanes, who add their squares by shuffles; a longer one to a CTA of its
-// own, with one barrier.  The weight comes from L2 each time: CTAs that kept it in
+// own, with one barrier.  (Packed fp32 pairs for the arithmetic, here and in the
+// convolution, took longer: 42 us for 4099 rows with codes against 36, and 67 against
+// 52; where each pair is unpacked from 16-bit types the moves undo what they save.)  The weight comes from L2 each time: CTAs that kept it in
 // registers and walked rows with the grid's stride, with or without the next row's
 // loads ahead, had fewer bytes in flight (4099 rows of 5120 bf16 with a residual,
 // an output and codes: 61 and 49 us against 39 with as many vectors a thread).
@@ -98,102 +100,163 @@ __device__ __forceinline__ void store_q8(const Args& a, int64_t row, int vec, co
   }
 }
 
-// LANES: lanes of a row, 0 for the whole CTA.  N vectors a thread.
+// Where a row's elements lie.
+template <typename T>
+struct Row {
+  const T* x;
+  T* residual;
+  const T* gate;
+  T* out;
+  __device__ __forceinline__ Row(const Args& a, int64_t row) {
+    const int64_t token = a.heads == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)a.heads);
+    const int head = (int)(row - token * a.heads);
+    x = reinterpret_cast<const T*>(a.x.at(token, head)), residual = reinterpret_cast<T*>(a.residual.at(token, head));
+    gate = reinterpret_cast<const T*>(a.gate.at(token, head)), out = reinterpret_cast<T*>(a.out.at(token, head));
+  }
+};
+
+// x + residual rounded to the type, which goes back to the residual; and the squares' sum.
+template <typename T>
+__device__ __forceinline__ float sum_squares(const Args& a, const Row<T>& r, int vec, bool mine, kv::Raw<T, 8>& x,
+                                             const kv::Raw<T, 8>& residual, float (&v)[8], float sum) {
+  x.get(v);
+  if (a.residual.data) {
+    float other[8];
+    residual.get(other);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += other[e];
+    x.set(v);
+    if (mine) x.store(r.residual + 8 * vec);
+    x.get(v);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
+  return sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void finish(const Args& a, const Row<T>& r, int64_t row, int vec, bool mine, float f, const float (&w)[8],
+                                       kv::Raw<T, 8>& gate, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * f * w[e];
+  if (a.gate.data) {
+    float z[8];
+    if (a.residual.data && mine) gate.load(r.gate + 8 * vec);
+    gate.get(z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= gdn::silu(z[e]);
+  }
+  if (a.codes) store_q8(a, row, vec, v, mine);
+  if (a.out.data && mine) kv::store8(r.out + 8 * vec, v);
+}
+
+// Rows of up to 8 LANES elements, N of them a group of lanes.
 template <typename T, int LANES, int N>
-__global__ void __launch_bounds__(LANES ? 256 : 1024) rms_norm_kernel(const Args a) {
-  __shared__ float s_part[32];
-  constexpr int kRows = LANES ? 256 / (LANES ? LANES : 1) : 1;  // rows that a CTA has at a time
-  const int step = LANES ? LANES : blockDim.x;
-  const int first = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
-  const int vecs = a.dim / 8;
+__global__ void __launch_bounds__(256) rms_heads_kernel(const Args a) {
+  constexpr int kRows = 256 / LANES;  // that a CTA takes N times
+  const int vec = threadIdx.x % LANES;
+  const bool in = 8 * vec < a.dim;
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t row = (int64_t)blockIdx.x * kRows + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
-  const bool here = row < a.rows;
-  const int64_t token = a.heads == 1 ? row : (int64_t)((uint32_t)row / (uint32_t)a.heads);
-  const int head = (int)(row - token * a.heads);
-  const T* x = reinterpret_cast<const T*>(a.x.at(token, head));
-  T* res = reinterpret_cast<T*>(a.residual.at(token, head));
-  const T* gate = reinterpret_cast<const T*>(a.gate.at(token, head));
+  const int64_t row0 = (int64_t)blockIdx.x * kRows * N + threadIdx.x / LANES;
   kv::Raw<T, 8> raw[N], other[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int vec = first + i * step;
+    const int64_t row = row0 + i * kRows;
     raw[i].clear();
     other[i].clear();
-    if (!here || vec >= vecs) continue;
-    raw[i].load(x + 8 * vec);
-    if (a.residual.data) other[i].load(res + 8 * vec);
-    else if (a.gate.data) other[i].load(gate + 8 * vec);
+    if (!in || row >= a.rows) continue;
+    const Row<T> r(a, row);
+    raw[i].load(r.x + 8 * vec);
+    if (a.residual.data) other[i].load(r.residual + 8 * vec);
+    else if (a.gate.data) other[i].load(r.gate + 8 * vec);
+  }
+  float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  if (a.weight && in) kv::load8(a.weight + 8 * vec, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t row = row0 + i * kRows;
+    const bool mine = in && row < a.rows;
+    const Row<T> r(a, row);
+    float v[8], sum = sum_squares(a, r, vec, mine, raw[i], other[i], v, 0.f);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    finish(a, r, row, vec, mine, 1.0f / sqrtf(sum / (float)a.dim + a.eps), w, other[i], v);
+  }
+}
+
+// A row a CTA, N vectors a thread.
+template <typename T, int N>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const Args a) {
+  __shared__ float s_part[32];
+  const int step = blockDim.x, vecs = a.dim / 8;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t row = blockIdx.x;
+  const Row<T> r(a, row);
+  kv::Raw<T, 8> raw[N], other[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int vec = threadIdx.x + i * step;
+    raw[i].clear();
+    other[i].clear();
+    if (vec >= vecs) continue;
+    raw[i].load(r.x + 8 * vec);
+    if (a.residual.data) other[i].load(r.residual + 8 * vec);
+    else if (a.gate.data) other[i].load(r.gate + 8 * vec);
   }
   float v[N][8], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int vec = first + i * step;
-    raw[i].get(v[i]);
-    if (a.residual.data) {
-      float r[8];
-      other[i].get(r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] += r[e];
-      raw[i].set(v[i]);
-      if (here && vec < vecs) raw[i].store(res + 8 * vec);
-      raw[i].get(v[i]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
+    const int vec = threadIdx.x + i * step;
+    sum = sum_squares(a, r, vec, vec < vecs, raw[i], other[i], v[i], sum);
   }
 #pragma unroll
-  for (int o = (LANES ? LANES : 32) / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (!LANES) {
-    if (threadIdx.x % 32 == 0) s_part[threadIdx.x / 32] = sum;
-    __syncthreads();
-    sum = 0.f;
-    const int warps = blockDim.x / 32;
-    if (threadIdx.x % 32 < warps) sum = s_part[threadIdx.x % 32];
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (threadIdx.x % 32 == 0) s_part[threadIdx.x / 32] = sum;
+  __syncthreads();
+  sum = 0.f;
+  const int warps = blockDim.x / 32;
+  if (threadIdx.x % 32 < warps) sum = s_part[threadIdx.x % 32];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
   const float f = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int vec = first + i * step;
-    const bool mine = here && vec < vecs;
+    const int vec = threadIdx.x + i * step;
     float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (a.weight && mine) kv::load8(a.weight + 8 * vec, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * f * w[e];
-    if (a.gate.data) {
-      float z[8];
-      if (a.residual.data && mine) other[i].load(gate + 8 * vec);
-      other[i].get(z);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= gdn::silu(z[e]);
-    }
-    if (a.codes) store_q8(a, row, vec, v[i], mine);
-    if (a.out.data && mine) kv::store8(reinterpret_cast<T*>(a.out.at(token, head)) + 8 * vec, v[i]);
+    if (a.weight && vec < vecs) kv::load8(a.weight + 8 * vec, w);
+    finish(a, r, row, vec, vec < vecs, f, w, other[i], v[i]);
   }
 }
 
-template <typename T, int LANES, int N>
-static cudaError_t launch(const Args& a, int64_t ctas, int threads, cudaStream_t st) {
-  return launch_dependent(rms_norm_kernel<T, LANES, N>, dim3((unsigned)ctas), dim3(threads), 0, st, a);
+template <typename T, int N>
+static cudaError_t launch(const Args& a, cudaStream_t st) {
+  const int threads = (a.dim / 8 + 32 * N - 1) / (32 * N) * 32;
+  return launch_dependent(rms_norm_kernel<T, N>, dim3((unsigned)a.rows), dim3(threads), 0, st, a);
+}
+template <typename T, int LANES>
+static cudaError_t launch_heads(const Args& a, cudaStream_t st) {
+  // Beyond two waves of CTAs a group takes two rows, for twice the loads in flight and half the CTAs' starts (gated f16 heads of
+  // 128 with 1, 2, 4 rows a group: 12288 3.9, 4.4, 4.9 us; 49152 10.6, 9.9, 10.8; 196608 43, 36, 37).
+  const int64_t ctas = (a.rows + 256 / LANES - 1) / (256 / LANES);
+  if (ctas <= 2 * 152 * 8) return launch_dependent(rms_heads_kernel<T, LANES, 1>, dim3((unsigned)ctas), dim3(256), 0, st, a);
+  return launch_dependent(rms_heads_kernel<T, LANES, 2>, dim3((unsigned)((ctas + 1) / 2)), dim3(256), 0, st, a);
 }
 
 template <typename T>
 static cudaError_t launch_norm(const Args& a, cudaStream_t st) {
   const int vecs = a.dim / 8;
-  if (vecs <= 8) return launch<T, 8, 1>(a, (a.rows + 31) / 32, 256, st);
-  if (vecs <= 16) return launch<T, 16, 1>(a, (a.rows + 15) / 16, 256, st);
-  if (vecs <= 32) return launch<T, 32, 1>(a, (a.rows + 7) / 8, 256, st);
+  if (vecs <= 8) return launch_heads<T, 8>(a, st);
+  if (vecs <= 16) return launch_heads<T, 16>(a, st);
+  if (vecs <= 32) return launch_heads<T, 32>(a, st);
   // Few rows, of up to a wave of CTAs, want many threads (one row of 5120 bf16 with a residual: 2.0, 2.3, 3.1 us with 1, 2, 4
   // vectors a thread; 304 rows 4.2, 4.7, 5.1).  Many want fewer that have more in flight each (4096 rows of 5120: 36, 30, 28 us;
   // of 8192: 71, 47, 42), but for short ones (8192 rows of 2048: 26, 22, 23) and fp32, whose four vectors are more than a
   // thread's 64 registers hold (4096 rows of 5120: 54, 51, 61).
-  auto threads = [&](int n) { return (vecs + 32 * n - 1) / (32 * n) * 32; };
-  if (vecs <= 1024 && a.rows <= 304) return launch<T, 0, 1>(a, a.rows, threads(1), st);
-  if (vecs <= (a.rows <= 304 || sizeof(T) == 4 ? 2048 : 512)) return launch<T, 0, 2>(a, a.rows, threads(2), st);
-  return launch<T, 0, 4>(a, a.rows, threads(4), st);
+  if (vecs <= 1024 && a.rows <= 304) return launch<T, 1>(a, st);
+  if (vecs <= (a.rows <= 304 || sizeof(T) == 4 ? 2048 : 512)) return launch<T, 2>(a, st);
+  return launch<T, 4>(a, st);
 }
 
 }  // namespace norm

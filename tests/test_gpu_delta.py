@@ -67,7 +67,8 @@ def _norm_close(y, want, dt, tiny=0.0):
 
 @pytest.mark.parametrize("dt", list(TYPES))
 @pytest.mark.parametrize("tokens,heads,dim", [(1, 1, 8), (3, 1, 264), (5, 1, 1032), (1, 1, 5120), (700, 1, 2560), (2, 1, 8200),
-                                              (3, 1, 32768), (17, 5, 64), (33, 3, 128), (9, 48, 128), (4, 2, 248), (1000, 1, 40)])
+                                              (3, 1, 32768), (17, 5, 64), (33, 3, 128), (9, 48, 128), (4, 2, 248), (1000, 1, 40),
+                                              (6487, 3, 248), (15577, 5, 40), (9733, 4, 128), (311, 1, 5128), (305, 1, 16392)])
 @pytest.mark.parametrize("residual,gate", [(False, False), (True, False), (False, True), (True, True)])
 def test_norm(kq, dt, tokens, heads, dim, residual, gate):
     g, t = _gen(tokens + dim), TYPES[dt]
