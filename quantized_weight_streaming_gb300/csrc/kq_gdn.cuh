@@ -74,7 +74,12 @@ int prompt_status(int clear);
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 // z / (1 + e^-z), e^-z good to 2^-22 and an error of |z| 2^-24 in its argument; 0 where e^-z passes 2^126.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float silu(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r;
+}
 // The logarithm of a token's decay from its gate.
 __device__ __forceinline__ float log_decay(float a, float a_log, float dt_bias) {
   const float x = a + dt_bias;
