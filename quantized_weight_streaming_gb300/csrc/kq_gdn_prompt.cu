@@ -37,6 +37,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kq_device.cuh"
 #include "kq_gdn.cuh"
@@ -113,6 +114,12 @@ __device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const 
   mma_f16(c1, ah, bl[2], bl[3]);
   mma_f16(c0, al, bh[0], bh[1]);
   mma_f16(c1, al, bh[2], bh[3]);
+}
+// A matrix of 8 x 8 fp16 numbers over a warp, its rows for its columns.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -219,19 +226,18 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
 __device__ __forceinline__ uint32_t lower_at(int i, int j) {
   return i / 32 * 16384 + 8192 + i % 32 * 256 + (((j / 4) ^ ((i & 7) << 1)) << 4) + j % 4 * 4;
 }
-constexpr int kSide = 80;  // bytes between rows of the 32 x 32 product in between, which lies behind the tile
 template <typename T>
-constexpr int kChunkSmem = kKqTile<T> + 2 * 32 * kSide;
+constexpr int kChunkSmem = kKqTile<T>;
 
 // One chunk and value head: T and X, the rows' factors.
 //
-// T is solved by blocks of 32: the two on the diagonal column by column, a thread each, then the one below by two products
-// with the tensor cores, T21 = T22 (-L21) T11.  X = P T follows from the products' own layout: what a warp's mma leaves of
+// T is solved by blocks of 16: the four on the diagonal column by column, a warp each, then what lies below two of them, and
+// below two such pairs, by two products with the tensor cores, T21 = T22 (-L21) T11.  (Diagonal blocks of 32 took two of the
+// warps 9200 of a task's 31000 cycles.)  X = P T follows from the products' own layout: what a warp's mma leaves of
 // its queries' rows is, times the decays, the operand of the next.  (Solving all of T and X in threads' registers took twice
 // the instructions: 382 us for 129 chunks of 48 heads.)
 template <typename T>
 __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(const PromptArgs p) {
-  constexpr int kSideAt = kKqTile<T>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) float s_fk[kChunk], s_fq[kChunk], s_beta[kChunk], s_hi[kChunk], s_lo[kChunk];
   __shared__ __align__(8) uint64_t s_full;
@@ -258,21 +264,25 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     mbar_arrive_expect_tx(&s_full, kKqTile<T>);
     bulk_g2s(smem, p.kq + (slot * a.k_heads + hk) * kKqTile<T>, kKqTile<T>, &s_full, l2_policy_evict_first());
   }
-  if (tid < 2 * kChunk) (tid < kChunk ? s_fk : s_fq)[tid % kChunk] = p.norms[(slot * a.k_heads + hk) * 2 * kChunk + tid];
-  {  // the largest value
-    kv::Raw<T, 8> raw[8];
+  // what is read comes at once: a wait for each after the other took 5000 of a task's 31000 cycles
+  kv::Raw<T, 8> raw[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = tid / 16 + e * 8;
-      raw[e].clear();
-      if (t < n) raw[e].load(reinterpret_cast<const T*>(a.v.at(first + t, h)) + 8 * (tid % 16));
-    }
+  for (int e = 0; e < 8; ++e) {
+    const int t = tid / 16 + e * 8;
+    raw[e].clear();
+    if (t < n) raw[e].load(reinterpret_cast<const T*>(a.v.at(first + t, h)) + 8 * (tid % 16));
+  }
+  const int64_t token = first + (tid < n ? tid : 0);
+  const T gate = reinterpret_cast<const T*>(a.a + token * a.a_stride)[h], strength = reinterpret_cast<const T*>(a.b + token * a.b_stride)[h];
+  const float a_log = a.a_log[h], dt_bias = a.dt_bias[h], norm = p.norms[(slot * a.k_heads + hk) * 2 * kChunk + tid];
+  {  // the largest value
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, pattern_max(raw[e]));
     top = __reduce_max_sync(~0u, top);
     if (lane == 0) s_vmax[warp] = top;
   }
+  (tid < kChunk ? s_fk : s_fq)[tid % kChunk] = norm;
 
   // decays: running sums of their base-2 logarithms in 64 bits, kept as two floats, for what counts is the difference of two
   // that may be large
@@ -280,11 +290,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   float beta = 0.f;
   if (tid < kChunk) {
     if (tid < n) {
-      const int64_t token = first + tid;
       // e^-200 is nothing in fp32, and sums of 64 such keep 2^-38 of what follows them
-      g = 1.4426950408889634 * (double)fmaxf(log_decay(kv::to_float(reinterpret_cast<const T*>(a.a + token * a.a_stride)[h]),
-                                                       a.a_log[h], a.dt_bias[h]), -200.f);
-      beta = sigmoid(kv::to_float(reinterpret_cast<const T*>(a.b + token * a.b_stride)[h]));
+      g = 1.4426950408889634 * (double)fmaxf(log_decay(kv::to_float(gate), a_log, dt_bias), -200.f);
+      beta = sigmoid(kv::to_float(strength));
     }
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -376,88 +384,82 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   __syncthreads();
 
   uint8_t* lowpart = smem + kTile / 2;
-  if (warp < 2) {  // column j of a diagonal block, from the first row down: t_i = [i = j] - sum_m L_im t_m
-    const int j = lane, at0 = 32 * warp;
-    const uint32_t turn = warp * 128;  // column 32 + m of row 32 + i lies where column m of row i does, but for this bit
-    float2 t[16];
+  {  // column j of a diagonal block, from the first row down: t_i = [i = j] - sum_m L_im t_m; half the lanes keep the low parts
+    const int j = lane % 16, at0 = 16 * warp;
+    const uint32_t turn = warp * 64, from = warp / 2 * 16384 + warp % 2 * 4096;  // of row 16 warp + i, column 16 warp + m
+    uint8_t* to = lane < 16 ? smem : lowpart;
+    float2 t[8];
 #pragma unroll
-    for (int m = 0; m < 16; ++m) t[m] = make_float2(0.f, 0.f);
+    for (int m = 0; m < 8; ++m) t[m] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       float2 s0 = make_float2(i == j ? 1.f : 0.f, 0.f), s1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < i; m += 4) {  // what lies at and past i is zero
-        const float4 l = *reinterpret_cast<const float4*>(smem + ((lower_at(i, m) ^ turn) + warp * 16384));
+        const float4 l = *reinterpret_cast<const float4*>(smem + ((lower_at(i, m) ^ turn) + from));
         s0 = fma2(make_float2(l.x, l.y), t[m / 2], s0);
         s1 = fma2(make_float2(l.z, l.w), t[m / 2 + 1], s1);
       }
       const float x = (s0.x + s1.x) + (s0.y + s1.y);
       (i % 2 ? t[i / 2].y : t[i / 2].x) = x;
       const __half hi = __float2half_rn(x);
-      const uint32_t at = swizzled(at0 + i, (at0 + j) / 8) + j % 8 * 2;
-      *reinterpret_cast<__half*>(smem + at) = hi;
-      *reinterpret_cast<__half*>(lowpart + at) = __float2half_rn(x - __half2float(hi));
+      *reinterpret_cast<__half*>(to + swizzled(at0 + i, (at0 + j) / 8) + j % 8 * 2) = lane < 16 ? hi : __float2half_rn(x - __half2float(hi));
     }
-  } else {  // zeros above the diagonal blocks
-    for (int e = tid - 64; e < 32 * 4 * 2; e += 64)
-      *reinterpret_cast<uint4*>((e & 1 ? lowpart : smem) + swizzled(e / 8, 4 + e / 2 % 4)) = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-
-  // the block below: a warp 16 of its 32 rows and 16 of its 32 columns
-  const int m0 = 32 + warp / 2 * 16, n0 = warp % 2 * 16;
-  const uint32_t low = base + kTile / 2, side = base + kSideAt;
-  {
-    float x0[4] = {}, x1[4] = {};
+  // Eight columns of T21 = T22 (-L21) T11 a warp, from row and column `at0` on, blocks of 16 * N: what the first product leaves
+  // is turned into the second's right operand in registers.
+  const uint32_t low = base + kTile / 2;
+  auto below = [&](auto blocks, int at0, int col) {
+    constexpr int N = decltype(blocks)::value;
+    auto product = [&](float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&b)[4]) {
+      mma_f16(c, ah, b[0], b[1]);
+      mma_f16(c, ah, b[2], b[3]);
+      mma_f16(c, al, b[0], b[1]);
+    };
+    uint32_t ah[4], al[4], b[N][4];  // of right operands: two registers of high parts, two of low ones
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t ah[4], al[4], bh[4], bl[4];
+    for (int k = 0; k < N; ++k) ldmatrix4_t(b[k], (lane < 16 ? base : low) + swizzled(at0 + k * 16 + lane % 16, (at0 + col) / 8));
+    float y[N][4] = {}, z[N][4] = {};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 l = *reinterpret_cast<const float2*>(smem + lower_at(m0 + lane / 4 + e % 2 * 8, k * 16 + lane % 4 * 2 + e / 2 * 8));
-        split2(l.x, l.y, ah[e], al[e]);
+    for (int m = 0; m < N; ++m)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (16 * k + 16 <= col) continue;  // above T11's diagonal
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = at0 + 16 * (N + m) + lane / 4 + e % 2 * 8;
+          const float2 l = *reinterpret_cast<const float2*>(smem + lower_at(row, at0 + k * 16 + lane % 4 * 2 + e / 2 * 8));
+          split2(l.x, l.y, ah[e], al[e]);
+        }
+        product(y[m], ah, al, b[k]);
       }
-      const uint32_t at = swizzled(k * 16 + lane % 16, n0 / 8 + lane / 16);
-      ldmatrix4_t(bh, base + at);
-      ldmatrix4_t(bl, low + at);
-      mma_parts(x0, x1, ah, al, bh, bl);
-    }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t hi, lo;
-      uint8_t* to = smem + kSideAt + (m0 - 32 + lane / 4 + e * 8) * kSide + (n0 + lane % 4 * 2) * 2;
-      split2(x0[2 * e], x0[2 * e + 1], hi, lo);
-      *reinterpret_cast<uint32_t*>(to) = hi, *reinterpret_cast<uint32_t*>(to + 32 * kSide) = lo;
-      split2(x1[2 * e], x1[2 * e + 1], hi, lo);
-      *reinterpret_cast<uint32_t*>(to + 16) = hi, *reinterpret_cast<uint32_t*>(to + 32 * kSide + 16) = lo;
+    for (int m = 0; m < N; ++m) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        split2(y[m][2 * e], y[m][2 * e + 1], b[m][e], b[m][2 + e]);
+        b[m][e] = turned(b[m][e]), b[m][2 + e] = turned(b[m][2 + e]);
+      }
+#pragma unroll
+      for (int k = 0; k <= m; ++k) {
+        const uint32_t at = swizzled(at0 + 16 * (N + m) + lane % 16, (at0 + 16 * (N + k)) / 8 + lane / 16);
+        ldmatrix4(ah, base + at);
+        ldmatrix4(al, low + at);
+        product(z[m], ah, al, b[k]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hi, lo;
+        const uint32_t at = swizzled(at0 + 16 * (N + m) + lane / 4 + e * 8, (at0 + col) / 8) + lane % 4 * 4;
+        split2(z[m][2 * e], z[m][2 * e + 1], hi, lo);
+        *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
+      }
     }
-  }
+  };
+  below(std::integral_constant<int, 1>{}, warp / 2 * 32, warp % 2 * 8);
   __syncthreads();
-  {
-    float x0[4] = {}, x1[4] = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t ah[4], al[4], bh[4], bl[4];
-      const uint32_t at = swizzled(m0 + lane % 16, 4 + k * 2 + lane / 16);
-      ldmatrix4(ah, base + at);
-      ldmatrix4(al, low + at);
-      const uint32_t from = side + (k * 16 + lane % 16) * kSide + (n0 + lane / 16 * 8) * 2;
-      ldmatrix4_t(bh, from);
-      ldmatrix4_t(bl, from + 32 * kSide);
-      mma_parts(x0, x1, ah, al, bh, bl);
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t hi, lo;
-      const int row = m0 + lane / 4 + e * 8;
-      uint32_t at = swizzled(row, n0 / 8) + lane % 4 * 4;
-      split2(x0[2 * e], x0[2 * e + 1], hi, lo);
-      *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
-      at = swizzled(row, n0 / 8 + 1) + lane % 4 * 4;
-      split2(x1[2 * e], x1[2 * e + 1], hi, lo);
-      *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
-    }
-  }
+  below(std::integral_constant<int, 2>{}, 0, warp * 8);
   __syncthreads();
 
   // X = P T
