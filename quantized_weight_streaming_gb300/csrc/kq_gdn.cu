@@ -282,14 +282,18 @@ __global__ void __launch_bounds__(kStepThreads) gdn_run_kernel(const RuleArgs p)
   __shared__ __align__(16) float s_k[kStepTokens][D], s_q[kStepTokens][D], s_v[kStepTokens][kStepCols];
   __shared__ float s_g[kStepTokens], s_beta[kStepTokens], s_kq[kStepTokens];
   __shared__ __align__(16) float s_part[2][4][2][kStepCols];
-  grid_dependency_wait();
+  const bool last = p.beside && blockIdx.x == gridDim.x - 1;
+  if (!p.beside) grid_dependency_wait();
   allow_dependent_launch();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int slice = blockIdx.x % kSlices, h = blockIdx.x / kSlices % p.v_heads;
   const int64_t r = blockIdx.x / kSlices / p.v_heads;
   const Request req = read_request(p.s, r, p.max_new);
   if (req.status && tid == 0) gdn_flag(req.status);
-  if (!req.count || req.count > p.short_most) return;
+  if (!req.count || req.count > p.short_most) {
+    if (last) grid_dependency_wait();
+    return;
+  }
   const int hk = h / (p.v_heads / p.k_heads);
   const int row0 = (warp * 4 + lane / 8) * kRows, col = (lane % 8) * 4, col0 = slice * kStepCols;
   float* state = p.state + ((int64_t)req.slot * p.v_heads + h) * D * D + (int64_t)row0 * D + col0 + col;
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(kStepThreads) gdn_run_kernel(const RuleArgs p)
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) *reinterpret_cast<float4*>(state + (int64_t)i * D) = S[i];
+  if (last) grid_dependency_wait();
 }
 
 template <typename T>
@@ -547,6 +552,7 @@ int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k
     a.short_most = requests == 1 ? 0 : gdn::kShortRun;
     KQ_CUDA_TRY(gdn::launch_prompt(a, dtype, d_ws, st));
     if (requests == 1) return KQ_OK;
+    a.beside = 1;
   }
   KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_step<float>(a, p->head_dim, st)
               : dtype == KQ_F16 ? gdn::launch_step<__half>(a, p->head_dim, st)

@@ -61,6 +61,7 @@ struct RuleArgs {
   int32_t k_heads, v_heads, unit, gates;
   float eps, scale;
   int32_t short_most;  // runs of up to so many tokens go token by token, longer ones in chunks
+  int32_t beside;      // runs beside the walk launched before them: it waited for what they read, and they end after it
 };
 
 constexpr int kChunk = 64;     // tokens that a prompt is worked through in at a time

@@ -67,8 +67,8 @@ struct PromptArgs {
   uint8_t* kq;      // [slot][key head] tiles
   uint8_t* tx;      // [slot][value head] tiles
   float* norms;     // [slot][key head]: of 64 keys and of 64 queries, what their rows are multiplied by to have unit length
-  // Of each request's chunks: those that are walked down, and those that chunk tasks are done for, where these are not all
-  // slots' (tasks_from < 0); `beside` where tasks run beside the walk launched before them.
+  // Of each request's chunks: those that are walked down, and those that rows and tasks are done for, where these are not all
+  // slots' (tasks_from < 0); `beside` where rows or tasks run beside the grid launched before them.
   int64_t from, to, tasks_from;
   int32_t beside;
   float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, G fq; G64, the largest value
@@ -177,17 +177,26 @@ __device__ __forceinline__ Place place_of(const RuleArgs& a, int64_t slot) {
   return p;
 }
 
+// A grid `beside` the one launched before it reads what grids before that one wrote (it waited for them) and writes what none
+// of them touches; that it ends after it, its last CTA sees to.
+__device__ __forceinline__ void end_beside(const PromptArgs& p) {
+  if (p.beside && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+}
+__device__ __forceinline__ int64_t first_slot(const PromptArgs& p) {
+  return p.tasks_from < 0 ? 0 : p.tasks_from + chunk_base(max(p.r.s.q_start[0], 0), 0);
+}
+
 // One chunk and key head: the tile of its keys and queries, each row brought to [1, 2) by a power of two and then fp16 (the
 // rows' values stay what they are), and the rows' norms.
 template <typename T>
 __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
-  grid_dependency_wait();
+  if (!p.beside) grid_dependency_wait();
   allow_dependent_launch();
   const RuleArgs& a = p.r;
   const int hk = blockIdx.x % a.k_heads;
-  const int64_t slot = blockIdx.x / a.k_heads;
+  const int64_t slot = first_slot(p) + blockIdx.x / a.k_heads;
   const Place at = place_of(a, slot);
-  if (!at.n) return;
+  if (!at.n) return end_beside(p);
   uint8_t* kq = p.kq + (slot * a.k_heads + hk) * kKqTile<T>;
   float* norms = p.norms + (slot * a.k_heads + hk) * 2 * kChunk;
   kv::Raw<T, 8> raw[8];
@@ -219,6 +228,7 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
     if (kParts<T> == 2) *reinterpret_cast<uint4*>(to + kTile) = lo;  // of 16-bit types it is zero
     if (vec == 0) norms[row] = i < at.n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
   }
+  end_beside(p);
 }
 
 // -L in fp32 over the tile's rows 64.., which the queries leave and X takes: rows of 256 bytes, 32 in each half of the tile,
@@ -243,19 +253,13 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   __shared__ __align__(8) uint64_t s_full;
   __shared__ double s_first;
   __shared__ uint32_t s_vmax[4];
-  // Beside a walk this grid reads what grids before that walk wrote (it waited for them) and writes what none before it
-  // touches; that it ends after the walk does, its last CTA sees to.
-  const bool last = blockIdx.x == gridDim.x - 1;
   if (!p.beside) grid_dependency_wait();
   allow_dependent_launch();
   const RuleArgs& a = p.r;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, h = blockIdx.x % a.v_heads;
-  const int64_t slot = blockIdx.x / a.v_heads + (p.tasks_from < 0 ? 0 : p.tasks_from + chunk_base(max(a.s.q_start[0], 0), 0));
+  const int64_t slot = first_slot(p) + blockIdx.x / a.v_heads;
   const Place place = place_of(a, slot);
-  if (!place.n) {
-    if (p.beside && last) grid_dependency_wait();
-    return;
-  }
+  if (!place.n) return end_beside(p);
   const int n = place.n, hk = h / (a.v_heads / a.k_heads);
   const int64_t first = place.first;
   if (tid == 0) {
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     }
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  if (p.beside && last) grid_dependency_wait();
+  end_beside(p);
 }
 
 // ---- the walk down the chunks --------------------------------------------------------
@@ -625,7 +629,20 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   const RuleArgs& a = p.r;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int h = blockIdx.x % a.v_heads;
-  const int64_t r = blockIdx.x / a.v_heads;
+  // The longest first, of 32 requests at a time (six ragged ones of 48 heads, two rounds of CTAs: 103 us as they come,
+  // 82 so).
+  int64_t r = blockIdx.x / a.v_heads;
+  if (a.s.requests > 1) {
+    const int64_t mine = r / 32 * 32 + lane;
+    const int count = mine < a.s.requests ? read_request(a.s, mine, a.max_new).count : -1;
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int other = __shfl_sync(~0u, count, i);
+      before += other > count || (other == count && i < lane);
+    }
+    r = r / 32 * 32 + __ffs(__ballot_sync(~0u, before == r % 32)) - 1;
+  }
   Request req = read_request(a.s, r, a.max_new);
   if (req.status && tid == 0) prompt_flag(req.status);
   if (!req.count || req.count <= a.short_most || p.from * kChunk >= req.count) return;
@@ -917,7 +934,9 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
   p.factors = p.norms + align256(slots * a.k_heads * 2 * kChunk * 4) / 4;
   if (cudaError_t e = cudaFuncSetAttribute(gdn_chunk_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem<T>)) return e;
   if (cudaError_t e = cudaFuncSetAttribute(gdn_prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk<T>::kSmem)) return e;
-  if (cudaError_t e = launch_dependent(gdn_rows_kernel<T>, dim3((unsigned)(slots * a.k_heads)), dim3(256), 0, st, p)) return e;
+  const auto rows = [&](int64_t chunks) {
+    return launch_dependent(gdn_rows_kernel<T>, dim3((unsigned)(chunks * a.k_heads)), dim3(256), 0, st, p);
+  };
   const auto tasks = [&](int64_t chunks) {
     return launch_dependent(gdn_chunk_kernel<T>, dim3((unsigned)(chunks * a.v_heads)), dim3(128), kChunkSmem<T>, st, p);
   };
@@ -925,25 +944,36 @@ static cudaError_t launch(const RuleArgs& a, void* ws, cudaStream_t st) {
     return launch_dependent(gdn_prompt_kernel<T>, dim3((unsigned)(a.s.requests * a.v_heads)), dim3(kWorkers + 128), Walk<T>::kSmem, st, p);
   };
   // One request's heads leave SMs idle: its chunks go in parts, and while one part is walked down, the next one's chunk tasks
-  // run on the other SMs (1.5 us a chunk on what 48 heads leave, against 2.6 of walking, so parts may grow).  8192 tokens of
-  // 48 heads: 503 us at once, 439 in parts; tasks and walk as CTAs of one kernel, which then held the registers of the larger,
-  // 500.
+  // and the rows of the one after run on the other SMs (1.4 us a chunk on what 48 heads leave, against 2.6 of walking, so
+  // parts may grow).  8192 tokens of 48 heads: 503 us at once, 439 in parts; tasks and walk as CTAs of one kernel, which then
+  // held the registers of the larger, 500.
   const int64_t chunks = (std::min(a.max_new, a.s.tokens) + kChunk - 1) / kChunk;
   if (a.s.requests == 1 && 2 * a.v_heads <= 152 && chunks >= 2 * kFirstPart) {
+    const auto part_after = [&](int64_t to, int64_t size) {  // what follows chunk `to`, the end of a part of that size
+      const int64_t left = chunks - to;
+      return left < 2 * size ? left : size * 3 / 2;
+    };
+    int64_t from = 0, size = kFirstPart, next = part_after(size, size);
     p.tasks_from = 0;
-    if (cudaError_t e = tasks(kFirstPart)) return e;
+    if (cudaError_t e = rows(size)) return e;
+    if (cudaError_t e = tasks(size)) return e;
     p.beside = 1;
-    for (int64_t from = 0, size = kFirstPart; from < chunks;) {
-      const int64_t next = from + size, left = chunks - next, then = left < 2 * size ? left : size * 3 / 2;
-      p.from = from, p.to = next, p.tasks_from = next;
+    p.tasks_from = size;
+    if (cudaError_t e = rows(next)) return e;
+    while (true) {
+      p.from = from, p.to = from + size;
       if (cudaError_t e = walk()) return e;
-      if (left > 0)
-        if (cudaError_t e = tasks(then)) return e;
-      from = next, size = then;
+      if (!next) return cudaSuccess;
+      p.tasks_from = p.to;
+      if (cudaError_t e = tasks(next)) return e;
+      from += size, size = next, next = part_after(from + size, size);
+      p.tasks_from = from + size;
+      if (next)
+        if (cudaError_t e = rows(next)) return e;
     }
-    return cudaSuccess;
   }
   p.to = INT64_MAX / kChunk, p.tasks_from = -1;
+  if (cudaError_t e = rows(slots)) return e;
   if (cudaError_t e = tasks(slots)) return e;
   return walk();
 }
