@@ -544,8 +544,9 @@ struct Walk {
   static constexpr int kSmem = kSlotsAt + kSlots * kSlot + 1024;  // and room to align
   static_assert(kSmem <= 232448 - 1024, "shared memory");
 };
-// tensor memory: S^T K; S^T Q; U and then X's part of O; R's parts; D3; S's parts, U's over the first of them
-constexpr int kDk = 0, kDq = 64, kDu = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
+// tensor memory: S^T K, and over each 16 tokens' columns of it, once they are read, these tokens' U in two parts; S^T Q; U and
+// then X's part of O; R's parts; D3; S's parts
+constexpr int kDk = 0, kU = 0, kDq = 64, kDu = 128, kR = 192, kD3 = 256, kS = 384, kColumns = 512;
 
 // Barriers that are waited on with a limit; after one ran out all waits return at once, and the warps run through.
 struct Gate {
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   constexpr int kRowWords = kD * (int)sizeof(T) / 16;  // of 16 bytes, of a row of values
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready[4], r_ready[4], u_ready[4],
-      u_done[4], o_read, k_done, s_done, x_done;
+      u_done[4], o_read, k_done, s_done[2], x_done;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
     for (int i = 0; i < 4; ++i)
       mbar_init(&s_ready[i], kWorkers / 4), mbar_init(&r_ready[i], kWorkers / 4), mbar_init(&u_ready[i], kWorkers / 4), mbar_init(&u_done[i], 1);
     mbar_init(&o_read, kWorkers);
-    for (uint64_t* b : {&k_done, &s_done, &x_done}) mbar_init(b, 1);
+    for (uint64_t* b : {&k_done, &s_done[0], &s_done[1], &x_done}) mbar_init(b, 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
     }
   } else if (warp == kWorkWarps) {  // products
     if (elect_one()) {
-      const uint32_t narrow = idesc_f16(128, kChunk), wide = idesc_f16(128, kD) | kAcross;
+      const uint32_t narrow = idesc_f16(128, kChunk), wide = idesc_f16(128, kD / 2) | kAcross;
       constexpr uint64_t kLower = (kChunk * 128) >> 4, kLowPart = (kTile / 2) >> 4;  // a tile's rows 64.., its low parts
       for (int c = 0; c < chunks; ++c) {
         const uint8_t* at = smem + c % kStages * kStage;
@@ -730,15 +731,15 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
                       rows + (pass == 2 ? kLowPart : 0) + (uint64_t)((k * 16 * 128 + k * 32) >> 4), idesc_f16(128, kChunk - 16 * k),
                       pass || k);
         };
-        auto update = [&](int k) {  // 16 tokens' U
-          gate.wait(&u_ready[k], c & 1);
-          tc_fence_after();
-#pragma unroll
-          for (int low = 0; low < 2; ++low)
-            tc_mma_ts(tmem + kD3, tmem + kS + low * (kChunk / 2) + k * 8, kt + (uint64_t)(k * 2048 >> 4), wide, low || k);
-          if (kParts<T> == 2) tc_mma_ts(tmem + kD3, tmem + kS + k * 8, kt + (uint64_t)((kTile + k * 2048) >> 4), wide, 1);
+        auto update = [&](int half, int k) {  // 16 tokens' U, 64 of S's key dimensions
+          const uint64_t keys = kt + (uint64_t)((half * 16384 + k * 2048) >> 4);
+          const uint32_t to = tmem + kD3 + half * (kD / 2), u = tmem + kU + k * 16;
+          tc_mma_ts(to, u, keys, wide, k);
+          tc_mma_ts(to, u + 8, keys, wide, 1);
+          if (kParts<T> == 2) tc_mma_ts(to, u, keys + (kTile >> 4), wide, 1);
         };
         gate.wait(&full[c % kStages], c / kStages & 1);
+        if (c) gate.wait(&s_done[1], c - 1 & 1);  // the last chunk's U, which the first product goes over, is read
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           gate.wait(&s_ready[j], c & 1);
@@ -761,8 +762,15 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           tc_commit(&u_done[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) update(j);
-        tc_commit(&s_done);
+        for (int j = 0; j < 4; ++j) {
+          gate.wait(&u_ready[j], c & 1);
+          tc_fence_after();
+          update(0, j);
+        }
+        tc_commit(&s_done[0]);  // half of S goes on while the other half is made
+#pragma unroll
+        for (int j = 0; j < 4; ++j) update(1, j);
+        tc_commit(&s_done[1]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j);
         tc_commit(&x_done);
@@ -881,12 +889,12 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           d[e] = mul2(d[e], make_float2(x.x, x.y)), d[e + 1] = mul2(d[e + 1], make_float2(x.z, x.w));
         }
       }
-      put_parts(mine + kS + sub * (kToks / 2), mine + kS + kChunk / 2 + sub * (kToks / 2), d);
+      put_parts(mine + kU + sub * kToks, mine + kU + sub * kToks + kToks / 2, d);
       tc_fence_before();
       mbar_arrive(&u_ready[sub]);
       const float decay = factors(c, 0)[4 * kChunk - sub * kToks], vmax = factors(c, 0)[4 * kChunk + 1 - sub * kToks];
       const float vnext = c + 1 < chunks ? strengthen(c + 1) : vmax;
-      gate.wait(&s_done, c & 1);
+      gate.wait(&s_done[sub / 2], c & 1);
       tc_fence_after();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
