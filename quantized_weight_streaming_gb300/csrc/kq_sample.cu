@@ -18,8 +18,8 @@
 // point, and sums are of 64-bit integers: a row of 2^18 equal ones still fits, sums
 // are exact, and no order of atomics or CTAs moves a border or a token.
 //
-// Measured: one row of 248320 fp32 with top_k 20 and top_p 0.8 18 us, 64 rows of 151936
-// fp16 with top_p 0.95 and min_p 0.02 28 us.  Bytes (0.15 and 2.9 us) bound neither:
+// Measured: one row of 248320 fp32 with top_k 20 and top_p 0.8 10 us, 64 rows of 151936
+// fp16 with top_p 0.95 and min_p 0.02 27 us.  Bytes (0.15 and 2.9 us) bound neither:
 // a row's path is a handful of passes over shared memory with a wait for the whole
 // cluster after each (1000 to 2500 cycles), and of a batch the weights' arithmetic
 // (15 instructions a logit and pass) and, without min_p, the bins' atomics.
@@ -66,6 +66,11 @@ typedef unsigned long long u64;
 constexpr int kList = 1024;
 constexpr int kFewK = 256;  // top_k up to which the candidates are gathered without a histogram
 
+// What each CTA of a cluster tells all others: its largest and least logit, whether it has a NaN, its bounds for the top_k-th,
+// how many logits it listed, the sum of its share of the bins, its weight, and of that what min_p leaves, and what is kept, how
+// many at the border it has.
+enum { kRange, kNan, kBounds, kListed, kBinned, kWhole, kOver, kKept, kTies, kTold };
+
 // What the CTAs of a cluster show one another.
 struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
   union {
@@ -85,13 +90,10 @@ struct alignas(16) Shared {  // the slice lies behind it, in words of 16 bytes
     uint32_t list[kList];  // keys of this slice's logits in the border's step
     u64 top[kList];        // of those that may be among the top_k, each above the complement of its id
   };
+  u64 told[kTold][kMostCluster];
   u64 part[kWarps];
-  u64 kept;              // this slice's kept weight
-  u64 whole, over;       // this slice's weight, and of those that min_p leaves
-  u64 bins;              // the sum of this CTA's share of the bins
-  float most, least;
   uint32_t at_k, at_share;
-  int32_t nan, ties, lowest, listed, members;
+  int32_t lowest, listed, members;
   int32_t bin, subbin;
   u64 above, inside, rest;
   uint32_t key;
@@ -260,6 +262,12 @@ __device__ __forceinline__ V block_reduce(V v, V* part, F join, V none) {
   return v;
 }
 
+// That all CTAs of the cluster run, before one writes another's memory.
+struct Started {
+  __device__ __forceinline__ Started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+  __device__ __forceinline__ void wait() const { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   extern __shared__ __align__(16) unsigned char s_raw[];
@@ -271,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   constexpr int warps = kWarps;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int first = rank * a.slice, n = max(0, min(a.slice, a.vocab - first));
+  Started started;
   grid_dependency_wait();
   allow_dependent_launch();
 
@@ -322,12 +331,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       for (int e = 0; e < kVec; e += 2) f(make_float2(kv::to_float(x.t[e]), kv::to_float(x.t[e + 1])));
     }
   };
-  // x of the cluster's CTAs, each lane that of one
-  auto of_lane = [&](const auto Shared::*field, auto none) {
-    auto v = none;
-    if (lane < ranks) v = cluster.map_shared_rank(&s, lane)->*field;
-    return v;
+  // Told to all, before the cluster's barrier, and read from this CTA's own memory after it, a lane each.  (Read by every warp
+  // from the others' memory, one word of one CTA a lane, it took 2 to 4 us each time that 16 CTAs met.)
+  auto tell = [&](int what, u64 x) {
+    if (tid < ranks) cluster.map_shared_rank(&s, tid)->told[what][rank] = x;
   };
+  auto told = [&](int what, u64 none) { return lane < ranks ? s.told[what][lane] : none; };
   float* fpart = reinterpret_cast<float*>(s.part);
   int* ipart = reinterpret_cast<int*>(s.part);
   if (few) {  // what the top_k-th largest of all cannot lie below: a CTA's own, or the least of the CTAs' shares of top_k
@@ -351,10 +360,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   most = block_reduce(most, fpart, [](float x, float y) { return fmaxf(x, y); }, -INFINITY);
   lowest = block_reduce(lowest, fpart, [](float x, float y) { return fminf(x, y); }, INFINITY);
   nan = __syncthreads_or(nan);
-  if (tid == 0) s.most = most, s.least = lowest, s.nan = nan;
+  started.wait();
+  const auto pair = [](uint32_t high, uint32_t low) { return (u64)high << 32 | low; };
+  tell(kRange, pair(__float_as_uint(most), __float_as_uint(lowest)));
+  tell(kNan, nan);
+  if (few) tell(kBounds, pair(s.at_k, s.at_share));
   cluster.sync();
-  most = of_lane(&Shared::most, -INFINITY), lowest = of_lane(&Shared::least, INFINITY);
-  nan = of_lane(&Shared::nan, 0);
+  const u64 range = told(kRange, pair(__float_as_uint(-INFINITY), __float_as_uint(INFINITY)));
+  most = __uint_as_float((uint32_t)(range >> 32)), lowest = __uint_as_float((uint32_t)range);
+  nan = (int)told(kNan, 0);
 #pragma unroll
   for (int o = 8; o; o >>= 1) {
     most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
@@ -363,7 +377,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   most = __shfl_sync(~0u, most, 0), lowest = __shfl_sync(~0u, lowest, 0);
   nan = __any_sync(~0u, nan);
   uint32_t bound = 0;
-  if (few) bound = max(__reduce_max_sync(~0u, of_lane(&Shared::at_k, 0u)), __reduce_min_sync(~0u, of_lane(&Shared::at_share, ~0u)));
+  if (few) {
+    const u64 bounds = told(kBounds, 0xFFFFFFFFu);
+    bound = max(__reduce_max_sync(~0u, (uint32_t)(bounds >> 32)), __reduce_min_sync(~0u, (uint32_t)bounds));
+  }
 
   const bool bad = nan || most == -INFINITY || !(t >= 0.f) || isinf(t) || isnan(top_p) || isnan(min_p);
   if (bad) {
@@ -443,8 +460,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         if (at < kList) s.top[at] = (u64)key_of(v) << 32 | (uint32_t)~(first + i * kVec + e);
       }
     }
+    __syncthreads();
+    tell(kListed, s.listed);
     cluster.sync();
-    const int part = of_lane(&Shared::listed, 0);
+    const int part = (int)told(kListed, 0);
     const int count = __reduce_add_sync(~0u, part);
     if (count <= kList) {  // the first CTA has them all then, and does the rest by itself
       if (rank == 0) {
@@ -509,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     for (int b = tid; b < bins; b += kThreads) s.hist.low[b] = s.hist.high[b] = 0;
     __syncthreads();
   };
-  // The cluster's sum of a field, and that of the CTAs before this one.
-  auto ranks_sum = [&](const u64 Shared::*field, u64& lower, u64& all) {
-    const u64 own = of_lane(field, (u64)0);
+  // The cluster's sum of what was told, and that of the CTAs before this one.
+  auto ranks_sum = [&](int what, u64& lower, u64& all) {
+    const u64 own = told(what, 0);
     u64 x = own;
 #pragma unroll
     for (int o = 1; o < kMostCluster; o *= 2) {
@@ -548,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (tid % threads) bin[0] = 0;
     const u64 own = bin[0] + bin[1] + bin[2] + bin[3];
     u64 all = 0, x = scan(own, all);
-    if (tid == 0) s.bins = all;
+    tell(kBinned, all);
     cluster.sync();
     u64 lower;
-    ranks_sum(&Shared::bins, lower, all);
+    ranks_sum(kBinned, lower, all);
     if (share >= 0.0) target = max((u64)ceil(share * (double)all), (u64)1);
     x += lower;
     if (x - own < target && target <= x) {
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   // The border at which the running sum, from the largest logit down, of one each (mass false) or of the weights of those at
   // `least` and above comes to `target`: the key there, how many of the equal ones belong, and how many there are.  False
   // where it lies below what min_p leaves, and so moves nothing: what min_p takes is summed, but neither binned nor gathered
-  // (64 rows of 151936 with top_p 0.95: 28 us with min_p 0.02, 54 without).
+  // (64 rows of 151936 with top_p 0.95: 27 us with min_p 0.02, 53 without).
   const float steps = 2047.f / fminf(fmaxf((most - lowest) * (1.0f / t), 1e-6f), 32.f) / t;
   auto step_of = [&](float v) {  // falls as v grows
     return (int)(__float_as_uint(fminf((most - v) * steps, 2047.f) + 8388608.f) & (kBins - 1));
@@ -606,10 +625,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       }
       if (min_p > 0.f) {
         scan(whole, whole), scan(over, over);
-        if (tid == 0) s.whole = whole, s.over = over;
+        tell(kWhole, whole), tell(kOver, over);
         cluster.sync();
-        ranks_sum(&Shared::whole, lower, whole);
-        ranks_sum(&Shared::over, lower, over);
+        ranks_sum(kWhole, lower, whole);
+        ranks_sum(kOver, lower, over);
         target = max((u64)ceil(share * (double)whole), (u64)1), share = -1.0;
         if (target > over) return false;
       }
@@ -638,8 +657,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
         if (at < kList) s.list[at] = key_of(v);
       }
     }
+    __syncthreads();
+    tell(kListed, s.listed);
     cluster.sync();
-    const int part = of_lane(&Shared::listed, 0);
+    const int part = (int)told(kListed, 0);
     const int count = __reduce_add_sync(~0u, part);
     if (count <= kList) {
       if (warp < ranks) {  // a warp copies a CTA's
@@ -784,9 +805,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
       if (i < warp) ahead += ipart[i];
       all += ipart[i];
     }
-    if (tid == 0) s.ties = all;
+    tell(kTies, all);
     cluster.sync();
-    ahead += __reduce_add_sync(~0u, lane < rank ? of_lane(&Shared::ties, 0) : 0);
+    ahead += __reduce_add_sync(~0u, lane < rank ? (int)told(kTies, 0) : 0);
     if (lane == 0) sum += of_ties(ahead, tied);
   }
 #pragma unroll
@@ -799,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (i < warp) lower += s.part[i];
     slice += s.part[i];
   }
-  if (tid == 0) s.kept = slice;
+  tell(kKept, slice);
   cluster.sync();
   u64 grand, others;
-  ranks_sum(&Shared::kept, others, grand);
+  ranks_sum(kKept, others, grand);
   lower += others;
   const u64 target = target_of(share, grand);
   if (lower < target && target <= lower + sum) {
