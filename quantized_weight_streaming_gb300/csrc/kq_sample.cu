@@ -11,11 +11,13 @@
 // numbers' leading bits, as a radix sort has them, put most of a row into a dozen
 // bins, and their atomics took 200 of 237 us for one row of 248320.)  Where more
 // than 1024 lie in the step, as where logits are equal, the border is found digit by
-// digit.  The token then is the first id, in the vocabulary's order, where the
+// digit.  A top_k of up to 256 needs no histogram: the threads' own largest logits bound
+// the top_k-th from below, the few logits above that bound go to the first CTA, and it
+// orders them.  The token then is the first id, in the vocabulary's order, where the
 // running sum of the kept weights passes u times their sum.
 //
 // A weight is exp((l - max) / temperature) in fixed point, 44 bits behind the
-// point, and sums are of 64-bit integers: a row of 2^18 equal ones still fits, sums
+// point, and sums are of 64-bit integers: a row of 393216 equal ones still fits, sums
 // are exact, and no order of atomics or CTAs moves a border or a token.
 //
 // Measured: one row of 248320 fp32 with top_k 20 and top_p 0.8 10 us, 64 rows of 151936
