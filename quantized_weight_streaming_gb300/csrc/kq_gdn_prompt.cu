@@ -61,6 +61,9 @@ constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
 template <typename T>
 constexpr int kKqTile = kParts<T> * kTile;
 constexpr int kRowFactors = 4 * kChunk + 4;
+// T, X, P and L, none of whose elements passes 1, enter as parts of 2^12 times themselves: the low part of an element as small
+// as 2^-15 is a normal fp16 number then.  (Unscaled, fp32 outputs were off by 1.4e-6 instead of ERRA.)
+constexpr float kUp = 4096.f, kDown = 1.f / kUp;
 
 struct PromptArgs {
   RuleArgs r;
@@ -71,7 +74,7 @@ struct PromptArgs {
   // slots' (tasks_from < 0); `beside` where rows or tasks run beside the grid launched before them.
   int64_t from, to, tasks_from;
   int32_t beside;
-  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G, G fq; G64, the largest value
+  float* factors;   // [slot][value head][kRowFactors]: beta G fk, beta, fk G64/G / kUp, G fq kUp; G64, the largest value
 };
 
 // Where a request's chunks lie among the slots: q_start / 64 + r is at least the slots of the requests before it.
@@ -91,12 +94,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two numbers as high and low fp16 parts: the first eleven bits, and what is left rounded to eleven more.
+// Two numbers as high and low fp16 parts, each rounded: 23 bits, and low parts of either sign, so that the products of two low
+// parts, which are left out, do not add up.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const float2 x = make_float2(a, b);
-  const float2 h = make_float2(__uint_as_float(__float_as_uint(a) & 0xFFFFE000u), __uint_as_float(__float_as_uint(b) & 0xFFFFE000u));
-  const float2 l = fma2(h, make_float2(-1.f, -1.f), x);
-  hi = h2_bits(__floats2half2_rn(h.x, h.y));
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 l = fma2(__half22float2(h), make_float2(-1.f, -1.f), make_float2(a, b));
+  hi = h2_bits(h);
   lo = h2_bits(__floats2half2_rn(l.x, l.y));
 }
 
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = warp * 16 + lane / 4 + e * 8;
-    const float f = s_fq[i];  // the scale, which no fp16 part may have to hold, comes with the outputs
+    const float f = kUp * s_fq[i];  // the scale, which no fp16 part may have to hold, comes with the outputs
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       if (b / 2 > warp) continue;
@@ -406,8 +409,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
       }
       const float x = (s0.x + s1.x) + (s0.y + s1.y);
       (i % 2 ? t[i / 2].y : t[i / 2].x) = x;
-      const __half hi = __float2half_rn(x);
-      *reinterpret_cast<__half*>(to + swizzled(at0 + i, (at0 + j) / 8) + j % 8 * 2) = lane < 16 ? hi : __float2half_rn(x - __half2float(hi));
+      const float y = x * kUp;
+      const __half hi = __float2half_rn(y);
+      *reinterpret_cast<__half*>(to + swizzled(at0 + i, (at0 + j) / 8) + j % 8 * 2) = lane < 16 ? hi : __float2half_rn(y - __half2float(hi));
     }
   }
   __syncthreads();
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
         for (int e = 0; e < 4; ++e) {
           const int row = at0 + 16 * (N + m) + lane / 4 + e % 2 * 8;
           const float2 l = *reinterpret_cast<const float2*>(smem + lower_at(row, at0 + k * 16 + lane % 4 * 2 + e / 2 * 8));
-          split2(l.x, l.y, ah[e], al[e]);
+          split2(l.x * kUp, l.y * kUp, ah[e], al[e]);
         }
         product(y[m], ah, al, b[k]);
       }
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     for (int m = 0; m < N; ++m) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        split2(y[m][2 * e], y[m][2 * e + 1], b[m][e], b[m][2 + e]);
+        split2(y[m][2 * e] * kDown, y[m][2 * e + 1] * kDown, b[m][e], b[m][2 + e]);
         b[m][e] = turned(b[m][e]), b[m][2 + e] = turned(b[m][2 + e]);
       }
 #pragma unroll
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
       for (int e = 0; e < 2; ++e) {
         uint32_t hi, lo;
         const uint32_t at = swizzled(at0 + 16 * (N + m) + lane / 4 + e * 8, (at0 + col) / 8) + lane % 4 * 4;
-        split2(z[m][2 * e], z[m][2 * e + 1], hi, lo);
+        split2(z[m][2 * e] * kDown, z[m][2 * e + 1] * kDown, hi, lo);
         *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
       }
     }
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     for (int e = 0; e < 2; ++e) {
       uint32_t hi, lo;
       const uint32_t at = swizzled(kChunk + warp * 16 + lane / 4 + e * 8, b) + lane % 4 * 4;
-      split2(x[b][2 * e], x[b][2 * e + 1], hi, lo);
+      split2(x[b][2 * e] * kDown, x[b][2 * e + 1] * kDown, hi, lo);
       *reinterpret_cast<uint32_t*>(smem + at) = hi, *reinterpret_cast<uint32_t*>(lowpart + at) = lo;
     }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -499,13 +503,13 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   }
   if (tid < kChunk) {
     float* f = p.factors + (slot * a.v_heads + h) * kRowFactors;
-    const float decay = exp2_fast(s_hi[tid]), beta_i = s_beta[tid], fk = s_fk[tid];
+    const float decay = exp2_fast(s_hi[tid]) * fmaf(s_lo[tid], 0.69314718f, 1.f), beta_i = s_beta[tid], fk = s_fk[tid];
     f[tid] = beta_i * decay * fk;
     f[kChunk + tid] = beta_i;
-    f[2 * kChunk + tid] = fk * exp2_fast((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
-    f[3 * kChunk + tid] = decay * s_fq[tid];
+    f[2 * kChunk + tid] = kDown * fk * exp2_fast((s_hi[kChunk - 1] - s_hi[tid]) + (s_lo[kChunk - 1] - s_lo[tid]));
+    f[3 * kChunk + tid] = kUp * decay * s_fq[tid];
     if (tid == 0) {
-      f[4 * kChunk] = exp2_fast(s_hi[kChunk - 1]);
+      f[4 * kChunk] = exp2_fast(s_hi[kChunk - 1]) * fmaf(s_lo[kChunk - 1], 0.69314718f, 1.f);
       f[4 * kChunk + 1] = pattern_value<T>(max(max(s_vmax[0], s_vmax[1]), max(s_vmax[2], s_vmax[3])));
     }
   }
@@ -718,25 +722,25 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       for (int c = 0; c < chunks; ++c) {
         const uint8_t* at = smem + c % kStages * kStage;
         const uint64_t kd = sw128_desc(at), td = sw128_desc(at + kKqTile<T>), kt = across_desc(at, 16384);
-        auto state = [&](uint32_t to, uint64_t rows, int k) {  // 16 of S's key dimensions: high and low parts, and K's low ones
-          rows += (uint64_t)((k / 4 * 16384 + k % 4 * 32) >> 4);
-          tc_mma_ts(tmem + to, tmem + kS + k * 8, rows, narrow, k);
-          tc_mma_ts(tmem + to, tmem + kS + kD / 2 + k * 8, rows, narrow, 1);
-          if (kParts<T> == 2) tc_mma_ts(tmem + to, tmem + kS + k * 8, rows + (kTile >> 4), narrow, 1);
+        // A sum on the tensor cores is cut off, not rounded, at each addition: what is small comes first where nothing waits.
+        constexpr int kPasses = kParts<T> + 1;
+        auto state = [&](uint32_t to, uint64_t rows, int k, int pass, bool more) {  // 16 of S's key dimensions
+          // low x whole, then high x low of K or Q where it has a low part, then high x high
+          const bool low = pass == 0, low_rows = kPasses == 3 && pass == 1;
+          tc_mma_ts(tmem + to, tmem + kS + low * (kD / 2) + k * 8,
+                    rows + (uint64_t)((k / 4 * 16384 + k % 4 * 32 + low_rows * kTile) >> 4), narrow, more);
         };
-        auto solved = [&](uint32_t to, uint64_t rows, int k) {  // 16 tokens' R, and the tokens from there on
-#pragma unroll
-          for (int pass = 0; pass < 3; ++pass)  // high x high, low x high, high x low
-            tc_mma_ts(tmem + to + 16 * k, tmem + kR + (pass == 1 ? kChunk / 2 : 0) + k * 8,
-                      rows + (pass == 2 ? kLowPart : 0) + (uint64_t)((k * 16 * 128 + k * 32) >> 4), idesc_f16(128, kChunk - 16 * k),
-                      pass || k);
+        auto solved = [&](uint32_t to, uint64_t rows, int k, int pass, bool more) {  // 16 tokens' R, and the tokens from there on
+          // low x high, high x low, high x high
+          tc_mma_ts(tmem + to + 16 * k, tmem + kR + (pass == 0 ? kChunk / 2 : 0) + k * 8,
+                    rows + (pass == 1 ? kLowPart : 0) + (uint64_t)((k * 16 * 128 + k * 32) >> 4), idesc_f16(128, kChunk - 16 * k), more);
         };
         auto update = [&](int half, int k) {  // 16 tokens' U, 64 of S's key dimensions
           const uint64_t keys = kt + (uint64_t)((half * 16384 + k * 2048) >> 4);
           const uint32_t to = tmem + kD3 + half * (kD / 2), u = tmem + kU + k * 16;
-          tc_mma_ts(to, u, keys, wide, k);
-          tc_mma_ts(to, u + 8, keys, wide, 1);
+          tc_mma_ts(to, u + 8, keys, wide, k);
           if (kParts<T> == 2) tc_mma_ts(to, u, keys + (kTile >> 4), wide, 1);
+          tc_mma_ts(to, u, keys, wide, 1);
         };
         gate.wait(&full[c % kStages], c / kStages & 1);
         if (c) gate.wait(&s_done[1], c - 1 & 1);  // the last chunk's U, which the first product goes over, is read
@@ -745,7 +749,9 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           gate.wait(&s_ready[j], c & 1);
           tc_fence_after();
 #pragma unroll
-          for (int k = 2 * j; k < 2 * j + 2; ++k) state(kDk, kd, k);
+          for (int k = 2 * j; k < 2 * j + 2; ++k)
+#pragma unroll
+            for (int pass = 0; pass < kPasses; ++pass) state(kDk, kd, k, pass, k || pass);
         }
         tc_commit(&k_done);
         if (c) {  // the last chunk's outputs are in registers
@@ -753,12 +759,15 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           tc_fence_after();
         }
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k);
+        for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k) state(kDq, kd + kLower, k, pass, k || pass);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           gate.wait(&r_ready[j], c & 1);
           tc_fence_after();
-          solved(kDu, td, j);
+#pragma unroll
+          for (int pass = 0; pass < 3; ++pass) solved(kDu, td, j, pass, j || pass);
           tc_commit(&u_done[j]);
         }
 #pragma unroll
@@ -772,7 +781,9 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
         for (int j = 0; j < 4; ++j) update(1, j);
         tc_commit(&s_done[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j);
+        for (int pass = 0; pass < 3; ++pass)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j, pass, j || pass);
         tc_commit(&x_done);
         tc_commit(&tiles_free[c % kStages]);
       }
@@ -860,7 +871,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
       tc_fence_before();
       mbar_arrive(&s_ready[sub]);
       if (c) outputs(c - 1);
-      down = a.scale * power_of_two(-power);
+      down = kDown * a.scale * power_of_two(-power);
       float2 d[kToks / 2];
       gate.wait(&k_done, c & 1);
       tc_fence_after();
