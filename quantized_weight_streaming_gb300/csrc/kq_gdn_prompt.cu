@@ -27,13 +27,14 @@
 // because no step of the rule lets a column grow by more than |v| (|k| <= 1, beta <
 // 1, decays of at most 1).  By the same bound no element of T or X passes 1.
 //
-// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 438 us (the
-// bytes alone 40; 118 TFLOP/s of the rule's own operations); six ragged requests of
-// 4613 tokens together, f16: 221.  Of the first, the rows take 26 us, the chunk
-// tasks 136, the walk 2.6 us a chunk, in which five waits follow one another (S^T K,
-// R, U, the update, S again), each a product of 100 to 500 cycles, its signal (150) and
-// a turn through registers: neither bytes nor products bound it but their latency.
-// States are within 2e-7 of 64-bit ones, fp32 outputs too.
+// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 402 us (the
+// bytes alone 40; 128 TFLOP/s of the rule's own operations); six ragged requests of
+// 4613 tokens together, f16: 177.  Of the second, rows take 17 us, the chunk tasks 72,
+// the walk 80; the first is the walk, 2.5 us a chunk, in which five waits follow one
+// another (S^T K, R, U, the update, S again), each a product of 250 to 500 cycles, its
+// signal (150) and a turn through registers of some hundred instructions a thread:
+// neither bytes nor products bound it but their latency.
+// States are within 2e-7 to 3e-7 of 64-bit ones, fp32 outputs within 3e-7 to 4e-7.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -62,7 +63,7 @@ template <typename T>
 constexpr int kKqTile = kParts<T> * kTile;
 constexpr int kRowFactors = 4 * kChunk + 4;
 // T, X, P and L, none of whose elements passes 1, enter as parts of 2^12 times themselves: the low part of an element as small
-// as 2^-15 is a normal fp16 number then.  (Unscaled, fp32 outputs were off by 1.4e-6 instead of ERRA.)
+// as 2^-15 is a normal fp16 number then.  (Unscaled, fp32 outputs were off by 1.4e-6 instead of 1.05e-6; rounding the high parts, not cutting them off, then made it 6.4e-7.)
 constexpr float kUp = 4096.f, kDown = 1.f / kUp;
 
 struct PromptArgs {
@@ -111,12 +112,12 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
 // c += (a_hi + a_lo) (b_hi + b_lo) of a 16 x 16 by 16 x 16 product, without that of the low parts.
 __device__ __forceinline__ void mma_parts(float (&c0)[4], float (&c1)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
                                           const uint32_t (&bh)[4], const uint32_t (&bl)[4]) {
-  mma_f16(c0, ah, bh[0], bh[1]);
-  mma_f16(c1, ah, bh[2], bh[3]);
   mma_f16(c0, ah, bl[0], bl[1]);
   mma_f16(c1, ah, bl[2], bl[3]);
   mma_f16(c0, al, bh[0], bh[1]);
   mma_f16(c1, al, bh[2], bh[3]);
+  mma_f16(c0, ah, bh[0], bh[1]);
+  mma_f16(c1, ah, bh[2], bh[3]);
 }
 // A matrix of 8 x 8 fp16 numbers over a warp, its rows for its columns.
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
@@ -326,29 +327,35 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     for (int b = 0; b < 8; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+    // the products with low parts first: a sum is cut off at each addition (fp32 outputs off by 3.1e-7, with all parts of a k
+    // at once 5.6e-7)
 #pragma unroll
-    for (int k = 0; k < kD / 16; ++k) {
-      const uint32_t half = base + k / 4 * 16384;
-      const uint32_t mine = half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16);
-      uint32_t fa[4], fa_low[4];
-      ldmatrix4(fa, mine);
-      if constexpr (kParts<T> == 2) ldmatrix4(fa_low, mine + kTile);
+    for (int low = kParts<T> - 1; low >= 0; --low)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
-        if (b > warp) continue;
-        const uint32_t keys = half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2);
-        uint32_t fb[4];
-        ldmatrix4(fb, keys);
-        if constexpr (kParts<T> == 2) {
-          uint32_t fb_low[4];
-          ldmatrix4(fb_low, keys + kTile);
-          mma_parts(acc[2 * b], acc[2 * b + 1], fa, fa_low, fb, fb_low);
-        } else {
-          mma_f16(acc[2 * b], fa, fb[0], fb[1]);
-          mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
+      for (int k = 0; k < kD / 16; ++k) {
+        const uint32_t half = base + k / 4 * 16384;
+        const uint32_t mine = half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16);
+        uint32_t fa[4], fa_low[4];
+        ldmatrix4(fa, mine);
+        if (low) ldmatrix4(fa_low, mine + kTile);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
+          if (b > warp) continue;
+          const uint32_t keys = half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2);
+          uint32_t fb[4], fb_low[4];
+          ldmatrix4(fb, keys);
+          if (low) {
+            ldmatrix4(fb_low, keys + kTile);
+            mma_f16(acc[2 * b], fa, fb_low[0], fb_low[1]);
+            mma_f16(acc[2 * b + 1], fa, fb_low[2], fb_low[3]);
+            mma_f16(acc[2 * b], fa_low, fb[0], fb[1]);
+            mma_f16(acc[2 * b + 1], fa_low, fb[2], fb[3]);
+          } else {
+            mma_f16(acc[2 * b], fa, fb[0], fb[1]);
+            mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
+          }
         }
       }
-    }
   };
   // of row i and the two columns from j on: the decays between, times the keys' norms
   auto decays = [&](int i, int j) {
@@ -421,9 +428,9 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   auto below = [&](auto blocks, int at0, int col) {
     constexpr int N = decltype(blocks)::value;
     auto product = [&](float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&b)[4]) {
-      mma_f16(c, ah, b[0], b[1]);
       mma_f16(c, ah, b[2], b[3]);
       mma_f16(c, al, b[0], b[1]);
+      mma_f16(c, ah, b[0], b[1]);
     };
     uint32_t ah[4], al[4], b[N][4];  // of right operands: two registers of high parts, two of low ones
 #pragma unroll

@@ -368,6 +368,18 @@ def test_gdn_values_of_any_size(kq, size):
     _ok(kq)
 
 
+@pytest.mark.parametrize("new", [[1176], [89, 50, 70]])
+def test_gdn_fp32_prompts_keep_fp32(kq, new):
+    """Chunks lose no more than fp32 itself does: a factor in two fp16 parts is off by h at most (four of them in an output),
+    and a product of 128 is eight additions that are cut off, by 2 h of what the sum is then, one of 64 four: 4 + 8 + 4 h."""
+    c = Delta("f32", (new, [0] * len(new), np.arange(len(new))), 2, 4, 128, seed=3)
+    out, state = c.run(kq)
+    used, done = [int(i) for i in c.slot], ~torch.isnan(c.want[:, 0, 0])
+    assert float((out.double()[done] - c.want[done]).norm() / c.want[done].norm()) <= 16 * H
+    assert float((state[used].double() - c.after[used]).norm() / c.after[used].norm()) <= 16 * H
+    _ok(kq)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["short", "mid"])
 @pytest.mark.parametrize("scale", [1e-6, -1e6])
