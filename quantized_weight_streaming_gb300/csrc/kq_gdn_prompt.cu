@@ -27,9 +27,9 @@
 // because no step of the rule lets a column grow by more than |v| (|k| <= 1, beta <
 // 1, decays of at most 1).  By the same bound no element of T or X passes 1.
 //
-// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 402 us (the
-// bytes alone 40; 128 TFLOP/s of the rule's own operations); six ragged requests of
-// 4613 tokens together, f16: 177.  Of the second, rows take 17 us, the chunk tasks 72,
+// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 405 us (the
+// bytes alone 40; 127 TFLOP/s of the rule's own operations); six ragged requests of
+// 4613 tokens together, f16: 173.  Of the second, rows take 17 us, the chunk tasks 68,
 // the walk 80; the first is the walk, 2.5 us a chunk, in which five waits follow one
 // another (S^T K, R, U, the update, S again), each a product of 250 to 500 cycles, its
 // signal (150) and a turn through registers of some hundred instructions a thread:
@@ -320,43 +320,47 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   __syncthreads();
   if (!mbar_wait_bounded(&s_full, 0)) prompt_flag(KQ_ERR_TIMEOUT);
 
-  // products of 16 rows a warp, of queries and then of keys, with the keys that they look back on
+  // products of 16 rows of queries and of keys a warp with the keys that they look back on, together, for these and the decays
+  // are theirs in common (3600 tasks: 72 us one after the other, 68 so, although 48 bytes spill; with four CTAs an SM none do: 73)
   const uint32_t base = smem_u32(smem);
-  auto products = [&](float (&acc)[8][4], int rows) {
+  float acc_p[8][4], acc_l[8][4];
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
+  for (int b = 0; b < 8; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
-    // the products with low parts first: a sum is cut off at each addition (fp32 outputs off by 3.1e-7, with all parts of a k
-    // at once 5.6e-7)
+    for (int e = 0; e < 4; ++e) acc_p[b][e] = acc_l[b][e] = 0.f;
+  // the products with low parts first: a sum is cut off at each addition (fp32 outputs off by 3.1e-7, with all parts of a k
+  // at once 5.6e-7)
 #pragma unroll
-    for (int low = kParts<T> - 1; low >= 0; --low)
+  for (int low = kParts<T> - 1; low >= 0; --low)
 #pragma unroll
-      for (int k = 0; k < kD / 16; ++k) {
-        const uint32_t half = base + k / 4 * 16384;
-        const uint32_t mine = half + swizzled(rows + warp * 16 + lane % 16, k % 4 * 2 + lane / 16);
-        uint32_t fa[4], fa_low[4];
-        ldmatrix4(fa, mine);
-        if (low) ldmatrix4(fa_low, mine + kTile);
+    for (int k = 0; k < kD / 16; ++k) {
+      const uint32_t half = base + k / 4 * 16384;
+      const uint32_t mine = half + swizzled(warp * 16 + lane % 16, k % 4 * 2 + lane / 16), queries = mine + kChunk * 128;
+      uint32_t fk[4], fq[4], fk_low[4], fq_low[4];
+      ldmatrix4(fk, mine);
+      ldmatrix4(fq, queries);
+      if (low) ldmatrix4(fk_low, mine + kTile), ldmatrix4(fq_low, queries + kTile);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
-          if (b > warp) continue;
-          const uint32_t keys = half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2);
-          uint32_t fb[4], fb_low[4];
-          ldmatrix4(fb, keys);
+      for (int b = 0; b < 4; ++b) {  // 16 tokens: the matrices of tokens 0-7 and 8-15, low and high half of the 16 dimensions
+        if (b > warp) continue;
+        const uint32_t keys = half + swizzled(b * 16 + lane % 8 + lane / 16 * 8, k % 4 * 2 + lane / 8 % 2);
+        uint32_t fb[4], fb_low[4];
+        ldmatrix4(fb, keys);
+        if (low) ldmatrix4(fb_low, keys + kTile);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
           if (low) {
-            ldmatrix4(fb_low, keys + kTile);
-            mma_f16(acc[2 * b], fa, fb_low[0], fb_low[1]);
-            mma_f16(acc[2 * b + 1], fa, fb_low[2], fb_low[3]);
-            mma_f16(acc[2 * b], fa_low, fb[0], fb[1]);
-            mma_f16(acc[2 * b + 1], fa_low, fb[2], fb[3]);
+            mma_f16(acc_p[2 * b + e], fq, fb_low[2 * e], fb_low[2 * e + 1]);
+            mma_f16(acc_l[2 * b + e], fk, fb_low[2 * e], fb_low[2 * e + 1]);
+            mma_f16(acc_p[2 * b + e], fq_low, fb[2 * e], fb[2 * e + 1]);
+            mma_f16(acc_l[2 * b + e], fk_low, fb[2 * e], fb[2 * e + 1]);
           } else {
-            mma_f16(acc[2 * b], fa, fb[0], fb[1]);
-            mma_f16(acc[2 * b + 1], fa, fb[2], fb[3]);
+            mma_f16(acc_p[2 * b + e], fq, fb[2 * e], fb[2 * e + 1]);
+            mma_f16(acc_l[2 * b + e], fk, fb[2 * e], fb[2 * e + 1]);
           }
         }
       }
-  };
+    }
   // of row i and the two columns from j on: the decays between, times the keys' norms
   auto decays = [&](int i, int j) {
     const float hi = s_hi[i], lo = s_lo[i];
@@ -364,35 +368,22 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
     const float2 fj = *reinterpret_cast<const float2*>(s_fk + j);
     return make_float2(fj.x * exp2_fast((hi - hj.x) + (lo - lj.x)), fj.y * exp2_fast((hi - hj.y) + (lo - lj.y)));
   };
-  float acc[8][4];
   uint32_t ph[4][4], pl[4][4];  // P as operands of 16 x 16
-  products(acc, kChunk);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = warp * 16 + lane / 4 + e * 8;
-    const float f = kUp * s_fq[i];  // the scale, which no fp16 part may have to hold, comes with the outputs
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      if (b / 2 > warp) continue;
-      const int j = b * 8 + lane % 4 * 2;
-      const float2 r = decays(i, j);
-      split2(j <= i ? acc[b][2 * e] * r.x * f : 0.f, j + 1 <= i ? acc[b][2 * e + 1] * r.y * f : 0.f, ph[b / 2][b % 2 * 2 + e],
-             pl[b / 2][b % 2 * 2 + e]);
-    }
-  }
-  products(acc, 0);
   __syncthreads();  // the tile is read: -L goes over its queries, T over its keys
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = warp * 16 + lane / 4 + e * 8;
-    const float f = -s_beta[i] * s_fk[i];
+    // the scale, which no fp16 part may have to hold, comes with the outputs
+    const float of_p = kUp * s_fq[i], of_l = -s_beta[i] * s_fk[i];
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       if (b / 2 > warp) continue;
       const int j = b * 8 + lane % 4 * 2;
       const float2 r = decays(i, j);
+      split2(j <= i ? acc_p[b][2 * e] * r.x * of_p : 0.f, j + 1 <= i ? acc_p[b][2 * e + 1] * r.y * of_p : 0.f, ph[b / 2][b % 2 * 2 + e],
+             pl[b / 2][b % 2 * 2 + e]);
       *reinterpret_cast<float2*>(smem + lower_at(i, j)) =
-          make_float2(j < i ? acc[b][2 * e] * r.x * f : 0.f, j + 1 < i ? acc[b][2 * e + 1] * r.y * f : 0.f);
+          make_float2(j < i ? acc_l[b][2 * e] * r.x * of_l : 0.f, j + 1 < i ? acc_l[b][2 * e + 1] * r.y * of_l : 0.f);
     }
   }
   __syncthreads();
