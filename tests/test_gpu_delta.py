@@ -368,6 +368,18 @@ def test_gdn_values_of_any_size(kq, size):
     _ok(kq)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_gdn_many_requests_of_all_lengths(kq, dt):
+    """More than are ordered by length at a time, some of equal lengths, skipped or without tokens, short ones among them."""
+    r = np.random.default_rng(31)
+    new = [int(n) for n in r.choice([0, 1, 7, 32, 33, 64, 65, 130], 71)]
+    slot = r.permutation(74)[:71]
+    slot[r.choice(71, 9, replace=False)] = -1
+    c = Delta(dt, (new, [int(n) for n in r.integers(0, 2, 71)], slot), 1, 2, 128, seed=32)
+    c.check(*c.run(kq))
+    _ok(kq)
+
+
 @pytest.mark.parametrize("new", [[1176], [89, 50, 70]])
 def test_gdn_fp32_prompts_keep_fp32(kq, new):
     """Chunks lose no more than fp32 itself does: a factor in two fp16 parts is off by h at most (four of them in an output),
@@ -522,6 +534,30 @@ def test_sample_ties(kq, dt):
         for s in (dict(top_k=7), dict(top_k=vocab // 2 + 1), dict(top_p=0.3), dict(top_k=100, top_p=0.5), dict(temperature=0.0),
                   dict(min_p=0.9), dict()):
             _check_sample(kq, x, u, **s)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("top_k", [2, 63, 64, 65, 128, 129, 256, 257])
+def test_sample_both_sides_of_each_count(kq, dt, top_k):
+    """Where few are ranked, sorted or found by a histogram; logits apart and in groups of equal ones; kept all and in part."""
+    for vocab in (300, 5001, 40000):
+        x = _logits(4, vocab, dt, vocab + top_k)
+        x[2:] = (x[2:].float() * 4).round().to(x.dtype) / 4
+        u = torch.rand(4, generator=_gen(top_k))
+        for s in (dict(), dict(top_p=0.9), dict(temperature=0.6, top_p=0.97, min_p=0.05)):
+            _check_sample(kq, x, u, top_k=top_k, **s)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("min_p", [1e-12, 1e-4, 0.02, 0.6])
+def test_sample_min_p_on_either_side_of_top_p(kq, dt, min_p):
+    """The border of one above, between and below that of the other, and of top_k's where there are three."""
+    x, u = _logits(5, 30011, dt, 77), torch.rand(5, generator=_gen(78))
+    x[3:] = (x[3:].float() * 8).round().to(x.dtype) / 8
+    for s in (dict(top_p=0.2), dict(top_p=0.95), dict(top_p=0.9999), dict(top_p=0.95, top_k=700), dict(top_p=0.5, top_k=5000)):
+        _check_sample(kq, x, u, min_p=min_p, **s)
     _ok(kq)
 
 
