@@ -2,6 +2,7 @@
 test_gpu_delta."""
 import math
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -165,4 +166,42 @@ def test_gdn_long_prompt_of_one_request(kq, dt, new, cached, before):  # noqa: F
     state, again = c.state.cuda(), torch.full(c.v.shape, 7.0, dtype=c.dt, device="cuda")
     kq.kq_gdn(p, q, k, v, a, b, _int([before, before + new]), _int([new + cached]), _int([2]), state, again, 100000, ws=ws)
     assert torch.equal(again, out)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+def test_calls_of_two_streams(kq, dt):  # noqa: F811
+    """Prompts in parts, ragged prompts, steps and sampling on two streams at once give what they give one after the other."""
+    t, g = TYPES[dt], torch.Generator().manual_seed(9)
+    hk, hv, d = 4, 12, 128
+    p = kq.GatedDelta(hk, hv, d, torch.zeros(hv, device="cuda"), torch.full((hv,), -3.0, device="cuda"))
+    steps = []
+    for new in ([1700], [300, 20, 0, 65, 500], [1] * 9, [1900]):
+        n, r = sum(new), len(new)
+        q, k = (torch.randn(n, hk, d, generator=g).to(t).cuda() for _ in range(2))
+        v = torch.randn(n, hv, d, generator=g).to(t).cuda()
+        a, b = (torch.randn(n, hv, generator=g).to(t).cuda() for _ in range(2))
+        ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (np.concatenate([[0], np.cumsum(new)]), [n + 1 for n in new], range(r))]
+        logits, u = (2 * torch.randn(3, 50000, generator=g)).to(t).cuda(), torch.rand(3, generator=g).cuda()
+        steps.append((new, q, k, v, a, b, ints, torch.randn(r, hv, d, d, generator=g).cuda(), logits, u))
+
+    def run(order):
+        got = []
+        for i, s in order:
+            new, q, k, v, a, b, ints, state, logits, u = steps[i]
+            with torch.cuda.stream(s):
+                out, state, token = torch.full_like(v, 7), state.clone(), torch.empty(3, dtype=torch.int32, device="cuda")
+                ws = torch.empty(max(16, kq.kq_gdn_workspace_bytes(p, t, len(new), v.shape[0], max(new))), dtype=torch.uint8, device="cuda")
+                kq.kq_gdn(p, q, k, v, a, b, *ints, state, out, max(new), ws=ws)
+                kq.kq_sample(logits, u, token, top_p=torch.full((3,), 0.9, device="cuda"))
+                got.append((i, out, state, token, ws))
+        torch.cuda.synchronize()
+        return sorted(got, key=lambda x: x[0])
+
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    want = run([(i, torch.cuda.current_stream()) for i in range(4)])
+    for _ in range(3):
+        for x, y in zip(run([(0, s1), (3, s2), (1, s1), (2, s2)]), want):
+            assert all(torch.equal(a, b) for a, b in zip(x[1:4], y[1:4])), x[0]
     _ok(kq)
