@@ -753,7 +753,7 @@ def kq_gdn(p, q, k, v, a, b, d_q_start, d_kv_len, d_slot, state, out, max_new, w
 def _per_row(t, rows, name):
     if t is None:
         return None
-    if str(t.dtype) == "torch.float32" and t.is_contiguous() and t.numel() >= rows:
+    if _kind(t.dtype)[0] == KQ_F32 and t.is_contiguous() and t.numel() >= rows:
         return t.data_ptr()
     raise KQError(KQ_ERR_SHAPE, f"{name}: a contiguous fp32 tensor of {rows} elements is needed, not {tuple(t.shape)} {t.dtype}")
 
