@@ -32,7 +32,7 @@ __device__ __forceinline__ void gdn_flag(int status) { atomicOr(&g_gdn_status, 1
 //
 // Measured: 64 requests' tokens of 10240 f16 channels 6.7 us (1.6 of bytes, the rest
 // two loads that wait for one another and a launch); 7 ragged requests of 5900 tokens
-// together, bf16, 52 us, 4.7 TB/s.  Eight channels a lane, or eight tokens' loads ahead, took
+// together, bf16, 49 us, 4.9 TB/s.  Eight channels a lane, or eight tokens' loads ahead, took
 // more registers and as long.
 
 constexpr int kConvWarps = 4, kConvAhead = 4, kConvWide = 4;
@@ -499,9 +499,14 @@ int kq_causal_conv(const kq_conv* p, int dtype, const kq_heads* x, const int32_t
   a.s = gdn::Requests{d_q_start, d_kv_len, d_slot, requests, tokens, slots};
   a.state = static_cast<char*>(d_state), a.weight = p->weight, a.bias = p->bias;
   a.channels = p->channels, a.silu = p->silu;
-  // short pieces where there are few, or the last wave of warps would be a long one; long ones where there are many, for
-  // the inputs before a piece are read again
-  a.piece = tokens <= 2048 ? 8 : 32;
+  // Pieces as short as keep the warps (4256 are resident) to a wave or so, for the inputs before a piece are read again; longer
+  // ones where there are many waves (one request's tokens of 10240 bf16 channels with pieces of 8, 16, 32, 64: 1000 13, 12, 14,
+  // 13 us; 2000 25, 21, 21, 26; 4000 49, 39, 37, 40; 8000 93, 74, 66, 66; 20000 -, 173, 154, 147).
+  const int64_t groups = (p->channels + 32 * gdn::kConvWide - 1) / (32 * gdn::kConvWide);
+  const auto warps = [&](int piece) { return (requests + (tokens + piece - 1) / piece) * groups; };
+  a.piece = 8;
+  while (a.piece < 32 && warps(a.piece) > 6000) a.piece *= 2;
+  if (a.piece == 32 && warps(32) > 14000) a.piece = 64;
   a.windows = (tokens + a.piece - 1) / a.piece;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   KQ_CUDA_TRY(dtype == KQ_F32   ? gdn::launch_conv<float>(a, p->width, st)

@@ -66,7 +66,9 @@ struct Args {
 typedef unsigned long long u64;
 
 constexpr int kList = 1024;
-constexpr int kFewK = 256;  // top_k up to which the candidates are gathered without a histogram
+// top_k up to which the candidates are gathered without a histogram (one row of 248320 fp32 with a top_k of 128, 256, 257: 14, 18,
+// 30 us; 64 rows of 151936 fp16 with 256, 257: 27, 43)
+constexpr int kFewK = 256;
 
 // What each CTA of a cluster tells all others: its largest and least logit, whether it has a NaN, its bounds for the top_k-th,
 // how many logits it listed, the sum of its share of the bins, its weight, and of that what min_p leaves, and what is kept, how

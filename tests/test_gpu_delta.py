@@ -219,6 +219,24 @@ def test_conv_in_pieces_is_conv_at_once(kq):
     assert torch.equal(c, a) and not torch.equal(parts[:3], whole[:3]) and torch.equal(parts[3:], whole[3:])
 
 
+@pytest.mark.parametrize("tokens", [700, 1500, 3100, 6100])
+def test_conv_of_many_channels_is_that_of_few(kq, tokens):
+    """Pieces are longer where there is more to do; nothing of a channel's arithmetic goes by them."""
+    g, c = _gen(tokens), 10240
+    x, w = torch.randn(tokens, c, generator=g).half().cuda(), torch.randn(c, 4, generator=g).cuda()
+    new = [5, 0, 129, 1, 2, tokens - 400, 263]
+    q_start, kv_len, slot = _arrays(new, np.array([0, 1, 1, 0, 3, 0, 2]), np.array([3, 0, 6, 1, 5, 2, 4]))
+    state = torch.randn(8, 3, c, generator=g).half().cuda()
+    args = _int(q_start), _int(kv_len), _int(slot)
+    out, after = torch.zeros_like(x), state.clone()
+    kq.kq_causal_conv(kq.CausalConv(w), x, *args, after, out)
+    for lo in range(0, c, 1024):
+        part, s = torch.zeros(tokens, 1024, dtype=x.dtype, device="cuda"), state[:, :, lo: lo + 1024].contiguous()
+        kq.kq_causal_conv(kq.CausalConv(w[lo: lo + 1024].contiguous()), x[:, lo: lo + 1024], *args, s, part)
+        assert torch.equal(part, out[:, lo: lo + 1024]) and torch.equal(s, after[:, :, lo: lo + 1024])
+    _ok(kq)
+
+
 def test_conv_malformed_requests(kq):
     x, w = torch.randn(20, 16).cuda(), torch.randn(16, 4).cuda()
     p = kq.CausalConv(w)
