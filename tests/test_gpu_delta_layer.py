@@ -166,6 +166,10 @@ def test_gdn_long_prompt_of_one_request(kq, dt, new, cached, before):  # noqa: F
     state, again = c.state.cuda(), torch.full(c.v.shape, 7.0, dtype=c.dt, device="cuda")
     kq.kq_gdn(p, q, k, v, a, b, _int([before, before + new]), _int([new + cached]), _int([2]), state, again, 100000, ws=ws)
     assert torch.equal(again, out)
+    # the outputs over the values
+    state, over = c.state.cuda(), v.contiguous().clone()
+    kq.kq_gdn(p, q, k, over, a, b, _int([before, before + new]), _int([new + cached]), _int([2]), state, over, new, ws=ws)
+    assert torch.equal(over[before: before + new], out[before: before + new])
     _ok(kq)
 
 
