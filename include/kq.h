@@ -680,7 +680,10 @@ size_t kq_attn_workspace_bytes(const kq_kv_cache* cache, int32_t q_heads, int64_
  *   s = x + residual   (rounded to dtype, written back to residual; s = x without)
  *   y = s / sqrt(mean(s^2) + eps) * weight * silu(gate)
  * weight fp32 [dim] (NULL: ones), silu(z) = z / (1 + e^-z), left out without a
- * gate.  fp32 arithmetic whatever the types, one rounding at the end.
+ * gate.  fp32 arithmetic whatever the types, one rounding at the end.  silu is
+ * off by at most 10 * 2^-24 of its value in fp32; for 16-bit types, here and in
+ * kq_causal_conv, by |z| 2^-23.7 + 2^-21 (2^-17 at |z| = 87).  It is 0 below
+ * -87.3.
  *   heads 1 to 4096; dim a multiple of 8 up to 32768; eps >= 0. */
 typedef struct {
   int32_t heads, dim;

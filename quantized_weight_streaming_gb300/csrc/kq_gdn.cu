@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) conv_kernel(const ConvArgs a)
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][e], past[j][e], s);
         s = fmaf(w[W - 1][e], v[e], s);
-        y[e] = a.silu ? silu(s) : s;
+        y[e] = a.silu ? silu<T>(s) : s;
 #pragma unroll
         for (int j = 0; j + 1 < W - 1; ++j) past[j][e] = past[j + 1][e];
         past[W - 2][e] = v[e];

@@ -144,7 +144,7 @@ __device__ __forceinline__ void finish(const Args& a, const Row<T>& r, int64_t r
     if (a.residual.data && mine) gate.load(r.gate + 8 * vec);
     gate.get(z);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= gdn::silu(z[e]);
+    for (int e = 0; e < 8; ++e) v[e] *= gdn::silu<T>(z[e]);
   }
   if (a.codes) store_q8(a, row, vec, v, mine);
   if (a.out.data && mine) kv::store8(r.out + 8 * vec, v);

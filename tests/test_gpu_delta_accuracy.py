@@ -1,0 +1,66 @@
+"""The delta layers' operators, the norm and sampling where their accuracy shows: against 64-bit values, with bounds that
+count the roundings of each step in units of H = 2^-24."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import delta_reference as ref  # noqa: E402
+from test_gpu_delta import H, TYPES, _half, _int, _ok, kq  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _silu_bound(dt, z):
+    """fp32: the exponential instruction 4 (2^-22), its correction 1, its product with z 1, the sum 1, the reciprocal instruction 2
+    (1 ulp), the last product 1: 10.  16-bit types: the argument's rounding and that of log2(e), 2^-24 + 2^-26.2 = 2^-23.7 of
+    |z|; the two instructions and what is around them 2^-21; the result's own."""
+    if dt == torch.float32:
+        return 10 * H
+    return z.abs() * 2.0 ** -23.7 + 2.0 ** -21 + _half(dt)
+
+
+def _arguments(dt):
+    g = torch.Generator().manual_seed(61)
+    z = torch.cat((120 * torch.rand(30000, generator=g) - 60, 40 * torch.rand(2712, generator=g) - 100,
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 88.8, -88.8, -103.0, 5e4])))
+    return z[: len(z) // 8 * 8].to(TYPES[dt])
+
+
+def _check_silu(y, z, dt):
+    z = z.double()
+    want = z * ref.sigmoid(z)
+    # nothing is left below -87.3, of less than 1.1e-36; subnormal results have steps of their own
+    least = 1.1e-36 + (0 if dt == torch.float32 else torch.finfo(dt).smallest_normal * torch.finfo(dt).eps)
+    bound = want.abs() * _silu_bound(dt, z) * 1.001 + least
+    err = (y.cpu().double().flatten() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_silu_of_the_convolution_over_its_range(kq, dt):  # noqa: F811
+    """A window that takes its last input alone leaves SiLU of the inputs."""
+    z = _arguments(dt)
+    for silu in (True, False):
+        out, state = torch.empty(1, len(z), dtype=z.dtype, device="cuda"), torch.zeros(1, 1, len(z), dtype=z.dtype, device="cuda")
+        p = kq.CausalConv(torch.tensor([0.0, 1.0]).expand(len(z), 2).contiguous().cuda(), None, silu)
+        kq.kq_causal_conv(p, z.cuda()[None], _int([0, 1]), None, _int([0]), state, out)
+        if silu:
+            _check_silu(out, z, z.dtype)
+        else:
+            assert torch.equal(out.cpu()[0].float(), z.float())
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("heads,dim", [(1, 2048), (5, 128), (3, 40)])
+def test_silu_of_the_norm_over_its_range(kq, dt, heads, dim):  # noqa: F811
+    """Rows of +-1 have a root mean square of 1 exactly, so their gated norm is SiLU of the gates with the rows' signs."""
+    z = _arguments(dt)
+    z = z[: len(z) // (heads * dim) * heads * dim].view(-1, heads, dim)
+    x = torch.where(torch.arange(dim) % 3 == 0, -1.0, 1.0).to(z.dtype).expand_as(z).contiguous()
+    out = torch.empty_like(x, device="cuda")
+    kq.kq_rms_norm(kq.RMSNorm(heads, dim, None, eps=0.0), x.cuda(), out, gate=z.cuda())
+    _check_silu(out.cpu() * x, z.flatten(), z.dtype)
+    _ok(kq)
