@@ -782,8 +782,8 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
         for (int pass = 0; pass < 3; ++pass)
 #pragma unroll
           for (int j = 0; j < 4; ++j) solved(kDu, td + kLower, j, pass, j || pass);
+        if (c + kStages < chunks) tc_commit(&tiles_free[c % kStages]);  // only where it is waited for
         tc_commit(&x_done);
-        tc_commit(&tiles_free[c % kStages]);
       }
       gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
     }
