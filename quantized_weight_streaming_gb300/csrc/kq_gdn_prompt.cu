@@ -318,7 +318,10 @@ __global__ void __launch_bounds__(128, sizeof(T) == 4 ? 3 : 5) gdn_chunk_kernel(
   }
 
   __syncthreads();
-  if (!mbar_wait_bounded(&s_full, 0)) prompt_flag(KQ_ERR_TIMEOUT);
+  if (!mbar_wait_bounded(&s_full, 0)) {
+    prompt_flag(KQ_ERR_TIMEOUT);
+    mbar_wait_bounded(&s_full, 0);  // the copy gets the same time again, for the memory goes to another task
+  }
 
   // products of 16 rows of queries and of keys a warp with the keys that they look back on, together, for these and the decays
   // are theirs in common (3600 tasks: 72 us one after the other, 68 so, although 48 bytes spill; with four CTAs an SM none do: 73)
@@ -553,11 +556,12 @@ constexpr int kDk = 0, kU = 0, kDq = 64, kDu = 128, kR = 192, kD3 = 256, kS = 38
 // Barriers that are waited on with a limit; after one ran out all waits return at once, and the warps run through.
 struct Gate {
   volatile int* abort;
+  __device__ __forceinline__ bool gone() const { return *abort != 0; }
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return;
     const long long start = clock64();
     while (!mbar_try_wait(bar, parity)) {
-      if (*abort) return;
+      if (gone()) return;
       if (clock64() - start > kWaitLimitCycles) {
         *abort = 1;
         prompt_flag(KQ_ERR_TIMEOUT);
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   constexpr int kRowWords = kD * (int)sizeof(T) / 16;  // of 16 bytes, of a row of values
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], tiles_free[kStages], slot_full[kSlots], slot_out[kSlots], slot_free[kSlots], s_ready[4], r_ready[4], u_ready[4],
-      u_done[4], o_read, k_done, s_done[2], x_done;
+      u_done[4], o_read, k_done, s_done[2], x_done, drained;
   __shared__ uint32_t s_tmem, s_most[2][kWorkWarps];
   __shared__ int s_abort;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
     for (int i = 0; i < 4; ++i)
       mbar_init(&s_ready[i], kWorkers / 4), mbar_init(&r_ready[i], kWorkers / 4), mbar_init(&u_ready[i], kWorkers / 4), mbar_init(&u_done[i], 1);
     mbar_init(&o_read, kWorkers);
-    for (uint64_t* b : {&k_done, &s_done[0], &s_done[1], &x_done}) mbar_init(b, 1);
+    for (uint64_t* b : {&k_done, &s_done[0], &s_done[1], &x_done, &drained}) mbar_init(b, 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -678,14 +682,18 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
   if (warp == kWorkWarps + 1) {  // tiles
     if (elect_one()) {
       const uint64_t policy = l2_policy_evict_first();
-      for (int c = 0; c < chunks; ++c) {
+      int c = 0;
+      for (; c < chunks; ++c) {
         uint8_t* at = smem + c % kStages * kStage;
         uint64_t* bar = &full[c % kStages];
         if (c >= kStages) gate.wait(&tiles_free[c % kStages], c / kStages - 1 & 1);
+        if (gate.gone()) break;
         mbar_arrive_expect_tx(bar, kStage);
         bulk_g2s(at, p.kq + ((slot0 + c) * a.k_heads + hk) * kKqTile<T>, kKqTile<T>, bar, policy);
         bulk_g2s(at + kKqTile<T>, p.tx + ((slot0 + c) * a.v_heads + h) * kTile, kTile, bar, policy);
       }
+      // the copies that nobody waits for after a wait ran out
+      for (int i = max(0, c - kStages); i < c; ++i) mbar_wait_bounded(&full[i % kStages], i / kStages & 1);
     }
     __syncwarp();
   } else if (warp == kWorkWarps + 2) {  // values, none past the last token, and factors
@@ -740,6 +748,7 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
           if (kParts<T> == 2) tc_mma_ts(to, u, keys + (kTile >> 4), wide, 1);
           tc_mma_ts(to, u, keys, wide, 1);
         };
+        if (gate.gone()) break;
         gate.wait(&full[c % kStages], c / kStages & 1);
         if (c) gate.wait(&s_done[1], c - 1 & 1);  // the last chunk's U, which the first product goes over, is read
 #pragma unroll
@@ -785,7 +794,11 @@ __global__ void __launch_bounds__(kWorkers + 128, 1) gdn_prompt_kernel(const Pro
         if (c + kStages < chunks) tc_commit(&tiles_free[c % kStages]);  // only where it is waited for
         tc_commit(&x_done);
       }
-      gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
+      if (!gate.gone()) gate.wait(&x_done, chunks - 1 & 1);  // nothing is in flight when the memory goes
+      if (gate.gone()) {  // a wait ran out, here or elsewhere: the products get the same time again
+        tc_commit(&drained);
+        mbar_wait_bounded(&drained, 0);
+      }
     }
     __syncwarp();
   } else {
