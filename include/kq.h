@@ -808,9 +808,9 @@ size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests,
  *    NULL one stands for 1, 1, 0, (d_u is needed) and 0 for every row.  u lies in
  *    [0, 1); what lies outside counts as the nearest end.
  *  - d_token int32 [rows], d_prob fp32 [rows] (NULL: not written).
- *  - A logit of -infinity is never chosen.  A row whose largest is infinity
- *    chooses among those alone.  A row that holds a NaN or nothing but
- *    -infinity, or whose temperature or top_p or min_p is a NaN or whose temperature is
+ *  - A logit of -infinity is never chosen, nor one more than 3.4e38 below the
+ *    largest.  A row whose largest is infinity chooses among those alone.  A row
+ *    that holds a NaN or nothing but -infinity, or whose temperature or top_p or min_p is a NaN or whose temperature is
  *    negative or infinite, gets token -1 and prob 0, and sets
  *    KQ_ERR_NONFINITE for kq_device_status.
  *  - exp is good to 2^-21 however large its argument; sums are of 64-bit

@@ -118,24 +118,22 @@ template <bool EXACT>
 struct Row {
   float most;      // the largest logit
   float hi, lo;    // log2(e) / temperature in two floats
-  float low;       // differences below it weigh nothing
   // exp((v - most) / temperature) of two logits, in packed operations: the product with the factor is kept to twice fp32's
-  // bits, so the error is that of the exponential instruction (2^-22) however large the argument is.
+  // bits, so the error is that of the exponential instruction (2^-22) however large the argument is.  Infinitely far below the
+  // largest, the exponential is 0 and what the product lacks is no number: 0 then, whatever the temperature.
   __device__ __forceinline__ float2 exp_of(float2 v) const {
-    float2 d = add2(v, make_float2(-most, -most));
-    d.x = fmaxf(d.x, low), d.y = fmaxf(d.y, low);
-    const float2 h = make_float2(hi, hi), p = mul2(d, h);
+    const float2 d = add2(v, make_float2(-most, -most)), h = make_float2(hi, hi), p = mul2(d, h);
     float2 rest = fma2(d, make_float2(lo, lo), fma2(d, h, make_float2(-p.x, -p.y)));
     if (EXACT) {
       const float2 minus = make_float2(-1.f, -1.f), b = fma2(v, minus, d);  // v - most = d + err exactly
-      float2 err = add2(fma2(fma2(b, minus, d), minus, v), fma2(b, minus, make_float2(-most, -most)));
-      err.x = d.x > low ? err.x : 0.f, err.y = d.y > low ? err.y : 0.f;
+      const float2 err = add2(fma2(fma2(b, minus, d), minus, v), fma2(b, minus, make_float2(-most, -most)));
       rest = fma2(err, h, rest);
     }
     float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(p.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(p.y));
-    return fma2(mul2(e, rest), make_float2(0.69314718f, 0.69314718f), e);
+    e = fma2(mul2(e, rest), make_float2(0.69314718f, 0.69314718f), e);
+    return make_float2(fmaxf(e.x, 0.f), fmaxf(e.y, 0.f));
   }
   __device__ __forceinline__ float exp_of(float v) const { return exp_of(make_float2(v, v)).x; }
   // In units of 2^-44, by additions that leave the wanted bits at the end of a number: 22 in front, then the rest (signed),
@@ -424,7 +422,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   w.hi = fminf(1.44269502f / t, 3.0e38f);
   w.lo = (fmaf(-w.hi, t, 1.44269502f) + 1.92596303e-8f) / t;
   if (!(fabsf(w.lo) < 1.0e30f)) w.lo = 0.f;
-  w.low = fmaxf(-200.f / w.hi, -3.0e38f);
 
   // This thread's running sum of x over the CTA, and the sum of all.
   auto scan = [&](u64 x, u64& all) {

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import delta_reference as ref  # noqa: E402
-from test_gpu_delta import H, TYPES, _half, _int, _ok, kq  # noqa: E402,F401
+from test_gpu_delta import H, TYPES, _check_sample, _half, _int, _logits, _ok, kq  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,4 +63,21 @@ def test_silu_of_the_norm_over_its_range(kq, dt, heads, dim):  # noqa: F811
     out = torch.empty_like(x, device="cuda")
     kq.kq_rms_norm(kq.RMSNorm(heads, dim, None, eps=0.0), x.cuda(), out, gate=z.cuda())
     _check_silu(out.cpu() * x, z.flatten(), z.dtype)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("vocab", [11, 1001, 40003])
+@pytest.mark.parametrize("temperature", [1e36, 1e37, 1e38, 3.4e38])
+def test_sample_masked_at_temperatures_that_leave_all_alike(kq, dt, vocab, temperature):  # noqa: F811
+    """However high the temperature is, a logit of -infinity weighs nothing, and no more do those that fill a slice's last
+    vector."""
+    x = _logits(5, vocab, dt, vocab)
+    x[0, 1:] = -math.inf
+    x[1, ::3] = -math.inf
+    x[2, vocab // 2:] = -math.inf
+    x[3, : vocab - 1] = -math.inf
+    u = torch.tensor([0.5, 0.999, 0.6, 0.1, 1 - 2.0 ** -24])
+    for s in (dict(), dict(top_p=0.9), dict(top_k=7), dict(top_k=vocab - 1, top_p=0.99), dict(min_p=0.5)):
+        _check_sample(kq, x, u, temperature=temperature, **s)
     _ok(kq)
