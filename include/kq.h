@@ -813,8 +813,11 @@ size_t kq_gdn_workspace_bytes(const kq_gdn_rule* p, int dtype, int64_t requests,
  *    that holds a NaN or nothing but -infinity, or whose temperature or top_p or min_p is a NaN or whose temperature is
  *    negative or infinite, gets token -1 and prob 0, and sets
  *    KQ_ERR_NONFINITE for kq_device_status.
- *  - exp is good to 2^-21 however large its argument; sums are of 64-bit
- *    integers, so the order of work changes no token.
+ *  - e_i is good to 2^-21 of itself however large the argument of exp; of 16-bit
+ *    logits, whose difference from the largest is rounded to fp32, to 2^-21 +
+ *    2^-24 of that argument.  It counts in whole 2^-44 of the largest's, so one
+ *    below 2^-45 is never chosen; sums are of 64-bit integers, so the order of work
+ *    changes no token.
  *  - vocab 1 to 393216; rows = 0 is a no-op.
  * Errors: KQ_ERR_INVALID_ARG, KQ_ERR_SHAPE, KQ_ERR_ALIGNMENT, KQ_ERR_CUDA. */
 int kq_sample(int dtype, const void* d_logits, int64_t row_stride, int64_t rows, int64_t vocab,

@@ -112,14 +112,16 @@ __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// A row's weights.  EXACT: the difference from the largest is kept to its rounding error too (of 16-bit logits it has none
-// that matters: 2^-20 at worst, where logits are 2^20 steps apart).
+// A row's weights.  EXACT: the difference from the largest is kept to its rounding error too.  Of 16-bit logits it is not: where a
+// large one is the largest and others are small (16.5 and odd multiples of 2^-24) it has one, 2^-24 of itself, and a weight is off by 2^-24 of its
+// exponent, 31 of it at most before nothing is left of the weight; their own rounding is 2^-12 and more of each logit (64 rows
+// of 151936 f16 with top_p 0.95, with and without min_p 0.02: 26.6 and 53 us, exactly 29 and 57).
 template <bool EXACT>
 struct Row {
   float most;      // the largest logit
   float hi, lo;    // log2(e) / temperature in two floats
   // exp((v - most) / temperature) of two logits, in packed operations: the product with the factor is kept to twice fp32's
-  // bits, so the error is that of the exponential instruction (2^-22) however large the argument is.  Infinitely far below the
+  // bits, so the error is that of the exponential instruction (2^-22) and the difference's.  Infinitely far below the
   // largest, the exponential is 0 and what the product lacks is no number: 0 then, whatever the temperature.
   __device__ __forceinline__ float2 exp_of(float2 v) const {
     const float2 d = add2(v, make_float2(-most, -most)), h = make_float2(hi, hi), p = mul2(d, h);

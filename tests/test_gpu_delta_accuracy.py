@@ -81,3 +81,22 @@ def test_sample_masked_at_temperatures_that_leave_all_alike(kq, dt, vocab, tempe
     for s in (dict(), dict(top_p=0.9), dict(top_k=7), dict(top_k=vocab - 1, top_p=0.99), dict(min_p=0.5)):
         _check_sample(kq, x, u, temperature=temperature, **s)
     _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_sample_weights_where_the_difference_is_rounded(kq, dt):  # noqa: F811
+    """The chance of the lesser of two logits, e / (1 + e).  Beside the largest of 16.5 small ones have bits that fp32's
+    difference does not hold; e is off by 2^-21, and by 2^-24 of its exponent for 16-bit types, and by half of 2^-44; the sum and
+    the quotient by a few 2^-53, the result by 2^-24."""
+    small = [k * s * 2.0 ** -24 for k in (1, 3, 5, 9, 15, 17, 31) for s in (1, -1)] + [0.0, 2.0 ** -12, -0.37]
+    cases = [(v, t) for v in small for t in (0.75, 0.8, 0.9, 1.0, 1.05, 1.1, 1.15, 1.3, 2.0, 5.0)]
+    x = torch.tensor([[16.5, v] for v, _ in cases]).to(TYPES[dt])
+    t = torch.tensor([t for _, t in cases])
+    token, prob = torch.empty(len(cases), dtype=torch.int32, device="cuda"), torch.empty(len(cases), device="cuda")
+    kq.kq_sample(x.cuda(), torch.ones(len(cases)).cuda(), token, prob, temperature=t.cuda())
+    assert bool((token == 1).all())
+    a = (x[:, 1].double() - 16.5) / t.double()
+    e = torch.exp(a)
+    bound = e * (2.0 ** -21 + (0 if dt == "f32" else 2.0 ** -24) * a.abs()) + 2.0 ** -45 + 2.0 ** -24 * e
+    assert bool(((prob.cpu().double() - e / (1 + e)).abs() <= bound).all())
+    _ok(kq)
