@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
   if (((uintptr_t)src & 15) == 0) {
     for (int i = tid; i < n / kVec; i += kThreads) {
       union { uint4 u; T t[kVec]; } x;
-      x.u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      x.u = reinterpret_cast<const uint4*>(src)[i];  // (no read-only load: the grid may have begun while the logits were written)
       reinterpret_cast<uint4*>(s_l)[i] = x.u;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) see(x.t[e]);
