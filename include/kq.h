@@ -694,10 +694,11 @@ typedef struct {
 
 /* y of `tokens` tokens to out (rows of `dtype` elements), to out_q8, or to both.
  *  - x, residual (in and out, or NULL), gate (or NULL), out (or NULL): rows of
- *    heads.  out may be x's, the residual's or the gate's own view; other
- *    overlaps are not allowed.  Rows that are written lie apart: along the
- *    smaller of their strides by dim at least, and along the larger past all
- *    of those (so too where kq_gdn writes).
+ *    heads.  out may be x's, the residual's or the gate's own view, the residual
+ *    x's; other overlaps are not allowed, and refused where the views' tokens are
+ *    one stride apart.  Rows that are written lie apart: along the smaller of
+ *    their strides by dim at least, and along the larger past all of those (so
+ *    too where kq_gdn writes).
  *  - out_q8 (or NULL): planes of KQ_Q8_0 with n = tokens * heads rows (token by
  *    token) and k = dim (then a multiple of 32), written by the rules of
  *    kq_quantize_q8_0 from the fp32 y, scale padding included.  A block that

@@ -103,6 +103,11 @@ __device__ __forceinline__ float log_decay(float a, float a_log, float dt_bias) 
 
 // check_heads of rows that are written: no two may share an element (kq_norm.cu).
 int check_out_rows(const kq_heads* h, const char* name, int dtype, int64_t tokens, int heads, int dim);
+// Whether two views of rows of `dim` elements are one; whether they share an element (kq_norm.cu).  The second is exact for views
+// whose tokens are one stride apart, as those of one buffer are; of others, and of more than 4096 pairs of heads that do not adjoin,
+// it says no.
+bool same_view(const kq_heads* x, const kq_heads* y, int64_t tokens, int heads);
+bool rows_overlap(const kq_heads* x, int x_heads, const kq_heads* y, int y_heads, int64_t tokens, int dim, int dtype);
 int read_norm_status(int clear);
 int read_gdn_status(int clear);
 int read_sample_status(int clear);

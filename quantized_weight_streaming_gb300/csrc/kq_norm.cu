@@ -272,6 +272,47 @@ int check_out_rows(const kq_heads* h, const char* name, int dtype, int64_t token
   return KQ_OK;
 }
 
+namespace {
+// Rows in bytes: `heads` blocks a token, each `wide` (neighbouring rows are one block).
+struct Blocks {
+  int64_t tokens, token_stride, heads, head_stride, wide;
+  __int128 extent() const { return (__int128)(tokens - 1) * token_stride + (__int128)(heads - 1) * head_stride + wide; }
+};
+Blocks blocks_of(const kq_heads* h, int64_t tokens, int heads, int dim, int size) {
+  Blocks b{tokens, h->token_stride * size, heads, h->head_stride * size, (int64_t)dim * size};
+  if (b.head_stride == 0) b.heads = 1;
+  if (b.token_stride == 0) b.tokens = 1;
+  for (int turn = 0; turn < 2; ++turn) {
+    if (b.heads > 1 && b.head_stride == b.wide) b.wide *= b.heads, b.heads = 1;
+    if (b.tokens > 1 && b.token_stride == b.wide) b.wide *= b.tokens, b.tokens = 1;
+  }
+  return b;
+}
+}  // namespace
+
+bool same_view(const kq_heads* x, const kq_heads* y, int64_t tokens, int heads) {
+  return x->data == y->data && (tokens <= 1 || x->token_stride == y->token_stride) && (heads <= 1 || x->head_stride == y->head_stride);
+}
+
+bool rows_overlap(const kq_heads* x, int x_heads, const kq_heads* y, int y_heads, int64_t tokens, int dim, int dtype) {
+  const int size = dtype == KQ_F32 ? 4 : 2;
+  const int64_t apart = static_cast<const char*>(y->data) - static_cast<const char*>(x->data);
+  const Blocks a = blocks_of(x, tokens, x_heads, dim, size), b = blocks_of(y, tokens, y_heads, dim, size);
+  if (apart >= a.extent() || -(__int128)apart >= b.extent()) return false;
+  const int64_t stride = b.tokens > 1 ? b.token_stride : a.token_stride;
+  if (a.tokens > 1 && b.tokens > 1 && a.token_stride != b.token_stride) return false;
+  if (a.heads * b.heads > 4096) return false;
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t j = 0; j < b.heads; ++j) {
+      // b's block of token n + k begins at off + k * stride from a's of token n: the first k whose ends behind that one's begin
+      const __int128 off = (__int128)apart + (__int128)j * b.head_stride - (__int128)i * a.head_stride, least = -(__int128)b.wide + 1;
+      __int128 k = -(a.tokens - 1);
+      if (stride > 0 && least - off > k * stride) k = (least - off) / stride + ((least - off) % stride > 0);
+      if (k <= b.tokens - 1 && off + k * stride >= least && off + k * stride < a.wide) return true;
+    }
+  return false;
+}
+
 int read_norm_status(int clear) {
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, norm::g_norm_status, sizeof(v)) != cudaSuccess) return -1;
@@ -307,6 +348,13 @@ extern "C" int kq_rms_norm(const kq_rms* p, int dtype, const kq_heads* x, const 
     if (int s = check_heads(gate, "gate", dtype)) return s;
   if (out)
     if (int s = check_out_rows(out, "out", dtype, tokens, p->heads, p->dim)) return s;
+  for (const kq_heads* from : {x, residual, gate})
+    if (from && out && !same_view(from, out, tokens, p->heads) && rows_overlap(from, p->heads, out, p->heads, tokens, p->dim, dtype))
+      return fail(KQ_ERR_INVALID_ARG, "out overlaps an input without being its view");
+  if (residual && !same_view(x, residual, tokens, p->heads) && rows_overlap(x, p->heads, residual, p->heads, tokens, p->dim, dtype))
+    return fail(KQ_ERR_INVALID_ARG, "residual overlaps x");
+  if (residual && gate && rows_overlap(gate, p->heads, residual, p->heads, tokens, p->dim, dtype))
+    return fail(KQ_ERR_INVALID_ARG, "residual overlaps gate");
   norm::Args a{};
   if (out_q8) {
     if (int s = check_qmat(out_q8, KQ_Q8_0)) return s;
