@@ -767,8 +767,9 @@ typedef struct {
 
 /* out of the step's tokens, and the states after them.
  *  - q, k [tokens][k_heads][D], v, out [tokens][v_heads][D]: rows of heads of
- *    `dtype`; out may be v's own view.  a, b: `dtype` [tokens][v_heads] with
- *    token strides of a_stride, b_stride elements (any alignment of a dtype's).
+ *    `dtype`; out may be v's own view, but not overlap q, k or v otherwise (refused
+ *    as in kq_rms_norm).  a, b: `dtype` [tokens][v_heads] with token strides of
+ *    a_stride, b_stride elements (any alignment of a dtype's).
  *  - d_state: fp32 [slots][v_heads][D][D], 16-byte aligned; updated.
  *  - max_new: an upper bound of the requests' new tokens (1 for a decode step).
  *  - fp32 arithmetic and states whatever the types, one rounding of the output.

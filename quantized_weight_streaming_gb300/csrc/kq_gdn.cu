@@ -549,11 +549,19 @@ int kq_gdn(const kq_gdn_rule* p, int dtype, const kq_heads* q, const kq_heads* k
   a.k_heads = p->k_heads, a.v_heads = p->v_heads, a.unit = p->unit, a.gates = p->gates, a.eps = p->eps, a.scale = p->scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.short_most = 0x7fffffff;
-  if (in_chunks(p, max_new)) {
+  const bool chunks = in_chunks(p, max_new);
+  if (chunks) {
     const size_t need = gdn::prompt_workspace(p->k_heads, p->v_heads, requests, tokens, dtype);
     if (!d_ws || ws_bytes < need)
       return fail(KQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", d_ws ? ws_bytes : (size_t)0, need);
     if (!aligned16(d_ws)) return fail(KQ_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+  }
+  // a head's CTAs read q and k when others may have put their outputs away
+  for (const kq_heads* from : {q, k})
+    if (rows_overlap(from, p->k_heads, out, p->v_heads, tokens, p->head_dim, dtype)) return fail(KQ_ERR_INVALID_ARG, "out overlaps q or k");
+  if (!same_view(v, out, tokens, p->v_heads) && rows_overlap(v, p->v_heads, out, p->v_heads, tokens, p->head_dim, dtype))
+    return fail(KQ_ERR_INVALID_ARG, "out overlaps v without being its view");
+  if (chunks) {
     a.short_most = requests == 1 ? 0 : gdn::kShortRun;
     KQ_CUDA_TRY(gdn::launch_prompt(a, dtype, d_ws, st));
     if (requests == 1) return KQ_OK;

@@ -44,6 +44,26 @@ def test_norm_refuses_views_that_cross(kq):  # noqa: F811
     assert _norm(kq, kq.KQ_F16, n, 4, d, far, None, whole, whole)
 
 
+def _gdn(kq, dtype, tokens, hk, hv, q, k, v, out, d=64, **over):
+    w = lambda a: ctypes.byref(kq.kq_heads(*a))  # noqa: E731
+    p = _struct(kq.kq_gdn_rule, dict(k_heads=hk, v_heads=hv, head_dim=d, unit=1, gates=1, eps=1e-6, scale=0.1, reserved=0, a_log=FAKE,
+                                     dt_bias=FAKE), over)
+    status = kq.lib().kq_gdn(p, dtype, w(q), w(k), w(v), FAKE, hv, FAKE, hv, FAKE, FAKE, FAKE, 2, tokens, 8, FAKE, 4, w(out), None, 0, None)
+    text = kq.lib().kq_last_error().decode()
+    return status == kq.KQ_ERR_INVALID_ARG and "overlaps" in text, status, text
+
+
+def test_gdn_refuses_outputs_over_its_inputs(kq):  # noqa: F811
+    apart = [(FAKE + (i << 24), 512, 64) for i in range(1, 5)]
+    q, k, v, out = apart
+    for i, dtype in enumerate((kq.KQ_F16, kq.KQ_F32, kq.KQ_BF16)):
+        assert _gdn(kq, dtype, 9, 4, 4, q, k, v, q)[0]
+        assert _gdn(kq, dtype, 9, 4, 4, q, k, v, k)[0]
+        assert _gdn(kq, dtype, 9, 2, 4, q, k, v, (q[0] + 128 * (1 + (dtype == kq.KQ_F32)), 512, 64))[0]
+        assert _gdn(kq, dtype, 9, 4, 4, q, k, v, (v[0] + 16, 512, 64))[0]  # the values' rows, but not their view
+        assert _gdn(kq, dtype, 9, 4, 4, q, k, v, (v[0] + 512 * 2 * (1 + (dtype == kq.KQ_F32)), 512, 64))[0]
+
+
 def test_overlaps_are_found_where_bytes_are_shared_and_nowhere_else(kq):  # noqa: F811
     """Random views of one buffer whose tokens are one stride apart, with heads that adjoin, lie apart or come first."""
     r = random.Random(5)
