@@ -12,12 +12,12 @@ from test_gpu_delta import H, TYPES, Delta, _half, _int, _ok, kq  # noqa: E402,F
 pytestmark = pytest.mark.gpu
 
 
-def _tight(c, out, state):
+def _tight(c, out, state, units=16):
     used, done = [int(s) for s, n in zip(c.slot, c.new) if s >= 0 and n], ~torch.isnan(c.want[:, 0, 0])
     off = float((out.double()[done] - c.want[done]).norm() / c.want[done].norm())
-    assert off <= 16 * H + _half(c.dt), off / H
+    assert off <= units * H + _half(c.dt), off / H
     off = float((state[used].double() - c.after[used]).norm() / c.after[used].norm())
-    assert off <= 16 * H, off / H
+    assert off <= units * H, off / H
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
@@ -37,4 +37,15 @@ def test_gdn_each_count_of_chunks(kq, dt, new):  # noqa: F811
     torch.cuda.synchronize()
     _tight(c, outs[0].cpu(), states[0].cpu())
     assert all(torch.equal(s, states[0]) for s in states) and all(torch.equal(o, outs[0]) for o in outs)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("new,cached,decay", [(1537, 0, None), (2100, 3, None), (2100, 3, -9.0)])
+def test_gdn_prompts_in_parts_keep_fp32(kq, dt, new, cached, decay):  # noqa: F811
+    """One request's prompt of 24 chunks and more, whose parts run beside one another.  With decays 16 H as above; where nothing
+    fades the state's own rounding, half of H a chunk, adds up at random over the chunks: below sqrt(chunks) H."""
+    c = Delta(dt, ([new], [cached], np.array([1])), 1, 2, 128, seed=81, decay=decay)
+    out, state = c.run(kq)
+    _tight(c, out, state, 16 + (0 if decay is None else (new / 64) ** 0.5))
     _ok(kq)
