@@ -112,8 +112,11 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // Lets the grid launched after this one on the stream as a programmatic
 // dependent begin: its CTAs take SMs as this grid's CTAs exit and run their
 // prologue, then wait in grid_dependency_wait until this grid has completed.
-// Every kernel of the library waits before its first global access, so the
-// trigger can come as early as right after that wait.
+// Every kernel of the library waits before its first global access and triggers
+// no earlier than right after that wait, so a grid that has begun may count on it
+// that all grids but the one launched just before it have completed.  Three
+// kernels of the delta rule (kq_gdn_prompt.cu, end_beside) use that: run beside
+// the grid before them, they do not wait.
 __device__ __forceinline__ void allow_dependent_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -18,8 +18,8 @@
 //
 // The states are fp32 and stay so.  K and Q enter as fp16 with a power of two per row
 // taken out, so that an element is off by at most 2^-25 of its row's largest (fp32
-// rows as two parts), their norms and decays as fp32 factors of rows; what is not a
-// 16-bit number to begin with (S, T, X, R, U) enters as two fp16 parts, 22 bits.
+// rows as two parts, by 2^-23), their norms and decays as fp32 factors of rows; what
+// is not a 16-bit number to begin with (S, T, X, R, U) enters as two fp16 parts, 23 bits.
 // Products of two such leave out the one of the low parts.  The update of S is added
 // in registers, with fp32's rounding (the tensor cores' sums cut off instead, and a
 // state that adds up over thousands of tokens would drift).  S, R and U share a power
@@ -27,7 +27,7 @@
 // because no step of the rule lets a column grow by more than |v| (|k| <= 1, beta <
 // 1, decays of at most 1).  By the same bound no element of T or X passes 1.
 //
-// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 405 us (the
+// Measured: 8192 tokens, 16 key and 48 value heads, bf16, one request: 407 us (the
 // bytes alone 40; 127 TFLOP/s of the rule's own operations); six ragged requests of
 // 4613 tokens together, f16: 173.  Of the second, rows take 17 us, the chunk tasks 68,
 // the walk 80; the first is the walk, 2.5 us a chunk, in which five waits follow one
@@ -181,8 +181,15 @@ __device__ __forceinline__ Place place_of(const RuleArgs& a, int64_t slot) {
   return p;
 }
 
-// A grid `beside` the one launched before it reads what grids before that one wrote (it waited for them) and writes what none
-// of them touches; that it ends after it, its last CTA sees to.
+// A grid `beside` the one launched before it does not wait for it.  What keeps that safe:
+//  - The grid before it is one of these kernels, and all of its CTAs triggered.  Each did so after its own wait, or is a grid beside
+//    one that did: what grids before those wrote had been written and made visible by then.  So it may read that, the caller's inputs
+//    and tiles of two launches back, and nothing that the grid before it, or the one that it ran beside, still writes.
+//  - It writes what neither of these reads or writes: rows and tasks other chunks' slots, runs other requests' states and outputs.
+//  - It ends after the grid before it, because its last CTA waits for that one; so whoever waits for it has waited for both.
+// A trigger before a wait, a launch in between, or rows, tasks and walks in another order break this.  That a grid sees what was
+// visible to the grid that triggered it, without a wait of its own, is how launches behave, not what PTX promises: waits there, where
+// the walk is to be overlapped, would end the overlap (8192 tokens of 48 heads: 407 us in parts, 503 without).
 __device__ __forceinline__ void end_beside(const PromptArgs& p) {
   if (p.beside && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
