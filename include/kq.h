@@ -701,7 +701,9 @@ typedef struct {
  *    too where kq_gdn writes).
  *  - out_q8 (or NULL): planes of KQ_Q8_0 with n = tokens * heads rows (token by
  *    token) and k = dim (then a multiple of 32), written by the rules of
- *    kq_quantize_q8_0 from the fp32 y, scale padding included.  A block that
+ *    kq_quantize_q8_0 from the fp32 y, scale padding included: rows to keep or
+ *    to send in 8 bits, which kq_dequantize reads back (the products of this
+ *    library take fp32 and fp16 activations, not these).  A block that
  *    holds a NaN or infinity reads back as NaN and sets KQ_ERR_NONFINITE for
  *    kq_device_status; one whose scale overflows fp16 as well, with KQ_ERR_RANGE.
  *  - tokens = 0 is a no-op; tokens * heads < 2^31.
@@ -776,8 +778,11 @@ typedef struct {
  *    With head_dim 128, unit = 1, gates = 1 and max_new > 32, runs of more than
  *    32 tokens (a single request's whatever its length) go in chunks of 64
  *    tokens whose products run on the tensor cores, with every factor that is
- *    not a 16-bit number as two fp16 parts (22 bits): what they err by is of the
+ *    not a 16-bit number as two fp16 parts (23 bits): what they err by is of the
  *    order of fp32's rounding of the largest value and state of a head's chunk.
+ *    All other runs go token by token, one behind another, 0.46 us a token with
+ *    12 heads of 64 and 0.6 with 48 of 128: a prompt of 6000 takes 2.8 and 3.6
+ *    ms so, where 48 heads of 128 in chunks take 0.3 (0.45 in fp32).
  *  - A NaN or infinity in a token's q, k, v or gates makes what it reaches
  *    unspecified: its heads' outputs from that token on (in a chunk, from the
  *    chunk's first on), and their state.

@@ -253,7 +253,7 @@ static cudaError_t launch_norm(const Args& a, cudaStream_t st) {
   // Few rows, of up to a wave of CTAs, want many threads (one row of 5120 bf16 with a residual: 2.0, 2.3, 3.1 us with 1, 2, 4
   // vectors a thread; 304 rows 4.2, 4.7, 5.1).  Many want fewer that have more in flight each (4096 rows of 5120: 36, 30, 28 us;
   // of 8192: 71, 47, 42), but for short ones (8192 rows of 2048: 26, 22, 23) and fp32, whose four vectors are more than a
-  // thread's 64 registers hold (4096 rows of 5120: 54, 51, 61).
+  // thread's 64 registers hold (240 bytes spill: 4096 rows of 5120: 54, 51, 61; in 16-bit types 48 bytes do).
   if (vecs <= 1024 && a.rows <= 304) return launch<T, 1>(a, st);
   if (vecs <= (a.rows <= 304 || sizeof(T) == 4 ? 2048 : 512)) return launch<T, 2>(a, st);
   return launch<T, 4>(a, st);
