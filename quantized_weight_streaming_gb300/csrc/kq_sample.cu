@@ -643,14 +643,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     u64 rest = target - s.above;
     if (tid == 0) s.listed = 0;
     __syncthreads();
-    // the step's values, and some more for the roundings
-    const float middle = most - (float)bin / steps, half = bin == kBins - 1 ? INFINITY : 0.51f / steps + 1e-6f * fabsf(most);
+    // the step's values, and some more for the roundings; all of them where the step has no end, or so high a temperature that its
+    // middle is no number
+    const float middle = most - (float)bin / steps;
+    const float half = bin == kBins - 1 || isinf(middle) ? INFINITY : 0.51f / steps + 1e-6f * fabsf(most);
     for (int i = tid; i < vecs; i += kThreads) {
       union { uint4 u; T t[kVec]; } x;
       x.u = reinterpret_cast<const uint4*>(s_l)[i];
       bool some = false;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) some |= fabsf(kv::to_float(x.t[e]) - middle) <= half;
+      for (int e = 0; e < kVec; ++e) some |= !(fabsf(kv::to_float(x.t[e]) - middle) > half);
       if (!some) continue;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {

@@ -84,6 +84,46 @@ def test_sample_masked_at_temperatures_that_leave_all_alike(kq, dt, vocab, tempe
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("vocab", [1500, 40003, 100000])
+@pytest.mark.parametrize("temperature", [0.7, 5e36, 1.1e37, 1e38])
+def test_sample_counts_down_into_masked_logits(kq, dt, vocab, temperature):  # noqa: F811
+    """A top_k that reaches into logits of -infinity, of which all, a few or one remain, at temperatures whose 32 times fp32
+    does not hold: the border is found, and whatever shared memory held before takes no part."""
+    x = _logits(5, vocab, dt, vocab + 3)
+    for r, finite in enumerate((3, 257, 700, vocab // 2, vocab - 1)):
+        x[r].scatter_(0, torch.randperm(vocab, generator=torch.Generator().manual_seed(r))[finite:], -math.inf)
+    u = torch.tensor([0.5, 0.999, 0.6, 0.1, 1 - 2.0 ** -24])
+    for s in (dict(top_k=vocab - 1), dict(top_k=300), dict(top_k=vocab // 2 + 5, top_p=0.9), dict(top_k=1400, min_p=0.1)):
+        _check_sample(kq, x, u, temperature=1.0, top_k=500)  # leaves a border of its own behind
+        _check_sample(kq, x, u, temperature=temperature, **s)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_sample_logits_as_large_as_fp32_holds(kq, dt):  # noqa: F811
+    """Logits up to some 10^38 with temperatures of their size."""
+    x, u = _logits(4, 30011, dt, 5), torch.tensor([0.2, 0.5, 0.9, 0.999])
+    x = (x.float() * 5e36).to(TYPES[dt])
+    for t in (5e36, 1e37, 4e37):
+        for s in (dict(), dict(top_p=0.9), dict(top_k=20), dict(top_k=700), dict(top_p=0.99, min_p=0.01)):
+            _check_sample(kq, x, u, temperature=t, **s)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("temperature", [1e-45, 1e-40, 1e-38, 1e-36, 1e-30, 1e-12])
+def test_sample_temperatures_that_leave_the_largest(kq, dt, temperature):  # noqa: F811
+    """However low the temperature is: the largest, or the equal ones at it by their share."""
+    x, u = _logits(4, 30011, dt, 6), torch.tensor([0.2, 0.5, 0.9, 0.999])
+    x[1, ::7] = x[1].max()
+    x[2] = 1.5
+    x[3, 5:] = -math.inf
+    for s in (dict(), dict(top_p=0.9), dict(top_k=20), dict(top_k=700, top_p=0.4), dict(min_p=0.01), dict(top_p=0.7, min_p=0.01)):
+        _check_sample(kq, x, u, temperature=temperature, **s)
+    _ok(kq)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
 def test_sample_weights_where_the_difference_is_rounded(kq, dt):  # noqa: F811
     """The chance of the lesser of two logits, e / (1 + e).  Beside the largest of 16.5 small ones have bits that fp32's
     difference does not hold; e is off by 2^-21, and by 2^-24 of its exponent for 16-bit types, and by half of 2^-44; the sum and
