@@ -237,7 +237,9 @@ __global__ void __launch_bounds__(256) gdn_rows_kernel(const PromptArgs p) {
     uint8_t* to = kq + vec / 8 * 16384 + swizzled(row, vec % 8);
     *reinterpret_cast<uint4*>(to) = hi;
     if (kParts<T> == 2) *reinterpret_cast<uint4*>(to + kTile) = lo;  // of 16-bit types it is zero
-    if (vec == 0) norms[row] = i < at.n ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
+    // 0 for a row of zeros (and one of subnormal numbers) as well: its 1 / sqrt(eps) would pass fp16's range in w U, and a zero of K
+    // times that is no number
+    if (vec == 0) norms[row] = i < at.n && power > 0 ? 1.0f / sqrtf(sum + (a.eps * f) * f) : 0.f;
   }
   end_beside(p);
 }
