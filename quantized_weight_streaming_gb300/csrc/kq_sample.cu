@@ -113,9 +113,9 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 }
 
 // A row's weights.  EXACT: the difference from the largest is kept to its rounding error too.  Of 16-bit logits it is not: where a
-// large one is the largest and others are small (16.5 and odd multiples of 2^-24) it has one, 2^-24 of itself, and a weight is off by 2^-24 of its
-// exponent, 31 of it at most before nothing is left of the weight; their own rounding is 2^-12 and more of each logit (64 rows
-// of 151936 f16 with top_p 0.95, with and without min_p 0.02: 26.6 and 53 us, exactly 29 and 57).
+// large one is the largest and others are small (16.5 and odd multiples of 2^-24) it has one, 2^-24 of itself, and a weight is
+// off by 2^-24 of its exponent, which is 31 at most before nothing is left of the weight; such logits' own rounding is 2^-12 of
+// them and more (64 rows of 151936 f16 with top_p 0.95, with and without min_p 0.02: 26.6 and 53 us, exactly 29 and 57).
 template <bool EXACT>
 struct Row {
   float most;      // the largest logit
